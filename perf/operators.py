@@ -248,7 +248,7 @@ def prepare(case, seed):
             state["list"] = tide.TensorList([n for _, _, _, n in pieces], [kind] * len(pieces))
             names = ("grads",) if op == "clip" else ("master", "grads", "exp_avg", "exp_avg_sq", "shards")
             state["tables"] = [tide.pointer_table([state[k][d, o:o + n] for d, _, o, n in pieces]) for k in names]
-            state["decays"] = [state["decay"][p] for _, p, _, _ in pieces]
+            state["decays"] = tide.float_table([state["decay"][p] for _, p, _, _ in pieces])
     return state
 
 
