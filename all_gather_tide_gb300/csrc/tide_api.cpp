@@ -7,12 +7,14 @@
 #include <vector>
 
 #include "../../include/tide.h"
+#include "api_common.h"
+#include "group.h"
 #include "tide_internal.h"
 
 namespace {
 
-constexpr int kSlots = 4;  // pointer-table ring depth
-constexpr int kMaxCeLanes = 8;  // helper streams for copy-engine work
+using tide::kMaxCeLanes;
+using tide::no_throw;
 constexpr uint32_t kAllFlags =
     TIDE_FLAG_VEC_STRICT | TIDE_FLAG_CE_STRICT | TIDE_FLAG_CE_2D | TIDE_FLAG_OVERLAP | TIDE_FLAG_CE_1D;
 
@@ -22,12 +24,6 @@ int cuda_fail(cudaError_t e) {
     g_last_cuda_error = int(e);
     return TIDE_ECUDA;
 }
-
-#define TIDE_CUDA(call)                                   \
-    do {                                                  \
-        cudaError_t e_ = (call);                          \
-        if (e_ != cudaSuccess) return cuda_fail(e_);      \
-    } while (0)
 
 // A copy enqueued on one of the copy-engine lanes: on failure the helper lanes are joined back to
 // the caller's stream (so nothing already enqueued on them outlives the call unordered) before the
@@ -41,71 +37,15 @@ int cuda_fail(cudaError_t e) {
         }                                                 \
     } while (0)
 
-// One entry of the ring of pointer tables.  The host copy is pinned so the upload is a true
-// asynchronous copy on the caller's stream; `done` is recorded after the kernel that reads the
-// device copy, so the slot is only rewritten once that kernel has finished.
-struct Slot {
-    std::vector<const void*> content;
-    const void** host = nullptr;
-    void** dev = nullptr;
-    cudaEvent_t done = nullptr;
-    cudaStream_t stream = nullptr;
-    uint64_t last_use = 0;
-    bool valid = false;
-    bool pending = false;
-};
-
 }  // namespace
 
 int tide::record_cuda_error(cudaError_t e) { return cuda_fail(e); }
-
-struct tide_group {
-    tide::Plan plan;
-    uint32_t flags = 0;
-    int device = 0;
-    int sm_count = 0;
-    int rs_ctas = 0, ag_ctas = 0;  // 0 = default
-    int rs_variant = TIDE_RS_AUTO;
-    int ag_variant = TIDE_AG_AUTO;
-    uint64_t timeout_ns = tide::kDefaultTimeoutNs;
-    uint32_t debug = 0;
-    int* d_status = nullptr;  // device status word written by bounded waits that expire
-    tide::RsSeg* d_rs = nullptr;
-    int32_t* d_rs_piece = nullptr;  // piece index of every register-path chunk
-    tide::RsSeg* d_rs_bulk = nullptr;
-    int32_t* d_rs_bulk_piece = nullptr;  // piece index of every bulk chunk
-    tide::RsSeg* d_rs_slots = nullptr;      // pieces of the summing step over staging slots
-    int32_t* d_rs_slot_piece = nullptr;     // piece (0..P-1) of every chunk of one destination
-    tide::AgSeg* d_ag_bulk = nullptr;
-    tide::AgSeg* d_ag = nullptr;
-    int32_t* d_ag_run = nullptr;  // run index of every register-path placement chunk
-    size_t slot_cap = 0;
-    Slot slots[kSlots];
-    uint64_t use_clock = 0;
-    int64_t last_ce_copies = 0;
-    int32_t last_ce_uniform = 0;
-    // copy-engine work is spread over `ce_lanes` streams forked from and joined back to the
-    // caller's stream, so several copy engines run at once
-    int ce_lanes = kMaxCeLanes;  // measured on GB300: 1-D copies over 8 streams reach ~0.94 x HBM peak
-    int ce_bands = 1;  // 2-D copies per parameter (bands of ranks)
-    cudaStream_t lane_stream[kMaxCeLanes] = {};
-    cudaEvent_t lane_done[kMaxCeLanes] = {};
-    cudaEvent_t fork = nullptr;
-    std::mutex mu;
-};
 
 namespace {
 
 void release(tide_group* g) {
     if (!g) return;
-    for (Slot& s : g->slots) {
-        if (s.done) {
-            cudaEventSynchronize(s.done);
-            cudaEventDestroy(s.done);
-        }
-        if (s.host) cudaFreeHost(s.host);
-        if (s.dev) cudaFree(s.dev);
-    }
+    g->ring.release();
     for (int i = 0; i < kMaxCeLanes; ++i) {
         if (g->lane_stream[i]) {
             cudaStreamSynchronize(g->lane_stream[i]);
@@ -127,49 +67,16 @@ void release(tide_group* g) {
     delete g;
 }
 
-int check_device(tide_group* g) {
-    int dev = -1;
-    TIDE_CUDA(cudaGetDevice(&dev));
-    return dev == g->device ? TIDE_OK : TIDE_EINVAL;
-}
+int check_device(const tide_group* g) { return tide::check_device(g->device); }
 
-// Uploads `ptrs` into a ring slot (or finds a slot already holding the same table for the
-// same stream) and returns its index.  The caller records slots[k].done after its launch.
+// Uploads `ptrs` into a ring slot; the caller calls finish_slot after its launch.
 int upload_table(tide_group* g, const std::vector<const void*>& ptrs, cudaStream_t stream, int* slot) {
-    for (int k = 0; k < kSlots; ++k) {
-        Slot& s = g->slots[k];
-        if (s.valid && s.stream == stream && s.content == ptrs) {
-            s.last_use = ++g->use_clock;
-            *slot = k;
-            return TIDE_OK;
-        }
-    }
-    // victim: an unused slot, else the least recently used one
-    int k = -1;
-    for (int i = 0; i < kSlots && k < 0; ++i)
-        if (!g->slots[i].valid) k = i;
-    if (k < 0) {
-        k = 0;
-        for (int i = 1; i < kSlots; ++i)
-            if (g->slots[i].last_use < g->slots[k].last_use) k = i;
-    }
-    Slot& s = g->slots[k];
-    if (s.pending) TIDE_CUDA(cudaEventSynchronize(s.done));
-    s.valid = false;
-    std::memcpy(s.host, ptrs.data(), ptrs.size() * sizeof(void*));
-    TIDE_CUDA(cudaMemcpyAsync(s.dev, s.host, ptrs.size() * sizeof(void*), cudaMemcpyHostToDevice, stream));
-    s.content = ptrs;
-    s.stream = stream;
-    s.valid = true;
-    s.last_use = ++g->use_clock;
-    *slot = k;
+    TIDE_CUDA(g->ring.upload(ptrs, stream, slot));
     return TIDE_OK;
 }
 
 int finish_slot(tide_group* g, int k, cudaStream_t stream) {
-    Slot& s = g->slots[k];
-    TIDE_CUDA(cudaEventRecord(s.done, stream));
-    s.pending = true;
+    TIDE_CUDA(g->ring.finish(k, stream));
     return TIDE_OK;
 }
 
@@ -295,19 +202,6 @@ RsBulkLaunch rs_bulk_launcher(const tide_group* g) {
     return g->rs_variant == TIDE_RS_BULK ? tide::launch_reduce_scatter_bulk : tide::launch_reduce_scatter_tmem;
 }
 
-// Entry points return a status, never an exception: an allocation that fails (host vectors of the
-// pointer tables and plans) becomes TIDE_ENOMEM, anything else thrown (a mutex error) TIDE_EINVAL.
-template <class F>
-int no_throw(F&& f) {
-    try {
-        return f();
-    } catch (const std::bad_alloc&) {
-        return TIDE_ENOMEM;
-    } catch (...) {
-        return TIDE_EINVAL;
-    }
-}
-
 }  // namespace
 
 extern "C" {
@@ -424,12 +318,7 @@ int tide_group_create(tide_group_t* out, int32_t R, int32_t P, const int64_t* ro
         if (e == cudaSuccess) e = cudaMemset(g->d_status, 0, sizeof(int));
         // a table holds the R*P gradient pointers + R shard pointers (reduce-scatter) or R + P
         // pointers (all-gather)
-        g->slot_cap = size_t(R) * P + R + P;
-        for (Slot& s : g->slots) {
-            if (e == cudaSuccess) e = cudaHostAlloc(reinterpret_cast<void**>(&s.host), g->slot_cap * sizeof(void*), cudaHostAllocDefault);
-            if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&s.dev), g->slot_cap * sizeof(void*));
-            if (e == cudaSuccess) e = cudaEventCreateWithFlags(&s.done, cudaEventDisableTiming);
-        }
+        if (e == cudaSuccess) e = g->ring.create(size_t(R) * P + R + P);
         if (e != cudaSuccess) {
             release(g);
             return e == cudaErrorMemoryAllocation ? (g_last_cuda_error = int(e), TIDE_ENOMEM) : cuda_fail(e);
@@ -510,7 +399,7 @@ int tide_reduce_scatter(tide_group_t g, const void* const* grads, void* const* s
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         int k = 0;
         if ((rc = upload_table(g, table, st, &k)) != TIDE_OK) return rc;
-        void** dev = g->slots[k].dev;
+        void** dev = g->ring.slots[k].dev;
         const auto* gp = reinterpret_cast<const uint16_t* const*>(dev);
         auto* sp = reinterpret_cast<float* const*>(dev + size_t(R) * P);
         cudaError_t e;
@@ -550,7 +439,7 @@ int tide_reduce_scatter_slots(tide_group_t g, int32_t d, const void* const* slot
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         int k = 0;
         if ((rc = upload_table(g, table, st, &k)) != TIDE_OK) return rc;
-        void** dev = g->slots[k].dev;
+        void** dev = g->ring.slots[k].dev;
         // one table entry per slot and one shard: the pieces carry p = 0 and d = 0
         const auto* gp = reinterpret_cast<const uint16_t* const*>(dev);
         auto* sp = reinterpret_cast<float* const*>(dev + R);
@@ -587,7 +476,7 @@ int tide_all_gather(tide_group_t g, const void* const* shards, void* const* para
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         int k = 0;
         if ((rc = upload_table(g, table, st, &k)) != TIDE_OK) return rc;
-        void** dev = g->slots[k].dev;
+        void** dev = g->ring.slots[k].dev;
         const auto* sp = reinterpret_cast<const uint16_t* const*>(dev);
         auto* pp = reinterpret_cast<uint16_t* const*>(dev + R);
         cudaError_t e;
