@@ -39,10 +39,16 @@ TIDE_AG_AUTO = 0
 TIDE_AG_REGISTER = 1
 TIDE_AG_BULK = 2
 TIDE_DEBUG_STALL_PRODUCER = 0x1
+TIDE_F32 = 0
+TIDE_BF16 = 1
+TIDE_I32 = 2
+TIDE_I64 = 3
+TIDE_ADAMW_SKIP_NONFINITE = 0x1
 
 _lib = None
 _i64p = ctypes.POINTER(ctypes.c_int64)
 _i32p = ctypes.POINTER(ctypes.c_int32)
+_f32p = ctypes.POINTER(ctypes.c_float)
 _vp = ctypes.c_void_p
 _vpp = ctypes.POINTER(ctypes.c_void_p)
 
@@ -82,6 +88,20 @@ SIGNATURES = {
     "tide_probe_ingest": (ctypes.c_int, [_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                          ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _vp, _vp]),
     "tide_stage_into_slots": (ctypes.c_int, [_vp, _vpp, _vpp, ctypes.c_int64, _vpp, _vp]),
+    "tide_embedding": (ctypes.c_int, [_vp, ctypes.c_int32, _vpp, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
+                                      _vp, ctypes.c_int32, ctypes.c_int64, _vp]),
+    "tide_embedding_grad_workspace": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64, _i64p]),
+    "tide_embedding_grad": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int32, _i64p, _vpp, ctypes.c_int32, _vpp, _i64p,
+                                           ctypes.c_int32, ctypes.c_float, ctypes.c_int32, _vpp, _vp, ctypes.c_int64,
+                                           _vp]),
+    "tide_tensors_create": (ctypes.c_int, [_vpp, ctypes.c_int32, _i64p, _i32p]),
+    "tide_tensors_destroy": (ctypes.c_int, [_vp]),
+    "tide_grad_norm": (ctypes.c_int, [_vp, _vpp, _vp, _vp, _vp]),
+    "tide_clip_grads": (ctypes.c_int, [_vp, _vpp, _vp, ctypes.c_float, _vp]),
+    "tide_clip_grad_norm": (ctypes.c_int, [_vp, _vpp, ctypes.c_float, _vp, _vp]),
+    "tide_adamw": (ctypes.c_int, [_vp, _vpp, _vpp, _vpp, _vpp, _vpp, _f32p, ctypes.c_double, ctypes.c_double,
+                                  ctypes.c_double, ctypes.c_double, ctypes.c_int64, _vp, ctypes.c_float, ctypes.c_uint32,
+                                  _vp]),
     "tide_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "tide_last_cuda_error": (ctypes.c_int, []),
     "tide_version": (ctypes.c_int, []),
@@ -136,6 +156,20 @@ def pointer_table(xs: Sequence) -> ctypes.Array:
     a millisecond of Python per call to read R*P data pointers.  The tensors must stay alive and
     unmoved while the table is in use."""
     return (ctypes.c_void_p * len(xs))(*[_ptr(x) for x in xs])
+
+
+def float_table(xs: Sequence[float]) -> ctypes.Array:
+    """Marshals per-tensor numbers (weight decays) once, as ``pointer_table`` does pointers."""
+    return (ctypes.c_float * len(xs))(*xs)
+
+
+def _dtype_code(x) -> int:
+    import torch
+
+    code = {torch.float32: TIDE_F32, torch.bfloat16: TIDE_BF16, torch.int32: TIDE_I32, torch.int64: TIDE_I64}
+    if x.dtype not in code:
+        raise TideError(TIDE_EINVAL, f"a tensor of {x.dtype}")
+    return code[x.dtype]
 
 
 def _stream(stream) -> Optional[int]:
@@ -362,7 +396,76 @@ def tide_probe_mixed(buf, bulk_bytes: int, st_buf, st_bytes: int, ctas: int, cop
            "tide_probe_mixed")
 
 
-# ---- convenience object -----------------------------------------------------------------------
+# ---- the sharded training step ------------------------------------------------------------------
+
+
+def tide_embedding(g: int, p: int, shards: Sequence, ids, out, scale: float = 1.0, stream=None) -> None:
+    """``shards``: R bf16 shards; ``ids``: contiguous int32 or int64 tensor of n ids; ``out``: bf16 or fp32
+    tensor whose last dimension is the row and whose rows lie ``out.stride(-2)`` apart (n of them)."""
+    _check(lib().tide_embedding(g, p, _ptr_array(shards), ids.data_ptr(), _dtype_code(ids), ids.numel(), scale,
+                                out.data_ptr(), _dtype_code(out), _row_stride(out), _stream(stream)), "tide_embedding")
+
+
+def _row_stride(x) -> int:
+    """Elements between the rows of a tensor whose last dimension is contiguous."""
+    return x.stride(-2) if x.dim() > 1 and x.shape[-2] > 1 else max(x.shape[-1], 1)
+
+
+def tide_embedding_grad_workspace(g: int, p: int, n: int) -> int:
+    v = ctypes.c_int64()
+    _check(lib().tide_embedding_grad_workspace(g, p, n, ctypes.byref(v)), "tide_embedding_grad_workspace")
+    return v.value
+
+
+def tide_embedding_grad(g: int, p: int, ids: Sequence, douts: Sequence, shards: Sequence, workspace, scale: float = 1.0,
+                        accumulate: bool = False, stream=None) -> None:
+    """``ids`` and ``douts``: B tensors each (batch b: n_b ids, n_b rows); ``shards``: R fp32 shards;
+    ``workspace``: uint8 tensor of ``tide_embedding_grad_workspace`` bytes."""
+    B = len(ids)
+    _check(lib().tide_embedding_grad(g, p, B, _i64_array([x.numel() for x in ids]), _ptr_array(ids), _dtype_code(ids[0]),
+                                     _ptr_array(douts), _i64_array([_row_stride(x) for x in douts]), _dtype_code(douts[0]),
+                                     scale, int(accumulate), _ptr_array(shards), workspace.data_ptr(), workspace.numel(),
+                                     _stream(stream)), "tide_embedding_grad")
+
+
+def tide_tensors_create(elems: Sequence[int], types=None) -> int:
+    h = ctypes.c_void_p()
+    K = len(elems)
+    ty = None if types is None else (ctypes.c_int32 * K)(*types)
+    _check(lib().tide_tensors_create(ctypes.byref(h), K, _i64_array(elems), ty), "tide_tensors_create")
+    return h.value
+
+
+def tide_tensors_destroy(t: int) -> None:
+    _check(lib().tide_tensors_destroy(t), "tide_tensors_destroy")
+
+
+def tide_grad_norm(t: int, grads: Sequence, norm, sumsq=None, stream=None) -> None:
+    """``norm``: fp32 device tensor of one element; ``sumsq``: fp64 device tensor of one element or None."""
+    _check(lib().tide_grad_norm(t, _ptr_array(grads), _ptr(norm), None if sumsq is None else _ptr(sumsq), _stream(stream)),
+           "tide_grad_norm")
+
+
+def tide_clip_grads(t: int, grads: Sequence, norm, max_norm: float, stream=None) -> None:
+    _check(lib().tide_clip_grads(t, _ptr_array(grads), _ptr(norm), max_norm, _stream(stream)), "tide_clip_grads")
+
+
+def tide_clip_grad_norm(t: int, grads: Sequence, max_norm: float, norm, stream=None) -> None:
+    _check(lib().tide_clip_grad_norm(t, _ptr_array(grads), max_norm, _ptr(norm), _stream(stream)), "tide_clip_grad_norm")
+
+
+def tide_adamw(t: int, params: Sequence, grads: Sequence, exp_avg: Sequence, exp_avg_sq: Sequence, shards=None, *, lr: float,
+               betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay=None, step: int, norm=None,
+               max_norm: float = 0.0, flags: int = 0, stream=None) -> None:
+    """``weight_decay``: K values (a sequence, or a ``float_table``) or None; ``shards``: K bf16 tensors or None."""
+    if weight_decay is not None and not isinstance(weight_decay, ctypes.Array):
+        weight_decay = float_table(weight_decay)
+    _check(lib().tide_adamw(t, _ptr_array(params), _ptr_array(grads), _ptr_array(exp_avg), _ptr_array(exp_avg_sq),
+                            None if shards is None else _ptr_array(shards), weight_decay, lr, betas[0], betas[1], eps, step,
+                            None if norm is None else _ptr(norm), max_norm, flags, _stream(stream)), "tide_adamw")
+
+
+# ---- convenience objects ----------------------------------------------------------------------
 
 
 class Group:
@@ -453,3 +556,122 @@ class Group:
 
     def set_debug(self, flags: int) -> None:
         tide_group_set_debug(self.handle, flags)
+
+    # ---- the sharded training step ----
+
+    def _want(self, ok: bool, where: str, what: str) -> None:
+        if not ok:
+            raise TideError(TIDE_EINVAL, f"{where}: {what}")
+
+    def embedding(self, p: int, shards: Sequence, ids, out, scale: float = 1.0, stream=None) -> None:
+        """Rows ``ids`` of parameter p read from the R bf16 ``shards``, times ``scale``, into ``out``
+        (``ids.numel()`` rows: ``[n, L]``, or contiguous ``[..., L]``)."""
+        self._want(len(shards) == self.R, "embedding", f"{self.R} shards are needed")
+        self._check_rows("embedding", p, ids, out)
+        tide_embedding(self.handle, p, shards, ids, out, scale, stream)
+
+    def embedding_grad_workspace(self, p: int, n: int):
+        """A device buffer that ``embedding_grad`` can work in for up to ``n`` positions."""
+        import torch
+
+        return torch.empty(tide_embedding_grad_workspace(self.handle, p, n), dtype=torch.uint8, device="cuda")
+
+    def embedding_grad(self, p: int, ids: Sequence, douts: Sequence, shards: Sequence, scale: float = 1.0,
+                       accumulate: bool = False, workspace=None, stream=None) -> None:
+        """The lookup's gradient into the R fp32 ``shards``: ``ids`` and ``douts`` are lists of batches.
+        Without a ``workspace`` one is allocated for the call."""
+        where = "embedding_grad"
+        self._want(len(shards) == self.R, where, f"{self.R} shards are needed")
+        self._want(len(ids) == len(douts) > 0, where, "one dout for each batch of ids, and one batch at least")
+        for i, x in zip(ids, douts):
+            self._check_rows(where, p, i, x)
+            self._want(i.dtype == ids[0].dtype and x.dtype == douts[0].dtype, where, "the batches differ in type")
+        if workspace is None:
+            import torch
+
+            workspace = self.embedding_grad_workspace(p, sum(x.numel() for x in ids))
+            if stream is not None:
+                s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+                s.wait_stream(torch.cuda.current_stream())
+                workspace.record_stream(s)
+        tide_embedding_grad(self.handle, p, ids, douts, shards, workspace, scale, accumulate, stream)
+
+    def _check_rows(self, where: str, p: int, ids, rows) -> None:
+        self._want(0 <= p < self.P, where, "no such parameter")
+        n, length = ids.numel(), self.row_len[p]
+        self._want(ids.is_contiguous(), where, "ids are not contiguous")
+        ok = rows.dim() >= 1 and rows.shape[-1] == length and rows.numel() == n * length
+        ok = ok and (rows.is_contiguous() or (rows.dim() == 2 and (length == 1 or rows.stride(1) == 1) and rows.stride(0) >= length))
+        self._want(ok, where, f"{n} rows of {length} elements are needed")
+
+    def pieces(self, buffers: Sequence) -> list:
+        """The valid rows of every (rank, parameter) piece of R shard buffers, as R*P views in the order
+        d*P + p: the tensors of a ``TensorList`` over the group's shards."""
+        out = []
+        for d in range(self.R):
+            for p in range(self.P):
+                o = self.param_layout(p)[1]
+                out.append(buffers[d][o:o + self.valid_rows(d, p) * self.row_len[p]])
+        return out
+
+
+class TensorList:
+    """Owns one ``tide_tensors_t``: K tensors of ``elems[k]`` elements whose gradients are of
+    ``types[k]`` (``TIDE_F32``, the default, or ``TIDE_BF16``).  Its calls take K tensors each, or the
+    ``pointer_table`` of them."""
+
+    def __init__(self, elems: Sequence[int], types=None):
+        self.elems = [int(n) for n in elems]
+        self.K = len(self.elems)
+        self.handle = None
+        self.handle = tide_tensors_create(self.elems, types)
+
+    def close(self) -> None:
+        if self.handle:
+            tide_tensors_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def _tensors(self, where: str, xs):
+        """xs, once its count (and, for tensors, their sizes) are those of the list."""
+        if len(xs) != self.K:
+            raise TideError(TIDE_EINVAL, f"{where}: {self.K} tensors are needed")
+        if not isinstance(xs, ctypes.Array):
+            for n, x in zip(self.elems, xs):
+                if not isinstance(x, int) and (x.numel() != n or not x.is_contiguous()):
+                    raise TideError(TIDE_EINVAL, f"{where}: a contiguous tensor of {n} elements is needed")
+        return xs
+
+    def grad_norm(self, grads, norm, sumsq=None, stream=None) -> None:
+        tide_grad_norm(self.handle, self._tensors("grad_norm", grads), norm, sumsq, stream)
+
+    def clip_grads(self, grads, norm, max_norm: float, stream=None) -> None:
+        tide_clip_grads(self.handle, self._tensors("clip_grads", grads), norm, max_norm, stream)
+
+    def clip_grad_norm(self, grads, max_norm: float, norm, stream=None) -> None:
+        tide_clip_grad_norm(self.handle, self._tensors("clip_grad_norm", grads), max_norm, norm, stream)
+
+    def adamw(self, params, grads, exp_avg, exp_avg_sq, shards=None, *, weight_decay=None, stream=None, **hyper) -> None:
+        """One step; ``lr``, ``betas``, ``eps``, ``step``, ``norm``, ``max_norm`` and ``flags`` as ``tide_adamw``.
+        ``weight_decay``: one number for all tensors, K of them, or a ``float_table``."""
+        where = "adamw"
+        for xs in (params, grads, exp_avg, exp_avg_sq):
+            self._tensors(where, xs)
+        if shards is not None:
+            self._tensors(where, shards)
+        if isinstance(weight_decay, (int, float)):
+            weight_decay = [weight_decay] * self.K
+        if weight_decay is not None and len(weight_decay) != self.K:
+            raise TideError(TIDE_EINVAL, f"{where}: {self.K} weight decays are needed")
+        tide_adamw(self.handle, params, grads, exp_avg, exp_avg_sq, shards, weight_decay=weight_decay, stream=stream, **hyper)

@@ -1,0 +1,103 @@
+// Internal declarations of the sharded training step: embedding lookup and gradient over the shards,
+// and the operators over lists of tensors.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace tide {
+
+// ---- embedding -------------------------------------------------------------------------------
+constexpr int kInlineRanks = 64;    // shard pointers that travel with a launch
+constexpr int kInlineBatches = 64;  // batches that travel with a launch
+
+// The R shard pointers of a call: in the launch's own parameters up to kInlineRanks, else in a device
+// table.
+struct ShardPtrs {
+    void* p[kInlineRanks];
+    void* const* table;  // nullptr: use p
+};
+
+// Where a parameter lies in the shards (group layout).
+struct TableView {
+    uint32_t rows;    // rows_p
+    uint32_t m;       // m_p
+    int64_t len;      // L_p
+    int64_t off;      // o_p
+    int32_t R;
+};
+
+// The positions of up to kInlineBatches batches, in order.
+struct Batches {
+    const void* ids[kInlineBatches];
+    const char* dout[kInlineBatches];
+    int64_t stride[kInlineBatches];         // bytes between dout rows
+    uint32_t start[kInlineBatches + 1];     // first position of every batch, and the end
+    int32_t count;
+    int32_t ids64;
+};
+
+cudaError_t launch_embedding(const ShardPtrs& shards, const TableView& tv, const void* ids, int ids64, int64_t n,
+                             float scale, void* out, int out_bf16, int64_t out_stride, int ctas, int* status,
+                             cudaStream_t stream);
+
+// Workspace of the gradient, carved from the caller's buffer.
+struct GradWorkspace {
+    uint32_t* keys;      // [N] sorted rows (rows = no token)
+    uint64_t* src;       // [N] dout row addresses in the same order
+    uint32_t* key_a;     // [N] intermediate sort passes
+    uint32_t* key_b;
+    uint32_t* idx_a;
+    uint32_t* idx_b;
+    uint32_t* pre_key;   // [N] rows and addresses expanded before the sort, when there are more than
+    uint64_t* pre_src;   //     kInlineBatches batches
+};
+// Carves the workspace for n positions at `base` (any pointer, also null) and returns its size.
+size_t carve_grad_workspace(char* base, int64_t n, GradWorkspace* w);
+
+cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t rows, const GradWorkspace& w,
+                                    int* status, cudaStream_t stream);
+cudaError_t launch_sort_positions(const Batches& b, bool expanded, uint32_t n, uint32_t rows, const GradWorkspace& w,
+                                  int* status, cudaStream_t stream);
+cudaError_t launch_zero_table(const ShardPtrs& shards, const TableView& tv, int ctas, cudaStream_t stream);
+cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, uint32_t n, const GradWorkspace& w,
+                                 int dout_bf16, float scale, int accumulate, int ctas, cudaStream_t stream);
+
+// ---- lists of tensors -------------------------------------------------------------------------
+constexpr int64_t kTsChunk = 2048;  // elements of one work item
+constexpr int kTsThreads = 256;
+constexpr int kTsCtasPerSm = 4;
+
+struct TsSeg {
+    int64_t elems;
+    int64_t chunk_begin;  // index of the tensor's first work item
+    int32_t bf16;         // the gradient's type
+    int32_t pad_;
+};
+
+struct AdamwArgs {
+    float beta1, one_minus_beta1, beta2, one_minus_beta2, eps, step_size, inv_sqrt_c2;
+    const float* norm;  // nullptr: no clipping
+    float max_norm;
+    int skip_nonfinite;
+};
+
+struct TsList {
+    const TsSeg* segs;
+    const int32_t* chunk_seg;  // tensor of every work item
+    int64_t chunks;
+    int32_t K;
+};
+
+cudaError_t launch_grad_norm(const TsList& l, const void* const* grads, double* partial, unsigned* ticket, float* norm,
+                             double* sumsq, int ctas, cudaStream_t stream);
+cudaError_t launch_clip(const TsList& l, void* const* grads, const float* norm, float max_norm, int ctas,
+                        cudaStream_t stream);
+// tables: K pointers each of params, grads, exp_avg, exp_avg_sq and shards (shards unused when
+// write_shards is 0), then K floats 1 - lr * weight_decay.
+cudaError_t launch_adamw(const TsList& l, void* const* tables, int write_shards, const AdamwArgs& a, int ctas,
+                         cudaStream_t stream);
+
+}  // namespace tide

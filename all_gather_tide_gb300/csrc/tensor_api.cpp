@@ -1,0 +1,236 @@
+// C ABI of the operators over lists of tensors: the list object, argument checks and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+#include <vector>
+
+#include "api_common.h"
+#include "step_internal.h"
+#include "table_ring.h"
+
+// The list behind tide_tensors_t.
+struct tide_tensors {
+    int32_t K = 0;
+    std::vector<int64_t> elems;
+    std::vector<uint8_t> bf16;
+    int64_t chunks = 0;
+    int device = 0;
+    int sm_count = 0;
+    char* d_block = nullptr;  // tickets, partial sums, segs and chunk_seg in one allocation
+    unsigned* d_ticket = nullptr;  // one per ring slot
+    double* d_partial = nullptr;   // max_ctas per ring slot
+    tide::TsSeg* d_segs = nullptr;
+    int32_t* d_chunk_seg = nullptr;
+    tide::TableRing ring;
+    std::mutex mu;
+
+    int max_ctas() const { return sm_count * tide::kTsCtasPerSm; }
+    tide::TsList list() const { return {d_segs, d_chunk_seg, chunks, K}; }
+};
+
+namespace {
+
+using tide::aligned;
+using tide::no_throw;
+
+constexpr int64_t kMaxElems = int64_t(1) << 42;
+
+void release(tide_tensors* t) {
+    t->ring.release();
+    if (t->d_block) cudaFree(t->d_block);
+    delete t;
+}
+
+// Appends K pointers to `table`, checking those of the tensors that have elements.
+int add_pointers(const tide_tensors* t, const void* const* ptrs, size_t elem, std::vector<const void*>* table) {
+    for (int k = 0; k < t->K; ++k) {
+        if (t->elems[k] > 0 && (!ptrs[k] || !aligned(ptrs[k], elem ? elem : t->bf16[k] ? 2 : 4))) return TIDE_EINVAL;
+        table->push_back(ptrs[k]);
+    }
+    return TIDE_OK;
+}
+
+int upload_grads(tide_tensors* t, const void* const* grads, cudaStream_t st, int* slot) {
+    std::vector<const void*> table;
+    table.reserve(size_t(t->K));
+    int rc = add_pointers(t, grads, 0, &table);
+    if (rc != TIDE_OK) return rc;
+    if ((rc = tide::check_device(t->device)) != TIDE_OK) return rc;
+    TIDE_CUDA(t->ring.upload(table, st, slot));
+    return TIDE_OK;
+}
+
+int norm_in_slot(tide_tensors* t, int slot, float* norm, double* sumsq, cudaStream_t st) {
+    TIDE_CUDA(tide::launch_grad_norm(t->list(), t->ring.slots[slot].dev, t->d_partial + int64_t(slot) * t->max_ctas(),
+                                     t->d_ticket + slot, norm, sumsq, t->max_ctas(), st));
+    return TIDE_OK;
+}
+
+int clip_in_slot(tide_tensors* t, int slot, const float* norm, float max_norm, cudaStream_t st) {
+    TIDE_CUDA(tide::launch_clip(t->list(), t->ring.slots[slot].dev, norm, max_norm, t->max_ctas(), st));
+    return TIDE_OK;
+}
+
+// Marks the slot's table as in use by what `st` holds, and passes on the launches' status.
+int finish(tide_tensors* t, int slot, cudaStream_t st, int rc) {
+    const cudaError_t e = t->ring.finish(slot, st);
+    return rc != TIDE_OK ? rc : e == cudaSuccess ? TIDE_OK : tide::record_cuda_error(e);
+}
+
+bool bad_max_norm(float v) { return !(v >= 0.0f); }  // NaN too
+
+}  // namespace
+
+extern "C" {
+
+int tide_tensors_create(tide_tensors_t* out, int32_t K, const int64_t* elems, const int32_t* types) {
+    return no_throw([&]() -> int {
+        if (!out) return TIDE_EINVAL;
+        *out = nullptr;
+        if (!elems || K < 1) return TIDE_EINVAL;
+        if (K > TIDE_MAX_TABLE / 8) return TIDE_ERANGE;
+        std::vector<tide::TsSeg> segs(static_cast<size_t>(K));
+        std::vector<uint8_t> bf16(static_cast<size_t>(K));
+        int64_t chunks = 0, total = 0;
+        for (int k = 0; k < K; ++k) {
+            if (elems[k] < 0) return TIDE_EINVAL;
+            if (types && types[k] != TIDE_F32 && types[k] != TIDE_BF16) return TIDE_EINVAL;
+            if (elems[k] > kMaxElems || (total += elems[k]) > kMaxElems) return TIDE_ERANGE;
+            bf16[size_t(k)] = types && types[k] == TIDE_BF16;
+            segs[size_t(k)] = {elems[k], chunks, bf16[size_t(k)], 0};
+            chunks += (elems[k] + tide::kTsChunk - 1) / tide::kTsChunk;
+        }
+        std::vector<int32_t> chunk_seg;
+        chunk_seg.reserve(size_t(chunks));
+        for (int k = 0; k < K; ++k)
+            chunk_seg.insert(chunk_seg.end(), size_t((k + 1 < K ? segs[size_t(k) + 1].chunk_begin : chunks) - segs[size_t(k)].chunk_begin), k);
+
+        tide_tensors* t = new tide_tensors();
+        t->K = K;
+        t->chunks = chunks;
+        cudaError_t e;
+        try {
+            t->elems.assign(elems, elems + K);
+            t->bf16 = std::move(bf16);
+            e = cudaGetDevice(&t->device);
+            if (e == cudaSuccess) e = cudaDeviceGetAttribute(&t->sm_count, cudaDevAttrMultiProcessorCount, t->device);
+            const size_t ticket_bytes = 256, partial_bytes = size_t(tide::kSlots) * size_t(t->max_ctas()) * sizeof(double);
+            const size_t seg_bytes = segs.size() * sizeof(tide::TsSeg);
+            if (e == cudaSuccess) e = cudaMalloc(&t->d_block, ticket_bytes + partial_bytes + seg_bytes + chunk_seg.size() * 4 + 8);
+            if (e == cudaSuccess) {
+                t->d_ticket = reinterpret_cast<unsigned*>(t->d_block);
+                t->d_partial = reinterpret_cast<double*>(t->d_block + ticket_bytes);
+                t->d_segs = reinterpret_cast<tide::TsSeg*>(t->d_block + ticket_bytes + partial_bytes);
+                t->d_chunk_seg = reinterpret_cast<int32_t*>(t->d_block + ticket_bytes + partial_bytes + seg_bytes);
+                e = cudaMemset(t->d_ticket, 0, ticket_bytes);
+            }
+            if (e == cudaSuccess) e = cudaMemcpy(t->d_segs, segs.data(), seg_bytes, cudaMemcpyHostToDevice);
+            if (e == cudaSuccess && !chunk_seg.empty())
+                e = cudaMemcpy(t->d_chunk_seg, chunk_seg.data(), chunk_seg.size() * 4, cudaMemcpyHostToDevice);
+            // five pointers and a factor for every tensor
+            if (e == cudaSuccess) e = t->ring.create(size_t(K) * 6);
+        } catch (...) {
+            release(t);
+            throw;
+        }
+        if (e != cudaSuccess) {
+            release(t);
+            tide::record_cuda_error(e);
+            return e == cudaErrorMemoryAllocation ? TIDE_ENOMEM : TIDE_ECUDA;
+        }
+        *out = t;
+        return TIDE_OK;
+    });
+}
+
+int tide_tensors_destroy(tide_tensors_t t) {
+    if (t) release(t);
+    return TIDE_OK;
+}
+
+int tide_grad_norm(tide_tensors_t t, const void* const* grads, float* norm, double* sumsq, void* stream) {
+    return no_throw([&]() -> int {
+        if (!t || !grads || !norm || !aligned(norm, 4) || !aligned(sumsq, 8)) return TIDE_EINVAL;
+        std::lock_guard<std::mutex> lock(t->mu);
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        int slot;
+        const int rc = upload_grads(t, grads, st, &slot);
+        if (rc != TIDE_OK) return rc;
+        return finish(t, slot, st, norm_in_slot(t, slot, norm, sumsq, st));
+    });
+}
+
+int tide_clip_grads(tide_tensors_t t, void* const* grads, const float* norm, float max_norm, void* stream) {
+    return no_throw([&]() -> int {
+        if (!t || !grads || !norm || !aligned(norm, 4) || bad_max_norm(max_norm)) return TIDE_EINVAL;
+        std::lock_guard<std::mutex> lock(t->mu);
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        int slot;
+        const int rc = upload_grads(t, grads, st, &slot);
+        if (rc != TIDE_OK) return rc;
+        return finish(t, slot, st, clip_in_slot(t, slot, norm, max_norm, st));
+    });
+}
+
+int tide_clip_grad_norm(tide_tensors_t t, void* const* grads, float max_norm, float* norm, void* stream) {
+    return no_throw([&]() -> int {
+        if (!t || !grads || !norm || !aligned(norm, 4) || bad_max_norm(max_norm)) return TIDE_EINVAL;
+        std::lock_guard<std::mutex> lock(t->mu);
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        int slot;
+        int rc = upload_grads(t, grads, st, &slot);
+        if (rc != TIDE_OK) return rc;
+        rc = norm_in_slot(t, slot, norm, nullptr, st);
+        if (rc == TIDE_OK) rc = clip_in_slot(t, slot, norm, max_norm, st);
+        return finish(t, slot, st, rc);
+    });
+}
+
+int tide_adamw(tide_tensors_t t, void* const* params, const void* const* grads, void* const* exp_avg,
+               void* const* exp_avg_sq, void* const* shards, const float* weight_decay, double lr, double beta1,
+               double beta2, double eps, int64_t step, const float* norm, float max_norm, uint32_t flags,
+               void* stream) {
+    return no_throw([&]() -> int {
+        if (!t || !params || !grads || !exp_avg || !exp_avg_sq || (flags & ~uint32_t(TIDE_ADAMW_SKIP_NONFINITE))) return TIDE_EINVAL;
+        if (!(lr >= 0) || !std::isfinite(lr) || !(eps >= 0) || !std::isfinite(eps) || step < 1) return TIDE_EINVAL;
+        if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1)) return TIDE_EINVAL;
+        if (norm && (!aligned(norm, 4) || bad_max_norm(max_norm))) return TIDE_EINVAL;
+        std::lock_guard<std::mutex> lock(t->mu);
+        const size_t K = size_t(t->K);
+        std::vector<const void*> table;
+        table.reserve(6 * K);
+        int rc = add_pointers(t, params, 4, &table);
+        if (rc == TIDE_OK) rc = add_pointers(t, grads, 0, &table);
+        if (rc == TIDE_OK) rc = add_pointers(t, exp_avg, 4, &table);
+        if (rc == TIDE_OK) rc = add_pointers(t, exp_avg_sq, 4, &table);
+        if (rc == TIDE_OK && shards) rc = add_pointers(t, shards, 2, &table);
+        if (rc != TIDE_OK) return rc;
+        table.resize(6 * K, nullptr);
+        float* keep = reinterpret_cast<float*>(table.data() + 5 * K);
+        for (size_t k = 0; k < K; ++k) {
+            const float d = weight_decay ? weight_decay[k] : 0.0f;
+            if (!(d >= 0) || !std::isfinite(d)) return TIDE_EINVAL;
+            keep[k] = float(1.0 - lr * double(d));
+        }
+        if ((rc = tide::check_device(t->device)) != TIDE_OK) return rc;
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        tide::AdamwArgs a{};
+        a.beta1 = float(beta1);
+        a.one_minus_beta1 = float(1.0 - beta1);
+        a.beta2 = float(beta2);
+        a.one_minus_beta2 = float(1.0 - beta2);
+        a.eps = float(eps);
+        a.step_size = float(lr / (1.0 - std::pow(beta1, double(step))));
+        a.inv_sqrt_c2 = float(1.0 / std::sqrt(1.0 - std::pow(beta2, double(step))));
+        a.norm = norm;
+        a.max_norm = max_norm;
+        a.skip_nonfinite = (flags & TIDE_ADAMW_SKIP_NONFINITE) ? 1 : 0;
+        int slot;
+        TIDE_CUDA(t->ring.upload(table, st, &slot));
+        const cudaError_t e = tide::launch_adamw(t->list(), t->ring.slots[slot].dev, shards ? 1 : 0, a, t->max_ctas(), st);
+        return finish(t, slot, st, e == cudaSuccess ? TIDE_OK : tide::record_cuda_error(e));
+    });
+}
+
+}  // extern "C"

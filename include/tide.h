@@ -30,7 +30,8 @@
  *   - The caller owns every device buffer.  A group owns only its plan tables (device), a small
  *     ring of pinned host / device pointer tables and CUDA events; tide_group_destroy frees them.
  *   - A group may be used from several host threads; calls on one group are serialised.
- *   - Inputs and outputs of one call must not overlap.  Nothing here traps on the device.
+ *   - Inputs and outputs of one call must not overlap (those a call updates in place are one buffer).
+ *     Nothing here traps on the device.
  */
 #ifndef TIDE_H
 #define TIDE_H
@@ -269,7 +270,8 @@ int tide_group_set_wait_timeout(tide_group_t g, uint64_t timeout_ns);
 /* Reads the group's device status word (0 = no wait expired; 1 = a reduce-scatter consumer wait
  * expired, 2 = a reduce-scatter producer wait expired, 4 = draining copies after an abort expired,
  * 8 = a placement load wait expired, 16 / 32 = TIDE_RS_TMEM: a consumer's wait for a drained Tensor
- * Memory buffer / a writer's wait for a filled one expired) and clears it.
+ * Memory buffer / a writer's wait for a filled one expired, 64 = an embedding call met an id >= the
+ * table's rows) and clears it.
  * Synchronous: copies from the device. */
 int tide_group_device_status(tide_group_t g, int32_t *status);
 
@@ -355,6 +357,140 @@ int tide_group_last_ce_copies(tide_group_t g, int64_t *copies, int32_t *uniform_
  */
 int tide_reduce_scatter_noalloc(int32_t R, int32_t P, const int64_t *rows, const int64_t *row_len,
                                 const void *const *grads, void *const *shards, void *stream);
+
+/* ---- the sharded training step ------------------------------------------------------------- */
+/*
+ * What a training step does between the reduce-scatter and the next all-gather, on the same shards:
+ * the embedding rows are read from the ranks' bf16 shards where they lie, the embedding's gradient
+ * is summed straight into the ranks' fp32 shards, the gradients' global norm is taken over many
+ * tensors and bounds them, and AdamW updates the fp32 shards and writes the bf16 shards that the
+ * next lookup and all-gather read.  (The paper has no counterpart: its collectives produce and
+ * consume these shards.)
+ */
+/* Element types of the calls below. */
+#define TIDE_F32 0
+#define TIDE_BF16 1
+#define TIDE_I32 2
+#define TIDE_I64 3
+
+/*
+ * tide_embedding — rows of parameter p read from the packed bf16 shards, without gathering it:
+ *     out[i*out_stride + j] = scale * shard_d[o_p + (t - d*m_p)*L_p + j],  t = ids[i],  d = t / m_p
+ * for 0 <= i < n, 0 <= j < L_p, the product in fp32, rounded once to out's type.  An id outside
+ * [0, rows_p) reads nothing and gives a row of +0 (a negative id marks a position without a token;
+ * an id >= rows_p also sets 64 in the group's device status word).  One token (n = 1) up to long
+ * prompts take the same call; n = 0 does nothing.
+ *   shards: host array of R device pointers, entry d = rank d's packed bf16 shard (S elements).  Up
+ *           to 64 ranks they travel with the launch, so the call can be captured into a CUDA graph.
+ *   ids:    device array of n ids of ids_type (TIDE_I32 or TIDE_I64).
+ *   out:    device, n rows of L_p elements of out_type (TIDE_BF16 or TIDE_F32), row i at element
+ *           i*out_stride (out_stride >= L_p).
+ * Any element alignment of shards, out and out_stride is accepted.  Asynchronous on `stream`.
+ * Errors: TIDE_EINVAL (null or misaligned pointers, p or n or a type or out_stride out of range,
+ * another device current), TIDE_ERANGE (rows_p > 2^31 - 2, or n*L_p overflows), TIDE_ECUDA.
+ */
+int tide_embedding(tide_group_t g, int32_t p, const void *const *shards, const void *ids, int32_t ids_type,
+                   int64_t n, float scale, void *out, int32_t out_type, int64_t out_stride, void *stream);
+
+/* Bytes of device workspace (256-byte aligned) that tide_embedding_grad needs on g for parameter p and n
+ * positions in all.  Errors: TIDE_EINVAL, TIDE_ERANGE (as tide_embedding_grad). */
+int tide_embedding_grad_workspace(tide_group_t g, int32_t p, int64_t n, int64_t *bytes);
+
+/*
+ * tide_embedding_grad — the lookup's gradient, summed by token straight into the fp32 shards.  The
+ * positions of B batches (one for each contributing rank, say; batch b has n[b] of them), in order:
+ *     shard_d[o_p + (t - d*m_p)*L_p + j] (+)= scale * sum over positions (b, i) with ids_b[i] = t of
+ *                                             dout_b[i*dout_stride[b] + j]
+ * for every row t < rows_p, d = t / m_p.  With accumulate = 0 the whole piece [o_p, o_p + s_p) of
+ * every shard is overwritten, rows without a token and the padding with +0.0f; with accumulate = 1
+ * the sums are added to what is there (a table that also has a gradient from elsewhere), and nothing
+ * but the rows that have a token is touched.  Other parameters' pieces are never touched.  Sums are
+ * fp32 in an order that depends on the ids alone, so equal calls give equal bits: the positions are
+ * sorted by token (stably), each token's are added in order within fixed stretches of the sorted
+ * list, the stretches' sums in order, and the total is scaled once.  Ids outside [0, rows_p) are
+ * skipped (their dout rows are not read), as in tide_embedding.
+ *   n, ids, douts, dout_stride: host arrays of B entries; ids_b and dout_b device pointers (null
+ *           only where n[b] = 0), dout_b rows of L_p elements of dout_type (TIDE_BF16 or TIDE_F32)
+ *           dout_stride[b] >= L_p elements apart.
+ *   shards: host array of R device pointers, entry d = rank d's fp32 shard of S elements.
+ *   workspace: device, 256-byte aligned, at least tide_embedding_grad_workspace's bytes for
+ *           n[0] + ... + n[B-1]; holds nothing between calls, not shared by calls that overlap.
+ * Asynchronous on `stream`.  Errors: TIDE_EINVAL (null or misaligned pointers, p, B, n, a type or a
+ * stride out of range, the workspace too small, another device current), TIDE_ERANGE (rows_p > 2^31 - 2,
+ * more than 2^31 - 2^16 positions, or B > TIDE_MAX_TABLE / 8), TIDE_ECUDA.
+ */
+int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t *n, const void *const *ids,
+                        int32_t ids_type, const void *const *douts, const int64_t *dout_stride, int32_t dout_type,
+                        float scale, int32_t accumulate, void *const *shards, void *workspace,
+                        int64_t workspace_bytes, void *stream);
+
+/*
+ * A list of K tensors that one launch walks: elems[k] >= 0 contiguous elements each (0: skipped, its
+ * pointers may be null).  types[k] is the type of tensor k's gradient, TIDE_F32 (a reduce-scatter's
+ * shard, or the valid rows of one parameter's piece of it) or TIDE_BF16 (a parameter's gradient
+ * before it); types = NULL means TIDE_F32 for all.  The list owns its work tables, a ring of pointer
+ * tables and the norm's partial sums; like a group it belongs to the device current at creation,
+ * its calls are serialised, and calls on different streams may overlap.  Tensor pointers need the
+ * alignment of their element; those whose addresses agree modulo 8 elements move in vectors.
+ * Errors: TIDE_EINVAL (null, K < 1, elems < 0, unknown type), TIDE_ERANGE (K > TIDE_MAX_TABLE / 8 or more
+ * than 2^42 elements), TIDE_ENOMEM, TIDE_ECUDA.
+ */
+typedef struct tide_tensors *tide_tensors_t;
+int tide_tensors_create(tide_tensors_t *out, int32_t K, const int64_t *elems, const int32_t *types);
+/* Frees the list after waiting for its own work in flight.  NULL is accepted. */
+int tide_tensors_destroy(tide_tensors_t t);
+
+/*
+ * tide_grad_norm — the global 2-norm over all tensors of the list:
+ *     norm[0] = sqrt(sum over k, i of grads_k[i]^2)
+ * Squares are summed in fp32 over 32 elements and in fp64 beyond, in a fixed order; squares that
+ * would leave fp32's range are summed in fp64, so neither large nor tiny gradients overflow or
+ * vanish.  NaN or infinite gradients give a NaN or infinite norm.
+ *   grads: host array of K device pointers.   norm: device fp32.
+ *   sumsq: device fp64 or NULL; receives the sum of squares (what ranks add up across GPUs).
+ * Errors: TIDE_EINVAL (null or misaligned pointers, another device current), TIDE_ECUDA.
+ */
+int tide_grad_norm(tide_tensors_t t, const void *const *grads, float *norm, double *sumsq, void *stream);
+
+/*
+ * tide_clip_grads — scales every gradient in place by c = min(1, max_norm / (norm[0] + 1e-6)), c in
+ * fp32, products in fp32 rounded once to the gradient's type.  The norm is read on the device, so
+ * nothing waits for the host.  With c = 1 nothing is written; a NaN norm makes every gradient NaN
+ * and an infinite one makes them 0 (NaN where they were infinite or NaN).  max_norm >= 0.
+ */
+int tide_clip_grads(tide_tensors_t t, void *const *grads, const float *norm, float max_norm, void *stream);
+
+/* tide_clip_grad_norm — tide_grad_norm into norm (the value before clipping), then tide_clip_grads. */
+int tide_clip_grad_norm(tide_tensors_t t, void *const *grads, float max_norm, float *norm, void *stream);
+
+/* tide_adamw leaves everything unchanged when norm[0] is NaN or infinite. */
+#define TIDE_ADAMW_SKIP_NONFINITE 0x1u
+
+/*
+ * tide_adamw — one AdamW step (Loshchilov and Hutter, "Decoupled Weight Decay Regularization", 2019)
+ * over the list's tensors, with the clip factor folded in.  For every element, in fp32:
+ *     g = c * grad,  c = min(1, max_norm / (norm[0] + 1e-6)), or 1 without a norm
+ *     m = beta1 * m + (1 - beta1) * g
+ *     v = beta2 * v + (1 - beta2) * g * g
+ *     param = param * (1 - lr * weight_decay_k)
+ *             - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *     shard = bf16(param)    (round to nearest even)
+ * Factors of the hyperparameters are formed in double on the host and rounded once to fp32.
+ * Gradients are read only.
+ *   params, exp_avg (m), exp_avg_sq (v): host arrays of K device pointers, fp32, updated in place.
+ *   grads:  host array of K device pointers of the list's types.
+ *   shards: host array of K device pointers, bf16, written; or NULL.
+ *   weight_decay: host array of K values >= 0, or NULL for none.
+ *   norm:   device fp32 (tide_grad_norm's), or NULL for no clipping (max_norm is then not used).
+ *   step:   1 for the first step.   flags: TIDE_ADAMW_*.
+ * Errors: TIDE_EINVAL (null or misaligned pointers, lr or eps or weight_decay negative or not finite, a
+ * beta outside [0, 1), step < 1, max_norm < 0 or NaN, an unknown flag, another device current),
+ * TIDE_ECUDA.
+ */
+int tide_adamw(tide_tensors_t t, void *const *params, const void *const *grads, void *const *exp_avg,
+               void *const *exp_avg_sq, void *const *shards, const float *weight_decay, double lr, double beta1,
+               double beta2, double eps, int64_t step, const float *norm, float max_norm, uint32_t flags,
+               void *stream);
 
 /* ---- interference probes (measurement kernels of the interference harness) ----------------- */
 /*
