@@ -69,6 +69,7 @@ cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, u
 constexpr int64_t kTsChunk = 2048;  // elements of one work item
 constexpr int kTsThreads = 256;
 constexpr int kTsCtasPerSm = 4;
+constexpr int kAdamwCtasPerSm = 3;
 
 struct TsSeg {
     int64_t elems;

@@ -99,7 +99,8 @@ int tide_tensors_create(tide_tensors_t* out, int32_t K, const int64_t* elems, co
             if (elems[k] > kMaxElems || (total += elems[k]) > kMaxElems) return TIDE_ERANGE;
             bf16[size_t(k)] = types && types[k] == TIDE_BF16;
             segs[size_t(k)] = {elems[k], chunks, bf16[size_t(k)], 0};
-            chunks += (elems[k] + tide::kTsChunk - 1) / tide::kTsChunk;
+            // one item more than the elements fill, where the first may start up to 7 before the tensor
+            if (elems[k] > 0) chunks += (elems[k] + 7 + tide::kTsChunk - 1) / tide::kTsChunk;
         }
         std::vector<int32_t> chunk_seg;
         chunk_seg.reserve(size_t(chunks));
@@ -228,7 +229,7 @@ int tide_adamw(tide_tensors_t t, void* const* params, const void* const* grads, 
         a.skip_nonfinite = (flags & TIDE_ADAMW_SKIP_NONFINITE) ? 1 : 0;
         int slot;
         TIDE_CUDA(t->ring.upload(table, st, &slot));
-        const cudaError_t e = tide::launch_adamw(t->list(), t->ring.slots[slot].dev, shards ? 1 : 0, a, t->max_ctas(), st);
+        const cudaError_t e = tide::launch_adamw(t->list(), t->ring.slots[slot].dev, shards ? 1 : 0, a, t->sm_count * tide::kAdamwCtasPerSm, st);
         return finish(t, slot, st, e == cudaSuccess ? TIDE_OK : tide::record_cuda_error(e));
     });
 }

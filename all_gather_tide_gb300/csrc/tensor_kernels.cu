@@ -1,6 +1,11 @@
 // Operators over a list of tensors: global gradient norm, clipping, AdamW (sm_103a).
 //
-// A work item is kTsChunk elements of one tensor; one warp takes one item at a time.
+// A work item is kTsChunk consecutive elements of one tensor, and one warp takes one item at a time,
+// so that thousands of small tensors spread over the GPU as well as a few large ones.  Items are cut
+// on the tensor's own 8-element boundaries (32 bytes of fp32, 16 of bf16): item i covers elements
+// [i*kTsChunk - mis, (i+1)*kTsChunk - mis) of a tensor whose first element lies mis elements past a
+// boundary, so every group of 8 that lies inside the tensor is one aligned vector, and only the
+// groups at the tensor's ends go element by element.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -11,20 +16,21 @@ namespace tide {
 namespace {
 
 constexpr int kWarps = kTsThreads / 32;
+constexpr int kGroups = int(kTsChunk / 256);  // groups of 8 elements a lane has in an item
 
-// Elements [lo, hi) of tensor k that work item c covers.
 struct Item {
-    int k;
-    int64_t lo, hi;
-    bool bf16;
+    int k;         // tensor
+    int64_t i;     // item of the tensor
+    int64_t elems;
+    bool bf16;     // the gradient's type
 };
 
 __device__ __forceinline__ Item item_of(const TsList& l, int64_t c) {
     Item it;
     it.k = __ldg(&l.chunk_seg[c]);
     const TsSeg* s = l.segs + it.k;
-    it.lo = (c - __ldg(&s->chunk_begin)) * kTsChunk;
-    it.hi = min(__ldg(&s->elems), it.lo + kTsChunk);
+    it.i = c - __ldg(&s->chunk_begin);
+    it.elems = __ldg(&s->elems);
     it.bf16 = __ldg(&s->bf16) != 0;
     return it;
 }
@@ -32,8 +38,72 @@ __device__ __forceinline__ Item item_of(const TsList& l, int64_t c) {
 __device__ __forceinline__ int64_t first_item() { return int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); }
 __device__ __forceinline__ int64_t item_stride() { return int64_t(gridDim.x) * kWarps; }
 
-__device__ __forceinline__ float load_grad(const void* p, int64_t i, bool bf16) {
-    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+// Elements a pointer lies past a boundary of 8.
+template <typename T>
+__device__ __forceinline__ unsigned misalign(const T* p) {
+    return unsigned(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & 7u;
+}
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void narrow(float* p, float v) { *p = v; }
+__device__ __forceinline__ void narrow(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// 8 elements at an aligned address, not kept in L1.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+    uint32_t w[4];
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p)
+                 : "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(w[j] << 16);
+        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+    uint4 w;
+    __nv_bfloat162 h;
+    h = __floats2bfloat162_rn(x[0], x[1]), w.x = *reinterpret_cast<uint32_t*>(&h);
+    h = __floats2bfloat162_rn(x[2], x[3]), w.y = *reinterpret_cast<uint32_t*>(&h);
+    h = __floats2bfloat162_rn(x[4], x[5]), w.z = *reinterpret_cast<uint32_t*>(&h);
+    h = __floats2bfloat162_rn(x[6], x[7]), w.w = *reinterpret_cast<uint32_t*>(&h);
+    *reinterpret_cast<uint4*>(p) = w;
+}
+
+// The group of 8 elements from e on of a tensor of n: whole groups as a vector where `vec` says that
+// the array has the alignment, else element by element; elements outside the tensor read as 0 and
+// are not written.
+template <typename T>
+__device__ __forceinline__ void load_group(const T* p, int64_t e, int64_t n, bool vec, float (&x)[8]) {
+    if (vec && e >= 0 && e + 8 <= n) {
+        load8(p + e, x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = e + j >= 0 && e + j < n ? widen(p[e + j]) : 0.0f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_group(T* p, int64_t e, int64_t n, bool vec, const float (&x)[8]) {
+    if (vec && e >= 0 && e + 8 <= n) {
+        store8(p + e, x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (e + j >= 0 && e + j < n) narrow(p + e + j, x[j]);
+    }
 }
 
 // Sum over the CTA in a fixed order; valid in thread 0.
@@ -48,18 +118,56 @@ __device__ __forceinline__ double block_sum(double v) {
     return v;
 }
 
-__global__ void __launch_bounds__(kTsThreads)
+// The sum of squares of 32 numbers.  In fp32 while no square can have left its range: a sum in
+// [2^-100, 2^126] has lost at most 32 * 2^-150 to squares below the smallest subnormal.  Else, unless
+// all are 0, in fp64 (a rare branch; NaN and infinity take it and stay what they are).
+__device__ __forceinline__ double sum_squares(const float (&x)[4][8]) {
+    float s[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        s[q] = x[q][0] * x[q][0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) s[q] = fmaf(x[q][j], x[q][j], s[q]);
+    }
+    const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    if (sum >= 0x1p-100f && sum <= 0x1p126f) return double(sum);
+    double d = 0.0;
+    uint32_t any = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) any |= __float_as_uint(x[q][j]) << 1;
+    if (any)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d += double(x[q][j]) * double(x[q][j]);
+    return d;
+}
+
+template <typename T>
+__device__ __forceinline__ double item_squares(const T* g, const Item& it) {
+    const int64_t base = it.i * kTsChunk - misalign(g) + (threadIdx.x & 31) * 8;
+    double sum = 0.0;
+#pragma unroll
+    for (int h = 0; h < kGroups; h += 4) {
+        if (base + h * 256 >= it.elems) break;
+        float x[4][8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_group(g, base + (h + q) * 256, it.elems, true, x[q]);
+        sum += sum_squares(x);
+    }
+    return sum;
+}
+
+__global__ void __launch_bounds__(kTsThreads, kTsCtasPerSm)
 grad_norm_kernel(TsList l, const void* const* __restrict__ grads, double* partial, unsigned* ticket, float* norm,
                  double* sumsq) {
-    const int lane = threadIdx.x & 31;
     double sum = 0.0;
     for (int64_t c = first_item(); c < l.chunks; c += item_stride()) {
         const Item it = item_of(l, c);
         const void* g = grads[it.k];
-        for (int64_t i = it.lo + lane; i < it.hi; i += 32) {
-            const float v = load_grad(g, i, it.bf16);
-            sum += double(v) * double(v);
-        }
+        sum += it.bf16 ? item_squares(static_cast<const __nv_bfloat16*>(g), it) : item_squares(static_cast<const float*>(g), it);
     }
     sum = block_sum(sum);
     // the CTA that arrives last adds the CTAs' sums in their order
@@ -88,23 +196,74 @@ __device__ __forceinline__ float clip_factor(const float* norm, float max_norm) 
     return q >= 1.0f ? 1.0f : q;
 }
 
-__global__ void __launch_bounds__(kTsThreads)
-clip_kernel(TsList l, void* const* __restrict__ grads, const float* __restrict__ norm, float max_norm) {
-    const float f = clip_factor(norm, max_norm);
-    if (f == 1.0f) return;
-    const int lane = threadIdx.x & 31;
-    for (int64_t c = first_item(); c < l.chunks; c += item_stride()) {
-        const Item it = item_of(l, c);
-        void* g = grads[it.k];
-        for (int64_t i = it.lo + lane; i < it.hi; i += 32) {
-            const float v = load_grad(g, i, it.bf16) * f;
-            if (it.bf16) static_cast<__nv_bfloat16*>(g)[i] = __float2bfloat16_rn(v);
-            else static_cast<float*>(g)[i] = v;
+template <typename T>
+__device__ __forceinline__ void scale_item(T* g, const Item& it, float f) {
+    const int64_t base = it.i * kTsChunk - misalign(g) + (threadIdx.x & 31) * 8;
+#pragma unroll
+    for (int h = 0; h < kGroups; h += 4) {
+        if (base + h * 256 >= it.elems) break;
+        float x[4][8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_group(g, base + (h + q) * 256, it.elems, true, x[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[q][j] *= f;
+            store_group(g, base + (h + q) * 256, it.elems, true, x[q]);
         }
     }
 }
 
-__global__ void __launch_bounds__(kTsThreads)
+__global__ void __launch_bounds__(kTsThreads, kTsCtasPerSm)
+clip_kernel(TsList l, void* const* __restrict__ grads, const float* __restrict__ norm, float max_norm) {
+    const float f = clip_factor(norm, max_norm);
+    if (f == 1.0f) return;
+    // from the last item to the first: what the norm read last is what L2 still holds
+    for (int64_t c = l.chunks - 1 - first_item(); c >= 0; c -= item_stride()) {
+        const Item it = item_of(l, c);
+        void* g = grads[it.k];
+        if (it.bf16) scale_item(static_cast<__nv_bfloat16*>(g), it, f);
+        else scale_item(static_cast<float*>(g), it, f);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void adamw_item(const TsList& l, const AdamwArgs& a, void* const* tables, int write_shards, const Item& it,
+                                           float f) {
+    const int64_t K = l.K;
+    float* p = static_cast<float*>(tables[it.k]);
+    const T* g = static_cast<const T*>(tables[K + it.k]);
+    float* m = static_cast<float*>(tables[2 * K + it.k]);
+    float* v = static_cast<float*>(tables[3 * K + it.k]);
+    auto* w = static_cast<__nv_bfloat16*>(tables[4 * K + it.k]);
+    const float keep = __ldg(reinterpret_cast<const float*>(tables + 5 * K) + it.k);
+    const unsigned mis = misalign(p);
+    const bool gv = misalign(g) == mis, mv = misalign(m) == mis, vv = misalign(v) == mis, wv = misalign(w) == mis;
+    const int64_t base = it.i * kTsChunk - mis + (threadIdx.x & 31) * 8;
+    for (int q = 0; q < kGroups; ++q) {
+        const int64_t e = base + q * 256;
+        if (e >= it.elems) break;
+        float pi[8], gi[8], mi[8], vi[8];
+        load_group(p, e, it.elems, true, pi);
+        load_group(g, e, it.elems, gv, gi);
+        load_group(m, e, it.elems, mv, mi);
+        load_group(v, e, it.elems, vv, vi);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = gi[j] * f;
+            mi[j] = a.beta1 * mi[j] + a.one_minus_beta1 * x;
+            vi[j] = a.beta2 * vi[j] + a.one_minus_beta2 * x * x;
+            const float den = __fsqrt_rn(vi[j]) * a.inv_sqrt_c2 + a.eps;
+            pi[j] = pi[j] * keep - a.step_size * __fdiv_rn(mi[j], den);
+        }
+        store_group(m, e, it.elems, mv, mi);
+        store_group(v, e, it.elems, vv, vi);
+        store_group(p, e, it.elems, true, pi);
+        if (write_shards) store_group(w, e, it.elems, wv, pi);
+    }
+}
+
+__global__ void __launch_bounds__(kTsThreads, kAdamwCtasPerSm)
 adamw_kernel(TsList l, void* const* __restrict__ tables, int write_shards, AdamwArgs a) {
     float f = 1.0f;
     if (a.norm) {
@@ -112,27 +271,10 @@ adamw_kernel(TsList l, void* const* __restrict__ tables, int write_shards, Adamw
         if (a.skip_nonfinite && !isfinite(n)) return;
         f = clip_factor(a.norm, a.max_norm);
     }
-    const int lane = threadIdx.x & 31;
-    const float* decay = reinterpret_cast<const float*>(tables + int64_t(5) * l.K);
     for (int64_t c = first_item(); c < l.chunks; c += item_stride()) {
         const Item it = item_of(l, c);
-        float* p = static_cast<float*>(tables[it.k]);
-        const void* g = tables[l.K + it.k];
-        float* m = static_cast<float*>(tables[2 * int64_t(l.K) + it.k]);
-        float* v = static_cast<float*>(tables[3 * int64_t(l.K) + it.k]);
-        auto* w = static_cast<__nv_bfloat16*>(tables[4 * int64_t(l.K) + it.k]);
-        const float keep = decay[it.k];
-        for (int64_t i = it.lo + lane; i < it.hi; i += 32) {
-            const float x = load_grad(g, i, it.bf16) * f;
-            const float mi = a.beta1 * m[i] + a.one_minus_beta1 * x;
-            const float vi = a.beta2 * v[i] + a.one_minus_beta2 * x * x;
-            const float den = __fsqrt_rn(vi) * a.inv_sqrt_c2 + a.eps;
-            const float pi = p[i] * keep - a.step_size * __fdiv_rn(mi, den);
-            m[i] = mi;
-            v[i] = vi;
-            p[i] = pi;
-            if (write_shards) w[i] = __float2bfloat16_rn(pi);
-        }
+        if (it.bf16) adamw_item<__nv_bfloat16>(l, a, tables, write_shards, it, f);
+        else adamw_item<float>(l, a, tables, write_shards, it, f);
     }
 }
 
