@@ -163,20 +163,26 @@ def float_table(xs: Sequence[float]) -> ctypes.Array:
     return (ctypes.c_float * len(xs))(*xs)
 
 
-def _dtype_code(x) -> int:
-    import torch
+_codes = {}
 
-    code = {torch.float32: TIDE_F32, torch.bfloat16: TIDE_BF16, torch.int32: TIDE_I32, torch.int64: TIDE_I64}
-    if x.dtype not in code:
+
+def _dtype_code(x) -> int:
+    if not _codes:
+        import torch
+
+        _codes.update({torch.float32: TIDE_F32, torch.bfloat16: TIDE_BF16, torch.int32: TIDE_I32, torch.int64: TIDE_I64})
+    code = _codes.get(x.dtype)
+    if code is None:
         raise TideError(TIDE_EINVAL, f"a tensor of {x.dtype}")
-    return code[x.dtype]
+    return code
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building the stream object (3 us on Grace)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -465,6 +471,10 @@ def tide_adamw(t: int, params: Sequence, grads: Sequence, exp_avg: Sequence, exp
                             None if norm is None else _ptr(norm), max_norm, flags, _stream(stream)), "tide_adamw")
 
 
+def _refuse(where: str, what: str) -> None:
+    raise TideError(TIDE_EINVAL, f"{where}: {what}")
+
+
 # ---- convenience objects ----------------------------------------------------------------------
 
 
@@ -559,14 +569,11 @@ class Group:
 
     # ---- the sharded training step ----
 
-    def _want(self, ok: bool, where: str, what: str) -> None:
-        if not ok:
-            raise TideError(TIDE_EINVAL, f"{where}: {what}")
-
     def embedding(self, p: int, shards: Sequence, ids, out, scale: float = 1.0, stream=None) -> None:
         """Rows ``ids`` of parameter p read from the R bf16 ``shards``, times ``scale``, into ``out``
         (``ids.numel()`` rows: ``[n, L]``, or contiguous ``[..., L]``)."""
-        self._want(len(shards) == self.R, "embedding", f"{self.R} shards are needed")
+        if len(shards) != self.R:
+            _refuse("embedding", f"{self.R} shards are needed")
         self._check_rows("embedding", p, ids, out)
         tide_embedding(self.handle, p, shards, ids, out, scale, stream)
 
@@ -581,11 +588,14 @@ class Group:
         """The lookup's gradient into the R fp32 ``shards``: ``ids`` and ``douts`` are lists of batches.
         Without a ``workspace`` one is allocated for the call."""
         where = "embedding_grad"
-        self._want(len(shards) == self.R, where, f"{self.R} shards are needed")
-        self._want(len(ids) == len(douts) > 0, where, "one dout for each batch of ids, and one batch at least")
+        if len(shards) != self.R:
+            _refuse(where, f"{self.R} shards are needed")
+        if not len(ids) == len(douts) > 0:
+            _refuse(where, "one dout for each batch of ids, and one batch at least")
         for i, x in zip(ids, douts):
             self._check_rows(where, p, i, x)
-            self._want(i.dtype == ids[0].dtype and x.dtype == douts[0].dtype, where, "the batches differ in type")
+            if i.dtype != ids[0].dtype or x.dtype != douts[0].dtype:
+                _refuse(where, "the batches differ in type")
         if workspace is None:
             import torch
 
@@ -597,12 +607,15 @@ class Group:
         tide_embedding_grad(self.handle, p, ids, douts, shards, workspace, scale, accumulate, stream)
 
     def _check_rows(self, where: str, p: int, ids, rows) -> None:
-        self._want(0 <= p < self.P, where, "no such parameter")
+        if not 0 <= p < self.P:
+            _refuse(where, "no such parameter")
         n, length = ids.numel(), self.row_len[p]
-        self._want(ids.is_contiguous(), where, "ids are not contiguous")
-        ok = rows.dim() >= 1 and rows.shape[-1] == length and rows.numel() == n * length
-        ok = ok and (rows.is_contiguous() or (rows.dim() == 2 and (length == 1 or rows.stride(1) == 1) and rows.stride(0) >= length))
-        self._want(ok, where, f"{n} rows of {length} elements are needed")
+        if not ids.is_contiguous():
+            _refuse(where, "ids are not contiguous")
+        if rows.dim() < 1 or rows.shape[-1] != length or rows.numel() != n * length:
+            _refuse(where, f"{n} rows of {length} elements are needed")
+        if not rows.is_contiguous() and not (rows.dim() == 2 and (length == 1 or rows.stride(1) == 1) and rows.stride(0) >= length):
+            _refuse(where, "rows are neither contiguous nor a row stride apart")
 
     def pieces(self, buffers: Sequence) -> list:
         """The valid rows of every (rank, parameter) piece of R shard buffers, as R*P views in the order
@@ -646,11 +659,11 @@ class TensorList:
     def _tensors(self, where: str, xs):
         """xs, once its count (and, for tensors, their sizes) are those of the list."""
         if len(xs) != self.K:
-            raise TideError(TIDE_EINVAL, f"{where}: {self.K} tensors are needed")
+            _refuse(where, f"{self.K} tensors are needed")
         if not isinstance(xs, ctypes.Array):
             for n, x in zip(self.elems, xs):
                 if not isinstance(x, int) and (x.numel() != n or not x.is_contiguous()):
-                    raise TideError(TIDE_EINVAL, f"{where}: a contiguous tensor of {n} elements is needed")
+                    _refuse(where, f"a contiguous tensor of {n} elements is needed")
         return xs
 
     def grad_norm(self, grads, norm, sumsq=None, stream=None) -> None:
@@ -673,5 +686,5 @@ class TensorList:
         if isinstance(weight_decay, (int, float)):
             weight_decay = [weight_decay] * self.K
         if weight_decay is not None and len(weight_decay) != self.K:
-            raise TideError(TIDE_EINVAL, f"{where}: {self.K} weight decays are needed")
+            _refuse(where, f"{self.K} weight decays are needed")
         tide_adamw(self.handle, params, grads, exp_avg, exp_avg_sq, shards, weight_decay=weight_decay, stream=stream, **hyper)

@@ -12,14 +12,15 @@ using tide::aligned;
 using tide::no_throw;
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 2;
+constexpr int64_t kMaxRowLen = int64_t(1) << 30;
 constexpr int64_t kMaxPositions = (int64_t(1) << 31) - (int64_t(1) << 16);
 
 int table_view(const tide_group* g, int32_t p, tide::TableView* tv) {
     if (p < 0 || p >= g->plan.P) return TIDE_EINVAL;
-    if (g->plan.rows[p] > kMaxRows) return TIDE_ERANGE;
+    if (g->plan.rows[p] > kMaxRows || g->plan.row_len[p] > kMaxRowLen) return TIDE_ERANGE;
     tv->rows = uint32_t(g->plan.rows[p]);
     tv->m = uint32_t(g->plan.m[p]);
-    tv->len = g->plan.row_len[p];
+    tv->len = uint32_t(g->plan.row_len[p]);
     tv->off = g->plan.o[p];
     tv->R = g->plan.R;
     return TIDE_OK;
@@ -29,8 +30,11 @@ int table_view(const tide_group* g, int32_t p, tide::TableView* tv) {
 // then, to be finished after the launches that read it).
 int shard_ptrs(tide_group* g, const void* const* shards, size_t elem, cudaStream_t st, tide::ShardPtrs* sp, int* slot) {
     const int R = g->plan.R;
-    for (int d = 0; d < R; ++d)
+    sp->bits = 0;
+    for (int d = 0; d < R; ++d) {
         if (!shards[d] || !aligned(shards[d], elem)) return TIDE_EINVAL;
+        sp->bits |= reinterpret_cast<uintptr_t>(shards[d]);
+    }
     *slot = -1;
     sp->table = nullptr;
     if (R <= tide::kInlineRanks) {
@@ -51,8 +55,9 @@ int finish(tide_group* g, int slot, cudaStream_t st, int rc) {
 }
 
 // CTAs the embedding kernels may use: everything, or the few of TIDE_FLAG_OVERLAP.
+bool overlap(const tide_group* g) { return (g->flags & TIDE_FLAG_OVERLAP) != 0; }
 int ctas_of(const tide_group* g, int per_sm) {
-    return (g->flags & TIDE_FLAG_OVERLAP) ? std::max(1, g->sm_count / 9) : std::max(1, g->sm_count * per_sm);
+    return overlap(g) ? std::max(1, g->sm_count / 9) : std::max(1, g->sm_count * per_sm);
 }
 
 size_t float_size(int32_t type) { return type == TIDE_F32 ? 4 : type == TIDE_BF16 ? 2 : 0; }
@@ -80,7 +85,7 @@ int tide_embedding(tide_group_t g, int32_t p, const void* const* shards, const v
         int slot;
         if ((rc = shard_ptrs(g, shards, 2, st, &sp, &slot)) != TIDE_OK) return rc;
         const cudaError_t e = tide::launch_embedding(sp, tv, ids, ids_type == TIDE_I64, n, scale, out, out_type == TIDE_BF16,
-                                                     out_stride, ctas_of(g, 8), g->d_status, st);
+                                                     out_stride, ctas_of(g, tide::kLookupCtasPerSm), overlap(g), g->d_status, st);
         return finish(g, slot, st, e == cudaSuccess ? TIDE_OK : tide::record_cuda_error(e));
     });
 }

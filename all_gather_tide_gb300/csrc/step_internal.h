@@ -11,6 +11,7 @@ namespace tide {
 
 // ---- embedding -------------------------------------------------------------------------------
 constexpr int kInlineRanks = 64;    // shard pointers that travel with a launch
+constexpr int kLookupCtasPerSm = 4;
 constexpr int kInlineBatches = 64;  // batches that travel with a launch
 
 // The R shard pointers of a call: in the launch's own parameters up to kInlineRanks, else in a device
@@ -18,13 +19,14 @@ constexpr int kInlineBatches = 64;  // batches that travel with a launch
 struct ShardPtrs {
     void* p[kInlineRanks];
     void* const* table;  // nullptr: use p
+    uintptr_t bits;      // all addresses, or'ed: what they are all aligned to
 };
 
 // Where a parameter lies in the shards (group layout).
 struct TableView {
     uint32_t rows;    // rows_p
     uint32_t m;       // m_p
-    int64_t len;      // L_p
+    uint32_t len;     // L_p
     int64_t off;      // o_p
     int32_t R;
 };
@@ -40,7 +42,7 @@ struct Batches {
 };
 
 cudaError_t launch_embedding(const ShardPtrs& shards, const TableView& tv, const void* ids, int ids64, int64_t n,
-                             float scale, void* out, int out_bf16, int64_t out_stride, int ctas, int* status,
+                             float scale, void* out, int out_bf16, int64_t out_stride, int ctas, bool overlap, int* status,
                              cudaStream_t stream);
 
 // Workspace of the gradient, carved from the caller's buffer.

@@ -44,24 +44,27 @@ __device__ __forceinline__ unsigned misalign(const T* p) {
     return unsigned(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & 7u;
 }
 
-__device__ __forceinline__ float widen(float v) { return v; }
-__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void narrow(float* p, float v) { *p = v; }
 __device__ __forceinline__ void narrow(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// 8 elements at an aligned address, not kept in L1.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+// 8 elements at an aligned address as they lie in memory (32-bit words), not kept in L1.
+__device__ __forceinline__ void load_raw(const float* p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                  : "l"(p)
                  : "memory");
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-    uint32_t w[4];
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+__device__ __forceinline__ void load_raw(const __nv_bfloat16* p, uint32_t (&w)[4]) {
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                  : "l"(p)
                  : "memory");
+}
+__device__ __forceinline__ void unpack(const uint32_t (&w)[8], float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[j]);
+}
+__device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&x)[8]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         x[2 * j] = __uint_as_float(w[j] << 16);
@@ -83,16 +86,23 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(p) = w;
 }
 
-// The group of 8 elements from e on of a tensor of n: whole groups as a vector where `vec` says that
-// the array has the alignment, else element by element; elements outside the tensor read as 0 and
-// are not written.
+// The group of 8 elements from e on of a tensor of n, as raw words: whole groups as a vector where
+// `vec` says that the array has the alignment, else element by element; elements outside the tensor
+// read as 0 (and, in store_group, are not written).
+__device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
+
 template <typename T>
-__device__ __forceinline__ void load_group(const T* p, int64_t e, int64_t n, bool vec, float (&x)[8]) {
+__device__ __forceinline__ void load_group(const T* p, int64_t e, int64_t n, bool vec, uint32_t (&w)[2 * sizeof(T)]) {
     if (vec && e >= 0 && e + 8 <= n) {
-        load8(p + e, x);
+        load_raw(p + e, w);
     } else {
+        constexpr int kPer = 4 / sizeof(T);  // elements in a word
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = e + j >= 0 && e + j < n ? widen(p[e + j]) : 0.0f;
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = e + j >= 0 && e + j < n ? bits_of(p[e + j]) : 0u;
+            w[j / kPer] = j % kPer ? w[j / kPer] | b << 16 : b;
+        }
     }
 }
 template <typename T>
@@ -145,17 +155,27 @@ __device__ __forceinline__ double sum_squares(const float (&x)[4][8]) {
     return d;
 }
 
+// Groups of 8 that a lane loads before it uses the first: 128 bytes in flight for either type.
+template <typename T>
+constexpr int kBatch = int(16 / sizeof(T));
+
 template <typename T>
 __device__ __forceinline__ double item_squares(const T* g, const Item& it) {
     const int64_t base = it.i * kTsChunk - misalign(g) + (threadIdx.x & 31) * 8;
     double sum = 0.0;
 #pragma unroll
-    for (int h = 0; h < kGroups; h += 4) {
+    for (int h = 0; h < kGroups; h += kBatch<T>) {
         if (base + h * 256 >= it.elems) break;
-        float x[4][8];
+        uint32_t w[kBatch<T>][2 * sizeof(T)];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) load_group(g, base + (h + q) * 256, it.elems, true, x[q]);
-        sum += sum_squares(x);
+        for (int q = 0; q < kBatch<T>; ++q) load_group(g, base + (h + q) * 256, it.elems, true, w[q]);
+#pragma unroll
+        for (int q = 0; q < kBatch<T>; q += 4) {
+            float x[4][8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) unpack(w[q + r], x[r]);
+            sum += sum_squares(x);
+        }
     }
     return sum;
 }
@@ -200,16 +220,18 @@ template <typename T>
 __device__ __forceinline__ void scale_item(T* g, const Item& it, float f) {
     const int64_t base = it.i * kTsChunk - misalign(g) + (threadIdx.x & 31) * 8;
 #pragma unroll
-    for (int h = 0; h < kGroups; h += 4) {
+    for (int h = 0; h < kGroups; h += kBatch<T>) {
         if (base + h * 256 >= it.elems) break;
-        float x[4][8];
+        uint32_t w[kBatch<T>][2 * sizeof(T)];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) load_group(g, base + (h + q) * 256, it.elems, true, x[q]);
+        for (int q = 0; q < kBatch<T>; ++q) load_group(g, base + (h + q) * 256, it.elems, true, w[q]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < kBatch<T>; ++q) {
+            float x[8];
+            unpack(w[q], x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[q][j] *= f;
-            store_group(g, base + (h + q) * 256, it.elems, true, x[q]);
+            for (int j = 0; j < 8; ++j) x[j] *= f;
+            store_group(g, base + (h + q) * 256, it.elems, true, x);
         }
     }
 }
@@ -243,11 +265,13 @@ __device__ __forceinline__ void adamw_item(const TsList& l, const AdamwArgs& a, 
     for (int q = 0; q < kGroups; ++q) {
         const int64_t e = base + q * 256;
         if (e >= it.elems) break;
+        uint32_t pw[8], gw[2 * sizeof(T)], mw[8], vw[8];
+        load_group(p, e, it.elems, true, pw);
+        load_group(g, e, it.elems, gv, gw);
+        load_group(m, e, it.elems, mv, mw);
+        load_group(v, e, it.elems, vv, vw);
         float pi[8], gi[8], mi[8], vi[8];
-        load_group(p, e, it.elems, true, pi);
-        load_group(g, e, it.elems, gv, gi);
-        load_group(m, e, it.elems, mv, mi);
-        load_group(v, e, it.elems, vv, vi);
+        unpack(pw, pi), unpack(gw, gi), unpack(mw, mi), unpack(vw, vi);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float x = gi[j] * f;

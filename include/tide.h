@@ -387,7 +387,8 @@ int tide_reduce_scatter_noalloc(int32_t R, int32_t P, const int64_t *rows, const
  *           i*out_stride (out_stride >= L_p).
  * Any element alignment of shards, out and out_stride is accepted.  Asynchronous on `stream`.
  * Errors: TIDE_EINVAL (null or misaligned pointers, p or n or a type or out_stride out of range,
- * another device current), TIDE_ERANGE (rows_p > 2^31 - 2, or n*L_p overflows), TIDE_ECUDA.
+ * another device current), TIDE_ERANGE (rows_p > 2^31 - 2, L_p > 2^30, or
+ * n*out_stride overflows), TIDE_ECUDA.
  */
 int tide_embedding(tide_group_t g, int32_t p, const void *const *shards, const void *ids, int32_t ids_type,
                    int64_t n, float scale, void *out, int32_t out_type, int64_t out_stride, void *stream);
@@ -416,7 +417,7 @@ int tide_embedding_grad_workspace(tide_group_t g, int32_t p, int64_t n, int64_t 
  *   workspace: device, 256-byte aligned, at least tide_embedding_grad_workspace's bytes for
  *           n[0] + ... + n[B-1]; holds nothing between calls, not shared by calls that overlap.
  * Asynchronous on `stream`.  Errors: TIDE_EINVAL (null or misaligned pointers, p, B, n, a type or a
- * stride out of range, the workspace too small, another device current), TIDE_ERANGE (rows_p > 2^31 - 2,
+ * stride out of range, the workspace too small, another device current), TIDE_ERANGE (rows_p > 2^31 - 2, L_p > 2^30,
  * more than 2^31 - 2^16 positions, or B > TIDE_MAX_TABLE / 8), TIDE_ECUDA.
  */
 int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t *n, const void *const *ids,

@@ -110,7 +110,6 @@ def test_pieces_are_the_valid_rows(tide):
 ])
 def test_rows_that_do_not_fit_are_refused(tide, ids, rows):
     g = _Shape(tide, 2, [(7, 4)])
-    g._want = tide.Group._want.__get__(g)
     with pytest.raises(tide.TideError) as e:
         tide.Group._check_rows(g, "embedding", 0, ids, rows)
     assert e.value.status == tide.TIDE_EINVAL
