@@ -96,7 +96,7 @@ int tide_embedding_grad_workspace(tide_group_t g, int32_t p, int64_t n, int64_t*
     const int rc = table_view(g, p, &tv);
     if (rc != TIDE_OK) return rc;
     if (n > kMaxPositions) return TIDE_ERANGE;
-    *bytes = int64_t(tide::carve_grad_workspace(nullptr, n, nullptr));
+    *bytes = int64_t(tide::carve_grad_workspace(nullptr, tv, n, nullptr));
     return TIDE_OK;
 }
 
@@ -120,7 +120,7 @@ int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t* n, 
             if (n[b] > 0 && (!ids[b] || !douts[b] || !aligned(ids[b], isz) || !aligned(douts[b], fsz))) return TIDE_EINVAL;
         }
         if (total > 0 && (!workspace || !aligned(workspace, 256) ||
-                          workspace_bytes < int64_t(tide::carve_grad_workspace(nullptr, total, nullptr))))
+                          workspace_bytes < int64_t(tide::carve_grad_workspace(nullptr, tv, total, nullptr))))
             return TIDE_EINVAL;
         std::lock_guard<std::mutex> lock(g->mu);
         if ((rc = tide::check_device(g->device)) != TIDE_OK) return rc;
@@ -129,29 +129,31 @@ int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t* n, 
         int slot;
         if ((rc = shard_ptrs(g, shards, 4, st, &sp, &slot)) != TIDE_OK) return rc;
         return finish(g, slot, st, [&]() -> int {
-            if (!accumulate) TIDE_CUDA(tide::launch_zero_table(sp, tv, ctas_of(g, 8), st));
-            if (total == 0) return TIDE_OK;
-            tide::GradWorkspace w;
-            tide::carve_grad_workspace(static_cast<char*>(workspace), total, &w);
-            const bool expanded = B > tide::kInlineBatches;
-            tide::Batches bt{};
-            bt.ids64 = ids_type == TIDE_I64;
-            // more batches than travel with one launch are expanded to rows and addresses first
-            for (int32_t b0 = 0, first = 0; b0 < B; b0 += tide::kInlineBatches) {
-                bt.count = std::min(B - b0, tide::kInlineBatches);
-                bt.start[0] = 0;
-                for (int k = 0; k < bt.count; ++k) {
-                    bt.ids[k] = ids[b0 + k];
-                    bt.dout[k] = static_cast<const char*>(douts[b0 + k]);
-                    bt.stride[k] = dout_stride[b0 + k] * int64_t(fsz);
-                    bt.start[k + 1] = bt.start[k] + uint32_t(n[b0 + k]);
+            tide::GradWorkspace w{};
+            bool dout_vec = true;
+            if (total > 0) {
+                tide::carve_grad_workspace(static_cast<char*>(workspace), tv, total, &w);
+                const bool expanded = B > tide::kInlineBatches;
+                tide::Batches bt{};
+                bt.ids64 = ids_type == TIDE_I64;
+                // more batches than travel with one launch are expanded to rows and addresses first
+                for (int32_t b0 = 0, first = 0; b0 < B; b0 += tide::kInlineBatches) {
+                    bt.count = std::min(B - b0, tide::kInlineBatches);
+                    bt.start[0] = 0;
+                    for (int k = 0; k < bt.count; ++k) {
+                        bt.ids[k] = ids[b0 + k];
+                        bt.dout[k] = static_cast<const char*>(douts[b0 + k]);
+                        bt.stride[k] = dout_stride[b0 + k] * int64_t(fsz);
+                        bt.start[k + 1] = bt.start[k] + uint32_t(n[b0 + k]);
+                        if (n[b0 + k] > 0) dout_vec &= aligned(bt.dout[k], 8 * fsz) && (n[b0 + k] == 1 || bt.stride[k] % int64_t(8 * fsz) == 0);
+                    }
+                    if (expanded) TIDE_CUDA(tide::launch_expand_positions(bt, uint32_t(first), tv.rows, w, g->d_status, st));
+                    first += int32_t(bt.start[bt.count]);
                 }
-                if (expanded) TIDE_CUDA(tide::launch_expand_positions(bt, uint32_t(first), tv.rows, w, g->d_status, st));
-                first += int32_t(bt.start[bt.count]);
+                TIDE_CUDA(tide::launch_sort_positions(bt, expanded, tv, uint32_t(total), !accumulate, w, g->d_status, st));
             }
-            TIDE_CUDA(tide::launch_sort_positions(bt, expanded, uint32_t(total), tv.rows, w, g->d_status, st));
-            TIDE_CUDA(tide::launch_sum_positions(sp, tv, uint32_t(total), w, dout_type == TIDE_BF16, scale, accumulate,
-                                                 ctas_of(g, 8), st));
+            TIDE_CUDA(tide::launch_sum_positions(sp, tv, uint32_t(total), w, dout_type == TIDE_BF16, dout_vec, scale,
+                                                 accumulate != 0, ctas_of(g, tide::kSumCtasPerSm), overlap(g), st));
             return TIDE_OK;
         }());
     });

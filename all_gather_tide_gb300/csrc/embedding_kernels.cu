@@ -136,6 +136,10 @@ embedding_kernel(const __grid_constant__ ShardPtrs shards, TableView tv, const v
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxBits = 10;
+constexpr uint32_t kSortMaxCtas = 8;     // of the cluster
+constexpr uint32_t kSortPerCta = 4096;   // positions for which another CTA joins it
+constexpr uint32_t kPieceMost = 64, kPieceLeast = 8;  // positions of a piece
+constexpr int64_t kPieceWarps = 152 * 24;  // warps for which pieces are cut shorter
 
 __device__ __forceinline__ int batch_of(const Batches& b, uint32_t i) {
     int lo = 0, hi = b.count;
@@ -159,11 +163,16 @@ expand_positions_kernel(const __grid_constant__ Batches b, uint32_t first, uint3
 
 // Stable radix sort, least significant digit first, by one cluster: each warp owns a contiguous run
 // of positions, counts its digits, and places them in order behind the digits of smaller value and
-// the same digit of earlier warps and CTAs.
+// the same digit of earlier warps and CTAs.  The counts of the CTAs meet in distributed shared
+// memory.  A batch of kSortBatch rounds of 32 positions is loaded at once; a run that is one batch
+// stays in registers between counting and placing.
+constexpr int kSortBatch = 8;
+
 struct SortArgs {
     Batches b;
     uint32_t n, rows;
-    int expanded, passes, bits;
+    int expanded, passes, bits, mark;
+    int64_t counters;
     GradWorkspace w;
     int* status;
 };
@@ -178,8 +187,23 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
     uint32_t* total = cnt + kSortWarps * bins; // [bins], read by the cluster
     uint32_t* base = total + bins;             // [bins]
     __shared__ uint32_t warp_sum[kSortWarps];
+    __shared__ Batches b;  // a copy: lanes look up different batches at once
+    for (int q = threadIdx.x; q < a.b.count; q += kSortThreads) {
+        b.ids[q] = a.b.ids[q];
+        b.dout[q] = a.b.dout[q];
+        b.stride[q] = a.b.stride[q];
+        b.start[q] = a.b.start[q];
+    }
+    if (threadIdx.x == 0) b.count = a.b.count;
     const uint32_t per = ((a.n + C * kSortWarps - 1) / (C * kSortWarps) + 31) & ~31u;
     const uint32_t lo = min(a.n, (c * kSortWarps + warp) * per), hi = min(a.n, lo + per);
+    uint32_t* mine = cnt + warp * bins;
+
+    // what the summing kernel finds cleared: its arrival counters, and the marks of rows with a token
+    // (set below, after the first cluster barrier)
+    for (int64_t q = c * kSortThreads + threadIdx.x; q < a.counters; q += C * kSortThreads) a.w.arrived[q] = 0;
+    if (a.mark)
+        for (uint32_t q = c * kSortThreads + threadIdx.x; q <= a.rows / 32; q += C * kSortThreads) a.w.marks[q] = 0;
 
     for (int pass = 0; pass < a.passes; ++pass) {
         const bool last = pass == a.passes - 1;
@@ -188,24 +212,37 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
         uint32_t* key_out = last ? a.w.keys : (pass & 1) ? a.w.key_b : a.w.key_a;
         uint32_t* idx_out = (pass & 1) ? a.w.idx_b : a.w.idx_a;
         const int shift = pass * a.bits;
-        auto key_at = [&](uint32_t i) -> uint32_t {
-            if (pass > 0) return __ldcg(key_in + i);
-            if (a.expanded) return a.w.pre_key[i];
-            const int k = batch_of(a.b, i);
-            return row_of(a.b.ids[k], a.b.ids64, i - a.b.start[k], a.rows, a.status);
+        uint32_t key[kSortBatch], idx[kSortBatch];
+        auto load = [&](uint32_t i0) {
+#pragma unroll
+            for (int u = 0; u < kSortBatch; ++u) {
+                const uint32_t i = i0 + u * 32 + lane;
+                key[u] = 0;
+                idx[u] = i;
+                if (i >= hi) continue;
+                if (pass > 0) {
+                    key[u] = __ldcg(key_in + i);
+                    idx[u] = __ldcg(idx_in + i);
+                } else if (a.expanded) {
+                    key[u] = a.w.pre_key[i];
+                } else {
+                    const int k = batch_of(b, i);
+                    key[u] = row_of(b.ids[k], a.b.ids64, i - b.start[k], a.rows, a.status);
+                }
+            }
         };
         for (int q = threadIdx.x; q < kSortWarps * bins; q += kSortThreads) cnt[q] = 0;
         __syncthreads();
-        for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
-            const uint32_t i = i0 + lane;
-            const uint32_t digit = i < hi ? (key_at(i) >> shift) & (bins - 1) : bins;
-            const uint32_t same = __match_any_sync(0xffffffffu, digit);
-            if (i < hi && lane == __ffs(same) - 1) cnt[warp * bins + digit] += __popc(same);
-            __syncwarp();
+        for (uint32_t i0 = lo; i0 < hi; i0 += kSortBatch * 32) {
+            load(i0);
+#pragma unroll
+            for (int u = 0; u < kSortBatch; ++u)
+                if (i0 + u * 32 + lane < hi) atomicAdd(&mine[(key[u] >> shift) & (bins - 1)], 1u);
         }
         __syncthreads();
         for (int q = threadIdx.x; q < bins; q += kSortThreads) {
             uint32_t run = 0;
+#pragma unroll 8
             for (int w = 0; w < kSortWarps; ++w) {
                 const uint32_t v = cnt[w * bins + q];
                 cnt[w * bins + q] = run;
@@ -223,37 +260,47 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
                 if (r < c) before += v;
                 all += v;
             }
-        uint32_t incl = all;
-        for (int s = 1; s < 32; s <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, s);
-            if (lane >= s) incl += v;
-        }
+        auto scan = [&](uint32_t v) {  // inclusive, over the warp
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, v, s);
+                if (lane >= s) v += o;
+            }
+            return v;
+        };
+        const uint32_t incl = scan(all);
         if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
-        uint32_t first = 0;
-        for (int w = 0; w < warp; ++w) first += warp_sum[w];
-        if (q < bins) base[q] = first + incl - all + before;
+        const uint32_t sums = scan(warp_sum[lane]);
+        const uint32_t first = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
+        if (q < bins) base[q] = (warp ? first : 0) + incl - all + before;
         __syncthreads();
-        for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
-            const uint32_t i = i0 + lane;
-            const uint32_t key = i < hi ? key_at(i) : 0;
-            const uint32_t digit = i < hi ? (key >> shift) & (bins - 1) : bins;
-            const uint32_t same = __match_any_sync(0xffffffffu, digit);
-            uint32_t at = 0;
-            if (i < hi) at = base[digit] + cnt[warp * bins + digit] + __popc(same & ((1u << lane) - 1u));
-            __syncwarp();
-            if (i < hi && lane == __ffs(same) - 1) cnt[warp * bins + digit] += __popc(same);
-            __syncwarp();
-            if (i < hi) {
-                const uint32_t idx = pass > 0 ? __ldcg(idx_in + i) : i;
-                key_out[at] = key;
+        for (uint32_t i0 = lo; i0 < hi; i0 += kSortBatch * 32) {
+            if (hi - lo > kSortBatch * 32) load(i0);
+#pragma unroll
+            for (int u = 0; u < kSortBatch; ++u) {
+                if (i0 + u * 32 >= hi) break;
+                const bool in = i0 + u * 32 + lane < hi;
+                const uint32_t digit = in ? (key[u] >> shift) & (bins - 1) : bins;
+                const uint32_t same = __match_any_sync(0xffffffffu, digit);
+                const int lead = __ffs(same) - 1;
+                // a mark for each row (several lanes may set one: the bits of equal keys are mostly dropped)
+                const uint32_t led = __shfl_sync(0xffffffffu, key[u], lead);
+                if (a.mark && pass == 0 && in && (lane == lead || key[u] != led)) atomicOr(&a.w.marks[key[u] >> 5], 1u << (key[u] & 31));
+                uint32_t at = 0;
+                if (in) at = base[digit] + mine[digit] + __popc(same & ((1u << lane) - 1u));
+                __syncwarp();
+                if (in && lane == lead) mine[digit] += __popc(same);
+                __syncwarp();
+                if (!in) continue;
+                key_out[at] = key[u];
                 if (!last) {
-                    idx_out[at] = idx;
+                    idx_out[at] = idx[u];
                 } else if (a.expanded) {
-                    a.w.src[at] = a.w.pre_src[idx];
+                    a.w.src[at] = a.w.pre_src[idx[u]];
                 } else {
-                    const int k = batch_of(a.b, idx);
-                    a.w.src[at] = reinterpret_cast<uint64_t>(a.b.dout[k] + int64_t(idx - a.b.start[k]) * a.b.stride[k]);
+                    const int k = batch_of(b, idx[u]);
+                    a.w.src[at] = reinterpret_cast<uint64_t>(b.dout[k] + int64_t(idx[u] - b.start[k]) * b.stride[k]);
                 }
             }
         }
@@ -264,42 +311,318 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
     }
 }
 
-__global__ void __launch_bounds__(kThreads)
-zero_table_kernel(const __grid_constant__ ShardPtrs shards, TableView tv) {
-    const int64_t n = int64_t(tv.m) * tv.len;
-    for (int d = 0; d < tv.R; ++d) {
-        float* p = reinterpret_cast<float*>(shard_base(shards, d)) + tv.off;
-        for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kThreads) p[i] = 0.0f;
+// ---- sums ---------------------------------------------------------------------------------------
+//
+// The sorted list is cut into pieces of `piece` positions; one warp sums one piece over kStretch
+// columns (8 to a lane), so the work is the same whatever the texts repeat.  A row whose positions
+// all lie in one piece is written at once.  One that runs over several pieces leaves a partial sum in
+// each; the warp that arrives last adds them in the order of the pieces, so the result does not
+// depend on who that is.  Positions without a token sort last and are not read.
+constexpr uint32_t kStretch = 256;
+
+struct SumArgs {
+    ShardPtrs shards;
+    TableView tv;
+    uint32_t n, piece, pieces, stretches;
+    GradWorkspace w;
+    float scale;
+    int accumulate;
+    uint32_t sum_blocks;   // CTAs' worth of sums, before those that write zeros
+    uint32_t zero_blocks;
+    uint32_t zero_rows;    // rows of the padded table that one CTA looks through for rows to zero
+};
+
+__device__ __forceinline__ float* table_row(const SumArgs& a, uint32_t t) {
+    const uint32_t d = t / a.tv.m;
+    return reinterpret_cast<float*>(shard_base(a.shards, d)) + a.tv.off + int64_t(t - d * a.tv.m) * a.tv.len;
+}
+
+// How a warp's 256 columns lie over its lanes: every 32nd element (kSingle), or 8 consecutive ones, whose
+// rows in the shard are 32-byte aligned (kWide) or not (kMixed).
+enum Layout { kSingle, kMixed, kWide };
+
+// 8 columns of a dout row: 8 consecutive ones (Vec), or every 32nd.
+template <typename In, bool Vec>
+struct Columns;
+template <>
+struct Columns<__nv_bfloat16, true> {
+    uint4 w;
+    __device__ __forceinline__ void load(uint64_t row, uint32_t col, uint32_t len) {
+        if (col < len) asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(row + col * 2ull));
+        else w = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void add(float (&acc)[8]) const {
+        float x[8];
+        widen(w, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += x[j];
+    }
+};
+template <>
+struct Columns<float, true> {
+    float x[8];
+    __device__ __forceinline__ void load(uint64_t row, uint32_t col, uint32_t len) {
+        if (col < len)
+            asm volatile("ld.global.nc.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                         : "l"(row + col * 4ull));
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+    }
+    __device__ __forceinline__ void add(float (&acc)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += x[j];
+    }
+};
+template <typename In>
+struct Columns<In, false> {
+    In x[8];
+    __device__ __forceinline__ void load(uint64_t row, uint32_t col, uint32_t len) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = col + 32 * j < len ? __ldg(reinterpret_cast<const In*>(row) + col + 32 * j) : In(0.0f);
+    }
+    __device__ __forceinline__ void add(float (&acc)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += float(x[j]);
+    }
+};
+
+// Adds without waiting for what was there: L2 reads, adds and writes.  Every element is added to once
+// in a call, so the result depends on no order.
+__device__ __forceinline__ void add_v4(float* p, float x, float y, float z, float w) {
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+__device__ __forceinline__ void add_v1(float* p, float x) { asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(x) : "memory"); }
+
+// The warp's sums to the shard: `acc` as the layout spreads them over the lanes.
+template <Layout kLayout>
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t t, uint32_t col0, const float (&acc)[8], float* stage) {
+    const int lane = threadIdx.x & 31;
+    float* dst = table_row(a, t) + col0;
+    const uint32_t left = a.tv.len - col0;
+    float x[8];
+    if (kLayout == kWide) {
+        if (lane * 8u >= left) return;
+        dst += lane * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = acc[j] * a.scale;
+        if (a.accumulate) {
+            add_v4(dst, x[0], x[1], x[2], x[3]);
+            add_v4(dst + 4, x[4], x[5], x[6], x[7]);
+        } else {
+            store_v8(dst, x);
+        }
+        return;
+    }
+    if (kLayout == kMixed) {  // lane * 8 + j -> lane + 32 * j, so that stores of single elements lie side by side
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) stage[lane * 9 + j] = acc[j];
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int q = lane + 32 * j;
+            x[j] = stage[q / 8 * 9 + q % 8];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = acc[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (lane + 32u * j < left) {
+            const float v = a.scale * x[j];
+            if (a.accumulate) add_v1(dst + lane + 32 * j, v);
+            else dst[lane + 32 * j] = v;
+        }
+}
+
+// Partial sums meet in two steps: those of up to kBlock consecutive pieces, then those of the
+// blocks.  `which`: 0 for the row that a piece (block) continues, 1 for the one that starts in it.
+constexpr uint32_t kBlock = 32;
+
+__device__ __forceinline__ int64_t slot_of(const SumArgs& a, uint32_t x, int which, uint32_t stretch) {
+    return (int64_t(x) * 2 + which) * a.stretches + stretch;
+}
+__device__ __forceinline__ float* partial_of(const SumArgs& a, uint32_t x, int which, uint32_t stretch) {
+    return a.w.partial + slot_of(a, x, which, stretch) * kStretch + (threadIdx.x & 31) * 8;
+}
+
+__device__ __forceinline__ void put_partial(float* p, const float (&acc)[8]) {
+    __stcg(reinterpret_cast<float4*>(p), make_float4(acc[0], acc[1], acc[2], acc[3]));
+    __stcg(reinterpret_cast<float4*>(p + 4), make_float4(acc[4], acc[5], acc[6], acc[7]));
+}
+
+// Arrives at a counter with everything written so far; true, with what the others wrote visible, for
+// the last of `count`.
+__device__ __forceinline__ bool last_to_arrive(uint32_t* counter, uint32_t count) {
+    __threadfence();
+    __syncwarp();
+    uint32_t earlier = 0;
+    if ((threadIdx.x & 31) == 0) earlier = atomicAdd(counter, 1u);
+    if (__shfl_sync(0xffffffffu, earlier, 0) != count - 1) return false;
+    __threadfence();
+    return true;
+}
+
+// sum += the partial sums of count pieces (blocks) from x on, of which only the first may start the row.
+__device__ __forceinline__ void add_partials(const SumArgs& a, uint32_t x, uint32_t count, int first_starts, uint32_t stretch, float (&sum)[8]) {
+#pragma unroll 8
+    for (uint32_t k = 0; k < count; ++k) {
+        const float* p = partial_of(a, x + k, k == 0 ? first_starts : 0, stretch);
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(p)), v = __ldcg(reinterpret_cast<const float4*>(p + 4));
+        sum[0] += u.x, sum[1] += u.y, sum[2] += u.z, sum[3] += u.w, sum[4] += v.x, sum[5] += v.y, sum[6] += v.z, sum[7] += v.w;
     }
 }
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// One warp per (first position of a row's run, 256 columns): adds the run's rows in order.
-template <typename In>
-__global__ void __launch_bounds__(kThreads)
-sum_positions_kernel(const __grid_constant__ ShardPtrs shards, TableView tv, uint32_t n, const uint32_t* __restrict__ keys,
-                     const uint64_t* __restrict__ src, float scale, int accumulate) {
-    const int lane = threadIdx.x & 31;
-    const int64_t segs = (tv.len + 255) / 256, items = int64_t(n) * segs;
-    for (int64_t it = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * (kThreads / 32)) {
-        const uint32_t i = uint32_t(it / segs);
-        const int64_t col = (it % segs) * 256 + lane;
-        const uint32_t t = keys[i];
-        if (t >= tv.rows || (i > 0 && keys[i - 1] == t)) continue;
-        float acc[8] = {};
-        for (uint32_t k = i; k < n && keys[k] == t; ++k) {
-            const In* row = reinterpret_cast<const In*>(src[k]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (col + 32 * j < tv.len) acc[j] += to_f32(row[col + 32 * j]);
+// After a piece has left a partial sum of row t: the last of the row's pieces in this block adds
+// the block's, and the last of its blocks adds the blocks', both in order, and writes the row.
+template <Layout kLayout>
+__device__ __forceinline__ void join_partials(const SumArgs& a, uint32_t t, uint32_t piece, uint32_t stretch, float* stage) {
+    const uint32_t lane = threadIdx.x & 31, block = piece / kBlock, p0 = block * kBlock, y = p0 + lane;
+    // the row has a position in piece y: its first or last position, or (t lying in between) both ends
+    // on either side; pieces that the row crosses begin or end with it
+    const bool begins = y < a.pieces && __ldg(&a.w.keys[y * a.piece]) == t;
+    const bool ends = y < a.pieces && __ldg(&a.w.keys[min(a.n, (y + 1) * a.piece) - 1]) == t;
+    const uint32_t in = __ballot_sync(0xffffffffu, begins || ends);
+    const uint32_t from = __ffs(in) - 1, count = __popc(in);
+    // the row starts in its first piece here unless that continues the one before
+    const uint32_t x = p0 + from;
+    const bool continued = x > 0 && __ldg(&a.w.keys[x * a.piece - 1]) == t;
+    const bool starts = !continued;
+    const uint32_t end = (x + count) * a.piece;
+    const bool goes_on = end < a.n && __ldg(&a.w.keys[end]) == t;
+    if (!last_to_arrive(&a.w.arrived[slot_of(a, x, starts, stretch)], count)) return;
+    float sum[8] = {};
+    add_partials(a, x, count, starts, stretch, sum);
+    if (continued || goes_on) {
+        // blocks are numbered after the pieces
+        put_partial(partial_of(a, a.pieces + block, starts, stretch), sum);
+        const uint32_t blocks = (a.pieces + kBlock - 1) / kBlock;
+        uint32_t first = block, last = block;
+        if (continued) {
+            for (uint32_t back = 1;; back += 32) {
+                const uint32_t z = back + lane;  // block - z ends with the row
+                const uint32_t out = ~__ballot_sync(0xffffffffu, z <= block && __ldg(&a.w.keys[(block - z + 1) * kBlock * a.piece - 1]) == t);
+                first = block - (back - 1) - (out ? __ffs(out) - 1 : 32);
+                if (out) break;
+            }
         }
-        const uint32_t d = t / tv.m;
-        float* dst = reinterpret_cast<float*>(shard_base(shards, d)) + tv.off + int64_t(t - d * tv.m) * tv.len;
+        if (goes_on) {
+            for (uint32_t ahead = 1;; ahead += 32) {
+                const uint32_t z = block + ahead + lane;  // block z begins with the row
+                const uint32_t out = ~__ballot_sync(0xffffffffu, z < blocks && __ldg(&a.w.keys[z * kBlock * a.piece]) == t);
+                last = block + (ahead - 1) + (out ? __ffs(out) - 1 : 32);
+                if (out) break;
+            }
+        }
+        // of these blocks, the row starts in the first
+        if (!last_to_arrive(&a.w.arrived[slot_of(a, a.pieces + first, 1, stretch)], last - first + 1)) return;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (col + 32 * j < tv.len) dst[col + 32 * j] = (accumulate ? dst[col + 32 * j] : 0.0f) + scale * acc[j];
+        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+        add_partials(a, a.pieces + first, last - first + 1, 1, stretch, sum);
+    }
+    write_row<kLayout>(a, t, stretch * kStretch, sum, stage);
+}
+
+template <typename In, Layout kLayout>
+__device__ __forceinline__ void sum_piece(const SumArgs& a, uint32_t piece, uint32_t stretch, float* stage) {
+    constexpr bool Vec = kLayout != kSingle;
+    constexpr int kAhead = 16 / sizeof(In);  // rows in flight: 128 bytes a lane
+    const int lane = threadIdx.x & 31;
+    const uint32_t lo = piece * a.piece, hi = min(a.n, lo + a.piece);
+    const uint32_t col0 = stretch * kStretch, col = col0 + (Vec ? lane * 8 : lane);
+    const uint32_t before = lo > 0 ? __ldg(&a.w.keys[lo - 1]) : ~0u;  // rows on either side of the piece
+    const uint32_t after = hi < a.n ? __ldg(&a.w.keys[hi]) : ~0u;
+    float acc[8] = {};
+    uint32_t cur = ~0u;    // the row being summed
+    bool starts = true;    // in this piece
+    uint32_t head = ~0u;   // the row that an earlier piece began and this one ends
+    for (uint32_t k0 = lo; k0 < hi; k0 += 32) {
+        // a lane holds one position
+        const uint32_t key = k0 + lane < hi ? __ldg(&a.w.keys[k0 + lane]) : a.tv.rows;
+        const unsigned long long src = key < a.tv.rows ? __ldg(reinterpret_cast<const unsigned long long*>(a.w.src) + k0 + lane) : 0;
+        const int held = __popc(__ballot_sync(0xffffffffu, key < a.tv.rows));  // sorted: they come first
+        for (int k = 0; k < held; k += kAhead) {
+            Columns<In, Vec> x[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const uint64_t row = __shfl_sync(0xffffffffu, src, (k + u) & 31);
+                if (k + u < held) x[u].load(row, col, a.tv.len);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (k + u >= held) break;
+                const uint32_t t = __shfl_sync(0xffffffffu, key, k + u);
+                if (t != cur) {
+                    if (cur != ~0u) {
+                        if (starts) {
+                            write_row<kLayout>(a, cur, col0, acc, stage);
+                        } else {
+                            put_partial(partial_of(a, piece, 0, stretch), acc);
+                            head = cur;
+                        }
+                    }
+                    cur = t;
+                    starts = t != before;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+                }
+                x[u].add(acc);
+            }
+        }
+        if (held < 32) break;
+    }
+    uint32_t tail = ~0u;  // the row that a later piece ends
+    if (cur != ~0u) {
+        const bool ends = cur != after;
+        if (starts && ends) {
+            write_row<kLayout>(a, cur, col0, acc, stage);
+        } else {
+            put_partial(partial_of(a, piece, starts ? 1 : 0, stretch), acc);
+            if (ends) head = cur; else tail = cur;
+        }
+    }
+    // rows that run over several pieces
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const uint32_t t = side ? tail : head;
+        if (t != ~0u) join_partials<kLayout>(a, t, piece, stretch, stage);
+    }
+}
+
+// Zeros from p on, n elements, by one warp: 32-byte stores between single ones at the ends.
+__device__ __forceinline__ void zero_run(float* p, uint32_t n) {
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t head = min(n, (8u - (unsigned(reinterpret_cast<uintptr_t>(p) / 4) & 7u)) & 7u);
+    const float z[8] = {};
+    if (lane < head) p[lane] = 0.0f;
+    const uint32_t vecs = (n - head) / 8;
+    for (uint32_t v = lane; v < vecs; v += 32) store_v8(p + head + v * 8, z);
+    for (uint32_t i = head + vecs * 8 + lane; i < n; i += 32) p[i] = 0.0f;
+}
+
+template <typename In, Layout kLayout>
+__global__ void __launch_bounds__(kThreads, kSumCtasPerSm) sum_positions_kernel(const __grid_constant__ SumArgs a) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ float stage[kWarps][kLayout == kMixed ? 32 * 9 : 1];
+    const uint32_t warp = threadIdx.x >> 5;
+    for (uint32_t b = blockIdx.x; b < a.sum_blocks + a.zero_blocks; b += gridDim.x) {
+        if (b < a.sum_blocks) {
+            const uint64_t item = uint64_t(b) * kWarps + warp;
+            const uint32_t piece = uint32_t(item / a.stretches);
+            if (piece < a.pieces) sum_piece<In, kLayout>(a, piece, uint32_t(item - uint64_t(piece) * a.stretches), stage[warp]);
+        } else {
+            const uint64_t r0 = uint64_t(b - a.sum_blocks) * a.zero_rows, r1 = min(r0 + a.zero_rows, uint64_t(a.tv.m) * a.tv.R);
+            for (uint64_t r = r0 + warp; r < r1; r += kWarps) {
+                // row r of the padded table: rows from tv.rows on are padding and have no mark
+                const bool has = r < a.tv.rows && a.n > 0 && (__ldg(&a.w.marks[r >> 5]) >> (r & 31) & 1);
+                if (has) continue;
+                const uint32_t d = uint32_t(r / a.tv.m);
+                zero_run(reinterpret_cast<float*>(shard_base(a.shards, d)) + a.tv.off + int64_t(r - uint64_t(d) * a.tv.m) * a.tv.len, a.tv.len);
+            }
+        }
     }
 }
 
@@ -359,12 +682,24 @@ cudaError_t launch_embedding(const ShardPtrs& shards, const TableView& tv, const
     return lookup_any(shards, tv, ids, ids64, n, scale, static_cast<float*>(out), out_stride, ctas, overlap, status, stream);
 }
 
-size_t carve_grad_workspace(char* base, int64_t n, GradWorkspace* w) {
+GradPlan plan_grad(const TableView& tv, int64_t n) {
+    GradPlan g;
+    g.stretches = (tv.len + kStretch - 1) / kStretch;
+    // shorter pieces while they would not fill the GPU's warps once
+    g.piece = kPieceMost;
+    while (g.piece > kPieceLeast && (n + g.piece - 1) / g.piece * g.stretches < kPieceWarps) g.piece >>= 1;
+    g.pieces = uint32_t((n + g.piece - 1) / g.piece);
+    g.slots = (int64_t(g.pieces) + (g.pieces + kBlock - 1) / kBlock) * 2 * g.stretches;
+    return g;
+}
+
+size_t carve_grad_workspace(char* base, const TableView& tv, int64_t n, GradWorkspace* w) {
+    const GradPlan p = plan_grad(tv, n);
     size_t at = 0;
     auto take = [&](size_t bytes) {
-        char* p = base + at;
+        char* q = base + at;
         at += (bytes + 255) / 256 * 256;
-        return p;
+        return q;
     };
     GradWorkspace g;
     g.keys = reinterpret_cast<uint32_t*>(take(size_t(n) * 4));
@@ -375,6 +710,9 @@ size_t carve_grad_workspace(char* base, int64_t n, GradWorkspace* w) {
     g.idx_b = reinterpret_cast<uint32_t*>(take(size_t(n) * 4));
     g.pre_key = reinterpret_cast<uint32_t*>(take(size_t(n) * 4));
     g.pre_src = reinterpret_cast<uint64_t*>(take(size_t(n) * 8));
+    g.marks = reinterpret_cast<uint32_t*>(take((size_t(tv.rows) / 32 + 1) * 4));
+    g.arrived = reinterpret_cast<uint32_t*>(take(size_t(p.slots) * 4));
+    g.partial = reinterpret_cast<float*>(take(size_t(p.slots) * kStretch * 4));
     if (w) *w = g;
     return at;
 }
@@ -388,34 +726,58 @@ cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t r
     return cudaGetLastError();
 }
 
-cudaError_t launch_sort_positions(const Batches& b, bool expanded, uint32_t n, uint32_t rows, const GradWorkspace& w,
-                                  int* status, cudaStream_t stream) {
+cudaError_t launch_sort_positions(const Batches& b, bool expanded, const TableView& tv, uint32_t n, bool mark,
+                                  const GradWorkspace& w, int* status, cudaStream_t stream) {
     int bits = 0;
-    while (rows >> bits) ++bits;  // keys are 0 .. rows
-    SortArgs a{b, n, rows, expanded ? 1 : 0, 0, 0, w, status};
+    while (tv.rows >> bits) ++bits;  // keys are 0 .. rows
+    const GradPlan p = plan_grad(tv, n);
+    SortArgs a{b, n, tv.rows, expanded ? 1 : 0, 0, 0, mark ? 1 : 0, p.slots, w, status};
     a.passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
     a.bits = (bits + a.passes - 1) / a.passes;
     const size_t smem = (size_t(kSortWarps) + 2) * (size_t(1) << a.bits) * 4;
     cudaError_t e = cudaFuncSetAttribute(sort_positions_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    sort_positions_kernel<<<1, kSortThreads, smem, stream>>>(a);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_zero_table(const ShardPtrs& shards, const TableView& tv, int ctas, cudaStream_t stream) {
-    zero_table_kernel<<<ctas, kThreads, 0, stream>>>(shards, tv);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    uint32_t c = 1;
+    while (c < kSortMaxCtas && n > c * kSortPerCta) c <<= 1;
+    attr.val.clusterDim.x = c;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sort_positions_kernel, a);
 }
 
 cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, uint32_t n, const GradWorkspace& w,
-                                 int dout_bf16, float scale, int accumulate, int ctas, cudaStream_t stream) {
-    if (n == 0) return cudaSuccess;
-    const int64_t items = int64_t(n) * ((tv.len + 255) / 256);
-    const int grid = int(std::min<int64_t>((items + 7) / 8, ctas));
-    if (dout_bf16)
-        sum_positions_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(shards, tv, n, w.keys, w.src, scale, accumulate);
-    else
-        sum_positions_kernel<float><<<grid, kThreads, 0, stream>>>(shards, tv, n, w.keys, w.src, scale, accumulate);
+                                 int dout_bf16, bool dout_vec, float scale, bool accumulate, int ctas, bool overlap,
+                                 cudaStream_t stream) {
+    const GradPlan p = plan_grad(tv, n);
+    SumArgs a{shards, tv, n, p.piece, p.pieces, p.stretches, w, scale, accumulate ? 1 : 0, 0, 0, 1};
+    const int64_t sums = (int64_t(p.pieces) * p.stretches + kThreads / 32 - 1) / (kThreads / 32);
+    int64_t zeros = 0;
+    if (!accumulate) {
+        // at least a row to each warp, and about 16 KB of zeros
+        a.zero_rows = uint32_t(std::max<int64_t>(1, 4096 / tv.len) * (kThreads / 32));
+        zeros = (int64_t(tv.m) * tv.R + a.zero_rows - 1) / a.zero_rows;
+    }
+    if (sums + zeros > INT32_MAX) return cudaErrorInvalidValue;
+    if (sums + zeros == 0) return cudaSuccess;
+    a.sum_blocks = uint32_t(sums);
+    a.zero_blocks = uint32_t(zeros);
+    const int grid = int(std::min<int64_t>(sums + zeros, overlap ? ctas : INT32_MAX));
+    const bool wide = tv.len % 8 == 0 && tv.off % 8 == 0 && shards.bits % 32 == 0;
+    const Layout layout = !dout_vec || tv.len % 8 ? kSingle : wide ? kWide : kMixed;
+    auto pick = [&](auto in) {
+        using In = decltype(in);
+        return layout == kWide ? sum_positions_kernel<In, kWide> : layout == kMixed ? sum_positions_kernel<In, kMixed> : sum_positions_kernel<In, kSingle>;
+    };
+    auto* kernel = dout_bf16 ? pick(__nv_bfloat16()) : pick(float());
+    kernel<<<grid, kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

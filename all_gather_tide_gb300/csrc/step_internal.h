@@ -12,6 +12,7 @@ namespace tide {
 // ---- embedding -------------------------------------------------------------------------------
 constexpr int kInlineRanks = 64;    // shard pointers that travel with a launch
 constexpr int kLookupCtasPerSm = 4;
+constexpr int kSumCtasPerSm = 3;
 constexpr int kInlineBatches = 64;  // batches that travel with a launch
 
 // The R shard pointers of a call: in the launch's own parameters up to kInlineRanks, else in a device
@@ -55,17 +56,29 @@ struct GradWorkspace {
     uint32_t* idx_b;
     uint32_t* pre_key;   // [N] rows and addresses expanded before the sort, when there are more than
     uint64_t* pre_src;   //     kInlineBatches batches
+    uint32_t* marks;     // a bit for every row that has a token (only where the table is overwritten)
+    uint32_t* arrived;   // [slots] counts of arrivals
+    float* partial;      // [slots][256] partial sums
 };
+// How the sorted list is summed: pieces of positions, stretches of columns, and room for two partial
+// sums of every stretch of every piece and of every block of pieces.
+struct GradPlan {
+    uint32_t piece, pieces, stretches;
+    int64_t slots;
+};
+GradPlan plan_grad(const TableView& tv, int64_t n);
 // Carves the workspace for n positions at `base` (any pointer, also null) and returns its size.
-size_t carve_grad_workspace(char* base, int64_t n, GradWorkspace* w);
+size_t carve_grad_workspace(char* base, const TableView& tv, int64_t n, GradWorkspace* w);
 
 cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t rows, const GradWorkspace& w,
                                     int* status, cudaStream_t stream);
-cudaError_t launch_sort_positions(const Batches& b, bool expanded, uint32_t n, uint32_t rows, const GradWorkspace& w,
-                                  int* status, cudaStream_t stream);
-cudaError_t launch_zero_table(const ShardPtrs& shards, const TableView& tv, int ctas, cudaStream_t stream);
+// mark: also mark the rows that have a token.
+cudaError_t launch_sort_positions(const Batches& b, bool expanded, const TableView& tv, uint32_t n, bool mark,
+                                  const GradWorkspace& w, int* status, cudaStream_t stream);
+// dout_vec: every dout row starts on a boundary of 8 elements.
 cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, uint32_t n, const GradWorkspace& w,
-                                 int dout_bf16, float scale, int accumulate, int ctas, cudaStream_t stream);
+                                 int dout_bf16, bool dout_vec, float scale, bool accumulate, int ctas, bool overlap,
+                                 cudaStream_t stream);
 
 // ---- lists of tensors -------------------------------------------------------------------------
 constexpr int64_t kTsChunk = 2048;  // elements of one work item
