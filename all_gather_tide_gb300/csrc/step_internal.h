@@ -48,15 +48,11 @@ cudaError_t launch_embedding(const ShardPtrs& shards, const TableView& tv, const
 
 // Workspace of the gradient, carved from the caller's buffer.
 struct GradWorkspace {
-    uint32_t* keys;      // [N] sorted rows (rows = no token)
-    uint64_t* src;       // [N] dout row addresses in the same order
-    uint32_t* key_a;     // [N] intermediate sort passes
-    uint32_t* key_b;
-    uint32_t* idx_a;
-    uint32_t* idx_b;
-    uint32_t* pre_key;   // [N] rows and addresses expanded before the sort, when there are more than
-    uint64_t* pre_src;   //     kInlineBatches batches
-    uint32_t* marks;     // a bit for every row that has a token (only where the table is overwritten)
+    // a position: its dout row's address (x, y) and its table row (z; rows = no token)
+    uint4* sorted;       // [N] by row
+    uint4* swap_a;       // [N] between passes of the sort
+    uint4* swap_b;
+    uint4* pre;          // [N] before the sort, when there are more than kInlineBatches batches
     uint32_t* arrived;   // [slots] counts of arrivals
     float* partial;      // [slots][256] partial sums
 };
@@ -72,8 +68,7 @@ size_t carve_grad_workspace(char* base, const TableView& tv, int64_t n, GradWork
 
 cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t rows, const GradWorkspace& w,
                                     int* status, cudaStream_t stream);
-// mark: also mark the rows that have a token.
-cudaError_t launch_sort_positions(const Batches& b, bool expanded, const TableView& tv, uint32_t n, bool mark,
+cudaError_t launch_sort_positions(const Batches& b, bool expanded, const TableView& tv, uint32_t n,
                                   const GradWorkspace& w, int* status, cudaStream_t stream);
 // dout_vec: every dout row starts on a boundary of 8 elements.
 cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, uint32_t n, const GradWorkspace& w,
