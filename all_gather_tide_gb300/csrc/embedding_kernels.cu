@@ -65,6 +65,12 @@ __device__ __forceinline__ void store_v8(float* p, const float (&x)[8]) {
                  "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
                  : "memory");
 }
+__device__ __forceinline__ void load_v8(const float* p, float (&x)[8]) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(p)
+                 : "memory");
+}
 __device__ __forceinline__ void put(float* p, const float (&x)[8]) { store_v8(p, x); }
 __device__ __forceinline__ void put(float* p, const float (&x)[4]) { __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3])); }
 __device__ __forceinline__ void put(float* p, const float (&x)[2]) { __stcs(reinterpret_cast<float2*>(p), make_float2(x[0], x[1])); }
@@ -345,13 +351,19 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
 // depend on who that is.  Positions without a token sort last and are not read.
 constexpr uint32_t kStretch = 256;
 
+// What a warp has in flight: groups of copies, 2 KB of dout rows each.
+template <typename In>
+struct Ring {
+    static constexpr int kGroups = 3, kGroup = 8 / sizeof(In), kRows = kGroup * kGroups;
+    static constexpr uint32_t kRow = kStretch * sizeof(In), kBytes = kRows * kRow;
+};
+
 struct SumArgs {
     ShardPtrs shards;
     TableView tv;
     uint32_t n, piece, pieces, stretches;
     GradWorkspace w;
     float scale;
-    int accumulate;
     uint32_t sum_blocks;   // CTAs' worth of sums, before those that write zeros
     uint32_t zero_blocks;
     uint32_t zero_rows;    // rows of the padded table that one warp looks through for rows to zero
@@ -369,42 +381,39 @@ __device__ __forceinline__ uint32_t row_at(const SumArgs& a, uint32_t i) { retur
 // rows in the shard are 32-byte aligned (kWide) or not (kMixed).
 enum Layout { kSingle, kMixed, kWide };
 
-// 8 columns of a dout row: 8 consecutive ones (Vec), or every 32nd.
-template <typename In, bool Vec>
-struct Columns;
-template <>
-struct Columns<__nv_bfloat16, true> {
-    uint4 w;
-    __device__ __forceinline__ void load(uint64_t row, uint32_t col, uint32_t len) {
-        if (col < len) asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(row + col * 2ull));
-        else w = make_uint4(0, 0, 0, 0);
+// A lane's 8 consecutive columns of a dout row, 16 or 32 bytes, copied to shared memory asynchronously:
+// what is in flight takes no registers.  Each lane copies and reads its own bytes only.
+template <typename In>
+struct Part {
+    static constexpr int kWords = sizeof(In) / 2;  // of 16 bytes
+    uint4 w[kWords];
+
+    static __device__ __forceinline__ void copy(uint32_t to, uint64_t from) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 16) : "memory");
+    }
+    __device__ __forceinline__ void read(uint32_t at) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w) : "r"(at + i * 512) : "memory");
     }
     __device__ __forceinline__ void add(float (&acc)[8]) const {
         float x[8];
-        widen(w, x);
+        if constexpr (kWords == 1) {
+            widen(w[0], x);
+        } else {
+            x[0] = __uint_as_float(w[0].x), x[1] = __uint_as_float(w[0].y), x[2] = __uint_as_float(w[0].z), x[3] = __uint_as_float(w[0].w);
+            x[4] = __uint_as_float(w[1].x), x[5] = __uint_as_float(w[1].y), x[6] = __uint_as_float(w[1].z), x[7] = __uint_as_float(w[1].w);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += x[j];
     }
 };
-template <>
-struct Columns<float, true> {
-    float x[8];
-    __device__ __forceinline__ void load(uint64_t row, uint32_t col, uint32_t len) {
-        if (col < len)
-            asm volatile("ld.global.nc.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
-                         : "l"(row + col * 4ull));
-        else
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-    }
-    __device__ __forceinline__ void add(float (&acc)[8]) const {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += x[j];
-    }
-};
+
+// Every 32nd of 256 columns, for rows that have no 16-byte alignment.
 template <typename In>
-struct Columns<In, false> {
+struct Singles {
     In x[8];
     __device__ __forceinline__ void load(uint64_t row, uint32_t col, uint32_t len) {
 #pragma unroll
@@ -418,29 +427,24 @@ struct Columns<In, false> {
 
 // Adds without waiting for what was there: L2 reads, adds and writes.  Every element is added to once
 // in a call, so the result depends on no order.
-__device__ __forceinline__ void add_v4(float* p, float x, float y, float z, float w) {
-    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
-}
 __device__ __forceinline__ void add_v1(float* p, float x) { asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(x) : "memory"); }
 
-// The warp's sums to the shard: `acc` as the layout spreads them over the lanes.
-template <Layout kLayout>
-__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t t, uint32_t col0, const float (&acc)[8], float* stage) {
+// The warp's sums to a stretch of a row, dst: `acc` as the layout spreads them over the lanes; `left`
+// columns of the row lie from dst on.
+template <Layout kLayout, bool Add>
+__device__ __forceinline__ void write_row(const SumArgs& a, float* dst, uint32_t left, const float (&acc)[8], float* stage) {
     const int lane = threadIdx.x & 31;
-    float* dst = table_row(a, t) + col0;
-    const uint32_t left = a.tv.len - col0;
     float x[8];
     if (kLayout == kWide) {
         if (lane * 8u >= left) return;
         dst += lane * 8;
+        float y[8] = {};
+        // read here and not ahead of need: copies of the rows made as early as dout's (or prefetches,
+        // or additions in L2) took 400 to 420 us where this took 371
+        if (Add) load_v8(dst, y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = acc[j] * a.scale;
-        if (a.accumulate) {
-            add_v4(dst, x[0], x[1], x[2], x[3]);
-            add_v4(dst + 4, x[4], x[5], x[6], x[7]);
-        } else {
-            store_v8(dst, x);
-        }
+        for (int j = 0; j < 8; ++j) x[j] = y[j] + a.scale * acc[j];
+        store_v8(dst, x);
         return;
     }
     if (kLayout == kMixed) {  // lane * 8 + j -> lane + 32 * j, so that stores of single elements lie side by side
@@ -461,7 +465,7 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t t, uint32_t
     for (int j = 0; j < 8; ++j)
         if (lane + 32u * j < left) {
             const float v = a.scale * x[j];
-            if (a.accumulate) add_v1(dst + lane + 32 * j, v);
+            if (Add) add_v1(dst + lane + 32 * j, v);
             else dst[lane + 32 * j] = v;
         }
 }
@@ -506,7 +510,7 @@ __device__ __forceinline__ void add_partials(const SumArgs& a, uint32_t x, uint3
 
 // After a piece has left a partial sum of row t: the last of the row's pieces in this block adds
 // the block's, and the last of its blocks adds the blocks', both in order, and writes the row.
-template <Layout kLayout>
+template <Layout kLayout, bool Add>
 __device__ __forceinline__ void join_partials(const SumArgs& a, uint32_t t, uint32_t piece, uint32_t stretch, float* stage) {
     const uint32_t lane = threadIdx.x & 31, block = piece / kBlock, p0 = block * kBlock, y = p0 + lane;
     // the row has a position in piece y: its first or last position, or (t lying in between) both ends
@@ -551,74 +555,128 @@ __device__ __forceinline__ void join_partials(const SumArgs& a, uint32_t t, uint
         for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
         add_partials(a, a.pieces + first, last - first + 1, 1, stretch, sum);
     }
-    write_row<kLayout>(a, t, stretch * kStretch, sum, stage);
+    const uint32_t col0 = stretch * kStretch;
+    write_row<kLayout, Add>(a, table_row(a, t) + col0, a.tv.len - col0, sum, stage);
 }
 
-template <typename In, Layout kLayout>
-__device__ __forceinline__ void sum_piece(const SumArgs& a, uint32_t piece, uint32_t stretch, float* stage) {
-    constexpr bool Vec = kLayout != kSingle;
-    constexpr int kAhead = Vec ? 16 / sizeof(In) : 4;  // rows in flight: 128 bytes a lane, or 32 single elements
-    const int lane = threadIdx.x & 31;
-    const uint32_t lo = piece * a.piece, hi = min(a.n, lo + a.piece);
-    const uint32_t col0 = stretch * kStretch, col = col0 + (Vec ? lane * 8 : lane);
-    const uint32_t before = lo > 0 ? row_at(a, lo - 1) : ~0u;  // rows on either side of the piece
-    const uint32_t after = hi < a.n ? row_at(a, hi) : ~0u;
+// The running sum of one piece.
+template <Layout kLayout, bool Add>
+struct Run {
+    const SumArgs& a;
+    uint32_t piece, stretch, before;
+    float* stage;
     float acc[8] = {};
     uint32_t cur = ~0u;    // the row being summed
+    float* dst = nullptr;  // its stretch in the shard
     bool starts = true;    // in this piece
-    uint32_t head = ~0u;   // the row that an earlier piece began and this one ends
-    for (uint32_t k0 = lo; k0 < hi; k0 += 32) {
-        // a lane holds one position
-        const uint4 position = k0 + lane < hi ? __ldg(&a.w.sorted[k0 + lane]) : make_uint4(0, 0, a.tv.rows, 0);
-        const uint32_t key = position.z;
-        const unsigned long long src = (unsigned long long)position.y << 32 | position.x;
-        const int held = __popc(__ballot_sync(0xffffffffu, key < a.tv.rows));  // sorted: they come first
+    uint32_t head = ~0u;   // the row that an earlier piece began and this one ended
+
+    __device__ __forceinline__ void write() { write_row<kLayout, Add>(a, dst, a.tv.len - stretch * kStretch, acc, stage); }
+
+    // The next position's row of the table, and where it lies; what the position adds follows.
+    __device__ __forceinline__ void turn_to(uint32_t t, float* to) {
+        if (cur != ~0u) {
+            if (starts) {
+                write();
+            } else {
+                put_partial(partial_of(a, piece, 0, stretch), acc);
+                head = cur;
+            }
+        }
+        cur = t;
+        dst = to;
+        starts = t != before;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    }
+
+    __device__ __forceinline__ void finish(uint32_t after) {
+        uint32_t tail = ~0u;  // the row that a later piece ends
+        if (cur != ~0u) {
+            const bool ends = cur != after;
+            if (starts && ends) {
+                write();
+            } else {
+                put_partial(partial_of(a, piece, starts ? 1 : 0, stretch), acc);
+                if (ends) head = cur; else tail = cur;
+            }
+        }
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {  // rows that run over several pieces
+            const uint32_t t = side ? tail : head;
+            if (t != ~0u) join_partials<kLayout, Add>(a, t, piece, stretch, stage);
+        }
+    }
+};
+
+template <typename In, Layout kLayout, bool Add>
+__device__ __forceinline__ void sum_piece(const SumArgs& a, uint32_t piece, uint32_t stretch, float* stage, uint32_t ring) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t lo = piece * a.piece, hi = min(a.n, lo + a.piece);
+    // a lane holds positions lane and 32 + lane of the piece; those without a token come last
+    static_assert(kPieceMost == 64, "two positions to a lane");
+    const uint4 none = make_uint4(0, 0, a.tv.rows, 0);
+    const uint4 p0 = lo + lane < hi ? __ldg(&a.w.sorted[lo + lane]) : none, p1 = lo + 32 + lane < hi ? __ldg(&a.w.sorted[lo + 32 + lane]) : none;
+    const int held = __popc(__ballot_sync(0xffffffffu, p0.z < a.tv.rows)) + __popc(__ballot_sync(0xffffffffu, p1.z < a.tv.rows));
+    auto of = [&](int k, auto x0, auto x1) { return __shfl_sync(0xffffffffu, k < 32 ? x0 : x1, k & 31); };
+    auto row = [&](int k) { return of(k, p0.z, p1.z); };
+    auto src = [&](int k) { return uint64_t(of(k, p0.y, p1.y)) << 32 | of(k, p0.x, p1.x); };
+    // where their rows lie in the shards, worked out by each lane for its own
+    const auto d0 = reinterpret_cast<unsigned long long>(p0.z < a.tv.rows ? table_row(a, p0.z) + stretch * kStretch : nullptr);
+    const auto d1 = reinterpret_cast<unsigned long long>(p1.z < a.tv.rows ? table_row(a, p1.z) + stretch * kStretch : nullptr);
+    auto place = [&](int k) { return reinterpret_cast<float*>(of(k, d0, d1)); };
+    Run<kLayout, Add> run{a, piece, stretch, lo > 0 ? row_at(a, lo - 1) : ~0u, stage};
+    const uint32_t after = hi < a.n ? row_at(a, hi) : ~0u;  // rows on either side of the piece
+    if constexpr (kLayout == kSingle) {
+        constexpr int kAhead = 4;
+        const uint32_t col = stretch * kStretch + lane;
         for (int k = 0; k < held; k += kAhead) {
-            Columns<In, Vec> x[kAhead];
+            Singles<In> x[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const uint64_t row = __shfl_sync(0xffffffffu, src, (k + u) & 31);
-                if (k + u < held) x[u].load(row, col, a.tv.len);
+                const uint64_t from = src(k + u);
+                if (k + u < held) x[u].load(from, col, a.tv.len);
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (k + u >= held) break;
-                const uint32_t t = __shfl_sync(0xffffffffu, key, k + u);
-                if (t != cur) {
-                    if (cur != ~0u) {
-                        if (starts) {
-                            write_row<kLayout>(a, cur, col0, acc, stage);
-                        } else {
-                            put_partial(partial_of(a, piece, 0, stretch), acc);
-                            head = cur;
-                        }
-                    }
-                    cur = t;
-                    starts = t != before;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-                }
-                x[u].add(acc);
+                const uint32_t t = row(k + u);
+                if (t != run.cur) run.turn_to(t, place(k + u));
+                x[u].add(run.acc);
             }
         }
-        if (held < 32) break;
-    }
-    uint32_t tail = ~0u;  // the row that a later piece ends
-    if (cur != ~0u) {
-        const bool ends = cur != after;
-        if (starts && ends) {
-            write_row<kLayout>(a, cur, col0, acc, stage);
-        } else {
-            put_partial(partial_of(a, piece, starts ? 1 : 0, stretch), acc);
-            if (ends) head = cur; else tail = cur;
+    } else {
+        using R = Ring<In>;
+        const uint32_t col = stretch * kStretch + lane * 8;
+        const bool in = col < a.tv.len;
+        auto slot = [&](int k) { return ring + uint32_t(k) % R::kRows * R::kRow; };
+        auto fetch = [&](int k) {
+#pragma unroll
+            for (int u = 0; u < R::kGroup; ++u) {
+                const uint64_t from = src(k + u);
+                if (in && k + u < held) Part<In>::copy(slot(k + u), from + uint64_t(col) * sizeof(In));
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int k = 0; k < R::kRows; k += R::kGroup) fetch(k);
+        for (int k = 0; k < held; k += R::kGroup) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(R::kGroups - 1) : "memory");
+            Part<In> x[R::kGroup];
+#pragma unroll
+            for (int u = 0; u < R::kGroup; ++u) x[u].read(slot(k + u));
+#pragma unroll
+            for (int u = 0; u < R::kGroup; ++u) {
+                if (k + u >= held) break;
+                const uint32_t t = row(k + u);
+                if (t != run.cur) run.turn_to(t, place(k + u));
+                x[u].add(run.acc);
+            }
+            fetch(k + R::kRows);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    // rows that run over several pieces
-#pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
-        const uint32_t t = side ? tail : head;
-        if (t != ~0u) join_partials<kLayout>(a, t, piece, stretch, stage);
-    }
+    run.finish(after);
 }
 
 // Zeros from p on, n elements, by one warp: 32-byte stores between single ones at the ends.
@@ -674,16 +732,19 @@ __device__ __forceinline__ void zero_rows(const SumArgs& a, uint64_t r0, uint32_
     }
 }
 
-template <typename In, Layout kLayout>
+template <typename In, Layout kLayout, bool Add>
 __global__ void __launch_bounds__(kThreads, kSumCtasPerSm) sum_positions_kernel(const __grid_constant__ SumArgs a) {
     constexpr int kWarps = kThreads / 32;
     __shared__ float stage[kWarps][kLayout == kMixed ? 32 * 9 : 1];
+    extern __shared__ __align__(16) unsigned char rings[];
     const uint32_t warp = threadIdx.x >> 5;
+    // the lane's 16 bytes of the warp's ring
+    const uint32_t ring = uint32_t(__cvta_generic_to_shared(rings)) + warp * Ring<In>::kBytes + (threadIdx.x & 31) * 16;
     for (uint32_t b = blockIdx.x; b < a.sum_blocks + a.zero_blocks; b += gridDim.x) {
         if (b < a.sum_blocks) {
             const uint64_t item = uint64_t(b) * kWarps + warp;
             const uint32_t piece = uint32_t(item / a.stretches);
-            if (piece < a.pieces) sum_piece<In, kLayout>(a, piece, uint32_t(item - uint64_t(piece) * a.stretches), stage[warp]);
+            if (piece < a.pieces) sum_piece<In, kLayout, Add>(a, piece, uint32_t(item - uint64_t(piece) * a.stretches), stage[warp], ring);
         } else {
             const uint64_t padded = uint64_t(a.tv.m) * a.tv.R;
             const uint64_t r0 = (uint64_t(b - a.sum_blocks) * kWarps + warp) * a.zero_rows;
@@ -821,7 +882,7 @@ cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, u
                                  int dout_bf16, bool dout_vec, float scale, bool accumulate, int ctas, bool overlap,
                                  cudaStream_t stream) {
     const GradPlan p = plan_grad(tv, n);
-    SumArgs a{shards, tv, n, p.piece, p.pieces, p.stretches, w, scale, accumulate ? 1 : 0, 0, 0, 1};
+    SumArgs a{shards, tv, n, p.piece, p.pieces, p.stretches, w, scale, 0, 0, 1};
     const int64_t sums = (int64_t(p.pieces) * p.stretches + kThreads / 32 - 1) / (kThreads / 32);
     int64_t zeros = 0;
     if (!accumulate) {
@@ -836,13 +897,22 @@ cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, u
     const int grid = int(std::min<int64_t>(sums + zeros, overlap ? ctas : INT32_MAX));
     const bool wide = tv.len % 8 == 0 && tv.off % 8 == 0 && shards.bits % 32 == 0;
     const Layout layout = !dout_vec || tv.len % 8 ? kSingle : wide ? kWide : kMixed;
-    auto pick = [&](auto in) {
-        using In = decltype(in);
-        return layout == kWide ? sum_positions_kernel<In, kWide> : layout == kMixed ? sum_positions_kernel<In, kMixed> : sum_positions_kernel<In, kSingle>;
+    auto launch = [&](auto* kernel, uint32_t ring) {
+        const int smem = int(ring * (kThreads / 32));
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kernel<<<grid, kThreads, smem, stream>>>(a);
+        return cudaGetLastError();
     };
-    auto* kernel = dout_bf16 ? pick(__nv_bfloat16()) : pick(float());
-    kernel<<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    auto pick = [&](auto in, auto add) {
+        using In = decltype(in);
+        constexpr bool kAdd = decltype(add)::value;
+        if (layout == kSingle) return launch(sum_positions_kernel<In, kSingle, kAdd>, 0);
+        if (layout == kMixed) return launch(sum_positions_kernel<In, kMixed, kAdd>, Ring<In>::kBytes);
+        return launch(sum_positions_kernel<In, kWide, kAdd>, Ring<In>::kBytes);
+    };
+    if (dout_bf16) return accumulate ? pick(__nv_bfloat16(), std::true_type()) : pick(__nv_bfloat16(), std::false_type());
+    return accumulate ? pick(float(), std::true_type()) : pick(float(), std::false_type());
 }
 
 }  // namespace tide
