@@ -150,6 +150,11 @@ int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t* n, 
                     if (expanded) TIDE_CUDA(tide::launch_expand_positions(bt, uint32_t(first), tv.rows, w, g->d_status, st));
                     first += int32_t(bt.start[bt.count]);
                 }
+                if (tide::short_list(total, B)) {
+                    TIDE_CUDA(tide::launch_sum_short(sp, tv, bt, uint32_t(total), dout_type == TIDE_BF16, dout_vec, scale, accumulate != 0,
+                                                     ctas_of(g, tide::kShortCtasPerSm), g->d_status, st));
+                    return TIDE_OK;
+                }
                 TIDE_CUDA(tide::launch_sort_positions(bt, expanded, tv, uint32_t(total), w, g->d_status, st));
             }
             TIDE_CUDA(tide::launch_sum_positions(sp, tv, uint32_t(total), w, dout_type == TIDE_BF16, dout_vec, scale,

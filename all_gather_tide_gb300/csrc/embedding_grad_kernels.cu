@@ -1,148 +1,27 @@
-// Embedding lookup over the packed dim-0 shards of a group, and its gradient (sm_103a).
+// Gradient of the embedding lookup, summed by token into the packed dim-0 shards (sm_103a).
 //
-// Row t of a table of `rows` rows split over R ranks lies on rank d = t / m, at element
-// off + (t - d*m) * len of that rank's shard.  The lookup copies scale * row for every position; the
-// gradient sorts the positions by row (stable, so that equal calls add in the same order) and adds
-// the rows of dout that share a row of the table.
+//     grad row t (+)= scale * sum of the dout rows of the positions that hold t
+//
+// The positions are sorted by row (stable, so that equal calls add in the same order) and each warp adds
+// one stretch of the sorted list over 256 columns; short lists are sorted by every CTA for itself.  What
+// bounds it is HBM: dout is read once, and either the whole piece of every shard is written or the
+// rows that have a token are read and written.
 #include <cooperative_groups.h>
-#include <cuda_bf16.h>
 
 #include <algorithm>
-#include <type_traits>
+#include <atomic>
 
-#include "step_internal.h"
+#include "embedding_device.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace tide {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kStatusBadId = 64;
-
-__device__ __forceinline__ char* shard_base(const ShardPtrs& s, uint32_t d) {
-    return static_cast<char*>(s.table ? s.table[d] : s.p[d]);
-}
-
-__device__ __forceinline__ int64_t load_id(const void* ids, int ids64, int64_t i) {
-    return ids64 ? __ldg(static_cast<const long long*>(ids) + i) : int64_t(__ldg(static_cast<const int*>(ids) + i));
-}
-
-// The table row of an id, or `rows` where the position holds no token.
-__device__ __forceinline__ uint32_t row_of(int64_t id, uint32_t rows) { return id < 0 || id >= int64_t(rows) ? rows : uint32_t(id); }
-
-// The same; ids >= rows are recorded.
-__device__ __forceinline__ uint32_t row_of(const void* ids, int ids64, int64_t i, uint32_t rows, int* status) {
-    const int64_t id = load_id(ids, ids64, i);
-    if (id >= int64_t(rows)) atomicCAS(status, 0, kStatusBadId);
-    return row_of(id, rows);
-}
-
-// V consecutive bf16 elements, widened and scaled.
-template <int V>
-struct Bf16Vec {
-    using Word = typename std::conditional<V == 8, uint4, typename std::conditional<V == 4, uint2, typename std::conditional<V == 2, uint32_t, uint16_t>::type>::type>::type;
-};
-
-__device__ __forceinline__ float low_f32(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-__device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
-    x[0] = low_f32(w.x), x[1] = high_f32(w.x), x[2] = low_f32(w.y), x[3] = high_f32(w.y);
-    x[4] = low_f32(w.z), x[5] = high_f32(w.z), x[6] = low_f32(w.w), x[7] = high_f32(w.w);
-}
-__device__ __forceinline__ void widen(const uint2& w, float (&x)[4]) { x[0] = low_f32(w.x), x[1] = high_f32(w.x), x[2] = low_f32(w.y), x[3] = high_f32(w.y); }
-__device__ __forceinline__ void widen(const uint32_t& w, float (&x)[2]) { x[0] = low_f32(w), x[1] = high_f32(w); }
-__device__ __forceinline__ void widen(const uint16_t& w, float (&x)[1]) { x[0] = low_f32(w); }
-
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ void store_v8(float* p, const float (&x)[8]) {
-    asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
-                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
-}
-__device__ __forceinline__ void load_v8(const float* p, float (&x)[8]) {
-    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
-                 : "l"(p)
-                 : "memory");
-}
-__device__ __forceinline__ void put(float* p, const float (&x)[8]) { store_v8(p, x); }
-__device__ __forceinline__ void put(float* p, const float (&x)[4]) { __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3])); }
-__device__ __forceinline__ void put(float* p, const float (&x)[2]) { __stcs(reinterpret_cast<float2*>(p), make_float2(x[0], x[1])); }
-__device__ __forceinline__ void put(float* p, const float (&x)[1]) { *p = x[0]; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[8]) {
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7])));
-}
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[4]) { __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack(x[0], x[1]), pack(x[2], x[3]))); }
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[2]) { *reinterpret_cast<uint32_t*>(p) = pack(x[0], x[1]); }
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[1]) { *p = __float2bfloat16_rn(x[0]); }
-
-// The lookup.  One warp takes `tokens` positions and a stretch of columns: its lanes look up one
-// position each (id, rank, shard pointer: a chain of loads and a division, paid once for all of the
-// warp's positions), then the warp copies row after row, each lane Cols vectors of V elements at a
-// time, with kLookupVectors<V> loads in flight before their stores.  Rows of fewer than 32 vectors go
-// several at a time (tx = 1 << tx_log lanes each).
-template <int V>
-constexpr int kLookupVectors = V >= 4 ? 8 : 16;
-
-template <typename Out, int V, int Cols>
-__global__ void __launch_bounds__(kThreads, kLookupCtasPerSm)
-embedding_kernel(const __grid_constant__ ShardPtrs shards, TableView tv, const void* __restrict__ ids, int ids64,
-                 int64_t n, float scale, Out* __restrict__ out, int64_t out_stride, int tx_log, int tokens,
-                 uint32_t stretches, int64_t items, int* status) {
-    constexpr int Rows = kLookupVectors<V> / Cols;
-    using Word = typename Bf16Vec<V>::Word;
-    const int lane = threadIdx.x & 31, tx = 1 << tx_log, x = lane & (tx - 1), y = lane >> tx_log, ty = 32 >> tx_log;
-    for (int64_t it = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * (kThreads / 32)) {
-        const int64_t group = it / stretches, i0 = group * tokens;
-        const uint32_t col0 = (uint32_t(it - group * stretches) * (Cols * tx) + x) * V;
-        const int held = int(min(int64_t(tokens), n - i0));
-        // where the lane's position finds its row; 0 where it has no token
-        unsigned long long at = 0;
-        if (lane < held) {
-            const uint32_t t = row_of(ids, ids64, i0 + lane, tv.rows, status);
-            const uint32_t d = t / tv.m;
-            if (t < tv.rows) at = reinterpret_cast<unsigned long long>(shard_base(shards, d)) + 2 * (tv.off + int64_t(t - d * tv.m) * tv.len);
-        }
-        for (int k0 = 0; k0 < held; k0 += Rows * ty) {
-            Word w[Rows][Cols];
-            float f[Rows];
-#pragma unroll
-            for (int r = 0; r < Rows; ++r) {
-                const int k = k0 + r * ty + y;
-                const auto* row = reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, at, k & 31));
-                const bool has = row && k < held;
-                f[r] = has ? scale : 0.0f;  // a row of +0 where there is no token
-#pragma unroll
-                for (int c = 0; c < Cols; ++c) {
-                    const uint32_t col = col0 + c * tx * V;
-                    w[r][c] = Word{};
-                    if (has && col < tv.len) w[r][c] = __ldg(reinterpret_cast<const Word*>(row + col));
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < Rows; ++r) {
-                const int k = k0 + r * ty + y;
-                Out* o = out + (i0 + k) * out_stride;
-#pragma unroll
-                for (int c = 0; c < Cols; ++c) {
-                    const uint32_t col = col0 + c * tx * V;
-                    if (k >= held || col >= tv.len) continue;
-                    float v[V];
-                    widen(w[r][c], v);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) v[j] *= f[r];
-                    put(o + col, v);
-                }
-            }
-        }
-    }
-}
+// Runs once the kernel before it in the stream has ended (launched to overlap with that one's end).
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel's CTAs start where there is room.
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---- sort of positions by row -----------------------------------------------------------------
 
@@ -151,8 +30,6 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMinBits = 6, kSortMaxBits = 10;  // of a digit
 constexpr uint32_t kSortMaxCtas = 16;     // of the cluster
 constexpr uint32_t kSortPerCta = 2048;   // positions for which another CTA joins it
-constexpr uint32_t kPieceMost = 64, kPieceLeast = 8;  // positions of a piece
-constexpr int64_t kPieceWarps = 152 * 24;  // warps for which pieces are cut shorter
 
 __device__ __forceinline__ int batch_of(const Batches& b, uint32_t i) {
     int lo = 0, hi = b.count;
@@ -195,8 +72,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
     const uint32_t C = cluster.num_blocks(), c = cluster.block_rank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int bins = 1 << kBits;
-    extern __shared__ uint32_t smem[];
-    uint32_t* cnt = smem;                       // [kSortWarps][bins]
+    extern __shared__ uint32_t sort_smem[];
+    uint32_t* cnt = sort_smem;                   // [kSortWarps][bins]
     uint32_t* base = cnt + kSortWarps * bins;   // [bins]
     uint32_t* totals = base + bins;             // [C][bins], written by the cluster
     __shared__ uint32_t warp_sum[kSortWarps];
@@ -334,6 +211,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
                 to[at] = make_uint4(uint32_t(src[u]), uint32_t(src[u] >> 32), key[u], 0);
             }
         }
+        if (last) let_next_kernel_start();
         // the next pass reads what other CTAs wrote, and writes their totals again
         if (!last) {
             __threadfence();
@@ -350,32 +228,32 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
 // each; the warp that arrives last adds them in the order of the pieces, so the result does not
 // depend on who that is.  Positions without a token sort last and are not read.
 constexpr uint32_t kStretch = 256;
+constexpr uint32_t kPieceMost = 64, kPieceLeast = 8;  // positions of a piece
+constexpr int64_t kPieceWarps = 152 * 24;             // warps for which pieces are cut shorter
 
-// What a warp has in flight: groups of copies, 2 KB of dout rows each.
-template <typename In>
-struct Ring {
-    static constexpr int kGroups = 3, kGroup = 8 / sizeof(In), kRows = kGroup * kGroups;
-    static constexpr uint32_t kRow = kStretch * sizeof(In), kBytes = kRows * kRow;
-};
-
-struct SumArgs {
+// What the sums go to.
+struct Target {
     ShardPtrs shards;
     TableView tv;
-    uint32_t n, piece, pieces, stretches;
-    GradWorkspace w;
+    uint32_t stretches;
     float scale;
     uint32_t sum_blocks;   // CTAs' worth of sums, before those that write zeros
     uint32_t zero_blocks;
     uint32_t zero_rows;    // rows of the padded table that one warp looks through for rows to zero
 };
 
-__device__ __forceinline__ float* table_row(const SumArgs& a, uint32_t t) {
+struct SumArgs : Target {
+    GradWorkspace w;
+    uint32_t n, piece, pieces;
+};
+
+__device__ __forceinline__ float* table_row(const Target& a, uint32_t t) {
     const uint32_t d = t / a.tv.m;
     return reinterpret_cast<float*>(shard_base(a.shards, d)) + a.tv.off + int64_t(t - d * a.tv.m) * a.tv.len;
 }
 
 // The table row of sorted position i (tv.rows: no token).
-__device__ __forceinline__ uint32_t row_at(const SumArgs& a, uint32_t i) { return __ldg(&a.w.sorted[i].z); }
+__device__ __forceinline__ uint32_t row_at(const SumArgs& a, uint32_t i) { return a.w.sorted[i].z; }
 
 // How a warp's 256 columns lie over its lanes: every 32nd element (kSingle), or 8 consecutive ones, whose
 // rows in the shard are 32-byte aligned (kWide) or not (kMixed).
@@ -425,14 +303,71 @@ struct Singles {
     }
 };
 
-// Adds without waiting for what was there: L2 reads, adds and writes.  Every element is added to once
-// in a call, so the result depends on no order.
-__device__ __forceinline__ void add_v1(float* p, float x) { asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(x) : "memory"); }
+// Rows of dout in flight for a warp: groups of copies, 2 KB each.
+template <typename In>
+struct Ring {
+    static constexpr int kGroups = 3, kGroup = 8 / sizeof(In), kRows = kGroup * kGroups;
+    static constexpr uint32_t kRow = kStretch * sizeof(In), kBytes = kRows * kRow;
+};
+
+// Adds a stretch of `count` rows of dout to acc, in order: src(k) is the k-th row's address, and turn(k) is
+// called before the k-th is added.  `ring`: the lane's place in the warp's shared memory.
+template <typename In, Layout kLayout, typename Src, typename Turn>
+__device__ __forceinline__ void add_rows(int count, uint32_t stretch, uint32_t len, uint32_t ring, Src src, Turn turn, float (&acc)[8]) {
+    const uint32_t lane = threadIdx.x & 31;
+    if constexpr (kLayout == kSingle) {
+        constexpr int kAhead = 4;
+        const uint32_t col = stretch * kStretch + lane;
+        for (int k = 0; k < count; k += kAhead) {
+            Singles<In> x[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const uint64_t from = src(k + u);
+                if (k + u < count) x[u].load(from, col, len);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (k + u >= count) break;
+                turn(k + u);
+                x[u].add(acc);
+            }
+        }
+    } else {
+        using R = Ring<In>;
+        const uint32_t col = stretch * kStretch + lane * 8;
+        const bool in = col < len;
+        auto slot = [&](int k) { return ring + uint32_t(k) % R::kRows * R::kRow; };
+        auto fetch = [&](int k) {
+#pragma unroll
+            for (int u = 0; u < R::kGroup; ++u) {
+                const uint64_t from = src(k + u);
+                if (in && k + u < count) Part<In>::copy(slot(k + u), from + uint64_t(col) * sizeof(In));
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int k = 0; k < R::kRows; k += R::kGroup) fetch(k);
+        for (int k = 0; k < count; k += R::kGroup) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(R::kGroups - 1) : "memory");
+            Part<In> x[R::kGroup];
+#pragma unroll
+            for (int u = 0; u < R::kGroup; ++u) x[u].read(slot(k + u));
+#pragma unroll
+            for (int u = 0; u < R::kGroup; ++u) {
+                if (k + u >= count) break;
+                turn(k + u);
+                x[u].add(acc);
+            }
+            fetch(k + R::kRows);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+}
 
 // The warp's sums to a stretch of a row, dst: `acc` as the layout spreads them over the lanes; `left`
 // columns of the row lie from dst on.
 template <Layout kLayout, bool Add>
-__device__ __forceinline__ void write_row(const SumArgs& a, float* dst, uint32_t left, const float (&acc)[8], float* stage) {
+__device__ __forceinline__ void write_row(float scale, float* dst, uint32_t left, const float (&acc)[8], float* stage) {
     const int lane = threadIdx.x & 31;
     float x[8];
     if (kLayout == kWide) {
@@ -443,7 +378,7 @@ __device__ __forceinline__ void write_row(const SumArgs& a, float* dst, uint32_t
         // or additions in L2) took 400 to 420 us where this took 371
         if (Add) load_v8(dst, y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = y[j] + a.scale * acc[j];
+        for (int j = 0; j < 8; ++j) x[j] = y[j] + scale * acc[j];
         store_v8(dst, x);
         return;
     }
@@ -461,13 +396,12 @@ __device__ __forceinline__ void write_row(const SumArgs& a, float* dst, uint32_t
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = acc[j];
     }
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = Add && lane + 32u * j < left ? dst[lane + 32 * j] : 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        if (lane + 32u * j < left) {
-            const float v = a.scale * x[j];
-            if (Add) add_v1(dst + lane + 32 * j, v);
-            else dst[lane + 32 * j] = v;
-        }
+        if (lane + 32u * j < left) dst[lane + 32 * j] = y[j] + scale * x[j];
 }
 
 // Partial sums meet in two steps: those of up to kBlock consecutive pieces, then those of the
@@ -556,7 +490,7 @@ __device__ __forceinline__ void join_partials(const SumArgs& a, uint32_t t, uint
         add_partials(a, a.pieces + first, last - first + 1, 1, stretch, sum);
     }
     const uint32_t col0 = stretch * kStretch;
-    write_row<kLayout, Add>(a, table_row(a, t) + col0, a.tv.len - col0, sum, stage);
+    write_row<kLayout, Add>(a.scale, table_row(a, t) + col0, a.tv.len - col0, sum, stage);
 }
 
 // The running sum of one piece.
@@ -571,7 +505,7 @@ struct Run {
     bool starts = true;    // in this piece
     uint32_t head = ~0u;   // the row that an earlier piece began and this one ended
 
-    __device__ __forceinline__ void write() { write_row<kLayout, Add>(a, dst, a.tv.len - stretch * kStretch, acc, stage); }
+    __device__ __forceinline__ void write() { write_row<kLayout, Add>(a.scale, dst, a.tv.len - stretch * kStretch, acc, stage); }
 
     // The next position's row of the table, and where it lies; what the position adds follows.
     __device__ __forceinline__ void turn_to(uint32_t t, float* to) {
@@ -616,66 +550,21 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, uint32_t piece, uint
     // a lane holds positions lane and 32 + lane of the piece; those without a token come last
     static_assert(kPieceMost == 64, "two positions to a lane");
     const uint4 none = make_uint4(0, 0, a.tv.rows, 0);
-    const uint4 p0 = lo + lane < hi ? __ldg(&a.w.sorted[lo + lane]) : none, p1 = lo + 32 + lane < hi ? __ldg(&a.w.sorted[lo + 32 + lane]) : none;
+    const uint4 p0 = lo + lane < hi ? a.w.sorted[lo + lane] : none, p1 = lo + 32 + lane < hi ? a.w.sorted[lo + 32 + lane] : none;
     const int held = __popc(__ballot_sync(0xffffffffu, p0.z < a.tv.rows)) + __popc(__ballot_sync(0xffffffffu, p1.z < a.tv.rows));
     auto of = [&](int k, auto x0, auto x1) { return __shfl_sync(0xffffffffu, k < 32 ? x0 : x1, k & 31); };
-    auto row = [&](int k) { return of(k, p0.z, p1.z); };
-    auto src = [&](int k) { return uint64_t(of(k, p0.y, p1.y)) << 32 | of(k, p0.x, p1.x); };
     // where their rows lie in the shards, worked out by each lane for its own
     const auto d0 = reinterpret_cast<unsigned long long>(p0.z < a.tv.rows ? table_row(a, p0.z) + stretch * kStretch : nullptr);
     const auto d1 = reinterpret_cast<unsigned long long>(p1.z < a.tv.rows ? table_row(a, p1.z) + stretch * kStretch : nullptr);
-    auto place = [&](int k) { return reinterpret_cast<float*>(of(k, d0, d1)); };
     Run<kLayout, Add> run{a, piece, stretch, lo > 0 ? row_at(a, lo - 1) : ~0u, stage};
     const uint32_t after = hi < a.n ? row_at(a, hi) : ~0u;  // rows on either side of the piece
-    if constexpr (kLayout == kSingle) {
-        constexpr int kAhead = 4;
-        const uint32_t col = stretch * kStretch + lane;
-        for (int k = 0; k < held; k += kAhead) {
-            Singles<In> x[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const uint64_t from = src(k + u);
-                if (k + u < held) x[u].load(from, col, a.tv.len);
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (k + u >= held) break;
-                const uint32_t t = row(k + u);
-                if (t != run.cur) run.turn_to(t, place(k + u));
-                x[u].add(run.acc);
-            }
-        }
-    } else {
-        using R = Ring<In>;
-        const uint32_t col = stretch * kStretch + lane * 8;
-        const bool in = col < a.tv.len;
-        auto slot = [&](int k) { return ring + uint32_t(k) % R::kRows * R::kRow; };
-        auto fetch = [&](int k) {
-#pragma unroll
-            for (int u = 0; u < R::kGroup; ++u) {
-                const uint64_t from = src(k + u);
-                if (in && k + u < held) Part<In>::copy(slot(k + u), from + uint64_t(col) * sizeof(In));
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-#pragma unroll
-        for (int k = 0; k < R::kRows; k += R::kGroup) fetch(k);
-        for (int k = 0; k < held; k += R::kGroup) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(R::kGroups - 1) : "memory");
-            Part<In> x[R::kGroup];
-#pragma unroll
-            for (int u = 0; u < R::kGroup; ++u) x[u].read(slot(k + u));
-#pragma unroll
-            for (int u = 0; u < R::kGroup; ++u) {
-                if (k + u >= held) break;
-                const uint32_t t = row(k + u);
-                if (t != run.cur) run.turn_to(t, place(k + u));
-                x[u].add(run.acc);
-            }
-            fetch(k + R::kRows);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    }
+    add_rows<In, kLayout>(
+        held, stretch, a.tv.len, ring, [&](int k) { return uint64_t(of(k, p0.y, p1.y)) << 32 | of(k, p0.x, p1.x); },
+        [&](int k) {
+            const uint32_t t = of(k, p0.z, p1.z);
+            if (t != run.cur) run.turn_to(t, reinterpret_cast<float*>(of(k, d0, d1)));
+        },
+        run.acc);
     run.finish(after);
 }
 
@@ -690,14 +579,14 @@ __device__ __forceinline__ void zero_run(float* p, uint32_t n) {
     for (uint32_t i = head + vecs * 8 + lane; i < n; i += 32) p[i] = 0.0f;
 }
 
-// The first sorted position in [lo, hi) whose row is >= r (hi if none), found by the whole warp, 32
+// The first of the sorted positions [lo, hi) whose row is >= r (hi if none), found by the whole warp, 32
 // places at a time.
-__device__ __forceinline__ uint32_t first_at_least(const SumArgs& a, uint32_t r, uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ uint32_t first_at_least(const uint4* sorted, uint32_t r, uint32_t lo, uint32_t hi) {
     const uint32_t lane = threadIdx.x & 31;
     while (lo < hi) {
         const uint32_t step = (hi - lo + 32) / 33;  // lane k looks at the last position of the k-th part
         const uint64_t x = uint64_t(lo) + uint64_t(lane + 1) * step - 1;
-        const uint32_t below = __ballot_sync(0xffffffffu, x < hi && row_at(a, uint32_t(x)) < r);
+        const uint32_t below = __ballot_sync(0xffffffffu, x < hi && sorted[x].z < r);
         const uint32_t k = __popc(below);  // sorted: a prefix of the lanes
         const uint64_t end = uint64_t(lo) + uint64_t(k + 1) * step - 1;
         lo += k * step;
@@ -706,22 +595,24 @@ __device__ __forceinline__ uint32_t first_at_least(const SumArgs& a, uint32_t r,
     return lo;
 }
 
-// Zeros to those of the rows [r0, r0 + count) of the padded table, count <= 32, that have no token, by one
-// warp.  Padding rows, from tv.rows on, never have one.
-__device__ __forceinline__ void zero_rows(const SumArgs& a, uint64_t r0, uint32_t count) {
-    const uint32_t lane = threadIdx.x & 31;
+// Zeros to those of the rows [r0, r0 + zero_rows) of the padded table that have none of the n sorted
+// positions, by one warp.  Padding rows, from tv.rows on, never have one.
+__device__ __forceinline__ void zero_rows(const Target& a, uint64_t r0, const uint4* sorted, uint32_t n) {
+    const uint64_t padded = uint64_t(a.tv.m) * a.tv.R;
+    if (r0 >= padded) return;
+    const uint32_t lane = threadIdx.x & 31, count = uint32_t(min(uint64_t(a.zero_rows), padded - r0));
     uint32_t has = 0;
     if (r0 < a.tv.rows) {
         const uint32_t real = uint32_t(min(uint64_t(count), a.tv.rows - r0));
-        const uint32_t lo = first_at_least(a, uint32_t(r0), 0, a.n), hi = first_at_least(a, uint32_t(r0) + real, lo, a.n);
+        const uint32_t lo = first_at_least(sorted, uint32_t(r0), 0, n), hi = first_at_least(sorted, uint32_t(r0) + real, lo, n);
         if (lo < hi) {  // some of them do: each lane looks for its own
             uint32_t x = lo, y = hi;
             if (lane < real)
                 while (x < y) {
                     const uint32_t mid = x + (y - x) / 2;
-                    if (row_at(a, mid) < uint32_t(r0) + lane) x = mid + 1; else y = mid;
+                    if (sorted[mid].z < uint32_t(r0) + lane) x = mid + 1; else y = mid;
                 }
-            has = __ballot_sync(0xffffffffu, lane < real && x < hi && row_at(a, x) == uint32_t(r0) + lane);
+            has = __ballot_sync(0xffffffffu, lane < real && x < hi && sorted[x].z == uint32_t(r0) + lane);
         }
     }
     for (uint32_t k = 0; k < count; ++k) {
@@ -732,82 +623,189 @@ __device__ __forceinline__ void zero_rows(const SumArgs& a, uint64_t r0, uint32_
     }
 }
 
-template <typename In, Layout kLayout, bool Add>
-__global__ void __launch_bounds__(kThreads, kSumCtasPerSm) sum_positions_kernel(const __grid_constant__ SumArgs a) {
-    constexpr int kWarps = kThreads / 32;
-    __shared__ float stage[kWarps][kLayout == kMixed ? 32 * 9 : 1];
-    extern __shared__ __align__(16) unsigned char rings[];
+// Dynamic shared memory of a CTA of sums: the warps' rings, or, for single elements, nothing; and for
+// kMixed what write_row turns the columns round in.
+template <typename In, Layout kLayout>
+constexpr uint32_t kSumSmem = kLayout == kSingle ? 0 : kWarps * (Ring<In>::kBytes + (kLayout == kMixed ? 32 * 9 * 4 : 0));
+
+template <typename In, Layout kLayout>
+__device__ __forceinline__ void sum_smem(unsigned char* smem, uint32_t* ring, float** stage) {
     const uint32_t warp = threadIdx.x >> 5;
-    // the lane's 16 bytes of the warp's ring
-    const uint32_t ring = uint32_t(__cvta_generic_to_shared(rings)) + warp * Ring<In>::kBytes + (threadIdx.x & 31) * 16;
+    *ring = uint32_t(__cvta_generic_to_shared(smem)) + warp * Ring<In>::kBytes + (threadIdx.x & 31) * 16;
+    *stage = reinterpret_cast<float*>(smem + kWarps * Ring<In>::kBytes) + warp * (32 * 9);
+}
+
+// CTAs of an SM that registers leave room for: 4, except where 3 measured faster (65536 positions into
+// 128000 x 8192, most of it zeros to write: 753 us with 3, 780 with 4; 131072 added to 128000 x 4096: 377
+// with 3, 363 with 4) or the rows in flight take registers (kSingle).
+template <Layout kLayout, bool Add>
+constexpr int kSumCtas = kLayout == kSingle || !Add ? 3 : kSumCtasPerSm;
+
+template <typename In, Layout kLayout, bool Add>
+__global__ void __launch_bounds__(kThreads, kSumCtas<kLayout, Add>) sum_positions_kernel(const __grid_constant__ SumArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint32_t ring;
+    float* stage;
+    sum_smem<In, kLayout>(smem, &ring, &stage);
+    wait_for_previous_kernel();
     for (uint32_t b = blockIdx.x; b < a.sum_blocks + a.zero_blocks; b += gridDim.x) {
         if (b < a.sum_blocks) {
-            const uint64_t item = uint64_t(b) * kWarps + warp;
+            const uint64_t item = uint64_t(b) * kWarps + (threadIdx.x >> 5);
             const uint32_t piece = uint32_t(item / a.stretches);
-            if (piece < a.pieces) sum_piece<In, kLayout, Add>(a, piece, uint32_t(item - uint64_t(piece) * a.stretches), stage[warp], ring);
+            if (piece < a.pieces) sum_piece<In, kLayout, Add>(a, piece, uint32_t(item - uint64_t(piece) * a.stretches), stage, ring);
         } else {
-            const uint64_t padded = uint64_t(a.tv.m) * a.tv.R;
-            const uint64_t r0 = (uint64_t(b - a.sum_blocks) * kWarps + warp) * a.zero_rows;
-            if (r0 < padded) zero_rows(a, r0, uint32_t(min(uint64_t(a.zero_rows), padded - r0)));
+            zero_rows(a, (uint64_t(b - a.sum_blocks) * kWarps + (threadIdx.x >> 5)) * a.zero_rows, a.w.sorted, a.n);
         }
     }
 }
 
-}  // namespace
+// ---- short lists ----------------------------------------------------------------------------------
+//
+// Up to kShortMost positions: one launch instead of two, no workspace.  Every CTA sorts the list for
+// itself (each position's place is the number of positions that come before it), and one warp adds all
+// positions of one row.
+constexpr uint32_t kShortMost = kThreads;
 
-namespace {
+struct ShortArgs : Target {
+    Batches b;
+    uint32_t n;
+    int* status;
+};
 
-// The widest vector (8, 4, 2 or 1 elements) that every row address of the table and, of `elem` bytes
-// an element, every row address of the other array allow.
-int vector_of(const TableView& tv, uintptr_t shard_bits, size_t shard_elem, uintptr_t other, int64_t stride, size_t elem) {
-    for (int v = 8; v > 1; v >>= 1)
-        if (tv.len % v == 0 && tv.off % v == 0 && stride % v == 0 && shard_bits % (v * shard_elem) == 0 && other % (v * elem) == 0) return v;
-    return 1;
-}
+template <typename In, Layout kLayout, bool Add>
+__global__ void __launch_bounds__(kThreads, 3) sum_short_kernel(const __grid_constant__ ShortArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ __align__(16) uint32_t keys[kShortMost];
+    __shared__ uint4 sorted[kShortMost];
+    uint32_t ring;
+    float* stage;
+    sum_smem<In, kLayout>(smem, &ring, &stage);
+    const uint32_t i = threadIdx.x;
+    uint32_t key = ~0u;
+    uint64_t src = 0;
+    if (i < a.n) {
+        const int k = batch_of(a.b, i);
+        const uint32_t j = i - a.b.start[k];
+        const int64_t id = load_id(a.b.ids[k], a.b.ids64, j);
+        if (blockIdx.x == 0 && id >= int64_t(a.tv.rows)) atomicCAS(a.status, 0, kStatusBadId);
+        key = row_of(id, a.tv.rows);
+        src = reinterpret_cast<uint64_t>(a.b.dout[k] + int64_t(j) * a.b.stride[k]);
+    }
+    keys[i] = key;
+    __syncthreads();
+    uint32_t place = 0;
+    for (uint32_t j = 0; j < a.n; j += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&keys[j]);  // ~0 from n on: behind every position
+        place += (o.x < key + (j < i)) + (o.y < key + (j + 1 < i)) + (o.z < key + (j + 2 < i)) + (o.w < key + (j + 3 < i));
+    }
+    if (i < a.n) sorted[place] = make_uint4(uint32_t(src), uint32_t(src >> 32), key, 0);
+    __syncthreads();
 
-template <typename Out, int V>
-cudaError_t lookup(const ShardPtrs& shards, const TableView& tv, const void* ids, int ids64, int64_t n, float scale,
-                   Out* out, int64_t out_stride, int ctas, bool overlap, int* status, cudaStream_t stream) {
-    const int64_t vecs = tv.len / V;
-    int tx_log = 0;
-    while (tx_log < 5 && (1 << tx_log) < vecs) ++tx_log;
-    const int cols = V <= 2 && vecs >= 256 ? 8 : vecs >= 128 ? 4 : vecs >= 64 ? 2 : 1;
-    const int64_t stretches = (vecs + cols * (1 << tx_log) - 1) / (cols * (1 << tx_log));
-    // Positions of a warp: at least 8 while that leaves each of the resident warps an item (one
-    // wave), fewer below; up to 32 while there are 8 waves of items, whose ends then cost little.
-    const int64_t slots = int64_t(ctas) * (kThreads / 32);
-    auto count = [&](int tokens) { return (n + tokens - 1) / tokens * stretches; };
-    int tokens = 32;
-    while (tokens > 8 && count(tokens) < 8 * slots) tokens >>= 1;
-    while (tokens > 1 && count(tokens) < slots) tokens >>= 1;
-    const int64_t items = count(tokens);
-    const int grid = int(std::min<int64_t>((items + kThreads / 32 - 1) / (kThreads / 32), overlap ? ctas : INT32_MAX));
-    auto* kernel = cols == 8 ? embedding_kernel<Out, V, V <= 2 ? 8 : 4> : cols == 4 ? embedding_kernel<Out, V, 4> : cols == 2 ? embedding_kernel<Out, V, 2> : embedding_kernel<Out, V, 1>;
-    kernel<<<grid, kThreads, 0, stream>>>(shards, tv, ids, ids64, n, scale, out, out_stride, tx_log, tokens, uint32_t(stretches), items, status);
-    return cudaGetLastError();
-}
-
-template <typename Out>
-cudaError_t lookup_any(const ShardPtrs& shards, const TableView& tv, const void* ids, int ids64, int64_t n, float scale,
-                       Out* out, int64_t out_stride, int ctas, bool overlap, int* status, cudaStream_t stream) {
-    switch (vector_of(tv, shards.bits, 2, reinterpret_cast<uintptr_t>(out), n > 1 ? out_stride : 0, sizeof(Out))) {
-        case 8: return lookup<Out, 8>(shards, tv, ids, ids64, n, scale, out, out_stride, ctas, overlap, status, stream);
-        case 4: return lookup<Out, 4>(shards, tv, ids, ids64, n, scale, out, out_stride, ctas, overlap, status, stream);
-        case 2: return lookup<Out, 2>(shards, tv, ids, ids64, n, scale, out, out_stride, ctas, overlap, status, stream);
-        default: return lookup<Out, 1>(shards, tv, ids, ids64, n, scale, out, out_stride, ctas, overlap, status, stream);
+    const uint32_t lane = threadIdx.x & 31;
+    for (uint32_t b = blockIdx.x; b < a.sum_blocks + a.zero_blocks; b += gridDim.x) {
+        if (b >= a.sum_blocks) {
+            zero_rows(a, (uint64_t(b - a.sum_blocks) * kWarps + (threadIdx.x >> 5)) * a.zero_rows, sorted, a.n);
+            continue;
+        }
+        const uint64_t item = uint64_t(b) * kWarps + (threadIdx.x >> 5);
+        if (item >= uint64_t(a.n) * a.stretches) continue;
+        const uint32_t p = uint32_t(item / a.stretches), stretch = uint32_t(item - uint64_t(p) * a.stretches);
+        const uint32_t t = sorted[p].z;
+        if (t >= a.tv.rows || (p > 0 && sorted[p - 1].z == t)) continue;  // the row's first position has it
+        uint32_t end = p + 1;
+        for (bool more = true; more;) {
+            const uint32_t out = ~__ballot_sync(0xffffffffu, end + lane < a.n && sorted[end + lane].z == t);
+            end += out ? __ffs(out) - 1 : 32;
+            more = out == 0;
+        }
+        float acc[8] = {};
+        add_rows<In, kLayout>(
+            int(end - p), stretch, a.tv.len, ring,
+            [&](int k) {
+                const uint4 x = sorted[min(p + k, a.n - 1)];
+                return uint64_t(x.y) << 32 | x.x;
+            },
+            [](int) {}, acc);
+        write_row<kLayout, Add>(a.scale, table_row(a, t) + stretch * kStretch, a.tv.len - stretch * kStretch, acc, stage);
     }
 }
 
-}  // namespace
-
-cudaError_t launch_embedding(const ShardPtrs& shards, const TableView& tv, const void* ids, int ids64, int64_t n,
-                             float scale, void* out, int out_bf16, int64_t out_stride, int ctas, bool overlap, int* status,
-                             cudaStream_t stream) {
-    if (n <= 0) return cudaSuccess;
-    if (out_bf16)
-        return lookup_any(shards, tv, ids, ids64, n, scale, static_cast<__nv_bfloat16*>(out), out_stride, ctas, overlap, status, stream);
-    return lookup_any(shards, tv, ids, ids64, n, scale, static_cast<float*>(out), out_stride, ctas, overlap, status, stream);
+// Sets a kernel's attributes once for each device.
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t> (&done)[4], F&& set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    std::atomic<uint64_t>& word = done[(dev >> 6) & 3];
+    if (dev < 256 && (word.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess && dev < 256) word.fetch_or(bit, std::memory_order_release);
+    return e;
 }
+
+template <typename In, Layout kLayout, bool Add>
+cudaError_t launch_sum(const SumArgs& a, int grid, cudaStream_t stream) {
+    static std::atomic<uint64_t> done[4];
+    auto* kernel = sum_positions_kernel<In, kLayout, Add>;
+    constexpr uint32_t smem = kSumSmem<In, kLayout>;
+    cudaError_t e = once_per_device(done, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); });
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = a.n > 0 ? 1 : 0;  // without positions no sort comes before it
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename In, Layout kLayout, bool Add>
+cudaError_t launch_short(const ShortArgs& a, int grid, cudaStream_t stream) {
+    static std::atomic<uint64_t> done[4];
+    auto* kernel = sum_short_kernel<In, kLayout, Add>;
+    constexpr uint32_t smem = kSumSmem<In, kLayout>;
+    cudaError_t e = once_per_device(done, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); });
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+// Calls launch.template operator()<In, kLayout, Add>() for the call's types and alignments.
+template <typename F>
+cudaError_t with_kinds(const Target& a, int dout_bf16, bool dout_vec, bool accumulate, F&& launch) {
+    const bool wide = a.tv.len % 8 == 0 && a.tv.off % 8 == 0 && a.shards.bits % 32 == 0;
+    const Layout layout = !dout_vec || a.tv.len % 8 ? kSingle : wide ? kWide : kMixed;
+    auto with_add = [&](auto in, auto add) {
+        if (layout == kSingle) return launch(in, std::integral_constant<Layout, kSingle>(), add);
+        if (layout == kMixed) return launch(in, std::integral_constant<Layout, kMixed>(), add);
+        return launch(in, std::integral_constant<Layout, kWide>(), add);
+    };
+    if (dout_bf16) return accumulate ? with_add(__nv_bfloat16(), std::true_type()) : with_add(__nv_bfloat16(), std::false_type());
+    return accumulate ? with_add(float(), std::true_type()) : with_add(float(), std::false_type());
+}
+
+// CTAs of sums and of zeros; false if they are more than a grid holds.
+bool cut_blocks(Target* a, int64_t items, bool accumulate) {
+    const int64_t sums = (items + kWarps - 1) / kWarps;
+    int64_t zeros = 0;
+    a->zero_rows = 1;
+    if (!accumulate) {
+        // one row to a warp, or up to 32 that make about 32 KB of zeros
+        a->zero_rows = uint32_t(std::min<int64_t>(32, std::max<int64_t>(1, 8192 / a->tv.len)));
+        zeros = (int64_t(a->tv.m) * a->tv.R + a->zero_rows * kWarps - 1) / (a->zero_rows * kWarps);
+    }
+    if (sums + zeros > INT32_MAX) return false;
+    a->sum_blocks = uint32_t(sums);
+    a->zero_blocks = uint32_t(zeros);
+    return true;
+}
+
+}  // namespace
 
 GradPlan plan_grad(const TableView& tv, int64_t n) {
     GradPlan g;
@@ -848,71 +846,76 @@ cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t r
     return cudaGetLastError();
 }
 
-cudaError_t launch_sort_positions(const Batches& b, bool expanded, const TableView& tv, uint32_t n,
-                                  const GradWorkspace& w, int* status, cudaStream_t stream) {
-    int bits = 0;
-    while (tv.rows >> bits) ++bits;  // keys are 0 .. rows
-    const GradPlan p = plan_grad(tv, n);
-    SortArgs a{b, n, tv.rows, expanded ? 1 : 0, (bits + kSortMaxBits - 1) / kSortMaxBits, p.slots, w, status};
-    const int digit = std::max(kSortMinBits, (bits + a.passes - 1) / a.passes);
-    static_assert(kSortMinBits == 6 && kSortMaxBits == 10, "one kernel for each digit size");
-    auto* kernel = digit == 6 ? sort_positions_kernel<6> : digit == 7 ? sort_positions_kernel<7> : digit == 8 ? sort_positions_kernel<8>
-                   : digit == 9 ? sort_positions_kernel<9> : sort_positions_kernel<10>;
-    uint32_t c = 1;
-    while (c < kSortMaxCtas && n > c * kSortPerCta) c <<= 1;
-    const size_t smem = (size_t(kSortWarps) + 1 + c) * (size_t(1) << digit) * 4;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+namespace {
+
+template <int kBits>
+cudaError_t launch_sort(const SortArgs& a, uint32_t ctas, cudaStream_t stream) {
+    static std::atomic<uint64_t> done[4];
+    auto* kernel = sort_positions_kernel<kBits>;
+    auto smem = [](uint32_t c) { return (size_t(kSortWarps) + 1 + c) * (size_t(1) << kBits) * 4; };
+    const cudaError_t e = once_per_device(done, [&] {
+        const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem(kSortMaxCtas)));
+        return s != cudaSuccess ? s : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = c;
+    attr.val.clusterDim.x = ctas;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(c);
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = smem(ctas);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+}  // namespace
+
+cudaError_t launch_sort_positions(const Batches& b, bool expanded, const TableView& tv, uint32_t n,
+                                  const GradWorkspace& w, int* status, cudaStream_t stream) {
+    int bits = 0;
+    while (tv.rows >> bits) ++bits;  // keys are 0 .. rows
+    SortArgs a{b, n, tv.rows, expanded ? 1 : 0, (bits + kSortMaxBits - 1) / kSortMaxBits, plan_grad(tv, n).slots, w, status};
+    uint32_t ctas = 1;
+    while (ctas < kSortMaxCtas && n > ctas * kSortPerCta) ctas <<= 1;
+    static_assert(kSortMinBits == 6 && kSortMaxBits == 10, "one kernel for each digit size");
+    switch (std::max(kSortMinBits, (bits + a.passes - 1) / a.passes)) {
+        case 6: return launch_sort<6>(a, ctas, stream);
+        case 7: return launch_sort<7>(a, ctas, stream);
+        case 8: return launch_sort<8>(a, ctas, stream);
+        case 9: return launch_sort<9>(a, ctas, stream);
+        default: return launch_sort<10>(a, ctas, stream);
+    }
+}
+
 cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, uint32_t n, const GradWorkspace& w,
                                  int dout_bf16, bool dout_vec, float scale, bool accumulate, int ctas, bool overlap,
                                  cudaStream_t stream) {
     const GradPlan p = plan_grad(tv, n);
-    SumArgs a{shards, tv, n, p.piece, p.pieces, p.stretches, w, scale, 0, 0, 1};
-    const int64_t sums = (int64_t(p.pieces) * p.stretches + kThreads / 32 - 1) / (kThreads / 32);
-    int64_t zeros = 0;
-    if (!accumulate) {
-        // one row to a warp, or up to 32 that make about 32 KB of zeros
-        a.zero_rows = uint32_t(std::min<int64_t>(32, std::max<int64_t>(1, 8192 / tv.len)));
-        zeros = (int64_t(tv.m) * tv.R + a.zero_rows * (kThreads / 32) - 1) / (a.zero_rows * (kThreads / 32));
-    }
-    if (sums + zeros > INT32_MAX) return cudaErrorInvalidValue;
-    if (sums + zeros == 0) return cudaSuccess;
-    a.sum_blocks = uint32_t(sums);
-    a.zero_blocks = uint32_t(zeros);
-    const int grid = int(std::min<int64_t>(sums + zeros, overlap ? ctas : INT32_MAX));
-    const bool wide = tv.len % 8 == 0 && tv.off % 8 == 0 && shards.bits % 32 == 0;
-    const Layout layout = !dout_vec || tv.len % 8 ? kSingle : wide ? kWide : kMixed;
-    auto launch = [&](auto* kernel, uint32_t ring) {
-        const int smem = int(ring * (kThreads / 32));
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        kernel<<<grid, kThreads, smem, stream>>>(a);
-        return cudaGetLastError();
-    };
-    auto pick = [&](auto in, auto add) {
-        using In = decltype(in);
-        constexpr bool kAdd = decltype(add)::value;
-        if (layout == kSingle) return launch(sum_positions_kernel<In, kSingle, kAdd>, 0);
-        if (layout == kMixed) return launch(sum_positions_kernel<In, kMixed, kAdd>, Ring<In>::kBytes);
-        return launch(sum_positions_kernel<In, kWide, kAdd>, Ring<In>::kBytes);
-    };
-    if (dout_bf16) return accumulate ? pick(__nv_bfloat16(), std::true_type()) : pick(__nv_bfloat16(), std::false_type());
-    return accumulate ? pick(float(), std::true_type()) : pick(float(), std::false_type());
+    SumArgs a{{shards, tv, p.stretches, scale}, w, n, p.piece, p.pieces};
+    if (!cut_blocks(&a, int64_t(p.pieces) * p.stretches, accumulate)) return cudaErrorInvalidValue;
+    const int64_t blocks = int64_t(a.sum_blocks) + a.zero_blocks;
+    if (blocks == 0) return cudaSuccess;
+    const int grid = int(std::min<int64_t>(blocks, overlap ? ctas : INT32_MAX));
+    return with_kinds(a, dout_bf16, dout_vec, accumulate, [&](auto in, auto layout, auto add) {
+        return launch_sum<decltype(in), decltype(layout)::value, decltype(add)::value>(a, grid, stream);
+    });
+}
+
+bool short_list(int64_t n, int32_t batches) { return n > 0 && n <= int64_t(kShortMost) && batches <= kInlineBatches; }
+
+cudaError_t launch_sum_short(const ShardPtrs& shards, const TableView& tv, const Batches& b, uint32_t n, int dout_bf16,
+                             bool dout_vec, float scale, bool accumulate, int ctas, int* status, cudaStream_t stream) {
+    ShortArgs a{{shards, tv, (tv.len + kStretch - 1) / kStretch, scale}, b, n, status};
+    if (!cut_blocks(&a, int64_t(n) * a.stretches, accumulate)) return cudaErrorInvalidValue;
+    // no more CTAs than fit at once: each sorts the list
+    const int grid = int(std::min<int64_t>(int64_t(a.sum_blocks) + a.zero_blocks, ctas));
+    return with_kinds(a, dout_bf16, dout_vec, accumulate, [&](auto in, auto layout, auto add) {
+        return launch_short<decltype(in), decltype(layout)::value, decltype(add)::value>(a, grid, stream);
+    });
 }
 
 }  // namespace tide

@@ -1,0 +1,126 @@
+// Embedding lookup over the packed dim-0 shards of a group (sm_103a).
+//
+// Row t of a table of `rows` rows split over R ranks lies on rank d = t / m, at element
+// off + (t - d*m) * len of that rank's shard; out row i = scale * row ids[i].
+#include <algorithm>
+
+#include "embedding_device.cuh"
+
+namespace tide {
+namespace {
+
+// The lookup.  One warp takes `tokens` positions and a stretch of columns: its lanes look up one
+// position each (id, rank, shard pointer: a chain of loads and a division, paid once for all of the
+// warp's positions), then the warp copies row after row, each lane Cols vectors of V elements at a
+// time, with kLookupVectors<V> loads in flight before their stores.  Rows of fewer than 32 vectors go
+// several at a time (tx = 1 << tx_log lanes each).
+template <int V>
+constexpr int kLookupVectors = V >= 4 ? 8 : 16;
+
+template <typename Out, int V, int Cols>
+__global__ void __launch_bounds__(kThreads, kLookupCtasPerSm)
+embedding_kernel(const __grid_constant__ ShardPtrs shards, TableView tv, const void* __restrict__ ids, int ids64,
+                 int64_t n, float scale, Out* __restrict__ out, int64_t out_stride, int tx_log, int tokens,
+                 uint32_t stretches, int64_t items, int* status) {
+    constexpr int Rows = kLookupVectors<V> / Cols;
+    using Word = typename Bf16Vec<V>::Word;
+    const int lane = threadIdx.x & 31, tx = 1 << tx_log, x = lane & (tx - 1), y = lane >> tx_log, ty = 32 >> tx_log;
+    for (int64_t it = int64_t(blockIdx.x) * (kWarps) + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * (kWarps)) {
+        const int64_t group = it / stretches, i0 = group * tokens;
+        const uint32_t col0 = (uint32_t(it - group * stretches) * (Cols * tx) + x) * V;
+        const int held = int(min(int64_t(tokens), n - i0));
+        // where the lane's position finds its row; 0 where it has no token
+        unsigned long long at = 0;
+        if (lane < held) {
+            const uint32_t t = row_of(ids, ids64, i0 + lane, tv.rows, status);
+            const uint32_t d = t / tv.m;
+            if (t < tv.rows) at = reinterpret_cast<unsigned long long>(shard_base(shards, d)) + 2 * (tv.off + int64_t(t - d * tv.m) * tv.len);
+        }
+        for (int k0 = 0; k0 < held; k0 += Rows * ty) {
+            Word w[Rows][Cols];
+            float f[Rows];
+#pragma unroll
+            for (int r = 0; r < Rows; ++r) {
+                const int k = k0 + r * ty + y;
+                const auto* row = reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, at, k & 31));
+                const bool has = row && k < held;
+                f[r] = has ? scale : 0.0f;  // a row of +0 where there is no token
+#pragma unroll
+                for (int c = 0; c < Cols; ++c) {
+                    const uint32_t col = col0 + c * tx * V;
+                    w[r][c] = Word{};
+                    if (has && col < tv.len) w[r][c] = __ldg(reinterpret_cast<const Word*>(row + col));
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < Rows; ++r) {
+                const int k = k0 + r * ty + y;
+                Out* o = out + (i0 + k) * out_stride;
+#pragma unroll
+                for (int c = 0; c < Cols; ++c) {
+                    const uint32_t col = col0 + c * tx * V;
+                    if (k >= held || col >= tv.len) continue;
+                    float v[V];
+                    widen(w[r][c], v);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) v[j] *= f[r];
+                    put(o + col, v);
+                }
+            }
+        }
+    }
+}
+
+// The widest vector (8, 4, 2 or 1 elements) that every row address of the table and, of `elem` bytes
+// an element, every row address of the other array allow.
+int vector_of(const TableView& tv, uintptr_t shard_bits, size_t shard_elem, uintptr_t other, int64_t stride, size_t elem) {
+    for (int v = 8; v > 1; v >>= 1)
+        if (tv.len % v == 0 && tv.off % v == 0 && stride % v == 0 && shard_bits % (v * shard_elem) == 0 && other % (v * elem) == 0) return v;
+    return 1;
+}
+
+template <typename Out, int V>
+cudaError_t lookup(const ShardPtrs& shards, const TableView& tv, const void* ids, int ids64, int64_t n, float scale,
+                   Out* out, int64_t out_stride, int ctas, bool overlap, int* status, cudaStream_t stream) {
+    const int64_t vecs = tv.len / V;
+    int tx_log = 0;
+    while (tx_log < 5 && (1 << tx_log) < vecs) ++tx_log;
+    const int cols = V <= 2 && vecs >= 256 ? 8 : vecs >= 128 ? 4 : vecs >= 64 ? 2 : 1;
+    const int64_t stretches = (vecs + cols * (1 << tx_log) - 1) / (cols * (1 << tx_log));
+    // Positions of a warp: at least 8 while that leaves each of the resident warps an item (one
+    // wave), fewer below; up to 32 while there are 8 waves of items, whose ends then cost little.
+    const int64_t slots = int64_t(ctas) * (kWarps);
+    auto count = [&](int tokens) { return (n + tokens - 1) / tokens * stretches; };
+    int tokens = 32;
+    while (tokens > 8 && count(tokens) < 8 * slots) tokens >>= 1;
+    while (tokens > 1 && count(tokens) < slots) tokens >>= 1;
+    const int64_t items = count(tokens);
+    const int grid = int(std::min<int64_t>((items + kWarps - 1) / (kWarps), overlap ? ctas : INT32_MAX));
+    auto* kernel = cols == 8 ? embedding_kernel<Out, V, V <= 2 ? 8 : 4> : cols == 4 ? embedding_kernel<Out, V, 4> : cols == 2 ? embedding_kernel<Out, V, 2> : embedding_kernel<Out, V, 1>;
+    kernel<<<grid, kThreads, 0, stream>>>(shards, tv, ids, ids64, n, scale, out, out_stride, tx_log, tokens, uint32_t(stretches), items, status);
+    return cudaGetLastError();
+}
+
+template <typename Out>
+cudaError_t lookup_any(const ShardPtrs& shards, const TableView& tv, const void* ids, int ids64, int64_t n, float scale,
+                       Out* out, int64_t out_stride, int ctas, bool overlap, int* status, cudaStream_t stream) {
+    switch (vector_of(tv, shards.bits, 2, reinterpret_cast<uintptr_t>(out), n > 1 ? out_stride : 0, sizeof(Out))) {
+        case 8: return lookup<Out, 8>(shards, tv, ids, ids64, n, scale, out, out_stride, ctas, overlap, status, stream);
+        case 4: return lookup<Out, 4>(shards, tv, ids, ids64, n, scale, out, out_stride, ctas, overlap, status, stream);
+        case 2: return lookup<Out, 2>(shards, tv, ids, ids64, n, scale, out, out_stride, ctas, overlap, status, stream);
+        default: return lookup<Out, 1>(shards, tv, ids, ids64, n, scale, out, out_stride, ctas, overlap, status, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(const ShardPtrs& shards, const TableView& tv, const void* ids, int ids64, int64_t n,
+                             float scale, void* out, int out_bf16, int64_t out_stride, int ctas, bool overlap, int* status,
+                             cudaStream_t stream) {
+    if (n <= 0) return cudaSuccess;
+    if (out_bf16)
+        return lookup_any(shards, tv, ids, ids64, n, scale, static_cast<__nv_bfloat16*>(out), out_stride, ctas, overlap, status, stream);
+    return lookup_any(shards, tv, ids, ids64, n, scale, static_cast<float*>(out), out_stride, ctas, overlap, status, stream);
+}
+
+}  // namespace tide

@@ -13,6 +13,7 @@ namespace tide {
 constexpr int kInlineRanks = 64;    // shard pointers that travel with a launch
 constexpr int kLookupCtasPerSm = 4;
 constexpr int kSumCtasPerSm = 4;
+constexpr int kShortCtasPerSm = 3;
 constexpr int kInlineBatches = 64;  // batches that travel with a launch
 
 // The R shard pointers of a call: in the launch's own parameters up to kInlineRanks, else in a device
@@ -56,8 +57,7 @@ struct GradWorkspace {
     uint32_t* arrived;   // [slots] counts of arrivals
     float* partial;      // [slots][256] partial sums
 };
-// How the sorted list is summed: pieces of positions, stretches of columns, and room for two partial
-// sums of every stretch of every piece and of every block of pieces.
+// How the sorted list is summed: pieces of positions, stretches of 256 columns, and slots for partial sums.
 struct GradPlan {
     uint32_t piece, pieces, stretches;
     int64_t slots;
@@ -74,6 +74,11 @@ cudaError_t launch_sort_positions(const Batches& b, bool expanded, const TableVi
 cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, uint32_t n, const GradWorkspace& w,
                                  int dout_bf16, bool dout_vec, float scale, bool accumulate, int ctas, bool overlap,
                                  cudaStream_t stream);
+
+// Whether a list goes by one launch that sorts and sums, without a workspace, and that launch.
+bool short_list(int64_t n, int32_t batches);
+cudaError_t launch_sum_short(const ShardPtrs& shards, const TableView& tv, const Batches& b, uint32_t n, int dout_bf16,
+                             bool dout_vec, float scale, bool accumulate, int ctas, int* status, cudaStream_t stream);
 
 // ---- lists of tensors -------------------------------------------------------------------------
 constexpr int64_t kTsChunk = 2048;  // elements of one work item
