@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libtide.so")
 SOURCES = ["plan.cpp", "tide_api.cpp", "rs_kernel.cu", "rs_bulk_kernel.cu", "ag_kernel.cu", "ag_bulk_kernel.cu", "noalloc.cu", "probes.cu",
            "embedding_api.cpp", "embedding_kernel.cu", "embedding_grad_kernels.cu", "tensor_api.cpp", "tensor_kernels.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("tide_internal.h", "table_ring.h", "group.h", "api_common.h", "step_internal.h",
-                                              "copy_any.cuh", "embedding_device.cuh")]
+                                              "copy_any.cuh", "embedding_device.cuh", "step_launch.cuh")]
 HEADERS.append(os.path.join(ROOT, "include", "tide.h"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

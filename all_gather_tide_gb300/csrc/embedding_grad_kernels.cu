@@ -12,16 +12,12 @@
 #include <atomic>
 
 #include "embedding_device.cuh"
+#include "step_launch.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace tide {
 namespace {
-
-// Runs once the kernel before it in the stream has ended (launched to overlap with that one's end).
-__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the next kernel's CTAs start where there is room.
-__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---- sort of positions by row -----------------------------------------------------------------
 
@@ -751,17 +747,7 @@ cudaError_t launch_sum(const SumArgs& a, int grid, cudaStream_t stream) {
     constexpr uint32_t smem = kSumSmem<In, kLayout>;
     cudaError_t e = once_per_device(done, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); });
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(grid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = a.n > 0 ? 1 : 0;  // without positions no sort comes before it
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return launch_after(kernel, grid, kThreads, smem, stream, a);
 }
 
 template <typename In, Layout kLayout, bool Add>
@@ -795,9 +781,10 @@ bool cut_blocks(Target* a, int64_t items, bool accumulate) {
     int64_t zeros = 0;
     a->zero_rows = 1;
     if (!accumulate) {
-        // one row to a warp, or up to 32 that make about 32 KB of zeros
-        a->zero_rows = uint32_t(std::min<int64_t>(32, std::max<int64_t>(1, 8192 / a->tv.len)));
-        zeros = (int64_t(a->tv.m) * a->tv.R + a->zero_rows * kWarps - 1) / (a->zero_rows * kWarps);
+        // one row to a warp, or up to 32 that make about 32 KB of zeros while the GPU's warps stay busy
+        const int64_t padded = int64_t(a->tv.m) * a->tv.R;
+        a->zero_rows = uint32_t(std::max<int64_t>(1, std::min<int64_t>({32, 8192 / a->tv.len, padded / kPieceWarps})));
+        zeros = (padded + a->zero_rows * kWarps - 1) / (a->zero_rows * kWarps);
     }
     if (sums + zeros > INT32_MAX) return false;
     a->sum_blocks = uint32_t(sums);

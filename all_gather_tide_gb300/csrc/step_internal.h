@@ -81,16 +81,17 @@ cudaError_t launch_sum_short(const ShardPtrs& shards, const TableView& tv, const
                              bool dout_vec, float scale, bool accumulate, int ctas, int* status, cudaStream_t stream);
 
 // ---- lists of tensors -------------------------------------------------------------------------
-constexpr int64_t kTsChunk = 2048;  // elements of one work item
+constexpr int kTsChunkMost = 2048, kTsChunkLeast = 256;  // elements of one work item
 constexpr int kTsThreads = 256;
 constexpr int kTsCtasPerSm = 4;
 constexpr int kAdamwCtasPerSm = 3;
 
-struct TsSeg {
-    int64_t elems;
-    int64_t chunk_begin;  // index of the tensor's first work item
-    int32_t bf16;         // the gradient's type
-    int32_t pad_;
+// One work item: elements [i*chunk, i*chunk + left) of tensor k, left cut off at chunk + 8.
+struct TsItem {
+    int32_t k;
+    uint32_t i;
+    int32_t left;
+    int32_t bf16;  // the gradient's type
 };
 
 struct AdamwArgs {
@@ -101,16 +102,19 @@ struct AdamwArgs {
 };
 
 struct TsList {
-    const TsSeg* segs;
-    const int32_t* chunk_seg;  // tensor of every work item
+    const TsItem* items;
     int64_t chunks;
     int32_t K;
+    int32_t chunk;  // elements of a work item
 };
 
 cudaError_t launch_grad_norm(const TsList& l, const void* const* grads, double* partial, unsigned* ticket, float* norm,
                              double* sumsq, int ctas, cudaStream_t stream);
 cudaError_t launch_clip(const TsList& l, void* const* grads, const float* norm, float max_norm, int ctas,
                         cudaStream_t stream);
+// The norm and clipping by it in two launches, the second of which ends the norm's sum.
+cudaError_t launch_clip_norm(const TsList& l, void* const* grads, double* partial, float* norm, float max_norm, int ctas,
+                             cudaStream_t stream);
 // tables: K pointers each of params, grads, exp_avg, exp_avg_sq and shards (shards unused when
 // write_shards is 0), then K floats 1 - lr * weight_decay.
 cudaError_t launch_adamw(const TsList& l, void* const* tables, int write_shards, const AdamwArgs& a, int ctas,

@@ -15,18 +15,19 @@ struct tide_tensors {
     std::vector<int64_t> elems;
     std::vector<uint8_t> bf16;
     int64_t chunks = 0;
+    int32_t chunk = tide::kTsChunkMost;
     int device = 0;
     int sm_count = 0;
-    char* d_block = nullptr;  // tickets, partial sums, segs and chunk_seg in one allocation
+    char* d_block = nullptr;       // tickets, partial sums and items in one allocation
     unsigned* d_ticket = nullptr;  // one per ring slot
     double* d_partial = nullptr;   // max_ctas per ring slot
-    tide::TsSeg* d_segs = nullptr;
-    int32_t* d_chunk_seg = nullptr;
+    tide::TsItem* d_items = nullptr;
     tide::TableRing ring;
     std::mutex mu;
 
     int max_ctas() const { return sm_count * tide::kTsCtasPerSm; }
-    tide::TsList list() const { return {d_segs, d_chunk_seg, chunks, K}; }
+    double* partial(int slot) const { return d_partial + int64_t(slot) * max_ctas(); }
+    tide::TsList list() const { return {d_items, chunks, K, chunk}; }
 };
 
 namespace {
@@ -35,6 +36,7 @@ using tide::aligned;
 using tide::no_throw;
 
 constexpr int64_t kMaxElems = int64_t(1) << 42;
+constexpr int64_t kItemsWanted = 152 * 32;  // the warps of a GB300 at four CTAs an SM
 
 void release(tide_tensors* t) {
     t->ring.release();
@@ -61,21 +63,11 @@ int upload_grads(tide_tensors* t, const void* const* grads, cudaStream_t st, int
     return TIDE_OK;
 }
 
-int norm_in_slot(tide_tensors* t, int slot, float* norm, double* sumsq, cudaStream_t st) {
-    TIDE_CUDA(tide::launch_grad_norm(t->list(), t->ring.slots[slot].dev, t->d_partial + int64_t(slot) * t->max_ctas(),
-                                     t->d_ticket + slot, norm, sumsq, t->max_ctas(), st));
-    return TIDE_OK;
-}
-
-int clip_in_slot(tide_tensors* t, int slot, const float* norm, float max_norm, cudaStream_t st) {
-    TIDE_CUDA(tide::launch_clip(t->list(), t->ring.slots[slot].dev, norm, max_norm, t->max_ctas(), st));
-    return TIDE_OK;
-}
-
 // Marks the slot's table as in use by what `st` holds, and passes on the launches' status.
-int finish(tide_tensors* t, int slot, cudaStream_t st, int rc) {
+int finish(tide_tensors* t, int slot, cudaStream_t st, cudaError_t launched) {
     const cudaError_t e = t->ring.finish(slot, st);
-    return rc != TIDE_OK ? rc : e == cudaSuccess ? TIDE_OK : tide::record_cuda_error(e);
+    if (launched != cudaSuccess) return tide::record_cuda_error(launched);
+    return e == cudaSuccess ? TIDE_OK : tide::record_cuda_error(e);
 }
 
 bool bad_max_norm(float v) { return !(v >= 0.0f); }  // NaN too
@@ -90,26 +82,31 @@ int tide_tensors_create(tide_tensors_t* out, int32_t K, const int64_t* elems, co
         *out = nullptr;
         if (!elems || K < 1) return TIDE_EINVAL;
         if (K > TIDE_MAX_TABLE / 8) return TIDE_ERANGE;
-        std::vector<tide::TsSeg> segs(static_cast<size_t>(K));
         std::vector<uint8_t> bf16(static_cast<size_t>(K));
-        int64_t chunks = 0, total = 0;
+        int64_t total = 0;
         for (int k = 0; k < K; ++k) {
             if (elems[k] < 0) return TIDE_EINVAL;
             if (types && types[k] != TIDE_F32 && types[k] != TIDE_BF16) return TIDE_EINVAL;
             if (elems[k] > kMaxElems || (total += elems[k]) > kMaxElems) return TIDE_ERANGE;
             bf16[size_t(k)] = types && types[k] == TIDE_BF16;
-            segs[size_t(k)] = {elems[k], chunks, bf16[size_t(k)], 0};
-            // one item more than the elements fill, where the first may start up to 7 before the tensor
-            if (elems[k] > 0) chunks += (elems[k] + 7 + tide::kTsChunk - 1) / tide::kTsChunk;
         }
-        std::vector<int32_t> chunk_seg;
-        chunk_seg.reserve(size_t(chunks));
+        // short items where long ones would not give every warp of the GPU one
+        int chunk = tide::kTsChunkMost;
+        while (chunk > tide::kTsChunkLeast && total / chunk < kItemsWanted) chunk >>= 1;
+        // one item more than the elements fill, where the first may start up to 7 before the tensor
+        auto count = [&](int64_t n) { return n > 0 ? (n + 7 + chunk - 1) / chunk : 0; };
+        int64_t chunks = 0;
+        for (int k = 0; k < K; ++k) chunks += count(elems[k]);
+        std::vector<tide::TsItem> items;
+        items.reserve(size_t(chunks));
         for (int k = 0; k < K; ++k)
-            chunk_seg.insert(chunk_seg.end(), size_t((k + 1 < K ? segs[size_t(k) + 1].chunk_begin : chunks) - segs[size_t(k)].chunk_begin), k);
+            for (int64_t i = 0, m = count(elems[k]); i < m; ++i)
+                items.push_back({k, uint32_t(i), int32_t(std::min<int64_t>(elems[k] - i * chunk, chunk + 8)), bf16[size_t(k)]});
 
         tide_tensors* t = new tide_tensors();
         t->K = K;
         t->chunks = chunks;
+        t->chunk = chunk;
         cudaError_t e;
         try {
             t->elems.assign(elems, elems + K);
@@ -117,18 +114,15 @@ int tide_tensors_create(tide_tensors_t* out, int32_t K, const int64_t* elems, co
             e = cudaGetDevice(&t->device);
             if (e == cudaSuccess) e = cudaDeviceGetAttribute(&t->sm_count, cudaDevAttrMultiProcessorCount, t->device);
             const size_t ticket_bytes = 256, partial_bytes = size_t(tide::kSlots) * size_t(t->max_ctas()) * sizeof(double);
-            const size_t seg_bytes = segs.size() * sizeof(tide::TsSeg);
-            if (e == cudaSuccess) e = cudaMalloc(&t->d_block, ticket_bytes + partial_bytes + seg_bytes + chunk_seg.size() * 4 + 8);
+            const size_t item_bytes = items.size() * sizeof(tide::TsItem);
+            if (e == cudaSuccess) e = cudaMalloc(&t->d_block, ticket_bytes + partial_bytes + item_bytes);
             if (e == cudaSuccess) {
                 t->d_ticket = reinterpret_cast<unsigned*>(t->d_block);
                 t->d_partial = reinterpret_cast<double*>(t->d_block + ticket_bytes);
-                t->d_segs = reinterpret_cast<tide::TsSeg*>(t->d_block + ticket_bytes + partial_bytes);
-                t->d_chunk_seg = reinterpret_cast<int32_t*>(t->d_block + ticket_bytes + partial_bytes + seg_bytes);
+                t->d_items = reinterpret_cast<tide::TsItem*>(t->d_block + ticket_bytes + partial_bytes);
                 e = cudaMemset(t->d_ticket, 0, ticket_bytes);
             }
-            if (e == cudaSuccess) e = cudaMemcpy(t->d_segs, segs.data(), seg_bytes, cudaMemcpyHostToDevice);
-            if (e == cudaSuccess && !chunk_seg.empty())
-                e = cudaMemcpy(t->d_chunk_seg, chunk_seg.data(), chunk_seg.size() * 4, cudaMemcpyHostToDevice);
+            if (e == cudaSuccess && item_bytes) e = cudaMemcpy(t->d_items, items.data(), item_bytes, cudaMemcpyHostToDevice);
             // five pointers and a factor for every tensor
             if (e == cudaSuccess) e = t->ring.create(size_t(K) * 6);
         } catch (...) {
@@ -158,7 +152,8 @@ int tide_grad_norm(tide_tensors_t t, const void* const* grads, float* norm, doub
         int slot;
         const int rc = upload_grads(t, grads, st, &slot);
         if (rc != TIDE_OK) return rc;
-        return finish(t, slot, st, norm_in_slot(t, slot, norm, sumsq, st));
+        return finish(t, slot, st,
+                      tide::launch_grad_norm(t->list(), t->ring.slots[slot].dev, t->partial(slot), t->d_ticket + slot, norm, sumsq, t->max_ctas(), st));
     });
 }
 
@@ -170,7 +165,7 @@ int tide_clip_grads(tide_tensors_t t, void* const* grads, const float* norm, flo
         int slot;
         const int rc = upload_grads(t, grads, st, &slot);
         if (rc != TIDE_OK) return rc;
-        return finish(t, slot, st, clip_in_slot(t, slot, norm, max_norm, st));
+        return finish(t, slot, st, tide::launch_clip(t->list(), t->ring.slots[slot].dev, norm, max_norm, t->max_ctas(), st));
     });
 }
 
@@ -180,11 +175,9 @@ int tide_clip_grad_norm(tide_tensors_t t, void* const* grads, float max_norm, fl
         std::lock_guard<std::mutex> lock(t->mu);
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         int slot;
-        int rc = upload_grads(t, grads, st, &slot);
+        const int rc = upload_grads(t, grads, st, &slot);
         if (rc != TIDE_OK) return rc;
-        rc = norm_in_slot(t, slot, norm, nullptr, st);
-        if (rc == TIDE_OK) rc = clip_in_slot(t, slot, norm, max_norm, st);
-        return finish(t, slot, st, rc);
+        return finish(t, slot, st, tide::launch_clip_norm(t->list(), t->ring.slots[slot].dev, t->partial(slot), norm, max_norm, t->max_ctas(), st));
     });
 }
 
@@ -229,8 +222,7 @@ int tide_adamw(tide_tensors_t t, void* const* params, const void* const* grads, 
         a.skip_nonfinite = (flags & TIDE_ADAMW_SKIP_NONFINITE) ? 1 : 0;
         int slot;
         TIDE_CUDA(t->ring.upload(table, st, &slot));
-        const cudaError_t e = tide::launch_adamw(t->list(), t->ring.slots[slot].dev, shards ? 1 : 0, a, t->sm_count * tide::kAdamwCtasPerSm, st);
-        return finish(t, slot, st, e == cudaSuccess ? TIDE_OK : tide::record_cuda_error(e));
+        return finish(t, slot, st, tide::launch_adamw(t->list(), t->ring.slots[slot].dev, shards ? 1 : 0, a, t->sm_count * tide::kAdamwCtasPerSm, st));
     });
 }
 

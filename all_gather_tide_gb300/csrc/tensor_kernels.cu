@@ -1,38 +1,41 @@
 // Operators over a list of tensors: global gradient norm, clipping, AdamW (sm_103a).
 //
-// A work item is kTsChunk consecutive elements of one tensor, and one warp takes one item at a time,
+// A work item is `chunk` consecutive elements of one tensor, and one warp takes one item at a time,
 // so that thousands of small tensors spread over the GPU as well as a few large ones.  Items are cut
 // on the tensor's own 8-element boundaries (32 bytes of fp32, 16 of bf16): item i covers elements
-// [i*kTsChunk - mis, (i+1)*kTsChunk - mis) of a tensor whose first element lies mis elements past a
+// [i*chunk - mis, (i+1)*chunk - mis) of a tensor whose first element lies mis elements past a
 // boundary, so every group of 8 that lies inside the tensor is one aligned vector, and only the
-// groups at the tensor's ends go element by element.
+// groups at the tensor's ends go element by element.  A list too short to give every warp of the GPU
+// 2048 elements has shorter items, down to one group for each lane.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
 #include "step_internal.h"
+#include "step_launch.cuh"
 
 namespace tide {
 namespace {
 
 constexpr int kWarps = kTsThreads / 32;
-constexpr int kGroups = int(kTsChunk / 256);  // groups of 8 elements a lane has in an item
 
+// Offsets are elements from the item's nominal first element, begin.
 struct Item {
-    int k;         // tensor
-    int64_t i;     // item of the tensor
-    int64_t elems;
-    bool bf16;     // the gradient's type
+    int k;          // tensor
+    int64_t begin;  // in the tensor
+    int left;       // elements of the tensor from there on, as far as they matter to the item
+    bool bf16;      // the gradient's type
+
+    // For an array that lies mis elements past a boundary: the first element of the lane's first
+    // group, the end of the item, and the least offset inside the tensor.
+    __device__ __forceinline__ int first(unsigned mis) const { return int(threadIdx.x & 31) * 8 - int(mis); }
+    __device__ __forceinline__ int end(unsigned mis, int chunk) const { return min(left, chunk - int(mis)); }
+    __device__ __forceinline__ int least() const { return begin == 0 ? 0 : -8; }
 };
 
 __device__ __forceinline__ Item item_of(const TsList& l, int64_t c) {
-    Item it;
-    it.k = __ldg(&l.chunk_seg[c]);
-    const TsSeg* s = l.segs + it.k;
-    it.i = c - __ldg(&s->chunk_begin);
-    it.elems = __ldg(&s->elems);
-    it.bf16 = __ldg(&s->bf16) != 0;
-    return it;
+    const int4 x = __ldg(reinterpret_cast<const int4*>(l.items) + c);
+    return {x.x, int64_t(uint32_t(x.y)) * l.chunk, x.z, x.w != 0};
 }
 
 __device__ __forceinline__ int64_t first_item() { return int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); }
@@ -86,33 +89,33 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(p) = w;
 }
 
-// The group of 8 elements from e on of a tensor of n, as raw words: whole groups as a vector where
-// `vec` says that the array has the alignment, else element by element; elements outside the tensor
-// read as 0 (and, in store_group, are not written).
+// The group of 8 elements from offset e on, as raw words: groups inside [lo, end) as a vector where
+// `vec` says that the array has the alignment, else element by element; elements outside read as 0
+// (and, in store_group, are not written).
 __device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
 __device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 
 template <typename T>
-__device__ __forceinline__ void load_group(const T* p, int64_t e, int64_t n, bool vec, uint32_t (&w)[2 * sizeof(T)]) {
-    if (vec && e >= 0 && e + 8 <= n) {
+__device__ __forceinline__ void load_group(const T* p, int e, int lo, int end, bool vec, uint32_t (&w)[2 * sizeof(T)]) {
+    if (vec && e >= lo && e + 8 <= end) {
         load_raw(p + e, w);
     } else {
         constexpr int kPer = 4 / sizeof(T);  // elements in a word
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t b = e + j >= 0 && e + j < n ? bits_of(p[e + j]) : 0u;
+            const uint32_t b = e + j >= lo && e + j < end ? bits_of(p[e + j]) : 0u;
             w[j / kPer] = j % kPer ? w[j / kPer] | b << 16 : b;
         }
     }
 }
 template <typename T>
-__device__ __forceinline__ void store_group(T* p, int64_t e, int64_t n, bool vec, const float (&x)[8]) {
-    if (vec && e >= 0 && e + 8 <= n) {
+__device__ __forceinline__ void store_group(T* p, int e, int lo, int end, bool vec, const float (&x)[8]) {
+    if (vec && e >= lo && e + 8 <= end) {
         store8(p + e, x);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (e + j >= 0 && e + j < n) narrow(p + e + j, x[j]);
+            if (e + j >= lo && e + j < end) narrow(p + e + j, x[j]);
     }
 }
 
@@ -126,6 +129,13 @@ __device__ __forceinline__ double block_sum(double v) {
     if (threadIdx.x == 0)
         for (int w = 1; w < kWarps; ++w) v += part[w];
     return v;
+}
+
+// The CTAs' sums of squares in their order, over the CTA; valid in thread 0.
+__device__ __forceinline__ double sum_partials(const double* partial, unsigned count) {
+    double all = 0.0;
+    for (unsigned b = threadIdx.x; b < count; b += kTsThreads) all += __ldcg(&partial[b]);
+    return block_sum(all);
 }
 
 // The sum of squares of 32 numbers.  In fp32 while no square can have left its range: a sum in
@@ -160,15 +170,15 @@ template <typename T>
 constexpr int kBatch = int(16 / sizeof(T));
 
 template <typename T>
-__device__ __forceinline__ double item_squares(const T* g, const Item& it) {
-    const int64_t base = it.i * kTsChunk - misalign(g) + (threadIdx.x & 31) * 8;
+__device__ __forceinline__ double item_squares(const T* g, const Item& it, int chunk) {
+    const unsigned mis = misalign(g);
+    const int lo = it.least(), end = it.end(mis, chunk);
+    g += it.begin;
     double sum = 0.0;
-#pragma unroll
-    for (int h = 0; h < kGroups; h += kBatch<T>) {
-        if (base + h * 256 >= it.elems) break;
+    for (int e = it.first(mis); e < end; e += kBatch<T> * 256) {
         uint32_t w[kBatch<T>][2 * sizeof(T)];
 #pragma unroll
-        for (int q = 0; q < kBatch<T>; ++q) load_group(g, base + (h + q) * 256, it.elems, true, w[q]);
+        for (int q = 0; q < kBatch<T>; ++q) load_group(g, e + q * 256, lo, end, true, w[q]);
 #pragma unroll
         for (int q = 0; q < kBatch<T>; q += 4) {
             float x[4][8];
@@ -180,17 +190,25 @@ __device__ __forceinline__ double item_squares(const T* g, const Item& it) {
     return sum;
 }
 
+// Sums of squares of the CTAs to partial; with Finish the CTA that arrives last adds them in the
+// CTAs' order.
+template <bool Finish>
 __global__ void __launch_bounds__(kTsThreads, kTsCtasPerSm)
 grad_norm_kernel(TsList l, const void* const* __restrict__ grads, double* partial, unsigned* ticket, float* norm,
                  double* sumsq) {
+    wait_for_previous_kernel();
     double sum = 0.0;
     for (int64_t c = first_item(); c < l.chunks; c += item_stride()) {
         const Item it = item_of(l, c);
         const void* g = grads[it.k];
-        sum += it.bf16 ? item_squares(static_cast<const __nv_bfloat16*>(g), it) : item_squares(static_cast<const float*>(g), it);
+        sum += it.bf16 ? item_squares(static_cast<const __nv_bfloat16*>(g), it, l.chunk) : item_squares(static_cast<const float*>(g), it, l.chunk);
     }
+    let_next_kernel_start();
     sum = block_sum(sum);
-    // the CTA that arrives last adds the CTAs' sums in their order
+    if (!Finish) {
+        if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+        return;
+    }
     __shared__ bool last;
     if (threadIdx.x == 0) {
         partial[blockIdx.x] = sum;
@@ -200,9 +218,7 @@ grad_norm_kernel(TsList l, const void* const* __restrict__ grads, double* partia
     __syncthreads();
     if (!last) return;
     __threadfence();
-    double all = 0.0;
-    for (unsigned b = threadIdx.x; b < gridDim.x; b += kTsThreads) all += __ldcg(&partial[b]);
-    all = block_sum(all);
+    const double all = sum_partials(partial, gridDim.x);
     if (threadIdx.x == 0) {
         norm[0] = float(sqrt(all));
         if (sumsq) sumsq[0] = all;
@@ -211,41 +227,56 @@ grad_norm_kernel(TsList l, const void* const* __restrict__ grads, double* partia
 }
 
 // min(1, max_norm / (norm + 1e-6)), NaN where that is NaN.
-__device__ __forceinline__ float clip_factor(const float* norm, float max_norm) {
-    const float q = __fdiv_rn(max_norm, __fadd_rn(*norm, 1e-6f));
+__device__ __forceinline__ float clip_factor(float norm, float max_norm) {
+    const float q = __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f));
     return q >= 1.0f ? 1.0f : q;
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_item(T* g, const Item& it, float f) {
-    const int64_t base = it.i * kTsChunk - misalign(g) + (threadIdx.x & 31) * 8;
-#pragma unroll
-    for (int h = 0; h < kGroups; h += kBatch<T>) {
-        if (base + h * 256 >= it.elems) break;
+__device__ __forceinline__ void scale_item(T* g, const Item& it, int chunk, float f) {
+    const unsigned mis = misalign(g);
+    const int lo = it.least(), end = it.end(mis, chunk);
+    g += it.begin;
+    for (int e = it.first(mis); e < end; e += kBatch<T> * 256) {
         uint32_t w[kBatch<T>][2 * sizeof(T)];
 #pragma unroll
-        for (int q = 0; q < kBatch<T>; ++q) load_group(g, base + (h + q) * 256, it.elems, true, w[q]);
+        for (int q = 0; q < kBatch<T>; ++q) load_group(g, e + q * 256, lo, end, true, w[q]);
 #pragma unroll
         for (int q = 0; q < kBatch<T>; ++q) {
             float x[8];
             unpack(w[q], x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] *= f;
-            store_group(g, base + (h + q) * 256, it.elems, true, x);
+            store_group(g, e + q * 256, lo, end, true, x);
         }
     }
 }
 
 __global__ void __launch_bounds__(kTsThreads, kTsCtasPerSm)
-clip_kernel(TsList l, void* const* __restrict__ grads, const float* __restrict__ norm, float max_norm) {
-    const float f = clip_factor(norm, max_norm);
+clip_kernel(TsList l, void* const* __restrict__ grads, float* norm, const double* partial, unsigned parts, float max_norm) {
+    wait_for_previous_kernel();
+    // the norm, or, straight after grad_norm_kernel<false>, what it left of it
+    float n;
+    if (parts) {
+        __shared__ float shared_norm;
+        const double all = sum_partials(partial, parts);
+        if (threadIdx.x == 0) {
+            shared_norm = float(sqrt(all));
+            if (blockIdx.x == 0) norm[0] = shared_norm;
+        }
+        __syncthreads();
+        n = shared_norm;
+    } else {
+        n = *norm;
+    }
+    const float f = clip_factor(n, max_norm);
     if (f == 1.0f) return;
     // from the last item to the first: what the norm read last is what L2 still holds
     for (int64_t c = l.chunks - 1 - first_item(); c >= 0; c -= item_stride()) {
         const Item it = item_of(l, c);
         void* g = grads[it.k];
-        if (it.bf16) scale_item(static_cast<__nv_bfloat16*>(g), it, f);
-        else scale_item(static_cast<float*>(g), it, f);
+        if (it.bf16) scale_item(static_cast<__nv_bfloat16*>(g), it, l.chunk, f);
+        else scale_item(static_cast<float*>(g), it, l.chunk, f);
     }
 }
 
@@ -261,15 +292,14 @@ __device__ __forceinline__ void adamw_item(const TsList& l, const AdamwArgs& a, 
     const float keep = __ldg(reinterpret_cast<const float*>(tables + 5 * K) + it.k);
     const unsigned mis = misalign(p);
     const bool gv = misalign(g) == mis, mv = misalign(m) == mis, vv = misalign(v) == mis, wv = misalign(w) == mis;
-    const int64_t base = it.i * kTsChunk - mis + (threadIdx.x & 31) * 8;
-    for (int q = 0; q < kGroups; ++q) {
-        const int64_t e = base + q * 256;
-        if (e >= it.elems) break;
+    const int lo = it.least(), end = it.end(mis, l.chunk);
+    p += it.begin, g += it.begin, m += it.begin, v += it.begin, w += it.begin;
+    for (int e = it.first(mis); e < end; e += 256) {
         uint32_t pw[8], gw[2 * sizeof(T)], mw[8], vw[8];
-        load_group(p, e, it.elems, true, pw);
-        load_group(g, e, it.elems, gv, gw);
-        load_group(m, e, it.elems, mv, mw);
-        load_group(v, e, it.elems, vv, vw);
+        load_group(p, e, lo, end, true, pw);
+        load_group(g, e, lo, end, gv, gw);
+        load_group(m, e, lo, end, mv, mw);
+        load_group(v, e, lo, end, vv, vw);
         float pi[8], gi[8], mi[8], vi[8];
         unpack(pw, pi), unpack(gw, gi), unpack(mw, mi), unpack(vw, vi);
 #pragma unroll
@@ -280,20 +310,21 @@ __device__ __forceinline__ void adamw_item(const TsList& l, const AdamwArgs& a, 
             const float den = __fsqrt_rn(vi[j]) * a.inv_sqrt_c2 + a.eps;
             pi[j] = pi[j] * keep - a.step_size * __fdiv_rn(mi[j], den);
         }
-        store_group(m, e, it.elems, mv, mi);
-        store_group(v, e, it.elems, vv, vi);
-        store_group(p, e, it.elems, true, pi);
-        if (write_shards) store_group(w, e, it.elems, wv, pi);
+        store_group(m, e, lo, end, mv, mi);
+        store_group(v, e, lo, end, vv, vi);
+        store_group(p, e, lo, end, true, pi);
+        if (write_shards) store_group(w, e, lo, end, wv, pi);
     }
 }
 
 __global__ void __launch_bounds__(kTsThreads, kAdamwCtasPerSm)
 adamw_kernel(TsList l, void* const* __restrict__ tables, int write_shards, AdamwArgs a) {
+    wait_for_previous_kernel();
     float f = 1.0f;
     if (a.norm) {
         const float n = *a.norm;
         if (a.skip_nonfinite && !isfinite(n)) return;
-        f = clip_factor(a.norm, a.max_norm);
+        f = clip_factor(n, a.max_norm);
     }
     for (int64_t c = first_item(); c < l.chunks; c += item_stride()) {
         const Item it = item_of(l, c);
@@ -308,22 +339,29 @@ int grid_of(const TsList& l, int ctas) { return int(std::max<int64_t>(1, std::mi
 
 cudaError_t launch_grad_norm(const TsList& l, const void* const* grads, double* partial, unsigned* ticket, float* norm,
                              double* sumsq, int ctas, cudaStream_t stream) {
-    grad_norm_kernel<<<grid_of(l, ctas), kTsThreads, 0, stream>>>(l, grads, partial, ticket, norm, sumsq);
-    return cudaGetLastError();
+    return launch_after(grad_norm_kernel<true>, grid_of(l, ctas), kTsThreads, 0, stream, l, grads, partial, ticket, norm, sumsq);
 }
 
 cudaError_t launch_clip(const TsList& l, void* const* grads, const float* norm, float max_norm, int ctas,
                         cudaStream_t stream) {
     if (l.chunks == 0) return cudaSuccess;
-    clip_kernel<<<grid_of(l, ctas), kTsThreads, 0, stream>>>(l, grads, norm, max_norm);
-    return cudaGetLastError();
+    return launch_after(clip_kernel, grid_of(l, ctas), kTsThreads, 0, stream, l, grads, const_cast<float*>(norm),
+                        static_cast<const double*>(nullptr), 0u, max_norm);
+}
+
+cudaError_t launch_clip_norm(const TsList& l, void* const* grads, double* partial, float* norm, float max_norm, int ctas,
+                             cudaStream_t stream) {
+    const int grid = grid_of(l, ctas);
+    const cudaError_t e = launch_after(grad_norm_kernel<false>, grid, kTsThreads, 0, stream, l, static_cast<const void* const*>(grads), partial,
+                                       static_cast<unsigned*>(nullptr), static_cast<float*>(nullptr), static_cast<double*>(nullptr));
+    if (e != cudaSuccess) return e;
+    return launch_after(clip_kernel, grid, kTsThreads, 0, stream, l, grads, norm, static_cast<const double*>(partial), unsigned(grid), max_norm);
 }
 
 cudaError_t launch_adamw(const TsList& l, void* const* tables, int write_shards, const AdamwArgs& a, int ctas,
                          cudaStream_t stream) {
     if (l.chunks == 0) return cudaSuccess;
-    adamw_kernel<<<grid_of(l, ctas), kTsThreads, 0, stream>>>(l, tables, write_shards, a);
-    return cudaGetLastError();
+    return launch_after(adamw_kernel, grid_of(l, ctas), kTsThreads, 0, stream, l, tables, write_shards, a);
 }
 
 }  // namespace tide
