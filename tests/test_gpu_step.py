@@ -469,3 +469,59 @@ def test_lists_on_several_streams(tide):
     torch.cuda.synchronize()
     for w, (_, norm) in zip(want, sets):
         assert abs(norm.item() - w) <= 18 * U * w
+
+
+# ---- all of it together --------------------------------------------------------------------------
+
+
+def _example():
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "sharded_step.py")
+    spec = importlib.util.spec_from_file_location("sharded_step", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_sharded_step_is_the_unsharded_step(tide):
+    """One step of the example against the same step on whole fp32 tensors: autograd through an index, dense
+    gradients rounded to bf16 per rank as the reduce-scatter reads them, sums, norm and AdamW in 64 bits."""
+    ex = _example()
+    R, vocab, dim, tokens = 3, 101, 64, 40
+    model = ex.ShardedModel(R, vocab, dim, tokens)
+    G = model.group
+    start = [torch.cat([model.master[d][G.param_layout(p)[1]:][:G.valid_rows(d, p) * dim] for d in range(R)]).view(-1, dim).clone() for p in (0, 1)]
+    data = ex.batches(R, vocab, tokens, 0)
+    model.step(data, lr=1e-2, max_norm=0.05, weight_decay=0.1)
+    sums = [torch.zeros_like(p, dtype=torch.float64) for p in start]
+    for t, target in data:
+        E, W = (p.bfloat16().requires_grad_(True) for p in start)
+        x = (start[0].bfloat16().float()[t] * dim ** 0.5).bfloat16().requires_grad_(True)
+        loss = torch.nn.functional.cross_entropy((torch.relu(x @ W) @ E.t()).float(), target) / R
+        loss.backward()
+        sums[0] += E.grad.double()
+        sums[1] += W.grad.double()
+        sums[0].index_add_(0, t, x.grad.double() * float(torch.tensor(dim ** 0.5, dtype=torch.float32)))
+    norm = math.sqrt(sum(float(s.square().sum()) for s in sums))
+    assert abs(model.norm.item() - norm) <= 1e-5 * norm and norm > 0.05
+    c = 0.05 / (norm + 1e-6)
+    for p in (0, 1):
+        g = sums[p] * c
+        want = start[p].double() * (1 - 1e-2 * 0.1) - 1e-2 * g / (g.abs() + 1e-8)  # the first step: m / sqrt(v) is the gradient's sign
+        got = torch.cat([model.master[d][G.param_layout(p)[1]:][:G.valid_rows(d, p) * dim] for d in range(R)]).view(-1, dim)
+        # near g = 0 the quotient turns fast: what the sums' rounding (at most 200 terms) can move it by
+        slack = 1e-2 * (1e-8 + 2e-5 * g.abs().max()) / (g.abs() + 1e-8)
+        assert bool(((got.double() - want).abs() <= 1e-6 + torch.minimum(slack, torch.tensor(2e-2))).all())
+    for d in range(R):
+        for p in (0, 1):
+            o, n = G.param_layout(p)[1], G.valid_rows(d, p) * dim
+            assert torch.equal(model.shards[d, o:o + n], model.master[d, o:o + n].bfloat16())
+
+
+def test_example_learns(tide):
+    ex = _example()
+    model = ex.ShardedModel(4, 211, 128, 256)
+    losses = [float(model.step(ex.batches(4, 211, 256, k))) for k in range(40)]
+    assert losses[0] > 4.5 and losses[-1] < 0.5 * losses[0] and all(math.isfinite(x) for x in losses), losses
