@@ -98,7 +98,8 @@ struct AdamwArgs {
     float beta1, one_minus_beta1, beta2, one_minus_beta2, eps, step_size, inv_sqrt_c2;
     const float* norm;  // nullptr: no clipping
     float max_norm;
-    int skip_nonfinite;
+    float lr;
+    int skip_nonfinite, write_shards, has_decay;
 };
 
 struct TsList {
@@ -115,9 +116,8 @@ cudaError_t launch_clip(const TsList& l, void* const* grads, const float* norm, 
 // The norm and clipping by it in two launches, the second of which ends the norm's sum.
 cudaError_t launch_clip_norm(const TsList& l, void* const* grads, double* partial, float* norm, float max_norm, int ctas,
                              cudaStream_t stream);
-// tables: K pointers each of params, grads, exp_avg, exp_avg_sq and shards (shards unused when
-// write_shards is 0), then K floats 1 - lr * weight_decay.
-cudaError_t launch_adamw(const TsList& l, void* const* tables, int write_shards, const AdamwArgs& a, int ctas,
-                         cudaStream_t stream);
+// tables: K pointers each of params, grads, exp_avg, exp_avg_sq and, where they are written, shards,
+// then, where there is any, K floats of weight decay.
+cudaError_t launch_adamw(const TsList& l, void* const* tables, const AdamwArgs& a, int ctas, cudaStream_t stream);
 
 }  // namespace tide

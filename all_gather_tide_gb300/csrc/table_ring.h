@@ -55,17 +55,34 @@ struct TableRing {
         for (Slot& s : slots) s = Slot{};
     }
 
-    // Uploads `ptrs` into a ring slot (or finds a slot already holding the same table for the
-    // same stream) and returns its index.  The caller calls finish(k) after its launch.
-    cudaError_t upload(const std::vector<const void*>& ptrs, cudaStream_t stream, int* slot) {
+    // A table given in parts, one after the other, each of whole 8-byte entries.
+    struct Part {
+        const void* data;
+        size_t words;
+    };
+
+    // The index of a slot that already holds this table for this stream, or -1.
+    int find(const Part* parts, int count, cudaStream_t stream) {
         for (int k = 0; k < kSlots; ++k) {
             Slot& s = slots[k];
-            if (s.valid && s.stream == stream && s.content == ptrs) {
-                s.last_use = ++use_clock;
-                *slot = k;
-                return cudaSuccess;
+            if (!s.valid || s.stream != stream) continue;
+            size_t at = 0;
+            bool same = true;
+            for (int i = 0; i < count && same; ++i) {
+                same = at + parts[i].words <= s.content.size() &&
+                       std::memcmp(s.content.data() + at, parts[i].data, parts[i].words * sizeof(void*)) == 0;
+                at += parts[i].words;
             }
+            if (!same || at != s.content.size()) continue;
+            s.last_use = ++use_clock;
+            return k;
         }
+        return -1;
+    }
+
+    // Uploads a table that find() did not find and returns its slot's index.  The caller calls
+    // finish(k) after its launch.
+    cudaError_t put(const Part* parts, int count, cudaStream_t stream, int* slot) {
         // victim: an unused slot, else the least recently used one
         int k = -1;
         for (int i = 0; i < kSlots && k < 0; ++i)
@@ -81,16 +98,28 @@ struct TableRing {
             if (e != cudaSuccess) return e;
         }
         s.valid = false;
-        std::memcpy(s.host, ptrs.data(), ptrs.size() * sizeof(void*));
-        const cudaError_t e =
-            cudaMemcpyAsync(s.dev, s.host, ptrs.size() * sizeof(void*), cudaMemcpyHostToDevice, stream);
+        s.content.clear();
+        for (int i = 0; i < count; ++i) {
+            const auto* from = static_cast<const void* const*>(parts[i].data);
+            s.content.insert(s.content.end(), from, from + parts[i].words);
+        }
+        const size_t bytes = s.content.size() * sizeof(void*);
+        std::memcpy(s.host, s.content.data(), bytes);
+        const cudaError_t e = cudaMemcpyAsync(s.dev, s.host, bytes, cudaMemcpyHostToDevice, stream);
         if (e != cudaSuccess) return e;
-        s.content = ptrs;
         s.stream = stream;
         s.valid = true;
         s.last_use = ++use_clock;
         *slot = k;
         return cudaSuccess;
+    }
+
+    // Uploads `ptrs` into a ring slot, or finds a slot already holding the same table for the same
+    // stream, and returns its index.
+    cudaError_t upload(const std::vector<const void*>& ptrs, cudaStream_t stream, int* slot) {
+        const Part part{ptrs.data(), ptrs.size()};
+        *slot = find(&part, 1, stream);
+        return *slot >= 0 ? cudaSuccess : put(&part, 1, stream, slot);
     }
 
     cudaError_t finish(int k, cudaStream_t stream) {

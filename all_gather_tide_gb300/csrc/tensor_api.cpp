@@ -44,22 +44,22 @@ void release(tide_tensors* t) {
     delete t;
 }
 
-// Appends K pointers to `table`, checking those of the tensors that have elements.
-int add_pointers(const tide_tensors* t, const void* const* ptrs, size_t elem, std::vector<const void*>* table) {
-    for (int k = 0; k < t->K; ++k) {
-        if (t->elems[k] > 0 && (!ptrs[k] || !aligned(ptrs[k], elem ? elem : t->bf16[k] ? 2 : 4))) return TIDE_EINVAL;
-        table->push_back(ptrs[k]);
-    }
-    return TIDE_OK;
+// Checks the pointers of the tensors that have elements; elem: bytes of theirs, 0 for gradients.
+bool good_pointers(const tide_tensors* t, const void* const* ptrs, size_t elem) {
+    for (int k = 0; k < t->K; ++k)
+        if (t->elems[k] > 0 && (!ptrs[k] || !aligned(ptrs[k], elem ? elem : t->bf16[k] ? 2 : 4))) return false;
+    return true;
 }
 
+// A slot that holds the gradients' pointers.  A table that the ring holds already was checked when it
+// came.
 int upload_grads(tide_tensors* t, const void* const* grads, cudaStream_t st, int* slot) {
-    std::vector<const void*> table;
-    table.reserve(size_t(t->K));
-    int rc = add_pointers(t, grads, 0, &table);
+    const tide::TableRing::Part part{grads, size_t(t->K)};
+    const int rc = tide::check_device(t->device);
     if (rc != TIDE_OK) return rc;
-    if ((rc = tide::check_device(t->device)) != TIDE_OK) return rc;
-    TIDE_CUDA(t->ring.upload(table, st, slot));
+    if ((*slot = t->ring.find(&part, 1, st)) >= 0) return TIDE_OK;
+    if (!good_pointers(t, grads, 0)) return TIDE_EINVAL;
+    TIDE_CUDA(t->ring.put(&part, 1, st, slot));
     return TIDE_OK;
 }
 
@@ -68,6 +68,13 @@ int finish(tide_tensors* t, int slot, cudaStream_t st, cudaError_t launched) {
     const cudaError_t e = t->ring.finish(slot, st);
     if (launched != cudaSuccess) return tide::record_cuda_error(launched);
     return e == cudaSuccess ? TIDE_OK : tide::record_cuda_error(e);
+}
+
+// A float in the first half of a table entry.
+uint64_t word_of(float v) {
+    uint64_t w = 0;
+    std::memcpy(&w, &v, sizeof v);
+    return w;
 }
 
 bool bad_max_norm(float v) { return !(v >= 0.0f); }  // NaN too
@@ -191,24 +198,30 @@ int tide_adamw(tide_tensors_t t, void* const* params, const void* const* grads, 
         if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1)) return TIDE_EINVAL;
         if (norm && (!aligned(norm, 4) || bad_max_norm(max_norm))) return TIDE_EINVAL;
         std::lock_guard<std::mutex> lock(t->mu);
-        const size_t K = size_t(t->K);
-        std::vector<const void*> table;
-        table.reserve(6 * K);
-        int rc = add_pointers(t, params, 4, &table);
-        if (rc == TIDE_OK) rc = add_pointers(t, grads, 0, &table);
-        if (rc == TIDE_OK) rc = add_pointers(t, exp_avg, 4, &table);
-        if (rc == TIDE_OK) rc = add_pointers(t, exp_avg_sq, 4, &table);
-        if (rc == TIDE_OK && shards) rc = add_pointers(t, shards, 2, &table);
+        int rc = tide::check_device(t->device);
         if (rc != TIDE_OK) return rc;
-        table.resize(6 * K, nullptr);
-        float* keep = reinterpret_cast<float*>(table.data() + 5 * K);
-        for (size_t k = 0; k < K; ++k) {
-            const float d = weight_decay ? weight_decay[k] : 0.0f;
-            if (!(d >= 0) || !std::isfinite(d)) return TIDE_EINVAL;
-            keep[k] = float(1.0 - lr * double(d));
-        }
-        if ((rc = tide::check_device(t->device)) != TIDE_OK) return rc;
         cudaStream_t st = static_cast<cudaStream_t>(stream);
+        const size_t K = size_t(t->K);
+        // the weight decays as they are: two to an entry, an odd one alone
+        const uint64_t odd = weight_decay && K % 2 ? word_of(weight_decay[K - 1]) : 0;
+        tide::TableRing::Part parts[7];
+        int count = 0;
+        for (const void* p : {static_cast<const void*>(params), static_cast<const void*>(grads), static_cast<const void*>(exp_avg),
+                              static_cast<const void*>(exp_avg_sq), static_cast<const void*>(shards)})
+            if (p) parts[count++] = {p, K};
+        if (weight_decay) {
+            parts[count++] = {weight_decay, K / 2};
+            parts[count++] = {&odd, K % 2};
+        }
+        int slot = t->ring.find(parts, count, st);
+        if (slot < 0) {
+            if (!good_pointers(t, params, 4) || !good_pointers(t, grads, 0) || !good_pointers(t, exp_avg, 4) ||
+                !good_pointers(t, exp_avg_sq, 4) || (shards && !good_pointers(t, shards, 2)))
+                return TIDE_EINVAL;
+            for (size_t k = 0; weight_decay && k < K; ++k)
+                if (!(weight_decay[k] >= 0) || !std::isfinite(weight_decay[k])) return TIDE_EINVAL;
+            TIDE_CUDA(t->ring.put(parts, count, st, &slot));
+        }
         tide::AdamwArgs a{};
         a.beta1 = float(beta1);
         a.one_minus_beta1 = float(1.0 - beta1);
@@ -220,9 +233,10 @@ int tide_adamw(tide_tensors_t t, void* const* params, const void* const* grads, 
         a.norm = norm;
         a.max_norm = max_norm;
         a.skip_nonfinite = (flags & TIDE_ADAMW_SKIP_NONFINITE) ? 1 : 0;
-        int slot;
-        TIDE_CUDA(t->ring.upload(table, st, &slot));
-        return finish(t, slot, st, tide::launch_adamw(t->list(), t->ring.slots[slot].dev, shards ? 1 : 0, a, t->sm_count * tide::kAdamwCtasPerSm, st));
+        a.lr = float(lr);
+        a.write_shards = shards ? 1 : 0;
+        a.has_decay = weight_decay ? 1 : 0;
+        return finish(t, slot, st, tide::launch_adamw(t->list(), t->ring.slots[slot].dev, a, t->sm_count * tide::kAdamwCtasPerSm, st));
     });
 }
 

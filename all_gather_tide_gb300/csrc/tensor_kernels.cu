@@ -281,15 +281,15 @@ clip_kernel(TsList l, void* const* __restrict__ grads, float* norm, const double
 }
 
 template <typename T>
-__device__ __forceinline__ void adamw_item(const TsList& l, const AdamwArgs& a, void* const* tables, int write_shards, const Item& it,
-                                           float f) {
+__device__ __forceinline__ void adamw_item(const TsList& l, const AdamwArgs& a, void* const* tables, const Item& it, float f) {
     const int64_t K = l.K;
     float* p = static_cast<float*>(tables[it.k]);
     const T* g = static_cast<const T*>(tables[K + it.k]);
     float* m = static_cast<float*>(tables[2 * K + it.k]);
     float* v = static_cast<float*>(tables[3 * K + it.k]);
-    auto* w = static_cast<__nv_bfloat16*>(tables[4 * K + it.k]);
-    const float keep = __ldg(reinterpret_cast<const float*>(tables + 5 * K) + it.k);
+    auto* w = a.write_shards ? static_cast<__nv_bfloat16*>(tables[4 * K + it.k]) : nullptr;
+    const float* decay = reinterpret_cast<const float*>(tables + (a.write_shards ? 5 : 4) * K);
+    const float keep = a.has_decay ? fmaf(-a.lr, __ldg(decay + it.k), 1.0f) : 1.0f;
     const unsigned mis = misalign(p);
     const bool gv = misalign(g) == mis, mv = misalign(m) == mis, vv = misalign(v) == mis, wv = misalign(w) == mis;
     const int lo = it.least(), end = it.end(mis, l.chunk);
@@ -313,12 +313,12 @@ __device__ __forceinline__ void adamw_item(const TsList& l, const AdamwArgs& a, 
         store_group(m, e, lo, end, mv, mi);
         store_group(v, e, lo, end, vv, vi);
         store_group(p, e, lo, end, true, pi);
-        if (write_shards) store_group(w, e, lo, end, wv, pi);
+        if (a.write_shards) store_group(w, e, lo, end, wv, pi);
     }
 }
 
 __global__ void __launch_bounds__(kTsThreads, kAdamwCtasPerSm)
-adamw_kernel(TsList l, void* const* __restrict__ tables, int write_shards, AdamwArgs a) {
+adamw_kernel(TsList l, void* const* __restrict__ tables, AdamwArgs a) {
     wait_for_previous_kernel();
     float f = 1.0f;
     if (a.norm) {
@@ -328,8 +328,8 @@ adamw_kernel(TsList l, void* const* __restrict__ tables, int write_shards, Adamw
     }
     for (int64_t c = first_item(); c < l.chunks; c += item_stride()) {
         const Item it = item_of(l, c);
-        if (it.bf16) adamw_item<__nv_bfloat16>(l, a, tables, write_shards, it, f);
-        else adamw_item<float>(l, a, tables, write_shards, it, f);
+        if (it.bf16) adamw_item<__nv_bfloat16>(l, a, tables, it, f);
+        else adamw_item<float>(l, a, tables, it, f);
     }
 }
 
@@ -358,10 +358,9 @@ cudaError_t launch_clip_norm(const TsList& l, void* const* grads, double* partia
     return launch_after(clip_kernel, grid, kTsThreads, 0, stream, l, grads, norm, static_cast<const double*>(partial), unsigned(grid), max_norm);
 }
 
-cudaError_t launch_adamw(const TsList& l, void* const* tables, int write_shards, const AdamwArgs& a, int ctas,
-                         cudaStream_t stream) {
+cudaError_t launch_adamw(const TsList& l, void* const* tables, const AdamwArgs& a, int ctas, cudaStream_t stream) {
     if (l.chunks == 0) return cudaSuccess;
-    return launch_after(adamw_kernel, grid_of(l, ctas), kTsThreads, 0, stream, l, tables, write_shards, a);
+    return launch_after(adamw_kernel, grid_of(l, ctas), kTsThreads, 0, stream, l, tables, a);
 }
 
 }  // namespace tide
