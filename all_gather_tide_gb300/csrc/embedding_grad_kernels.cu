@@ -251,21 +251,28 @@ __device__ __forceinline__ float* table_row(const Target& a, uint32_t t) {
 // The table row of sorted position i (tv.rows: no token).
 __device__ __forceinline__ uint32_t row_at(const SumArgs& a, uint32_t i) { return a.w.sorted[i].z; }
 
-// How a warp's 256 columns lie over its lanes: every 32nd element (kSingle), or 8 consecutive ones, whose
-// rows in the shard are 32-byte aligned (kWide) or not (kMixed).
+// How a warp's 256 columns lie over its lanes: every 32nd element (kSingle), or so that 16 bytes of dout
+// are one lane's and the next 16 the next lane's, the rows in the shard being 32-byte aligned (kWide)
+// or not (kMixed).
 enum Layout { kSingle, kMixed, kWide };
 
-// A lane's 8 consecutive columns of a dout row, 16 or 32 bytes, copied to shared memory asynchronously:
-// what is in flight takes no registers.  Each lane copies and reads its own bytes only.
+// A lane's 8 columns of a dout row, 16 bytes of bf16 or twice 16 bytes of fp32 (512 bytes apart, so that a
+// warp's copies cover whole lines), copied to shared memory asynchronously: what is in flight takes no
+// registers.  Each lane copies and reads its own bytes only.
 template <typename In>
 struct Part {
-    static constexpr int kWords = sizeof(In) / 2;  // of 16 bytes
+    static constexpr int kWords = sizeof(In) / 2;           // of 16 bytes
+    static constexpr int kEach = 8 / kWords;                // columns of one
+    static constexpr uint32_t kApart = 256 / kWords;        // columns from one to the next
     uint4 w[kWords];
 
-    static __device__ __forceinline__ void copy(uint32_t to, uint64_t from) {
+    // The lane's j-th column of 256.
+    static __device__ __forceinline__ uint32_t column(uint32_t lane, int j) { return j / kEach * kApart + lane * kEach + j % kEach; }
+    // from: the lane's first column, of which, counted from it, `left` (may be negative) are the row's.
+    static __device__ __forceinline__ void copy(uint32_t to, uint64_t from, int left) {
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 16) : "memory");
+            if (int(i * kApart) < left) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 512) : "memory");
     }
     __device__ __forceinline__ void read(uint32_t at) {
 #pragma unroll
@@ -310,10 +317,9 @@ struct Ring {
 // called before the k-th is added.  `ring`: the lane's place in the warp's shared memory.
 template <typename In, Layout kLayout, typename Src, typename Turn>
 __device__ __forceinline__ void add_rows(int count, uint32_t stretch, uint32_t len, uint32_t ring, Src src, Turn turn, float (&acc)[8]) {
-    const uint32_t lane = threadIdx.x & 31;
     if constexpr (kLayout == kSingle) {
         constexpr int kAhead = 4;
-        const uint32_t col = stretch * kStretch + lane;
+        const uint32_t col = stretch * kStretch + (threadIdx.x & 31);
         for (int k = 0; k < count; k += kAhead) {
             Singles<In> x[kAhead];
 #pragma unroll
@@ -330,14 +336,14 @@ __device__ __forceinline__ void add_rows(int count, uint32_t stretch, uint32_t l
         }
     } else {
         using R = Ring<In>;
-        const uint32_t col = stretch * kStretch + lane * 8;
-        const bool in = col < len;
+        const uint32_t col = stretch * kStretch + Part<In>::column(threadIdx.x & 31, 0);
+        const int left = int(len) - int(col);
         auto slot = [&](int k) { return ring + uint32_t(k) % R::kRows * R::kRow; };
         auto fetch = [&](int k) {
 #pragma unroll
             for (int u = 0; u < R::kGroup; ++u) {
                 const uint64_t from = src(k + u);
-                if (in && k + u < count) Part<In>::copy(slot(k + u), from + uint64_t(col) * sizeof(In));
+                if (k + u < count) Part<In>::copy(slot(k + u), from + uint64_t(col) * sizeof(In), left);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -362,42 +368,54 @@ __device__ __forceinline__ void add_rows(int count, uint32_t stretch, uint32_t l
 
 // The warp's sums to a stretch of a row, dst: `acc` as the layout spreads them over the lanes; `left`
 // columns of the row lie from dst on.
-template <Layout kLayout, bool Add>
+template <typename In, Layout kLayout, bool Add>
 __device__ __forceinline__ void write_row(float scale, float* dst, uint32_t left, const float (&acc)[8], float* stage) {
-    const int lane = threadIdx.x & 31;
-    float x[8];
-    if (kLayout == kWide) {
-        if (lane * 8u >= left) return;
+    using P = Part<In>;
+    const uint32_t lane = threadIdx.x & 31;
+    float x[8], y[8] = {};
+    // What is added to is read here and not ahead of need: copies of the rows made as early as dout's (or
+    // prefetches, or additions in L2) took 400 to 420 us where this took 371.
+    if constexpr (kLayout == kWide && P::kWords == 1) {
+        if (lane * 8 >= left) return;
         dst += lane * 8;
-        float y[8] = {};
-        // read here and not ahead of need: copies of the rows made as early as dout's (or prefetches,
-        // or additions in L2) took 400 to 420 us where this took 371
         if (Add) load_v8(dst, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = y[j] + scale * acc[j];
         store_v8(dst, x);
-        return;
-    }
-    if (kLayout == kMixed) {  // lane * 8 + j -> lane + 32 * j, so that stores of single elements lie side by side
-        __syncwarp();
+    } else if constexpr (kLayout == kWide) {
+        float4* to[2];
+        bool in[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) stage[lane * 9 + j] = acc[j];
-        __syncwarp();
+        for (int i = 0; i < 2; ++i) {
+            to[i] = reinterpret_cast<float4*>(dst + P::column(lane, 4 * i));
+            in[i] = P::column(lane, 4 * i) < left;
+            if (Add && in[i]) {
+                const float4 v = *to[i];
+                y[4 * i] = v.x, y[4 * i + 1] = v.y, y[4 * i + 2] = v.z, y[4 * i + 3] = v.w;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = y[j] + scale * acc[j];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (in[i]) __stcs(to[i], make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+    } else {
+        if constexpr (kLayout == kMixed) {  // turned round so that stores of single elements lie side by side
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) stage[P::column(lane, j) + P::column(lane, j) / 8] = acc[j];
+            __syncwarp();
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int q = lane + 32 * j;
-            x[j] = stage[q / 8 * 9 + q % 8];
+            const uint32_t q = lane + 32 * j;
+            x[j] = kLayout == kMixed ? stage[q + q / 8] : acc[j];
+            if (Add && q < left) y[j] = dst[q];
         }
-    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = acc[j];
+        for (int j = 0; j < 8; ++j)
+            if (lane + 32 * j < left) dst[lane + 32 * j] = y[j] + scale * x[j];
     }
-    float y[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = Add && lane + 32u * j < left ? dst[lane + 32 * j] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (lane + 32u * j < left) dst[lane + 32 * j] = y[j] + scale * x[j];
 }
 
 // Partial sums meet in two steps: those of up to kBlock consecutive pieces, then those of the
@@ -411,9 +429,17 @@ __device__ __forceinline__ float* partial_of(const SumArgs& a, uint32_t x, int w
     return a.w.partial + slot_of(a, x, which, stretch) * kStretch + (threadIdx.x & 31) * 8;
 }
 
-__device__ __forceinline__ void put_partial(float* p, const float (&acc)[8]) {
-    __stcg(reinterpret_cast<float4*>(p), make_float4(acc[0], acc[1], acc[2], acc[3]));
-    __stcg(reinterpret_cast<float4*>(p + 4), make_float4(acc[4], acc[5], acc[6], acc[7]));
+// Through L2 both ways: another SM reads what one wrote.
+__device__ __forceinline__ void put_partial(float* p, const float (&x)[8]) {
+    asm volatile("st.global.cg.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+__device__ __forceinline__ void get_partial(const float* p, float (&x)[8]) {
+    asm volatile("ld.global.cg.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(p)
+                 : "memory");
 }
 
 // Arrives at a counter with everything written so far; true, with what the others wrote visible, for
@@ -432,15 +458,16 @@ __device__ __forceinline__ bool last_to_arrive(uint32_t* counter, uint32_t count
 __device__ __forceinline__ void add_partials(const SumArgs& a, uint32_t x, uint32_t count, int first_starts, uint32_t stretch, float (&sum)[8]) {
 #pragma unroll 8
     for (uint32_t k = 0; k < count; ++k) {
-        const float* p = partial_of(a, x + k, k == 0 ? first_starts : 0, stretch);
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(p)), v = __ldcg(reinterpret_cast<const float4*>(p + 4));
-        sum[0] += u.x, sum[1] += u.y, sum[2] += u.z, sum[3] += u.w, sum[4] += v.x, sum[5] += v.y, sum[6] += v.z, sum[7] += v.w;
+        float y[8];
+        get_partial(partial_of(a, x + k, k == 0 ? first_starts : 0, stretch), y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += y[j];
     }
 }
 
 // After a piece has left a partial sum of row t: the last of the row's pieces in this block adds
 // the block's, and the last of its blocks adds the blocks', both in order, and writes the row.
-template <Layout kLayout, bool Add>
+template <typename In, Layout kLayout, bool Add>
 __device__ __forceinline__ void join_partials(const SumArgs& a, uint32_t t, uint32_t piece, uint32_t stretch, float* stage) {
     const uint32_t lane = threadIdx.x & 31, block = piece / kBlock, p0 = block * kBlock, y = p0 + lane;
     // the row has a position in piece y: its first or last position, or (t lying in between) both ends
@@ -486,11 +513,11 @@ __device__ __forceinline__ void join_partials(const SumArgs& a, uint32_t t, uint
         add_partials(a, a.pieces + first, last - first + 1, 1, stretch, sum);
     }
     const uint32_t col0 = stretch * kStretch;
-    write_row<kLayout, Add>(a.scale, table_row(a, t) + col0, a.tv.len - col0, sum, stage);
+    write_row<In, kLayout, Add>(a.scale, table_row(a, t) + col0, a.tv.len - col0, sum, stage);
 }
 
 // The running sum of one piece.
-template <Layout kLayout, bool Add>
+template <typename In, Layout kLayout, bool Add>
 struct Run {
     const SumArgs& a;
     uint32_t piece, stretch, before;
@@ -501,7 +528,7 @@ struct Run {
     bool starts = true;    // in this piece
     uint32_t head = ~0u;   // the row that an earlier piece began and this one ended
 
-    __device__ __forceinline__ void write() { write_row<kLayout, Add>(a.scale, dst, a.tv.len - stretch * kStretch, acc, stage); }
+    __device__ __forceinline__ void write() { write_row<In, kLayout, Add>(a.scale, dst, a.tv.len - stretch * kStretch, acc, stage); }
 
     // The next position's row of the table, and where it lies; what the position adds follows.
     __device__ __forceinline__ void turn_to(uint32_t t, float* to) {
@@ -534,7 +561,7 @@ struct Run {
 #pragma unroll 1
         for (int side = 0; side < 2; ++side) {  // rows that run over several pieces
             const uint32_t t = side ? tail : head;
-            if (t != ~0u) join_partials<kLayout, Add>(a, t, piece, stretch, stage);
+            if (t != ~0u) join_partials<In, kLayout, Add>(a, t, piece, stretch, stage);
         }
     }
 };
@@ -552,7 +579,7 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, uint32_t piece, uint
     // where their rows lie in the shards, worked out by each lane for its own
     const auto d0 = reinterpret_cast<unsigned long long>(p0.z < a.tv.rows ? table_row(a, p0.z) + stretch * kStretch : nullptr);
     const auto d1 = reinterpret_cast<unsigned long long>(p1.z < a.tv.rows ? table_row(a, p1.z) + stretch * kStretch : nullptr);
-    Run<kLayout, Add> run{a, piece, stretch, lo > 0 ? row_at(a, lo - 1) : ~0u, stage};
+    Run<In, kLayout, Add> run{a, piece, stretch, lo > 0 ? row_at(a, lo - 1) : ~0u, stage};
     const uint32_t after = hi < a.n ? row_at(a, hi) : ~0u;  // rows on either side of the piece
     add_rows<In, kLayout>(
         held, stretch, a.tv.len, ring, [&](int k) { return uint64_t(of(k, p0.y, p1.y)) << 32 | of(k, p0.x, p1.x); },
@@ -722,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 3) sum_short_kernel(const __grid_con
                 return uint64_t(x.y) << 32 | x.x;
             },
             [](int) {}, acc);
-        write_row<kLayout, Add>(a.scale, table_row(a, t) + stretch * kStretch, a.tv.len - stretch * kStretch, acc, stage);
+        write_row<In, kLayout, Add>(a.scale, table_row(a, t) + stretch * kStretch, a.tv.len - stretch * kStretch, acc, stage);
     }
 }
 
@@ -797,9 +824,12 @@ bool cut_blocks(Target* a, int64_t items, bool accumulate) {
 GradPlan plan_grad(const TableView& tv, int64_t n) {
     GradPlan g;
     g.stretches = (tv.len + kStretch - 1) / kStretch;
-    // shorter pieces while they would not fill the GPU's warps once
+    // shorter pieces while they would not go round the GPU's warps often enough to end together, and
+    // still shorter ones while they would not fill them once
+    auto items = [&] { return (n + g.piece - 1) / g.piece * g.stretches; };
     g.piece = kPieceMost;
-    while (g.piece > kPieceLeast && (n + g.piece - 1) / g.piece * g.stretches < kPieceWarps) g.piece >>= 1;
+    while (g.piece > 2 * kPieceLeast && items() < 6 * kPieceWarps) g.piece >>= 1;
+    while (g.piece > kPieceLeast && items() < kPieceWarps) g.piece >>= 1;
     g.pieces = uint32_t((n + g.piece - 1) / g.piece);
     g.slots = (int64_t(g.pieces) + (g.pieces + kBlock - 1) / kBlock) * 2 * g.stretches;
     return g;
