@@ -408,8 +408,12 @@ def tide_probe_mixed(buf, bulk_bytes: int, st_buf, st_bytes: int, ctas: int, cop
 def tide_embedding(g: int, p: int, shards: Sequence, ids, out, scale: float = 1.0, stream=None) -> None:
     """``shards``: R bf16 shards; ``ids``: contiguous int32 or int64 tensor of n ids; ``out``: bf16 or fp32
     tensor whose last dimension is the row and whose rows lie ``out.stride(-2)`` apart (n of them)."""
+    _embedding(g, p, shards, ids, out, _row_stride(out), scale, stream)
+
+
+def _embedding(g, p, shards, ids, out, stride, scale, stream) -> None:
     _check(lib().tide_embedding(g, p, _ptr_array(shards), ids.data_ptr(), _dtype_code(ids), ids.numel(), scale,
-                                out.data_ptr(), _dtype_code(out), _row_stride(out), _stream(stream)), "tide_embedding")
+                                out.data_ptr(), _dtype_code(out), stride, _stream(stream)), "tide_embedding")
 
 
 def _row_stride(x) -> int:
@@ -427,10 +431,16 @@ def tide_embedding_grad(g: int, p: int, ids: Sequence, douts: Sequence, shards: 
                         accumulate: bool = False, stream=None) -> None:
     """``ids`` and ``douts``: B tensors each (batch b: n_b ids, n_b rows); ``shards``: R fp32 shards;
     ``workspace``: uint8 tensor of ``tide_embedding_grad_workspace`` bytes."""
-    B = len(ids)
-    _check(lib().tide_embedding_grad(g, p, B, _i64_array([x.numel() for x in ids]), _ptr_array(ids), _dtype_code(ids[0]),
-                                     _ptr_array(douts), _i64_array([_row_stride(x) for x in douts]), _dtype_code(douts[0]),
-                                     scale, int(accumulate), _ptr_array(shards), workspace.data_ptr(), workspace.numel(),
+    _embedding_grad(g, p, [x.numel() for x in ids], ids, douts, [_row_stride(x) for x in douts], shards, workspace, scale,
+                    accumulate, stream)
+
+
+def _embedding_grad(g, p, counts, ids, douts, strides, shards, workspace, scale, accumulate, stream) -> None:
+    B = len(counts)
+    i64, vp = ctypes.c_int64 * B, ctypes.c_void_p * B
+    _check(lib().tide_embedding_grad(g, p, B, i64(*counts), vp(*[x.data_ptr() for x in ids]), _dtype_code(ids[0]),
+                                     vp(*[x.data_ptr() for x in douts]), i64(*strides), _dtype_code(douts[0]), scale,
+                                     accumulate, _ptr_array(shards), workspace.data_ptr(), workspace.numel(),
                                      _stream(stream)), "tide_embedding_grad")
 
 
@@ -574,8 +584,8 @@ class Group:
         (``ids.numel()`` rows: ``[n, L]``, or contiguous ``[..., L]``)."""
         if len(shards) != self.R:
             _refuse("embedding", f"{self.R} shards are needed")
-        self._check_rows("embedding", p, ids, out)
-        tide_embedding(self.handle, p, shards, ids, out, scale, stream)
+        stride = self._check_rows("embedding", p, ids, out)
+        _embedding(self.handle, p, shards, ids, out, stride, scale, stream)
 
     def embedding_grad_workspace(self, p: int, n: int):
         """A device buffer that ``embedding_grad`` can work in for up to ``n`` positions."""
@@ -592,30 +602,37 @@ class Group:
             _refuse(where, f"{self.R} shards are needed")
         if not len(ids) == len(douts) > 0:
             _refuse(where, "one dout for each batch of ids, and one batch at least")
+        kinds = ids[0].dtype, douts[0].dtype
+        counts, strides = [], []
         for i, x in zip(ids, douts):
-            self._check_rows(where, p, i, x)
-            if i.dtype != ids[0].dtype or x.dtype != douts[0].dtype:
+            strides.append(self._check_rows(where, p, i, x))
+            counts.append(i.numel())
+            if (i.dtype, x.dtype) != kinds:
                 _refuse(where, "the batches differ in type")
         if workspace is None:
             import torch
 
-            workspace = self.embedding_grad_workspace(p, sum(x.numel() for x in ids))
+            workspace = self.embedding_grad_workspace(p, sum(counts))
             if stream is not None:
                 s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
                 s.wait_stream(torch.cuda.current_stream())
                 workspace.record_stream(s)
-        tide_embedding_grad(self.handle, p, ids, douts, shards, workspace, scale, accumulate, stream)
+        _embedding_grad(self.handle, p, counts, ids, douts, strides, shards, workspace, scale, accumulate, stream)
 
-    def _check_rows(self, where: str, p: int, ids, rows) -> None:
+    def _check_rows(self, where: str, p: int, ids, rows) -> int:
+        """Refuses ids and rows that do not fit parameter p; returns the rows' stride."""
         if not 0 <= p < self.P:
             _refuse(where, "no such parameter")
-        n, length = ids.numel(), self.row_len[p]
+        n, length, shape = ids.numel(), self.row_len[p], rows.shape
         if not ids.is_contiguous():
             _refuse(where, "ids are not contiguous")
-        if rows.dim() < 1 or rows.shape[-1] != length or rows.numel() != n * length:
-            _refuse(where, f"{n} rows of {length} elements are needed")
-        if not rows.is_contiguous() and not (rows.dim() == 2 and (length == 1 or rows.stride(1) == 1) and rows.stride(0) >= length):
-            _refuse(where, "rows are neither contiguous nor a row stride apart")
+        if len(shape) == 2 and shape[0] == n and shape[1] == length:
+            stride, inner = rows.stride()
+            if (length == 1 or inner == 1) and (n <= 1 or stride >= length):
+                return stride if n > 1 else length
+        elif len(shape) and shape[-1] == length and rows.numel() == n * length and rows.is_contiguous():
+            return length
+        _refuse(where, f"{n} rows of {length} elements, contiguous or a row stride apart, are needed")
 
     def pieces(self, buffers: Sequence) -> list:
         """The valid rows of every (rank, parameter) piece of R shard buffers, as R*P views in the order

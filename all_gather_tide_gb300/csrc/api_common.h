@@ -24,6 +24,13 @@ inline int check_device(int want) {
     return dev == want ? TIDE_OK : TIDE_EINVAL;
 }
 
+// Pointer tables of a ring are shared with later calls, so work that reads one is not put into a graph.
+inline int check_not_captured(cudaStream_t stream) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    TIDE_CUDA(cudaStreamIsCapturing(stream, &status));
+    return status == cudaStreamCaptureStatusNone ? TIDE_OK : TIDE_EINVAL;
+}
+
 // Entry points return a status, never an exception: an allocation that fails (host vectors of the
 // pointer tables and plans) becomes TIDE_ENOMEM, anything else thrown (a mutex error) TIDE_EINVAL.
 template <class F>

@@ -42,6 +42,8 @@ int shard_ptrs(tide_group* g, const void* const* shards, size_t elem, cudaStream
         for (int d = R; d < tide::kInlineRanks; ++d) sp->p[d] = nullptr;
         return TIDE_OK;
     }
+    const int rc = tide::check_not_captured(st);
+    if (rc != TIDE_OK) return rc;
     std::vector<const void*> table(shards, shards + R);
     TIDE_CUDA(g->ring.upload(table, st, slot));
     sp->table = g->ring.slots[*slot].dev;

@@ -35,7 +35,7 @@ namespace {
 using tide::aligned;
 using tide::no_throw;
 
-constexpr int64_t kMaxElems = int64_t(1) << 42;
+constexpr int64_t kMaxElems = int64_t(1) << 38;
 constexpr int64_t kItemsWanted = 152 * 32;  // the warps of a GB300 at four CTAs an SM
 
 void release(tide_tensors* t) {
@@ -55,7 +55,8 @@ bool good_pointers(const tide_tensors* t, const void* const* ptrs, size_t elem) 
 // came.
 int upload_grads(tide_tensors* t, const void* const* grads, cudaStream_t st, int* slot) {
     const tide::TableRing::Part part{grads, size_t(t->K)};
-    const int rc = tide::check_device(t->device);
+    int rc = tide::check_device(t->device);
+    if (rc == TIDE_OK) rc = tide::check_not_captured(st);
     if (rc != TIDE_OK) return rc;
     if ((*slot = t->ring.find(&part, 1, st)) >= 0) return TIDE_OK;
     if (!good_pointers(t, grads, 0)) return TIDE_EINVAL;
@@ -198,9 +199,10 @@ int tide_adamw(tide_tensors_t t, void* const* params, const void* const* grads, 
         if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1)) return TIDE_EINVAL;
         if (norm && (!aligned(norm, 4) || bad_max_norm(max_norm))) return TIDE_EINVAL;
         std::lock_guard<std::mutex> lock(t->mu);
-        int rc = tide::check_device(t->device);
-        if (rc != TIDE_OK) return rc;
         cudaStream_t st = static_cast<cudaStream_t>(stream);
+        int rc = tide::check_device(t->device);
+        if (rc == TIDE_OK) rc = tide::check_not_captured(st);
+        if (rc != TIDE_OK) return rc;
         const size_t K = size_t(t->K);
         // the weight decays as they are: two to an entry, an odd one alone
         const uint64_t odd = weight_decay && K % 2 ? word_of(weight_decay[K - 1]) : 0;

@@ -381,7 +381,8 @@ int tide_reduce_scatter_noalloc(int32_t R, int32_t P, const int64_t *rows, const
  * an id >= rows_p also sets 64 in the group's device status word).  One token (n = 1) up to long
  * prompts take the same call; n = 0 does nothing.
  *   shards: host array of R device pointers, entry d = rank d's packed bf16 shard (S elements).  Up
- *           to 64 ranks they travel with the launch, so the call can be captured into a CUDA graph.
+ *           to 64 ranks they travel with the launch, so the call can be captured into a CUDA graph;
+ *           beyond, a stream that is being captured is refused.
  *   ids:    device array of n ids of ids_type (TIDE_I32 or TIDE_I64).
  *   out:    device, n rows of L_p elements of out_type (TIDE_BF16 or TIDE_F32), row i at element
  *           i*out_stride (out_stride >= L_p).
@@ -416,6 +417,7 @@ int tide_embedding_grad_workspace(tide_group_t g, int32_t p, int64_t n, int64_t 
  *   shards: host array of R device pointers, entry d = rank d's fp32 shard of S elements.
  *   workspace: device, 256-byte aligned, at least tide_embedding_grad_workspace's bytes for
  *           n[0] + ... + n[B-1]; holds nothing between calls, not shared by calls that overlap.
+ * Up to 64 ranks the call can be captured into a CUDA graph.
  * Asynchronous on `stream`.  Errors: TIDE_EINVAL (null or misaligned pointers, p, B, n, a type or a
  * stride out of range, the workspace too small, another device current), TIDE_ERANGE (rows_p > 2^31 - 2, L_p > 2^30,
  * more than 2^31 - 2^16 positions, or B > TIDE_MAX_TABLE / 8), TIDE_ECUDA.
@@ -431,10 +433,12 @@ int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t *n, 
  * shard, or the valid rows of one parameter's piece of it) or TIDE_BF16 (a parameter's gradient
  * before it); types = NULL means TIDE_F32 for all.  The list owns its work tables, a ring of pointer
  * tables and the norm's partial sums; like a group it belongs to the device current at creation,
- * its calls are serialised, and calls on different streams may overlap.  Tensor pointers need the
- * alignment of their element; those whose addresses agree modulo 8 elements move in vectors.
+ * its calls are serialised, and calls on different streams may overlap.  Its calls are refused
+ * (TIDE_EINVAL) on a stream that is being captured: the pointer tables are shared with later calls.
+ * Tensor pointers need the alignment of their element; those whose addresses agree modulo 8 elements
+ * move in vectors.
  * Errors: TIDE_EINVAL (null, K < 1, elems < 0, unknown type), TIDE_ERANGE (K > TIDE_MAX_TABLE / 8 or more
- * than 2^42 elements), TIDE_ENOMEM, TIDE_ECUDA.
+ * than 2^38 elements), TIDE_ENOMEM, TIDE_ECUDA.
  */
 typedef struct tide_tensors *tide_tensors_t;
 int tide_tensors_create(tide_tensors_t *out, int32_t K, const int64_t *elems, const int32_t *types);
@@ -476,8 +480,8 @@ int tide_clip_grad_norm(tide_tensors_t t, void *const *grads, float max_norm, fl
  *     param = param * (1 - lr * weight_decay_k)
  *             - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
  *     shard = bf16(param)    (round to nearest even)
- * Factors of the hyperparameters are formed in double on the host and rounded once to fp32.
- * Gradients are read only.
+ * Factors of the betas, the step and lr are formed in double on the host and rounded once to fp32, the
+ * decay's factor in fp32 with one rounding.  Gradients are read only.
  *   params, exp_avg (m), exp_avg_sq (v): host arrays of K device pointers, fp32, updated in place.
  *   grads:  host array of K device pointers of the list's types.
  *   shards: host array of K device pointers, bf16, written; or NULL.

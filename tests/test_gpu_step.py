@@ -50,11 +50,11 @@ class Table:
     """A group with one parameter `before` a table of rows x length, on R ranks, and plain forms of the
     lookup and its gradient on its CPU copy."""
 
-    def __init__(self, tide, R, rows, length, before=0):
+    def __init__(self, tide, R, rows, length, before=0, flags=0):
         self.R, self.rows, self.len = R, rows, length
         params = ([(before, 1)] if before else []) + [(rows, length)]
         self.p = len(params) - 1
-        self.G = tide.Group(R, params)
+        self.G = tide.Group(R, params, flags)
         self.m, self.o = self.G.param_layout(self.p)
         self.S = self.G.S
 
@@ -138,6 +138,21 @@ def test_lookup_of_batches_of_ids_and_in_a_graph(tide):
         assert torch.equal(out.cpu(), t.rows_of(shards)[ids.cpu()])
 
 
+def test_lookup_of_few_ctas_and_on_a_side_stream(tide):
+    """TIDE_FLAG_OVERLAP bounds the CTAs, which then walk the work; ids, shards and out made on the stream used."""
+    t, g = Table(tide, 4, 5000, 264, 8, tide.TIDE_FLAG_OVERLAP), gen(4)
+    shards = [torch.randn(t.S, generator=g).bfloat16() for _ in range(4)]
+    ids = draw_ids(g, 30_000, 5000, 0.1)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        dev, di = [s.cuda() for s in shards], ids.cuda()
+        out = torch.empty(30_000, 264, dtype=torch.bfloat16, device="cuda")
+    t.G.embedding(t.p, dev, di, out, stream=side)
+    side.synchronize()
+    whole = torch.cat([t.rows_of(shards), torch.zeros(1, 264).bfloat16()])
+    assert torch.equal(out.cpu(), whole[ids])
+
+
 def check_grad(t, ids, douts, old, shards, scale, add):
     """R CPU shards against sums in 64 bits; `old`: the shards before the call."""
     i = torch.cat([x.long() for x in ids])
@@ -219,6 +234,76 @@ def test_gradient_over_many_rows_and_positions(tide, rows, n):
     t, g = Table(tide, 3, rows, 8), gen(rows)
     ids = [draw_ids(g, n, rows, 0.01, "i32")]
     run_grad(tide, t, ids, [torch.randn(n, 8, generator=g)], 1.0, False)
+
+
+def test_gradient_does_not_read_rows_of_positions_without_a_token(tide):
+    for length in (256, 13):
+        t, g = Table(tide, 2, 50, length), gen(7)
+        for n in (100, 1000):  # a short list and a sorted one
+            ids = draw_ids(g, n, 50, 0.3)
+            x = torch.randn(n, length, generator=g)
+            x[ids < 0] = float("nan")
+            shards = [torch.zeros(t.S, device="cuda") for _ in range(2)]
+            t.G.embedding_grad(t.p, [ids.cuda()], [x.cuda()], shards)
+            assert all(bool(s.isfinite().all()) for s in shards)
+            check_grad(t, [ids], [torch.nan_to_num(x)], [torch.zeros(t.S)] * 2, [s.cpu() for s in shards], 1.0, False)
+
+
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("n", [200, 20_000])
+def test_gradient_of_few_ctas_on_a_side_stream_without_a_workspace(tide, n, add):
+    t, g = Table(tide, 4, 3000, 520, 8, tide.TIDE_FLAG_OVERLAP), gen(n)
+    ids, x = draw_ids(g, n, 3000, 0.1), torch.randn(n, 520, generator=g).bfloat16()
+    old = [torch.randn(t.S, generator=g) for _ in range(4)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        dev, di, dx = [o.cuda() for o in old], ids.cuda(), x.cuda()
+    t.G.embedding_grad(t.p, [di], [dx], dev, 1.5, add, stream=side)
+    side.synchronize()
+    check_grad(t, [ids], [x.float()], old, [d.cpu() for d in dev], 1.5, add)
+
+
+@pytest.mark.parametrize("n", [50, 3000])
+def test_gradient_in_a_graph(tide, n):
+    t, g = Table(tide, 3, 400, 64), gen(n)
+    ids, x = draw_ids(g, n, 400).cuda(), torch.randn(n, 64, generator=g).cuda()
+    shards = [torch.empty(t.S, device="cuda") for _ in range(3)]
+    work = t.G.embedding_grad_workspace(t.p, n)
+    t.G.embedding_grad(t.p, [ids], [x], shards, workspace=work)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        t.G.embedding_grad(t.p, [ids], [x], shards, workspace=work)
+    for seed in range(3):
+        ids.copy_(draw_ids(gen(seed), n, 400))
+        graph.replay()
+        check_grad(t, [ids.cpu()], [x.cpu()], [torch.zeros(t.S)] * 3, [s.cpu() for s in shards], 1.0, False)
+
+
+def test_table_of_more_than_2_to_the_31_elements(tide):
+    rows, length = 70_000, 32_768  # 2.3 billion elements on one rank
+    G = tide.Group(1, [(rows, length)])
+    shard = torch.zeros(G.S, dtype=torch.bfloat16, device="cuda")
+    table = shard.view(rows, length)
+    ids = torch.tensor([69_999, 65_536, 0, 65_535, 69_999, -1], device="cuda")
+    for k, t in enumerate((69_999, 65_536, 0, 65_535)):
+        table[t] = k + 1
+    out = torch.empty(6, length, device="cuda")
+    G.embedding(0, [shard], ids, out, 2.0)
+    assert out[:, 0].tolist() == [2, 4, 6, 8, 2, 0] and bool((out == out[:, :1]).all())
+    grad = torch.full((G.S,), 7.0, device="cuda")
+    for many in (1, 100):  # a short list and a sorted one
+        G.embedding_grad(0, [ids.repeat(many)], [out.repeat(many, 1)], [grad])
+        rows_sum = grad.view(rows, length)
+        assert rows_sum[[69_999, 65_536, 0, 65_535], 5].tolist() == [4 * many, 4 * many, 6 * many, 8 * many]
+        assert float(rows_sum.sum(dtype=torch.float64)) == 22.0 * many * length
+    del table, rows_sum
+    norm = torch.zeros(1, device="cuda")
+    T = tide.TensorList([G.S])
+    T.clip_grad_norm([grad], 1.0, norm)
+    want = 100 * math.sqrt((16 + 16 + 36 + 64) * length)
+    assert abs(norm.item() - want) <= 18 * U * want
+    assert abs(float(grad.square().sum(dtype=torch.float64)) - 1) < 1e-5
 
 
 def test_gradient_is_the_lookups_difference(tide):
@@ -451,6 +536,21 @@ def test_list_refusals(tide):
         assert status(T.adamw, f, views, f, f, **dict(good, **bad)) == E, bad
     assert status(T.adamw, f, views, f, f, [f[0].bfloat16()], **good) == E
     torch.cuda.synchronize()
+
+
+def test_lists_are_not_captured(tide):
+    """Their pointer tables are shared with later calls, so a graph must not hold them."""
+    T = tide.TensorList((100,))
+    x, norm = torch.ones(100, device="cuda"), torch.zeros(1, device="cuda")
+    T.grad_norm([x], norm)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        with pytest.raises(tide.TideError) as e:
+            T.grad_norm([x], norm)
+        norm.add_(1)
+    assert e.value.status == tide.TIDE_EINVAL
+    T.grad_norm([x], norm)
+    assert norm.item() == 10
 
 
 def test_lists_on_several_streams(tide):
