@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
     const uint32_t lo = min(a.n, (c * kSortWarps + warp) * per), hi = min(a.n, lo + per);
     uint32_t* mine = cnt + warp * bins;
 
+    wait_for_previous_kernel();
     // no CTA writes to another's shared memory before that one runs (awaited before the first such write)
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
@@ -680,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, kSumCtas<kLayout, Add>) sum_position
             zero_rows(a, (uint64_t(b - a.sum_blocks) * kWarps + (threadIdx.x >> 5)) * a.zero_rows, a.w.sorted, a.n);
         }
     }
+    let_next_kernel_start();
 }
 
 // ---- short lists ----------------------------------------------------------------------------------
@@ -706,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 3) sum_short_kernel(const __grid_con
     const uint32_t i = threadIdx.x;
     uint32_t key = ~0u;
     uint64_t src = 0;
+    wait_for_previous_kernel();
     if (i < a.n) {
         const int k = batch_of(a.b, i);
         const uint32_t j = i - a.b.start[k];
@@ -751,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 3) sum_short_kernel(const __grid_con
             [](int) {}, acc);
         write_row<In, kLayout, Add>(a.scale, table_row(a, t) + stretch * kStretch, a.tv.len - stretch * kStretch, acc, stage);
     }
+    let_next_kernel_start();
 }
 
 // Sets a kernel's attributes once for each device.
@@ -784,8 +788,7 @@ cudaError_t launch_short(const ShortArgs& a, int grid, cudaStream_t stream) {
     constexpr uint32_t smem = kSumSmem<In, kLayout>;
     cudaError_t e = once_per_device(done, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); });
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(kernel, grid, kThreads, smem, stream, a);
 }
 
 // Calls launch.template operator()<In, kLayout, Add>() for the call's types and alignments.
@@ -875,17 +878,19 @@ cudaError_t launch_sort(const SortArgs& a, uint32_t ctas, cudaStream_t stream) {
         return s != cudaSuccess ? s : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     });
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ctas;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kSortThreads);
     cfg.dynamicSmemBytes = smem(ctas);
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 

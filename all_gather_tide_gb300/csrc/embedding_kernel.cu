@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "embedding_device.cuh"
+#include "step_launch.cuh"
 
 namespace tide {
 namespace {
@@ -25,6 +26,7 @@ embedding_kernel(const __grid_constant__ ShardPtrs shards, TableView tv, const v
     constexpr int Rows = kLookupVectors<V> / Cols;
     using Word = typename Bf16Vec<V>::Word;
     const int lane = threadIdx.x & 31, tx = 1 << tx_log, x = lane & (tx - 1), y = lane >> tx_log, ty = 32 >> tx_log;
+    wait_for_previous_kernel();
     for (int64_t it = int64_t(blockIdx.x) * (kWarps) + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * (kWarps)) {
         const int64_t group = it / stretches, i0 = group * tokens;
         const uint32_t col0 = (uint32_t(it - group * stretches) * (Cols * tx) + x) * V;
@@ -69,6 +71,7 @@ embedding_kernel(const __grid_constant__ ShardPtrs shards, TableView tv, const v
             }
         }
     }
+    let_next_kernel_start();
 }
 
 // The widest vector (8, 4, 2 or 1 elements) that every row address of the table and, of `elem` bytes
@@ -97,8 +100,8 @@ cudaError_t lookup(const ShardPtrs& shards, const TableView& tv, const void* ids
     const int64_t items = count(tokens);
     const int grid = int(std::min<int64_t>((items + kWarps - 1) / (kWarps), overlap ? ctas : INT32_MAX));
     auto* kernel = cols == 8 ? embedding_kernel<Out, V, V <= 2 ? 8 : 4> : cols == 4 ? embedding_kernel<Out, V, 4> : cols == 2 ? embedding_kernel<Out, V, 2> : embedding_kernel<Out, V, 1>;
-    kernel<<<grid, kThreads, 0, stream>>>(shards, tv, ids, ids64, n, scale, out, out_stride, tx_log, tokens, uint32_t(stretches), items, status);
-    return cudaGetLastError();
+    return launch_after(kernel, grid, kThreads, 0, stream, shards, tv, ids, ids64, n, scale, out, out_stride, tx_log, tokens,
+                        uint32_t(stretches), items, status);
 }
 
 template <typename Out>

@@ -278,6 +278,7 @@ clip_kernel(TsList l, void* const* __restrict__ grads, float* norm, const double
         if (it.bf16) scale_item(static_cast<__nv_bfloat16*>(g), it, l.chunk, f);
         else scale_item(static_cast<float*>(g), it, l.chunk, f);
     }
+    let_next_kernel_start();
 }
 
 template <typename T>
@@ -331,6 +332,7 @@ adamw_kernel(TsList l, void* const* __restrict__ tables, AdamwArgs a) {
         if (it.bf16) adamw_item<__nv_bfloat16>(l, a, tables, it, f);
         else adamw_item<float>(l, a, tables, it, f);
     }
+    let_next_kernel_start();
 }
 
 int grid_of(const TsList& l, int ctas) { return int(std::max<int64_t>(1, std::min<int64_t>(ctas, (l.chunks + kWarps - 1) / kWarps))); }
