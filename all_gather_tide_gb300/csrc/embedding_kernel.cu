@@ -51,7 +51,7 @@ embedding_kernel(const __grid_constant__ ShardPtrs shards, TableView tv, const v
                 for (int c = 0; c < Cols; ++c) {
                     const uint32_t col = col0 + c * tx * V;
                     w[r][c] = Word{};
-                    if (has && col < tv.len) w[r][c] = __ldg(reinterpret_cast<const Word*>(row + col));
+                    if (has && col < tv.len) w[r][c] = __ldcg(reinterpret_cast<const Word*>(row + col));
                 }
             }
 #pragma unroll
