@@ -8,7 +8,9 @@ fails loudly if the library has not been built.
 
 "TIDE" is "The Endgame of FSDP Communication: Layout-Aware Collectives on Copy Engines, RDMA, and
 NVSwitch" (arXiv 2610.38228): the reduce-scatter is its TIDE-RS (abstract; Fig. 2b), the
-placement its TIDE-AG landing (abstract; Fig. 5b), the layout its Table 2.
+placement its TIDE-AG landing (abstract; Fig. 5b), the layout its Table 2.  Between the two, the
+rest of a training step runs on the same shards: embedding lookup and gradient, the gradients' norm and
+clipping, AdamW.
 """
 from __future__ import annotations
 
@@ -582,8 +584,7 @@ class Group:
     def embedding(self, p: int, shards: Sequence, ids, out, scale: float = 1.0, stream=None) -> None:
         """Rows ``ids`` of parameter p read from the R bf16 ``shards``, times ``scale``, into ``out``
         (``ids.numel()`` rows: ``[n, L]``, or contiguous ``[..., L]``)."""
-        if len(shards) != self.R:
-            _refuse("embedding", f"{self.R} shards are needed")
+        self._check_shards("embedding", shards, 2)
         stride = self._check_rows("embedding", p, ids, out)
         _embedding(self.handle, p, shards, ids, out, stride, scale, stream)
 
@@ -598,8 +599,7 @@ class Group:
         """The lookup's gradient into the R fp32 ``shards``: ``ids`` and ``douts`` are lists of batches.
         Without a ``workspace`` one is allocated for the call."""
         where = "embedding_grad"
-        if len(shards) != self.R:
-            _refuse(where, f"{self.R} shards are needed")
+        self._check_shards(where, shards, 4)
         if not len(ids) == len(douts) > 0:
             _refuse(where, "one dout for each batch of ids, and one batch at least")
         kinds = ids[0].dtype, douts[0].dtype
@@ -619,13 +619,22 @@ class Group:
                 workspace.record_stream(s)
         _embedding_grad(self.handle, p, counts, ids, douts, strides, shards, workspace, scale, accumulate, stream)
 
+    def _check_shards(self, where: str, shards, size: int) -> None:
+        """Refuses all but R shards (tensors are looked at; addresses and pointer tables are not)."""
+        if len(shards) != self.R:
+            _refuse(where, f"{self.R} shards are needed")
+        if not isinstance(shards, ctypes.Array):
+            for x in shards:
+                if not isinstance(x, int) and not (x.is_cuda and x.element_size() == size and x.numel() >= self.S and x.is_contiguous()):
+                    _refuse(where, f"a shard is {self.S} elements of {size} bytes on the GPU")
+
     def _check_rows(self, where: str, p: int, ids, rows) -> int:
         """Refuses ids and rows that do not fit parameter p; returns the rows' stride."""
         if not 0 <= p < self.P:
             _refuse(where, "no such parameter")
         n, length, shape = ids.numel(), self.row_len[p], rows.shape
-        if not ids.is_contiguous():
-            _refuse(where, "ids are not contiguous")
+        if not (ids.is_contiguous() and ids.is_cuda and rows.is_cuda):
+            _refuse(where, "contiguous ids, and rows, on the GPU are needed")
         if len(shape) == 2 and shape[0] == n and shape[1] == length:
             stride, inner = rows.stride()
             if (length == 1 or inner == 1) and (n <= 1 or stride >= length):
@@ -653,6 +662,7 @@ class TensorList:
     def __init__(self, elems: Sequence[int], types=None):
         self.elems = [int(n) for n in elems]
         self.K = len(self.elems)
+        self.grad_bytes = [2 if t == TIDE_BF16 else 4 for t in types] if types is not None else [4] * self.K
         self.handle = None
         self.handle = tide_tensors_create(self.elems, types)
 
@@ -673,33 +683,45 @@ class TensorList:
     def __exit__(self, *exc):
         self.close()
 
-    def _tensors(self, where: str, xs):
-        """xs, once its count (and, for tensors, their sizes) are those of the list."""
+    def _tensors(self, where: str, xs, size: int = 0):
+        """xs, once it has the list's count (and tensors its sizes); ``size``: bytes of an element, 0 for gradients."""
         if len(xs) != self.K:
             _refuse(where, f"{self.K} tensors are needed")
         if not isinstance(xs, ctypes.Array):
-            for n, x in zip(self.elems, xs):
-                if not isinstance(x, int) and (x.numel() != n or not x.is_contiguous()):
-                    _refuse(where, f"a contiguous tensor of {n} elements is needed")
+            for n, b, x in zip(self.elems, self.grad_bytes, xs):
+                if not isinstance(x, int) and not (x.numel() == n and x.is_cuda and x.is_contiguous() and x.element_size() == (size or b)):
+                    _refuse(where, f"a contiguous tensor of {n} elements of {size or b} bytes on the GPU is needed")
         return xs
 
+    @staticmethod
+    def _scalar(where: str, x, size: int = 4):
+        """x, unless it is a tensor that cannot hold one number of `size` bytes on the GPU."""
+        if not (x is None or isinstance(x, int)) and not (x.is_cuda and x.is_floating_point() and x.element_size() == size and x.numel() > 0):
+            _refuse(where, f"a floating-point tensor of {size}-byte elements on the GPU is needed")
+        return x
+
     def grad_norm(self, grads, norm, sumsq=None, stream=None) -> None:
-        tide_grad_norm(self.handle, self._tensors("grad_norm", grads), norm, sumsq, stream)
+        where = "grad_norm"
+        tide_grad_norm(self.handle, self._tensors(where, grads), self._scalar(where, norm), self._scalar(where, sumsq, 8), stream)
 
     def clip_grads(self, grads, norm, max_norm: float, stream=None) -> None:
-        tide_clip_grads(self.handle, self._tensors("clip_grads", grads), norm, max_norm, stream)
+        where = "clip_grads"
+        tide_clip_grads(self.handle, self._tensors(where, grads), self._scalar(where, norm), max_norm, stream)
 
     def clip_grad_norm(self, grads, max_norm: float, norm, stream=None) -> None:
-        tide_clip_grad_norm(self.handle, self._tensors("clip_grad_norm", grads), max_norm, norm, stream)
+        where = "clip_grad_norm"
+        tide_clip_grad_norm(self.handle, self._tensors(where, grads), max_norm, self._scalar(where, norm), stream)
 
     def adamw(self, params, grads, exp_avg, exp_avg_sq, shards=None, *, weight_decay=None, stream=None, **hyper) -> None:
         """One step; ``lr``, ``betas``, ``eps``, ``step``, ``norm``, ``max_norm`` and ``flags`` as ``tide_adamw``.
         ``weight_decay``: one number for all tensors, K of them, or a ``float_table``."""
         where = "adamw"
-        for xs in (params, grads, exp_avg, exp_avg_sq):
-            self._tensors(where, xs)
+        self._tensors(where, grads)
+        for xs in (params, exp_avg, exp_avg_sq):
+            self._tensors(where, xs, 4)
         if shards is not None:
-            self._tensors(where, shards)
+            self._tensors(where, shards, 2)
+        self._scalar(where, hyper.get("norm"))
         if isinstance(weight_decay, (int, float)):
             weight_decay = [weight_decay] * self.K
         if weight_decay is not None and len(weight_decay) != self.K:

@@ -11,10 +11,11 @@ namespace tide {
 
 // ---- embedding -------------------------------------------------------------------------------
 constexpr int kInlineRanks = 64;    // shard pointers that travel with a launch
+constexpr int kInlineBatches = 64;  // batches that travel with a launch
+// CTAs of 256 threads on an SM, as the kernels' registers are bounded for.
 constexpr int kLookupCtasPerSm = 4;
 constexpr int kSumCtasPerSm = 4;
 constexpr int kShortCtasPerSm = 3;
-constexpr int kInlineBatches = 64;  // batches that travel with a launch
 
 // The R shard pointers of a call: in the launch's own parameters up to kInlineRanks, else in a device
 // table.

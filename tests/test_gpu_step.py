@@ -351,7 +351,7 @@ def test_gradient_refusals(tide):
     assert status(douts=[x[:2]]) == E and status(douts=[x.t()]) == E
     assert status(workspace=work[:-1]) == E
     assert status(workspace=torch.empty(work.numel() + 1, dtype=torch.uint8, device="cuda")[1:]) == E
-    assert status(shards=[shards[0].view(torch.uint8)[1:-3], shards[1]]) == E
+    assert status(shards=[shards[0].data_ptr() + 2, shards[1]]) == E and status(shards=[s.bfloat16() for s in shards]) == E
     with pytest.raises(tide.TideError) as e:
         tide.tide_embedding_grad_workspace(t.G.handle, t.p, 1 << 31)
     assert e.value.status == tide.TIDE_ERANGE
@@ -368,7 +368,7 @@ def test_gradient_refusals(tide):
 
 # ---- lists of tensors ----------------------------------------------------------------------------
 
-LISTS = [(1,), (0, 1, 0), (31, 32, 33), (2047, 2048, 2049, 7), (8, 5, 100_003, 0, 1, 4096), (300_000,), tuple(range(0, 900, 7))]
+LISTS = [(1,), (0, 1, 0), (31, 32, 33), (2047, 2048, 2049, 7), (8, 5, 100_003, 0, 1, 4096), (300_000,), tuple(range(0, 900, 7)), (0,), (0, 0)]
 
 
 def make_list(tide, elems, kinds, seed, sigma=1.0, shift=0):
@@ -441,6 +441,16 @@ def test_clip(tide, elems, kinds, shift, max_norm):
         # the factor's sum and quotient, the product: 3 u; then one rounding to bf16
         lim = 4 * U * want.abs() + (2.0 ** -8 * want.abs() if x.dtype == torch.bfloat16 else 0) + 2.0 ** -140
         assert bool(((got.double() - want).abs() <= lim).all())
+
+
+def test_a_list_without_elements(tide):
+    T = tide.TensorList((0, 0))
+    norm = torch.full((1,), 5.0, device="cuda")
+    T.clip_grad_norm([0, 0], 1.0, norm)
+    assert norm.item() == 0
+    T.clip_grads([0, 0], norm, 1.0)
+    T.adamw([0, 0], [0, 0], [0, 0], [0, 0], lr=0.1, step=1)
+    torch.cuda.synchronize()
 
 
 def test_clip_by_a_norm_that_is_not_finite(tide):
@@ -528,6 +538,8 @@ def test_list_refusals(tide):
     assert status(T.grad_norm, [views[0], views[1][:5]], norm) == E
     assert status(T.grad_norm, [views[0].data_ptr() + 2, views[1]], norm) == E
     assert status(T.grad_norm, [0, views[1]], norm) == E
+    assert status(T.grad_norm, [views[0], views[1].float()], norm) == E and status(T.grad_norm, views, norm.double()) == E
+    assert status(T.grad_norm, views, norm, norm) == E and status(T.grad_norm, [v.cpu() for v in views], norm) == E
     assert status(T.clip_grads, views, norm, -1.0) == E and status(T.clip_grads, views, norm, float("nan")) == E
     assert status(T.clip_grad_norm, views, -1.0, norm) == E
     good = dict(lr=0.1, step=1)

@@ -101,6 +101,16 @@ def test_pieces_are_the_valid_rows(tide):
     assert sum(v.numel() for v in views) == 5 * 3 + 7 * 4 + 2 * 6
 
 
+class _OnGpu:
+    """A CPU tensor that says it lies on the GPU, for checks that look no further."""
+
+    def __init__(self, x):
+        self.x = x
+
+    def __getattr__(self, name):
+        return True if name == "is_cuda" else getattr(self.x, name)
+
+
 @pytest.mark.parametrize("ids, rows", [
     (torch.zeros(6, dtype=torch.int64)[::2], torch.empty(3, 4)),  # ids with gaps
     (torch.zeros(3, dtype=torch.int64), torch.empty(3, 5)),  # another row length
@@ -110,8 +120,27 @@ def test_pieces_are_the_valid_rows(tide):
 ])
 def test_rows_that_do_not_fit_are_refused(tide, ids, rows):
     g = _Shape(tide, 2, [(7, 4)])
+    check = lambda i, x: tide.Group._check_rows(g, "embedding", 0, _OnGpu(i), _OnGpu(x))
     with pytest.raises(tide.TideError) as e:
-        tide.Group._check_rows(g, "embedding", 0, ids, rows)
+        check(ids, rows)
     assert e.value.status == tide.TIDE_EINVAL
-    tide.Group._check_rows(g, "embedding", 0, torch.zeros(3, dtype=torch.int64), torch.empty(3, 6)[:, :4])
-    tide.Group._check_rows(g, "embedding", 0, torch.zeros(2, 3, dtype=torch.int64), torch.empty(2, 3, 4))
+    assert check(torch.zeros(3, dtype=torch.int64), torch.empty(3, 6)[:, :4]) == 6
+    assert check(torch.zeros(2, 3, dtype=torch.int64), torch.empty(2, 3, 4)) == 4
+    assert check(torch.zeros(1, dtype=torch.int64), torch.empty(1, 4)) == 4
+
+
+def test_tensors_of_the_host_are_refused(tide):
+    g = _Shape(tide, 2, [(7, 4)])
+    i, x = torch.zeros(3, dtype=torch.int64), torch.empty(3, 4)
+    refused = [lambda: tide.Group._check_rows(g, "embedding", 0, i, _OnGpu(x)), lambda: tide.Group._check_rows(g, "embedding", 0, _OnGpu(i), x),
+               lambda: tide.Group._check_shards(g, "embedding", [torch.empty(g.S)] * 2, 4),
+               lambda: tide.Group._check_shards(g, "embedding", [_OnGpu(torch.empty(g.S))] * 2, 2),  # the element size of the other kind
+               lambda: tide.Group._check_shards(g, "embedding", [_OnGpu(torch.empty(g.S - 1))] * 2, 4),
+               lambda: tide.TensorList._scalar("grad_norm", torch.empty(1)),
+               lambda: tide.TensorList._scalar("grad_norm", _OnGpu(torch.empty(1, dtype=torch.int32)))]
+    for f in refused:
+        with pytest.raises(tide.TideError) as e:
+            f()
+        assert e.value.status == tide.TIDE_EINVAL
+    tide.Group._check_shards(g, "embedding", [_OnGpu(torch.empty(g.S))] * 2, 4)
+    tide.Group._check_shards(g, "embedding", tide.pointer_table([1, 2]), 4)
