@@ -50,6 +50,84 @@ expand_positions_kernel(const __grid_constant__ Batches b, uint32_t first, uint3
     }
 }
 
+// Sort of up to kRankMost positions: a position's place is the number of positions that come before it, of
+// smaller rows or earlier with the same row.  Every CTA has all rows in shared memory and places
+// kRankPositions of them, eight lanes to a position.  n^2 comparisons, but no passes and no barriers between
+// CTAs: a gradient of 257, 1024 and 2048 positions takes 10.2, 15.3 and 18.3 us with this sort and 16.8, 21.9 and
+// 24.7 with the one below (rows of 4096 columns); at 4096 positions it is 26.0 against 29.6, but 24.0 against 22.4
+// where rows are short, and beyond it loses.
+constexpr uint32_t kRankMost = 2048;
+constexpr uint32_t kRankPositions = kThreads / 8;
+
+struct SortArgs {
+    Batches b;
+    uint32_t n, rows;
+    int expanded, passes;
+    int64_t counters;
+    GradWorkspace w;
+    int* status;
+};
+
+__global__ void __launch_bounds__(kThreads) rank_positions_kernel(const __grid_constant__ SortArgs a) {
+    extern __shared__ __align__(16) uint32_t rank_keys[];
+    const uint32_t padded = (a.n + 31) & ~31u, first = blockIdx.x * kRankPositions;
+    wait_for_previous_kernel();
+    // what the summing kernel finds cleared: its arrival counters
+    for (int64_t q = int64_t(blockIdx.x) * kThreads + threadIdx.x; q < a.counters; q += int64_t(gridDim.x) * kThreads) a.w.arrived[q] = 0;
+    constexpr int kAhead = 8;  // ids loaded before one is used
+    for (uint32_t j0 = threadIdx.x; j0 < padded; j0 += kAhead * kThreads) {
+        int64_t id[kAhead];
+        int k = a.expanded || j0 >= a.n ? 0 : batch_of(a.b, j0);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const uint32_t j = j0 + u * kThreads;
+            id[u] = -1;
+            if (j >= a.n) continue;
+            if (a.expanded) {
+                id[u] = a.w.pre[j].z;
+            } else {
+                while (j >= a.b.start[k + 1]) ++k;
+                id[u] = load_id(a.b.ids[k], a.b.ids64, j - a.b.start[k]);
+            }
+        }
+        bool bad = false;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const uint32_t j = j0 + u * kThreads;
+            bad |= id[u] >= int64_t(a.rows);
+            if (j < padded) rank_keys[j] = j < a.n ? row_of(id[u], a.rows) : ~0u;  // behind every position
+        }
+        if (bad && !a.expanded && blockIdx.x == 0) atomicCAS(a.status, 0, kStatusBadId);
+    }
+    __syncthreads();
+    const uint32_t i = first + threadIdx.x / 8, part = threadIdx.x & 7;
+    const uint32_t key = rank_keys[min(i, a.n - 1)];
+    uint32_t place = 0;
+    for (uint32_t v = part; v < padded / 4; v += 8) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&rank_keys[4 * v]);
+        if (v == i / 4) {
+            place += (o.x < key + (4 * v < i)) + (o.y < key + (4 * v + 1 < i)) + (o.z < key + (4 * v + 2 < i)) + (o.w < key);
+        } else {
+            const uint32_t below = key + (v < i / 4);  // of earlier positions, equal rows come before too
+            place += (o.x < below) + (o.y < below) + (o.z < below) + (o.w < below);
+        }
+    }
+#pragma unroll
+    for (int m = 4; m > 0; m >>= 1) place += __shfl_xor_sync(0xffffffffu, place, m);
+    if (part == 0 && i < a.n) {
+        uint64_t src;
+        if (a.expanded) {
+            const uint4 x = a.w.pre[i];
+            src = uint64_t(x.y) << 32 | x.x;
+        } else {
+            const int k = batch_of(a.b, i);
+            src = reinterpret_cast<uint64_t>(a.b.dout[k] + int64_t(i - a.b.start[k]) * a.b.stride[k]);
+        }
+        a.w.sorted[place] = make_uint4(uint32_t(src), uint32_t(src >> 32), key, 0);
+    }
+    let_next_kernel_start();
+}
+
 // Stable radix sort, least significant digit first, by one cluster: each warp owns a contiguous run
 // of positions, counts its digits, and places them in order behind the digits of smaller value and
 // the same digit of earlier warps and CTAs.  The counts of the CTAs meet in distributed shared
@@ -60,15 +138,6 @@ expand_positions_kernel(const __grid_constant__ Batches b, uint32_t first, uint3
 // Bound by the placing, a scattered 16-byte store for every position and pass from 16 SMs, and by a few
 // barriers a pass.
 constexpr int kSortBatch = 8;
-
-struct SortArgs {
-    Batches b;
-    uint32_t n, rows;
-    int expanded, passes;
-    int64_t counters;
-    GradWorkspace w;
-    int* status;
-};
 
 template <int kBits>
 __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const __grid_constant__ SortArgs a) {
@@ -703,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, kSumCtas<kLayout, Add>) sum_position
 // Up to kShortMost positions: one launch instead of two, no workspace.  Every CTA sorts the list for
 // itself (each position's place is the number of positions that come before it: n^2 comparisons in
 // shared memory), and one warp adds all positions of one row.  Bound by latency: 64 positions of 256
-// columns 4.0 us, 256 of 256 and of 4096 columns 6.3 and 10.9 us, where the two launches for 257 take 16.6.
+// columns 4.0 us, 256 of 256 and of 4096 columns 6.3 and 10.9 us; the two launches for 257 take 10.1 and 10.2.
 constexpr uint32_t kShortMost = kThreads;
 
 struct ShortArgs : Target {
@@ -918,6 +987,8 @@ cudaError_t launch_sort_positions(const Batches& b, bool expanded, const TableVi
     int bits = 0;
     while (tv.rows >> bits) ++bits;  // keys are 0 .. rows
     SortArgs a{b, n, tv.rows, expanded ? 1 : 0, (bits + kSortMaxBits - 1) / kSortMaxBits, plan_grad(tv, n).slots, w, status};
+    if (n <= kRankMost)
+        return launch_after(rank_positions_kernel, int((n + kRankPositions - 1) / kRankPositions), kThreads, ((size_t(n) + 31) & ~size_t(31)) * 4, stream, a);
     uint32_t ctas = 1;
     while (ctas < kSortMaxCtas && n > ctas * kSortPerCta) ctas <<= 1;
     static_assert(kSortMinBits == 6 && kSortMaxBits == 10, "one kernel for each digit size");

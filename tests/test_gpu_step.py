@@ -228,9 +228,10 @@ def test_gradient_of_unusual_texts(tide, what, add):
     assert t.G.device_status() == (64 if what == "past the table" else 0)
 
 
-@pytest.mark.parametrize("rows, n", [(1, 300), (2, 70000), (1023, 20000), (1024, 20000), (200_000, 50_000), (1_100_000, 9000)])
+@pytest.mark.parametrize("rows, n", [(50, 256), (50, 257), (3000, 2048), (3000, 2049), (1, 300), (2, 70000), (1023, 20000), (1024, 20000), (200_000, 50_000), (1_100_000, 9000)])
 def test_gradient_over_many_rows_and_positions(tide, rows, n):
-    """Row counts on both sides of one, two and three digits of the sort, and lists beyond one CTA's."""
+    """Row counts on both sides of one, two and three digits of the sort, lists on both sides of the lengths
+    at which another sort takes over, and lists beyond one CTA's."""
     t, g = Table(tide, 3, rows, 8), gen(rows)
     ids = [draw_ids(g, n, rows, 0.01, "i32")]
     run_grad(tide, t, ids, [torch.randn(n, 8, generator=g)], 1.0, False)
