@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 
 #include "step_internal.h"
+#include "step_launch.cuh"
 
 namespace tide {
 namespace {
@@ -20,7 +21,7 @@ __device__ __forceinline__ char* shard_base(const ShardPtrs& s, uint32_t d) {
 }
 
 __device__ __forceinline__ int64_t load_id(const void* ids, int ids64, int64_t i) {
-    return ids64 ? __ldg(static_cast<const long long*>(ids) + i) : int64_t(__ldg(static_cast<const int*>(ids) + i));
+    return ids64 ? load_here(static_cast<const int64_t*>(ids) + i) : int64_t(load_here(static_cast<const int32_t*>(ids) + i));
 }
 
 // The table row of an id, or `rows` where the position holds no token.

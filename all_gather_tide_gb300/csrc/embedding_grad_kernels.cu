@@ -12,7 +12,6 @@
 #include <atomic>
 
 #include "embedding_device.cuh"
-#include "step_launch.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
                 for (int u = 0; u < kSortBatch; ++u) {
                     const uint32_t i = i0 + u * 32 + lane;
                     uint4 x = make_uint4(0, 0, 0, 0);
-                    if (i < hi) x = __ldcg((pass > 0 ? from : a.w.pre) + i);
+                    if (i < hi) x = load_here((pass > 0 ? from : a.w.pre) + i);
                     key[u] = x.z;
                     src[u] = uint64_t(x.y) << 32 | x.x;
                 }

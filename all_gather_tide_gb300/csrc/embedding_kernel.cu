@@ -5,7 +5,6 @@
 #include <algorithm>
 
 #include "embedding_device.cuh"
-#include "step_launch.cuh"
 
 namespace tide {
 namespace {

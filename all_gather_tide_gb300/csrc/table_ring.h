@@ -20,7 +20,7 @@ struct Slot {
     const void** host = nullptr;
     void** dev = nullptr;
     cudaEvent_t done = nullptr;
-    cudaStream_t stream = nullptr;
+    unsigned long long stream = 0;  // its id: a handle may mean another stream later, or in another thread
     uint64_t last_use = 0;
     bool valid = false;
     bool pending = false;
@@ -63,9 +63,11 @@ struct TableRing {
 
     // The index of a slot that already holds this table for this stream, or -1.
     int find(const Part* parts, int count, cudaStream_t stream) {
+        unsigned long long id;
+        if (cudaStreamGetId(stream, &id) != cudaSuccess) return -1;  // put() reports it
         for (int k = 0; k < kSlots; ++k) {
             Slot& s = slots[k];
-            if (!s.valid || s.stream != stream) continue;
+            if (!s.valid || s.stream != id) continue;
             size_t at = 0;
             bool same = true;
             for (int i = 0; i < count && same; ++i) {
@@ -83,6 +85,8 @@ struct TableRing {
     // Uploads a table that find() did not find and returns its slot's index.  The caller calls
     // finish(k) after its launch.
     cudaError_t put(const Part* parts, int count, cudaStream_t stream, int* slot) {
+        unsigned long long id;
+        if (const cudaError_t e = cudaStreamGetId(stream, &id); e != cudaSuccess) return e;
         // victim: an unused slot, else the least recently used one
         int k = -1;
         for (int i = 0; i < kSlots && k < 0; ++i)
@@ -107,7 +111,7 @@ struct TableRing {
         std::memcpy(s.host, s.content.data(), bytes);
         const cudaError_t e = cudaMemcpyAsync(s.dev, s.host, bytes, cudaMemcpyHostToDevice, stream);
         if (e != cudaSuccess) return e;
-        s.stream = stream;
+        s.stream = id;
         s.valid = true;
         s.last_use = ++use_clock;
         *slot = k;

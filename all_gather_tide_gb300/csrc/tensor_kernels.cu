@@ -138,7 +138,7 @@ __device__ __forceinline__ double block_sum(double v) {
 // The CTAs' sums of squares in their order, over the CTA; valid in thread 0.
 __device__ __forceinline__ double sum_partials(const double* partial, unsigned count) {
     double all = 0.0;
-    for (unsigned b = threadIdx.x; b < count; b += kTsThreads) all += __ldcg(&partial[b]);
+    for (unsigned b = threadIdx.x; b < count; b += kTsThreads) all += load_here(&partial[b]);
     return block_sum(all);
 }
 

@@ -584,6 +584,33 @@ def test_lists_on_several_streams(tide):
         assert abs(norm.item() - w) <= 18 * U * w
 
 
+def test_one_handle_for_the_streams_of_several_threads(tide):
+    """Handle 2 is each thread's own default stream: calls of two threads with equal arguments share nothing on the device."""
+    import threading
+
+    per_thread = 2
+    elems = (3_000_000, 70_001)
+    T = tide.TensorList(elems)
+    xs = [torch.randn(n, generator=gen(n)).cuda() for n in elems]
+    want = math.sqrt(sum(float(x.double().square().sum()) for x in xs))
+    norms = torch.zeros(2, 200, device="cuda")
+    torch.cuda.synchronize()
+    start = threading.Barrier(2)
+
+    def run(k):
+        start.wait()
+        for rep in range(norms.shape[1]):
+            T.grad_norm(xs, norms[k, rep : rep + 1], stream=per_thread)
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert float((norms.double() - want).abs().max()) <= 18 * U * want
+
+
 # ---- all of it together --------------------------------------------------------------------------
 
 
