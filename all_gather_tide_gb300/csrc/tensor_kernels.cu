@@ -123,23 +123,44 @@ __device__ __forceinline__ void store_group(T* p, int e, int lo, int end, bool v
     }
 }
 
-// Sum over the CTA in a fixed order; valid in thread 0.
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double part[kWarps];
+// Sum over the warp.
+__device__ __forceinline__ double warp_sum(double v) {
     for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x == 0)
-        for (int w = 1; w < kWarps; ++w) v += part[w];
     return v;
 }
 
-// The CTAs' sums of squares in their order, over the CTA; valid in thread 0.
+// Sum over the CTA in a fixed order; valid in warp 0, which adds for all: a warp's fp64 addition takes the SM
+// as long as 16 or more of fp32.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double part[kTsThreads];
+    part[threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.x >= 32) return 0.0;
+    double x[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) x[w] = part[threadIdx.x + 32 * w];
+#pragma unroll
+    for (int s = kWarps / 2; s > 0; s >>= 1)
+#pragma unroll
+        for (int w = 0; w < s; ++w) x[w] += x[w + s];
+    return warp_sum(x[0]);
+}
+
+// The CTAs' sums of squares in a fixed order, by one warp, 16 loads of each lane in flight.
 __device__ __forceinline__ double sum_partials(const double* partial, unsigned count) {
+    constexpr int kAhead = 16;
     double all = 0.0;
-    for (unsigned b = threadIdx.x; b < count; b += kTsThreads) all += load_here(&partial[b]);
-    return block_sum(all);
+    for (unsigned b = threadIdx.x & 31; b < count; b += 32 * kAhead) {
+        double x[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) x[u] = b + 32 * u < count ? load_here(&partial[b + 32 * u]) : 0.0;
+#pragma unroll
+        for (int s = kAhead / 2; s > 0; s >>= 1)
+#pragma unroll
+            for (int u = 0; u < s; ++u) x[u] += x[u + s];
+        all += x[0];
+    }
+    return warp_sum(all);
 }
 
 // The sum of squares of 32 numbers: 32 is what a lane holds at once, and keeps fp64, whose adds the GPU
@@ -221,7 +242,7 @@ grad_norm_kernel(TsList l, const void* const* __restrict__ grads, double* partia
         last = atomicAdd(ticket, 1u) == gridDim.x - 1;
     }
     __syncthreads();
-    if (!last) return;
+    if (!last || threadIdx.x >= 32) return;
     __threadfence();
     const double all = sum_partials(partial, gridDim.x);
     if (threadIdx.x == 0) {
@@ -264,10 +285,12 @@ clip_kernel(TsList l, void* const* __restrict__ grads, float* norm, const double
     float n;
     if (parts) {
         __shared__ float shared_norm;
-        const double all = sum_partials(partial, parts);
-        if (threadIdx.x == 0) {
-            shared_norm = float(sqrt(all));
-            if (blockIdx.x == 0) norm[0] = shared_norm;
+        if (threadIdx.x < 32) {
+            const double all = sum_partials(partial, parts);
+            if (threadIdx.x == 0) {
+                shared_norm = float(sqrt(all));
+                if (blockIdx.x == 0) norm[0] = shared_norm;
+            }
         }
         __syncthreads();
         n = shared_norm;
