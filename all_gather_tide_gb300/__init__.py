@@ -93,7 +93,8 @@ SIGNATURES = {
     "tide_embedding": (ctypes.c_int, [_vp, ctypes.c_int32, _vpp, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                                       _vp, ctypes.c_int32, ctypes.c_int64, _vp]),
     "tide_embedding_grad_workspace": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64, _i64p]),
-    "tide_embedding_grad": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int32, _i64p, _vpp, ctypes.c_int32, _vpp, _i64p,
+    # n, ids, douts and dout_stride as addresses: the binding passes parts of one array
+    "tide_embedding_grad": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int32, _vp, _vp, ctypes.c_int32, _vp, _vp,
                                            ctypes.c_int32, ctypes.c_float, ctypes.c_int32, _vpp, _vp, ctypes.c_int64,
                                            _vp]),
     "tide_tensors_create": (ctypes.c_int, [_vpp, ctypes.c_int32, _i64p, _i32p]),
@@ -179,12 +180,19 @@ def _dtype_code(x) -> int:
     return code
 
 
+_current_stream = None  # torch's functions for the current device and its current stream's handle
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
+        global _current_stream
+        if _current_stream is None:
+            import torch
 
+            _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         # the handle of torch.cuda.current_stream(), without building the stream object (3 us on Grace)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        device, handle = _current_stream
+        return handle(device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -439,11 +447,12 @@ def tide_embedding_grad(g: int, p: int, ids: Sequence, douts: Sequence, shards: 
 
 def _embedding_grad(g, p, counts, ids, douts, strides, shards, workspace, scale, accumulate, stream) -> None:
     B = len(counts)
-    i64, vp = ctypes.c_int64 * B, ctypes.c_void_p * B
-    _check(lib().tide_embedding_grad(g, p, B, i64(*counts), vp(*[x.data_ptr() for x in ids]), _dtype_code(ids[0]),
-                                     vp(*[x.data_ptr() for x in douts]), i64(*strides), _dtype_code(douts[0]), scale,
-                                     accumulate, _ptr_array(shards), workspace.data_ptr(), workspace.numel(),
-                                     _stream(stream)), "tide_embedding_grad")
+    # the four arrays of the call in one
+    a = (ctypes.c_int64 * (4 * B))(*counts, *[x.data_ptr() for x in ids], *[x.data_ptr() for x in douts], *strides)
+    at = ctypes.addressof(a)
+    _check(lib().tide_embedding_grad(g, p, B, at, at + 8 * B, _dtype_code(ids[0]), at + 16 * B, at + 24 * B,
+                                     _dtype_code(douts[0]), scale, accumulate, _ptr_array(shards), workspace.data_ptr(),
+                                     workspace.numel(), _stream(stream)), "tide_embedding_grad")
 
 
 def tide_tensors_create(elems: Sequence[int], types=None) -> int:
@@ -662,6 +671,7 @@ class TensorList:
     def __init__(self, elems: Sequence[int], types=None):
         self.elems = [int(n) for n in elems]
         self.K = len(self.elems)
+        self._table = ctypes.c_void_p * self.K  # the type of a pointer_table of K tensors
         self.grad_bytes = [2 if t == TIDE_BF16 else 4 for t in types] if types is not None else [4] * self.K
         self.handle = None
         self.handle = tide_tensors_create(self.elems, types)
@@ -685,6 +695,8 @@ class TensorList:
 
     def _tensors(self, where: str, xs, size: int = 0):
         """xs, once it has the list's count (and tensors its sizes); ``size``: bytes of an element, 0 for gradients."""
+        if type(xs) is self._table:
+            return xs
         if len(xs) != self.K:
             _refuse(where, f"{self.K} tensors are needed")
         if not isinstance(xs, ctypes.Array):
@@ -716,11 +728,13 @@ class TensorList:
         """One step; ``lr``, ``betas``, ``eps``, ``step``, ``norm``, ``max_norm`` and ``flags`` as ``tide_adamw``.
         ``weight_decay``: one number for all tensors, K of them, or a ``float_table``."""
         where = "adamw"
-        self._tensors(where, grads)
-        for xs in (params, exp_avg, exp_avg_sq):
-            self._tensors(where, xs, 4)
-        if shards is not None:
-            self._tensors(where, shards, 2)
+        table = self._table
+        if not (type(params) is type(grads) is type(exp_avg) is type(exp_avg_sq) is table and (shards is None or type(shards) is table)):
+            self._tensors(where, grads)
+            for xs in (params, exp_avg, exp_avg_sq):
+                self._tensors(where, xs, 4)
+            if shards is not None:
+                self._tensors(where, shards, 2)
         self._scalar(where, hyper.get("norm"))
         if isinstance(weight_decay, (int, float)):
             weight_decay = [weight_decay] * self.K
