@@ -237,6 +237,38 @@ def test_gradient_over_many_rows_and_positions(tide, rows, n):
     run_grad(tide, t, ids, [torch.randn(n, 8, generator=g)], 1.0, False)
 
 
+@pytest.mark.parametrize("rows", [127, 129, 4095, 8193, (1 << 22) - 1, (1 << 22) + 1])
+def test_gradient_zeros_the_rows_without_a_token(tide, rows):
+    """Tables on both sides of the sizes at which zeros go beside the sort and in larger groups of rows; tokens at the
+    ends of groups, one of them repeated."""
+    t = Table(tide, 3, rows, 2)
+    ids = torch.cat([torch.arange(0, rows, max(1, rows // 300)), torch.tensor([0, 1, rows - 1, rows - 2, rows // 2]).repeat(80), torch.full((300,), 31)])
+    for k in range(5, 13):
+        ids = torch.cat([ids, torch.tensor([x for x in ((1 << k) - 1, 1 << k, (128 << k) - 1, 128 << k) if x < rows], dtype=torch.long)])
+    x = torch.randn(ids.numel(), 2, generator=gen(rows))
+    run_grad(tide, t, [ids], [x], 1.0, False)
+
+
+@pytest.mark.parametrize("n", [300, 5000])
+def test_gradient_is_written_after_the_kernel_before_has_read_the_shard(tide, n):
+    """Zeros are written while the positions are sorted, but not before what was launched earlier has ended."""
+    t, g = Table(tide, 1, 100_000, 256), gen(n)
+    ids, x = draw_ids(g, n, t.rows).cuda(), torch.randn(n, 256, generator=g).cuda()
+    T = tide.TensorList([t.S])
+    grad, moment, other = torch.ones(t.S, device="cuda"), torch.zeros(t.S, device="cuda"), torch.zeros(t.S, device="cuda")
+    param, work = torch.zeros(t.S, device="cuda"), t.G.embedding_grad_workspace(t.p, n)
+    for rep in range(5):
+        grad.fill_(1.0)
+        moment.zero_()
+        torch.cuda.synchronize()
+        T.adamw([param], [grad], [moment], [other], lr=0.1, betas=(0.5, 0.5), step=1)
+        t.G.embedding_grad(t.p, [ids], [x], [grad], workspace=work)
+        assert bool((moment == 0.5).all())
+        held = torch.zeros(t.rows, dtype=torch.bool, device="cuda")
+        held[ids[ids >= 0]] = True
+        assert bool((grad.view(t.rows, 256)[~held] == 0).all())
+
+
 def test_gradient_does_not_read_rows_of_positions_without_a_token(tide):
     for length in (256, 13):
         t, g = Table(tide, 2, 50, length), gen(7)
