@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
 //
 // Bound by HBM: 65536 positions of 8192 bf16 columns into 128000 rows, 727 us for 5.26 GB (7.2 TB/s, most of
 // it zeros written); 131072 of 4096 added to 128000 rows, 330 us for 2.10 GB (6.4 TB/s, reads and writes
-// mixed).  512 or 1024 columns to a warp took 411 and 461 us for the latter where 256 took 400.
+// mixed); 60000 bf16 rows of 1001 columns, without alignment, added to 20000 rows, 78 us.  512 or 1024 columns to
+// a warp took 411 and 461 us for the second where 256 took 400.
 constexpr uint32_t kStretch = 256;
 // Positions of a piece (plan_grad), and the warps that they have to keep busy: those of a GB300 at three
 // CTAs an SM.
@@ -334,10 +335,10 @@ __device__ __forceinline__ float* table_row(const Target& a, uint32_t t) {
 // The table row of sorted position i (tv.rows: no token).
 __device__ __forceinline__ uint32_t row_at(const SumArgs& a, uint32_t i) { return a.w.sorted[i].z; }
 
-// How a warp's 256 columns lie over its lanes: every 32nd element (kSingle), or so that 16 bytes of dout
-// are one lane's and the next 16 the next lane's, the rows in the shard being 32-byte aligned (kWide)
-// or not (kMixed).
-enum Layout { kSingle, kMixed, kWide };
+// How a warp's 256 columns lie over its lanes: every 32nd element (kShifted, where dout rows have no 16-byte
+// alignment), or so that 16 bytes of dout are one lane's and the next 16 the next lane's, the rows in the shard
+// being 32-byte aligned (kWide) or not (kMixed).
+enum Layout { kShifted, kMixed, kWide };
 
 // A lane's 8 columns of a dout row, 16 bytes of bf16 or twice 16 bytes of fp32 (512 bytes apart, so that a
 // warp's copies cover whole lines), copied to shared memory asynchronously: what is in flight takes no
@@ -375,50 +376,72 @@ struct Part {
     }
 };
 
-// Every 32nd of 256 columns, for rows that have no 16-byte alignment.
-template <typename In>
-struct Singles {
-    In x[8];
-    __device__ __forceinline__ void load(uint64_t row, uint32_t col, uint32_t len) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = col + 32 * j < len ? __ldg(reinterpret_cast<const In*>(row) + col + 32 * j) : In(0.0f);
-    }
-    __device__ __forceinline__ void add(float (&acc)[8]) const {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += float(x[j]);
-    }
+// Rows of dout in flight for a warp: groups of copies.  A shifted row lies in the ring as it does between
+// 16-byte boundaries.  Measured in us, shifted (60000 bf16 rows of 1001 columns added to 20000, and 127618 of 1123
+// written to 39540): 3 groups of 4 rows 90 and 125, 4 of 2 87 and 116, 3 of 2 85 and 115, 8 of 1 84 and 115, but for
+// fp32 rows 114 where 3 of 1 takes 106; loads of single elements instead 110 and 117.  Aligned (131072 rows of 4096
+// added to 128000, 48042 of 1368 to 1552): 3 groups of 4 362 and 64.8, 8 of 1 361 and 63.5.
+template <typename In, Layout kLayout>
+struct Ring {
+    static constexpr int kGroups = kLayout == kShifted ? 3 : 8, kGroup = kLayout == kShifted ? 4 / sizeof(In) : 1, kRows = kGroup * kGroups;
+    static constexpr uint32_t kRow = kStretch * sizeof(In) + (kLayout == kShifted ? 16 : 0), kBytes = kRows * kRow;
 };
 
-// Rows of dout in flight for a warp: groups of copies, 2 KB each.
-template <typename In>
-struct Ring {
-    static constexpr int kGroups = 3, kGroup = 8 / sizeof(In), kRows = kGroup * kGroups;
-    static constexpr uint32_t kRow = kStretch * sizeof(In), kBytes = kRows * kRow;
-};
+// The aligned 16 bytes, by the warp's lanes, that hold `bytes` bytes from `from` on; what lies behind these is not
+// read.  What lies before them in their first 16 is: it is of the same allocation.
+__device__ __forceinline__ void copy_shifted(uint32_t to, uint64_t from, uint32_t bytes) {
+    bytes += uint32_t(from) & 15;
+    from &= ~uint64_t(15);
+    for (uint32_t at = (threadIdx.x & 31) * 16; at < bytes; at += 32 * 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + at), "l"(from + at), "r"(min(16u, bytes - at)) : "memory");
+}
+__device__ __forceinline__ float load_shared(uint32_t at, float) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float load_shared(uint32_t at, __nv_bfloat16) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    return __uint_as_float(uint32_t(v) << 16);
+}
 
 // Adds a stretch of `count` rows of dout to acc, in order: src(k) is the k-th row's address, and turn(k) is
 // called before the k-th is added.  `ring`: the lane's place in the warp's shared memory.
 template <typename In, Layout kLayout, typename Src, typename Turn>
 __device__ __forceinline__ void add_rows(int count, uint32_t stretch, uint32_t len, uint32_t ring, Src src, Turn turn, float (&acc)[8]) {
-    if constexpr (kLayout == kSingle) {
-        constexpr int kAhead = 4;
-        const uint32_t col = stretch * kStretch + (threadIdx.x & 31);
-        for (int k = 0; k < count; k += kAhead) {
-            Singles<In> x[kAhead];
+    using R = Ring<In, kLayout>;
+    if constexpr (kLayout == kShifted) {
+        const uint32_t lane = threadIdx.x & 31, first = stretch * kStretch, bytes = min(kStretch, len - first) * sizeof(In);
+        ring -= lane * 16;
+        auto slot = [&](int k) { return ring + uint32_t(k) % R::kRows * R::kRow; };
+        auto fetch = [&](int k) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
+            for (int u = 0; u < R::kGroup; ++u) {
                 const uint64_t from = src(k + u);
-                if (k + u < count) x[u].load(from, col, len);
+                if (k + u < count) copy_shifted(slot(k + u), from + uint64_t(first) * sizeof(In), bytes);
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
+        for (int k = 0; k < R::kRows; k += R::kGroup) fetch(k);
+        for (int k = 0; k < count; k += R::kGroup) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(R::kGroups - 1) : "memory");
+            __syncwarp();  // lanes read what others copied
+#pragma unroll
+            for (int u = 0; u < R::kGroup; ++u) {
+                const uint32_t at = slot(k + u) + ((uint32_t(src(k + u)) + first * uint32_t(sizeof(In))) & 15) + lane * uint32_t(sizeof(In));
                 if (k + u >= count) break;
                 turn(k + u);
-                x[u].add(acc);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] += load_shared(at + 32 * j * uint32_t(sizeof(In)), In());
             }
+            __syncwarp();
+            fetch(k + R::kRows);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
     } else {
-        using R = Ring<In>;
         const uint32_t col = stretch * kStretch + Part<In>::column(threadIdx.x & 31, 0);
         const int left = int(len) - int(col);
         auto slot = [&](int k) { return ring + uint32_t(k) % R::kRows * R::kRow; };
@@ -449,55 +472,56 @@ __device__ __forceinline__ void add_rows(int count, uint32_t stretch, uint32_t l
     }
 }
 
-// The warp's sums to a stretch of a row, dst: `acc` as the layout spreads them over the lanes; `left`
-// columns of the row lie from dst on.
-template <typename In, Layout kLayout, bool Add>
-__device__ __forceinline__ void write_row(float scale, float* dst, uint32_t left, const float (&acc)[8], float* stage) {
+// What a stretch of a row, dst, holds, as the layout spreads its columns over the lanes; `left` columns of the
+// row lie from dst on.
+template <typename In, Layout kLayout>
+__device__ __forceinline__ void read_row(const float* dst, uint32_t left, float (&y)[8]) {
     using P = Part<In>;
     const uint32_t lane = threadIdx.x & 31;
-    float x[8], y[8] = {};
-    // What is added to is read here and not ahead of need: copies of the rows made as early as dout's (or
-    // prefetches, or additions in L2) took 400 to 420 us where this took 371.
     if constexpr (kLayout == kWide && P::kWords == 1) {
-        if (lane * 8 >= left) return;
-        dst += lane * 8;
-        if (Add) load_v8(dst, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = y[j] + scale * acc[j];
-        store_v8(dst, x);
+        if (lane * 8 < left) load_v8(dst + lane * 8, y);
     } else if constexpr (kLayout == kWide) {
-        float4* to[2];
-        bool in[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            to[i] = reinterpret_cast<float4*>(dst + P::column(lane, 4 * i));
-            in[i] = P::column(lane, 4 * i) < left;
-            if (Add && in[i]) {
-                const float4 v = *to[i];
-                y[4 * i] = v.x, y[4 * i + 1] = v.y, y[4 * i + 2] = v.z, y[4 * i + 3] = v.w;
-            }
+            if (P::column(lane, 4 * i) >= left) continue;
+            const float4 v = *reinterpret_cast<const float4*>(dst + P::column(lane, 4 * i));
+            y[4 * i] = v.x, y[4 * i + 1] = v.y, y[4 * i + 2] = v.z, y[4 * i + 3] = v.w;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = y[j] + scale * acc[j];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (in[i]) __stcs(to[i], make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
     } else {
-        if constexpr (kLayout == kMixed) {  // turned round so that stores of single elements lie side by side
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) stage[P::column(lane, j) + P::column(lane, j) / 8] = acc[j];
-            __syncwarp();
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t q = lane + 32 * j;
-            x[j] = kLayout == kMixed ? stage[q + q / 8] : acc[j];
-            if (Add && q < left) y[j] = dst[q];
-        }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (lane + 32 * j < left) dst[lane + 32 * j] = y[j] + scale * x[j];
+            if (lane + 32 * j < left) y[j] = dst[lane + 32 * j];
+    }
+}
+
+// The warp's sums, scaled and added to y, to a stretch of a row: `acc` as the layout spreads them, y as read_row
+// read it (or zeros).
+template <typename In, Layout kLayout>
+__device__ __forceinline__ void write_row(float scale, float* dst, uint32_t left, const float (&acc)[8], const float (&y)[8], float* stage) {
+    using P = Part<In>;
+    const uint32_t lane = threadIdx.x & 31;
+    float x[8];
+    if constexpr (kLayout == kMixed) {  // turned round so that stores of single elements lie side by side
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) stage[P::column(lane, j) + P::column(lane, j) / 8] = acc[j];
+        __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t q = lane + 32 * j;
+        x[j] = y[j] + scale * (kLayout == kMixed ? stage[q + q / 8] : acc[j]);
+    }
+    if constexpr (kLayout == kWide && P::kWords == 1) {
+        if (lane * 8 < left) store_v8(dst + lane * 8, x);
+    } else if constexpr (kLayout == kWide) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (P::column(lane, 4 * i) < left) __stcs(reinterpret_cast<float4*>(dst + P::column(lane, 4 * i)), make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (lane + 32 * j < left) dst[lane + 32 * j] = x[j];
     }
 }
 
@@ -595,23 +619,26 @@ __device__ __forceinline__ void join_partials(const SumArgs& a, uint32_t t, uint
         for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
         add_partials(a, a.pieces + first, last - first + 1, 1, stretch, sum);
     }
-    const uint32_t col0 = stretch * kStretch;
-    write_row<In, kLayout, Add>(a.scale, table_row(a, t) + col0, a.tv.len - col0, sum, stage);
+    const uint32_t left = a.tv.len - stretch * kStretch;
+    float* dst = table_row(a, t) + stretch * kStretch;
+    float old[8] = {};
+    if (Add) read_row<In, kLayout>(dst, left, old);
+    write_row<In, kLayout>(a.scale, dst, left, sum, old, stage);
 }
 
 // The running sum of one piece.
 template <typename In, Layout kLayout, bool Add>
 struct Run {
     const SumArgs& a;
-    uint32_t piece, stretch, before;
+    uint32_t piece, stretch, before, after;  // rows on either side of the piece
     float* stage;
-    float acc[8] = {};
+    float acc[8] = {}, old[8] = {};
     uint32_t cur = ~0u;    // the row being summed
     float* dst = nullptr;  // its stretch in the shard
     bool starts = true;    // in this piece
     uint32_t head = ~0u;   // the row that an earlier piece began and this one ended
 
-    __device__ __forceinline__ void write() { write_row<In, kLayout, Add>(a.scale, dst, a.tv.len - stretch * kStretch, acc, stage); }
+    __device__ __forceinline__ void write() { write_row<In, kLayout>(a.scale, dst, a.tv.len - stretch * kStretch, acc, old, stage); }
 
     // The next position's row of the table, and where it lies; what the position adds follows.
     __device__ __forceinline__ void turn_to(uint32_t t, float* to) {
@@ -628,9 +655,13 @@ struct Run {
         starts = t != before;
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+        // What this piece will write alone is read before the row's positions are awaited: 60000 rows of 1001
+        // columns added 78 us, 85 if read where it is written.  Read as early as the dout rows are copied, or
+        // prefetched, it takes longer (131072 rows of 4096: 400 to 420 us where reading it last took 371).
+        if (Add && starts && t != after) read_row<In, kLayout>(dst, a.tv.len - stretch * kStretch, old);
     }
 
-    __device__ __forceinline__ void finish(uint32_t after) {
+    __device__ __forceinline__ void finish() {
         uint32_t tail = ~0u;  // the row that a later piece ends
         if (cur != ~0u) {
             const bool ends = cur != after;
@@ -662,8 +693,7 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, uint32_t piece, uint
     // where their rows lie in the shards, worked out by each lane for its own
     const auto d0 = reinterpret_cast<unsigned long long>(p0.z < a.tv.rows ? table_row(a, p0.z) + stretch * kStretch : nullptr);
     const auto d1 = reinterpret_cast<unsigned long long>(p1.z < a.tv.rows ? table_row(a, p1.z) + stretch * kStretch : nullptr);
-    Run<In, kLayout, Add> run{a, piece, stretch, lo > 0 ? row_at(a, lo - 1) : ~0u, stage};
-    const uint32_t after = hi < a.n ? row_at(a, hi) : ~0u;  // rows on either side of the piece
+    Run<In, kLayout, Add> run{a, piece, stretch, lo > 0 ? row_at(a, lo - 1) : ~0u, hi < a.n ? row_at(a, hi) : ~0u, stage};
     add_rows<In, kLayout>(
         held, stretch, a.tv.len, ring, [&](int k) { return uint64_t(of(k, p0.y, p1.y)) << 32 | of(k, p0.x, p1.x); },
         [&](int k) {
@@ -671,7 +701,7 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, uint32_t piece, uint
             if (t != run.cur) run.turn_to(t, reinterpret_cast<float*>(of(k, d0, d1)));
         },
         run.acc);
-    run.finish(after);
+    run.finish();
 }
 
 // Zeros from p on, n elements, by one warp: 32-byte stores between single ones at the ends.
@@ -729,23 +759,23 @@ __device__ __forceinline__ void zero_rows(const Target& a, uint64_t r0, const ui
     }
 }
 
-// Dynamic shared memory of a CTA of sums: the warps' rings, or, for single elements, nothing; and for
-// kMixed what write_row turns the columns round in.
+// Dynamic shared memory of a CTA of sums: the warps' rings, and for kMixed what write_row turns the columns
+// round in.
 template <typename In, Layout kLayout>
-constexpr uint32_t kSumSmem = kLayout == kSingle ? 0 : kWarps * (Ring<In>::kBytes + (kLayout == kMixed ? 32 * 9 * 4 : 0));
+constexpr uint32_t kSumSmem = kWarps * (Ring<In, kLayout>::kBytes + (kLayout == kMixed ? 32 * 9 * 4 : 0));
 
 template <typename In, Layout kLayout>
 __device__ __forceinline__ void sum_smem(unsigned char* smem, uint32_t* ring, float** stage) {
     const uint32_t warp = threadIdx.x >> 5;
-    *ring = uint32_t(__cvta_generic_to_shared(smem)) + warp * Ring<In>::kBytes + (threadIdx.x & 31) * 16;
-    *stage = reinterpret_cast<float*>(smem + kWarps * Ring<In>::kBytes) + warp * (32 * 9);
+    *ring = uint32_t(__cvta_generic_to_shared(smem)) + warp * Ring<In, kLayout>::kBytes + (threadIdx.x & 31) * 16;
+    *stage = reinterpret_cast<float*>(smem + kWarps * Ring<In, kLayout>::kBytes) + warp * (32 * 9);
 }
 
 // CTAs of an SM that registers leave room for: 4, except where 3 measured faster (65536 positions into
 // 128000 x 8192, most of it zeros to write: 753 us with 3, 780 with 4; 131072 added to 128000 x 4096: 377
-// with 3, 363 with 4) or the rows in flight take registers (kSingle).
+// with 3, 363 with 4; 60000 bf16 rows of 4099 columns into 128000: 462 with 3, 453 with 4).
 template <Layout kLayout, bool Add>
-constexpr int kSumCtas = kLayout == kSingle || !Add ? 3 : kSumCtasPerSm;
+constexpr int kSumCtas = Add || kLayout == kShifted ? kSumCtasPerSm : 3;
 
 template <typename In, Layout kLayout, bool Add>
 __global__ void __launch_bounds__(kThreads, kSumCtas<kLayout, Add>) sum_positions_kernel(const __grid_constant__ SumArgs a) {
@@ -827,7 +857,10 @@ __global__ void __launch_bounds__(kThreads, kShortCtasPerSm) sum_short_kernel(co
             end += out ? __ffs(out) - 1 : 32;
             more = out == 0;
         }
-        float acc[8] = {};
+        const uint32_t left = a.tv.len - stretch * kStretch;
+        float* dst = table_row(a, t) + stretch * kStretch;
+        float acc[8] = {}, old[8] = {};
+        if (Add) read_row<In, kLayout>(dst, left, old);
         add_rows<In, kLayout>(
             int(end - p), stretch, a.tv.len, ring,
             [&](int k) {
@@ -835,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, kShortCtasPerSm) sum_short_kernel(co
                 return uint64_t(x.y) << 32 | x.x;
             },
             [](int) {}, acc);
-        write_row<In, kLayout, Add>(a.scale, table_row(a, t) + stretch * kStretch, a.tv.len - stretch * kStretch, acc, stage);
+        write_row<In, kLayout>(a.scale, dst, left, acc, old, stage);
     }
     let_next_kernel_start();
 }
@@ -878,9 +911,9 @@ cudaError_t launch_short(const ShortArgs& a, int grid, cudaStream_t stream) {
 template <typename F>
 cudaError_t with_kinds(const Target& a, int dout_bf16, bool dout_vec, bool accumulate, F&& launch) {
     const bool wide = a.tv.len % 8 == 0 && a.tv.off % 8 == 0 && a.shards.bits % 32 == 0;
-    const Layout layout = !dout_vec || a.tv.len % 8 ? kSingle : wide ? kWide : kMixed;
+    const Layout layout = !dout_vec || a.tv.len % 8 ? kShifted : wide ? kWide : kMixed;
     auto with_add = [&](auto in, auto add) {
-        if (layout == kSingle) return launch(in, std::integral_constant<Layout, kSingle>(), add);
+        if (layout == kShifted) return launch(in, std::integral_constant<Layout, kShifted>(), add);
         if (layout == kMixed) return launch(in, std::integral_constant<Layout, kMixed>(), add);
         return launch(in, std::integral_constant<Layout, kWide>(), add);
     };
