@@ -78,5 +78,24 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[4]) { __s
 __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[2]) { *reinterpret_cast<uint32_t*>(p) = pack(x[0], x[1]); }
 __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[1]) { *p = __float2bfloat16_rn(x[0]); }
 
+// The aligned 16 bytes, by the warp's lanes, that hold `bytes` bytes from `from` on; what lies behind these is not
+// read.  What lies before them in their first 16 is: it is of the same allocation.
+__device__ __forceinline__ void copy_shifted(uint32_t to, uint64_t from, uint32_t bytes) {
+    bytes += uint32_t(from) & 15;
+    from &= ~uint64_t(15);
+    for (uint32_t at = (threadIdx.x & 31) * 16; at < bytes; at += 32 * 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + at), "l"(from + at), "r"(min(16u, bytes - at)) : "memory");
+}
+__device__ __forceinline__ float load_shared(uint32_t at, float) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float load_shared(uint32_t at, __nv_bfloat16) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    return __uint_as_float(uint32_t(v) << 16);
+}
+
 }  // namespace
 }  // namespace tide

@@ -387,25 +387,6 @@ struct Ring {
     static constexpr uint32_t kRow = kStretch * sizeof(In) + (kLayout == kShifted ? 16 : 0), kBytes = kRows * kRow;
 };
 
-// The aligned 16 bytes, by the warp's lanes, that hold `bytes` bytes from `from` on; what lies behind these is not
-// read.  What lies before them in their first 16 is: it is of the same allocation.
-__device__ __forceinline__ void copy_shifted(uint32_t to, uint64_t from, uint32_t bytes) {
-    bytes += uint32_t(from) & 15;
-    from &= ~uint64_t(15);
-    for (uint32_t at = (threadIdx.x & 31) * 16; at < bytes; at += 32 * 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + at), "l"(from + at), "r"(min(16u, bytes - at)) : "memory");
-}
-__device__ __forceinline__ float load_shared(uint32_t at, float) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
-}
-__device__ __forceinline__ float load_shared(uint32_t at, __nv_bfloat16) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
-    return __uint_as_float(uint32_t(v) << 16);
-}
-
 // Adds a stretch of `count` rows of dout to acc, in order: src(k) is the k-th row's address, and turn(k) is
 // called before the k-th is added.  `ring`: the lane's place in the warp's shared memory.
 template <typename In, Layout kLayout, typename Src, typename Turn>

@@ -111,6 +111,28 @@ def test_lookup_is_exact(tide, shape, n):
     assert t.G.device_status() == 0
 
 
+@pytest.mark.parametrize("length", [127, 128, 129, 256, 511, 512, 513, 1025, 1537])
+def test_lookup_of_rows_that_lie_anywhere(tide, length):
+    """Row lengths on both sides of the stretches that a warp takes; tables and outputs off their alignment; NaN in every row
+    that no position asks for, so that nothing of a row's neighbours may enter."""
+    for before, out_type, out_shift, pad in ((1, "bf16", 0, 0), (3, "bf16", 1, 2), (1, "f32", 1, 3), (5, "f32", 0, 0), (2, "bf16", 3, 1)):
+        t, g = Table(tide, 2, 60, length, before), gen(length)
+        ids = 2 * torch.randint(0, 30, (45,), generator=g)
+        ids[::7] = -1
+        shards = [torch.randn(t.S, generator=g).bfloat16() for _ in range(2)]
+        for s, first in zip(shards, (0, t.m)):
+            s[t.o:t.o + t.m * length].view(t.m, length)[(torch.arange(t.m) + first) % 2 == 1] = float("nan")
+        dev = [Guarded(s, 1) for s in shards]
+        out = Guarded(torch.full((45, length + pad), 55.0).to(TYPES[out_type]), out_shift)
+        t.G.embedding(t.p, [d.view for d in dev], ids.cuda(), out.view[:, :length], -1.5)
+        whole = torch.cat([t.rows_of(shards), torch.zeros(1, length).bfloat16()])
+        want = (whole[ids].double() * -1.5).float().to(TYPES[out_type])
+        want[ids < 0] = 0.0
+        got = out.cpu()
+        assert torch.equal(got[:, :length], want) and not bool(torch.signbit(got[ids < 0]).any())
+        assert bool((got[:, length:] == 55).all())
+
+
 def test_lookup_of_ids_past_the_table_gives_zero_rows_and_a_status(tide):
     t = Table(tide, 2, 10, 16)
     shards = [torch.ones(t.S, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
@@ -235,6 +257,23 @@ def test_gradient_over_many_rows_and_positions(tide, rows, n):
     t, g = Table(tide, 3, rows, 8), gen(rows)
     ids = [draw_ids(g, n, rows, 0.01, "i32")]
     run_grad(tide, t, ids, [torch.randn(n, 8, generator=g)], 1.0, False)
+
+
+@pytest.mark.parametrize("n", [200, 900])
+@pytest.mark.parametrize("length", [9, 255, 257, 520, 1027])
+def test_gradient_of_rows_that_lie_anywhere(tide, length, n):
+    """Douts off their alignment by every number of elements in 16 bytes, short lists and sorted ones; rows of positions
+    without a token, which lie beside the others, hold NaN."""
+    t, g = Table(tide, 2, 300, length, 3), gen(length + n)
+    for shift in range(8):
+        dout, add = (torch.bfloat16, torch.float32)[shift % 2], shift % 4 < 2
+        ids = draw_ids(g, n, 300, 0.3)
+        x = torch.randn(n, length, generator=g).to(dout)
+        x[ids < 0] = float("nan")
+        old = [torch.randn(t.S, generator=g) for _ in range(2)]
+        dev, dx = [Guarded(o, shift % 3) for o in old], Guarded(x, shift)
+        t.G.embedding_grad(t.p, [ids.cuda()], [dx.view], [d.view for d in dev], 0.7, add)
+        check_grad(t, [ids], [torch.nan_to_num(x.float())], old, [d.cpu() for d in dev], 0.7, add)
 
 
 @pytest.mark.parametrize("rows", [127, 129, 4095, 8193, (1 << 22) - 1, (1 << 22) + 1])
