@@ -441,18 +441,20 @@ def tide_embedding_grad(g: int, p: int, ids: Sequence, douts: Sequence, shards: 
                         accumulate: bool = False, stream=None) -> None:
     """``ids`` and ``douts``: B tensors each (batch b: n_b ids, n_b rows); ``shards``: R fp32 shards;
     ``workspace``: uint8 tensor of ``tide_embedding_grad_workspace`` bytes."""
-    _embedding_grad(g, p, [x.numel() for x in ids], ids, douts, [_row_stride(x) for x in douts], shards, workspace, scale,
-                    accumulate, stream)
+    batches = [v for i, x in zip(ids, douts) for v in (i.numel(), i.data_ptr(), x.data_ptr(), _row_stride(x))]
+    _embedding_grad(g, p, batches, ids[0], douts[0], shards, workspace, scale, accumulate, stream)
 
 
-def _embedding_grad(g, p, counts, ids, douts, strides, shards, workspace, scale, accumulate, stream) -> None:
-    B = len(counts)
+def _embedding_grad(g, p, batches, ids, dout, shards, workspace, scale, accumulate, stream) -> None:
+    """``batches``: positions, address of the ids, address of the douts and their row stride, batch after batch; ``ids`` and
+    ``dout``: one of each, for the types."""
+    B = len(batches) // 4
     # the four arrays of the call in one
-    a = (ctypes.c_int64 * (4 * B))(*counts, *[x.data_ptr() for x in ids], *[x.data_ptr() for x in douts], *strides)
+    a = (ctypes.c_int64 * (4 * B))(*batches[::4], *batches[1::4], *batches[2::4], *batches[3::4])
     at = ctypes.addressof(a)
-    _check(lib().tide_embedding_grad(g, p, B, at, at + 8 * B, _dtype_code(ids[0]), at + 16 * B, at + 24 * B,
-                                     _dtype_code(douts[0]), scale, accumulate, _ptr_array(shards), workspace.data_ptr(),
-                                     workspace.numel(), _stream(stream)), "tide_embedding_grad")
+    _check(lib().tide_embedding_grad(g, p, B, at, at + 8 * B, _dtype_code(ids), at + 16 * B, at + 24 * B, _dtype_code(dout),
+                                     scale, accumulate, _ptr_array(shards), workspace.data_ptr(), workspace.numel(),
+                                     _stream(stream)), "tide_embedding_grad")
 
 
 def tide_tensors_create(elems: Sequence[int], types=None) -> int:
@@ -504,6 +506,7 @@ class Group:
 
     def __init__(self, R: int, params: Sequence[Tuple[int, int]], flags: int = 0):
         self.R = R
+        self._table = ctypes.c_void_p * R  # the type of a pointer_table of R shards
         self.rows = [int(r) for r, _ in params]
         self.row_len = [int(l) for _, l in params]
         self.P = len(self.rows)
@@ -593,7 +596,8 @@ class Group:
     def embedding(self, p: int, shards: Sequence, ids, out, scale: float = 1.0, stream=None) -> None:
         """Rows ``ids`` of parameter p read from the R bf16 ``shards``, times ``scale``, into ``out``
         (``ids.numel()`` rows: ``[n, L]``, or contiguous ``[..., L]``)."""
-        self._check_shards("embedding", shards, 2)
+        if type(shards) is not self._table:
+            self._check_shards("embedding", shards, 2)
         stride = self._check_rows("embedding", p, ids, out)
         _embedding(self.handle, p, shards, ids, out, stride, scale, stream)
 
@@ -608,25 +612,25 @@ class Group:
         """The lookup's gradient into the R fp32 ``shards``: ``ids`` and ``douts`` are lists of batches.
         Without a ``workspace`` one is allocated for the call."""
         where = "embedding_grad"
-        self._check_shards(where, shards, 4)
+        if type(shards) is not self._table:
+            self._check_shards(where, shards, 4)
         if not len(ids) == len(douts) > 0:
             _refuse(where, "one dout for each batch of ids, and one batch at least")
-        kinds = ids[0].dtype, douts[0].dtype
-        counts, strides = [], []
+        kind, form, batches = ids[0].dtype, douts[0].dtype, []
         for i, x in zip(ids, douts):
-            strides.append(self._check_rows(where, p, i, x))
-            counts.append(i.numel())
-            if (i.dtype, x.dtype) != kinds:
+            stride = self._check_rows(where, p, i, x)
+            if i.dtype is not kind or x.dtype is not form:
                 _refuse(where, "the batches differ in type")
+            batches += i.numel(), i.data_ptr(), x.data_ptr(), stride
         if workspace is None:
             import torch
 
-            workspace = self.embedding_grad_workspace(p, sum(counts))
+            workspace = self.embedding_grad_workspace(p, sum(batches[::4]))
             if stream is not None:
                 s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
                 s.wait_stream(torch.cuda.current_stream())
                 workspace.record_stream(s)
-        _embedding_grad(self.handle, p, counts, ids, douts, strides, shards, workspace, scale, accumulate, stream)
+        _embedding_grad(self.handle, p, batches, ids[0], douts[0], shards, workspace, scale, accumulate, stream)
 
     def _check_shards(self, where: str, shards, size: int) -> None:
         """Refuses all but R shards (tensors are looked at; addresses and pointer tables are not)."""
@@ -644,7 +648,9 @@ class Group:
         n, length, shape = ids.numel(), self.row_len[p], rows.shape
         if not (ids.is_contiguous() and ids.is_cuda and rows.is_cuda):
             _refuse(where, "contiguous ids, and rows, on the GPU are needed")
-        if len(shape) == 2 and shape[0] == n and shape[1] == length:
+        if shape == (n, length):
+            if rows.is_contiguous():
+                return length
             stride, inner = rows.stride()
             if (length == 1 or inner == 1) and (n <= 1 or stride >= length):
                 return stride if n > 1 else length
