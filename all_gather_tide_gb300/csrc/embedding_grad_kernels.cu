@@ -931,14 +931,17 @@ bool cut_blocks(Target* a, int64_t items, bool accumulate) {
 GradPlan plan_grad(const TableView& tv, int64_t n) {
     GradPlan g;
     g.stretches = (tv.len + kStretch - 1) / kStretch;
-    // Shorter pieces while they would not go round the GPU's warps often enough to end together, and
-    // still shorter ones while they would not fill them once: 72833 fp32 positions of 3384 columns took 364
-    // us with the first rule at one round, 358 at six, 371 at twelve; 12289 of 1027 took 122 us with pieces
-    // of 64 and 69 with pieces of 8.
+    // Shorter pieces, which end together, while the GPU's warps go round fewer than six times; still shorter ones,
+    // which leave more partial sums, only while they do not all have one, and the shortest while an SM has
+    // fewer than seven.  In us with 64, 32, 16, 8 positions (warps with 32): 60000 bf16 positions of 1001 columns
+    // added (7500) 84, 74, 79, 92; 20000 of 2048 written (5000) 65, 66, 70, 77; 12289 fp32 of 1027 written (1925) 69,
+    // 63, 59, 59; 6000 of 4096 added (3008) -, 40, 36, 38; 6273 of 704 written (588) -, 27, 23, 25; 1024 of 4096
+    // added (512) -, 19, 16, 15.
     auto items = [&] { return (n + g.piece - 1) / g.piece * g.stretches; };
     g.piece = kPieceMost;
-    while (g.piece > 2 * kPieceLeast && items() < 6 * kPieceWarps) g.piece >>= 1;
-    while (g.piece > kPieceLeast && items() < kPieceWarps) g.piece >>= 1;
+    if (items() < 6 * kPieceWarps) g.piece = 32;
+    if (items() < kPieceWarps) g.piece = 16;
+    if (items() < 152 * 7) g.piece = kPieceLeast;
     g.pieces = uint32_t((n + g.piece - 1) / g.piece);
     g.slots = (int64_t(g.pieces) + (g.pieces + kBlock - 1) / kBlock) * 2 * g.stretches;
     return g;
