@@ -26,9 +26,9 @@ constexpr int kSortWarps = kSortThreads / 32;
 // equal size; below 6 a pass gets no cheaper.
 constexpr int kSortMinBits = 6, kSortMaxBits = 10;
 // CTAs of the cluster, and positions for which the next ones join.  131072 positions sort in 54 us on 8 CTAs
-// and in 34 on 16 (before counts were pushed; 25 since); a gradient of 12289 positions takes 63.7 us with
-// a CTA for every 4096, 60.9 for every 2048, 60.2 for every 1024.
-constexpr uint32_t kSortMaxCtas = 16, kSortPerCta = 2048;
+// and in 34 on 16 (before counts were pushed; 25 since); gradients of 4000 positions of 1024 columns and 6273 of 704
+// take 22.0 and 22.0 us with a CTA for every 1024, 23.1 and 23.2 for every 2048, 22.3 and 22.3 for every 512.
+constexpr uint32_t kSortMaxCtas = 16, kSortPerCta = 1024;
 
 __device__ __forceinline__ int batch_of(const Batches& b, uint32_t i) {
     int lo = 0, hi = b.count;
