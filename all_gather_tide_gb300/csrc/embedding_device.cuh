@@ -79,12 +79,18 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[2]) { *re
 __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[1]) { *p = __float2bfloat16_rn(x[0]); }
 
 // The aligned 16 bytes, by the warp's lanes, that hold `bytes` bytes from `from` on; what lies behind these is not
-// read.  What lies before them in their first 16 is: it is of the same allocation.
+// read.  What lies before them in their first 16 is: it is of the same allocation.  bytes <= kMost, so that the
+// copies are predicated and not a loop (127618 rows of 1123 columns summed in 93 us, with a loop 100).
+template <uint32_t kMost>
 __device__ __forceinline__ void copy_shifted(uint32_t to, uint64_t from, uint32_t bytes) {
     bytes += uint32_t(from) & 15;
     from &= ~uint64_t(15);
-    for (uint32_t at = (threadIdx.x & 31) * 16; at < bytes; at += 32 * 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + at), "l"(from + at), "r"(min(16u, bytes - at)) : "memory");
+    const uint32_t lane16 = (threadIdx.x & 31) * 16;
+#pragma unroll
+    for (uint32_t i = 0; i < kMost + 15; i += 32 * 16) {
+        const uint32_t at = lane16 + i;
+        if (at < bytes) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + at), "l"(from + at), "r"(min(16u, bytes - at)) : "memory");
+    }
 }
 __device__ __forceinline__ float load_shared(uint32_t at, float) {
     float v;

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_positions_kernel(const _
 //
 // Bound by HBM: 65536 positions of 8192 bf16 columns into 128000 rows, 727 us for 5.26 GB (7.2 TB/s, most of
 // it zeros written); 131072 of 4096 added to 128000 rows, 330 us for 2.10 GB (6.4 TB/s, reads and writes
-// mixed); 60000 bf16 rows of 1001 columns, without alignment, added to 20000 rows, 78 us.  512 or 1024 columns to
+// mixed); 60000 bf16 rows of 1001 columns, without alignment, added to 20000 rows, 72 us.  512 or 1024 columns to
 // a warp took 411 and 461 us for the second where 256 took 400.
 constexpr uint32_t kStretch = 256;
 // Positions of a piece (plan_grad), and the warps that they have to keep busy: those of a GB300 at three
@@ -387,10 +387,10 @@ struct Ring {
     static constexpr uint32_t kRow = kStretch * sizeof(In) + (kLayout == kShifted ? 16 : 0), kBytes = kRows * kRow;
 };
 
-// Adds a stretch of `count` rows of dout to acc, in order: src(k) is the k-th row's address, and turn(k) is
-// called before the k-th is added.  `ring`: the lane's place in the warp's shared memory.
-template <typename In, Layout kLayout, typename Src, typename Turn>
-__device__ __forceinline__ void add_rows(int count, uint32_t stretch, uint32_t len, uint32_t ring, Src src, Turn turn, float (&acc)[8]) {
+// Adds a stretch of `count` rows of dout to acc, in order: src(k) is the k-th row's address, low(k) its low 32
+// bits, and turn(k) is called before the k-th is added.  `ring`: the lane's place in the warp's shared memory.
+template <typename In, Layout kLayout, typename Src, typename Low, typename Turn>
+__device__ __forceinline__ void add_rows(int count, uint32_t stretch, uint32_t len, uint32_t ring, Src src, Low low, Turn turn, float (&acc)[8]) {
     using R = Ring<In, kLayout>;
     if constexpr (kLayout == kShifted) {
         const uint32_t lane = threadIdx.x & 31, first = stretch * kStretch, bytes = min(kStretch, len - first) * sizeof(In);
@@ -400,7 +400,7 @@ __device__ __forceinline__ void add_rows(int count, uint32_t stretch, uint32_t l
 #pragma unroll
             for (int u = 0; u < R::kGroup; ++u) {
                 const uint64_t from = src(k + u);
-                if (k + u < count) copy_shifted(slot(k + u), from + uint64_t(first) * sizeof(In), bytes);
+                if (k + u < count) copy_shifted<kStretch * sizeof(In)>(slot(k + u), from + uint64_t(first) * sizeof(In), bytes);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -411,7 +411,7 @@ __device__ __forceinline__ void add_rows(int count, uint32_t stretch, uint32_t l
             __syncwarp();  // lanes read what others copied
 #pragma unroll
             for (int u = 0; u < R::kGroup; ++u) {
-                const uint32_t at = slot(k + u) + ((uint32_t(src(k + u)) + first * uint32_t(sizeof(In))) & 15) + lane * uint32_t(sizeof(In));
+                const uint32_t at = slot(k + u) + ((low(k + u) + first * uint32_t(sizeof(In))) & 15) + lane * uint32_t(sizeof(In));
                 if (k + u >= count) break;
                 turn(k + u);
 #pragma unroll
@@ -676,7 +676,7 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, uint32_t piece, uint
     const auto d1 = reinterpret_cast<unsigned long long>(p1.z < a.tv.rows ? table_row(a, p1.z) + stretch * kStretch : nullptr);
     Run<In, kLayout, Add> run{a, piece, stretch, lo > 0 ? row_at(a, lo - 1) : ~0u, hi < a.n ? row_at(a, hi) : ~0u, stage};
     add_rows<In, kLayout>(
-        held, stretch, a.tv.len, ring, [&](int k) { return uint64_t(of(k, p0.y, p1.y)) << 32 | of(k, p0.x, p1.x); },
+        held, stretch, a.tv.len, ring, [&](int k) { return uint64_t(of(k, p0.y, p1.y)) << 32 | of(k, p0.x, p1.x); }, [&](int k) { return of(k, p0.x, p1.x); },
         [&](int k) {
             const uint32_t t = of(k, p0.z, p1.z);
             if (t != run.cur) run.turn_to(t, reinterpret_cast<float*>(of(k, d0, d1)));
@@ -853,6 +853,7 @@ __global__ void __launch_bounds__(kThreads, kShortCtasPerSm) sum_short_kernel(co
                 const uint4 x = sorted[min(p + k, a.n - 1)];
                 return uint64_t(x.y) << 32 | x.x;
             },
+            [&](int k) { return sorted[min(p + k, a.n - 1)].x; },
             [](int) {}, acc);
         write_row<In, kLayout>(a.scale, dst, left, acc, old, stage);
     }

@@ -82,8 +82,8 @@ embedding_kernel(const __grid_constant__ ShardPtrs shards, TableView tv, const v
 // read back element by element, each lane two at a time where they are written as bf16.
 //
 // Bound by instructions, about 10 for two elements, and for long rows by HBM: 30000 rows of 2048 columns, off by
-// one element, 38 us for 0.25 GB (two-byte loads 75); 4099 of 1027 columns to fp32 6.2 us (9.1); 64000 of 129
-// columns 16.9 us (19.9), but of 101 17.1 (15.3), so shorter rows go by two-byte loads.  Stretches of up to 256
+// one element, 36 us for 0.25 GB (two-byte loads 75); 4099 of 1027 columns to fp32 5.7 us (9.1); 64000 of 129
+// columns 16.3 us (19.9), but of 101 17.1 (15.3), so shorter rows go by two-byte loads.  Stretches of up to 256
 // columns, 8 rows in flight, took 52 us for the first, of up to 768 with 3 rows 36, but for 30000 rows of 1001 columns
 // 25.2 where 512 take 23.0.  Four-byte vectors are not worth replacing (32000 rows of 1026 columns 26.9 us both ways).
 constexpr int kShiftedRows = 4;
@@ -110,7 +110,7 @@ embedding_shifted_kernel(const __grid_constant__ ShardPtrs shards, TableView tv,
         }
         auto fetch = [&](int k) {
             const unsigned long long from = __shfl_sync(0xffffffffu, at, k & 31);
-            if (k < held && from) copy_shifted(slot(k), from, cols * 2);
+            if (k < held && from) copy_shifted<kShiftedMost * 2>(slot(k), from, cols * 2);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
 #pragma unroll 1
