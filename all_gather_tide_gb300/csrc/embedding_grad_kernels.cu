@@ -697,7 +697,8 @@ __device__ __forceinline__ void zero_run(float* p, uint64_t n) {
 }
 
 // The first of the sorted positions [lo, hi) whose row is >= r (hi if none), found by the whole warp, 32
-// places at a time.
+// places at a time: the last positions of the first 32 of 33 parts.  The 33rd part's is not looked at, so where all
+// 32 lie below r (k = 32) nothing is known of it and hi stays.
 __device__ __forceinline__ uint32_t first_at_least(const uint4* sorted, uint32_t r, uint32_t lo, uint32_t hi) {
     const uint32_t lane = threadIdx.x & 31;
     while (lo < hi) {
@@ -707,7 +708,7 @@ __device__ __forceinline__ uint32_t first_at_least(const uint4* sorted, uint32_t
         const uint32_t k = __popc(below);  // sorted: a prefix of the lanes
         const uint64_t end = uint64_t(lo) + uint64_t(k + 1) * step - 1;
         lo += k * step;
-        if (end < hi) hi = uint32_t(end);
+        if (k < 32 && end < hi) hi = uint32_t(end);
     }
     return lo;
 }

@@ -288,6 +288,43 @@ def test_gradient_zeros_the_rows_without_a_token(tide, rows):
     run_grad(tide, t, [ids], [x], 1.0, False)
 
 
+def whole_numbers(n, length, dtype, seed):
+    """Rows of whole numbers from -8 to 8 on the GPU."""
+    return torch.randint(-8, 9, (n, length), generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").to(dtype)
+
+
+def check_exactly(t, ids, x, add, cuts=(), seed=0):
+    """The gradient of douts that are whole numbers, whose sums fp32 holds exactly: every element of every shard is what sums
+    in 64 bits give, zeros, padding and the other parameters' pieces among them.  cuts: where batches after the first begin."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    old = torch.randint(-8, 9, (t.R, t.S), generator=g, device="cuda").float()
+    shards, at = old.clone(), [0, *cuts, ids.numel()]
+    t.G.embedding_grad(t.p, [ids[a:b] for a, b in zip(at, at[1:])], [x[a:b] for a, b in zip(at, at[1:])], list(shards), 0.5, add)
+    keep = (ids >= 0) & (ids < t.rows)
+    total = torch.zeros(t.R * t.m, t.len, dtype=torch.float64, device="cuda").index_add_(0, ids[keep].long(), x[keep].double() * 0.5)
+    assert float(total.abs().max()) < 2 ** 22
+    want, piece = old.double(), slice(t.o, t.o + t.m * t.len)
+    want[:, piece] = total.view(t.R, -1) + (want[:, piece] if add else 0)
+    wrong = (shards.double() != want).nonzero()
+    assert wrong.numel() == 0, (wrong.shape[0], wrong[0].tolist())
+
+
+@pytest.mark.parametrize("below", [0, 4000])
+def test_gradient_keeps_the_last_row_of_a_group_that_is_zeroed(tide, below):
+    """A short list and a sorted one; 33 positions in the group of rows 127,968 to 127,999, of which the last is alone in its row:
+    one more than the search for the group's end looks at in one step."""
+    t = Table(tide, 8, 128_000, 64)
+    ids = torch.cat([torch.arange(below) % 1000, 127_968 + torch.arange(32) // 4, torch.tensor([127_990])]).cuda()
+    check_exactly(t, ids, whole_numbers(ids.numel(), 64, torch.float32, below), False)
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_gradient_of_many_rows_that_are_written_beside_zeros(tide, seed):
+    t, n = Table(tide, 8, 128_000, 128), 131_072
+    ids = torch.randint(0, t.rows, (n,), generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+    check_exactly(t, ids, whole_numbers(n, 128, torch.bfloat16, seed), False)
+
+
 @pytest.mark.parametrize("n", [300, 5000])
 def test_gradient_is_written_after_the_kernel_before_has_read_the_shard(tide, n):
     """Zeros are written while the positions are sorted, but not before what was launched earlier has ended."""
