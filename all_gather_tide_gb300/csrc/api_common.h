@@ -24,6 +24,10 @@ inline int check_device(int want) {
     return dev == want ? TIDE_OK : TIDE_EINVAL;
 }
 
+// What an object's creation uploaded has arrived.  A memset, or a copy from pageable memory that has been staged, may
+// return before, and streams made with cudaStreamNonBlocking are not ordered behind the stream that it is on.
+inline cudaError_t wait_for_uploads() { return cudaStreamSynchronize(cudaStreamLegacy); }
+
 // Pointer tables of a ring are shared with later calls, so work that reads one is not put into a graph.
 inline int check_not_captured(cudaStream_t stream) {
     cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;

@@ -131,6 +131,7 @@ int tide_tensors_create(tide_tensors_t* out, int32_t K, const int64_t* elems, co
                 e = cudaMemset(t->d_ticket, 0, ticket_bytes);
             }
             if (e == cudaSuccess && item_bytes) e = cudaMemcpy(t->d_items, items.data(), item_bytes, cudaMemcpyHostToDevice);
+            if (e == cudaSuccess) e = tide::wait_for_uploads();
             // five pointers and a factor for every tensor
             if (e == cudaSuccess) e = t->ring.create(size_t(K) * 6);
         } catch (...) {

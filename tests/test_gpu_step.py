@@ -674,6 +674,21 @@ def test_lists_are_not_captured(tide):
     assert norm.item() == 10
 
 
+@pytest.mark.parametrize("elems", [(0,), (100,), (5000, 7)], ids=str)
+def test_a_list_is_on_the_device_when_it_is_created(tide, elems):
+    """Its first call may be on a stream that does not wait for the default one, which is busy here."""
+    x, norm, side = [torch.ones(n, device="cuda") for n in elems], torch.full((1,), -1.0, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    assert not torch.cuda.default_stream().query()
+    T = tide.TensorList(elems)
+    assert torch.cuda.default_stream().query()
+    T.grad_norm(x, norm, stream=side)
+    side.synchronize()
+    want = math.sqrt(sum(elems))
+    assert abs(norm.item() - want) <= 18 * U * want
+
+
 def test_lists_on_several_streams(tide):
     """One list, other tensors on each of six streams (more than its ring holds), all in flight at once."""
     elems = (100_000, 3, 70_001)
