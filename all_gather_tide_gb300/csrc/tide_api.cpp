@@ -316,6 +316,7 @@ int tide_group_create(tide_group_t* out, int32_t R, int32_t P, const int64_t* ro
         }
         if (e == cudaSuccess) e = cudaMalloc(&g->d_status, sizeof(int));
         if (e == cudaSuccess) e = cudaMemset(g->d_status, 0, sizeof(int));
+        if (e == cudaSuccess) e = tide::wait_for_uploads();
         // a table holds the R*P gradient pointers + R shard pointers (reduce-scatter) or R + P
         // pointers (all-gather)
         if (e == cudaSuccess) e = g->ring.create(size_t(R) * P + R + P);

@@ -70,3 +70,10 @@ def created(fake, create, destroy):
 def test_a_list_waits_for_its_uploads(fake, elems):
     uploads, pending = created(fake, f"tide.tide_tensors_create({elems})", "tide.tide_tensors_destroy")
     assert uploads > 0 and pending == 0
+
+
+@pytest.mark.parametrize("params", [[(3, 1)], [(50, 16), (7, 24)], [(300, 8192)]], ids=str)
+def test_a_group_waits_for_its_uploads(fake, params):
+    rows, length = [r for r, _ in params], [n for _, n in params]
+    uploads, pending = created(fake, f"tide.tide_group_create(3, {rows}, {length})", "tide.tide_group_destroy")
+    assert uploads > 1 and pending == 0
