@@ -24,7 +24,7 @@ inline int check_device(int want) {
     return dev == want ? TIDE_OK : TIDE_EINVAL;
 }
 
-// What an object's creation uploaded has arrived.  A memset, or a copy from pageable memory that has been staged, may
+// What a synchronous call uploaded has arrived.  A memset, or a copy from pageable memory that has been staged, may
 // return before, and streams made with cudaStreamNonBlocking are not ordered behind the stream that it is on.
 inline cudaError_t wait_for_uploads() { return cudaStreamSynchronize(cudaStreamLegacy); }
 

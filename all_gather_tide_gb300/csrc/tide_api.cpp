@@ -627,7 +627,10 @@ int tide_group_device_status(tide_group_t g, int32_t* status) {
     if (rc != TIDE_OK) return rc;
     int v = 0;
     TIDE_CUDA(cudaMemcpy(&v, g->d_status, sizeof(int), cudaMemcpyDeviceToHost));
-    if (v) TIDE_CUDA(cudaMemset(g->d_status, 0, sizeof(int)));
+    if (v) {
+        TIDE_CUDA(cudaMemset(g->d_status, 0, sizeof(int)));
+        TIDE_CUDA(tide::wait_for_uploads());
+    }
     *status = v;
     return TIDE_OK;
 }

@@ -1,9 +1,9 @@
-"""What an object's creation uploads has arrived when the call returns, on the CPU.
+"""What a synchronous call sends to the device has arrived when the call returns, on the CPU.
 
 A device memset, and a copy from pageable memory that has only been staged, may still be under way on the legacy
 default stream when they return to the host, and streams made with cudaStreamNonBlocking are not ordered behind
-that stream.  The library runs here, in a process of its own, on a fake of the runtime calls that a creation
-makes; the fake counts the uploads that no synchronisation has covered.
+that stream.  The library runs here, in a process of its own, on a fake of the CUDA runtime that counts the uploads
+which no synchronisation has covered.
 """
 import os
 import subprocess
@@ -23,12 +23,14 @@ int fake_pending(void) { return pending; }
 static int upload(void) { ++uploads; ++pending; return 0; }
 int cudaGetDevice(int *d) { *d = 0; return 0; }
 int cudaDeviceGetAttribute(int *v, int attr, int d) { *v = 152; return 0; }
-int cudaMalloc(void **p, size_t n) { *p = malloc(n ? n : 1); return 0; }
+static void *last;
+void fake_set_last(int v) { *(int *)last = v; } /* the last device word that was allocated */
+int cudaMalloc(void **p, size_t n) { *p = malloc(n ? n : 1); if (n == sizeof(int)) last = *p; return 0; }
 int cudaFree(void *p) { free(p); return 0; }
 int cudaHostAlloc(void **p, size_t n, unsigned flags) { *p = malloc(n ? n : 1); return 0; }
 int cudaFreeHost(void *p) { free(p); return 0; }
 int cudaMemset(void *p, int v, size_t n) { memset(p, v, n); return upload(); }
-int cudaMemcpy(void *to, const void *from, size_t n, int kind) { memcpy(to, from, n); return upload(); }
+int cudaMemcpy(void *to, const void *from, size_t n, int kind) { memcpy(to, from, n); return kind == 2 ? 0 : upload(); } /* 2: to the host */
 int cudaEventCreateWithFlags(void **e, unsigned flags) { *e = malloc(1); return 0; }
 int cudaEventSynchronize(void *e) { return 0; }
 int cudaEventDestroy(void *e) { free(e); return 0; }
@@ -42,6 +44,7 @@ sys.path.insert(0, {root!r})
 fake = ctypes.CDLL({fake!r}, ctypes.RTLD_GLOBAL)  # found before the runtime that the library is linked to
 import all_gather_tide_gb300 as tide
 handle = {create}
+{then}
 print(fake.fake_uploads(), fake.fake_pending())
 {destroy}(handle)
 """
@@ -58,9 +61,9 @@ def fake(tmp_path_factory):
     return str(path / "fake.so")
 
 
-def created(fake, create, destroy):
-    """Uploads that the creation made, and those of them that it did not wait for."""
-    child = textwrap.dedent(CHILD).format(root=ROOT, fake=fake, create=create, destroy=destroy)
+def created(fake, create, destroy, then=""):
+    """Uploads that the creation and what follows it made, and those of them that were not waited for."""
+    child = textwrap.dedent(CHILD).format(root=ROOT, fake=fake, create=create, destroy=destroy, then=then)
     out = subprocess.run([sys.executable, "-c", child], capture_output=True, text=True, timeout=300)
     assert out.returncode == 0, out.stderr
     return tuple(int(v) for v in out.stdout.split())
@@ -76,4 +79,11 @@ def test_a_list_waits_for_its_uploads(fake, elems):
 def test_a_group_waits_for_its_uploads(fake, params):
     rows, length = [r for r, _ in params], [n for _, n in params]
     uploads, pending = created(fake, f"tide.tide_group_create(3, {rows}, {length})", "tide.tide_group_destroy")
+    assert uploads > 1 and pending == 0
+
+
+def test_clearing_a_status_is_waited_for(fake):
+    """A kernel of a later call may record its own, which a clearing that comes late would lose."""
+    read = "fake.fake_set_last(64); assert tide.tide_group_device_status(handle) == 64; assert tide.tide_group_device_status(handle) == 0"
+    uploads, pending = created(fake, "tide.tide_group_create(3, [50], [16])", "tide.tide_group_destroy", read)
     assert uploads > 1 and pending == 0
