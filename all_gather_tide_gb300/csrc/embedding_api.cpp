@@ -98,7 +98,7 @@ int tide_embedding_grad_workspace(tide_group_t g, int32_t p, int64_t n, int64_t*
     const int rc = table_view(g, p, &tv);
     if (rc != TIDE_OK) return rc;
     if (n > kMaxPositions) return TIDE_ERANGE;
-    *bytes = int64_t(tide::carve_grad_workspace(nullptr, tv, n, nullptr));
+    *bytes = int64_t(tide::grad_workspace_size(tv, n));
     return TIDE_OK;
 }
 

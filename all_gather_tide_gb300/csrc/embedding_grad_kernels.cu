@@ -968,6 +968,21 @@ size_t carve_grad_workspace(char* base, const TableView& tv, int64_t n, GradWork
     return at;
 }
 
+size_t grad_workspace_size(const TableView& tv, int64_t n) {
+    // A size grows with n as long as the pieces keep their length, and falls where they get longer and leave fewer
+    // partial sums; so the largest is that of n or of the last list with a shorter length.
+    size_t most = carve_grad_workspace(nullptr, tv, n, nullptr);
+    for (uint32_t piece = kPieceLeast; piece < plan_grad(tv, n).piece; piece *= 2) {
+        int64_t lo = 0, hi = n;  // pieces of lo positions are this long at most, of hi longer
+        while (hi - lo > 1) {
+            const int64_t mid = lo + (hi - lo) / 2;
+            if (plan_grad(tv, mid).piece <= piece) lo = mid; else hi = mid;
+        }
+        most = std::max(most, carve_grad_workspace(nullptr, tv, lo, nullptr));
+    }
+    return most;
+}
+
 cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t rows, const GradWorkspace& w,
                                     int* status, cudaStream_t stream) {
     const uint32_t n = b.start[b.count];

@@ -66,6 +66,8 @@ struct GradPlan {
 GradPlan plan_grad(const TableView& tv, int64_t n);
 // Carves the workspace for n positions at `base` (any pointer, also null) and returns its size.
 size_t carve_grad_workspace(char* base, const TableView& tv, int64_t n, GradWorkspace* w);
+// The largest size that up to n positions need.
+size_t grad_workspace_size(const TableView& tv, int64_t n);
 
 cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t rows, const GradWorkspace& w,
                                     int* status, cudaStream_t stream);

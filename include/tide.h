@@ -394,8 +394,9 @@ int tide_reduce_scatter_noalloc(int32_t R, int32_t P, const int64_t *rows, const
 int tide_embedding(tide_group_t g, int32_t p, const void *const *shards, const void *ids, int32_t ids_type,
                    int64_t n, float scale, void *out, int32_t out_type, int64_t out_stride, void *stream);
 
-/* Bytes of device workspace (256-byte aligned) that tide_embedding_grad needs on g for parameter p and n
- * positions in all.  Errors: TIDE_EINVAL, TIDE_ERANGE (as tide_embedding_grad). */
+/* Bytes of device workspace (256-byte aligned) with which tide_embedding_grad serves any call on g for
+ * parameter p with up to n positions in all; never fewer for a larger n.  Errors: TIDE_EINVAL,
+ * TIDE_ERANGE (as tide_embedding_grad). */
 int tide_embedding_grad_workspace(tide_group_t g, int32_t p, int64_t n, int64_t *bytes);
 
 /*
@@ -416,7 +417,8 @@ int tide_embedding_grad_workspace(tide_group_t g, int32_t p, int64_t n, int64_t 
  *           dout_stride[b] >= L_p elements apart.
  *   shards: host array of R device pointers, entry d = rank d's fp32 shard of S elements.
  *   workspace: device, 256-byte aligned, at least tide_embedding_grad_workspace's bytes for
- *           n[0] + ... + n[B-1]; holds nothing between calls, not shared by calls that overlap.
+ *           n[0] + ... + n[B-1] positions or more; holds nothing between calls, not shared by calls
+ *           that overlap.
  * Up to 64 ranks the call can be captured into a CUDA graph.
  * Asynchronous on `stream`.  Errors: TIDE_EINVAL (null or misaligned pointers, p, B, n, a type or a
  * stride out of range, the workspace too small, another device current), TIDE_ERANGE (rows_p > 2^31 - 2, L_p > 2^30,

@@ -475,6 +475,27 @@ def test_gradient_refusals(tide):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("length", [1, 300, 1024, 4096, 8192])
+def test_workspace_sizes_never_fall(tide, length):
+    t = Table(tide, 1, 10, length)
+    sizes = [tide.tide_embedding_grad_workspace(t.G.handle, t.p, n) for n in (*range(0, 130_000, 5), 10 ** 6, 10 ** 7, 10 ** 9, 2 * 10 ** 9)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("length, most", [(1024, 4241), (4096, 7265)])
+def test_a_workspace_serves_fewer_positions(tide, length, most):
+    """Lists on both sides of the lengths at which pieces get shorter, of which a shorter list has more partial sums."""
+    t = Table(tide, 2, 500, length)
+    work = Guarded(torch.zeros(t.G.embedding_grad_workspace(t.p, most).numel(), dtype=torch.uint8), 256 - GUARD)
+    for n in (most, most - 1, most - 16, 4233, 3000, 1500, 1057, 1056, 257, 256, 1):
+        ids, x = torch.arange(n, device="cuda") * 7 % 400, whole_numbers(n, length, torch.float32, n)
+        shards = [torch.full((t.S,), 3.0, device="cuda") for _ in range(2)]
+        t.G.embedding_grad(t.p, [ids], [x], shards, workspace=work.view)
+        want = torch.zeros(500, length, dtype=torch.float64, device="cuda").index_add_(0, ids, x.double())
+        assert torch.equal(torch.stack(shards).double().view(500, length), want)
+    work.cpu()
+
+
 # ---- lists of tensors ----------------------------------------------------------------------------
 
 LISTS = [(1,), (0, 1, 0), (31, 32, 33), (2047, 2048, 2049, 7), (8, 5, 100_003, 0, 1, 4096), (300_000,), tuple(range(0, 900, 7)), (0,), (0, 0)]
