@@ -45,6 +45,8 @@ TIDE_F32 = 0
 TIDE_BF16 = 1
 TIDE_I32 = 2
 TIDE_I64 = 3
+TIDE_SHORT_POSITIONS = 256
+TIDE_SHORT_BATCHES = 64
 TIDE_ADAMW_SKIP_NONFINITE = 0x1
 
 _lib = None
@@ -440,7 +442,8 @@ def tide_embedding_grad_workspace(g: int, p: int, n: int) -> int:
 def tide_embedding_grad(g: int, p: int, ids: Sequence, douts: Sequence, shards: Sequence, workspace, scale: float = 1.0,
                         accumulate: bool = False, stream=None) -> None:
     """``ids`` and ``douts``: B tensors each (batch b: n_b ids, n_b rows); ``shards``: R fp32 shards;
-    ``workspace``: uint8 tensor of ``tide_embedding_grad_workspace`` bytes."""
+    ``workspace``: uint8 tensor of ``tide_embedding_grad_workspace`` bytes, or None for a list that needs none
+    (``TIDE_SHORT_POSITIONS`` positions in ``TIDE_SHORT_BATCHES`` batches at most)."""
     batches = [v for i, x in zip(ids, douts) for v in (i.numel(), i.data_ptr(), x.data_ptr(), _row_stride(x))]
     _embedding_grad(g, p, batches, ids[0], douts[0], shards, workspace, scale, accumulate, stream)
 
@@ -452,9 +455,9 @@ def _embedding_grad(g, p, batches, ids, dout, shards, workspace, scale, accumula
     # the four arrays of the call in one
     a = (ctypes.c_int64 * (4 * B))(*batches[::4], *batches[1::4], *batches[2::4], *batches[3::4])
     at = ctypes.addressof(a)
+    work, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _check(lib().tide_embedding_grad(g, p, B, at, at + 8 * B, _dtype_code(ids), at + 16 * B, at + 24 * B, _dtype_code(dout),
-                                     scale, accumulate, _ptr_array(shards), workspace.data_ptr(), workspace.numel(),
-                                     _stream(stream)), "tide_embedding_grad")
+                                     scale, accumulate, _ptr_array(shards), work, size, _stream(stream)), "tide_embedding_grad")
 
 
 def tide_tensors_create(elems: Sequence[int], types=None) -> int:
@@ -610,7 +613,7 @@ class Group:
     def embedding_grad(self, p: int, ids: Sequence, douts: Sequence, shards: Sequence, scale: float = 1.0,
                        accumulate: bool = False, workspace=None, stream=None) -> None:
         """The lookup's gradient into the R fp32 ``shards``: ``ids`` and ``douts`` are lists of batches.
-        Without a ``workspace`` one is allocated for the call."""
+        Without a ``workspace`` one is allocated for the call, unless the list is short enough to need none."""
         where = "embedding_grad"
         if type(shards) is not self._table:
             self._check_shards(where, shards, 4)
@@ -622,10 +625,10 @@ class Group:
             if i.dtype is not kind or x.dtype is not form:
                 _refuse(where, "the batches differ in type")
             batches += i.numel(), i.data_ptr(), x.data_ptr(), stride
-        if workspace is None:
+        if workspace is None and ((n := sum(batches[::4])) > TIDE_SHORT_POSITIONS or len(ids) > TIDE_SHORT_BATCHES):
             import torch
 
-            workspace = self.embedding_grad_workspace(p, sum(batches[::4]))
+            workspace = self.embedding_grad_workspace(p, n)
             if stream is not None:
                 s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
                 s.wait_stream(torch.cuda.current_stream())

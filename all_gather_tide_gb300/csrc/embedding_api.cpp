@@ -121,8 +121,9 @@ int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t* n, 
             if (__builtin_mul_overflow(n[b], dout_stride[b], &last) || __builtin_mul_overflow(last, int64_t(4), &last)) return TIDE_ERANGE;
             if (n[b] > 0 && (!ids[b] || !douts[b] || !aligned(ids[b], isz) || !aligned(douts[b], fsz))) return TIDE_EINVAL;
         }
-        if (total > 0 && (!workspace || !aligned(workspace, 256) ||
-                          workspace_bytes < int64_t(tide::carve_grad_workspace(nullptr, tv, total, nullptr))))
+        // a short list goes without a workspace; one that is given has to be good all the same
+        if (total > 0 && (workspace || !tide::short_list(total, B)) &&
+            (!workspace || !aligned(workspace, 256) || workspace_bytes < int64_t(tide::carve_grad_workspace(nullptr, tv, total, nullptr))))
             return TIDE_EINVAL;
         std::lock_guard<std::mutex> lock(g->mu);
         if ((rc = tide::check_device(g->device)) != TIDE_OK) return rc;
@@ -134,7 +135,7 @@ int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t* n, 
             tide::GradWorkspace w{};
             bool dout_vec = true;
             if (total > 0) {
-                tide::carve_grad_workspace(static_cast<char*>(workspace), tv, total, &w);
+                if (workspace) tide::carve_grad_workspace(static_cast<char*>(workspace), tv, total, &w);
                 const bool expanded = B > tide::kInlineBatches;
                 tide::Batches bt{};
                 bt.ids64 = ids_type == TIDE_I64;

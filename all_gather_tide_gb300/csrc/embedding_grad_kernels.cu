@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "../../include/tide.h"
 #include "embedding_device.cuh"
 
 namespace cg = cooperative_groups;
@@ -1055,6 +1056,7 @@ cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, u
     });
 }
 
+static_assert(kShortMost == TIDE_SHORT_POSITIONS && kInlineBatches == TIDE_SHORT_BATCHES, "what the header promises");
 bool short_list(int64_t n, int32_t batches) { return n > 0 && n <= int64_t(kShortMost) && batches <= kInlineBatches; }
 
 cudaError_t launch_sum_short(const ShardPtrs& shards, const TableView& tv, const Batches& b, uint32_t n, int dout_bf16,

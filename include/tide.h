@@ -399,6 +399,10 @@ int tide_embedding(tide_group_t g, int32_t p, const void *const *shards, const v
  * TIDE_ERANGE (as tide_embedding_grad). */
 int tide_embedding_grad_workspace(tide_group_t g, int32_t p, int64_t n, int64_t *bytes);
 
+/* Lists of up to so many positions and batches are sorted and summed by one launch without a workspace. */
+#define TIDE_SHORT_POSITIONS 256
+#define TIDE_SHORT_BATCHES 64
+
 /*
  * tide_embedding_grad — the lookup's gradient, summed by token straight into the fp32 shards.  The
  * positions of B batches (one for each contributing rank, say; batch b has n[b] of them), in order:
@@ -418,7 +422,8 @@ int tide_embedding_grad_workspace(tide_group_t g, int32_t p, int64_t n, int64_t 
  *   shards: host array of R device pointers, entry d = rank d's fp32 shard of S elements.
  *   workspace: device, 256-byte aligned, at least tide_embedding_grad_workspace's bytes for
  *           n[0] + ... + n[B-1] positions or more; holds nothing between calls, not shared by calls
- *           that overlap.
+ *           that overlap.  May be NULL for up to TIDE_SHORT_POSITIONS positions in up to
+ *           TIDE_SHORT_BATCHES batches, which need none.
  * Up to 64 ranks the call can be captured into a CUDA graph.
  * Asynchronous on `stream`.  Errors: TIDE_EINVAL (null or misaligned pointers, p, B, n, a type or a
  * stride out of range, the workspace too small, another device current), TIDE_ERANGE (rows_p > 2^31 - 2, L_p > 2^30,

@@ -496,6 +496,28 @@ def test_a_workspace_serves_fewer_positions(tide, length, most):
     work.cpu()
 
 
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("sizes", [(0,), (1,), (256,), (0, 100, 3), (4,) * 64], ids=lambda s: f"{len(s)}x{sum(s)}")
+def test_short_lists_need_no_workspace(tide, sizes, add, monkeypatch):
+    t, g = Table(tide, 3, 90, 520, 8), gen(sum(sizes))
+    ids = draw_ids(g, sum(sizes), 90, 0.1).cuda()
+    cuts = torch.tensor(sizes).cumsum(0)[:-1].tolist()
+    monkeypatch.setattr(t.G, "embedding_grad_workspace", lambda *a: pytest.fail("a workspace was allocated"))
+    check_exactly(t, ids, whole_numbers(ids.numel(), 520, torch.bfloat16, 1), add, cuts)
+
+
+def test_longer_lists_need_a_workspace(tide):
+    t = Table(tide, 2, 90, 64)
+    shards = [torch.zeros(t.S, device="cuda") for _ in range(2)]
+    for sizes in ((257,), (2,) * 65):
+        ids, x = [torch.zeros(n, dtype=torch.int64, device="cuda") for n in sizes], [torch.zeros(n, 64, device="cuda") for n in sizes]
+        with pytest.raises(tide.TideError) as e:
+            tide.tide_embedding_grad(t.G.handle, t.p, ids, x, shards, None)
+        assert e.value.status == tide.TIDE_EINVAL
+        t.G.embedding_grad(t.p, ids, x, shards)  # allocates one
+    torch.cuda.synchronize()
+
+
 # ---- lists of tensors ----------------------------------------------------------------------------
 
 LISTS = [(1,), (0, 1, 0), (31, 32, 33), (2047, 2048, 2049, 7), (8, 5, 100_003, 0, 1, 4096), (300_000,), tuple(range(0, 900, 7)), (0,), (0, 0)]
