@@ -442,7 +442,7 @@ def tide_embedding_grad_workspace(g: int, p: int, n: int) -> int:
 def tide_embedding_grad(g: int, p: int, ids: Sequence, douts: Sequence, shards: Sequence, workspace, scale: float = 1.0,
                         accumulate: bool = False, stream=None) -> None:
     """``ids`` and ``douts``: B tensors each (batch b: n_b ids, n_b rows); ``shards``: R fp32 shards;
-    ``workspace``: uint8 tensor of ``tide_embedding_grad_workspace`` bytes, or None for a list that needs none
+    ``workspace``: contiguous tensor of ``tide_embedding_grad_workspace`` bytes, or None for a list that needs none
     (``TIDE_SHORT_POSITIONS`` positions in ``TIDE_SHORT_BATCHES`` batches at most)."""
     batches = [v for i, x in zip(ids, douts) for v in (i.numel(), i.data_ptr(), x.data_ptr(), _row_stride(x))]
     _embedding_grad(g, p, batches, ids[0], douts[0], shards, workspace, scale, accumulate, stream)
@@ -455,7 +455,7 @@ def _embedding_grad(g, p, batches, ids, dout, shards, workspace, scale, accumula
     # the four arrays of the call in one
     a = (ctypes.c_int64 * (4 * B))(*batches[::4], *batches[1::4], *batches[2::4], *batches[3::4])
     at = ctypes.addressof(a)
-    work, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    work, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(lib().tide_embedding_grad(g, p, B, at, at + 8 * B, _dtype_code(ids), at + 16 * B, at + 24 * B, _dtype_code(dout),
                                      scale, accumulate, _ptr_array(shards), work, size, _stream(stream)), "tide_embedding_grad")
 
@@ -625,6 +625,7 @@ class Group:
             if i.dtype is not kind or x.dtype is not form:
                 _refuse(where, "the batches differ in type")
             batches += i.numel(), i.data_ptr(), x.data_ptr(), stride
+        self._check_workspace(where, workspace)
         if workspace is None and ((n := sum(batches[::4])) > TIDE_SHORT_POSITIONS or len(ids) > TIDE_SHORT_BATCHES):
             import torch
 
@@ -634,6 +635,12 @@ class Group:
                 s.wait_stream(torch.cuda.current_stream())
                 workspace.record_stream(s)
         _embedding_grad(self.handle, p, batches, ids[0], douts[0], shards, workspace, scale, accumulate, stream)
+
+    @staticmethod
+    def _check_workspace(where: str, x) -> None:
+        """Refuses all but a contiguous tensor on the GPU, or None."""
+        if not (x is None or (not isinstance(x, int) and x.is_cuda and x.is_contiguous())):
+            _refuse(where, "a workspace is a contiguous tensor on the GPU")
 
     def _check_shards(self, where: str, shards, size: int) -> None:
         """Refuses all but R shards (tensors are looked at; addresses and pointer tables are not)."""

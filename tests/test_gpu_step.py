@@ -518,6 +518,22 @@ def test_longer_lists_need_a_workspace(tide):
     torch.cuda.synchronize()
 
 
+def test_workspaces_that_do_not_fit_are_refused(tide):
+    """On the host, with gaps, or too small; one of other elements is as large as its bytes."""
+    t, n = Table(tide, 2, 500, 64), 1000
+    ids, x = torch.arange(n, device="cuda") % 500, whole_numbers(n, 64, torch.float32, 0)
+    need = tide.tide_embedding_grad_workspace(t.G.handle, t.p, n)
+    shards = [torch.zeros(t.S, device="cuda") for _ in range(2)]
+    for bad in (torch.empty(2 * need, dtype=torch.uint8), torch.empty(need, dtype=torch.uint8).pin_memory(), torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2],
+                torch.empty(need // 4 - 1, device="cuda"), torch.empty(0, dtype=torch.uint8, device="cuda")):
+        with pytest.raises(tide.TideError) as e:
+            t.G.embedding_grad(t.p, [ids], [x], shards, workspace=bad)
+        assert e.value.status == tide.TIDE_EINVAL
+    t.G.embedding_grad(t.p, [ids], [x], shards, workspace=torch.empty(need // 4, device="cuda"))
+    want = torch.zeros(500, 64, dtype=torch.float64, device="cuda").index_add_(0, ids, x.double())
+    assert torch.equal(torch.stack(shards).double().view(500, 64), want)
+
+
 # ---- lists of tensors ----------------------------------------------------------------------------
 
 LISTS = [(1,), (0, 1, 0), (31, 32, 33), (2047, 2048, 2049, 7), (8, 5, 100_003, 0, 1, 4096), (300_000,), tuple(range(0, 900, 7)), (0,), (0, 0)]

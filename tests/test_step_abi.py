@@ -144,3 +144,12 @@ def test_tensors_of_the_host_are_refused(tide):
         assert e.value.status == tide.TIDE_EINVAL
     tide.Group._check_shards(g, "embedding", [_OnGpu(torch.empty(g.S))] * 2, 4)
     tide.Group._check_shards(g, "embedding", tide.pointer_table([1, 2]), 4)
+
+
+def test_a_workspace_of_the_host_or_with_gaps_is_refused(tide):
+    for bad in (torch.empty(4096, dtype=torch.uint8), _OnGpu(torch.empty(8192, dtype=torch.uint8)[::2]), 4096):
+        with pytest.raises(tide.TideError) as e:
+            tide.Group._check_workspace("embedding_grad", bad)
+        assert e.value.status == tide.TIDE_EINVAL
+    for good in (None, _OnGpu(torch.empty(4096, dtype=torch.uint8)), _OnGpu(torch.empty(64, 16))):
+        tide.Group._check_workspace("embedding_grad", good)
