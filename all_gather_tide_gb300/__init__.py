@@ -182,6 +182,20 @@ def _dtype_code(x) -> int:
     return code
 
 
+_NAMES = {2: "bf16", 4: "fp32"}
+_kinds = {}  # bytes of an element -> the types that hold it
+
+
+def _holds(x, size: int) -> bool:
+    """Whether x holds numbers of ``size`` bytes as the kernels read them: fp32, or bf16, also as the 16-bit integers of
+    its bits."""
+    if not _kinds:
+        import torch
+
+        _kinds.update({4: (torch.float32,), 2: (torch.bfloat16, torch.int16, torch.uint16)})
+    return x.dtype in _kinds[size]
+
+
 _current_stream = None  # torch's functions for the current device and its current stream's handle
 
 
@@ -648,8 +662,8 @@ class Group:
             _refuse(where, f"{self.R} shards are needed")
         if not isinstance(shards, ctypes.Array):
             for x in shards:
-                if not isinstance(x, int) and not (x.is_cuda and x.element_size() == size and x.numel() >= self.S and x.is_contiguous()):
-                    _refuse(where, f"a shard is {self.S} elements of {size} bytes on the GPU")
+                if not isinstance(x, int) and not (x.is_cuda and _holds(x, size) and x.numel() >= self.S and x.is_contiguous()):
+                    _refuse(where, f"a shard is {self.S} contiguous elements of {_NAMES[size]} on the GPU")
 
     def _check_rows(self, where: str, p: int, ids, rows) -> int:
         """Refuses ids and rows that do not fit parameter p; returns the rows' stride."""
@@ -717,8 +731,8 @@ class TensorList:
             _refuse(where, f"{self.K} tensors are needed")
         if not isinstance(xs, ctypes.Array):
             for n, b, x in zip(self.elems, self.grad_bytes, xs):
-                if not isinstance(x, int) and not (x.numel() == n and x.is_cuda and x.is_contiguous() and x.element_size() == (size or b)):
-                    _refuse(where, f"a contiguous tensor of {n} elements of {size or b} bytes on the GPU is needed")
+                if not isinstance(x, int) and not (x.numel() == n and x.is_cuda and x.is_contiguous() and _holds(x, size or b)):
+                    _refuse(where, f"a contiguous tensor of {n} elements of {_NAMES[size or b]} on the GPU is needed")
         return xs
 
     @staticmethod

@@ -153,3 +153,25 @@ def test_a_workspace_of_the_host_or_with_gaps_is_refused(tide):
         assert e.value.status == tide.TIDE_EINVAL
     for good in (None, _OnGpu(torch.empty(4096, dtype=torch.uint8)), _OnGpu(torch.empty(64, 16))):
         tide.Group._check_workspace("embedding_grad", good)
+
+
+@pytest.mark.parametrize("size, right, wrong", [(2, (torch.bfloat16, torch.int16, torch.uint16), (torch.float16,)), (4, (torch.float32,), (torch.int32, torch.uint32))], ids=str)
+def test_tensors_of_another_type_of_the_same_size_are_refused(tide, size, right, wrong):
+    g = _Shape(tide, 2, [(7, 4)])
+
+    class List:  # what _tensors looks at of a TensorList
+        elems, K, grad_bytes, _table = [5, 3], 2, [size, size], ctypes.c_void_p * 2
+
+    def calls(dtype):
+        a, b = (_OnGpu(torch.zeros(n, dtype=dtype)) for n in List.elems)
+        return (lambda: tide.Group._check_shards(g, "embedding", [_OnGpu(torch.zeros(g.S, dtype=dtype))] * 2, size),
+                lambda: tide.TensorList._tensors(List, "adamw", [a, b], size), lambda: tide.TensorList._tensors(List, "grad_norm", [a, b]))
+
+    for dtype in right:
+        for f in calls(dtype):
+            f()
+    for dtype in wrong:
+        for f in calls(dtype):
+            with pytest.raises(tide.TideError) as e:
+                f()
+            assert e.value.status == tide.TIDE_EINVAL
