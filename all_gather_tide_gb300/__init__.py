@@ -196,6 +196,29 @@ def _holds(x, size: int) -> bool:
     return x.dtype in _kinds[size]
 
 
+_gpus = 0  # that torch sees, once asked
+
+
+def _current_device() -> int:
+    import torch
+
+    return torch.cuda.current_device()
+
+
+def _elsewhere(*xs) -> bool:
+    """Whether one of the GPU tensors lies on another GPU than the current one (which the C calls compare with the group's).
+    Not asked again once there is found to be no other."""
+    global _gpus
+    if not _gpus:
+        import torch
+
+        _gpus = max(1, torch.cuda.device_count())
+    if _gpus == 1:
+        return False
+    here = _current_device()
+    return any(x.device.index not in (None, here) for x in xs)
+
+
 _current_stream = None  # torch's functions for the current device and its current stream's handle
 
 
@@ -653,7 +676,7 @@ class Group:
     @staticmethod
     def _check_workspace(where: str, x) -> None:
         """Refuses all but a contiguous tensor on the GPU, or None."""
-        if not (x is None or (not isinstance(x, int) and x.is_cuda and x.is_contiguous())):
+        if not (x is None or (not isinstance(x, int) and x.is_cuda and x.is_contiguous() and not (_gpus != 1 and _elsewhere(x)))):
             _refuse(where, "a workspace is a contiguous tensor on the GPU")
 
     def _check_shards(self, where: str, shards, size: int) -> None:
@@ -662,7 +685,7 @@ class Group:
             _refuse(where, f"{self.R} shards are needed")
         if not isinstance(shards, ctypes.Array):
             for x in shards:
-                if not isinstance(x, int) and not (x.is_cuda and _holds(x, size) and x.numel() >= self.S and x.is_contiguous()):
+                if not isinstance(x, int) and not (x.is_cuda and _holds(x, size) and x.numel() >= self.S and x.is_contiguous() and not (_gpus != 1 and _elsewhere(x))):
                     _refuse(where, f"a shard is {self.S} contiguous elements of {_NAMES[size]} on the GPU")
 
     def _check_rows(self, where: str, p: int, ids, rows) -> int:
@@ -670,7 +693,7 @@ class Group:
         if not 0 <= p < self.P:
             _refuse(where, "no such parameter")
         n, length, shape = ids.numel(), self.row_len[p], rows.shape
-        if not (ids.is_contiguous() and ids.is_cuda and rows.is_cuda):
+        if not (ids.is_contiguous() and ids.is_cuda and rows.is_cuda) or (_gpus != 1 and _elsewhere(ids, rows)):
             _refuse(where, "contiguous ids, and rows, on the GPU are needed")
         if shape == (n, length):
             if rows.is_contiguous():
@@ -731,14 +754,14 @@ class TensorList:
             _refuse(where, f"{self.K} tensors are needed")
         if not isinstance(xs, ctypes.Array):
             for n, b, x in zip(self.elems, self.grad_bytes, xs):
-                if not isinstance(x, int) and not (x.numel() == n and x.is_cuda and x.is_contiguous() and _holds(x, size or b)):
+                if not isinstance(x, int) and not (x.numel() == n and x.is_cuda and x.is_contiguous() and _holds(x, size or b) and not (_gpus != 1 and _elsewhere(x))):
                     _refuse(where, f"a contiguous tensor of {n} elements of {_NAMES[size or b]} on the GPU is needed")
         return xs
 
     @staticmethod
     def _scalar(where: str, x, size: int = 4):
         """x, unless it is a tensor that cannot hold one number of `size` bytes on the GPU."""
-        if not (x is None or isinstance(x, int)) and not (x.is_cuda and x.is_floating_point() and x.element_size() == size and x.numel() > 0):
+        if not (x is None or isinstance(x, int)) and not (x.is_cuda and x.is_floating_point() and x.element_size() == size and x.numel() > 0 and not (_gpus != 1 and _elsewhere(x))):
             _refuse(where, f"a floating-point tensor of {size}-byte elements on the GPU is needed")
         return x
 

@@ -175,3 +175,32 @@ def test_tensors_of_another_type_of_the_same_size_are_refused(tide, size, right,
             with pytest.raises(tide.TideError) as e:
                 f()
             assert e.value.status == tide.TIDE_EINVAL
+
+
+class _OnAnotherGpu(_OnGpu):
+    def __getattr__(self, name):
+        return torch.device("cuda", 1) if name == "device" else super().__getattr__(name)
+
+
+def test_tensors_of_another_gpu_are_refused(tide, monkeypatch):
+    """Where there are several, all of a call's lie on the current one, which is the group's."""
+    g, here, there = _Shape(tide, 2, [(7, 4)]), _OnGpu, _OnAnotherGpu
+    ids, x, shard, work = torch.zeros(3, dtype=torch.int64), torch.zeros(3, 4), torch.zeros(g.S), torch.zeros(64)
+
+    class List:
+        elems, K, grad_bytes, _table = [5], 1, [4], ctypes.c_void_p
+
+    calls = [lambda a, b: tide.Group._check_rows(g, "embedding", 0, a(ids), b(x)), lambda a, b: tide.Group._check_shards(g, "embedding", [a(shard), b(shard)], 4),
+             lambda a, b: tide.Group._check_workspace("embedding_grad", (b if a is here else a)(work)),
+             lambda a, b: tide.TensorList._tensors(List, "grad_norm", [(b if a is here else a)(torch.zeros(5))]),
+             lambda a, b: tide.TensorList._scalar("grad_norm", (b if a is here else a)(torch.zeros(1)))]
+    monkeypatch.setattr(tide, "_gpus", 2)
+    monkeypatch.setattr(tide, "_current_device", lambda: 0)
+    for f in calls:
+        f(here, here)
+        for a, b in ((here, there), (there, here)):
+            with pytest.raises(tide.TideError) as e:
+                f(a, b)
+            assert e.value.status == tide.TIDE_EINVAL
+    monkeypatch.setattr(tide, "_current_device", lambda: 1)
+    calls[0](there, there)
