@@ -150,7 +150,7 @@ int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t* n, 
                         bt.start[k + 1] = bt.start[k] + uint32_t(n[b0 + k]);
                         if (n[b0 + k] > 0) dout_vec &= aligned(bt.dout[k], 8 * fsz) && (n[b0 + k] == 1 || bt.stride[k] % int64_t(8 * fsz) == 0);
                     }
-                    if (expanded) TIDE_CUDA(tide::launch_expand_positions(bt, uint32_t(first), tv.rows, w, g->d_status, st));
+                    if (expanded) TIDE_CUDA(tide::launch_expand_positions(bt, uint32_t(first), tv.rows, w, ctas_of(g, tide::kExpandCtasPerSm), g->d_status, st));
                     first += int32_t(bt.start[bt.count]);
                 }
                 if (tide::short_list(total, B)) {
@@ -158,7 +158,7 @@ int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t* n, 
                                                      ctas_of(g, tide::kShortCtasPerSm), g->d_status, st));
                     return TIDE_OK;
                 }
-                TIDE_CUDA(tide::launch_sort_positions(bt, expanded, tv, uint32_t(total), w, g->d_status, st));
+                TIDE_CUDA(tide::launch_sort_positions(bt, expanded, tv, uint32_t(total), w, ctas_of(g, 1), g->d_status, st));
             }
             TIDE_CUDA(tide::launch_sum_positions(sp, tv, uint32_t(total), w, dout_type == TIDE_BF16, dout_vec, scale,
                                                  accumulate != 0, ctas_of(g, tide::kSumCtasPerSm), overlap(g), st));

@@ -70,7 +70,7 @@ struct SortArgs {
 
 __global__ void __launch_bounds__(kThreads) rank_positions_kernel(const __grid_constant__ SortArgs a) {
     extern __shared__ __align__(16) uint32_t rank_keys[];
-    const uint32_t padded = (a.n + 31) & ~31u, first = blockIdx.x * kRankPositions;
+    const uint32_t padded = (a.n + 31) & ~31u;
     wait_for_previous_kernel();
     // what the summing kernel finds cleared: its arrival counters
     for (int64_t q = int64_t(blockIdx.x) * kThreads + threadIdx.x; q < a.counters; q += int64_t(gridDim.x) * kThreads) a.w.arrived[q] = 0;
@@ -100,30 +100,33 @@ __global__ void __launch_bounds__(kThreads) rank_positions_kernel(const __grid_c
         if (bad && !a.expanded && blockIdx.x == 0) atomicCAS(a.status, 0, kStatusBadId);
     }
     __syncthreads();
-    const uint32_t i = first + threadIdx.x / 8, part = threadIdx.x & 7;
-    const uint32_t key = rank_keys[min(i, a.n - 1)];
-    uint32_t place = 0;
-    for (uint32_t v = part; v < padded / 4; v += 8) {
-        const uint4 o = *reinterpret_cast<const uint4*>(&rank_keys[4 * v]);
-        if (v == i / 4) {
-            place += (o.x < key + (4 * v < i)) + (o.y < key + (4 * v + 1 < i)) + (o.z < key + (4 * v + 2 < i)) + (o.w < key);
-        } else {
-            const uint32_t below = key + (v < i / 4);  // of earlier positions, equal rows come before too
-            place += (o.x < below) + (o.y < below) + (o.z < below) + (o.w < below);
+    // as many groups of positions as CTAs, but for a launch that may have few
+    for (uint32_t first = blockIdx.x * kRankPositions; first < a.n; first += gridDim.x * kRankPositions) {
+        const uint32_t i = first + threadIdx.x / 8, part = threadIdx.x & 7;
+        const uint32_t key = rank_keys[min(i, a.n - 1)];
+        uint32_t place = 0;
+        for (uint32_t v = part; v < padded / 4; v += 8) {
+            const uint4 o = *reinterpret_cast<const uint4*>(&rank_keys[4 * v]);
+            if (v == i / 4) {
+                place += (o.x < key + (4 * v < i)) + (o.y < key + (4 * v + 1 < i)) + (o.z < key + (4 * v + 2 < i)) + (o.w < key);
+            } else {
+                const uint32_t below = key + (v < i / 4);  // of earlier positions, equal rows come before too
+                place += (o.x < below) + (o.y < below) + (o.z < below) + (o.w < below);
+            }
         }
-    }
 #pragma unroll
-    for (int m = 4; m > 0; m >>= 1) place += __shfl_xor_sync(0xffffffffu, place, m);
-    if (part == 0 && i < a.n) {
-        uint64_t src;
-        if (a.expanded) {
-            const uint4 x = a.w.pre[i];
-            src = uint64_t(x.y) << 32 | x.x;
-        } else {
-            const int k = batch_of(a.b, i);
-            src = reinterpret_cast<uint64_t>(a.b.dout[k] + int64_t(i - a.b.start[k]) * a.b.stride[k]);
+        for (int m = 4; m > 0; m >>= 1) place += __shfl_xor_sync(0xffffffffu, place, m);
+        if (part == 0 && i < a.n) {
+            uint64_t src;
+            if (a.expanded) {
+                const uint4 x = a.w.pre[i];
+                src = uint64_t(x.y) << 32 | x.x;
+            } else {
+                const int k = batch_of(a.b, i);
+                src = reinterpret_cast<uint64_t>(a.b.dout[k] + int64_t(i - a.b.start[k]) * a.b.stride[k]);
+            }
+            a.w.sorted[place] = make_uint4(uint32_t(src), uint32_t(src >> 32), key, 0);
         }
-        a.w.sorted[place] = make_uint4(uint32_t(src), uint32_t(src >> 32), key, 0);
     }
     let_next_kernel_start();
 }
@@ -984,11 +987,11 @@ size_t grad_workspace_size(const TableView& tv, int64_t n) {
     return most;
 }
 
-cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t rows, const GradWorkspace& w,
+cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t rows, const GradWorkspace& w, int ctas,
                                     int* status, cudaStream_t stream) {
     const uint32_t n = b.start[b.count];
     if (n == 0) return cudaSuccess;
-    const int grid = int(std::min<uint32_t>((n + kThreads - 1) / kThreads, 1024u));
+    const int grid = int(std::min<uint32_t>((n + kThreads - 1) / kThreads, uint32_t(ctas)));
     expand_positions_kernel<<<grid, kThreads, 0, stream>>>(b, first, rows, w.pre, status);
     return cudaGetLastError();
 }
@@ -1024,21 +1027,22 @@ cudaError_t launch_sort(const SortArgs& a, uint32_t ctas, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_sort_positions(const Batches& b, bool expanded, const TableView& tv, uint32_t n,
-                                  const GradWorkspace& w, int* status, cudaStream_t stream) {
+                                  const GradWorkspace& w, int ctas, int* status, cudaStream_t stream) {
     int bits = 0;
     while (tv.rows >> bits) ++bits;  // keys are 0 .. rows
     SortArgs a{b, n, tv.rows, expanded ? 1 : 0, (bits + kSortMaxBits - 1) / kSortMaxBits, plan_grad(tv, n).slots, w, status};
     if (n <= kRankMost)
-        return launch_after(rank_positions_kernel, int((n + kRankPositions - 1) / kRankPositions), kThreads, ((size_t(n) + 31) & ~size_t(31)) * 4, stream, a);
-    uint32_t ctas = 1;
-    while (ctas < kSortMaxCtas && n > ctas * kSortPerCta) ctas <<= 1;
+        return launch_after(rank_positions_kernel, std::min(int((n + kRankPositions - 1) / kRankPositions), ctas), kThreads,
+                            ((size_t(n) + 31) & ~size_t(31)) * 4, stream, a);
+    uint32_t cluster = 1;
+    while (cluster < kSortMaxCtas && 2 * cluster <= uint32_t(ctas) && n > cluster * kSortPerCta) cluster <<= 1;
     static_assert(kSortMinBits == 6 && kSortMaxBits == 10, "one kernel for each digit size");
     switch (std::max(kSortMinBits, (bits + a.passes - 1) / a.passes)) {
-        case 6: return launch_sort<6>(a, ctas, stream);
-        case 7: return launch_sort<7>(a, ctas, stream);
-        case 8: return launch_sort<8>(a, ctas, stream);
-        case 9: return launch_sort<9>(a, ctas, stream);
-        default: return launch_sort<10>(a, ctas, stream);
+        case 6: return launch_sort<6>(a, cluster, stream);
+        case 7: return launch_sort<7>(a, cluster, stream);
+        case 8: return launch_sort<8>(a, cluster, stream);
+        case 9: return launch_sort<9>(a, cluster, stream);
+        default: return launch_sort<10>(a, cluster, stream);
     }
 }
 

@@ -14,6 +14,7 @@ constexpr int kInlineRanks = 64;    // shard pointers that travel with a launch
 constexpr int kInlineBatches = 64;  // batches that travel with a launch
 // CTAs of 256 threads on an SM, as the kernels' registers are bounded for.
 constexpr int kLookupCtasPerSm = 4;
+constexpr int kExpandCtasPerSm = 8;
 constexpr int kSumCtasPerSm = 4;
 constexpr int kShortCtasPerSm = 3;
 
@@ -69,10 +70,11 @@ size_t carve_grad_workspace(char* base, const TableView& tv, int64_t n, GradWork
 // The largest size that up to n positions need.
 size_t grad_workspace_size(const TableView& tv, int64_t n);
 
-cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t rows, const GradWorkspace& w,
+// ctas: the most that a launch may have.
+cudaError_t launch_expand_positions(const Batches& b, uint32_t first, uint32_t rows, const GradWorkspace& w, int ctas,
                                     int* status, cudaStream_t stream);
 cudaError_t launch_sort_positions(const Batches& b, bool expanded, const TableView& tv, uint32_t n,
-                                  const GradWorkspace& w, int* status, cudaStream_t stream);
+                                  const GradWorkspace& w, int ctas, int* status, cudaStream_t stream);
 // dout_vec: every dout row starts on a boundary of 8 elements.
 cudaError_t launch_sum_positions(const ShardPtrs& shards, const TableView& tv, uint32_t n, const GradWorkspace& w,
                                  int dout_bf16, bool dout_vec, float scale, bool accumulate, int ctas, bool overlap,

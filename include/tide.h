@@ -365,7 +365,8 @@ int tide_reduce_scatter_noalloc(int32_t R, int32_t P, const int64_t *rows, const
  * is summed straight into the ranks' fp32 shards, the gradients' global norm is taken over many
  * tensors and bounds them, and AdamW updates the fp32 shards and writes the bf16 shards that the
  * next lookup and all-gather read.  (The paper has no counterpart: its collectives produce and
- * consume these shards.)
+ * consume these shards.)  On a group with TIDE_FLAG_OVERLAP no launch of the embedding calls has more
+ * than sm_count / 9 CTAs; the calls on lists of tensors have no such mode.
  */
 /* Element types of the calls below. */
 #define TIDE_F32 0

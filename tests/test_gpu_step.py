@@ -5,6 +5,7 @@ Bounds are those of fp32 arithmetic with unit roundoff u = 2^-24: a sum of n ter
 The lookup has one rounding of a product (and one to bf16), so it is compared bit for bit.  Every
 buffer has guard bands around it.
 """
+import ctypes
 import math
 
 import pytest
@@ -532,6 +533,53 @@ def test_workspaces_that_do_not_fit_are_refused(tide):
     t.G.embedding_grad(t.p, [ids], [x], shards, workspace=torch.empty(need // 4, device="cuda"))
     want = torch.zeros(500, 64, dtype=torch.float64, device="cuda").index_add_(0, ids, x.double())
     assert torch.equal(torch.stack(shards).double().view(500, 64), want)
+
+
+def launches_of(call):
+    """Grid sizes of the kernels that call(stream) launches, in order: the call is captured into a graph and not run."""
+    cu = ctypes.CDLL("libcuda.so.1")
+
+    class Kernel(ctypes.Structure):  # CUDA_KERNEL_NODE_PARAMS
+        _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3), ("shared", ctypes.c_uint),
+                    ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p), ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+    stream, graph, count, kind, out = torch.cuda.Stream(), ctypes.c_void_p(), ctypes.c_size_t(), ctypes.c_int(), []
+    handle = ctypes.c_void_p(stream.cuda_stream)
+    assert cu.cuStreamBeginCapture_v2(handle, 2) == 0  # relaxed
+    try:
+        call(stream)
+    finally:
+        ended = cu.cuStreamEndCapture(handle, ctypes.byref(graph))
+    assert ended == 0 and cu.cuGraphGetNodes(graph, None, ctypes.byref(count)) == 0
+    nodes = (ctypes.c_void_p * count.value)()
+    assert cu.cuGraphGetNodes(graph, nodes, ctypes.byref(count)) == 0
+    for node in nodes:
+        p = Kernel()
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value == 0 and cu.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0:
+            out.append(p.grid[0])
+    assert cu.cuGraphDestroy(graph) == 0
+    return out
+
+
+@pytest.mark.parametrize("n, batches", [(100, 1), (300, 1), (2048, 1), (20_000, 1), (100, 70), (2000, 70), (60_000, 130)])
+def test_few_ctas_are_kept_by_every_launch(tide, n, batches):
+    """Short lists, counted and sorted ones, and more batches than travel with a launch, under TIDE_FLAG_OVERLAP."""
+    t, g = Table(tide, 4, 3000, 64, 0, tide.TIDE_FLAG_OVERLAP), gen(n)
+    ids, x = draw_ids(g, n, t.rows, 0.1).cuda(), whole_numbers(n, 64, torch.float32, n)
+    shards, work = [torch.zeros(t.S, device="cuda") for _ in range(4)], t.G.embedding_grad_workspace(t.p, n)
+    cuts = [n * k // batches for k in range(batches + 1)]
+    parts = [ids[a:b] for a, b in zip(cuts, cuts[1:])], [x[a:b] for a, b in zip(cuts, cuts[1:])]
+    torch.cuda.synchronize()
+    grids = launches_of(lambda s: t.G.embedding_grad(t.p, *parts, shards, workspace=work, stream=s))
+    few = torch.cuda.get_device_properties(0).multi_processor_count // 9
+    assert len(grids) == (1 if n <= 256 and batches <= 64 else 2 + (-(-batches // 64) if batches > 64 else 0))
+    assert max(grids) <= few, grids
+    out, table = torch.empty(n, 64, device="cuda"), [torch.zeros(t.S, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    looked_up = launches_of(lambda s: t.G.embedding(t.p, table, ids, out, stream=s))
+    assert len(looked_up) == 1 and looked_up[0] <= few
+    for add in (False, True):
+        check_exactly(t, ids, x, add, cuts[1:-1])
 
 
 # ---- lists of tensors ----------------------------------------------------------------------------
