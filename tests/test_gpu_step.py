@@ -582,6 +582,21 @@ def test_few_ctas_are_kept_by_every_launch(tide, n, batches):
         check_exactly(t, ids, x, add, cuts[1:-1])
 
 
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("n, length, piece", [(600, 8, 8), (20_000, 300, 16), (4000, 8192, 32), (140_000, 8, 32), (710_000, 300, 64), (1_500_000, 8, 64)])
+def test_gradient_in_pieces_of_every_length(tide, n, length, piece, add):
+    """A frequent row runs over many pieces and, from 140,000 positions on, over many blocks of pieces; from there on a warp of the
+    sort also takes its positions in several batches.  Sums of whole numbers, so that a position lost or added twice shows."""
+    t, g = Table(tide, 3, 500, length, 5), gen(n)
+    ids, x = draw_ids(g, n, t.rows, 0.05).cuda(), whole_numbers(n, length, torch.bfloat16 if n % 3 else torch.float32, n)
+    shards, work = [torch.zeros(t.S, device="cuda") for _ in range(3)], t.G.embedding_grad_workspace(t.p, n)
+    torch.cuda.synchronize()
+    grids = launches_of(lambda s: t.G.embedding_grad(t.p, [ids], [x], shards, accumulate=True, workspace=work, stream=s))
+    assert grids[-1] == -(-(-(-n // piece) * -(-length // 256)) // 8)  # eight warps to a CTA
+    check_exactly(t, ids, x, add, (n // 3, n // 2))
+    check_exactly(t, torch.where(ids < 0, ids, 7), x, add, (n // 3, n // 2))
+
+
 # ---- lists of tensors ----------------------------------------------------------------------------
 
 LISTS = [(1,), (0, 1, 0), (31, 32, 33), (2047, 2048, 2049, 7), (8, 5, 100_003, 0, 1, 4096), (300_000,), tuple(range(0, 900, 7)), (0,), (0, 0)]
