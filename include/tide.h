@@ -379,7 +379,7 @@ int tide_reduce_scatter_noalloc(int32_t R, int32_t P, const int64_t *rows, const
  *     out[i*out_stride + j] = scale * shard_d[o_p + (t - d*m_p)*L_p + j],  t = ids[i],  d = t / m_p
  * for 0 <= i < n, 0 <= j < L_p, the product in fp32, rounded once to out's type.  An id outside
  * [0, rows_p) reads nothing and gives a row of +0 (a negative id marks a position without a token;
- * an id >= rows_p also sets 64 in the group's device status word).  One token (n = 1) up to long
+ * an id >= rows_p also sets 64 in the group's device status word, if that holds 0).  One token (n = 1) up to long
  * prompts take the same call; n = 0 does nothing.
  *   shards: host array of R device pointers, entry d = rank d's packed bf16 shard (S elements).  Up
  *           to 64 ranks they travel with the launch, so the call can be captured into a CUDA graph;
@@ -469,7 +469,8 @@ int tide_grad_norm(tide_tensors_t t, const void *const *grads, float *norm, doub
  * tide_clip_grads — scales every gradient in place by c = min(1, max_norm / (norm[0] + 1e-6)), c in
  * fp32, products in fp32 rounded once to the gradient's type.  The norm is read on the device, so
  * nothing waits for the host.  With c = 1 nothing is written; a NaN norm makes every gradient NaN
- * and an infinite one makes them 0 (NaN where they were infinite or NaN).  max_norm >= 0.
+ * and an infinite one makes them 0 (NaN where they were infinite or NaN).  max_norm >= 0; an infinite
+ * one bounds nothing, and with an infinite norm c is their quotient, NaN.
  */
 int tide_clip_grads(tide_tensors_t t, void *const *grads, const float *norm, float max_norm, void *stream);
 

@@ -693,6 +693,14 @@ def test_clip_by_a_norm_that_is_not_finite(tide):
     assert all(bool(d.cpu().isnan().all()) for d in dev)
 
 
+def test_clip_by_a_bound_that_is_infinite(tide):
+    """Nothing is scaled, unless the norm is infinite too: the factor is then a quotient of infinities."""
+    for value, nan in ((3.0, False), (float("inf"), True)):
+        T, host, dev = make_list(tide, (100, 3000), "mixed", 5)
+        T.clip_grads([d.view for d in dev], torch.full((1,), value, device="cuda"), float("inf"))
+        assert all(bool(d.cpu().isnan().all()) if nan else torch.equal(d.cpu(), x) for x, d in zip(host, dev))
+
+
 def check_adamw(p, g, m, v, c, lr, b1, b2, eps, wd, step, got):
     """got: (param, exp_avg, exp_avg_sq, shard or None) against 64 bits."""
     p, g, m, v = (x.double() for x in (p, g, m, v))
