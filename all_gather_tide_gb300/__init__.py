@@ -183,17 +183,16 @@ def _dtype_code(x) -> int:
 
 
 _NAMES = {2: "bf16", 4: "fp32"}
-_kinds = {}  # bytes of an element -> the types that hold it
+_held = {}
 
 
-def _holds(x, size: int) -> bool:
-    """Whether x holds numbers of ``size`` bytes as the kernels read them: fp32, or bf16, also as the 16-bit integers of
-    its bits."""
-    if not _kinds:
+def _held_as() -> dict:
+    """Bytes of an element -> the types that hold it: fp32, or bf16, also as the 16-bit integers of its bits."""
+    if not _held:
         import torch
 
-        _kinds.update({4: (torch.float32,), 2: (torch.bfloat16, torch.int16, torch.uint16)})
-    return x.dtype in _kinds[size]
+        _held.update({4: (torch.float32,), 2: (torch.bfloat16, torch.int16, torch.uint16)})
+    return _held
 
 
 _gpus = 0  # that torch sees, once asked
@@ -684,8 +683,9 @@ class Group:
         if len(shards) != self.R:
             _refuse(where, f"{self.R} shards are needed")
         if not isinstance(shards, ctypes.Array):
+            types = _held_as()[size]
             for x in shards:
-                if not isinstance(x, int) and not (x.is_cuda and _holds(x, size) and x.numel() >= self.S and x.is_contiguous() and not (_gpus != 1 and _elsewhere(x))):
+                if not isinstance(x, int) and not (x.is_cuda and x.dtype in types and x.numel() >= self.S and x.is_contiguous() and not (_gpus != 1 and _elsewhere(x))):
                     _refuse(where, f"a shard is {self.S} contiguous elements of {_NAMES[size]} on the GPU")
 
     def _check_rows(self, where: str, p: int, ids, rows) -> int:
@@ -753,8 +753,9 @@ class TensorList:
         if len(xs) != self.K:
             _refuse(where, f"{self.K} tensors are needed")
         if not isinstance(xs, ctypes.Array):
+            types = _held_as()
             for n, b, x in zip(self.elems, self.grad_bytes, xs):
-                if not isinstance(x, int) and not (x.numel() == n and x.is_cuda and x.is_contiguous() and _holds(x, size or b) and not (_gpus != 1 and _elsewhere(x))):
+                if not isinstance(x, int) and not (x.numel() == n and x.is_cuda and x.is_contiguous() and x.dtype in types[size or b] and not (_gpus != 1 and _elsewhere(x))):
                     _refuse(where, f"a contiguous tensor of {n} elements of {_NAMES[size or b]} on the GPU is needed")
         return xs
 

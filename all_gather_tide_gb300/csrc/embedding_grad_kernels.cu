@@ -53,7 +53,7 @@ expand_positions_kernel(const __grid_constant__ Batches b, uint32_t first, uint3
 // Sort of up to kRankMost positions: a position's place is the number of positions that come before it, of
 // smaller rows or earlier with the same row.  Every CTA has all rows in shared memory and places
 // kRankPositions of them, eight lanes to a position.  n^2 comparisons, but no passes and no barriers between
-// CTAs: a gradient of 257, 1024 and 2048 positions takes 10.2, 15.3 and 18.3 us with this sort and 16.8, 21.9 and
+// CTAs: a gradient of 257, 1024 and 2048 positions takes 10.2, 15.2 and 18.8 us with this sort and 16.8, 21.9 and
 // 24.7 with the one below (rows of 4096 columns); at 4096 positions it is 26.0 against 29.6, but 24.0 against 22.4
 // where rows are short, and beyond it loses.
 constexpr uint32_t kRankMost = 2048;

@@ -379,8 +379,8 @@ int tide_reduce_scatter_noalloc(int32_t R, int32_t P, const int64_t *rows, const
  *     out[i*out_stride + j] = scale * shard_d[o_p + (t - d*m_p)*L_p + j],  t = ids[i],  d = t / m_p
  * for 0 <= i < n, 0 <= j < L_p, the product in fp32, rounded once to out's type.  An id outside
  * [0, rows_p) reads nothing and gives a row of +0 (a negative id marks a position without a token;
- * an id >= rows_p also sets 64 in the group's device status word, if that holds 0).  One token (n = 1) up to long
- * prompts take the same call; n = 0 does nothing.
+ * an id >= rows_p also sets 64 in the group's device status word, if that holds 0).  One token (n = 1)
+ * up to long prompts take the same call; n = 0 does nothing.
  *   shards: host array of R device pointers, entry d = rank d's packed bf16 shard (S elements).  Up
  *           to 64 ranks they travel with the launch, so the call can be captured into a CUDA graph;
  *           beyond, a stream that is being captured is refused.
