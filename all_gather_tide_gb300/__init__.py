@@ -10,7 +10,8 @@ fails loudly if the library has not been built.
 NVSwitch" (arXiv 2610.38228): the reduce-scatter is its TIDE-RS (abstract; Fig. 2b), the
 placement its TIDE-AG landing (abstract; Fig. 5b), the layout its Table 2.  Between the two, the
 rest of a training step runs on the same shards: embedding lookup and gradient, the gradients' norm and
-clipping, AdamW.
+clipping, AdamW; and a layer of experts between the two: tokens to their experts and back, and products in
+8-bit floating point with weights read from the shards and gradients written for the reduce-scatter.
 """
 from __future__ import annotations
 
@@ -48,6 +49,8 @@ TIDE_I64 = 3
 TIDE_SHORT_POSITIONS = 256
 TIDE_SHORT_BATCHES = 64
 TIDE_ADAMW_SKIP_NONFINITE = 0x1
+TIDE_MAX_EXPERTS = 1024
+TIDE_MAX_CHOICES = 32
 
 _lib = None
 _i64p = ctypes.POINTER(ctypes.c_int64)
@@ -55,6 +58,16 @@ _i32p = ctypes.POINTER(ctypes.c_int32)
 _f32p = ctypes.POINTER(ctypes.c_float)
 _vp = ctypes.c_void_p
 _vpp = ctypes.POINTER(ctypes.c_void_p)
+
+
+class _Fp8(ctypes.Structure):
+    """tide_fp8_t"""
+
+    _fields_ = [("codes", ctypes.c_void_p), ("stride", ctypes.c_int64), ("batch", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("scale_stride", ctypes.c_int64), ("scale_batch", ctypes.c_int64)]
+
+
+_fp8p = ctypes.POINTER(_Fp8)
 
 # name -> (restype, argtypes); every symbol declared in include/tide.h
 SIGNATURES = {
@@ -107,6 +120,28 @@ SIGNATURES = {
     "tide_adamw": (ctypes.c_int, [_vp, _vpp, _vpp, _vpp, _vpp, _vpp, _f32p, ctypes.c_double, ctypes.c_double,
                                   ctypes.c_double, ctypes.c_double, ctypes.c_int64, _vp, ctypes.c_float, ctypes.c_uint32,
                                   _vp]),
+    "tide_experts_create": (ctypes.c_int, [_vpp, ctypes.c_int32, ctypes.c_int32, ctypes.c_uint32]),
+    "tide_experts_destroy": (ctypes.c_int, [_vp]),
+    "tide_experts_device_status": (ctypes.c_int, [_vp, _i32p]),
+    "tide_experts_set_wait_timeout": (ctypes.c_int, [_vp, ctypes.c_uint64]),
+    "tide_experts_sort_workspace": (ctypes.c_int, [_vp, ctypes.c_int64, _i64p]),
+    "tide_experts_sort": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, ctypes.c_int64, _vp, _vp, _vp, _vp, ctypes.c_int64, _vp]),
+    "tide_experts_dispatch": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp, _vp,
+                                             ctypes.c_int64, _vp]),
+    "tide_experts_dispatch_fp8": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp, _fp8p,
+                                                 _vp]),
+    "tide_experts_combine": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp, _vp, _vp,
+                                            ctypes.c_int64, _vp]),
+    "tide_experts_combine_grad": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, ctypes.c_int64, _vp, ctypes.c_int64, ctypes.c_int64,
+                                                 ctypes.c_int64, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp]),
+    "tide_fp8_padded_rows": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, _i64p]),
+    "tide_experts_quantize": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                             _vp, _vp, _fp8p, _fp8p, _vp]),
+    "tide_all_gather_fp8": (ctypes.c_int, [_vp, ctypes.c_int32, _i32p, _vpp, _fp8p, _fp8p, _vp]),
+    "tide_experts_matmul": (ctypes.c_int, [_vp, _fp8p, ctypes.c_int64, _vp, _fp8p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _vp,
+                                           ctypes.c_int32, ctypes.c_int64, _vp]),
+    "tide_experts_weight_grad": (ctypes.c_int, [_vp, _fp8p, _fp8p, ctypes.c_int64, _vp, ctypes.c_int64, ctypes.c_int64, _vpp,
+                                                ctypes.c_int32, _vp]),
     "tide_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "tide_last_cuda_error": (ctypes.c_int, []),
     "tide_version": (ctypes.c_int, []),
@@ -533,6 +568,104 @@ def tide_adamw(t: int, params: Sequence, grads: Sequence, exp_avg: Sequence, exp
                             None if norm is None else _ptr(norm), max_norm, flags, _stream(stream)), "tide_adamw")
 
 
+# ---- a layer of experts --------------------------------------------------------------------------
+
+
+def tide_experts_create(E: int, k: int, flags: int = 0) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().tide_experts_create(ctypes.byref(h), E, k, flags), "tide_experts_create")
+    return h.value
+
+
+def tide_experts_destroy(x: int) -> None:
+    _check(lib().tide_experts_destroy(x), "tide_experts_destroy")
+
+
+def tide_experts_device_status(x: int) -> int:
+    v = ctypes.c_int32()
+    _check(lib().tide_experts_device_status(x, ctypes.byref(v)), "tide_experts_device_status")
+    return v.value
+
+
+def tide_experts_set_wait_timeout(x: int, timeout_ns: int) -> None:
+    _check(lib().tide_experts_set_wait_timeout(x, timeout_ns), "tide_experts_set_wait_timeout")
+
+
+def tide_experts_sort_workspace(x: int, T: int) -> int:
+    v = ctypes.c_int64()
+    _check(lib().tide_experts_sort_workspace(x, T, ctypes.byref(v)), "tide_experts_sort_workspace")
+    return v.value
+
+
+def _address(x) -> Optional[int]:
+    return None if x is None else x.data_ptr()
+
+
+def tide_experts_sort(x: int, ids, T: int, offsets, slots, tokens, workspace=None, stream=None) -> None:
+    """``ids``: contiguous int32 or int64 tensor of T*k ids; ``offsets``, ``slots``, ``tokens``: int32 tensors; ``workspace``: contiguous
+    tensor of ``tide_experts_sort_workspace`` bytes, or None where that is 0."""
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().tide_experts_sort(x, ids.data_ptr(), _dtype_code(ids), T, offsets.data_ptr(), slots.data_ptr(), tokens.data_ptr(), _address(workspace), size,
+                                   _stream(stream)), "tide_experts_sort")
+
+
+def tide_experts_dispatch(x: int, src, slots, rows, stream=None) -> None:
+    """``src``: T rows of bf16 or fp32; ``rows``: T*k of the same type; both 2-D, their rows contiguous."""
+    _check(lib().tide_experts_dispatch(x, src.data_ptr(), _dtype_code(src), _row_stride(src), src.shape[0], src.shape[1], slots.data_ptr(), rows.data_ptr(),
+                                       _row_stride(rows), _stream(stream)), "tide_experts_dispatch")
+
+
+def tide_experts_dispatch_fp8(x: int, src, slots, rows, stream=None) -> None:
+    """``rows``: an ``Fp8Rows``."""
+    _check(lib().tide_experts_dispatch_fp8(x, src.data_ptr(), _dtype_code(src), _row_stride(src), src.shape[0], src.shape[1], slots.data_ptr(), rows.c,
+                                           _stream(stream)), "tide_experts_dispatch_fp8")
+
+
+def tide_experts_combine(x: int, rows, slots, weights, out, stream=None) -> None:
+    """``weights``: T*k contiguous fp32, or None for 1."""
+    _check(lib().tide_experts_combine(x, rows.data_ptr(), _dtype_code(rows), _row_stride(rows), out.shape[0], out.shape[1], slots.data_ptr(), _address(weights),
+                                      out.data_ptr(), _row_stride(out), _stream(stream)), "tide_experts_combine")
+
+
+def tide_experts_combine_grad(x: int, dout, rows, slots, weights, drows, dweights, stream=None) -> None:
+    _check(lib().tide_experts_combine_grad(x, dout.data_ptr(), _dtype_code(dout), _row_stride(dout), rows.data_ptr(), _row_stride(rows), dout.shape[0],
+                                           dout.shape[1], slots.data_ptr(), weights.data_ptr(), drows.data_ptr(), _row_stride(drows), dweights.data_ptr(),
+                                           _stream(stream)), "tide_experts_combine_grad")
+
+
+def tide_fp8_padded_rows(M: int, E: int) -> int:
+    v = ctypes.c_int64()
+    _check(lib().tide_fp8_padded_rows(M, E, ctypes.byref(v)), "tide_fp8_padded_rows")
+    return v.value
+
+
+def tide_experts_quantize(x: int, src, M: int, offsets, tokens=None, rows=None, columns=None, stream=None) -> None:
+    """``rows``: an ``Fp8Rows`` or None; ``columns``: an ``Fp8Columns`` or None; ``tokens``: which row of ``src`` each is, or None."""
+    _check(lib().tide_experts_quantize(x, src.data_ptr(), _dtype_code(src), _row_stride(src), src.shape[0], M, src.shape[1], _address(offsets), _address(tokens),
+                                       None if rows is None else rows.c, None if columns is None else columns.c, _stream(stream)), "tide_experts_quantize")
+
+
+def tide_all_gather_fp8(g: int, ps, shards: Sequence, w, stream=None) -> None:
+    """``ps``: the parameters' indexes; ``w``: an ``Fp8Weights``."""
+    if not isinstance(ps, ctypes.Array):
+        ps = (ctypes.c_int32 * len(ps))(*ps)
+    _check(lib().tide_all_gather_fp8(g, len(ps), ps, _ptr_array(shards), w.c, w.c_transposed, _stream(stream)), "tide_all_gather_fp8")
+
+
+def tide_experts_matmul(x: int, a, offsets, w, out, transposed: bool = False, stream=None) -> None:
+    """``a``: an ``Fp8Rows``; ``w``: an ``Fp8Weights``; ``out``: bf16 or fp32 rows."""
+    N, K = (w.K, w.N) if transposed else (w.N, w.K)
+    codes = w.c_transposed if transposed else w.c
+    _check(lib().tide_experts_matmul(x, a.c, a.M, _address(offsets), codes, transposed, N, K, out.data_ptr(), _dtype_code(out), _row_stride(out), _stream(stream)),
+           "tide_experts_matmul")
+
+
+def tide_experts_weight_grad(x: int, dy, a, offsets, grads, grad_type: int = TIDE_BF16, stream=None) -> None:
+    """``dy``, ``a``: ``Fp8Columns``; ``grads``: E tensors or the ``pointer_table`` of them."""
+    _check(lib().tide_experts_weight_grad(x, dy.c, a.c, dy.M, _address(offsets), dy.len, a.len, _ptr_array(grads), grad_type, _stream(stream)),
+           "tide_experts_weight_grad")
+
+
 def _refuse(where: str, what: str) -> None:
     raise TideError(TIDE_EINVAL, f"{where}: {what}")
 
@@ -705,6 +838,19 @@ class Group:
             return length
         _refuse(where, f"{n} rows of {length} elements, contiguous or a row stride apart, are needed")
 
+    def all_gather_fp8(self, ps: Sequence[int], shards: Sequence, w: "Fp8Weights", stream=None) -> None:
+        """All-gather placement in 8 bits: the parameters ``ps``, all of one shape, read from the R bf16 ``shards`` as the experts'
+        matrices of ``w`` (and their transposes, where ``w`` has them)."""
+        where = "all_gather_fp8"
+        if type(shards) is not self._table:
+            self._check_shards(where, shards, 2)
+        if not isinstance(w, Fp8Weights) or len(ps) != w.E or (_gpus != 1 and _elsewhere(w.codes)):
+            _refuse(where, "one parameter is needed for each matrix of an Fp8Weights on this GPU")
+        for p in ps:
+            if not 0 <= p < self.P or (self.rows[p], self.row_len[p]) != (w.N, w.K):
+                _refuse(where, f"a parameter of {w.N} rows of {w.K} elements is needed")
+        tide_all_gather_fp8(self.handle, ps, shards, w, stream)
+
     def pieces(self, buffers: Sequence) -> list:
         """The valid rows of every (rank, parameter) piece of R shard buffers, as R*P views in the order
         d*P + p: the tensors of a ``TensorList`` over the group's shards."""
@@ -795,3 +941,267 @@ class TensorList:
         if weight_decay is not None and len(weight_decay) != self.K:
             _refuse(where, f"{self.K} weight decays are needed")
         tide_adamw(self.handle, params, grads, exp_avg, exp_avg_sq, shards, weight_decay=weight_decay, stream=stream, **hyper)
+
+
+# ---- a layer of experts --------------------------------------------------------------------------
+
+
+def _fp8_struct(codes, scales, batch: int = 0, scale_batch: int = 0):
+    return _Fp8(codes.data_ptr(), codes.stride(-2), batch, scales.data_ptr(), scales.stride(-2), scale_batch)
+
+
+def _up(n: int, to: int) -> int:
+    return -(-n // to) * to
+
+
+def _bytes_as_e4m3(*shape):
+    import torch
+
+    return torch.empty(*shape, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+
+
+class Fp8Rows:
+    """M rows of ``len`` e4m3 ``codes`` and their fp32 ``scales``, one for each block of 128 columns: what
+    ``dispatch_fp8`` and ``quantize`` write and ``matmul`` reads.  The value is ``codes[s, c] * scales[s, c // 128]``."""
+
+    def __init__(self, M: int, len: int):
+        import torch
+
+        self.M, self.len = M, len
+        self.codes = _bytes_as_e4m3(M, _up(len, 16))[:, :len]
+        self.scales = torch.empty(M, -(-len // 128), device="cuda")
+        self.c = _fp8_struct(self.codes, self.scales)
+
+
+class Fp8Columns:
+    """The transposed form of M rows of ``len`` columns in the order of E experts: ``len`` rows of ``codes`` in which each expert's
+    rows begin at a multiple of 128, and the ``scales`` of their blocks of 128, [block, column]: what ``quantize`` writes and
+    ``weight_grad`` reads."""
+
+    def __init__(self, M: int, len: int, E: int):
+        import torch
+
+        self.M, self.len, self.E = M, len, E
+        padded = max(128, tide_fp8_padded_rows(M, E))
+        self.codes = _bytes_as_e4m3(len, padded)
+        self.scales = torch.empty(padded // 128, len, device="cuda")
+        self.c = _fp8_struct(self.codes, self.scales)
+
+
+class Fp8Weights:
+    """E matrices of N rows of K e4m3 ``codes`` ([E, N, K]) and their fp32 ``scales`` ([E, ceil(N / 128), ceil(K / 128)], one for each
+    block of 128 x 128), and, with ``transposed``, the same codes transposed (``codes_transposed``, [E, K, N]) for products
+    with the transposed matrices.  ``Group.all_gather_fp8`` writes them; a checkpoint's can be copied into them."""
+
+    def __init__(self, E: int, N: int, K: int, transposed: bool = False):
+        import torch
+
+        codes = _bytes_as_e4m3(E, N, _up(K, 16))[:, :, :K]
+        scales = torch.empty(E, -(-N // 128), -(-K // 128), device="cuda")
+        self._hold(codes, scales, _bytes_as_e4m3(E, K, _up(N, 16))[:, :, :N] if transposed else None)
+
+    def _hold(self, codes, scales, codes_transposed) -> None:
+        self.E, self.N, self.K = codes.shape
+        self.codes, self.scales, self.codes_transposed = codes, scales, codes_transposed
+        self.c = _fp8_struct(codes, scales, codes.stride(0), scales.stride(0))
+        self.c_transposed = None
+        if codes_transposed is not None:
+            self.c_transposed = _fp8_struct(codes_transposed, scales, codes_transposed.stride(0), scales.stride(0))
+
+    def part(self, first: int, rows: int) -> "Fp8Weights":
+        """Rows ``first`` to ``first + rows`` of every matrix, in place: several parameters side by side in one product.  Both are
+        multiples of 128, but the rows of the last part."""
+        if first < 0 or rows < 1 or first % 128 or first + rows > self.N or (rows % 128 and first + rows != self.N):
+            _refuse("part", "whole blocks of 128 rows are needed")
+        end, w = first + rows, Fp8Weights.__new__(Fp8Weights)
+        t = self.codes_transposed
+        w._hold(self.codes[:, first:end], self.scales[:, first // 128:-(-end // 128)], None if t is None else t[:, :, first:end])
+        return w
+
+
+class Route:
+    """The order of T tokens' pairs: ``offsets`` [E + 1], ``slots`` [T, k] and ``tokens`` [T*k], int32, as ``Experts.sort`` writes them."""
+
+    def __init__(self, experts: "Experts", T: int):
+        import torch
+
+        self.T, self.E, self.k = T, experts.E, experts.k
+        self.M = T * experts.k
+        self.offsets = torch.zeros(experts.E + 1, dtype=torch.int32, device="cuda")
+        self.slots = torch.full((T, experts.k), -1, dtype=torch.int32, device="cuda")
+        self.tokens = torch.full((self.M,), -1, dtype=torch.int32, device="cuda")
+        size = tide_experts_sort_workspace(experts.handle, T)
+        self.workspace = torch.empty(size, dtype=torch.uint8, device="cuda") if size else None
+
+
+class Experts:
+    """Owns one ``tide_experts_t``: E experts, k choices a token."""
+
+    def __init__(self, E: int, k: int, flags: int = 0):
+        self.E, self.k = E, k
+        self._table = ctypes.c_void_p * E  # the type of a pointer_table of E gradients
+        self.handle = None
+        self.handle = tide_experts_create(E, k, flags)
+
+    def close(self) -> None:
+        if self.handle:
+            tide_experts_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def device_status(self) -> int:
+        return tide_experts_device_status(self.handle)
+
+    def set_wait_timeout(self, timeout_ns: int) -> None:
+        tide_experts_set_wait_timeout(self.handle, timeout_ns)
+
+    def route(self, T: int) -> Route:
+        """Buffers for the order of T tokens."""
+        return Route(self, T)
+
+    # ---- order, rows there and back ----
+
+    def sort(self, ids, route: Route, stream=None) -> None:
+        """The experts' order of the pairs with ``ids`` ([T, k], int32 or int64; negative: no expert) into ``route``."""
+        where = "sort"
+        self._check_route(where, route)
+        if not (ids.is_cuda and ids.is_contiguous() and ids.numel() == route.M) or (_gpus != 1 and _elsewhere(ids)):
+            _refuse(where, f"{route.M} contiguous ids on the GPU are needed")
+        tide_experts_sort(self.handle, ids, route.T, route.offsets, route.slots, route.tokens, route.workspace, stream)
+
+    def dispatch(self, x, route: Route, rows, stream=None) -> None:
+        """The tokens' rows ``x`` ([T, D], bf16 or fp32) into ``rows`` ([T*k, D]) in the experts' order."""
+        where = "dispatch"
+        self._check_route(where, route)
+        self._check_rows(where, x, route.T, x.shape[-1])
+        self._check_rows(where, rows, route.M, x.shape[-1], x.dtype)
+        tide_experts_dispatch(self.handle, x, route.slots, rows, stream)
+
+    def dispatch_fp8(self, x, route: Route, rows: Fp8Rows, stream=None) -> None:
+        """The same into 8-bit ``rows``."""
+        where = "dispatch_fp8"
+        self._check_route(where, route)
+        self._check_rows(where, x, route.T, x.shape[-1])
+        self._check_fp8(where, rows, Fp8Rows, route.M, x.shape[-1])
+        tide_experts_dispatch_fp8(self.handle, x, route.slots, rows, stream)
+
+    def combine(self, rows, route: Route, out, weights=None, stream=None) -> None:
+        """The experts' ``rows`` ([T*k, D]) back at their tokens, ``out`` ([T, D]), summed with ``weights`` ([T, k] fp32; None: 1, the
+        gradient of ``dispatch``)."""
+        where = "combine"
+        self._check_route(where, route)
+        self._check_rows(where, rows, route.M, rows.shape[-1])
+        self._check_rows(where, out, route.T, rows.shape[-1], rows.dtype)
+        if weights is not None:
+            self._check_weights(where, weights, route)
+        tide_experts_combine(self.handle, rows, route.slots, weights, out, stream)
+
+    def combine_grad(self, dout, rows, route: Route, weights, drows, dweights, stream=None) -> None:
+        """The gradients of ``combine`` with ``weights``, into ``drows`` and ``dweights``."""
+        where = "combine_grad"
+        self._check_route(where, route)
+        self._check_rows(where, dout, route.T, dout.shape[-1])
+        for x in (rows, drows):
+            self._check_rows(where, x, route.M, dout.shape[-1], dout.dtype)
+        for x in (weights, dweights):
+            self._check_weights(where, x, route)
+        tide_experts_combine_grad(self.handle, dout, rows, route.slots, weights, drows, dweights, stream)
+
+    # ---- products in 8 bits ----
+
+    def quantize(self, x, route: Optional[Route], rows: Optional[Fp8Rows] = None, columns: Optional[Fp8Columns] = None, gather: bool = False,
+                 stream=None) -> None:
+        """Rows in the experts' order in 8 bits: ``x`` ([T*k, D]), or with ``gather`` the tokens' rows ``x`` ([T, D]), as they are
+        and/or transposed.  ``route`` may be None where one expert has all rows."""
+        where = "quantize"
+        M = self._check_all_rows(where, route, x.shape[0])
+        if gather and route is None:
+            _refuse(where, "gathering needs a route")
+        self._check_rows(where, x, route.T if gather else M, x.shape[-1])
+        if rows is not None:
+            self._check_fp8(where, rows, Fp8Rows, M, x.shape[-1])
+        if columns is not None:
+            self._check_fp8(where, columns, Fp8Columns, M, x.shape[-1])
+        tide_experts_quantize(self.handle, x, M, None if route is None else route.offsets, route.tokens if gather else None, rows, columns, stream)
+
+    def matmul(self, a: Fp8Rows, w: Fp8Weights, route: Optional[Route], out, transposed: bool = False, stream=None) -> None:
+        """Every expert's rows of ``a`` times its matrix of ``w``: ``out[s] = w[e] @ a[s]`` ([T*k, N], bf16 or fp32), or with ``transposed``
+        ``w[e].T @ a[s]`` ([T*k, K])."""
+        where = "matmul"
+        if not isinstance(w, Fp8Weights) or w.E != self.E or (transposed and w.c_transposed is None) or (_gpus != 1 and _elsewhere(w.codes)):
+            _refuse(where, f"the Fp8Weights of {self.E} experts on this GPU are needed, with transposed codes for a transposed product")
+        N, K = (w.K, w.N) if transposed else (w.N, w.K)
+        M = self._check_all_rows(where, route, a.M)
+        self._check_fp8(where, a, Fp8Rows, M, K)
+        self._check_rows(where, out, M, N)
+        tide_experts_matmul(self.handle, a, None if route is None else route.offsets, w, out, transposed, stream)
+
+    def weight_grad(self, dy: Fp8Columns, a: Fp8Columns, route: Optional[Route], grads, grad_type: int = TIDE_BF16, stream=None) -> None:
+        """The gradient of every expert's matrix, ``dy[e].T @ a[e]``, into ``grads``: E contiguous tensors of N*K elements, bf16 or
+        fp32, one tensor [E, N, K], or the ``pointer_table`` of E tensors of ``grad_type``."""
+        where = "weight_grad"
+        M = self._check_all_rows(where, route, dy.M)
+        self._check_fp8(where, dy, Fp8Columns, M, dy.len)
+        self._check_fp8(where, a, Fp8Columns, M, a.len)
+        if type(grads) is not self._table:
+            if isinstance(grads, ctypes.Array) or len(grads) != self.E:
+                _refuse(where, f"{self.E} gradients are needed")
+            grad_type = _dtype_code(grads[0])
+            if grad_type not in (TIDE_F32, TIDE_BF16):
+                _refuse(where, "gradients are bf16 or fp32")
+            if isinstance(grads, (list, tuple)):
+                for g in grads:
+                    if not (g.is_cuda and g.dtype is grads[0].dtype and g.is_contiguous() and g.numel() == dy.len * a.len) or (_gpus != 1 and _elsewhere(g)):
+                        _refuse(where, f"contiguous gradients of {dy.len} x {a.len} elements of one type on the GPU are needed")
+                grads = _ptr_array(grads)
+            else:
+                if not (grads.is_cuda and grads.is_contiguous() and grads.numel() == self.E * dy.len * a.len) or (_gpus != 1 and _elsewhere(grads)):
+                    _refuse(where, f"a contiguous gradient of {self.E} x {dy.len} x {a.len} elements on the GPU is needed")
+                first, each = grads.data_ptr(), dy.len * a.len * grads.element_size()
+                grads = self._table(*range(first, first + self.E * each, each))
+        tide_experts_weight_grad(self.handle, dy, a, None if route is None else route.offsets, grads, grad_type, stream)
+
+    # ---- checks ----
+
+    def _check_route(self, where: str, route) -> None:
+        if not isinstance(route, Route) or route.E != self.E or route.k != self.k or (_gpus != 1 and _elsewhere(route.offsets)):
+            _refuse(where, f"a route of {self.E} experts and {self.k} choices on this GPU is needed")
+
+    def _check_all_rows(self, where: str, route, M: int) -> int:
+        """The rows of a product: the route's, or without one all M of one expert."""
+        if route is not None:
+            self._check_route(where, route)
+            return route.M
+        if self.E != 1:
+            _refuse(where, "several experts need a route")
+        return M
+
+    @staticmethod
+    def _check_rows(where: str, x, n: int, length: int, dtype=None) -> None:
+        """Refuses all but n rows of `length` contiguous bf16 or fp32 elements on the GPU that do not overlap."""
+        if not (x.is_cuda and x.dim() == 2 and tuple(x.shape) == (n, length) and length > 0) or (_gpus != 1 and _elsewhere(x)):
+            _refuse(where, f"{n} rows of {length} elements on the GPU are needed")
+        if _dtype_code(x) not in (TIDE_F32, TIDE_BF16) or (dtype is not None and x.dtype is not dtype):
+            _refuse(where, "rows are bf16 or fp32, and of one type in a call")
+        if not x.is_contiguous() and not ((length == 1 or x.stride(1) == 1) and (n <= 1 or x.stride(0) >= length)):
+            _refuse(where, "rows are contiguous, or a row stride apart")
+
+    @staticmethod
+    def _check_weights(where: str, x, route: Route) -> None:
+        if not (x.is_cuda and _dtype_code(x) == TIDE_F32 and x.is_contiguous() and x.numel() == route.M) or (_gpus != 1 and _elsewhere(x)):
+            _refuse(where, f"{route.M} contiguous fp32 weights on the GPU are needed")
+
+    def _check_fp8(self, where: str, x, kind, M: int, length: int) -> None:
+        if not isinstance(x, kind) or x.M != M or x.len != length or (kind is Fp8Columns and x.E != self.E) or (_gpus != 1 and _elsewhere(x.codes)):
+            _refuse(where, f"{kind.__name__} of {M} rows of {length} elements on this GPU are needed")

@@ -1,8 +1,10 @@
-// C ABI of the embedding lookup and gradient over a group's shards: argument checks and launches.
+// C ABI of the embedding lookup and gradient over a group's shards, and of the placement of its parameters in 8 bits:
+// argument checks and launches.
 #include <algorithm>
 #include <vector>
 
 #include "api_common.h"
+#include "experts.h"
 #include "group.h"
 #include "step_internal.h"
 
@@ -164,6 +166,42 @@ int tide_embedding_grad(tide_group_t g, int32_t p, int32_t B, const int64_t* n, 
                                                  accumulate != 0, ctas_of(g, tide::kSumCtasPerSm), overlap(g), st));
             return TIDE_OK;
         }());
+    });
+}
+
+int tide_all_gather_fp8(tide_group_t g, int32_t E, const int32_t* ps, const void* const* shards, const tide_fp8_t* w, const tide_fp8_t* wt, void* stream) {
+    return no_throw([&]() -> int {
+        if (!g || !ps || !shards || !w || E < 1 || E > TIDE_MAX_EXPERTS) return TIDE_EINVAL;
+        tide::TableView tv;
+        tide::ExpertParams params{};
+        for (int e = 0; e < E; ++e) {
+            const int rc = table_view(g, ps[e], &tv);
+            if (rc != TIDE_OK) return rc;
+            if (g->plan.rows[ps[e]] != g->plan.rows[ps[0]] || g->plan.row_len[ps[e]] != g->plan.row_len[ps[0]]) return TIDE_EINVAL;
+            params.off[e] = tv.off;
+        }
+        const int64_t N = tv.rows, K = tv.len;
+        auto extent = [](int64_t n, int64_t each) {
+            int64_t v;
+            return !__builtin_mul_overflow(n, each, &v) && v < (int64_t(1) << 60);
+        };
+        for (const tide_fp8_t* m : {w, wt}) {
+            if (!m) continue;
+            const int64_t rows = m == w ? N : K, len = m == w ? K : N;
+            if (!m->codes || !aligned(m->codes, 16) || m->stride % 16 != 0 || m->stride < (len + 15) / 16 * 16 || (E > 1 && (m->batch % 16 != 0 || m->batch < 0))) return TIDE_EINVAL;
+            if (!extent(rows, m->stride) || !extent(E, E > 1 ? m->batch : 0)) return TIDE_ERANGE;
+        }
+        if (!w->scales || !aligned(w->scales, 4) || w->scale_stride < (K + tide::kBlock - 1) / tide::kBlock || (E > 1 && w->scale_batch < 0)) return TIDE_EINVAL;
+        if (!extent((N + tide::kBlock - 1) / tide::kBlock, w->scale_stride) || !extent(E, E > 1 ? w->scale_batch : 0)) return TIDE_ERANGE;
+        std::lock_guard<std::mutex> lock(g->mu);
+        int rc = tide::check_device(g->device);
+        if (rc != TIDE_OK) return rc;
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        tide::ShardPtrs sp;
+        int slot;
+        if ((rc = shard_ptrs(g, shards, 2, st, &sp, &slot)) != TIDE_OK) return rc;
+        const cudaError_t e = tide::launch_all_gather_fp8(sp, tv, E, params, *w, wt, {g->sm_count, overlap(g) ? ctas_of(g, 1) : 0}, st);
+        return finish(g, slot, st, e == cudaSuccess ? TIDE_OK : tide::record_cuda_error(e));
     });
 }
 

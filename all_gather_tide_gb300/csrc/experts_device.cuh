@@ -1,0 +1,95 @@
+// Device helpers shared by the kernels of a layer of experts.
+#pragma once
+
+#include <cstdint>
+
+#include "embedding_device.cuh"
+#include "experts.h"
+
+namespace tide {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// v[0..n] = the sums of f(0..n-1) before each index, and their total at n; n <= 1024.  All of the block's
+// threads call it; `sums` is 32 words of shared memory.
+template <typename F>
+__device__ __forceinline__ void exclusive_sums(int32_t* v, int n, int32_t* sums, F&& f) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if (threadIdx.x < 32) sums[threadIdx.x] = 0;
+    __syncthreads();
+    for (int s = warp; s * 32 < n; s += warps) {
+        const int i = s * 32 + lane;
+        const int32_t own = i < n ? f(i) : 0;
+        int32_t x = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t y = __shfl_up_sync(kFull, x, d);
+            if (lane >= d) x += y;
+        }
+        if (i < n) v[i] = x - own;
+        if (lane == 31) sums[s] = x;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int32_t own = sums[lane];
+        int32_t x = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t y = __shfl_up_sync(kFull, x, d);
+            if (lane >= d) x += y;
+        }
+        sums[lane] = x - own;
+        if (lane == 31) v[n] = x;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) v[i] += sums[i >> 5];
+    __syncthreads();
+}
+
+// Rows of expert e that are there: [first, first + count), inside [0, M) whatever the offsets hold.
+struct Span {
+    int32_t first, count;
+};
+__device__ __forceinline__ Span span_of(const int32_t* offsets, int e, int32_t M) {
+    if (!offsets) return {0, M};
+    const int32_t a = min(max(load_here(offsets + e), 0), M), b = min(max(load_here(offsets + e + 1), a), M);
+    return {a, b - a};
+}
+
+// The last index of starts[0..n) whose value is <= x; starts[0] = 0 <= x.  Of equal ones it is the last.
+__device__ __forceinline__ int last_at_most(const int32_t* starts, int n, int32_t x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (starts[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// V elements of T as one load.
+template <typename T, int V>
+struct Vec;
+template <int V>
+struct Vec<__nv_bfloat16, V> {
+    using Word = typename Bf16Vec<V>::Word;
+};
+template <>
+struct Vec<float, 4> {
+    using Word = float4;
+};
+template <>
+struct Vec<float, 2> {
+    using Word = float2;
+};
+template <>
+struct Vec<float, 1> {
+    using Word = float;
+};
+__device__ __forceinline__ void widen(const float4& w, float (&x)[4]) { x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w; }
+__device__ __forceinline__ void widen(const float2& w, float (&x)[2]) { x[0] = w.x, x[1] = w.y; }
+__device__ __forceinline__ void widen(const float& w, float (&x)[1]) { x[0] = w; }
+
+}  // namespace
+}  // namespace tide

@@ -1,0 +1,413 @@
+// Tokens sorted by expert and back, with the router's weights, and the gradients (sm_103a).
+//
+// Pair i = t*k + j is choice j of token t.  The stable order by expert puts pair i at row
+//     slot[i] = offsets[id_i] + |{i' < i: id_i' = id_i}|,    offsets[e] = |{i: id_i < e}|.
+#include <algorithm>
+
+#include "experts_device.cuh"
+
+namespace tide {
+namespace {
+
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kCtasPerSm = 4;  // of 256 threads
+
+__device__ __forceinline__ int expert_of(const void* ids, int ids64, int64_t i, int E, int* status) {
+    return int(row_of(ids, ids64, i, uint32_t(E), status));
+}
+
+// How many pairs of its piece go to each expert, for every CTA.
+__global__ void __launch_bounds__(kSortThreads) count_experts_kernel(const void* ids, int ids64, int32_t n, int32_t piece, int E, int32_t* counts, int* status) {
+    __shared__ int32_t count[TIDE_MAX_EXPERTS + 1];
+    for (int e = threadIdx.x; e <= E; e += kSortThreads) count[e] = 0;
+    wait_for_previous_kernel();
+    __syncthreads();
+    const int64_t first = int64_t(blockIdx.x) * piece, end = min(first + piece, int64_t(n));
+    for (int64_t i = first + threadIdx.x; i < end; i += kSortThreads) atomicAdd(&count[expert_of(ids, ids64, i, E, status)], 1);
+    __syncthreads();
+    let_next_kernel_start();
+    for (int e = threadIdx.x; e < E; e += kSortThreads) counts[int64_t(blockIdx.x) * E + e] = count[e];
+}
+
+// The rows of a piece's pairs.  Each warp has a stretch of the piece.  It first counts its pairs by expert, 32 at a time: lanes
+// with the same expert find one another (match) and their first adds their number, so no atomics are needed.
+// The counts of the warps before it, of the CTAs before (`counts`, unless this CTA sorts alone) and of all
+// experts before give the row of its first pair of each expert, and a second pass over the stretch, the same way,
+// the row of every pair.
+//
+// Bound by the latency of two short launches: 524288 pairs and 128 experts are 2 MB to 4 MB read twice and 4 MB written.
+__global__ void __launch_bounds__(kSortThreads)
+sort_experts_kernel(const void* ids, int ids64, int32_t n, int32_t piece, int k, int E, const int32_t* counts, int32_t* offsets, int32_t* slots,
+                    int32_t* tokens, int* status) {
+    extern __shared__ int32_t smem[];
+    int32_t* base = smem;                      // [E + 1] rows before each expert
+    int32_t* before = base + E + 1;            // [E] pairs of the CTAs before
+    int32_t* total = before + E;               // [E] pairs of all CTAs
+    int32_t* warp_count = total + E;           // [kSortWarps][E + 1]
+    __shared__ int32_t sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t* mine = warp_count + warp * (E + 1);
+    for (int e = threadIdx.x; e < E; e += kSortThreads) before[e] = total[e] = 0;
+    for (int e = lane; e <= E; e += 32) mine[e] = 0;
+    wait_for_previous_kernel();
+    __syncthreads();
+    const int64_t first = int64_t(blockIdx.x) * piece, end = min(first + piece, int64_t(n));
+    const int64_t stretch = ((end - first + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int64_t lo = min(first + warp * stretch, end), hi = min(lo + stretch, end);
+    // alone, this pass records ids past the experts too; else the counting kernel has
+    int* const bad = counts ? nullptr : status;
+    auto expert = [&](int64_t i) {
+        if (i >= hi) return E;
+        return bad ? expert_of(ids, ids64, i, E, bad) : int(row_of(load_id(ids, ids64, i), uint32_t(E)));
+    };
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+        const int e = expert(i0 + lane);
+        const unsigned same = __match_any_sync(kFull, e);
+        if ((same & ((1u << lane) - 1)) == 0) mine[e] += __popc(same);
+        __syncwarp();
+    }
+    if (counts) {
+        // threads in as many teams as there are, each over every so many-th CTA
+        int width = 32;
+        while (width < E && width < kSortThreads) width <<= 1;
+        const int teams = kSortThreads / width, team = threadIdx.x / width;
+        for (int e = threadIdx.x % width; e < E; e += width) {
+            int32_t b = 0, t = 0;
+#pragma unroll 8
+            for (int c = team; c < int(gridDim.x); c += teams) {
+                const int32_t v = load_here(counts + int64_t(c) * E + e);
+                t += v;
+                if (c < int(blockIdx.x)) b += v;
+            }
+            atomicAdd(&before[e], b);
+            atomicAdd(&total[e], t);
+        }
+    }
+    __syncthreads();
+    if (!counts) {
+        for (int e = threadIdx.x; e < E; e += kSortThreads) {
+            int32_t t = 0;
+            for (int w = 0; w < kSortWarps; ++w) t += warp_count[w * (E + 1) + e];
+            total[e] = t;
+        }
+        __syncthreads();
+    }
+    exclusive_sums(base, E, sums, [&](int e) { return total[e]; });
+    const int32_t held = base[E];
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= E; e += kSortThreads) offsets[e] = base[e];
+    for (int e = threadIdx.x; e < E; e += kSortThreads) {
+        int32_t at = base[e] + before[e];
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int32_t c = warp_count[w * (E + 1) + e];
+            warp_count[w * (E + 1) + e] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+        const int64_t i = i0 + lane;
+        const int e = i < hi ? int(row_of(load_id(ids, ids64, i), uint32_t(E))) : E;
+        const unsigned same = __match_any_sync(kFull, e), earlier = same & ((1u << lane) - 1);
+        const int32_t row = mine[e] + __popc(earlier);
+        __syncwarp();
+        if (earlier == 0) mine[e] += __popc(same);
+        __syncwarp();
+        if (i < hi) {
+            slots[i] = e < E ? row : -1;
+            if (e < E) tokens[row] = int32_t(uint32_t(i) / uint32_t(k));
+        }
+    }
+    // the rows behind the last
+    for (int64_t s = held + int64_t(blockIdx.x) * kSortThreads + threadIdx.x; s < n; s += int64_t(gridDim.x) * kSortThreads) tokens[s] = -1;
+    let_next_kernel_start();
+}
+
+// Which of the token's pairs, a lane each, have a row, and where.
+__device__ __forceinline__ unsigned held_pairs(const int32_t* slots, int64_t t, int k, int32_t M, int lane, int32_t* slot) {
+    *slot = lane < k ? load_here(slots + t * k + lane) : -1;
+    return __ballot_sync(kFull, uint32_t(*slot) < uint32_t(M));
+}
+
+// The tokens' rows to where their pairs go.  A warp takes a token and a stretch of 32*U vectors of its row into
+// registers and writes them once for each pair, so every row of src is read once.
+//
+// Bound by HBM writes.
+template <typename Word, int U>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+dispatch_kernel(const Word* src, int64_t src_stride, int64_t T, int k, int32_t M, uint32_t vecs, const int32_t* slots, Word* rows, int64_t rows_stride,
+                uint32_t stretches, int64_t items) {
+    const int lane = threadIdx.x & 31;
+    wait_for_previous_kernel();
+    for (int64_t it = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * kWarps) {
+        const int64_t t = it / stretches;
+        const uint32_t col = uint32_t(it - t * stretches) * (32 * U) + lane;
+        Word v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (col + 32 * u < vecs) v[u] = __ldcg(src + t * src_stride + col + 32 * u);
+        int32_t slot;
+        unsigned held = held_pairs(slots, t, k, M, lane, &slot);
+        while (held) {
+            const int j = __ffs(held) - 1;
+            held &= held - 1;
+            Word* to = rows + int64_t(__shfl_sync(kFull, slot, j)) * rows_stride + col;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (col + 32 * u < vecs) to[32 * u] = v[u];
+        }
+    }
+    let_next_kernel_start();
+}
+
+// The rows back at their tokens, weighted.  A warp takes a token and a stretch of 32*Cols vectors; kAtOnce rows are in
+// flight before their products are added, in fp32 and in the pairs' order.
+//
+// Bound by HBM reads.
+constexpr int kAtOnce = 4;
+template <typename T, int V, int Cols>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+combine_kernel(const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_t M, uint32_t len, const int32_t* slots, const float* weights, T* out,
+               int64_t out_stride, uint32_t stretches, int64_t items) {
+    using Word = typename Vec<T, V>::Word;
+    const int lane = threadIdx.x & 31;
+    wait_for_previous_kernel();
+    for (int64_t it = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * kWarps) {
+        const int64_t t = it / stretches;
+        const uint32_t col = (uint32_t(it - t * stretches) * (32 * Cols) + lane) * V;
+        int32_t slot;
+        unsigned held = held_pairs(slots, t, k, M, lane, &slot);
+        const float weight = weights && lane < k ? __ldcg(weights + t * k + lane) : 1.0f;
+        float acc[Cols][V] = {};
+        while (held) {
+            Word w[kAtOnce][Cols];
+            float f[kAtOnce];
+            int many = 0;
+#pragma unroll
+            for (int r = 0; r < kAtOnce; ++r) {
+                if (!held) break;
+                const int j = __ffs(held) - 1;
+                held &= held - 1;
+                const T* from = rows + int64_t(__shfl_sync(kFull, slot, j)) * rows_stride + col;
+                f[r] = __shfl_sync(kFull, weight, j);
+                ++many;
+#pragma unroll
+                for (int c = 0; c < Cols; ++c)
+                    if (col + c * 32 * V < len) w[r][c] = __ldcs(reinterpret_cast<const Word*>(from + c * 32 * V));
+            }
+#pragma unroll
+            for (int r = 0; r < kAtOnce; ++r) {
+                if (r >= many) break;
+#pragma unroll
+                for (int c = 0; c < Cols; ++c) {
+                    if (col + c * 32 * V >= len) continue;
+                    float x[V];
+                    widen(w[r][c], x);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[c][v] = weights ? fmaf(f[r], x[v], acc[c][v]) : acc[c][v] + x[v];
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < Cols; ++c)
+            if (col + c * 32 * V < len) put(out + t * out_stride + col + c * 32 * V, acc[c]);
+    }
+    let_next_kernel_start();
+}
+
+// The gradients of the weighted sum.  `team` warps take a token, a share of its columns each, and all of up to
+// kPairs pairs at once: a vector of dout is read once, those of the pairs' rows beside it, and each pair's
+// product with its weight is written while the dot product is added up.  A lane's sums run over its columns in order, then
+// over the warp's lanes and the team's warps as a tree.
+//
+// Bound by HBM: a row read and a row written for each pair.
+constexpr int kPairs = 8;
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, 2)
+combine_grad_kernel(const T* dout, int64_t dout_stride, const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_t M, uint32_t len,
+                    const int32_t* slots, const float* weights, T* drows, int64_t drows_stride, float* dweights, int team) {
+    using Word = typename Vec<T, V>::Word;
+    __shared__ float partial[kWarps][kPairs];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % team, each = kWarps / team;
+    wait_for_previous_kernel();
+    for (int64_t t0 = int64_t(blockIdx.x) * each; t0 < tokens; t0 += int64_t(gridDim.x) * each) {
+        const int64_t t = t0 + warp / team;
+        const bool here = t < tokens;
+        int32_t slot = -1;
+        float weight = 0.0f;
+        if (here && lane < k) slot = load_here(slots + t * k + lane), weight = __ldcg(weights + t * k + lane);
+        for (int j0 = 0; j0 < k; j0 += kPairs) {
+            float dot[kPairs] = {}, w[kPairs];
+            int32_t s[kPairs];
+            unsigned any = 0;
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                s[j] = __shfl_sync(kFull, slot, (j0 + j) & 31);
+                w[j] = __shfl_sync(kFull, weight, (j0 + j) & 31);
+                if (j0 + j >= k || uint32_t(s[j]) >= uint32_t(M)) s[j] = -1;
+                else any = 1;
+            }
+            if (any) {
+                for (uint32_t col = (part * 32 + lane) * V; col < len; col += team * 32 * V) {
+                    Word r[kPairs];
+                    const Word d = __ldcg(reinterpret_cast<const Word*>(dout + t * dout_stride + col));
+#pragma unroll
+                    for (int j = 0; j < kPairs; ++j)
+                        if (s[j] >= 0) r[j] = __ldcs(reinterpret_cast<const Word*>(rows + int64_t(s[j]) * rows_stride + col));
+                    float x[V];
+                    widen(d, x);
+#pragma unroll
+                    for (int j = 0; j < kPairs; ++j) {
+                        if (s[j] < 0) continue;
+                        float y[V], z[V];
+                        widen(r[j], y);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) dot[j] = fmaf(x[v], y[v], dot[j]), z[v] = w[j] * x[v];
+                        put(drows + int64_t(s[j]) * drows_stride + col, z);
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+#pragma unroll
+                for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(kFull, dot[j], d);
+            }
+            if (team > 1) {
+                if (lane == 0)
+#pragma unroll
+                    for (int j = 0; j < kPairs; ++j) partial[warp][j] = dot[j];
+                __syncthreads();
+                if (here && part == 0 && lane < kPairs && j0 + lane < k) {
+                    float sum = 0.0f;
+                    for (int p = 0; p < team; ++p) sum += partial[warp + p][lane];
+                    dweights[t * k + j0 + lane] = sum;
+                }
+                __syncthreads();
+            } else if (here) {
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j)
+                    if (lane == j && j0 + j < k) dweights[t * k + j0 + j] = dot[j];
+            }
+        }
+    }
+    let_next_kernel_start();
+}
+
+int grid_of(int64_t blocks, const Ctas& c, int per_sm) {
+    return int(std::max<int64_t>(1, std::min<int64_t>(blocks, c.most ? c.most : int64_t(c.sms) * per_sm)));
+}
+
+// The widest vector, in bytes up to 16, that all rows of both arrays allow.
+int vector_bytes(const void* a, int64_t a_stride, int64_t a_rows, const void* b, int64_t b_stride, int64_t b_rows, int64_t len, int elem) {
+    const uint64_t all = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | uint64_t(len * elem) |
+                         (a_rows > 1 ? uint64_t(a_stride * elem) : 0) | (b_rows > 1 ? uint64_t(b_stride * elem) : 0);
+    int v = 16;
+    while (v > elem && all % v) v >>= 1;
+    return v;
+}
+
+template <typename Word>
+cudaError_t dispatch(const RowsView& src, int elem, int64_t T, int k, int64_t len, const int32_t* slots, void* rows, int64_t rows_stride, const Ctas& c,
+                     cudaStream_t stream) {
+    constexpr int U = 4;
+    const int per = int(sizeof(Word)) / elem;
+    const uint32_t vecs = uint32_t(len / per), stretches = (vecs + 32 * U - 1) / (32 * U);
+    const int64_t items = T * stretches;
+    return launch_after(dispatch_kernel<Word, U>, grid_of((items + kWarps - 1) / kWarps, c, 8), kThreads, 0, stream, static_cast<const Word*>(src.p), src.stride / per, T, k,
+                        int32_t(T * k), vecs, slots, static_cast<Word*>(rows), rows_stride / per, stretches, items);
+}
+
+template <typename T, int V>
+cudaError_t combine(const RowsView& rows, int64_t tokens, int k, int64_t len, const int32_t* slots, const float* weights, void* out, int64_t out_stride,
+                    const Ctas& c, cudaStream_t stream) {
+    auto go = [&](auto* kernel, int cols) {
+        const uint32_t stretches = uint32_t((len + 32 * V * cols - 1) / (32 * V * cols));
+        const int64_t items = tokens * stretches;
+        return launch_after(kernel, grid_of((items + kWarps - 1) / kWarps, c, 8), kThreads, 0, stream, static_cast<const T*>(rows.p), rows.stride, tokens, k,
+                            int32_t(tokens * k), uint32_t(len), slots, weights, static_cast<T*>(out), out_stride, stretches, items);
+    };
+    return len > 32 * V ? go(combine_kernel<T, V, 2>, 2) : go(combine_kernel<T, V, 1>, 1);
+}
+
+template <typename T, int V>
+cudaError_t combine_grad(const RowsView& dout, const RowsView& rows, int64_t tokens, int k, int64_t len, const int32_t* slots, const float* weights, void* drows,
+                         int64_t drows_stride, float* dweights, const Ctas& c, cudaStream_t stream) {
+    // more warps for a token while the tokens do not fill the GPU and the row has a vector for each lane
+    int team = 1;
+    while (team < kWarps && tokens * team < int64_t(c.sms) * 16 && len > int64_t(team) * 32 * V) team *= 2;
+    const int64_t blocks = (tokens + kWarps / team - 1) / (kWarps / team);
+    return launch_after(combine_grad_kernel<T, V>, grid_of(blocks, c, 4), kThreads, 0, stream, static_cast<const T*>(dout.p), dout.stride, static_cast<const T*>(rows.p),
+                        rows.stride, tokens, k, int32_t(tokens * k), uint32_t(len), slots, weights, static_cast<T*>(drows), drows_stride, dweights, team);
+}
+
+}  // namespace
+
+int sort_ctas(int64_t pairs, const Ctas& c) {
+    if (pairs <= kSortAlone) return 1;
+    // a piece is 2048 pairs at least: four steps of every warp
+    return int(std::max<int64_t>(1, std::min<int64_t>((pairs + 2047) / 2048, c.most ? c.most : c.sms)));
+}
+
+cudaError_t launch_sort(const void* ids, int ids64, int64_t pairs, int k, int E, int32_t* offsets, int32_t* slots, int32_t* tokens, int32_t* counts, const Ctas& c,
+                        int* status, cudaStream_t stream) {
+    const size_t smem = sizeof(int32_t) * (size_t(E) + 1 + 2 * size_t(E) + size_t(kSortWarps) * (E + 1));
+    cudaError_t e = cudaFuncSetAttribute(sort_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(int32_t) * (19 * (TIDE_MAX_EXPERTS + 1))));
+    if (e != cudaSuccess) return e;
+    const int ctas = sort_ctas(pairs, c);
+    const int32_t piece = int32_t((pairs + ctas - 1) / ctas);
+    if (ctas > 1) {
+        e = launch_after(count_experts_kernel, ctas, kSortThreads, 0, stream, ids, ids64, int32_t(pairs), piece, E, counts, status);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_after(sort_experts_kernel, ctas, kSortThreads, smem, stream, ids, ids64, int32_t(pairs), piece, k, E,
+                        ctas > 1 ? static_cast<const int32_t*>(counts) : nullptr, offsets, slots, tokens, status);
+}
+
+cudaError_t launch_dispatch(const RowsView& src, int bf16, int64_t T, int k, int64_t len, const int32_t* slots, void* rows, int64_t rows_stride, const Ctas& c,
+                            cudaStream_t stream) {
+    if (T <= 0 || len <= 0) return cudaSuccess;
+    const int elem = bf16 ? 2 : 4;
+    switch (vector_bytes(src.p, src.stride, T, rows, rows_stride, T * k, len, elem)) {
+        case 16: return dispatch<uint4>(src, elem, T, k, len, slots, rows, rows_stride, c, stream);
+        case 8: return dispatch<uint2>(src, elem, T, k, len, slots, rows, rows_stride, c, stream);
+        case 4: return dispatch<uint32_t>(src, elem, T, k, len, slots, rows, rows_stride, c, stream);
+        default: return dispatch<uint16_t>(src, elem, T, k, len, slots, rows, rows_stride, c, stream);
+    }
+}
+
+cudaError_t launch_combine(const RowsView& rows, int bf16, int64_t T, int k, int64_t len, const int32_t* slots, const float* weights, void* out, int64_t out_stride,
+                           const Ctas& c, cudaStream_t stream) {
+    if (T <= 0 || len <= 0) return cudaSuccess;
+    const int v = vector_bytes(rows.p, rows.stride, T * k, out, out_stride, T, len, bf16 ? 2 : 4);
+    if (bf16) switch (v) {
+            case 16: return combine<__nv_bfloat16, 8>(rows, T, k, len, slots, weights, out, out_stride, c, stream);
+            case 8: return combine<__nv_bfloat16, 4>(rows, T, k, len, slots, weights, out, out_stride, c, stream);
+            case 4: return combine<__nv_bfloat16, 2>(rows, T, k, len, slots, weights, out, out_stride, c, stream);
+            default: return combine<__nv_bfloat16, 1>(rows, T, k, len, slots, weights, out, out_stride, c, stream);
+        }
+    switch (v) {
+        case 16: return combine<float, 4>(rows, T, k, len, slots, weights, out, out_stride, c, stream);
+        case 8: return combine<float, 2>(rows, T, k, len, slots, weights, out, out_stride, c, stream);
+        default: return combine<float, 1>(rows, T, k, len, slots, weights, out, out_stride, c, stream);
+    }
+}
+
+cudaError_t launch_combine_grad(const RowsView& dout, const RowsView& rows, int bf16, int64_t T, int k, int64_t len, const int32_t* slots, const float* weights,
+                                void* drows, int64_t drows_stride, float* dweights, const Ctas& c, cudaStream_t stream) {
+    if (T <= 0) return cudaSuccess;
+    const int elem = bf16 ? 2 : 4;
+    const int v = std::min(vector_bytes(dout.p, dout.stride, T, rows.p, rows.stride, T * k, len, elem), vector_bytes(drows, drows_stride, T * k, rows.p, rows.stride, T * k, len, elem));
+    if (bf16) switch (v) {
+            case 16: return combine_grad<__nv_bfloat16, 8>(dout, rows, T, k, len, slots, weights, drows, drows_stride, dweights, c, stream);
+            case 8: return combine_grad<__nv_bfloat16, 4>(dout, rows, T, k, len, slots, weights, drows, drows_stride, dweights, c, stream);
+            case 4: return combine_grad<__nv_bfloat16, 2>(dout, rows, T, k, len, slots, weights, drows, drows_stride, dweights, c, stream);
+            default: return combine_grad<__nv_bfloat16, 1>(dout, rows, T, k, len, slots, weights, drows, drows_stride, dweights, c, stream);
+        }
+    switch (v) {
+        case 16: return combine_grad<float, 4>(dout, rows, T, k, len, slots, weights, drows, drows_stride, dweights, c, stream);
+        case 8: return combine_grad<float, 2>(dout, rows, T, k, len, slots, weights, drows, drows_stride, dweights, c, stream);
+        default: return combine_grad<float, 1>(dout, rows, T, k, len, slots, weights, drows, drows_stride, dweights, c, stream);
+    }
+}
+
+}  // namespace tide

@@ -506,6 +506,180 @@ int tide_adamw(tide_tensors_t t, void *const *params, const void *const *grads, 
                double beta2, double eps, int64_t step, const float *norm, float max_norm, uint32_t flags,
                void *stream);
 
+/* ---- a layer of experts --------------------------------------------------------------------- */
+/*
+ * What a mixture-of-experts layer does with its tokens between the all-gather of the experts' weights and
+ * the reduce-scatter of their gradients.  T tokens go to k of E experts each; a pair is one token's choice
+ * of one expert, pair i = t*k + j being choice j of token t.  tide_experts_sort puts the M = T*k pairs
+ * into the experts' order, tide_experts_dispatch(_fp8) copies the tokens' rows into it,
+ * tide_experts_matmul multiplies each expert's rows with its weights in 8-bit floating point, and
+ * tide_experts_combine brings the rows back.  The gradients: tide_experts_combine_grad,
+ * tide_experts_combine without weights (dispatch's), tide_experts_matmul with the transposed weights, and
+ * tide_experts_weight_grad, which writes each expert's gradient where tide_reduce_scatter reads it.
+ * tide_all_gather_fp8 turns the ranks' bf16 shards into the 8-bit weights.  (The paper has no counterpart:
+ * its collectives deliver these weights and take these gradients.)
+ *
+ * 8-bit matrices.  A value is an e4m3 code (4 exponent bits of bias 7, 3 mantissa bits, at most 448, no
+ * infinity) times the fp32 scale of its block of 128 values: 1 x 128 of a row, or 128 x 128 of a weight.
+ * The calls that write them take for a block whose largest magnitude is a > 0 the smallest power of two
+ * from 2^-126 to 2^120 with a / scale <= 448 (1 for a block of zeros), and code = x / scale rounded to
+ * nearest even; a block with a NaN or an infinity gets a NaN scale.  The calls that read them accept any
+ * scales.
+ */
+typedef struct tide_fp8 {
+    void *codes;          /* device, 16-byte aligned; the matrix's rows are `stride` bytes apart */
+    int64_t stride;       /* a multiple of 16, at least the row length; bytes behind a row's end in the last of
+                             its groups of 16 may be overwritten by calls that write rows */
+    int64_t batch;        /* bytes between the experts' matrices (weights only), a multiple of 16 */
+    float *scales;        /* device; rows of ceil(row length / 128) scales `scale_stride` elements apart: one for
+                             each row of the matrix, or for weights one for each 128 rows */
+    int64_t scale_stride;
+    int64_t scale_batch;  /* elements between the experts' scales (weights only) */
+} tide_fp8_t;
+
+#define TIDE_MAX_EXPERTS 1024
+#define TIDE_MAX_CHOICES 32
+
+/*
+ * A layer's experts: E experts, k choices a token.  The object owns a device status word; its calls keep
+ * nothing else between them, can be captured into CUDA graphs and may overlap on several streams and host
+ * threads (each with its own outputs and workspace).  It belongs to the device current at creation, which
+ * has to be current at every call.
+ *   flags: 0, or TIDE_FLAG_OVERLAP: no launch has more than sm_count / 9 CTAs.
+ * Errors: TIDE_EINVAL (null, E or k < 1, E > TIDE_MAX_EXPERTS, k > TIDE_MAX_CHOICES, an unknown flag),
+ * TIDE_ENOMEM, TIDE_ECUDA.
+ */
+typedef struct tide_experts *tide_experts_t;
+int tide_experts_create(tide_experts_t *out, int32_t E, int32_t k, uint32_t flags);
+/* Frees the object; the work that uses it must have ended.  NULL is accepted. */
+int tide_experts_destroy(tide_experts_t x);
+/* Reads the status word (0; 1 = a wait of a product's kernel expired; 64 = tide_experts_sort met an
+ * expert >= E) and clears it.  Synchronous: copies from the device. */
+int tide_experts_device_status(tide_experts_t x, int32_t *status);
+/* Every wait of the products' kernels gives up after `timeout_ns` (0 = the default, 2 s). */
+int tide_experts_set_wait_timeout(tide_experts_t x, uint64_t timeout_ns);
+
+/* Bytes of device workspace (256-byte aligned) with which tide_experts_sort serves up to T tokens; 0 where
+ * it needs none.  Errors: TIDE_EINVAL, TIDE_ERANGE (T*k > 2^31 - 2^16). */
+int tide_experts_sort_workspace(tide_experts_t x, int64_t T, int64_t *bytes);
+
+/*
+ * tide_experts_sort — the experts' order of the pairs, stable (an expert's pairs in the order of their
+ * numbers):
+ *     offsets[e]      = pairs of experts < e, for 0 <= e <= E
+ *     slots[i]        = the row of pair i in that order, -1 where it has no expert
+ *     tokens[slots[i]] = i / k;  -1 for the rows from offsets[E] on
+ * A negative id marks a pair without an expert (padding, a dropped choice); an id >= E is one too and sets
+ * 64 in the status word, if that holds 0.  A token may choose one expert several times.
+ *   ids: device, T*k ids of ids_type (TIDE_I32 or TIDE_I64).   offsets, slots, tokens: device, E + 1, T*k and
+ *   T*k int32.   workspace: device, 256-byte aligned, at least tide_experts_sort_workspace's bytes for T
+ *   tokens or more (may be NULL where that is 0); not shared by calls that overlap.
+ * Errors: TIDE_EINVAL (null or misaligned pointers, T < 0, a type, the workspace too small, another device
+ * current), TIDE_ERANGE (T*k > 2^31 - 2^16), TIDE_ECUDA.
+ */
+int tide_experts_sort(tide_experts_t x, const void *ids, int32_t ids_type, int64_t T, int32_t *offsets,
+                      int32_t *slots, int32_t *tokens, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * tide_experts_dispatch — the tokens' rows in the experts' order:
+ *     rows[slots[t*k + j]] = src[t]      for every pair with 0 <= slot < T*k
+ * Rows of len elements of `type` (TIDE_F32 or TIDE_BF16), src_stride and rows_stride (>= len) elements
+ * apart; T rows of src, T*k of rows.  Rows that no pair has are left as they are.  Any element alignment is
+ * accepted.
+ * Errors of this and the following calls: TIDE_EINVAL (null or misaligned pointers, a negative size, a type, a
+ * stride too small, another device current), TIDE_ERANGE (more than 2^31 - 2^16 pairs, len > 2^30, an
+ * extent in bytes beyond int64), TIDE_ECUDA.
+ */
+int tide_experts_dispatch(tide_experts_t x, const void *src, int32_t type, int64_t src_stride, int64_t T, int64_t len,
+                          const int32_t *slots, void *rows, int64_t rows_stride, void *stream);
+
+/* tide_experts_dispatch_fp8 — the same with the rows in 8 bits, a scale for each block of 128 columns.
+ *   rows: T*k rows of len codes; rows->scales T*k rows of ceil(len / 128). */
+int tide_experts_dispatch_fp8(tide_experts_t x, const void *src, int32_t type, int64_t src_stride, int64_t T, int64_t len,
+                              const int32_t *slots, const tide_fp8_t *rows, void *stream);
+
+/*
+ * tide_experts_combine — the rows back at their tokens:
+ *     out[t] = sum over j with 0 <= slots[t*k + j] < T*k of weights[t*k + j] * rows[slots[t*k + j]]
+ * in fp32, j ascending, rounded once to `type`; +0 for a token without a pair.  weights: device fp32, or NULL for
+ * 1 (the gradient of tide_experts_dispatch).  Rows of `type` and strides as there.
+ */
+int tide_experts_combine(tide_experts_t x, const void *rows, int32_t type, int64_t rows_stride, int64_t T, int64_t len,
+                         const int32_t *slots, const float *weights, void *out, int64_t out_stride, void *stream);
+
+/*
+ * tide_experts_combine_grad — the gradients of tide_experts_combine with weights:
+ *     drows[slots[i]] = weights[i] * dout[i / k]         dweights[i] = sum over columns of dout[i / k] * rows[slots[i]]
+ * the products in fp32 and rounded once to `type`, the sums in fp32 in an order that depends on the sizes alone; pairs without
+ * a row have dweights 0, rows without a pair are left as they are.
+ */
+int tide_experts_combine_grad(tide_experts_t x, const void *dout, int32_t type, int64_t dout_stride, const void *rows,
+                              int64_t rows_stride, int64_t T, int64_t len, const int32_t *slots, const float *weights,
+                              void *drows, int64_t drows_stride, float *dweights, void *stream);
+
+/* Columns that the transposed form of M rows in E experts' order takes: each expert's rows begin at a multiple
+ * of 128, so that no block of 128 has rows of two.  Errors: TIDE_EINVAL, TIDE_ERANGE. */
+int tide_fp8_padded_rows(int64_t M, int32_t E, int64_t *columns);
+
+/*
+ * tide_experts_quantize — rows in the experts' order in 8 bits: as they are, a scale for each block of 128
+ * columns, and/or transposed, a scale for each block of 128 rows of one expert (what tide_experts_weight_grad
+ * sums over).
+ *   src: rows of len elements of `type`, src_stride apart; row s is src[s], M of them, or with tokens (device,
+ *   M int32, tide_experts_sort's) src[tokens[s]] of the src_rows rows of src.
+ *   offsets: tide_experts_sort's; only rows before offsets[E] are read and written (NULL, for E = 1: all M).
+ *   rows: M rows of len codes, or NULL.
+ *   columns: len rows of tide_fp8_padded_rows(M, E) codes, or NULL; expert e's rows are columns P_e to
+ *   P_e + offsets[e+1] - offsets[e], P_e = 128 * sum over e' < e of ceil((offsets[e'+1] - offsets[e']) / 128);
+ *   zeros follow up to the next multiple of 128, and nothing is written behind the last expert's.  Their scales
+ *   lie the other way round, len of them for each block: that of (column c of src, block b) is
+ *   columns->scales[b * scale_stride + c].
+ */
+int tide_experts_quantize(tide_experts_t x, const void *src, int32_t type, int64_t src_stride, int64_t src_rows, int64_t M,
+                          int64_t len, const int32_t *offsets, const int32_t *tokens, const tide_fp8_t *rows,
+                          const tide_fp8_t *columns, void *stream);
+
+/*
+ * tide_all_gather_fp8 — all-gather placement in 8 bits: E parameters of one shape (rows_p = N, L_p = K; an
+ * expert each) read from the packed bf16 shards, without gathering them in bf16, a scale for each block of
+ * 128 x 128.
+ *   ps: host array of E parameter indexes (1 <= E <= TIDE_MAX_EXPERTS).   shards: host array of R device
+ *   pointers, as tide_all_gather's.  Up to 64 ranks the call can be captured into a CUDA graph.
+ *   w: E matrices of N rows of K codes; ceil(N / 128) rows of scales each.
+ *   wt: NULL, or the codes of the transposed matrices, K rows of N; its scales are w's and its scale fields are
+ *   not used.
+ * Errors: TIDE_EINVAL (as above, parameters of several shapes), TIDE_ERANGE, TIDE_ECUDA.
+ */
+int tide_all_gather_fp8(tide_group_t g, int32_t E, const int32_t *ps, const void *const *shards, const tide_fp8_t *w,
+                        const tide_fp8_t *wt, void *stream);
+
+/*
+ * tide_experts_matmul — every expert's rows times its weights:
+ *     out[s, n] = sum over blocks b of 128 of a.scale[s, b] * w.scale[e, n/128, b] * sum over c in b of a[s, c] * w[e, n, c]
+ * for the rows s of expert e (offsets[e] <= s < offsets[e+1]) and 0 <= n < N, c < K; blocks' sums and their total
+ * in fp32, rounded once to out_type (TIDE_BF16 or TIDE_F32).  Rows from offsets[E] on are left as they are.
+ *   a: M rows of K codes.   w: E matrices of N rows of K codes.   offsets: as tide_experts_quantize's.
+ *   transposed: 0; or 1 where w->codes are tide_all_gather_fp8's wt and w->scales those of its w, of which the scale
+ *   of (n, block b) is then [e, b, n/128]: the product with the untransposed weights of K rows of N, the gradient
+ *   of the rows.
+ *   out: M rows of N elements, out_stride (>= N) apart.
+ */
+int tide_experts_matmul(tide_experts_t x, const tide_fp8_t *a, int64_t M, const int32_t *offsets, const tide_fp8_t *w,
+                        int32_t transposed, int64_t N, int64_t K, void *out, int32_t out_type, int64_t out_stride,
+                        void *stream);
+
+/*
+ * tide_experts_weight_grad — the gradients of the weights, from the transposed forms of the output's gradient and
+ * of the rows:
+ *     grads_e[n*K + c] = sum over blocks b of 128 rows of e of dy.scale[b, n] * a.scale[b, c] * sum over s in b of dy[n, s] * a[c, s]
+ * in fp32, rounded once; zeros for an expert without rows.
+ *   dy, a: N and K rows of tide_fp8_padded_rows(M, E) codes, as tide_experts_quantize writes columns.
+ *   grads: host array of E device pointers to contiguous N x K gradients of grad_type (TIDE_BF16, as
+ *   tide_reduce_scatter reads them, or TIDE_F32).
+ */
+int tide_experts_weight_grad(tide_experts_t x, const tide_fp8_t *dy, const tide_fp8_t *a, int64_t M, const int32_t *offsets,
+                             int64_t N, int64_t K, void *const *grads, int32_t grad_type, void *stream);
+
 /* ---- interference probes (measurement kernels of the interference harness) ----------------- */
 /*
  * tide_probe_hold — launches `ctas` CTAs of `threads` threads, each claiming `smem_bytes` of

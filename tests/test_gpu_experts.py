@@ -1,0 +1,454 @@
+"""A layer of experts on the GPU, against plain implementations in 64 bits.
+
+Order, copies, codes and scales are compared bit for bit.  Sums of n products in fp32 (u = 2^-24) are off by at most
+(n + 1) u times the sum of the products' magnitudes, and the result by half a step of its type more.  In a product of
+8-bit matrices the 128 products of a block are exact and added by the tensor cores, taken to lose at most 2u of
+the block's magnitudes with each; the blocks' sums are scaled (at most three roundings) and added in fp32: (128 + blocks + 3) * 2u
+of the sum of all magnitudes.  Buffers have guard bands around them.
+"""
+import ctypes
+
+import pytest
+import torch
+
+from test_gpu_step import TYPES, U, Guarded, gen
+
+pytestmark = pytest.mark.gpu
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}  # half a step, relative to the value
+
+
+@pytest.fixture(scope="module")
+def tide():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import all_gather_tide_gb300 as t
+
+    t.lib()
+    return t
+
+
+# ---- plain forms ---------------------------------------------------------------------------------
+
+
+def order_of(ids, E):
+    """offsets, slots, tokens of [T, k] CPU ids, pair by pair."""
+    T, k = ids.shape
+    flat = [int(i) for i in ids.flatten()]
+    rows = [i for e in range(E) for i in [j for j, x in enumerate(flat) if x == e]] if len(flat) * E <= 100000 else None
+    if rows is None:
+        x = ids.flatten().long()
+        held = (x >= 0) & (x < E)
+        rows = torch.argsort(torch.where(held, x, E), stable=True)[:int(held.sum())].tolist()
+    offsets = torch.tensor([sum(1 for x in flat if 0 <= x < e) for e in range(E + 1)] if len(flat) * E <= 100000 else
+                           [0] + torch.bincount(ids.flatten()[(ids.flatten() >= 0) & (ids.flatten() < E)].long(), minlength=E).cumsum(0).tolist())
+    slots, tokens = torch.full((T * k,), -1), torch.full((T * k,), -1)
+    r = torch.tensor(rows, dtype=torch.long)
+    slots[r] = torch.arange(len(rows))
+    tokens[:len(rows)] = r // k
+    return offsets, slots.view(T, k), tokens
+
+
+def draw_ids(g, T, k, E, masked=0.1):
+    ids = torch.randint(0, E, (T, k), generator=g)
+    ids = torch.minimum(ids, torch.randint(0, E, (T, k), generator=g))  # low experts are more popular; choices may repeat
+    ids[torch.rand(T, k, generator=g) < masked] = -1
+    return ids
+
+
+def e4m3(x, dims):
+    """Codes (as values) and scales of x in 64 bits, one power of two for each block over `dims`, by comparison with every candidate."""
+    amax = x.abs().amax(dims, keepdim=True)
+    bad = ~torch.isfinite(amax)
+    m, e = torch.frexp(torch.where(bad | (amax == 0), torch.ones_like(amax), amax))
+    p = torch.where(m <= 0.875, e - 9, e - 8).clamp(-126, 120)
+    scale = torch.where(amax == 0, 1.0, torch.ldexp(torch.ones_like(amax), p))
+    scale = torch.where(bad, float("nan"), scale)
+    y = x / scale
+    step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
+    return torch.where(bad, float("nan"), torch.round(y / step) * step), scale
+
+
+def in_rows(x):
+    """[n, len] -> codes [n, len], scales [n, blocks]"""
+    parts = [e4m3(x[:, c:c + 128].double(), (1,)) for c in range(0, x.shape[1], 128)]
+    return torch.cat([c for c, _ in parts], 1), torch.cat([s for _, s in parts], 1)
+
+
+def in_blocks(w):
+    """[N, K] -> codes, scales [N / 128, K / 128]"""
+    rows = []
+    for n in range(0, w.shape[0], 128):
+        parts = [e4m3(w[n:n + 128, c:c + 128].double(), (0, 1)) for c in range(0, w.shape[1], 128)]
+        rows.append((torch.cat([c for c, _ in parts], 1), torch.cat([s for _, s in parts], 1)))
+    return torch.cat([c for c, _ in rows]), torch.cat([s for _, s in rows])
+
+
+def values(codes, scales):
+    """Codes times the scales of their blocks of 128 in the last dimension."""
+    return codes * scales.repeat_interleave(128, -1)[..., :codes.shape[-1]]
+
+
+def same(a, b):
+    """Equal, NaN where NaN."""
+    return torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+
+
+def routed(tide, E, k, ids, kind="i64", flags=0):
+    ex = tide.Experts(E, k, flags)
+    route = ex.route(ids.shape[0])
+    ex.sort(ids.to(TYPES[kind]).cuda(), route)
+    return ex, route
+
+
+# ---- order ---------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("E", [1, 2, 31, 128, 1000, 1024])
+@pytest.mark.parametrize("T, k", [(0, 2), (1, 1), (1, 8), (3, 5), (77, 3), (400, 32), (2048, 2), (2049, 2), (20011, 1), (40000, 8)])
+def test_sort(tide, T, k, E):
+    for masked, kind in ((0.0, "i64"), (0.3, "i32"), (1.0, "i64")):
+        ids = draw_ids(gen(T + E), T, k, E, masked)
+        offsets, slots, tokens = order_of(ids, E)
+        ex = tide.Experts(E, k)
+        route = ex.route(T)
+        for x in (route.offsets, route.slots, route.tokens):
+            x.fill_(-7)
+        ex.sort(ids.to(TYPES[kind]).cuda(), route)
+        assert torch.equal(route.offsets.cpu().long(), offsets)
+        assert torch.equal(route.slots.cpu().long(), slots)
+        assert torch.equal(route.tokens.cpu().long(), tokens)
+        assert ex.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [5, 5000])
+def test_sort_ids_past_the_experts(tide, T):
+    ids = torch.full((T, 2), 3)
+    ids[T // 2] = torch.tensor([4, 1 << 40])
+    ids[0] = torch.tensor([-(1 << 40), 0])
+    ex, route = routed(tide, 4, 2, ids)
+    assert torch.equal(route.slots.cpu().long(), order_of(ids, 4)[1])
+    assert ex.device_status() == 64 and ex.device_status() == 0
+
+
+def test_sort_on_few_ctas(tide):
+    ids = draw_ids(gen(1), 9000, 4, 60)
+    ex, route = routed(tide, 60, 4, ids, flags=tide.TIDE_FLAG_OVERLAP)
+    want = order_of(ids, 60)
+    for x, y in zip((route.offsets, route.slots, route.tokens), want):
+        assert torch.equal(x.cpu().long(), y)
+
+
+# ---- rows there and back --------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [1, 3, 8, 100, 256, 1027, 2048, 4100])
+def test_rows_there_and_back(tide, D, kind):
+    g = gen(D)
+    for T, k, E, shift, pad, masked in ((1, 1, 1, 0, 0, 0.0), (40, 8, 7, 0, 0, 0.1), (33, 3, 50, 1, 3, 0.5), (130, 32, 9, 2, 2, 0.05), (5, 2, 3, 4, 4, 1.0)):
+        ids = draw_ids(g, T, k, E, masked)
+        ex, route = routed(tide, E, k, ids)
+        slots, held = route.slots.cpu().long(), int(route.offsets[-1])
+        at = slots >= 0
+        x = torch.randn(T, D + pad, generator=g).to(TYPES[kind])
+        dx = Guarded(x, shift)
+        rows = Guarded(torch.full((T * k, D + pad), 55.0).to(TYPES[kind]), shift)
+        ex.dispatch(dx.view[:, :D], route, rows.view[:, :D])
+        want = torch.full((T * k, D + pad), 55.0).to(TYPES[kind])
+        want[slots[at], :D] = x[:, :D].repeat_interleave(k, 0).view(T, k, D)[at]
+        got = rows.cpu()
+        assert torch.equal(got, want)
+
+        # back: rows that no pair has hold NaN, which must not enter
+        y = torch.randn(T * k, D + pad, generator=g).to(TYPES[kind])
+        y[held:] = float("nan")
+        w = torch.randn(T, k, generator=g)
+        dy, dw = Guarded(y, shift), Guarded(w)
+        for weights in (None, dw):
+            out = Guarded(torch.full((T, D + pad), 55.0).to(TYPES[kind]), shift)
+            ex.combine(dy.view[:, :D], route, out.view[:, :D], None if weights is None else dw.view)
+            f = torch.where(at, w.double() if weights is not None else 1.0, 0.0)
+            parts = torch.where(at[:, :, None], y[slots.clamp(min=0), :D].double(), 0.0) * f[:, :, None]
+            total, size = parts.sum(1), parts.abs().sum(1)
+            got = out.cpu()
+            err = (got[:, :D].double() - total).abs()
+            assert bool((err <= (k + 1) * U * size * 1.01 + HALF[kind] * total.abs() * 1.01 + 1e-40).all())
+            assert bool((got[:, D:] == 55).all())
+
+        # the gradients
+        dout = torch.randn(T, D + pad, generator=g).to(TYPES[kind])
+        ddout, drows, dweights = Guarded(dout, shift), Guarded(torch.full((T * k, D + pad), 55.0).to(TYPES[kind]), shift), Guarded(torch.full((T, k), 55.0))
+        ex.combine_grad(ddout.view[:, :D], dy.view[:, :D], route, dw.view, drows.view[:, :D], dweights.view)
+        want = torch.full((T * k, D + pad), 55.0).to(TYPES[kind])
+        product = dout[:, None, :D].float() * w[:, :, None]  # fp32, as the call forms it
+        want[slots[at], :D] = product.to(TYPES[kind])[at]
+        assert torch.equal(drows.cpu(), want)
+        parts = torch.where(at[:, :, None], y[slots.clamp(min=0), :D].double(), 0.0) * dout[:, None, :D].double()
+        err = (dweights.cpu().double() - parts.sum(2)).abs()
+        assert bool((err <= (D + 1) * U * parts.abs().sum(2) * 1.01 + 1e-40).all())
+        assert bool((dweights.cpu()[~at] == 0).all())
+
+
+def test_gradients_by_differences(tide):
+    """combine's gradients against differences of its own outputs, whose quotient is exact for a bilinear form but for roundings."""
+    T, k, E, D = 6, 3, 4, 40
+    g = gen(5)
+    ids = draw_ids(g, T, k, E, 0.2)
+    ex, route = routed(tide, E, k, ids)
+    y, w, dout = torch.randn(T * k, D, generator=g).cuda(), torch.randn(T, k, generator=g).cuda(), torch.randn(T, D, generator=g).cuda()
+    drows, dweights, out = torch.zeros(T * k, D, device="cuda"), torch.zeros(T, k, device="cuda"), torch.zeros(T, D, device="cuda")
+    ex.combine_grad(dout, y, route, w, drows, dweights)
+
+    def loss(y, w):
+        ex.combine(y, route, out, w)
+        return float((out.double() * dout.double()).sum())
+
+    # each output is off by (k + 1) u of its products' magnitudes, at most 4 * 4 * 5 in all for |normal| <= 5; the loss sums T * D of them times |dout| <= 5
+    slack = 2 * (k + 1) * U * 3 * 25 * 5 * T * D
+    for i in range(T):
+        for j in range(k):
+            a, b = w.clone(), w.clone()
+            a[i, j] += 0.5
+            b[i, j] -= 0.5
+            assert abs(loss(y, a) - loss(y, b) - float(dweights[i, j])) <= slack + (D + 1) * U * 25 * D
+    for s in range(0, int(route.offsets[-1]), 3):
+        for c in range(0, D, 7):
+            a, b = y.clone(), y.clone()
+            a[s, c] += 0.5
+            b[s, c] -= 0.5
+            assert abs(loss(a, w) - loss(b, w) - float(drows[s, c])) <= slack
+
+
+def test_slots_outside_the_rows_count_as_none(tide):
+    ex = tide.Experts(3, 2)
+    route = ex.route(4)
+    slots = torch.tensor([[0, 8], [-5, 1], [1 << 30, -(1 << 31)], [7, 2]], dtype=torch.int32)
+    route.slots.copy_(slots)
+    x = torch.arange(4 * 6, dtype=torch.float32).view(4, 6)
+    rows = Guarded(torch.full((8, 6), 55.0))
+    ex.dispatch(x.cuda(), route, rows.view)
+    want = torch.full((8, 6), 55.0)
+    want[0], want[1], want[7], want[2] = x[0], x[1], x[3], x[3]
+    assert torch.equal(rows.cpu(), want)
+    out = torch.full((4, 6), 9.0, device="cuda")
+    ex.combine(rows.view, route, out)
+    assert torch.equal(out.cpu(), torch.stack([x[0], x[1], torch.zeros(6), 2 * x[3]]))
+
+
+# ---- 8-bit matrices --------------------------------------------------------------------------------
+
+
+def strange(x):
+    """Blocks of zeros, tiny and huge values, exact ties, NaN and infinity among ordinary ones."""
+    n, c = x.shape
+    x[0, :128] = 0.0
+    if n > 1:
+        x[1] *= 2.0 ** -120
+    if n > 2:
+        x[2] *= 2.0 ** 100
+    if n > 3:
+        x[3] = torch.where(torch.arange(c) % 2 == 0, 448.0, 17.0)  # 17 lies between 16 and 18
+    if n > 4:
+        x[4, c // 2] = float("nan")
+    if n > 5:
+        x[5, c // 3] = float("inf")
+    if n > 6:
+        x[6] = 2.0 ** -133
+    if n > 7:
+        x[7] = torch.where(torch.arange(c) % 2 == 0, 449.0, -448.0)
+    return x
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [1, 8, 100, 128, 136, 513, 1027, 2048])
+def test_rows_in_8_bits(tide, D, kind):
+    g = gen(D)
+    for T, k, E, shift, pad in ((1, 1, 1, 0, 0), (41, 3, 7, 0, 0), (30, 2, 5, 1, 3), (300, 4, 6, 8, 8)):
+        ids = draw_ids(g, T, k, E)
+        ex, route = routed(tide, E, k, ids)
+        M, held, offsets = T * k, int(route.offsets[-1]), route.offsets.cpu().tolist()
+        x = strange(torch.randn(T, D + pad, generator=g)).to(TYPES[kind])
+        dx = Guarded(x, shift)
+        codes, scales = in_rows(x[:, :D])
+        tokens = route.tokens.cpu().long()[:held]
+
+        def check(q):
+            assert same(q.codes.float().cpu()[:held].double(), codes[tokens]) and same(q.scales.cpu()[:held].double(), scales[tokens])
+
+        q = tide.Fp8Rows(M, D)
+        ex.dispatch_fp8(dx.view[:, :D], route, q)
+        check(q)
+        # the same by way of rows in the experts' order, and by gathering
+        rows = Guarded(torch.full((M, D + pad), float("nan")).to(TYPES[kind]), shift)
+        ex.dispatch(dx.view[:, :D], route, rows.view[:, :D])
+        blocks = [-(-(b - a) // 128) for a, b in zip(offsets, offsets[1:])]
+        for source, gather in ((rows.view[:, :D], False), (dx.view[:, :D], True)):
+            q, qt = tide.Fp8Rows(M, D), tide.Fp8Columns(M, D, E)
+            q.codes.view(torch.uint8).fill_(0x55)
+            qt.codes.view(torch.uint8).fill_(0x55)
+            ex.quantize(source, route, rows=q, columns=qt, gather=gather)
+            check(q)
+            assert bool((q.codes.view(torch.uint8)[held:] == 0x55).all())
+            both = [q, qt]
+            got, got_scales = qt.codes.float().cpu().double(), qt.scales.cpu().double()
+            for e, (a, b) in enumerate(zip(offsets, offsets[1:])):
+                at = sum(blocks[:e])
+                part = torch.zeros(D, blocks[e] * 128, dtype=torch.float64)
+                part[:, :b - a] = x[tokens[a:b], :D].double().t()
+                if b > a:
+                    c, s = in_rows(part)
+                    assert same(got[:, at * 128:(at + blocks[e]) * 128], c) and same(got_scales[at:at + blocks[e]], s.t())
+            assert bool((qt.codes.view(torch.uint8)[:, sum(blocks) * 128:] == 0x55).all())
+            # each alone
+            q, qt = tide.Fp8Rows(M, D), tide.Fp8Columns(M, D, E)
+            ex.quantize(source, route, rows=q, gather=gather)
+            ex.quantize(source, route, columns=qt, gather=gather)
+            check(q)
+            n = sum(blocks)
+            assert torch.equal(qt.codes.view(torch.uint8)[:, :n * 128], both[1].codes.view(torch.uint8)[:, :n * 128])
+            assert same(qt.scales[:n].cpu(), both[1].scales[:n].cpu())
+
+
+@pytest.mark.parametrize("R, N, K, before, E", [(1, 1, 1, 0, 1), (2, 128, 128, 0, 3), (3, 331, 525, 5, 4), (8, 768, 256, 8, 2), (4, 130, 1027, 0, 2), (8, 3, 200, 1, 5), (70, 200, 64, 0, 2)])
+def test_all_gather_fp8(tide, R, N, K, before, E):
+    g = gen(N)
+    params = ([(before, 1)] if before else []) + [(N, K)] * E
+    G = tide.Group(R, params)
+    m = -(-N // R)
+    shards = [Guarded(torch.full((G.S,), float("nan")).bfloat16(), 0) for _ in range(R)]
+    first = 1 if before else 0
+    w = [strange(torch.randn(N, K, generator=g)).bfloat16() if e == 1 else torch.randn(N, K, generator=g).bfloat16() for e in range(E)]
+    for e in range(E):
+        o = G.param_layout(first + e)[1]
+        for d in range(R):
+            part = w[e][d * m:(d + 1) * m].reshape(-1)
+            shards[d].view[o:o + part.numel()].copy_(part)
+    for transposed in (False, True):
+        W = tide.Fp8Weights(E, N, K, transposed)
+        ps = list(range(first, first + E))[::-1]  # any order
+        G.all_gather_fp8(ps, [s.view for s in shards], W)
+        for i, p in enumerate(ps):
+            codes, scales = in_blocks(w[p - first])
+            assert same(W.codes[i].float().cpu().double(), codes) and same(W.scales[i].cpu().double(), scales)
+            if transposed:
+                assert same(W.codes_transposed[i].float().cpu().double(), codes.t())
+
+
+def test_parts_of_weights_side_by_side(tide):
+    N, K, E = 256, 320, 3
+    g = gen(0)
+    G = tide.Group(2, [(N, K)] * (2 * E))
+    shards = torch.randn(2, G.S, generator=g).bfloat16().cuda()
+    both, one, two = tide.Fp8Weights(E, 2 * N, K, True), tide.Fp8Weights(E, N, K, True), tide.Fp8Weights(E, N, K, True)
+    for q, i in ((both.part(0, N), 0), (both.part(N, N), 1), (one, 0), (two, 1)):
+        G.all_gather_fp8(range(i, 2 * E, 2), list(shards), q)
+    assert torch.equal(both.codes.view(torch.uint8), torch.cat([one.codes, two.codes], 1).view(torch.uint8))
+    assert torch.equal(both.scales, torch.cat([one.scales, two.scales], 1))
+    assert torch.equal(both.codes_transposed.view(torch.uint8), torch.cat([one.codes_transposed, two.codes_transposed], 2).view(torch.uint8))
+    for first, rows in ((64, 128), (0, 100), (128, 512), (-128, 128)):
+        with pytest.raises(tide.TideError):
+            both.part(first, rows)
+
+
+# ---- products --------------------------------------------------------------------------------------
+
+
+def random_fp8(g, x, scales=True):
+    """Fills codes with finite values of all sizes and scales with numbers that are no powers of two."""
+    bits = torch.randint(0, 256, tuple(x.codes.shape), generator=g).to(torch.uint8)
+    bits[(bits & 0x7F) == 0x7F] = 0x3A
+    x.codes.view(torch.uint8).copy_(bits)
+    if scales:
+        x.scales.copy_(torch.exp(torch.randn(tuple(x.scales.shape), generator=g)))
+
+
+def bound(blocks, size):
+    return (128 + blocks + 3) * 2 * U * size
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T, k, E, N, K", [(1, 1, 1, 1, 1), (1, 8, 16, 200, 300), (37, 2, 5, 128, 128), (300, 3, 4, 331, 525), (200, 4, 6, 513, 129), (1000, 2, 3, 260, 1040),
+                                           (5000, 4, 9, 768, 384), (3000, 8, 20, 1003, 200)])
+def test_products(tide, T, k, E, N, K, kind):
+    g = gen(N + K)
+    ids = draw_ids(g, T, k, E, 0.1)
+    ex, route = routed(tide, E, k, ids)
+    M, held, offsets = T * k, int(route.offsets[-1]), route.offsets.cpu().tolist()
+    W = tide.Fp8Weights(E, N, K, transposed=True)
+    random_fp8(g, W)
+    W.codes_transposed.view(torch.uint8).copy_(W.codes.view(torch.uint8).transpose(1, 2))
+    w = W.codes.cpu().float().double() * W.scales.cpu().double().repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)[:, :, :K]
+    for transposed, n, c in ((False, N, K), (True, K, N)):
+        A = tide.Fp8Rows(M, c)
+        random_fp8(g, A)
+        A.codes.view(torch.uint8)[held:] = 0x7F  # NaN in the rows that no pair has
+        A.scales[held:] = float("nan")
+        a = values(A.codes.cpu().float().double(), A.scales.cpu().double())[:held]
+        for shift, pad in ((0, 0), (3, 5)):
+            out = Guarded(torch.full((M, n + pad), 55.0).to(TYPES[kind]), shift)
+            ex.matmul(A, W, route, out.view[:, :n], transposed=transposed)
+            got = out.cpu()
+            assert bool((got[held:] == 55).all()) and bool((got[:, n:] == 55).all())
+            for e, (x, y) in enumerate(zip(offsets, offsets[1:])):
+                m = w[e] if transposed else w[e].t()
+                want, size = a[x:y] @ m, a[x:y].abs() @ m.abs()
+                err = (got[x:y, :n].double() - want).abs()
+                assert bool((err <= bound(-(-c // 128), size) + HALF[kind] * want.abs() * 1.01).all()), (transposed, e, float((err / (size + 1e-30)).max()))
+    assert ex.device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T, k, E, N, K", [(1, 1, 1, 1, 1), (1, 4, 16, 200, 300), (37, 2, 5, 128, 128), (300, 3, 4, 331, 525), (1000, 2, 3, 260, 1040), (3000, 4, 9, 768, 384)])
+def test_weight_gradients(tide, T, k, E, N, K, kind):
+    g = gen(N + K + 1)
+    ids = draw_ids(g, T, k, E, 0.1)
+    ids[ids == 1] = 0  # an expert without rows
+    ex, route = routed(tide, E, k, ids)
+    M, offsets = T * k, route.offsets.cpu().tolist()
+    dy, a = tide.Fp8Columns(M, N, E), tide.Fp8Columns(M, K, E)
+    grads = [Guarded(torch.full((N * K,), 55.0).to(TYPES[kind]), 3 * e) for e in range(E)]
+    random_fp8(g, dy)
+    random_fp8(g, a)
+    blocks = [-(-(y - x) // 128) for x, y in zip(offsets, offsets[1:])]
+    at = 0
+    for e, b in enumerate(blocks):  # zeros behind each expert's rows, NaN behind the last
+        dy.codes.view(torch.uint8)[:, at * 128 + offsets[e + 1] - offsets[e]:(at + b) * 128] = 0
+        at += b
+    for x in (dy, a):
+        x.codes.view(torch.uint8)[:, at * 128:] = 0x7F
+        x.scales[at:] = float("nan")
+    ex.weight_grad(dy, a, route, [x.view for x in grads])
+    at = 0
+    for e, b in enumerate(blocks):
+        p, q = (values(x.codes.cpu().float().double()[:, at * 128:(at + b) * 128], x.scales.cpu().double()[at:at + b].t()) for x in (dy, a))
+        want, size = p @ q.t(), p.abs() @ q.abs().t()
+        err = (grads[e].cpu().view(N, K).double() - want).abs()
+        assert bool((err <= bound(b, size) + HALF[kind] * want.abs() * 1.01).all()), (e, float((err / (size + 1e-30)).max()))
+        at += b
+    assert ex.device_status() == 0
+    # one tensor of all gradients gets the same bits
+    whole = torch.full((E, N, K), 55.0, device="cuda").to(TYPES[kind])
+    ex.weight_grad(dy, a, route, whole)
+    assert all(torch.equal(whole[e].cpu().flatten(), grads[e].cpu()) for e in range(E))
+
+
+def test_a_product_of_all_rows_without_a_route(tide):
+    """One expert: a plain linear layer's product and gradients."""
+    g = gen(3)
+    M, N, K = 400, 192, 320
+    x, dy, w = torch.randn(M, K, generator=g).bfloat16().cuda(), torch.randn(M, N, generator=g).bfloat16().cuda(), torch.randn(N, K, generator=g).bfloat16().cuda()
+    ex, G = tide.Experts(1, 1), tide.Group(1, [(N, K)])
+    W, X, D, XT, DT = tide.Fp8Weights(1, N, K, True), tide.Fp8Rows(M, K), tide.Fp8Rows(M, N), tide.Fp8Columns(M, K, 1), tide.Fp8Columns(M, N, 1)
+    G.all_gather_fp8([0], [w.view(-1)], W)
+    ex.quantize(x, None, rows=X, columns=XT)
+    ex.quantize(dy, None, rows=D, columns=DT)
+    y, dx, dw = torch.empty(M, N, device="cuda"), torch.empty(M, K, device="cuda"), torch.empty(N, K, device="cuda")
+    ex.matmul(X, W, None, y)
+    ex.matmul(D, W, None, dx, transposed=True)
+    ex.weight_grad(DT, XT, None, [dw])
+    w8 = in_blocks(w.cpu())
+    w8 = w8[0] * w8[1].repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    x8, d8 = values(*in_rows(x.cpu())), values(*in_rows(dy.cpu()))
+    xt8, dt8 = values(*in_rows(x.cpu().t())), values(*in_rows(dy.cpu().t()))
+    for got, p, q in ((y, x8, w8.t()), (dx, d8, w8), (dw, dt8, xt8.t())):
+        assert bool(((got.cpu().double() - p @ q).abs() <= bound(4, p.abs() @ q.abs()) + U * (p @ q).abs()).all())
