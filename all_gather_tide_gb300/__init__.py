@@ -51,6 +51,8 @@ TIDE_SHORT_BATCHES = 64
 TIDE_ADAMW_SKIP_NONFINITE = 0x1
 TIDE_MAX_EXPERTS = 1024
 TIDE_MAX_CHOICES = 32
+TIDE_FP8_TRANSPOSED = 0x1
+TIDE_FP8_ANY_SCALES = 0x2
 
 _lib = None
 _i64p = ctypes.POINTER(ctypes.c_int64)
@@ -138,10 +140,10 @@ SIGNATURES = {
     "tide_experts_quantize": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                              _vp, _vp, _fp8p, _fp8p, _vp]),
     "tide_all_gather_fp8": (ctypes.c_int, [_vp, ctypes.c_int32, _i32p, _vpp, _fp8p, _fp8p, _vp]),
-    "tide_experts_matmul": (ctypes.c_int, [_vp, _fp8p, ctypes.c_int64, _vp, _fp8p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _vp,
+    "tide_experts_matmul": (ctypes.c_int, [_vp, _fp8p, ctypes.c_int64, _vp, _fp8p, ctypes.c_uint32, ctypes.c_int64, ctypes.c_int64, _vp,
                                            ctypes.c_int32, ctypes.c_int64, _vp]),
-    "tide_experts_weight_grad": (ctypes.c_int, [_vp, _fp8p, _fp8p, ctypes.c_int64, _vp, ctypes.c_int64, ctypes.c_int64, _vpp,
-                                                ctypes.c_int32, _vp]),
+    "tide_experts_weight_grad": (ctypes.c_int, [_vp, _fp8p, _fp8p, ctypes.c_int64, _vp, ctypes.c_uint32, ctypes.c_int64, ctypes.c_int64,
+                                                _vpp, ctypes.c_int32, _vp]),
     "tide_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "tide_last_cuda_error": (ctypes.c_int, []),
     "tide_version": (ctypes.c_int, []),
@@ -652,17 +654,18 @@ def tide_all_gather_fp8(g: int, ps, shards: Sequence, w, stream=None) -> None:
     _check(lib().tide_all_gather_fp8(g, len(ps), ps, _ptr_array(shards), w.c, w.c_transposed, _stream(stream)), "tide_all_gather_fp8")
 
 
-def tide_experts_matmul(x: int, a, offsets, w, out, transposed: bool = False, stream=None) -> None:
+def tide_experts_matmul(x: int, a, offsets, w, out, flags: int = 0, stream=None) -> None:
     """``a``: an ``Fp8Rows``; ``w``: an ``Fp8Weights``; ``out``: bf16 or fp32 rows."""
+    transposed = flags & TIDE_FP8_TRANSPOSED
     N, K = (w.K, w.N) if transposed else (w.N, w.K)
     codes = w.c_transposed if transposed else w.c
-    _check(lib().tide_experts_matmul(x, a.c, a.M, _address(offsets), codes, transposed, N, K, out.data_ptr(), _dtype_code(out), _row_stride(out), _stream(stream)),
+    _check(lib().tide_experts_matmul(x, a.c, a.M, _address(offsets), codes, flags, N, K, out.data_ptr(), _dtype_code(out), _row_stride(out), _stream(stream)),
            "tide_experts_matmul")
 
 
-def tide_experts_weight_grad(x: int, dy, a, offsets, grads, grad_type: int = TIDE_BF16, stream=None) -> None:
+def tide_experts_weight_grad(x: int, dy, a, offsets, grads, grad_type: int = TIDE_BF16, flags: int = 0, stream=None) -> None:
     """``dy``, ``a``: ``Fp8Columns``; ``grads``: E tensors or the ``pointer_table`` of them."""
-    _check(lib().tide_experts_weight_grad(x, dy.c, a.c, dy.M, _address(offsets), dy.len, a.len, _ptr_array(grads), grad_type, _stream(stream)),
+    _check(lib().tide_experts_weight_grad(x, dy.c, a.c, dy.M, _address(offsets), flags, dy.len, a.len, _ptr_array(grads), grad_type, _stream(stream)),
            "tide_experts_weight_grad")
 
 
@@ -1135,9 +1138,9 @@ class Experts:
             self._check_fp8(where, columns, Fp8Columns, M, x.shape[-1])
         tide_experts_quantize(self.handle, x, M, None if route is None else route.offsets, route.tokens if gather else None, rows, columns, stream)
 
-    def matmul(self, a: Fp8Rows, w: Fp8Weights, route: Optional[Route], out, transposed: bool = False, stream=None) -> None:
+    def matmul(self, a: Fp8Rows, w: Fp8Weights, route: Optional[Route], out, transposed: bool = False, any_scales: bool = False, stream=None) -> None:
         """Every expert's rows of ``a`` times its matrix of ``w``: ``out[s] = w[e] @ a[s]`` ([T*k, N], bf16 or fp32), or with ``transposed``
-        ``w[e].T @ a[s]`` ([T*k, K])."""
+        ``w[e].T @ a[s]`` ([T*k, K]).  ``any_scales``: scales may be other numbers than powers of two (a checkpoint's)."""
         where = "matmul"
         if not isinstance(w, Fp8Weights) or w.E != self.E or (transposed and w.c_transposed is None) or (_gpus != 1 and _elsewhere(w.codes)):
             _refuse(where, f"the Fp8Weights of {self.E} experts on this GPU are needed, with transposed codes for a transposed product")
@@ -1145,11 +1148,12 @@ class Experts:
         M = self._check_all_rows(where, route, a.M)
         self._check_fp8(where, a, Fp8Rows, M, K)
         self._check_rows(where, out, M, N)
-        tide_experts_matmul(self.handle, a, None if route is None else route.offsets, w, out, transposed, stream)
+        tide_experts_matmul(self.handle, a, None if route is None else route.offsets, w, out, (TIDE_FP8_TRANSPOSED if transposed else 0) | (TIDE_FP8_ANY_SCALES if any_scales else 0),
+                            stream)
 
-    def weight_grad(self, dy: Fp8Columns, a: Fp8Columns, route: Optional[Route], grads, grad_type: int = TIDE_BF16, stream=None) -> None:
+    def weight_grad(self, dy: Fp8Columns, a: Fp8Columns, route: Optional[Route], grads, grad_type: int = TIDE_BF16, any_scales: bool = False, stream=None) -> None:
         """The gradient of every expert's matrix, ``dy[e].T @ a[e]``, into ``grads``: E contiguous tensors of N*K elements, bf16 or
-        fp32, one tensor [E, N, K], or the ``pointer_table`` of E tensors of ``grad_type``."""
+        fp32, one tensor [E, N, K], or the ``pointer_table`` of E tensors of ``grad_type``.  ``any_scales`` as ``matmul``'s."""
         where = "weight_grad"
         M = self._check_all_rows(where, route, dy.M)
         self._check_fp8(where, dy, Fp8Columns, M, dy.len)
@@ -1170,7 +1174,7 @@ class Experts:
                     _refuse(where, f"a contiguous gradient of {self.E} x {dy.len} x {a.len} elements on the GPU is needed")
                 first, each = grads.data_ptr(), dy.len * a.len * grads.element_size()
                 grads = self._table(*range(first, first + self.E * each, each))
-        tide_experts_weight_grad(self.handle, dy, a, None if route is None else route.offsets, grads, grad_type, stream)
+        tide_experts_weight_grad(self.handle, dy, a, None if route is None else route.offsets, grads, grad_type, TIDE_FP8_ANY_SCALES if any_scales else 0, stream)
 
     # ---- checks ----
 

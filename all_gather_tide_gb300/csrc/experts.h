@@ -72,9 +72,9 @@ struct GradPtrs {
     void* p[TIDE_MAX_EXPERTS];
 };
 // TIDE_OK or a negative status.
-int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, const tide_fp8_t& w, int transposed, int64_t N, int64_t K,
+int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, const tide_fp8_t& w, uint32_t flags, int64_t N, int64_t K,
                   void* out, int out_bf16, int64_t out_stride, const Ctas& c, int* status, uint64_t timeout_ns, cudaStream_t stream);
-int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, int64_t N, int64_t K,
+int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, uint32_t flags, int64_t N, int64_t K,
                        const GradPtrs& grads, int grad_bf16, const Ctas& c, int* status, uint64_t timeout_ns, cudaStream_t stream);
 
 }  // namespace tide

@@ -234,28 +234,29 @@ int tide_experts_quantize(tide_experts_t x, const void* src, int32_t type, int64
     });
 }
 
-int tide_experts_matmul(tide_experts_t x, const tide_fp8_t* a, int64_t M, const int32_t* offsets, const tide_fp8_t* w, int32_t transposed, int64_t N, int64_t K, void* out,
+int tide_experts_matmul(tide_experts_t x, const tide_fp8_t* a, int64_t M, const int32_t* offsets, const tide_fp8_t* w, uint32_t flags, int64_t N, int64_t K, void* out,
                         int32_t out_type, int64_t out_stride, void* stream) {
     return no_throw([&]() -> int {
         const size_t elem = float_size(out_type);
-        if (!x || !a || !w || !elem || M < 0 || N < 1 || K < 1 || (transposed != 0 && transposed != 1)) return TIDE_EINVAL;
+        if (!x || !a || !w || !elem || M < 0 || N < 1 || K < 1 || (flags & ~(TIDE_FP8_TRANSPOSED | TIDE_FP8_ANY_SCALES))) return TIDE_EINVAL;
         if (M > tide::kMaxPairs || N > kMaxLen || K > kMaxLen) return TIDE_ERANGE;
+        const bool transposed = flags & TIDE_FP8_TRANSPOSED;
         int rc = check_offsets(x, offsets);
         if (rc == TIDE_OK) rc = check_fp8(*a, M, K, M, blocks_of(K), 1, true);
         if (rc == TIDE_OK) rc = check_fp8(*w, N, K, blocks_of(transposed ? K : N), blocks_of(transposed ? N : K), x->E, true);
         if (rc == TIDE_OK) rc = check_rows(out, M, out_stride, N, elem);
         if (rc == TIDE_OK) rc = tide::check_device(x->device);
         if (rc != TIDE_OK) return rc;
-        return tide::launch_matmul(*a, M, x->E, offsets, *w, transposed, N, K, out, out_type == TIDE_BF16, out_stride, ctas_of(x), x->d_status, timeout_of(x),
+        return tide::launch_matmul(*a, M, x->E, offsets, *w, flags, N, K, out, out_type == TIDE_BF16, out_stride, ctas_of(x), x->d_status, timeout_of(x),
                                    static_cast<cudaStream_t>(stream));
     });
 }
 
-int tide_experts_weight_grad(tide_experts_t x, const tide_fp8_t* dy, const tide_fp8_t* a, int64_t M, const int32_t* offsets, int64_t N, int64_t K, void* const* grads,
-                             int32_t grad_type, void* stream) {
+int tide_experts_weight_grad(tide_experts_t x, const tide_fp8_t* dy, const tide_fp8_t* a, int64_t M, const int32_t* offsets, uint32_t flags, int64_t N, int64_t K,
+                             void* const* grads, int32_t grad_type, void* stream) {
     return no_throw([&]() -> int {
         const size_t elem = float_size(grad_type);
-        if (!x || !dy || !a || !grads || !elem || M < 0 || N < 1 || K < 1) return TIDE_EINVAL;
+        if (!x || !dy || !a || !grads || !elem || M < 0 || N < 1 || K < 1 || (flags & ~TIDE_FP8_ANY_SCALES)) return TIDE_EINVAL;
         if (M > tide::kMaxPairs || N > kMaxLen || K > kMaxLen) return TIDE_ERANGE;
         int rc = check_offsets(x, offsets);
         const int64_t blocks = tide::padded_blocks(M, x->E);
@@ -269,7 +270,7 @@ int tide_experts_weight_grad(tide_experts_t x, const tide_fp8_t* dy, const tide_
             ptrs.p[e] = grads[e];
         }
         if ((rc = tide::check_device(x->device)) != TIDE_OK) return rc;
-        return tide::launch_weight_grad(*dy, *a, M, x->E, offsets, N, K, ptrs, grad_type == TIDE_BF16, ctas_of(x), x->d_status, timeout_of(x),
+        return tide::launch_weight_grad(*dy, *a, M, x->E, offsets, flags, N, K, ptrs, grad_type == TIDE_BF16, ctas_of(x), x->d_status, timeout_of(x),
                                         static_cast<cudaStream_t>(stream));
     });
 }

@@ -523,9 +523,12 @@ int tide_adamw(tide_tensors_t t, void *const *params, const void *const *grads, 
  * infinity) times the fp32 scale of its block of 128 values: 1 x 128 of a row, or 128 x 128 of a weight.
  * The calls that write them take for a block whose largest magnitude is a > 0 the smallest power of two
  * from 2^-126 to 2^120 with a / scale <= 448 (1 for a block of zeros), and code = x / scale rounded to
- * nearest even; a block with a NaN or an infinity gets a NaN scale.  The calls that read them accept any
- * scales.
+ * nearest even; a block with a NaN or an infinity gets a NaN scale.  The calls that read them take such scales,
+ * which the tensor cores apply (another number counts as the power of two below it, and sets 2 in the status
+ * word, if that holds 0), or with TIDE_FP8_ANY_SCALES any, at a lower rate.
  */
+#define TIDE_FP8_TRANSPOSED 0x1u
+#define TIDE_FP8_ANY_SCALES 0x2u
 typedef struct tide_fp8 {
     void *codes;          /* device, 16-byte aligned; the matrix's rows are `stride` bytes apart */
     int64_t stride;       /* a multiple of 16, at least the row length; bytes behind a row's end in the last of
@@ -553,8 +556,8 @@ typedef struct tide_experts *tide_experts_t;
 int tide_experts_create(tide_experts_t *out, int32_t E, int32_t k, uint32_t flags);
 /* Frees the object; the work that uses it must have ended.  NULL is accepted. */
 int tide_experts_destroy(tide_experts_t x);
-/* Reads the status word (0; 1 = a wait of a product's kernel expired; 64 = tide_experts_sort met an
- * expert >= E) and clears it.  Synchronous: copies from the device. */
+/* Reads the status word (0; 1 = a wait of a product's kernel expired; 2 = a product met a scale that is no power of
+ * two; 64 = tide_experts_sort met an expert >= E) and clears it.  Synchronous: copies from the device. */
 int tide_experts_device_status(tide_experts_t x, int32_t *status);
 /* Every wait of the products' kernels gives up after `timeout_ns` (0 = the default, 2 s). */
 int tide_experts_set_wait_timeout(tide_experts_t x, uint64_t timeout_ns);
@@ -659,13 +662,13 @@ int tide_all_gather_fp8(tide_group_t g, int32_t E, const int32_t *ps, const void
  * for the rows s of expert e (offsets[e] <= s < offsets[e+1]) and 0 <= n < N, c < K; blocks' sums and their total
  * in fp32, rounded once to out_type (TIDE_BF16 or TIDE_F32).  Rows from offsets[E] on are left as they are.
  *   a: M rows of K codes.   w: E matrices of N rows of K codes.   offsets: as tide_experts_quantize's.
- *   transposed: 0; or 1 where w->codes are tide_all_gather_fp8's wt and w->scales those of its w, of which the scale
- *   of (n, block b) is then [e, b, n/128]: the product with the untransposed weights of K rows of N, the gradient
- *   of the rows.
+ *   flags: TIDE_FP8_ANY_SCALES, and TIDE_FP8_TRANSPOSED where w->codes are tide_all_gather_fp8's wt and w->scales those
+ *   of its w, of which the scale of (n, block b) is then [e, b, n/128]: the product with the untransposed weights of K
+ *   rows of N, the gradient of the rows.
  *   out: M rows of N elements, out_stride (>= N) apart.
  */
 int tide_experts_matmul(tide_experts_t x, const tide_fp8_t *a, int64_t M, const int32_t *offsets, const tide_fp8_t *w,
-                        int32_t transposed, int64_t N, int64_t K, void *out, int32_t out_type, int64_t out_stride,
+                        uint32_t flags, int64_t N, int64_t K, void *out, int32_t out_type, int64_t out_stride,
                         void *stream);
 
 /*
@@ -674,11 +677,12 @@ int tide_experts_matmul(tide_experts_t x, const tide_fp8_t *a, int64_t M, const 
  *     grads_e[n*K + c] = sum over blocks b of 128 rows of e of dy.scale[b, n] * a.scale[b, c] * sum over s in b of dy[n, s] * a[c, s]
  * in fp32, rounded once; zeros for an expert without rows.
  *   dy, a: N and K rows of tide_fp8_padded_rows(M, E) codes, as tide_experts_quantize writes columns.
+ *   flags: 0 or TIDE_FP8_ANY_SCALES.
  *   grads: host array of E device pointers to contiguous N x K gradients of grad_type (TIDE_BF16, as
  *   tide_reduce_scatter reads them, or TIDE_F32).
  */
 int tide_experts_weight_grad(tide_experts_t x, const tide_fp8_t *dy, const tide_fp8_t *a, int64_t M, const int32_t *offsets,
-                             int64_t N, int64_t K, void *const *grads, int32_t grad_type, void *stream);
+                             uint32_t flags, int64_t N, int64_t K, void *const *grads, int32_t grad_type, void *stream);
 
 /* ---- interference probes (measurement kernels of the interference harness) ----------------- */
 /*

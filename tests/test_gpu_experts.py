@@ -2,9 +2,9 @@
 
 Order, copies, codes and scales are compared bit for bit.  Sums of n products in fp32 (u = 2^-24) are off by at most
 (n + 1) u times the sum of the products' magnitudes, and the result by half a step of its type more.  In a product of
-8-bit matrices the 128 products of a block are exact and added by the tensor cores, taken to lose at most 2u of
-the block's magnitudes with each; the blocks' sums are scaled (at most three roundings) and added in fp32: (128 + blocks + 3) * 2u
-of the sum of all magnitudes.  Buffers have guard bands around them.
+8-bit matrices the products are exact and added by the tensor cores, 32 at a time, taken to lose at most 2u of the magnitudes
+so far with each step of 32 and of the block's with each product; blocks' sums that are scaled apart have at most three
+roundings each and are added in fp32: (128 + blocks + 3) * 2u of the sum of all magnitudes bounds both up to 33 blocks.  Buffers have guard bands around them.
 """
 import ctypes
 
@@ -353,13 +353,13 @@ def test_parts_of_weights_side_by_side(tide):
 # ---- products --------------------------------------------------------------------------------------
 
 
-def random_fp8(g, x, scales=True):
-    """Fills codes with finite values of all sizes and scales with numbers that are no powers of two."""
+def random_fp8(g, x, any_scales):
+    """Fills codes with finite values of all sizes and scales with powers of two, or numbers that are none."""
     bits = torch.randint(0, 256, tuple(x.codes.shape), generator=g).to(torch.uint8)
     bits[(bits & 0x7F) == 0x7F] = 0x3A
     x.codes.view(torch.uint8).copy_(bits)
-    if scales:
-        x.scales.copy_(torch.exp(torch.randn(tuple(x.scales.shape), generator=g)))
+    r = torch.randn(tuple(x.scales.shape), generator=g)
+    x.scales.copy_(torch.exp(r) if any_scales else torch.exp2(torch.round(2 * r)))
 
 
 def bound(blocks, size):
@@ -369,24 +369,25 @@ def bound(blocks, size):
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("T, k, E, N, K", [(1, 1, 1, 1, 1), (1, 8, 16, 200, 300), (37, 2, 5, 128, 128), (300, 3, 4, 331, 525), (200, 4, 6, 513, 129), (1000, 2, 3, 260, 1040),
                                            (5000, 4, 9, 768, 384), (3000, 8, 20, 1003, 200)])
-def test_products(tide, T, k, E, N, K, kind):
+@pytest.mark.parametrize("any_scales", [False, True])
+def test_products(tide, T, k, E, N, K, kind, any_scales):
     g = gen(N + K)
     ids = draw_ids(g, T, k, E, 0.1)
     ex, route = routed(tide, E, k, ids)
     M, held, offsets = T * k, int(route.offsets[-1]), route.offsets.cpu().tolist()
     W = tide.Fp8Weights(E, N, K, transposed=True)
-    random_fp8(g, W)
+    random_fp8(g, W, any_scales)
     W.codes_transposed.view(torch.uint8).copy_(W.codes.view(torch.uint8).transpose(1, 2))
     w = W.codes.cpu().float().double() * W.scales.cpu().double().repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)[:, :, :K]
     for transposed, n, c in ((False, N, K), (True, K, N)):
         A = tide.Fp8Rows(M, c)
-        random_fp8(g, A)
+        random_fp8(g, A, any_scales)
         A.codes.view(torch.uint8)[held:] = 0x7F  # NaN in the rows that no pair has
         A.scales[held:] = float("nan")
         a = values(A.codes.cpu().float().double(), A.scales.cpu().double())[:held]
         for shift, pad in ((0, 0), (3, 5)):
             out = Guarded(torch.full((M, n + pad), 55.0).to(TYPES[kind]), shift)
-            ex.matmul(A, W, route, out.view[:, :n], transposed=transposed)
+            ex.matmul(A, W, route, out.view[:, :n], transposed=transposed, any_scales=any_scales)
             got = out.cpu()
             assert bool((got[held:] == 55).all()) and bool((got[:, n:] == 55).all())
             for e, (x, y) in enumerate(zip(offsets, offsets[1:])):
@@ -399,7 +400,8 @@ def test_products(tide, T, k, E, N, K, kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("T, k, E, N, K", [(1, 1, 1, 1, 1), (1, 4, 16, 200, 300), (37, 2, 5, 128, 128), (300, 3, 4, 331, 525), (1000, 2, 3, 260, 1040), (3000, 4, 9, 768, 384)])
-def test_weight_gradients(tide, T, k, E, N, K, kind):
+@pytest.mark.parametrize("any_scales", [False, True])
+def test_weight_gradients(tide, T, k, E, N, K, kind, any_scales):
     g = gen(N + K + 1)
     ids = draw_ids(g, T, k, E, 0.1)
     ids[ids == 1] = 0  # an expert without rows
@@ -407,8 +409,8 @@ def test_weight_gradients(tide, T, k, E, N, K, kind):
     M, offsets = T * k, route.offsets.cpu().tolist()
     dy, a = tide.Fp8Columns(M, N, E), tide.Fp8Columns(M, K, E)
     grads = [Guarded(torch.full((N * K,), 55.0).to(TYPES[kind]), 3 * e) for e in range(E)]
-    random_fp8(g, dy)
-    random_fp8(g, a)
+    random_fp8(g, dy, any_scales)
+    random_fp8(g, a, any_scales)
     blocks = [-(-(y - x) // 128) for x, y in zip(offsets, offsets[1:])]
     at = 0
     for e, b in enumerate(blocks):  # zeros behind each expert's rows, NaN behind the last
@@ -417,7 +419,7 @@ def test_weight_gradients(tide, T, k, E, N, K, kind):
     for x in (dy, a):
         x.codes.view(torch.uint8)[:, at * 128:] = 0x7F
         x.scales[at:] = float("nan")
-    ex.weight_grad(dy, a, route, [x.view for x in grads])
+    ex.weight_grad(dy, a, route, [x.view for x in grads], any_scales=any_scales)
     at = 0
     for e, b in enumerate(blocks):
         p, q = (values(x.codes.cpu().float().double()[:, at * 128:(at + b) * 128], x.scales.cpu().double()[at:at + b].t()) for x in (dy, a))
@@ -428,7 +430,7 @@ def test_weight_gradients(tide, T, k, E, N, K, kind):
     assert ex.device_status() == 0
     # one tensor of all gradients gets the same bits
     whole = torch.full((E, N, K), 55.0, device="cuda").to(TYPES[kind])
-    ex.weight_grad(dy, a, route, whole)
+    ex.weight_grad(dy, a, route, whole, any_scales=any_scales)
     assert all(torch.equal(whole[e].cpu().flatten(), grads[e].cpu()) for e in range(E))
 
 
@@ -452,3 +454,33 @@ def test_a_product_of_all_rows_without_a_route(tide):
     xt8, dt8 = values(*in_rows(x.cpu().t())), values(*in_rows(dy.cpu().t()))
     for got, p, q in ((y, x8, w8.t()), (dx, d8, w8), (dw, dt8, xt8.t())):
         assert bool(((got.cpu().double() - p @ q).abs() <= bound(4, p.abs() @ q.abs()) + U * (p @ q).abs()).all())
+
+
+def test_scales_that_are_no_powers_of_two_are_told_of(tide):
+    for bad in (1.5, 0.0, -2.0):
+        ex, W, A, out = tide.Experts(1, 1), tide.Fp8Weights(1, 130, 200), tide.Fp8Rows(9, 200), torch.empty(9, 130, device="cuda")
+        random_fp8(gen(0), W, False)
+        random_fp8(gen(1), A, False)
+        ex.matmul(A, W, None, out)
+        assert ex.device_status() == 0
+        A.scales[8, 1] = bad
+        ex.matmul(A, W, None, out)
+        assert ex.device_status() == 2
+        A.scales[8, 1] = 1.0
+        W.scales[0, 1, 0] = bad
+        ex.matmul(A, W, None, out)
+        assert ex.device_status() == 2 and ex.device_status() == 0
+
+
+def test_a_nan_scale_makes_its_rows_nan_alone(tide):
+    ex, W, A, out = tide.Experts(1, 1), tide.Fp8Weights(1, 300, 400), tide.Fp8Rows(200, 400), torch.empty(200, 300, device="cuda")
+    for any_scales in (False, True):
+        random_fp8(gen(0), W, False)
+        random_fp8(gen(1), A, False)
+        A.scales[70, 2] = float("nan")
+        W.scales[0, 1, 3] = float("nan")
+        ex.matmul(A, W, None, out, any_scales=any_scales)
+        want = torch.zeros(200, 300, dtype=torch.bool)
+        want[70] = True
+        want[:, 128:256] = True
+        assert torch.equal(torch.isnan(out).cpu(), want) and ex.device_status() == 0
