@@ -972,7 +972,7 @@ class Fp8Rows:
 
         self.M, self.len = M, len
         self.codes = _bytes_as_e4m3(M, _up(len, 16))[:, :len]
-        self.scales = torch.empty(M, -(-len // 128), device="cuda")
+        self.scales = torch.empty(M, _up(-(-len // 128), 4), device="cuda")[:, :-(-len // 128)]
         self.c = _fp8_struct(self.codes, self.scales)
 
 
@@ -1000,7 +1000,7 @@ class Fp8Weights:
         import torch
 
         codes = _bytes_as_e4m3(E, N, _up(K, 16))[:, :, :K]
-        scales = torch.empty(E, -(-N // 128), -(-K // 128), device="cuda")
+        scales = torch.empty(E, -(-N // 128), _up(-(-K // 128), 4), device="cuda")[:, :, :-(-K // 128)]
         self._hold(codes, scales, _bytes_as_e4m3(E, K, _up(N, 16))[:, :, :N] if transposed else None)
 
     def _hold(self, codes, scales, codes_transposed) -> None:

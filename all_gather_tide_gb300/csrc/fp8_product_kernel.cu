@@ -27,10 +27,9 @@ constexpr int kSumWarps = 8;
 constexpr int kTmemCols = 512;
 constexpr int kStatusWait = 1, kStatusScale = 2;
 
-template <int BN>
-constexpr int kTileBytes = (kTileM + BN) * kBlock;
-template <int BN>
-constexpr int kStages = 196608 / kTileBytes<BN>;
+// A CTA's share of a stage: 128 rows of A and its part of B's BN, half of them where two CTAs work on one tile.
+__host__ __device__ constexpr int share_bytes(int bn, bool pair) { return (kTileM + (pair ? bn / 2 : bn)) * kBlock; }
+__host__ __device__ constexpr int stages_of(int bn, bool pair) { return 196608 / share_bytes(bn, pair); }
 
 struct ProductArgs {
     CUtensorMap a, b;
@@ -45,6 +44,7 @@ struct ProductArgs {
     int32_t most_blocks;  // of the transposed operands (gradient only)
     void* out;
     int64_t out_stride;
+    int scale_vectors;  // scales of consecutive blocks can be read four at a time
     int out_vectors;  // rows of the result can be written 32 bytes at a time
     GradPtrs grads;
     int* status;
@@ -62,9 +62,20 @@ __device__ __forceinline__ void barrier_arrive(uint64_t* bar) { asm volatile("mb
 __device__ __forceinline__ void barrier_expect(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
+// The barrier at the same place of the pair's first CTA.
+__device__ __forceinline__ uint32_t of_first_cta(uint64_t* bar) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
+    return at;
+}
+template <bool Pair>
+__device__ __forceinline__ void arrive_at_first(uint64_t* bar) {
+    if constexpr (Pair) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_first_cta(bar)) : "memory");
+    else barrier_arrive(bar);
+}
 __device__ __forceinline__ bool barrier_try(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
     return ok != 0;
 }
 
@@ -97,24 +108,37 @@ struct Cursor {
     }
 };
 
+// Boxes of codes; a pair's count at the barrier of its first CTA.
+template <bool Pair>
 __device__ __forceinline__ void load_2d(void* to, const CUtensorMap* map, int32_t x, int32_t y, uint64_t* bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(to)), "l"(map), "r"(x), "r"(y),
-                 "r"(smem_u32(bar))
-                 : "memory");
+    if constexpr (Pair)
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(to)), "l"(map), "r"(x),
+                     "r"(y), "r"(of_first_cta(bar))
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(to)), "l"(map), "r"(x), "r"(y),
+                     "r"(smem_u32(bar))
+                     : "memory");
 }
+template <bool Pair>
 __device__ __forceinline__ void load_3d(void* to, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(to)), "l"(map), "r"(x), "r"(y), "r"(z),
-                 "r"(smem_u32(bar))
-                 : "memory");
+    if constexpr (Pair)
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(to)), "l"(map), "r"(x),
+                     "r"(y), "r"(z), "r"(of_first_cta(bar))
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(to)), "l"(map), "r"(x), "r"(y),
+                     "r"(z), "r"(smem_u32(bar))
+                     : "memory");
 }
 
 // A tile of rows of 128 bytes, swizzled in groups of 8 rows (1024 bytes), K along the row.
 __device__ __forceinline__ uint64_t tile_descriptor(const void* tile) {
     return uint64_t((smem_u32(tile) & 0x3ffff) >> 4) | uint64_t(1) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
 }
-// fp32 sums of e4m3 products, both operands K-major.
-template <int BN>
-constexpr uint32_t kInstruction = 1u << 4 | uint32_t(BN >> 3) << 17 | uint32_t(kTileM >> 4) << 24;
+// Instruction descriptors: fp32 sums of e4m3 products, both operands K-major, BN columns; with scales, exponents of 8 bits.
+__host__ __device__ constexpr uint32_t plain_instruction(int bn) { return 1u << 4 | uint32_t(bn >> 3) << 17 | uint32_t(kTileM >> 4) << 24; }
+__host__ __device__ constexpr uint32_t scaled_instruction(int bn, bool pair) { return 1u << 23 | uint32_t(bn >> 3) << 17 | uint32_t((pair ? 2 * kTileM : kTileM) >> 4) << 24; }
 
 __device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t instruction, bool add) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(instruction),
@@ -122,21 +146,32 @@ __device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uin
                  : "memory");
 }
 // The same with a power of two for each row of A and of B, whose exponents lie in Tensor Memory: row r's in lane r % 32 (and
-// at the same place in each quarter), column r / 32, lowest byte.
-template <int BN>
-constexpr uint32_t kScaledInstruction = 1u << 23 | uint32_t(BN >> 3) << 17 | uint32_t(kTileM >> 4) << 24;
+// at the same place in each quarter), column r / 32, in the byte that the instruction names.
+template <bool Pair>
 __device__ __forceinline__ void multiply_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t instruction, uint32_t a_scales, uint32_t b_scales, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(instruction), "r"(a_scales), "r"(b_scales), "r"(uint32_t(add))
-                 : "memory");
+    if constexpr (Pair)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(instruction), "r"(a_scales), "r"(b_scales), "r"(uint32_t(add))
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(instruction), "r"(a_scales), "r"(b_scales), "r"(uint32_t(add))
+                     : "memory");
 }
-// 128 rows' exponents, 16 bytes for each of 32 lanes, into four columns of all quarters.
+// 128 rows' exponents, 16 bytes for each of 32 lanes, into four columns of all quarters; a pair's CTAs each their own.
+template <bool Pair>
 __device__ __forceinline__ void copy_exponents(uint32_t to, const void* from) {
     const uint64_t descriptor = uint64_t((smem_u32(from) & 0x3ffff) >> 4) | uint64_t(128 >> 4) << 32 | uint64_t(1) << 46;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(descriptor) : "memory");
+    if constexpr (Pair) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(descriptor) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(descriptor) : "memory");
 }
+// The barrier, that of each CTA of a pair, is arrived at when all that this thread issued has ended.
+template <bool Pair>
 __device__ __forceinline__ void commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    if constexpr (Pair)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // 32 columns of this warp's 32 rows.
@@ -171,42 +206,45 @@ __device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
 
 // What a CTA does next: a tile's operands, blocks and place.
 struct Tile {
-    int e, row0, rows_end, col0;  // rows row0.. (to rows_end) and columns col0.. of the result
-    int a_row, k0, blocks;        // first row of A, first column of both operands, blocks of 128 of them
+    int e, row0, rows_end, col0;  // rows row0.. (to rows_end; of A too) and columns col0.. of the result
+    int k0, blocks;               // first column of both operands, blocks of 128 of them
 };
 
-template <int BN, bool Grad>
+// Tiles of `Rows` rows and BN columns.
+template <int Rows, int BN, bool Grad>
 struct Tiles {
     const ProductArgs& p;
-    const int32_t* starts;  // [E + 1] tiles of 128 rows before each expert
+    const int32_t* starts;  // [E + 1] before each expert: tiles down the result, or blocks of a gradient's operands
     const int32_t* first;   // [E + 1] first row of each expert
     uint32_t across, down;
+    int64_t count;
     // All of the block's threads call it.
     __device__ __forceinline__ Tiles(const ProductArgs& p, int32_t* starts, int32_t* first, int32_t* sums)
-        : p(p), starts(starts), first(first), across(uint32_t((p.N + BN - 1) / BN)), down(uint32_t((p.rows + kTileM - 1) / kTileM)) {
+        : p(p), starts(starts), first(first), across(uint32_t((p.N + BN - 1) / BN)), down(uint32_t((p.rows + Rows - 1) / Rows)) {
+        constexpr int kUnit = Grad ? kBlock : Rows;
         for (int e = threadIdx.x; e <= p.E; e += kProductThreads) {
             const Span s = span_of(p.offsets, min(e, p.E - 1), p.M);
             first[e] = e < p.E ? s.first : s.first + s.count;
         }
-        exclusive_sums(starts, p.E, sums, [&](int e) { return (span_of(p.offsets, e, p.M).count + kTileM - 1) / kTileM; });
+        exclusive_sums(starts, p.E, sums, [&](int e) { return (span_of(p.offsets, e, p.M).count + kUnit - 1) / kUnit; });
         if (Grad) {  // whatever the offsets hold, no tile reaches past the transposed operands
             for (int e = threadIdx.x; e <= p.E; e += kProductThreads) starts[e] = min(starts[e], p.most_blocks);
             __syncthreads();
         }
+        count = Grad ? int64_t(p.E) * across * down : int64_t(starts[p.E]) * across;
     }
-    __device__ __forceinline__ int64_t count() const { return Grad ? int64_t(p.E) * across * down : int64_t(starts[p.E]) * across; }
     __device__ __forceinline__ Tile at(int64_t it) const {
         Tile t;
         if (Grad) {
             const uint32_t each = across * down;
             t.e = int(it / each);
             const uint32_t in = uint32_t(it - int64_t(t.e) * each), d = in / across;
-            t.row0 = t.a_row = int(d) * kTileM, t.rows_end = p.rows, t.col0 = int(in - d * across) * BN;
+            t.row0 = int(d) * Rows, t.rows_end = p.rows, t.col0 = int(in - d * across) * BN;
             t.k0 = starts[t.e] * kBlock, t.blocks = starts[t.e + 1] - starts[t.e];
         } else {
             const int32_t d = int32_t(it / across);
             t.e = last_at_most(starts, p.E, d);
-            t.row0 = t.a_row = first[t.e] + (d - starts[t.e]) * kTileM;
+            t.row0 = first[t.e] + (d - starts[t.e]) * Rows;
             t.rows_end = first[t.e + 1];
             t.col0 = int(it - int64_t(d) * across) * BN;
             t.k0 = 0, t.blocks = (p.K + kBlock - 1) / kBlock;
@@ -215,40 +253,44 @@ struct Tiles {
     }
 };
 
-// The loads of all of a CTA's tiles.
-template <int BN, bool Grad>
-__device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles<BN, Grad>& tiles, int64_t count, unsigned char* ring, uint64_t* full, uint64_t* empty, const Waits& wait) {
+// The loads of all of a CTA's tiles; a pair's CTAs each load their rows of A and their half of B's.
+template <int BN, bool Pair, bool Grad, typename Tiles>
+__device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles& tiles, int rank, int64_t begin, int64_t step, unsigned char* ring, uint64_t* full, uint64_t* empty,
+                                           const Waits& wait) {
+    constexpr int kShare = share_bytes(BN, Pair), kStages = stages_of(BN, Pair);
     Cursor s;
     int64_t uses = 0;
     bool ok = true;
-    for (int64_t it = blockIdx.x; ok && it < count; it += gridDim.x) {
+    for (int64_t it = begin; ok && it < tiles.count; it += step) {
         const Tile t = tiles.at(it);
+        const int row = t.row0 + rank * kTileM, col = t.col0 + rank * (BN / 2);
         for (int b = 0; b < t.blocks; ++b) {
             if (!(ok = wait(&empty[s.at], s.phase ^ 1))) break;
-            unsigned char* a = ring + s.at * kTileBytes<BN>;
-            barrier_expect(&full[s.at], kTileBytes<BN>);
-            load_2d(a, &p.a, t.k0 + b * kBlock, t.a_row, &full[s.at]);
-            if (Grad) load_2d(a + kTileM * kBlock, &p.b, t.k0 + b * kBlock, t.col0, &full[s.at]);
-            else load_3d(a + kTileM * kBlock, &p.b, b * kBlock, t.col0, t.e, &full[s.at]);
-            s.next(kStages<BN>);
+            unsigned char* a = ring + s.at * kShare;
+            if (rank == 0) barrier_expect(&full[s.at], Pair ? 2 * kShare : kShare);
+            load_2d<Pair>(a, &p.a, t.k0 + b * kBlock, row, &full[s.at]);
+            if (Grad) load_2d<Pair>(a + kTileM * kBlock, &p.b, t.k0 + b * kBlock, col, &full[s.at]);
+            else load_3d<Pair>(a + kTileM * kBlock, &p.b, b * kBlock, col, t.e, &full[s.at]);
+            s.next(kStages);
             ++uses;
         }
     }
-    // no copy, and no arrival of the products that read it, is left on its way to this CTA's memory; a stopped CTA
-    // waits for its copies alone
+    // No copy, and no arrival of the products that read it, is left on its way to this CTA's memory. One that was
+    // stopped waits for its copies alone: 20 ms, or until they are counted as landed where the barrier is its own.
     const bool all = ok && !*wait.stop;
-    for (int64_t u = max(int64_t(0), uses - kStages<BN>); u < uses; ++u) {
-        const int at = int(u % kStages<BN>);
-        const uint32_t parity = uint32_t(u / kStages<BN>) & 1;
-        const uint64_t end = globaltimer() + (all ? p.timeout_ns : 100000000ull);
-        while (!barrier_try(all ? &empty[at] : &full[at], parity) && globaltimer() < end) {
+    for (int64_t u = max(int64_t(0), uses - kStages); u < uses; ++u) {
+        const int at = int(u % kStages);
+        const uint32_t parity = uint32_t(u / kStages) & 1;
+        const uint64_t end = globaltimer() + (all ? p.timeout_ns : 20000000ull);
+        while (!((all || rank == 0) && barrier_try(all ? &empty[at] : &full[at], parity)) && globaltimer() < end) {
         }
     }
 }
 
 // The products on their way end before the Tensor Memory is given back.
+template <bool Pair>
 __device__ __forceinline__ void end_products(uint64_t* ended) {
-    commit(ended);
+    commit<Pair>(ended);
     const uint64_t end = globaltimer() + 100000000ull;
     while (!barrier_try(ended, 0) && globaltimer() < end) {
     }
@@ -284,152 +326,196 @@ __device__ __forceinline__ void put_sums(Out* to, const uint32_t (&x)[Count], in
 
 // ---- scales that are powers of two ------------------------------------------------------------------
 //
-// Two warps turn the scales of A's rows and B's into exponents beside each stage's tiles, from where the MMA thread copies
-// them to Tensor Memory. Two tiles' sums lie there at a time, so that one's are taken out while the next is
+// Two warps turn the scales of A's rows and B's into exponents, four blocks' to a word, from where the MMA thread copies them
+// to Tensor Memory once for those blocks. Two tiles' sums lie there at a time, so that one's are taken out while the next is
 // multiplied; for BN = 256 they share 32 columns, as the exponents need 24 of the 512: the warps that hold the
 // shared columns take these out first and the next tile begins then.
-constexpr int kExponentCols = 480;  // from here on; a stage's take 4 + 8, two stages' lie there
-template <int BN>
-constexpr int kExponentBytes = 4 * (kTileM + BN);
-template <int BN>
-constexpr int kSecondTile = BN == 256 ? 224 : BN;  // column of the other tile's sums
+//
+// With Pair two CTAs, on the two SMs of a cluster, work on one tile of 256 rows and BN columns: each loads 128 rows of A
+// and half of B's, the first one's MMA thread multiplies for both, and each takes out its own rows. An SM's shared memory then
+// takes in and gives out 32 KB each for 512 cycles of products, of the 128 bytes a cycle that it has for both; a tile of
+// 128 x 256 of its own needs 48 KB each, 768 cycles.
+constexpr int kExponentCols = 480;  // from here on; four blocks' take 4 + 8, two such groups' lie there
+constexpr int kAhead = 4;           // blocks in a word
+__host__ __device__ constexpr int exponent_bytes(int bn) { return 4 * (kTileM + bn); }
+__host__ __device__ constexpr int second_tile(int bn) { return bn == 256 ? 224 : bn; }  // column of the other tile's sums
 
-// A scale as a power of two's exponent, biased; `count`: whether its row is there and another number is to be told of.
-__device__ __forceinline__ uint32_t exponent_of(float scale, bool count, bool& bad) {
+// A scale as a power of two's exponent, biased; `there`: whether its row is, and another number is to be told of.
+__device__ __forceinline__ uint32_t exponent_of(float scale, bool there, bool& bad) {
     const uint32_t bits = __float_as_uint(scale), e = bits >> 23;
-    bad |= count && (((bits & 0x7fffffu) != 0 && e != 255) || e - 1 > 254);
+    bad |= there && (((bits & 0x7fffffu) != 0 && e != 255) || e - 1 > 254);
     return e & 255;
 }
 
-template <int BN, bool Grad, typename Out>
+// One warp's part: the exponents of A's rows, from `row0` of the tile on, or of B's, Count rows for each lane (lane, lane + 32,
+// ...). The next group's scales are on their way while one is written.
+template <int Rows, int BN, bool Grad, int Count, typename Tiles>
+__device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tiles& tiles, bool of_a, int row0, int64_t begin, int64_t step, unsigned char* exponents, int bytes,
+                                                uint64_t* full, uint64_t* empty, bool pair, const Waits& wait) {
+    const int lane = threadIdx.x & 31;
+    Cursor g;
+    bool ok = true, bad = false;
+    for (int64_t it = begin; ok && it < tiles.count; it += step) {
+        const Tile t = tiles.at(it);
+        // the scale of (row r, block b) is base[r * row_step + b * block_step]; rows past the last read the last one's
+        const int from = (of_a ? t.row0 : t.col0) + row0, end = of_a ? t.rows_end : p.N;
+        const float* base = of_a ? p.a_scales : p.b_scales;
+        int64_t row_step = 1, block_step = of_a ? p.a_scale_stride : p.b_scale_stride;
+        if (Grad) base += t.k0 / kBlock * block_step;
+        else if (of_a) row_step = block_step, block_step = 1;
+        else {
+            base += t.e * p.b_scale_batch;
+            if (!p.transposed) row_step = block_step, block_step = 1;
+        }
+        const float* at[Count];
+#pragma unroll
+        for (int i = 0; i < Count; ++i) {
+            const int row = min(from + lane + 32 * i, end - 1);
+            at[i] = base + int64_t(!Grad && !of_a ? row / kBlock : row) * row_step;
+        }
+        const bool vectors = block_step == 1 && p.scale_vectors;
+        float x[Count][kAhead];
+        auto fetch = [&](int b0) {
+#pragma unroll
+            for (int i = 0; i < Count; ++i) {
+                if (vectors) {
+                    const float4 v = *reinterpret_cast<const float4*>(at[i] + b0);
+                    x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kAhead; ++q) x[i][q] = at[i][min(b0 + q, t.blocks - 1) * block_step];
+                }
+            }
+        };
+        if (t.blocks) fetch(0);
+        for (int b0 = 0; b0 < t.blocks; b0 += kAhead) {
+            uint32_t w[Count];
+#pragma unroll
+            for (int i = 0; i < Count; ++i) {
+                w[i] = 0;
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q) w[i] |= exponent_of(x[i][q], b0 + q < t.blocks && from + lane + 32 * i < end, bad) << (8 * q);
+            }
+            if (b0 + kAhead < t.blocks) fetch(b0 + kAhead);
+            ok = __all_sync(kFull, wait(&empty[g.at], g.phase ^ 1));
+            if (!ok) break;
+            unsigned char* to = exponents + g.at * bytes + lane * 16;
+#pragma unroll
+            for (int i = 0; i < Count; i += 4) *reinterpret_cast<uint4*>(to + 128 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                if (pair) arrive_at_first<true>(&full[g.at]);
+                else arrive_at_first<false>(&full[g.at]);
+            }
+            g.next(2);
+        }
+    }
+    if (bad) atomicCAS(p.status, 0, kStatusScale);
+}
+
+// All threads of the CTA, or of both of a pair.
+template <bool Pair>
+__device__ __forceinline__ void both_ctas() {
+    __syncwarp();
+    if constexpr (Pair) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else __syncthreads();
+}
+
+template <int BN, bool Pair, bool Grad, typename Out>
 __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(const __grid_constant__ ProductArgs p) {
-    constexpr int kHalf = BN / 2, kChunks = kHalf / 32, kGroups = BN / 128;
-    constexpr bool kShared = kSecondTile<BN> < BN;
+    constexpr int kHalf = BN / 2, kChunks = kHalf / 32, kGroups = BN / 128, kStages = stages_of(BN, Pair), kShare = share_bytes(BN, Pair);
+    constexpr int kCtas = Pair ? 2 : 1;
+    constexpr bool kShared = second_tile(BN) < BN;
     extern __shared__ unsigned char dynamic_smem[];
     unsigned char* const ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic_smem) + 1023) & ~uintptr_t(1023));
-    unsigned char* const exponents = ring + kStages<BN> * kTileBytes<BN>;
-    __shared__ __align__(8) uint64_t full[kStages<BN>], empty[kStages<BN>], ready[2], drained, ended;
+    unsigned char* const exponents = ring + kStages * kShare;
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], scales_full[2], scales_empty[2], ready[2], drained, ended;
     __shared__ uint32_t tmem_at;
     __shared__ int stopped;
     __shared__ int32_t starts[TIDE_MAX_EXPERTS + 1], first[TIDE_MAX_EXPERTS + 1], sums[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = Pair ? blockIdx.x & 1 : 0;
+    const int64_t begin = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages<BN>; ++s) barrier_init(&full[s], 3), barrier_init(&empty[s], 1);
-        barrier_init(&ready[0], 1), barrier_init(&ready[1], 1), barrier_init(&drained, kSumWarps), barrier_init(&ended, 1);
+        for (int s = 0; s < kStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
+        for (int i = 0; i < 2; ++i) barrier_init(&scales_full[i], 2 * kCtas), barrier_init(&scales_empty[i], 1), barrier_init(&ready[i], 1);
+        barrier_init(&drained, kSumWarps * kCtas), barrier_init(&ended, 1);
         stopped = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)), "r"(kTmemCols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (Pair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)), "r"(kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)), "r"(kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
+    both_ctas<Pair>();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_at;
     wait_for_previous_kernel();
-    const Tiles<BN, Grad> tiles(p, starts, first, sums);
-    const int64_t count = tiles.count();
+    const Tiles<kCtas * kTileM, BN, Grad> tiles(p, starts, first, sums);
     const Waits wait{&stopped, p.status, p.timeout_ns};
 
     if (warp == 0 && lane == 0) {
-        load_tiles<BN, Grad>(p, tiles, count, ring, full, empty, wait);
+        load_tiles<BN, Pair, Grad>(p, tiles, rank, begin, step, ring, full, empty, wait);
     } else if (warp == 1 && lane == 0) {
-        Cursor s;
-        uint32_t tile = 0, buffer = 0;
-        bool ok = true;
-        for (int64_t it = blockIdx.x; ok && it < count; it += gridDim.x) {
-            const Tile t = tiles.at(it);
-            if (t.blocks == 0) continue;
-            const uint32_t to = tmem + (tile & 1) * kSecondTile<BN>;
-            // where the tile before began to be taken out, the one before that has been
-            if (!(ok = tile == 0 || wait(&drained, (tile - 1) & 1))) break;
-            for (int b = 0; b < t.blocks; ++b) {
-                if (!(ok = wait(&full[s.at], s.phase))) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const unsigned char* a = ring + s.at * kTileBytes<BN>;
-                const unsigned char* x = exponents + s.at * kExponentBytes<BN>;
-                const uint32_t a_scales = tmem + kExponentCols + (buffer & 1) * 12, b_scales = a_scales + 4;
-                ++buffer;
-                copy_exponents(a_scales, x);
+        if (rank == 0) {
+            Cursor s, g;
+            uint32_t tile = 0;
+            bool ok = true;
+            for (int64_t it = begin; ok && it < tiles.count; it += step) {
+                const Tile t = tiles.at(it);
+                if (t.blocks == 0) continue;
+                const uint32_t to = tmem + (tile & 1) * second_tile(BN);
+                // where the tile before began to be taken out, the one before that has been
+                if (!(ok = tile == 0 || wait(&drained, (tile - 1) & 1))) break;
+                uint32_t a_scales = 0, b_scales = 0;
+                for (int b = 0; b < t.blocks; ++b) {
+                    const uint32_t in = b % kAhead;
+                    if (in == 0) {
+                        if (!(ok = wait(&scales_full[g.at], g.phase))) break;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const unsigned char* x = exponents + g.at * exponent_bytes(BN);
+                        a_scales = tmem + kExponentCols + g.at * 12, b_scales = a_scales + 4;
+                        copy_exponents<Pair>(a_scales, x);
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) copy_exponents(b_scales + 4 * g, x + 512 * (1 + g));
-                const uint64_t da = tile_descriptor(a), db = tile_descriptor(a + kTileM * kBlock);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) multiply_scaled(to, da + 2 * k, db + 2 * k, kScaledInstruction<BN>, a_scales, b_scales, b > 0 || k > 0);
-                commit(&empty[s.at]);
-                s.next(kStages<BN>);
-            }
-            if (ok) commit(&ready[tile & 1]);
-            ++tile;
-        }
-        if (!ok) end_products(&ended);
-    } else if (warp == 2 || warp == 3) {
-        // warp 2: A's scales, warp 3: B's; each lane has rows lane, lane + 32, ... and up to four blocks ahead
-        constexpr int kAhead = 4;
-        const bool of_a = warp == 2;
-        const int rows = of_a ? 4 : 4 * kGroups;
-        Cursor s;
-        bool ok = true, bad = false;
-        for (int64_t it = blockIdx.x; ok && it < count; it += gridDim.x) {
-            const Tile t = tiles.at(it);
-            // scale of (row i, block b) at base[i * row_step + b * step]; rows past the last read the last one's
-            const int row0 = of_a ? t.row0 : t.col0, end = of_a ? t.rows_end : p.N;
-            const float* base;
-            int64_t row_step, step;
-            if (Grad) {
-                base = (of_a ? p.a_scales + t.k0 / kBlock * p.a_scale_stride : p.b_scales + t.k0 / kBlock * p.b_scale_stride);
-                row_step = 1, step = of_a ? p.a_scale_stride : p.b_scale_stride;
-            } else if (of_a) {
-                base = p.a_scales, row_step = p.a_scale_stride, step = 1;
-            } else {
-                base = p.b_scales + t.e * p.b_scale_batch;
-                row_step = p.transposed ? 1 : p.b_scale_stride, step = p.transposed ? p.b_scale_stride : 1;
-            }
-            const float* at[4 * kGroups];
-#pragma unroll
-            for (int i = 0; i < 4 * kGroups; ++i) {
-                const int row = min(row0 + lane + 32 * i, end - 1);
-                at[i] = base + int64_t(!Grad && !of_a ? row / kBlock : row) * row_step;
-            }
-            for (int b0 = 0; ok && b0 < t.blocks; b0 += kAhead) {
-                float x[kAhead][4 * kGroups];
-#pragma unroll
-                for (int q = 0; q < kAhead; ++q)
-#pragma unroll
-                    for (int i = 0; i < 4 * kGroups; ++i)
-                        if (i < rows) x[q][i] = at[i][min(b0 + q, t.blocks - 1) * step];
-#pragma unroll
-                for (int q = 0; q < kAhead; ++q) {
-                    if (!ok || b0 + q >= t.blocks) break;
-                    ok = __all_sync(kFull, wait(&empty[s.at], s.phase ^ 1));
-                    if (!ok) break;
-                    unsigned char* to = exponents + s.at * kExponentBytes<BN> + (of_a ? 0 : 512) + lane * 16;
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        if (4 * g >= rows) break;
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) w[i] = exponent_of(x[q][4 * g + i], row0 + lane + 32 * (4 * g + i) < end, bad);
-                        *reinterpret_cast<uint4*>(to + 512 * g) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int i = 0; i < kGroups; ++i) copy_exponents<Pair>(b_scales + 4 * i, x + 512 * (1 + i));
+                        commit<Pair>(&scales_empty[g.at]);
+                        g.next(2);
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) barrier_arrive(&full[s.at]);
-                    s.next(kStages<BN>);
+                    if (!(ok = wait(&full[s.at], s.phase))) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const unsigned char* a = ring + s.at * kShare;
+                    const uint64_t da = tile_descriptor(a), db = tile_descriptor(a + kTileM * kBlock);
+                    const uint32_t instruction = scaled_instruction(BN, Pair) | in << 29 | in << 4;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) multiply_scaled<Pair>(to, da + 2 * k, db + 2 * k, instruction, a_scales, b_scales, b > 0 || k > 0);
+                    commit<Pair>(&empty[s.at]);
+                    s.next(kStages);
                 }
+                if (ok) commit<Pair>(&ready[tile & 1]);
+                ++tile;
             }
+            if (!ok) end_products<Pair>(&ended);
         }
-        if (bad) atomicCAS(p.status, 0, kStatusScale);
+    } else if (warp == 2) {
+        write_exponents<kCtas * kTileM, BN, Grad, 4>(p, tiles, true, rank * kTileM, begin, step, exponents, exponent_bytes(BN), scales_full, scales_empty, Pair, wait);
+    } else if (warp == 3) {
+        write_exponents<kCtas * kTileM, BN, Grad, 4 * kGroups>(p, tiles, false, 0, begin, step, exponents + 512, exponent_bytes(BN), scales_full, scales_empty, Pair, wait);
     } else if (warp >= 4) {
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t from = tmem + (uint32_t(quarter * 32) << 16) + half * kHalf;
         uint32_t tile = 0;
         bool ok = true;
-        for (int64_t it = blockIdx.x; ok && it < count; it += gridDim.x) {
+        for (int64_t it = begin; ok && it < tiles.count; it += step) {
             const Tile t = tiles.at(it);
-            const int row = t.row0 + quarter * 32 + lane, col = t.col0 + half * kHalf;
+            const int row = t.row0 + rank * kTileM + quarter * 32 + lane, col = t.col0 + half * kHalf;
             const bool here = row < t.rows_end;
             Out* const to = static_cast<Out*>(Grad ? p.grads.p[t.e] : p.out) + row * p.out_stride + col;
             if (t.blocks == 0) {
@@ -440,11 +526,11 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
             ok = __all_sync(kFull, wait(&ready[tile & 1], (tile >> 1) & 1));
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t at = from + (tile & 1) * kSecondTile<BN>;
+            const uint32_t at = from + (tile & 1) * second_tile(BN);
             // the columns that the next tile's sums share come first: of the first buffer the last, of the second the first
             const bool backwards = kShared && !(tile & 1);
             const bool holds = kShared && half == int(backwards);
-            if (!holds && lane == 0) barrier_arrive(&drained);
+            if (!holds && lane == 0) arrive_at_first<Pair>(&drained);
             uint32_t x[2][32];
             auto column = [&](int c) { return (backwards ? kChunks - 1 - c : c) * 32; };
             load_sums(x[0], at + column(0));
@@ -454,7 +540,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
                 if (c + 1 < kChunks) load_sums(x[(c + 1) & 1], at + column(c + 1));
                 if (holds && c == 0) {
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                    if (lane == 0) barrier_arrive(&drained);
+                    if (lane == 0) arrive_at_first<Pair>(&drained);
                 }
                 if (here) put_sums(to + column(c), x[c & 1], p.N - col - column(c), p.out_vectors);
             }
@@ -463,10 +549,13 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
     }
     __syncwarp();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
+    both_ctas<Pair>();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     let_next_kernel_start();
-    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    if (warp == 2) {
+        if constexpr (Pair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
 }
 
 // ---- any scales --------------------------------------------------------------------------------------
@@ -476,10 +565,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
 // buffer. No sum of more than 128 products is formed before its scale is applied.
 template <int BN, bool Grad, typename Out>
 __global__ void __launch_bounds__(kProductThreads, 1) any_scales_kernel(const __grid_constant__ ProductArgs p) {
-    constexpr int kBuffers = kTmemCols / BN, kHalf = BN / 2, kChunks = kHalf / 32;
+    constexpr int kBuffers = kTmemCols / BN, kHalf = BN / 2, kChunks = kHalf / 32, kStages = stages_of(BN, false), kShare = share_bytes(BN, false);
     extern __shared__ unsigned char dynamic_smem[];
     unsigned char* const ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic_smem) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full[kStages<BN>], empty[kStages<BN>], ready[kBuffers], drained[kBuffers], ended;
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], ready[kBuffers], drained[kBuffers], ended;
     __shared__ uint32_t tmem_at;
     __shared__ int stopped;
     __shared__ int32_t starts[TIDE_MAX_EXPERTS + 1], first[TIDE_MAX_EXPERTS + 1], sums[32];
@@ -487,7 +576,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) any_scales_kernel(const __
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages<BN>; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
+        for (int s = 0; s < kStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
         for (int b = 0; b < kBuffers; ++b) barrier_init(&ready[b], 1), barrier_init(&drained[b], kSumWarps);
         barrier_init(&ended, 1);
         stopped = 0;
@@ -502,36 +591,35 @@ __global__ void __launch_bounds__(kProductThreads, 1) any_scales_kernel(const __
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_at;
     wait_for_previous_kernel();
-    const Tiles<BN, Grad> tiles(p, starts, first, sums);
-    const int64_t count = tiles.count();
+    const Tiles<kTileM, BN, Grad> tiles(p, starts, first, sums);
     const Waits wait{&stopped, p.status, p.timeout_ns};
 
     if (warp == 0 && lane == 0) {
-        load_tiles<BN, Grad>(p, tiles, count, ring, full, empty, wait);
+        load_tiles<BN, false, Grad>(p, tiles, 0, blockIdx.x, gridDim.x, ring, full, empty, wait);
     } else if (warp == 1 && lane == 0) {
         Cursor s, d;
         bool ok = true;
-        for (int64_t it = blockIdx.x; ok && it < count; it += gridDim.x) {
+        for (int64_t it = blockIdx.x; ok && it < tiles.count; it += gridDim.x) {
             const Tile t = tiles.at(it);
             for (int b = 0; b < t.blocks; ++b) {
                 if (!(ok = wait(&drained[d.at], d.phase ^ 1) && wait(&full[s.at], s.phase))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const unsigned char* a = ring + s.at * kTileBytes<BN>;
+                const unsigned char* a = ring + s.at * kShare;
                 const uint64_t da = tile_descriptor(a), db = tile_descriptor(a + kTileM * kBlock);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) multiply(tmem + d.at * BN, da + 2 * k, db + 2 * k, kInstruction<BN>, k > 0);
-                commit(&empty[s.at]);
-                commit(&ready[d.at]);
-                s.next(kStages<BN>), d.next(kBuffers);
+                for (int k = 0; k < 4; ++k) multiply(tmem + d.at * BN, da + 2 * k, db + 2 * k, plain_instruction(BN), k > 0);
+                commit<false>(&empty[s.at]);
+                commit<false>(&ready[d.at]);
+                s.next(kStages), d.next(kBuffers);
             }
         }
-        if (!ok) end_products(&ended);
+        if (!ok) end_products<false>(&ended);
     } else if (warp >= 4) {
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t from = tmem + (uint32_t(quarter * 32) << 16) + half * kHalf;
         Cursor d;
         bool ok = true;
-        for (int64_t it = blockIdx.x; ok && it < count; it += gridDim.x) {
+        for (int64_t it = blockIdx.x; ok && it < tiles.count; it += gridDim.x) {
             const Tile t = tiles.at(it);
             const int row = t.row0 + quarter * 32 + lane, col = t.col0 + half * kHalf;
             uint64_t acc[kHalf / 2];
@@ -631,17 +719,32 @@ int describe(CUtensorMap* map, const tide_fp8_t& m, int64_t len, int64_t rows, i
     return r == CUDA_SUCCESS ? TIDE_OK : record_cuda_error(cudaErrorInvalidValue);
 }
 
-template <int BN, bool Grad, typename Out>
+template <int BN, bool Pair, bool Grad, typename Out>
 int launch(const ProductArgs& p, bool any_scales, int64_t most_tiles, const Ctas& c, cudaStream_t stream) {
-    auto* kernel = any_scales ? any_scales_kernel<BN == 256 ? 128 : BN, Grad, Out> : scaled_product_kernel<BN, Grad, Out>;
-    const int smem = kStages<BN> * (kTileBytes<BN> + kExponentBytes<BN>) + 1024;
+    void (*kernel)(ProductArgs) = scaled_product_kernel<BN, Pair, Grad, Out>;
+    if constexpr (!Pair)
+        if (any_scales) kernel = any_scales_kernel<BN, Grad, Out>;
+    const int smem = stages_of(BN, Pair) * share_bytes(BN, Pair) + 2 * exponent_bytes(BN) + 1024;
     TIDE_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(most_tiles, c.most ? c.most : c.sms));
-    TIDE_CUDA(launch_after(kernel, int(ctas), kProductThreads, smem, stream, p));
+    const int64_t at_once = (c.most ? c.most : c.sms) / (Pair ? 2 : 1);
+    const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(most_tiles, at_once));
+    TIDE_CUDA(launch_clusters_after(kernel, Pair ? 2 : 1, int(tiles * (Pair ? 2 : 1)), kProductThreads, smem, stream, p));
     return TIDE_OK;
 }
 
 bool vectors32(const void* p, int64_t stride, int64_t rows, int elem) { return aligned(p, 32) && (rows <= 1 || stride * elem % 32 == 0); }
+
+// The kernel for `down` tiles of 128 rows of `N` columns. Pairs' tiles of 256 x 256 where they are many enough to keep all SMs busy
+// and experts have rows enough to fill them; else tiles of 128 x 128, as also where sums go to registers.
+bool pairs(int64_t rows, int64_t down, int64_t N, bool any_scales, const Ctas& c) {
+    return !any_scales && c.most != 1 && rows >= 2 * kTileM && down * ((N + 255) / 256) >= 2 * c.sms;
+}
+
+template <bool Grad>
+int launch_any(const ProductArgs& p, bool pair, bool any_scales, int64_t tiles, int bf16, const Ctas& c, cudaStream_t stream) {
+    if (pair) return bf16 ? launch<256, true, Grad, __nv_bfloat16>(p, false, tiles, c, stream) : launch<256, true, Grad, float>(p, false, tiles, c, stream);
+    return bf16 ? launch<128, false, Grad, __nv_bfloat16>(p, any_scales, tiles, c, stream) : launch<128, false, Grad, float>(p, any_scales, tiles, c, stream);
+}
 
 }  // namespace
 
@@ -649,21 +752,21 @@ int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets,
                   int64_t out_stride, const Ctas& c, int* status, uint64_t timeout_ns, cudaStream_t stream) {
     if (M <= 0) return TIDE_OK;
     ProductArgs p{};
-    // narrow tiles where wide ones are fewer than the SMs, and for sums in registers
     const bool any = flags & TIDE_FP8_ANY_SCALES;
     const int64_t down = padded_blocks(M, E);
-    const bool narrow = any || down * ((N + 255) / 256) < c.sms;
+    const bool pair = pairs(M / E, down, N, any, c);
     int rc = describe(&p.a, a, K, M, 0, kTileM);
-    if (rc == TIDE_OK) rc = describe(&p.b, w, K, N, E, narrow ? 128 : 256);
+    if (rc == TIDE_OK) rc = describe(&p.b, w, K, N, E, 128);
     if (rc != TIDE_OK) return rc;
     p.a_scales = a.scales, p.a_scale_stride = a.scale_stride;
     p.b_scales = w.scales, p.b_scale_stride = w.scale_stride, p.b_scale_batch = w.scale_batch, p.transposed = (flags & TIDE_FP8_TRANSPOSED) != 0;
+    // what such a vector holds behind a row's last scale is read and not used; it is of the same 16 bytes
+    p.scale_vectors = aligned(a.scales, 16) && a.scale_stride % 4 == 0 && aligned(w.scales, 16) && w.scale_stride % 4 == 0 && (E == 1 || w.scale_batch % 4 == 0);
     p.offsets = offsets, p.M = int32_t(M), p.E = E, p.N = int32_t(N), p.K = int32_t(K), p.rows = 0;
     p.out = out, p.out_stride = out_stride, p.out_vectors = vectors32(out, out_stride, M, out_bf16 ? 2 : 4);
     p.status = status, p.timeout_ns = timeout_ns;
-    const int64_t tiles = down * ((N + (narrow ? 127 : 255)) / (narrow ? 128 : 256));
-    if (out_bf16) return narrow ? launch<128, false, __nv_bfloat16>(p, any, tiles, c, stream) : launch<256, false, __nv_bfloat16>(p, any, tiles, c, stream);
-    return narrow ? launch<128, false, float>(p, any, tiles, c, stream) : launch<256, false, float>(p, any, tiles, c, stream);
+    // padded_blocks counts tiles of 128 rows; of 256 there are fewer
+    return launch_any<false>(p, pair, any, down * ((N + (pair ? 255 : 127)) / (pair ? 256 : 128)), out_bf16, c, stream);
 }
 
 int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, uint32_t flags, int64_t N, int64_t K, const GradPtrs& grads,
@@ -672,10 +775,10 @@ int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int
     const bool any = flags & TIDE_FP8_ANY_SCALES;
     const int64_t padded = std::max<int64_t>(1, padded_blocks(M, E)) * kBlock;
     const int64_t down = int64_t(E) * ((N + kTileM - 1) / kTileM);
-    const bool narrow = any || down * ((K + 255) / 256) < c.sms;
+    const bool pair = pairs(N, down, K, any, c);
     if (M > 0) {  // else there is nothing to sum
         int rc = describe(&p.a, dy, padded, N, 0, kTileM);
-        if (rc == TIDE_OK) rc = describe(&p.b, a, padded, K, 0, narrow ? 128 : 256);
+        if (rc == TIDE_OK) rc = describe(&p.b, a, padded, K, 0, 128);
         if (rc != TIDE_OK) return rc;
     }
     p.most_blocks = int32_t(padded / kBlock);
@@ -686,9 +789,8 @@ int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int
     p.out_vectors = 1;
     for (int e = 0; e < E; ++e) p.out_vectors &= vectors32(grads.p[e], K, N, grad_bf16 ? 2 : 4);
     p.status = status, p.timeout_ns = timeout_ns;
-    const int64_t tiles = down * ((K + (narrow ? 127 : 255)) / (narrow ? 128 : 256));
-    if (grad_bf16) return narrow ? launch<128, true, __nv_bfloat16>(p, any, tiles, c, stream) : launch<256, true, __nv_bfloat16>(p, any, tiles, c, stream);
-    return narrow ? launch<128, true, float>(p, any, tiles, c, stream) : launch<256, true, float>(p, any, tiles, c, stream);
+    const int64_t tiles = int64_t(E) * (pair ? (N + 2 * kTileM - 1) / (2 * kTileM) : (N + kTileM - 1) / kTileM) * ((K + (pair ? 255 : 127)) / (pair ? 256 : 128));
+    return launch_any<true>(p, pair, any, tiles, grad_bf16, c, stream);
 }
 
 }  // namespace tide

@@ -399,7 +399,8 @@ def test_products(tide, T, k, E, N, K, kind, any_scales):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
-@pytest.mark.parametrize("T, k, E, N, K", [(1, 1, 1, 1, 1), (1, 4, 16, 200, 300), (37, 2, 5, 128, 128), (300, 3, 4, 331, 525), (1000, 2, 3, 260, 1040), (3000, 4, 9, 768, 384)])
+@pytest.mark.parametrize("T, k, E, N, K", [(1, 1, 1, 1, 1), (1, 4, 16, 200, 300), (37, 2, 5, 128, 128), (300, 3, 4, 331, 525), (1000, 2, 3, 260, 1040), (3000, 4, 9, 768, 384),
+                                           (900, 4, 16, 900, 1100)])
 @pytest.mark.parametrize("any_scales", [False, True])
 def test_weight_gradients(tide, T, k, E, N, K, kind, any_scales):
     g = gen(N + K + 1)
