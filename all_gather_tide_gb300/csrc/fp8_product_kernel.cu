@@ -99,6 +99,14 @@ struct Waits {
     }
 };
 
+// One lane of a whole warp. The warps that issue copies and products run as a whole up to there, so that addresses and
+// descriptors stay in uniform registers: with a branch for one lane around the loop, a block's four products took 450 ns to issue.
+__device__ __forceinline__ bool elected() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // A position in a ring: its index and how often it has come round.
 struct Cursor {
     int at = 0;
@@ -265,12 +273,15 @@ __device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles& ti
         const Tile t = tiles.at(it);
         const int row = t.row0 + rank * kTileM, col = t.col0 + rank * (BN / 2);
         for (int b = 0; b < t.blocks; ++b) {
-            if (!(ok = wait(&empty[s.at], s.phase ^ 1))) break;
+            if (!(ok = __all_sync(kFull, wait(&empty[s.at], s.phase ^ 1)))) break;
             unsigned char* a = ring + s.at * kShare;
-            if (rank == 0) barrier_expect(&full[s.at], Pair ? 2 * kShare : kShare);
-            load_2d<Pair>(a, &p.a, t.k0 + b * kBlock, row, &full[s.at]);
-            if (Grad) load_2d<Pair>(a + kTileM * kBlock, &p.b, t.k0 + b * kBlock, col, &full[s.at]);
-            else load_3d<Pair>(a + kTileM * kBlock, &p.b, b * kBlock, col, t.e, &full[s.at]);
+            if (elected()) {
+                if (rank == 0) barrier_expect(&full[s.at], Pair ? 2 * kShare : kShare);
+                load_2d<Pair>(a, &p.a, t.k0 + b * kBlock, row, &full[s.at]);
+                if (Grad) load_2d<Pair>(a + kTileM * kBlock, &p.b, t.k0 + b * kBlock, col, &full[s.at]);
+                else load_3d<Pair>(a + kTileM * kBlock, &p.b, b * kBlock, col, t.e, &full[s.at]);
+            }
+            __syncwarp();
             s.next(kStages);
             ++uses;
         }
@@ -290,7 +301,7 @@ __device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles& ti
 // The products on their way end before the Tensor Memory is given back.
 template <bool Pair>
 __device__ __forceinline__ void end_products(uint64_t* ended) {
-    commit<Pair>(ended);
+    if (elected()) commit<Pair>(ended);
     const uint64_t end = globaltimer() + 100000000ull;
     while (!barrier_try(ended, 0) && globaltimer() < end) {
     }
@@ -340,44 +351,51 @@ constexpr int kAhead = 4;           // blocks in a word
 __host__ __device__ constexpr int exponent_bytes(int bn) { return 4 * (kTileM + bn); }
 __host__ __device__ constexpr int second_tile(int bn) { return bn == 256 ? 224 : bn; }  // column of the other tile's sums
 
-// A scale as a power of two's exponent, biased; `there`: whether its row is, and another number is to be told of.
-__device__ __forceinline__ uint32_t exponent_of(float scale, bool there, bool& bad) {
-    const uint32_t bits = __float_as_uint(scale), e = bits >> 23;
-    bad |= there && (((bits & 0x7fffffu) != 0 && e != 255) || e - 1 > 254);
-    return e & 255;
+// Four scales' exponents, biased, a byte each.
+__device__ __forceinline__ uint32_t exponents_of(const float (&x)[kAhead]) {
+    return (__float_as_uint(x[0]) >> 23 & 0xffu) | (__float_as_uint(x[1]) >> 15 & 0xff00u) | (__float_as_uint(x[2]) >> 7 & 0xff0000u) | (__float_as_uint(x[3]) << 1 & 0xff000000u);
+}
+// Whether a scale is neither a power of two from 2^-126 on nor NaN.
+__device__ __forceinline__ bool no_power(float scale) {
+    const uint32_t bits = __float_as_uint(scale);
+    return (bits & 0x807fffffu) != 0 ? (bits & 0x7fffffffu) <= 0x7f800000u : bits == 0;
 }
 
 // One warp's part: the exponents of A's rows, from `row0` of the tile on, or of B's, Count rows for each lane (lane, lane + 32,
-// ...). The next group's scales are on their way while one is written.
-template <int Rows, int BN, bool Grad, int Count, typename Tiles>
-__device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tiles& tiles, bool of_a, int row0, int64_t begin, int64_t step, unsigned char* exponents, int bytes,
-                                                uint64_t* full, uint64_t* empty, bool pair, const Waits& wait) {
+// ...). Scales are loaded two groups ahead, behind the fence of the group before, which would wait for them. The first tile
+// in each row or column of tiles looks whether they are powers of two.
+template <bool Grad, bool OfA, int Count, typename Tiles>
+__device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tiles& tiles, int row0, int64_t begin, int64_t step, unsigned char* exponents, int bytes, uint64_t* full,
+                                                uint64_t* empty, bool pair, const Waits& wait) {
+    // a product's weights have one scale for 128 rows: four words are one
+    constexpr bool kUniform = !OfA && !Grad;
+    constexpr int kLoads = kUniform ? Count / 4 : Count, kEach = Count / kLoads;
     const int lane = threadIdx.x & 31;
     Cursor g;
     bool ok = true, bad = false;
     for (int64_t it = begin; ok && it < tiles.count; it += step) {
         const Tile t = tiles.at(it);
         // the scale of (row r, block b) is base[r * row_step + b * block_step]; rows past the last read the last one's
-        const int from = (of_a ? t.row0 : t.col0) + row0, end = of_a ? t.rows_end : p.N;
-        const float* base = of_a ? p.a_scales : p.b_scales;
-        int64_t row_step = 1, block_step = of_a ? p.a_scale_stride : p.b_scale_stride;
+        const int from = (OfA ? t.row0 : t.col0) + row0, end = OfA ? t.rows_end : p.N;
+        const float* base = OfA ? p.a_scales : p.b_scales;
+        int64_t row_step = 1, block_step = OfA ? p.a_scale_stride : p.b_scale_stride;
         if (Grad) base += t.k0 / kBlock * block_step;
-        else if (of_a) row_step = block_step, block_step = 1;
+        else if (OfA) row_step = block_step, block_step = 1;
         else {
             base += t.e * p.b_scale_batch;
             if (!p.transposed) row_step = block_step, block_step = 1;
         }
-        const float* at[Count];
+        const float* at[kLoads];
 #pragma unroll
-        for (int i = 0; i < Count; ++i) {
-            const int row = min(from + lane + 32 * i, end - 1);
-            at[i] = base + int64_t(!Grad && !of_a ? row / kBlock : row) * row_step;
+        for (int i = 0; i < kLoads; ++i) {
+            const int row = min(from + (kUniform ? kBlock * i : lane + 32 * i), end - 1);
+            at[i] = base + int64_t(kUniform ? row / kBlock : row) * row_step;
         }
         const bool vectors = block_step == 1 && p.scale_vectors;
-        float x[Count][kAhead];
-        auto fetch = [&](int b0) {
+        auto fetch = [&](float (&x)[kLoads][kAhead], int b0) {
+            if (b0 >= t.blocks) return;
 #pragma unroll
-            for (int i = 0; i < Count; ++i) {
+            for (int i = 0; i < kLoads; ++i) {
                 if (vectors) {
                     const float4 v = *reinterpret_cast<const float4*>(at[i] + b0);
                     x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
@@ -387,21 +405,21 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
                 }
             }
         };
-        if (t.blocks) fetch(0);
-        for (int b0 = 0; b0 < t.blocks; b0 += kAhead) {
-            uint32_t w[Count];
+        const bool look = OfA ? t.col0 == 0 : t.row0 == (Grad ? 0 : tiles.first[t.e]);
+        auto put = [&](const float (&x)[kLoads][kAhead], int b0) {
+            uint32_t w[kLoads];
 #pragma unroll
-            for (int i = 0; i < Count; ++i) {
-                w[i] = 0;
+            for (int i = 0; i < kLoads; ++i) w[i] = exponents_of(x[i]);
+            if (look)
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q) w[i] |= exponent_of(x[i][q], b0 + q < t.blocks && from + lane + 32 * i < end, bad) << (8 * q);
-            }
-            if (b0 + kAhead < t.blocks) fetch(b0 + kAhead);
+                for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+                    for (int q = 0; q < kAhead; ++q) bad |= b0 + q < t.blocks && from + (kUniform ? kBlock * i : lane + 32 * i) < end && no_power(x[i][q]);
             ok = __all_sync(kFull, wait(&empty[g.at], g.phase ^ 1));
-            if (!ok) break;
+            if (!ok) return;
             unsigned char* to = exponents + g.at * bytes + lane * 16;
 #pragma unroll
-            for (int i = 0; i < Count; i += 4) *reinterpret_cast<uint4*>(to + 128 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            for (int i = 0; i < Count; i += 4) *reinterpret_cast<uint4*>(to + 128 * i) = make_uint4(w[i / kEach], w[(i + 1) / kEach], w[(i + 2) / kEach], w[(i + 3) / kEach]);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
@@ -409,6 +427,16 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
                 else arrive_at_first<false>(&full[g.at]);
             }
             g.next(2);
+        };
+        float x[kLoads][kAhead], y[kLoads][kAhead];
+        fetch(x, 0);
+        fetch(y, kAhead);
+        for (int b0 = 0; ok && b0 < t.blocks; b0 += 2 * kAhead) {
+            put(x, b0);
+            fetch(x, b0 + 2 * kAhead);
+            if (!ok || b0 + kAhead >= t.blocks) break;
+            put(y, b0 + kAhead);
+            fetch(y, b0 + 3 * kAhead);
         }
     }
     if (bad) atomicCAS(p.status, 0, kStatusScale);
@@ -462,9 +490,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
     const Tiles<kCtas * kTileM, BN, Grad> tiles(p, starts, first, sums);
     const Waits wait{&stopped, p.status, p.timeout_ns};
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         load_tiles<BN, Pair, Grad>(p, tiles, rank, begin, step, ring, full, empty, wait);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         if (rank == 0) {
             Cursor s, g;
             uint32_t tile = 0;
@@ -474,40 +502,46 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
                 if (t.blocks == 0) continue;
                 const uint32_t to = tmem + (tile & 1) * second_tile(BN);
                 // where the tile before began to be taken out, the one before that has been
-                if (!(ok = tile == 0 || wait(&drained, (tile - 1) & 1))) break;
+                if (!(ok = tile == 0 || __all_sync(kFull, wait(&drained, (tile - 1) & 1)))) break;
                 uint32_t a_scales = 0, b_scales = 0;
                 for (int b = 0; b < t.blocks; ++b) {
                     const uint32_t in = b % kAhead;
                     if (in == 0) {
-                        if (!(ok = wait(&scales_full[g.at], g.phase))) break;
+                        if (!(ok = __all_sync(kFull, wait(&scales_full[g.at], g.phase)))) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         const unsigned char* x = exponents + g.at * exponent_bytes(BN);
                         a_scales = tmem + kExponentCols + g.at * 12, b_scales = a_scales + 4;
-                        copy_exponents<Pair>(a_scales, x);
+                        if (elected()) {
+                            copy_exponents<Pair>(a_scales, x);
 #pragma unroll
-                        for (int i = 0; i < kGroups; ++i) copy_exponents<Pair>(b_scales + 4 * i, x + 512 * (1 + i));
-                        commit<Pair>(&scales_empty[g.at]);
+                            for (int i = 0; i < kGroups; ++i) copy_exponents<Pair>(b_scales + 4 * i, x + 512 * (1 + i));
+                            commit<Pair>(&scales_empty[g.at]);
+                        }
+                        __syncwarp();
                         g.next(2);
                     }
-                    if (!(ok = wait(&full[s.at], s.phase))) break;
+                    if (!(ok = __all_sync(kFull, wait(&full[s.at], s.phase)))) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const unsigned char* a = ring + s.at * kShare;
                     const uint64_t da = tile_descriptor(a), db = tile_descriptor(a + kTileM * kBlock);
                     const uint32_t instruction = scaled_instruction(BN, Pair) | in << 29 | in << 4;
+                    if (elected()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) multiply_scaled<Pair>(to, da + 2 * k, db + 2 * k, instruction, a_scales, b_scales, b > 0 || k > 0);
-                    commit<Pair>(&empty[s.at]);
+                        for (int k = 0; k < 4; ++k) multiply_scaled<Pair>(to, da + 2 * k, db + 2 * k, instruction, a_scales, b_scales, b > 0 || k > 0);
+                        commit<Pair>(&empty[s.at]);
+                        if (b + 1 == t.blocks) commit<Pair>(&ready[tile & 1]);
+                    }
+                    __syncwarp();
                     s.next(kStages);
                 }
-                if (ok) commit<Pair>(&ready[tile & 1]);
                 ++tile;
             }
             if (!ok) end_products<Pair>(&ended);
         }
     } else if (warp == 2) {
-        write_exponents<kCtas * kTileM, BN, Grad, 4>(p, tiles, true, rank * kTileM, begin, step, exponents, exponent_bytes(BN), scales_full, scales_empty, Pair, wait);
+        write_exponents<Grad, true, 4>(p, tiles, rank * kTileM, begin, step, exponents, exponent_bytes(BN), scales_full, scales_empty, Pair, wait);
     } else if (warp == 3) {
-        write_exponents<kCtas * kTileM, BN, Grad, 4 * kGroups>(p, tiles, false, 0, begin, step, exponents + 512, exponent_bytes(BN), scales_full, scales_empty, Pair, wait);
+        write_exponents<Grad, false, 4 * kGroups>(p, tiles, 0, begin, step, exponents + 512, exponent_bytes(BN), scales_full, scales_empty, Pair, wait);
     } else if (warp >= 4) {
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t from = tmem + (uint32_t(quarter * 32) << 16) + half * kHalf;
@@ -594,22 +628,25 @@ __global__ void __launch_bounds__(kProductThreads, 1) any_scales_kernel(const __
     const Tiles<kTileM, BN, Grad> tiles(p, starts, first, sums);
     const Waits wait{&stopped, p.status, p.timeout_ns};
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         load_tiles<BN, false, Grad>(p, tiles, 0, blockIdx.x, gridDim.x, ring, full, empty, wait);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         Cursor s, d;
         bool ok = true;
         for (int64_t it = blockIdx.x; ok && it < tiles.count; it += gridDim.x) {
             const Tile t = tiles.at(it);
             for (int b = 0; b < t.blocks; ++b) {
-                if (!(ok = wait(&drained[d.at], d.phase ^ 1) && wait(&full[s.at], s.phase))) break;
+                if (!(ok = __all_sync(kFull, wait(&drained[d.at], d.phase ^ 1) && wait(&full[s.at], s.phase)))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const unsigned char* a = ring + s.at * kShare;
                 const uint64_t da = tile_descriptor(a), db = tile_descriptor(a + kTileM * kBlock);
+                if (elected()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) multiply(tmem + d.at * BN, da + 2 * k, db + 2 * k, plain_instruction(BN), k > 0);
-                commit<false>(&empty[s.at]);
-                commit<false>(&ready[d.at]);
+                    for (int k = 0; k < 4; ++k) multiply(tmem + d.at * BN, da + 2 * k, db + 2 * k, plain_instruction(BN), k > 0);
+                    commit<false>(&empty[s.at]);
+                    commit<false>(&ready[d.at]);
+                }
+                __syncwarp();
                 s.next(kStages), d.next(kBuffers);
             }
         }
