@@ -68,14 +68,16 @@ __device__ __forceinline__ uint32_t of_first_cta(uint64_t* bar) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
     return at;
 }
+// What is handed over this way lies in Tensor Memory, or in this CTA's shared memory behind a proxy fence, so the arrival has
+// the CTA's scope: with the cluster's it waits for all of the thread's loads and stores, 2000 cycles.
 template <bool Pair>
 __device__ __forceinline__ void arrive_at_first(uint64_t* bar) {
-    if constexpr (Pair) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_first_cta(bar)) : "memory");
+    if constexpr (Pair) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(of_first_cta(bar)) : "memory");
     else barrier_arrive(bar);
 }
 __device__ __forceinline__ bool barrier_try(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
     return ok != 0;
 }
 
@@ -428,15 +430,19 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
             }
             g.next(2);
         };
-        float x[kLoads][kAhead], y[kLoads][kAhead];
+        float x[kLoads][kAhead], y[kLoads][kAhead], z[kLoads][kAhead];
         fetch(x, 0);
         fetch(y, kAhead);
-        for (int b0 = 0; ok && b0 < t.blocks; b0 += 2 * kAhead) {
+        fetch(z, 2 * kAhead);
+        for (int b0 = 0; ok && b0 < t.blocks; b0 += 3 * kAhead) {
             put(x, b0);
-            fetch(x, b0 + 2 * kAhead);
+            fetch(x, b0 + 3 * kAhead);
             if (!ok || b0 + kAhead >= t.blocks) break;
             put(y, b0 + kAhead);
-            fetch(y, b0 + 3 * kAhead);
+            fetch(y, b0 + 4 * kAhead);
+            if (!ok || b0 + 2 * kAhead >= t.blocks) break;
+            put(z, b0 + 2 * kAhead);
+            fetch(z, b0 + 5 * kAhead);
         }
     }
     if (bad) atomicCAS(p.status, 0, kStatusScale);
