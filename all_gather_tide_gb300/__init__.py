@@ -987,7 +987,7 @@ class Fp8Columns:
         self.M, self.len, self.E = M, len, E
         padded = max(128, tide_fp8_padded_rows(M, E))
         self.codes = _bytes_as_e4m3(len, padded)
-        self.scales = torch.empty(padded // 128, len, device="cuda")
+        self.scales = torch.empty(padded // 128, _up(len, 4), device="cuda")[:, :len]
         self.c = _fp8_struct(self.codes, self.scales)
 
 

@@ -22,8 +22,10 @@ namespace tide {
 namespace {
 
 constexpr int kTileM = 128;
-constexpr int kProductThreads = 384;  // a warp each for TMA and MMA, two for the scales, then eight that take the sums out
 constexpr int kSumWarps = 8;
+// A warp each for TMA and MMA, two for the scales, eight that take the sums out, two more for the scales.
+constexpr int kScaledThreads = 32 * (4 + kSumWarps + 2);
+constexpr int kAnyThreads = 32 * (4 + kSumWarps);
 constexpr int kTmemCols = 512;
 constexpr int kStatusWait = 1, kStatusScale = 2;
 
@@ -33,6 +35,7 @@ __host__ __device__ constexpr int stages_of(int bn, bool pair) { return 196608 /
 
 struct ProductArgs {
     CUtensorMap a, b;
+    CUtensorMap result;  // boxes of 32 rows of 64 bytes, where `bulk`
     const float* a_scales;  // product: [row][block]; gradient: [block][row]
     const float* b_scales;  // product: [expert][column / 128][block], or transposed; gradient: [block][column]
     int64_t a_scale_stride, b_scale_stride, b_scale_batch;
@@ -44,7 +47,8 @@ struct ProductArgs {
     int32_t most_blocks;  // of the transposed operands (gradient only)
     void* out;
     int64_t out_stride;
-    int scale_vectors;  // scales of consecutive blocks can be read four at a time
+    int scale_vectors;  // scales that lie side by side can be read four at a time
+    int bulk;         // the result can be written by TMA
     int out_vectors;  // rows of the result can be written 32 bytes at a time
     GradPtrs grads;
     int* status;
@@ -232,13 +236,13 @@ struct Tiles {
     __device__ __forceinline__ Tiles(const ProductArgs& p, int32_t* starts, int32_t* first, int32_t* sums)
         : p(p), starts(starts), first(first), across(uint32_t((p.N + BN - 1) / BN)), down(uint32_t((p.rows + Rows - 1) / Rows)) {
         constexpr int kUnit = Grad ? kBlock : Rows;
-        for (int e = threadIdx.x; e <= p.E; e += kProductThreads) {
+        for (int e = threadIdx.x; e <= p.E; e += int(blockDim.x)) {
             const Span s = span_of(p.offsets, min(e, p.E - 1), p.M);
             first[e] = e < p.E ? s.first : s.first + s.count;
         }
         exclusive_sums(starts, p.E, sums, [&](int e) { return (span_of(p.offsets, e, p.M).count + kUnit - 1) / kUnit; });
         if (Grad) {  // whatever the offsets hold, no tile reaches past the transposed operands
-            for (int e = threadIdx.x; e <= p.E; e += kProductThreads) starts[e] = min(starts[e], p.most_blocks);
+            for (int e = threadIdx.x; e <= p.E; e += int(blockDim.x)) starts[e] = min(starts[e], p.most_blocks);
             __syncthreads();
         }
         count = Grad ? int64_t(p.E) * across * down : int64_t(starts[p.E]) * across;
@@ -337,6 +341,43 @@ __device__ __forceinline__ void put_sums(Out* to, const uint32_t (&x)[Count], in
     }
 }
 
+// 64 bytes of each of the warp's 32 rows, by way of 2 KB of shared memory in which 16-byte pieces are swizzled as the tensor
+// map says: a lane's own stores of 32 bytes reach 32 lines an instruction, and those of all eight warps were what bounded
+// short products.
+constexpr int kStagingBytes = 2048;  // a warp
+template <bool Grad>
+__device__ __forceinline__ void put_bulk(const ProductArgs& p, unsigned char* staging, const uint32_t (&w)[16], int col, int row, int e) {
+    const int lane = threadIdx.x & 31;
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the bytes before have been read
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staging + lane * 64 + (i ^ (lane >> 1 & 3)) * 16) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        if constexpr (Grad)
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&p.result), "r"(col), "r"(row), "r"(e), "r"(smem_u32(staging)) : "memory");
+        else
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&p.result), "r"(col), "r"(row), "r"(smem_u32(staging)) : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+// 32 sums of each row, in that way.
+template <bool Grad, typename Out>
+__device__ __forceinline__ void put_sums_bulk(const ProductArgs& p, unsigned char* staging, const uint32_t (&x)[32], int col, int row, int e) {
+    constexpr int kCols = 64 / sizeof(Out);
+#pragma unroll
+    for (int c = 0; c < 32; c += kCols) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if constexpr (sizeof(Out) == 2) w[i] = pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            else w[i] = x[c + i];
+        }
+        if (col + c < p.N) put_bulk<Grad>(p, staging, w, col + c, row, e);
+    }
+}
+
 // ---- scales that are powers of two ------------------------------------------------------------------
 //
 // Two warps turn the scales of A's rows and B's into exponents, four blocks' to a word, from where the MMA thread copies them
@@ -350,12 +391,13 @@ __device__ __forceinline__ void put_sums(Out* to, const uint32_t (&x)[Count], in
 // 128 x 256 of its own needs 48 KB each, 768 cycles.
 constexpr int kExponentCols = 480;  // from here on; four blocks' take 4 + 8, two such groups' lie there
 constexpr int kAhead = 4;           // blocks in a word
-__host__ __device__ constexpr int exponent_bytes(int bn) { return 4 * (kTileM + bn); }
+__host__ __device__ constexpr int exponent_words(int bn) { return (bn + 127) / 128 * 4; }  // of B for each lane
+__host__ __device__ constexpr int exponent_bytes(int bn) { return 512 + 128 * exponent_words(bn); }
 __host__ __device__ constexpr int second_tile(int bn) { return bn == 256 ? 224 : bn; }  // column of the other tile's sums
 
 // Four scales' exponents, biased, a byte each.
-__device__ __forceinline__ uint32_t exponents_of(const float (&x)[kAhead]) {
-    return (__float_as_uint(x[0]) >> 23 & 0xffu) | (__float_as_uint(x[1]) >> 15 & 0xff00u) | (__float_as_uint(x[2]) >> 7 & 0xff0000u) | (__float_as_uint(x[3]) << 1 & 0xff000000u);
+__device__ __forceinline__ uint32_t exponents_of(float a, float b, float c, float d) {
+    return (__float_as_uint(a) >> 23 & 0xffu) | (__float_as_uint(b) >> 15 & 0xff00u) | (__float_as_uint(c) >> 7 & 0xff0000u) | (__float_as_uint(d) << 1 & 0xff000000u);
 }
 // Whether a scale is neither a power of two from 2^-126 on nor NaN.
 __device__ __forceinline__ bool no_power(float scale) {
@@ -363,86 +405,105 @@ __device__ __forceinline__ bool no_power(float scale) {
     return (bits & 0x807fffffu) != 0 ? (bits & 0x7fffffffu) <= 0x7f800000u : bits == 0;
 }
 
-// One warp's part: the exponents of A's rows, from `row0` of the tile on, or of B's, Count rows for each lane (lane, lane + 32,
-// ...). Scales are loaded two groups ahead, behind the fence of the group before, which would wait for them. The first tile
-// in each row or column of tiles looks whether they are powers of two.
-template <bool Grad, bool OfA, int Count, typename Tiles>
-__device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tiles& tiles, int row0, int64_t begin, int64_t step, unsigned char* exponents, int bytes, uint64_t* full,
+// The exponents of A's rows, 128 from `row0` of the tile on, or of B's BN: one warp writes every other group of four blocks, those of
+// buffer `which`. What a lane loads of a group:
+//   a product's A: the four blocks of rows lane, lane + 32, lane + 64 and lane + 96, v[i];
+//   a product's B: the four blocks of 32 columns, which have one scale: v[0] of lane i those of columns 32*i on;
+//   a gradient's: rows 4*lane to 4*lane + 3, and these + 128, of block q, v[q] and v[4 + q].
+// Per group it takes 4 to 8 loads and some 60 instructions: with a load for each scale, and their addresses, the writers, not the
+// products, bounded the gradient (438 us for 187).
+template <int BN, bool Grad, bool OfA, typename Tiles>
+__device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tiles& tiles, int row0, int which, int64_t begin, int64_t step, unsigned char* to, uint64_t* full,
                                                 uint64_t* empty, bool pair, const Waits& wait) {
-    // a product's weights have one scale for 128 rows: four words are one
-    constexpr bool kUniform = !OfA && !Grad;
-    constexpr int kLoads = kUniform ? Count / 4 : Count, kEach = Count / kLoads;
+    constexpr int kWords = OfA ? 4 : exponent_words(BN), kSets = kWords / 4, kLoads = Grad ? 4 * kSets : OfA ? 4 : 1;
     const int lane = threadIdx.x & 31;
-    Cursor g;
-    bool ok = true, bad = false;
-    for (int64_t it = begin; ok && it < tiles.count; it += step) {
+    uint32_t phase = 0, before = 0;  // groups before the tile
+    bool bad = false;
+    for (int64_t it = begin; it < tiles.count; it += step) {
         const Tile t = tiles.at(it);
-        // the scale of (row r, block b) is base[r * row_step + b * block_step]; rows past the last read the last one's
+        const int groups = (t.blocks + kAhead - 1) / kAhead, own = (which - int(before)) & 1;
+        before += groups;
+        if (own >= groups) continue;
         const int from = (OfA ? t.row0 : t.col0) + row0, end = OfA ? t.rows_end : p.N;
-        const float* base = OfA ? p.a_scales : p.b_scales;
-        int64_t row_step = 1, block_step = OfA ? p.a_scale_stride : p.b_scale_stride;
-        if (Grad) base += t.k0 / kBlock * block_step;
-        else if (OfA) row_step = block_step, block_step = 1;
-        else {
-            base += t.e * p.b_scale_batch;
-            if (!p.transposed) row_step = block_step, block_step = 1;
-        }
-        const float* at[kLoads];
+        const int64_t stride = OfA ? p.a_scale_stride : p.b_scale_stride;
+        const bool vectors = p.scale_vectors && (Grad || OfA || !p.transposed);
+        // rows past the last read the last one's, or what lies in the same 16 bytes
+        const float* at[Grad ? kSets : kLoads];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int row = min(from + (kUniform ? kBlock * i : lane + 32 * i), end - 1);
-            at[i] = base + int64_t(kUniform ? row / kBlock : row) * row_step;
+        for (int i = 0; i < (Grad ? kSets : kLoads); ++i) {
+            if (Grad) at[i] = (OfA ? p.a_scales : p.b_scales) + t.k0 / kBlock * stride + min(from + 4 * lane + 128 * i, (end - 1) & ~3);
+            else if (OfA) at[i] = p.a_scales + min(from + lane + 32 * i, end - 1) * stride;
+            else {
+                const int n = min(from + 32 * min(lane, kWords - 1), end - 1) / kBlock;
+                at[i] = p.b_scales + t.e * p.b_scale_batch + (p.transposed ? n : n * stride);
+            }
         }
-        const bool vectors = block_step == 1 && p.scale_vectors;
-        auto fetch = [&](float (&x)[kLoads][kAhead], int b0) {
-            if (b0 >= t.blocks) return;
+        float4 v[kLoads];
+        auto load = [&](int g) {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                if (vectors) {
-                    const float4 v = *reinterpret_cast<const float4*>(at[i] + b0);
-                    x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+                if (Grad) {
+                    const float* x = at[i / 4] + min(kAhead * g + i % 4, t.blocks - 1) * stride;
+                    const int left = end - 1 - min(from + 4 * lane + 128 * (i / 4), (end - 1) & ~3);
+                    if (vectors) v[i] = *reinterpret_cast<const float4*>(x);
+                    else v[i] = make_float4(x[0], x[min(1, left)], x[min(2, left)], x[min(3, left)]);
                 } else {
-#pragma unroll
-                    for (int q = 0; q < kAhead; ++q) x[i][q] = at[i][min(b0 + q, t.blocks - 1) * block_step];
+                    const int b = kAhead * g, last = t.blocks - 1;
+                    const int64_t each = OfA || !p.transposed ? 1 : stride;
+                    if (vectors) v[i] = *reinterpret_cast<const float4*>(at[i] + b);
+                    else v[i] = make_float4(at[i][b * each], at[i][min(b + 1, last) * each], at[i][min(b + 2, last) * each], at[i][min(b + 3, last) * each]);
                 }
             }
         };
         const bool look = OfA ? t.col0 == 0 : t.row0 == (Grad ? 0 : tiles.first[t.e]);
-        auto put = [&](const float (&x)[kLoads][kAhead], int b0) {
-            uint32_t w[kLoads];
+        load(own);
+        for (int g = own; g < groups; g += 2) {
+            uint32_t w[kWords];
+            if (Grad) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) w[i] = exponents_of(x[i]);
+                for (int i = 0; i < kSets; ++i) {
+                    const float4 &a = v[4 * i], &b = v[4 * i + 1], &c = v[4 * i + 2], &d = v[4 * i + 3];
+                    w[4 * i] = exponents_of(a.x, b.x, c.x, d.x), w[4 * i + 1] = exponents_of(a.y, b.y, c.y, d.y);
+                    w[4 * i + 2] = exponents_of(a.z, b.z, c.z, d.z), w[4 * i + 3] = exponents_of(a.w, b.w, c.w, d.w);
+                }
+            } else if (OfA) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = exponents_of(v[i].x, v[i].y, v[i].z, v[i].w);
+            } else {
+                const uint32_t own_word = exponents_of(v[0].x, v[0].y, v[0].z, v[0].w);
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) w[i] = __shfl_sync(kFull, own_word, i);
+            }
+            // the first tile in each row or column of tiles looks whether they are powers of two
             if (look)
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i)
+                for (int i = 0; i < kLoads; ++i) {
+                    const float x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-                    for (int q = 0; q < kAhead; ++q) bad |= b0 + q < t.blocks && from + (kUniform ? kBlock * i : lane + 32 * i) < end && no_power(x[i][q]);
-            ok = __all_sync(kFull, wait(&empty[g.at], g.phase ^ 1));
-            if (!ok) return;
-            unsigned char* to = exponents + g.at * bytes + lane * 16;
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = from + (Grad ? 4 * lane + 128 * (i / 4) + j : OfA ? lane + 32 * i : lane < kWords ? 32 * lane : 1 << 30), block = kAhead * g + (Grad ? i % 4 : j);
+                        bad |= row < end && block < t.blocks && no_power(x[j]);
+                    }
+                }
+            if (g + 2 < groups) load(g + 2);
+            if (!__all_sync(kFull, wait(empty, phase ^ 1))) return;
+            phase ^= 1;
+            if (Grad) {
 #pragma unroll
-            for (int i = 0; i < Count; i += 4) *reinterpret_cast<uint4*>(to + 128 * i) = make_uint4(w[i / kEach], w[(i + 1) / kEach], w[(i + 2) / kEach], w[(i + 3) / kEach]);
+                for (int i = 0; i < kWords; ++i) {
+                    const int row = 4 * lane + (i & 3);
+                    *reinterpret_cast<uint32_t*>(to + 512 * (i / 4) + (row & 31) * 16 + (row >> 5) * 4) = w[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kWords; i += 4) *reinterpret_cast<uint4*>(to + 128 * i + lane * 16) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-                if (pair) arrive_at_first<true>(&full[g.at]);
-                else arrive_at_first<false>(&full[g.at]);
+                if (pair) arrive_at_first<true>(full);
+                else arrive_at_first<false>(full);
             }
-            g.next(2);
-        };
-        float x[kLoads][kAhead], y[kLoads][kAhead], z[kLoads][kAhead];
-        fetch(x, 0);
-        fetch(y, kAhead);
-        fetch(z, 2 * kAhead);
-        for (int b0 = 0; ok && b0 < t.blocks; b0 += 3 * kAhead) {
-            put(x, b0);
-            fetch(x, b0 + 3 * kAhead);
-            if (!ok || b0 + kAhead >= t.blocks) break;
-            put(y, b0 + kAhead);
-            fetch(y, b0 + 4 * kAhead);
-            if (!ok || b0 + 2 * kAhead >= t.blocks) break;
-            put(z, b0 + 2 * kAhead);
-            fetch(z, b0 + 5 * kAhead);
         }
     }
     if (bad) atomicCAS(p.status, 0, kStatusScale);
@@ -457,14 +518,15 @@ __device__ __forceinline__ void both_ctas() {
 }
 
 template <int BN, bool Pair, bool Grad, typename Out>
-__global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(const __grid_constant__ ProductArgs p) {
-    constexpr int kHalf = BN / 2, kChunks = kHalf / 32, kGroups = BN / 128, kStages = stages_of(BN, Pair), kShare = share_bytes(BN, Pair);
+__global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const __grid_constant__ ProductArgs p) {
+    constexpr int kChunks = BN / 32, kFirstHalf = (kChunks + 1) / 2, kStages = stages_of(BN, Pair), kShare = share_bytes(BN, Pair);
     constexpr int kCtas = Pair ? 2 : 1;
     constexpr bool kShared = second_tile(BN) < BN;
     extern __shared__ unsigned char dynamic_smem[];
     unsigned char* const ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic_smem) + 1023) & ~uintptr_t(1023));
-    unsigned char* const exponents = ring + kStages * kShare;
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], scales_full[2], scales_empty[2], ready[2], drained, ended;
+    unsigned char* const staging = ring + kStages * kShare;
+    unsigned char* const exponents = staging + kSumWarps * kStagingBytes;
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], scales_full[2], scales_empty[2], ready[2], drained[2], taken, ended;
     __shared__ uint32_t tmem_at;
     __shared__ int stopped;
     __shared__ int32_t starts[TIDE_MAX_EXPERTS + 1], first[TIDE_MAX_EXPERTS + 1], sums[32];
@@ -475,7 +537,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
         for (int i = 0; i < 2; ++i) barrier_init(&scales_full[i], 2 * kCtas), barrier_init(&scales_empty[i], 1), barrier_init(&ready[i], 1);
-        barrier_init(&drained, kSumWarps * kCtas), barrier_init(&ended, 1);
+        for (int i = 0; i < 2; ++i) barrier_init(&drained[i], kSumWarps * kCtas);
+        barrier_init(&taken, kSumWarps / 2 * kCtas), barrier_init(&ended, 1);
         stopped = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -503,14 +566,18 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
             Cursor s, g;
             uint32_t tile = 0;
             bool ok = true;
-            for (int64_t it = begin; ok && it < tiles.count; it += step) {
-                const Tile t = tiles.at(it);
-                if (t.blocks == 0) continue;
+            int blocks = begin < tiles.count ? tiles.at(begin).blocks : 0, next = 0;
+            for (int64_t it = begin; ok && it < tiles.count; it += step, blocks = next) {
+                if (blocks == 0) {
+                    next = it + step < tiles.count ? tiles.at(it + step).blocks : 0;
+                    continue;
+                }
                 const uint32_t to = tmem + (tile & 1) * second_tile(BN);
-                // where the tile before began to be taken out, the one before that has been
-                if (!(ok = tile == 0 || __all_sync(kFull, wait(&drained, (tile - 1) & 1)))) break;
+                // the tile before the last has been taken out, and of the last the columns that it shares
+                if (!(ok = tile < 2 || __all_sync(kFull, wait(&drained[tile & 1], ((tile >> 1) - 1) & 1)))) break;
+                if (kShared && !(ok = tile == 0 || __all_sync(kFull, wait(&taken, (tile - 1) & 1)))) break;
                 uint32_t a_scales = 0, b_scales = 0;
-                for (int b = 0; b < t.blocks; ++b) {
+                for (int b = 0; b < blocks; ++b) {
                     const uint32_t in = b % kAhead;
                     if (in == 0) {
                         if (!(ok = __all_sync(kFull, wait(&scales_full[g.at], g.phase)))) break;
@@ -520,7 +587,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
                         if (elected()) {
                             copy_exponents<Pair>(a_scales, x);
 #pragma unroll
-                            for (int i = 0; i < kGroups; ++i) copy_exponents<Pair>(b_scales + 4 * i, x + 512 * (1 + i));
+                            for (int i = 0; i < exponent_words(BN) / 4; ++i) copy_exponents<Pair>(b_scales + 4 * i, x + 512 * (1 + i));
                             commit<Pair>(&scales_empty[g.at]);
                         }
                         __syncwarp();
@@ -535,32 +602,38 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
 #pragma unroll
                         for (int k = 0; k < 4; ++k) multiply_scaled<Pair>(to, da + 2 * k, db + 2 * k, instruction, a_scales, b_scales, b > 0 || k > 0);
                         commit<Pair>(&empty[s.at]);
-                        if (b + 1 == t.blocks) commit<Pair>(&ready[tile & 1]);
+                        if (b + 1 == blocks) commit<Pair>(&ready[tile & 1]);
                     }
                     __syncwarp();
                     s.next(kStages);
+                    // the next tile is found while this one's products wait for their turn
+                    if (b == 0) next = it + step < tiles.count ? tiles.at(it + step).blocks : 0;
                 }
                 ++tile;
             }
             if (!ok) end_products<Pair>(&ended);
         }
-    } else if (warp == 2) {
-        write_exponents<Grad, true, 4>(p, tiles, rank * kTileM, begin, step, exponents, exponent_bytes(BN), scales_full, scales_empty, Pair, wait);
-    } else if (warp == 3) {
-        write_exponents<Grad, false, 4 * kGroups>(p, tiles, 0, begin, step, exponents + 512, exponent_bytes(BN), scales_full, scales_empty, Pair, wait);
-    } else if (warp >= 4) {
+    } else if (warp < 4 || warp >= 4 + kSumWarps) {
+        // warps 2 and 3 write A's and B's exponents into the first buffer, the last two into the second
+        const int which = warp >= 4;
+        unsigned char* const to = exponents + which * exponent_bytes(BN);
+        if ((warp & 1) == 0) write_exponents<BN, Grad, true>(p, tiles, rank * kTileM, which, begin, step, to, &scales_full[which], &scales_empty[which], Pair, wait);
+        else write_exponents<BN, Grad, false>(p, tiles, 0, which, begin, step, to + 512, &scales_full[which], &scales_empty[which], Pair, wait);
+    } else {
         const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t from = tmem + (uint32_t(quarter * 32) << 16) + half * kHalf;
+        const int first_col = half * kFirstHalf * 32, chunks = half ? kChunks - kFirstHalf : kFirstHalf;
+        const uint32_t from = tmem + (uint32_t(quarter * 32) << 16) + first_col;
         uint32_t tile = 0;
         bool ok = true;
         for (int64_t it = begin; ok && it < tiles.count; it += step) {
             const Tile t = tiles.at(it);
-            const int row = t.row0 + rank * kTileM + quarter * 32 + lane, col = t.col0 + half * kHalf;
+            const int row = t.row0 + rank * kTileM + quarter * 32 + lane, col = t.col0 + first_col;
             const bool here = row < t.rows_end;
+            const bool bulk = p.bulk && row - lane + 32 <= t.rows_end;  // TMA writes whole boxes, so all of the warp's rows have to be there
             Out* const to = static_cast<Out*>(Grad ? p.grads.p[t.e] : p.out) + row * p.out_stride + col;
             if (t.blocks == 0) {
                 const uint32_t none[32] = {};
-                for (int c = 0; here && c < kChunks; ++c) put_sums(to + c * 32, none, p.N - col - c * 32, p.out_vectors);
+                for (int c = 0; here && c < chunks; ++c) put_sums(to + c * 32, none, p.N - col - c * 32, p.out_vectors);
                 continue;
             }
             ok = __all_sync(kFull, wait(&ready[tile & 1], (tile >> 1) & 1));
@@ -570,22 +643,28 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
             // the columns that the next tile's sums share come first: of the first buffer the last, of the second the first
             const bool backwards = kShared && !(tile & 1);
             const bool holds = kShared && half == int(backwards);
-            if (!holds && lane == 0) arrive_at_first<Pair>(&drained);
             uint32_t x[2][32];
-            auto column = [&](int c) { return (backwards ? kChunks - 1 - c : c) * 32; };
+            auto column = [&](int c) { return (backwards ? chunks - 1 - c : c) * 32; };
             load_sums(x[0], at + column(0));
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
+            for (int c = 0; c < kFirstHalf; ++c) {
+                if (c >= chunks) break;
                 sums_loaded();
-                if (c + 1 < kChunks) load_sums(x[(c + 1) & 1], at + column(c + 1));
-                if (holds && c == 0) {
+                if (c + 1 < chunks) load_sums(x[(c + 1) & 1], at + column(c + 1));
+                if ((holds && c == 0) || c + 1 == chunks) {
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                    if (lane == 0) arrive_at_first<Pair>(&drained);
+                    if (lane == 0) {
+                        if (holds && c == 0) arrive_at_first<Pair>(&taken);
+                        if (c + 1 == chunks) arrive_at_first<Pair>(&drained[tile & 1]);
+                    }
                 }
-                if (here) put_sums(to + column(c), x[c & 1], p.N - col - column(c), p.out_vectors);
+                if (bulk) put_sums_bulk<Grad, Out>(p, staging + (warp - 4) * kStagingBytes, x[c & 1], col + column(c), row - lane, t.e);
+                else if (here) put_sums(to + column(c), x[c & 1], p.N - col - column(c), p.out_vectors);
             }
             ++tile;
         }
+        // what lies in shared memory has been read, and written
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncwarp();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -604,7 +683,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) scaled_product_kernel(cons
 // them with the block's scales and add them to the tile's sums in registers, while the next block is multiplied into another
 // buffer. No sum of more than 128 products is formed before its scale is applied.
 template <int BN, bool Grad, typename Out>
-__global__ void __launch_bounds__(kProductThreads, 1) any_scales_kernel(const __grid_constant__ ProductArgs p) {
+__global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid_constant__ ProductArgs p) {
     constexpr int kBuffers = kTmemCols / BN, kHalf = BN / 2, kChunks = kHalf / 32, kStages = stages_of(BN, false), kShare = share_bytes(BN, false);
     extern __shared__ unsigned char dynamic_smem[];
     unsigned char* const ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic_smem) + 1023) & ~uintptr_t(1023));
@@ -762,29 +841,48 @@ int describe(CUtensorMap* map, const tide_fp8_t& m, int64_t len, int64_t rows, i
     return r == CUDA_SUCCESS ? TIDE_OK : record_cuda_error(cudaErrorInvalidValue);
 }
 
+// The result for TMA: `batches` matrices (0: one) of `rows` rows of `N` elements, if they lie as it needs them.
+int describe_result(ProductArgs* p, const void* at, int bf16, int64_t N, int64_t rows, int64_t stride, int64_t batches, int64_t batch_bytes) {
+    const int elem = bf16 ? 2 : 4;
+    p->bulk = aligned(at, 16) && stride * elem % 16 == 0 && stride * elem < int64_t(1) << 40 && (batches <= 1 || (batch_bytes > 0 && batch_bytes % 16 == 0 && batch_bytes < int64_t(1) << 40));
+    if (!p->bulk) return TIDE_OK;
+    decltype(&cuTensorMapEncodeTiled) encode;
+    const int rc = encoder(&encode);
+    if (rc != TIDE_OK) return rc;
+    const cuuint64_t dims[3] = {cuuint64_t(N), cuuint64_t(rows), cuuint64_t(batches)};
+    const cuuint64_t strides[2] = {cuuint64_t(stride * elem), cuuint64_t(batches > 1 ? batch_bytes : stride * elem * rows)};
+    const cuuint32_t boxes[3] = {cuuint32_t(64 / elem), 32, 1}, steps[3] = {1, 1, 1};
+    const CUresult r = encode(&p->result, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, batches > 0 ? 3 : 2, const_cast<void*>(at), dims, strides, boxes, steps,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? TIDE_OK : record_cuda_error(cudaErrorInvalidValue);
+}
+
 template <int BN, bool Pair, bool Grad, typename Out>
 int launch(const ProductArgs& p, bool any_scales, int64_t most_tiles, const Ctas& c, cudaStream_t stream) {
     void (*kernel)(ProductArgs) = scaled_product_kernel<BN, Pair, Grad, Out>;
     if constexpr (!Pair)
         if (any_scales) kernel = any_scales_kernel<BN, Grad, Out>;
-    const int smem = stages_of(BN, Pair) * share_bytes(BN, Pair) + 2 * exponent_bytes(BN) + 1024;
+    const int smem = stages_of(BN, Pair) * share_bytes(BN, Pair) + kSumWarps * kStagingBytes + 2 * exponent_bytes(BN) + 1024;
     TIDE_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     const int64_t at_once = (c.most ? c.most : c.sms) / (Pair ? 2 : 1);
     const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(most_tiles, at_once));
-    TIDE_CUDA(launch_clusters_after(kernel, Pair ? 2 : 1, int(tiles * (Pair ? 2 : 1)), kProductThreads, smem, stream, p));
+    TIDE_CUDA(launch_clusters_after(kernel, Pair ? 2 : 1, int(tiles * (Pair ? 2 : 1)), any_scales ? kAnyThreads : kScaledThreads, smem, stream, p));
     return TIDE_OK;
 }
 
 bool vectors32(const void* p, int64_t stride, int64_t rows, int elem) { return aligned(p, 32) && (rows <= 1 || stride * elem % 32 == 0); }
 
-// The kernel for `down` tiles of 128 rows of `N` columns. Pairs' tiles of 256 x 256 where they are many enough to keep all SMs busy
-// and experts have rows enough to fill them; else tiles of 128 x 128, as also where sums go to registers.
+// Whether `down` tiles of 128 rows by N columns go to pairs of CTAs, in tiles of 256 x 256: where these are many enough to keep all
+// SMs busy, and experts have rows enough to fill them. Else, and where sums go to registers, tiles are 128 x 128. (Pairs' tiles of
+// 192 and 224 columns, whose sums share none with the next tile's, were slower at every length: 524288 rows of 2048 by 1536 columns
+// 1141 and 1122 us, with 256 1083; 131072 of 768 by 2048 195 and 296, with 256 180.)
 bool pairs(int64_t rows, int64_t down, int64_t N, bool any_scales, const Ctas& c) {
     return !any_scales && c.most != 1 && rows >= 2 * kTileM && down * ((N + 255) / 256) >= 2 * c.sms;
 }
 
 template <bool Grad>
-int launch_any(const ProductArgs& p, bool pair, bool any_scales, int64_t tiles, int bf16, const Ctas& c, cudaStream_t stream) {
+int launch_any(const ProductArgs& p, bool pair, bool any_scales, int64_t down, int bf16, const Ctas& c, cudaStream_t stream) {
+    const int64_t tiles = down * ((p.N + (pair ? 255 : 127)) / (pair ? 256 : 128));
     if (pair) return bf16 ? launch<256, true, Grad, __nv_bfloat16>(p, false, tiles, c, stream) : launch<256, true, Grad, float>(p, false, tiles, c, stream);
     return bf16 ? launch<128, false, Grad, __nv_bfloat16>(p, any_scales, tiles, c, stream) : launch<128, false, Grad, float>(p, any_scales, tiles, c, stream);
 }
@@ -808,8 +906,9 @@ int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets,
     p.offsets = offsets, p.M = int32_t(M), p.E = E, p.N = int32_t(N), p.K = int32_t(K), p.rows = 0;
     p.out = out, p.out_stride = out_stride, p.out_vectors = vectors32(out, out_stride, M, out_bf16 ? 2 : 4);
     p.status = status, p.timeout_ns = timeout_ns;
-    // padded_blocks counts tiles of 128 rows; of 256 there are fewer
-    return launch_any<false>(p, pair, any, down * ((N + (pair ? 255 : 127)) / (pair ? 256 : 128)), out_bf16, c, stream);
+    if ((rc = describe_result(&p, out, out_bf16, N, M, out_stride, 0, 0)) != TIDE_OK) return rc;
+    // `down` counts tiles of 128 rows; of 256 there are fewer
+    return launch_any<false>(p, pair, any, down, out_bf16, c, stream);
 }
 
 int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, uint32_t flags, int64_t N, int64_t K, const GradPtrs& grads,
@@ -827,13 +926,21 @@ int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int
     p.most_blocks = int32_t(padded / kBlock);
     p.a_scales = dy.scales, p.a_scale_stride = dy.scale_stride;
     p.b_scales = a.scales, p.b_scale_stride = a.scale_stride;
+    p.scale_vectors = aligned(dy.scales, 16) && dy.scale_stride % 4 == 0 && aligned(a.scales, 16) && a.scale_stride % 4 == 0;
     p.offsets = offsets, p.M = int32_t(M), p.E = E, p.N = int32_t(K), p.rows = int32_t(N);
     p.grads = grads, p.out_stride = K;
     p.out_vectors = 1;
     for (int e = 0; e < E; ++e) p.out_vectors &= vectors32(grads.p[e], K, N, grad_bf16 ? 2 : 4);
     p.status = status, p.timeout_ns = timeout_ns;
-    const int64_t tiles = int64_t(E) * (pair ? (N + 2 * kTileM - 1) / (2 * kTileM) : (N + kTileM - 1) / kTileM) * ((K + (pair ? 255 : 127)) / (pair ? 256 : 128));
-    return launch_any<true>(p, pair, any, tiles, grad_bf16, c, stream);
+    // gradients at one distance from each other are one array to TMA
+    const int64_t pitch = E > 1 ? static_cast<const char*>(grads.p[1]) - static_cast<const char*>(grads.p[0]) : 0;
+    bool even = true;
+    for (int e = 2; e < E; ++e) even &= static_cast<const char*>(grads.p[e]) - static_cast<const char*>(grads.p[e - 1]) == pitch;
+    if (even) {
+        const int rc = describe_result(&p, grads.p[0], grad_bf16, K, N, K, E, pitch);
+        if (rc != TIDE_OK) return rc;
+    }
+    return launch_any<true>(p, pair, any, down, grad_bf16, c, stream);
 }
 
 }  // namespace tide

@@ -368,7 +368,7 @@ def bound(blocks, size):
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("T, k, E, N, K", [(1, 1, 1, 1, 1), (1, 8, 16, 200, 300), (37, 2, 5, 128, 128), (300, 3, 4, 331, 525), (200, 4, 6, 513, 129), (1000, 2, 3, 260, 1040),
-                                           (5000, 4, 9, 768, 384), (3000, 8, 20, 1003, 200)])
+                                           (5000, 4, 9, 768, 384), (3000, 8, 20, 1003, 200), (3000, 8, 4, 512, 2600)])
 @pytest.mark.parametrize("any_scales", [False, True])
 def test_products(tide, T, k, E, N, K, kind, any_scales):
     g = gen(N + K)
@@ -400,7 +400,7 @@ def test_products(tide, T, k, E, N, K, kind, any_scales):
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("T, k, E, N, K", [(1, 1, 1, 1, 1), (1, 4, 16, 200, 300), (37, 2, 5, 128, 128), (300, 3, 4, 331, 525), (1000, 2, 3, 260, 1040), (3000, 4, 9, 768, 384),
-                                           (900, 4, 16, 900, 1100)])
+                                           (900, 4, 16, 900, 1100), (6000, 4, 16, 1280, 512)])
 @pytest.mark.parametrize("any_scales", [False, True])
 def test_weight_gradients(tide, T, k, E, N, K, kind, any_scales):
     g = gen(N + K + 1)
