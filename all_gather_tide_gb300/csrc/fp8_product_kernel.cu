@@ -49,7 +49,7 @@ struct ProductArgs {
     int64_t out_stride;
     int scale_vectors;  // scales that lie side by side can be read four at a time
     int bulk;         // the result can be written by TMA
-    int out_vectors;  // rows of the result can be written 32 bytes at a time
+    int out_vectors;  // and 16 bytes of a row at a time
     GradPtrs grads;
     int* status;
     uint64_t timeout_ns;
@@ -236,11 +236,9 @@ struct Tiles {
     __device__ __forceinline__ Tiles(const ProductArgs& p, int32_t* starts, int32_t* first, int32_t* sums)
         : p(p), starts(starts), first(first), across(uint32_t((p.N + BN - 1) / BN)), down(uint32_t((p.rows + Rows - 1) / Rows)) {
         constexpr int kUnit = Grad ? kBlock : Rows;
-        for (int e = threadIdx.x; e <= p.E; e += int(blockDim.x)) {
-            const Span s = span_of(p.offsets, min(e, p.E - 1), p.M);
-            first[e] = e < p.E ? s.first : s.first + s.count;
-        }
-        exclusive_sums(starts, p.E, sums, [&](int e) { return (span_of(p.offsets, e, p.M).count + kUnit - 1) / kUnit; });
+        for (int e = threadIdx.x; e <= p.E; e += int(blockDim.x)) first[e] = !p.offsets ? (e ? p.M : 0) : min(max(load_here(p.offsets + e), 0), p.M);
+        __syncthreads();
+        exclusive_sums(starts, p.E, sums, [&](int e) { return (max(first[e + 1] - first[e], 0) + kUnit - 1) / kUnit; });
         if (Grad) {  // whatever the offsets hold, no tile reaches past the transposed operands
             for (int e = threadIdx.x; e <= p.E; e += int(blockDim.x)) starts[e] = min(starts[e], p.most_blocks);
             __syncthreads();
@@ -313,59 +311,77 @@ __device__ __forceinline__ void end_products(uint64_t* ended) {
     }
 }
 
-__device__ __forceinline__ void put32(void* p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
-}
-
 // Sums of a row, of which `left` columns are there.
 template <typename Out, int Count>
 __device__ __forceinline__ void put_sums(Out* to, const uint32_t (&x)[Count], int left, bool vectors) {
-    constexpr int kStep = 32 / sizeof(Out);
+    constexpr int kStep = 16 / sizeof(Out);
 #pragma unroll
     for (int j = 0; j < Count; j += kStep) {
-        if (vectors && j + kStep <= left) {
-            uint32_t w[8];
+        float v[kStep];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if constexpr (sizeof(Out) == 2) w[i] = pack(__uint_as_float(x[j + 2 * i]), __uint_as_float(x[j + 2 * i + 1]));
-                else w[i] = x[j + i];
-            }
-            put32(to + j, w);
+        for (int i = 0; i < kStep; ++i) v[i] = __uint_as_float(x[j + i]);
+        if (vectors && j + kStep <= left) {
+            put(to + j, v);
         } else {
 #pragma unroll
             for (int i = 0; i < kStep; ++i) {
-                const float v[1] = {__uint_as_float(x[j + i])};
-                if (j + i < left) put(to + j + i, v);
+                const float one[1] = {v[i]};
+                if (j + i < left) put(to + j + i, one);
             }
         }
     }
 }
 
-// 64 bytes of each of the warp's 32 rows, by way of 2 KB of shared memory in which 16-byte pieces are swizzled as the tensor
-// map says: a lane's own stores of 32 bytes reach 32 lines an instruction, and those of all eight warps were what bounded
-// short products.
+// A warp's 32 rows of sums go to the result by way of 2 KB of shared memory, 64 bytes of each row at a time, in which 16-byte pieces
+// are swizzled as the tensor map says: whole boxes by TMA, others (an expert's last rows, results that TMA cannot address) row by
+// row. A lane's own stores would reach 32 lines an instruction: those of all eight warps bounded short products, and of two
+// bytes each took 10 us for a tile.
 constexpr int kStagingBytes = 2048;  // a warp
-template <bool Grad>
-__device__ __forceinline__ void put_bulk(const ProductArgs& p, unsigned char* staging, const uint32_t (&w)[16], int col, int row, int e) {
+template <bool Grad, typename Out>
+__device__ __forceinline__ void put_staged(const ProductArgs& p, unsigned char* staging, const uint32_t (&w)[16], int e, int row0, int rows, int col) {
+    constexpr int kCols = 64 / sizeof(Out);
     const int lane = threadIdx.x & 31;
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the bytes before have been read
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staging + lane * 64 + (i ^ (lane >> 1 & 3)) * 16) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (p.bulk && rows >= 32) {  // TMA writes whole boxes, so all of the rows have to be there
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            if constexpr (Grad)
+                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&p.result), "r"(col), "r"(row0), "r"(e), "r"(smem_u32(staging)) : "memory");
+            else
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&p.result), "r"(col), "r"(row0), "r"(smem_u32(staging)) : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        return;
+    }
     __syncwarp();
-    if (lane == 0) {
-        if constexpr (Grad)
-            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&p.result), "r"(col), "r"(row), "r"(e), "r"(smem_u32(staging)) : "memory");
-        else
-            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&p.result), "r"(col), "r"(row), "r"(smem_u32(staging)) : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    Out* const to = static_cast<Out*>(Grad ? p.grads.p[e] : p.out) + row0 * p.out_stride + col;
+    if (p.out_vectors && col + kCols <= p.N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + lane / 4, piece = lane & 3;
+            if (row < rows) *reinterpret_cast<uint4*>(to + row * p.out_stride + piece * (16 / sizeof(Out))) = *reinterpret_cast<const uint4*>(staging + row * 64 + (piece ^ (row >> 1 & 3)) * 16);
+        }
+    } else {
+        // row kRows * i + r of step i; its swizzle depends on i alone
+        constexpr int kRows = 32 / kCols;
+        const int c = lane % kCols, r = lane / kCols, piece = c * int(sizeof(Out)) / 16;
+        const unsigned char* from = staging + r * 64 + c * int(sizeof(Out)) % 16;
+        const int left = col + c < p.N ? rows - r : 0;
+        Out* at = to + r * p.out_stride + c;
+#pragma unroll
+        for (int i = 0; i < 32 / kRows; ++i, at += kRows * p.out_stride)
+            if (kRows * i < left) *at = *reinterpret_cast<const Out*>(from + i * kRows * 64 + (piece ^ (kRows * i >> 1 & 3)) * 16);
     }
 }
-// 32 sums of each row, in that way.
+// 32 sums of each row, in that way; `rows` of the warp's rows are there.
 template <bool Grad, typename Out>
-__device__ __forceinline__ void put_sums_bulk(const ProductArgs& p, unsigned char* staging, const uint32_t (&x)[32], int col, int row, int e) {
+__device__ __forceinline__ void put_sums_staged(const ProductArgs& p, unsigned char* staging, const uint32_t (&x)[32], int e, int row0, int rows, int col) {
     constexpr int kCols = 64 / sizeof(Out);
+    if (rows <= 0) return;
 #pragma unroll
     for (int c = 0; c < 32; c += kCols) {
         uint32_t w[16];
@@ -374,7 +390,7 @@ __device__ __forceinline__ void put_sums_bulk(const ProductArgs& p, unsigned cha
             if constexpr (sizeof(Out) == 2) w[i] = pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
             else w[i] = x[c + i];
         }
-        if (col + c < p.N) put_bulk<Grad>(p, staging, w, col + c, row, e);
+        if (col + c < p.N) put_staged<Grad, Out>(p, staging, w, e, row0, min(rows, 32), col + c);
     }
 }
 
@@ -627,13 +643,11 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
         bool ok = true;
         for (int64_t it = begin; ok && it < tiles.count; it += step) {
             const Tile t = tiles.at(it);
-            const int row = t.row0 + rank * kTileM + quarter * 32 + lane, col = t.col0 + first_col;
-            const bool here = row < t.rows_end;
-            const bool bulk = p.bulk && row - lane + 32 <= t.rows_end;  // TMA writes whole boxes, so all of the warp's rows have to be there
-            Out* const to = static_cast<Out*>(Grad ? p.grads.p[t.e] : p.out) + row * p.out_stride + col;
+            const int row0 = t.row0 + rank * kTileM + quarter * 32, rows = t.rows_end - row0, col = t.col0 + first_col;
+            unsigned char* const mine = staging + (warp - 4) * kStagingBytes;
             if (t.blocks == 0) {
                 const uint32_t none[32] = {};
-                for (int c = 0; here && c < chunks; ++c) put_sums(to + c * 32, none, p.N - col - c * 32, p.out_vectors);
+                for (int c = 0; c < chunks; ++c) put_sums_staged<Grad, Out>(p, mine, none, t.e, row0, rows, col + c * 32);
                 continue;
             }
             ok = __all_sync(kFull, wait(&ready[tile & 1], (tile >> 1) & 1));
@@ -658,8 +672,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
                         if (c + 1 == chunks) arrive_at_first<Pair>(&drained[tile & 1]);
                     }
                 }
-                if (bulk) put_sums_bulk<Grad, Out>(p, staging + (warp - 4) * kStagingBytes, x[c & 1], col + column(c), row - lane, t.e);
-                else if (here) put_sums(to + column(c), x[c & 1], p.N - col - column(c), p.out_vectors);
+                put_sums_staged<Grad, Out>(p, mine, x[c & 1], t.e, row0, rows, col + column(c));
             }
             ++tile;
         }
@@ -870,7 +883,7 @@ int launch(const ProductArgs& p, bool any_scales, int64_t most_tiles, const Ctas
     return TIDE_OK;
 }
 
-bool vectors32(const void* p, int64_t stride, int64_t rows, int elem) { return aligned(p, 32) && (rows <= 1 || stride * elem % 32 == 0); }
+bool vectors16(const void* p, int64_t stride, int64_t rows, int elem) { return aligned(p, 16) && (rows <= 1 || stride * elem % 16 == 0); }
 
 // Whether `down` tiles of 128 rows by N columns go to pairs of CTAs, in tiles of 256 x 256: where these are many enough to keep all
 // SMs busy, and experts have rows enough to fill them. Else, and where sums go to registers, tiles are 128 x 128. (Pairs' tiles of
@@ -904,7 +917,7 @@ int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets,
     // what such a vector holds behind a row's last scale is read and not used; it is of the same 16 bytes
     p.scale_vectors = aligned(a.scales, 16) && a.scale_stride % 4 == 0 && aligned(w.scales, 16) && w.scale_stride % 4 == 0 && (E == 1 || w.scale_batch % 4 == 0);
     p.offsets = offsets, p.M = int32_t(M), p.E = E, p.N = int32_t(N), p.K = int32_t(K), p.rows = 0;
-    p.out = out, p.out_stride = out_stride, p.out_vectors = vectors32(out, out_stride, M, out_bf16 ? 2 : 4);
+    p.out = out, p.out_stride = out_stride, p.out_vectors = vectors16(out, out_stride, M, out_bf16 ? 2 : 4);
     p.status = status, p.timeout_ns = timeout_ns;
     if ((rc = describe_result(&p, out, out_bf16, N, M, out_stride, 0, 0)) != TIDE_OK) return rc;
     // `down` counts tiles of 128 rows; of 256 there are fewer
@@ -930,7 +943,7 @@ int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int
     p.offsets = offsets, p.M = int32_t(M), p.E = E, p.N = int32_t(K), p.rows = int32_t(N);
     p.grads = grads, p.out_stride = K;
     p.out_vectors = 1;
-    for (int e = 0; e < E; ++e) p.out_vectors &= vectors32(grads.p[e], K, N, grad_bf16 ? 2 : 4);
+    for (int e = 0; e < E; ++e) p.out_vectors &= vectors16(grads.p[e], K, N, grad_bf16 ? 2 : 4);
     p.status = status, p.timeout_ns = timeout_ns;
     // gradients at one distance from each other are one array to TMA
     const int64_t pitch = E > 1 ? static_cast<const char*>(grads.p[1]) - static_cast<const char*>(grads.p[0]) : 0;
