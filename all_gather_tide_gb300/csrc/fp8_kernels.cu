@@ -29,11 +29,20 @@ __device__ __forceinline__ uint32_t codes2(float a, float b) {
 }
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) { return codes2(a, b) | codes2(c, d) << 16; }
 
-// Eight consecutive values of a row as they lie in memory, zeros behind `left` of them.
+// Two bf16 values times two powers of two: exact, but for values so small that their codes are zeros.
+__device__ __forceinline__ uint32_t times(uint32_t w, uint32_t f) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(f));
+    return r;
+}
+
+// Eight consecutive values of a row as they lie in memory, zeros behind `left` of them; and what a power of two, or one for
+// each, times them looks like in that type.
 template <typename T>
 struct Eight;
 template <>
 struct Eight<__nv_bfloat16> {
+    using Factor = uint16_t;  // a power of two, as bf16
     uint4 w;
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
     template <bool Vector>
@@ -54,8 +63,7 @@ struct Eight<__nv_bfloat16> {
         const uint32_t a = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
         return max(a << 16, a & 0xffff0000u);
     }
-    __device__ __forceinline__ void values(float (&x)[8]) const { widen(w, x); }
-    // Largest magnitudes of each of the eight columns so far.
+    // The larger magnitudes of each of the eight columns.
     __device__ __forceinline__ void raise(const Eight& o) {
         const uint32_t m = 0x7fff7fffu;
         w = make_uint4(__vmaxu2(w.x & m, o.w.x & m), __vmaxu2(w.y & m, o.w.y & m), __vmaxu2(w.z & m, o.w.z & m), __vmaxu2(w.w & m, o.w.w & m));
@@ -65,9 +73,26 @@ struct Eight<__nv_bfloat16> {
         o.w = make_uint4(__shfl_xor_sync(kFull, w.x, 16), __shfl_xor_sync(kFull, w.y, 16), __shfl_xor_sync(kFull, w.z, 16), __shfl_xor_sync(kFull, w.w, 16));
         return o;
     }
+    static __device__ __forceinline__ uint32_t magnitude(uint16_t bits) { return uint32_t(bits) << 16; }  // of a value that raise left
+    using Bits = uint16_t;
+    static __device__ __forceinline__ Factor factor(float f) { return uint16_t(__float_as_uint(f) >> 16); }
+    __device__ __forceinline__ void scale(Factor f) {
+        const uint32_t g = uint32_t(f) << 16 | f;
+        w = make_uint4(times(w.x, g), times(w.y, g), times(w.z, g), times(w.w, g));
+    }
+    // Each by its own factor, eight in order at f.
+    __device__ __forceinline__ void scale_each(const Factor* f) {
+        const uint4 g = *reinterpret_cast<const uint4*>(f);
+        w = make_uint4(times(w.x, g.x), times(w.y, g.y), times(w.z, g.z), times(w.w, g.w));
+    }
+    __device__ __forceinline__ float value(int j) const {
+        const uint32_t v = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
+        return j & 1 ? high_f32(v) : low_f32(v);
+    }
 };
 template <>
 struct Eight<float> {
+    using Factor = float;
     float x[8];
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -92,10 +117,6 @@ struct Eight<float> {
         for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(x[j]) & 0x7fffffffu);
         return a;
     }
-    __device__ __forceinline__ void values(float (&y)[8]) const {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[j];
-    }
     __device__ __forceinline__ void raise(const Eight& o) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(max(__float_as_uint(x[j]) & 0x7fffffffu, __float_as_uint(o.x[j]) & 0x7fffffffu));
@@ -106,7 +127,23 @@ struct Eight<float> {
         for (int j = 0; j < 8; ++j) o.x[j] = __uint_as_float(__shfl_xor_sync(kFull, __float_as_uint(x[j]), 16));
         return o;
     }
+    static __device__ __forceinline__ uint32_t magnitude(uint32_t bits) { return bits; }
+    using Bits = uint32_t;
+    static __device__ __forceinline__ Factor factor(float f) { return f; }
+    __device__ __forceinline__ void scale(Factor f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= f;
+    }
+    __device__ __forceinline__ void scale_each(const Factor* f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= f[j];
+    }
+    __device__ __forceinline__ float value(int j) const { return x[j]; }
 };
+template <typename T>
+__device__ __forceinline__ uint2 codes_of(const Eight<T>& x) {
+    return make_uint2(codes4(x.value(0), x.value(1), x.value(2), x.value(3)), codes4(x.value(4), x.value(5), x.value(6), x.value(7)));
+}
 
 // ---- the tokens' rows to where their pairs go, in 8 bits ----------------------------------------
 //
@@ -132,11 +169,9 @@ dispatch_fp8_kernel(const T* src, int64_t src_stride, int64_t tokens, int k, int
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) largest = max(largest, __shfl_xor_sync(kFull, largest, d));
         const Scale s = scale_of(largest);
-        float x[8], y[8];
-        a.values(x), b.values(y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= s.inverse, y[j] *= s.inverse;
-        const uint4 codes = make_uint4(codes4(x[0], x[1], x[2], x[3]), codes4(x[4], x[5], x[6], x[7]), codes4(y[0], y[1], y[2], y[3]), codes4(y[4], y[5], y[6], y[7]));
+        a.scale(Eight<T>::factor(s.inverse)), b.scale(Eight<T>::factor(s.inverse));
+        const uint2 lo = codes_of(a), hi = codes_of(b);
+        const uint4 codes = make_uint4(lo.x, lo.y, hi.x, hi.y);
         while (held) {
             const int j = __ffs(held) - 1;
             held &= held - 1;
@@ -159,19 +194,25 @@ dispatch_fp8_kernel(const T* src, int64_t src_stride, int64_t tokens, int k, int
 // the loads of whole columns meet in a bank.
 //
 // Bound by HBM: 2 or 4 bytes read a value and 1 or 2 written.
+// CTAs of an SM, as the registers are bounded for.
+template <typename T>
+constexpr int kTileCtasPerSm = sizeof(T) == 2 ? 4 : 2;
+
 struct TileOut {
     tide_fp8_t rows, columns;
     int has_rows, has_columns;
 };
 
+template <typename T>
 struct TileSmem {
-    uint64_t row_at[kBlock];                       // where each row lies; 0: none
-    __align__(16) uint32_t largest[kWarps][kBlock];  // of each column, as fp32 bits
+    uint64_t row_at[kBlock];                                     // where each row lies; 0: none
+    __align__(16) Eight<T> largest[kWarps][kBlock / 8];          // magnitudes of each column
+    __align__(16) typename Eight<T>::Factor column[kBlock];      // what each column is multiplied by
     __align__(16) unsigned char turned[kBlock * kBlock];
 };
 
 template <typename T>
-__device__ __forceinline__ void load_tile(Eight<T> (&x)[8], const TileSmem& sm, uint32_t col, uint32_t len, bool vector) {
+__device__ __forceinline__ void load_tile(Eight<T> (&x)[8], const TileSmem<T>& sm, uint32_t col, uint32_t len, bool vector) {
     const int row0 = (threadIdx.x >> 4) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -182,42 +223,49 @@ __device__ __forceinline__ void load_tile(Eight<T> (&x)[8], const TileSmem& sm, 
     }
 }
 
-// Codes of the tile's rows, `held` of them, at the matrix's row `first` and column `col`.
+// Codes of the tile's rows, scaled already, `held` of them, at the matrix's column `col`.
 template <typename T>
-__device__ __forceinline__ void put_rows(const Eight<T> (&x)[8], const float (&inverse)[8], char* codes, int64_t stride, int held, uint32_t col, uint32_t len) {
-    const int row0 = (threadIdx.x >> 4) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (row0 + i >= held || col >= len) continue;
-        float v[8];
-        x[i].values(v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= inverse[i];
-        *reinterpret_cast<uint2*>(codes + int64_t(row0 + i) * stride + col) = make_uint2(codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7]));
-    }
+__device__ __forceinline__ void put_row(const Eight<T>& x, int i, char* codes, int64_t stride, int held, uint32_t col, uint32_t len) {
+    const int row = (threadIdx.x >> 4) * 8 + i;
+    if (row < held && col < len) *reinterpret_cast<uint2*>(codes + row * stride + col) = codes_of(x);
 }
 
-// Turns the tile: codes of its columns from `col0` on, `columns` of them, each of `count` rows (a multiple of 16).
+// Turns the tile, scaled already: codes of `columns` of its columns, each of `count` rows (a multiple of 16).
 template <typename T>
-__device__ __forceinline__ void put_columns(const Eight<T> (&x)[8], const float (&inverse)[8], TileSmem& sm, char* codes, int64_t stride, int columns, int count) {
+__device__ __forceinline__ void put_columns(const Eight<T> (&x)[8], TileSmem<T>& sm, char* codes, int64_t stride, int columns, int count) {
     const int group = threadIdx.x & 15, rows8 = threadIdx.x >> 4;
-    float v[8][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i].values(v[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float f = inverse[j];
-        const uint2 w = make_uint2(codes4(v[0][j] * f, v[1][j] * f, v[2][j] * f, v[3][j] * f), codes4(v[4][j] * f, v[5][j] * f, v[6][j] * f, v[7][j] * f));
-        *reinterpret_cast<uint2*>(sm.turned + (group * 8 + j) * kBlock + ((rows8 ^ group) * 8)) = w;
-    }
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint2*>(sm.turned + (group * 8 + j) * kBlock + ((rows8 ^ group) * 8)) =
+            make_uint2(codes4(x[0].value(j), x[1].value(j), x[2].value(j), x[3].value(j)), codes4(x[4].value(j), x[5].value(j), x[6].value(j), x[7].value(j)));
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int at = q * 256 + threadIdx.x, c = at >> 3, pair = at & 7, g = c >> 3;
         uint4 w = *reinterpret_cast<const uint4*>(sm.turned + c * kBlock + ((pair ^ (g >> 1)) * 16));
         if (g & 1) w = make_uint4(w.z, w.w, w.x, w.y);
-        if (c < columns && pair * 16 < count) *reinterpret_cast<uint4*>(codes + int64_t(c) * stride + pair * 16) = w;
+        if (c < columns && pair * 16 < count) *reinterpret_cast<uint4*>(codes + c * stride + pair * 16) = w;
     }
+}
+
+// The largest magnitudes (fp32 bits) of the thread's eight rows over the 16 lanes that have them: lanes 2*i and 2*i + 1 of
+// the 16 return that of row i. Each step hands half of the rows to the lanes that keep them: 8 shuffles.
+__device__ __forceinline__ uint32_t largest_of_rows(const uint32_t (&a)[8]) {
+    const int lane = threadIdx.x;
+    uint32_t b[4], c[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t mine = lane & 8 ? a[4 + i] : a[i], theirs = lane & 8 ? a[i] : a[4 + i];
+        b[i] = max(mine, __shfl_xor_sync(kFull, theirs, 8));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t mine = lane & 4 ? b[2 + i] : b[i], theirs = lane & 4 ? b[i] : b[2 + i];
+        c[i] = max(mine, __shfl_xor_sync(kFull, theirs, 4));
+    }
+    const uint32_t mine = lane & 2 ? c[1] : c[0], theirs = lane & 2 ? c[0] : c[1];
+    const uint32_t d = max(mine, __shfl_xor_sync(kFull, theirs, 2));
+    return max(d, __shfl_xor_sync(kFull, d, 1));
 }
 
 struct QuantizeArgs {
@@ -233,11 +281,11 @@ struct QuantizeArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
-    __shared__ TileSmem sm;
+__global__ void __launch_bounds__(kThreads, kTileCtasPerSm<T>) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
+    __shared__ TileSmem<T> sm;
     __shared__ int32_t starts[TIDE_MAX_EXPERTS + 1];  // row tiles before each expert
     __shared__ int32_t sums[32];
-    const int group = threadIdx.x & 15, row0 = (threadIdx.x >> 4) * 8, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, group = threadIdx.x & 15, row0 = (threadIdx.x >> 4) * 8, warp = threadIdx.x >> 5;
     wait_for_previous_kernel();
     exclusive_sums(starts, a.E, sums, [&](int e) { return (span_of(a.offsets, e, a.M).count + kBlock - 1) / kBlock; });
     const int64_t tiles = int64_t(min(starts[a.E], a.most_blocks)) * a.across;
@@ -246,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
         const uint32_t col0 = uint32_t(it - int64_t(down) * a.across) * kBlock, col = col0 + group * 8;
         const Span span = span_of(a.offsets, e, a.M);
         const int32_t s0 = span.first + (down - starts[e]) * kBlock, held = min(kBlock, span.first + span.count - s0);
-        __syncthreads();  // the tile before has been read
         if (threadIdx.x < kBlock) {
             uint64_t at = 0;
             if (int(threadIdx.x) < held) {
@@ -260,17 +307,19 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
         Eight<T> x[8];
         load_tile(x, sm, col, a.len, a.vector);
         if (a.out.has_rows) {
-            float inverse[8];
+            uint32_t m[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = x[i].largest();
+            const Scale s = scale_of(largest_of_rows(m));
+            const int own = row0 + ((lane & 15) >> 1);
+            if ((lane & 1) == 0 && own < held) a.out.rows.scales[int64_t(s0 + own) * a.out.rows.scale_stride + col0 / kBlock] = s.scale;
+            char* const codes = static_cast<char*>(a.out.rows.codes) + int64_t(s0) * a.out.rows.stride;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                uint32_t largest = x[i].largest();
-#pragma unroll
-                for (int d = 1; d < 16; d <<= 1) largest = max(largest, __shfl_xor_sync(kFull, largest, d));
-                const Scale s = scale_of(largest);
-                inverse[i] = s.inverse;
-                if (group == i && row0 + i < held) a.out.rows.scales[int64_t(s0 + row0 + i) * a.out.rows.scale_stride + col0 / kBlock] = s.scale;
+                Eight<T> y = x[i];
+                y.scale(Eight<T>::factor(__shfl_sync(kFull, s.inverse, (lane & 16) + 2 * i)));
+                put_row(y, i, codes, a.out.rows.stride, held, col, a.len);
             }
-            put_rows(x, inverse, static_cast<char*>(a.out.rows.codes) + int64_t(s0) * a.out.rows.stride, a.out.rows.stride, held, col, a.len);
         }
         if (a.out.has_columns) {
             Eight<T> m;
@@ -278,29 +327,24 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 8; ++i) m.raise(x[i]);
             m.raise(m.other_half());
-            float v[8], inverse[8];
-            m.values(v);
-            if ((threadIdx.x & 16) == 0)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sm.largest[warp][group * 8 + j] = __float_as_uint(v[j]);
+            if (lane < 16) sm.largest[warp][group] = m;
             __syncthreads();
-            uint32_t largest[8] = {};
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const uint4 lo = *reinterpret_cast<const uint4*>(&sm.largest[w][group * 8]), hi = *reinterpret_cast<const uint4*>(&sm.largest[w][group * 8 + 4]);
-                largest[0] = max(largest[0], lo.x), largest[1] = max(largest[1], lo.y), largest[2] = max(largest[2], lo.z), largest[3] = max(largest[3], lo.w);
-                largest[4] = max(largest[4], hi.x), largest[5] = max(largest[5], hi.y), largest[6] = max(largest[6], hi.z), largest[7] = max(largest[7], hi.w);
-            }
             const int64_t block = down;  // of the transposed rows: the experts' tiles lie one after the other
+            if (threadIdx.x < kBlock) {
+                uint32_t bits = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const Scale s = scale_of(largest[j]);
-                inverse[j] = s.inverse;
-                if ((threadIdx.x >> 4) == j && col + j < a.len) a.out.columns.scales[block * a.out.columns.scale_stride + col + j] = s.scale;
+                for (int w = 0; w < kWarps; ++w) bits = max(bits, uint32_t(reinterpret_cast<const typename Eight<T>::Bits*>(sm.largest[w])[threadIdx.x]));
+                const Scale s = scale_of(Eight<T>::magnitude(bits));
+                sm.column[threadIdx.x] = Eight<T>::factor(s.inverse);
+                if (col0 + threadIdx.x < a.len) a.out.columns.scales[block * a.out.columns.scale_stride + col0 + threadIdx.x] = s.scale;
             }
-            put_columns(x, inverse, sm, static_cast<char*>(a.out.columns.codes) + int64_t(col0) * a.out.columns.stride + block * kBlock, a.out.columns.stride,
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i].scale_each(sm.column + group * 8);
+            put_columns(x, sm, static_cast<char*>(a.out.columns.codes) + int64_t(col0) * a.out.columns.stride + block * kBlock, a.out.columns.stride,
                         int(min(uint32_t(kBlock), a.len - col0)), kBlock);
         }
+        __syncthreads();  // what the next tile writes has been read
     }
     let_next_kernel_start();
 }
@@ -317,8 +361,8 @@ struct GatherArgs {
     int vector;
 };
 
-__global__ void __launch_bounds__(kThreads, 3) all_gather_fp8_kernel(const __grid_constant__ GatherArgs a) {
-    __shared__ TileSmem sm;
+__global__ void __launch_bounds__(kThreads, kTileCtasPerSm<__nv_bfloat16>) all_gather_fp8_kernel(const __grid_constant__ GatherArgs a) {
+    __shared__ TileSmem<__nv_bfloat16> sm;
     __shared__ uint32_t of_warp[kWarps];
     const int group = threadIdx.x & 15, warp = threadIdx.x >> 5;
     wait_for_previous_kernel();
@@ -326,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 3) all_gather_fp8_kernel(const __gri
         const uint32_t each = a.across * a.down, e = uint32_t(it / each), in = uint32_t(it - int64_t(e) * each), down = in / a.across, across = in - down * a.across;
         const uint32_t n0 = down * kBlock, col0 = across * kBlock, col = col0 + group * 8;
         const int held = int(min(uint32_t(kBlock), a.tv.rows - n0));
-        __syncthreads();  // the tile before has been read
         if (threadIdx.x < kBlock) {
             uint64_t at = 0;
             if (int(threadIdx.x) < held) {
@@ -348,13 +391,16 @@ __global__ void __launch_bounds__(kThreads, 3) all_gather_fp8_kernel(const __gri
         for (int w = 0; w < kWarps; ++w) largest = max(largest, of_warp[w]);
         const Scale s = scale_of(largest);
         if (threadIdx.x == 0) a.w.scales[int64_t(e) * a.w.scale_batch + int64_t(down) * a.w.scale_stride + across] = s.scale;
-        float inverse[8];
+        char* const codes = static_cast<char*>(a.w.codes) + int64_t(e) * a.w.batch + int64_t(n0) * a.w.stride;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) inverse[j] = s.inverse;
-        put_rows(x, inverse, static_cast<char*>(a.w.codes) + int64_t(e) * a.w.batch + int64_t(n0) * a.w.stride, a.w.stride, held, col, a.tv.len);
+        for (int i = 0; i < 8; ++i) {
+            x[i].scale(Eight<__nv_bfloat16>::factor(s.inverse));
+            put_row(x[i], i, codes, a.w.stride, held, col, a.tv.len);
+        }
         if (a.has_wt)
-            put_columns(x, inverse, sm, static_cast<char*>(a.wt.codes) + int64_t(e) * a.wt.batch + int64_t(col0) * a.wt.stride + n0, a.wt.stride,
-                        int(min(uint32_t(kBlock), a.tv.len - col0)), (held + 15) / 16 * 16);
+            put_columns(x, sm, static_cast<char*>(a.wt.codes) + int64_t(e) * a.wt.batch + int64_t(col0) * a.wt.stride + n0, a.wt.stride, int(min(uint32_t(kBlock), a.tv.len - col0)),
+                        (held + 15) / 16 * 16);
+        __syncthreads();  // what the next tile writes has been read
     }
     let_next_kernel_start();
 }
@@ -396,7 +442,7 @@ cudaError_t launch_quantize(const RowsView& src, int bf16, int64_t src_rows, int
     a.across = uint32_t((len + kBlock - 1) / kBlock);
     a.vector = vectors(reinterpret_cast<uintptr_t>(src.p), src.stride, src_rows, len, bf16 ? 2 : 4);
     const int64_t tiles = padded_blocks(M, E) * a.across;
-    return launch_after(bf16 ? quantize_kernel<__nv_bfloat16> : quantize_kernel<float>, grid_of(tiles, c, 4), kThreads, 0, stream, a);
+    return launch_after(bf16 ? quantize_kernel<__nv_bfloat16> : quantize_kernel<float>, grid_of(tiles, c, bf16 ? kTileCtasPerSm<__nv_bfloat16> : kTileCtasPerSm<float>), kThreads, 0, stream, a);
 }
 
 cudaError_t launch_all_gather_fp8(const ShardPtrs& shards, const TableView& tv, int E, const ExpertParams& ps, const tide_fp8_t& w, const tide_fp8_t* wt, const Ctas& c,
@@ -408,7 +454,7 @@ cudaError_t launch_all_gather_fp8(const ShardPtrs& shards, const TableView& tv, 
     a.tiles = int64_t(E) * a.across * a.down;
     a.vector = vectors(shards.bits, 0, 1, tv.len, 2);
     for (int e = 0; e < E; ++e) a.vector &= ps.off[e] % 8 == 0;
-    return launch_after(all_gather_fp8_kernel, grid_of(a.tiles, c, 4), kThreads, 0, stream, a);
+    return launch_after(all_gather_fp8_kernel, grid_of(a.tiles, c, kTileCtasPerSm<__nv_bfloat16>), kThreads, 0, stream, a);
 }
 
 }  // namespace tide
