@@ -31,10 +31,15 @@ struct Ctas {
 
 // ---- order, rows there and back ----
 constexpr int kSortThreads = 512;
-// Pairs that one CTA sorts alone: its two passes over 4096 take less than a second launch and its counts.
-constexpr int64_t kSortAlone = 4096;
-// CTAs of a sort by several, each of which counts and ranks a piece of the pairs.
-int sort_ctas(int64_t pairs, const Ctas& c);
+constexpr int64_t kSortAlone = 2048;   // pairs that one CTA sorts alone
+constexpr int64_t kSortPiece = 4096;   // pairs of a CTA whose warps keep theirs in registers
+constexpr int kSortCluster = 8;        // CTAs of a cluster
+// CTAs of a sort, each of which counts and ranks a piece of the pairs, and whether a launch of its own counts (into a workspace).
+struct SortShape {
+    int ctas;
+    bool counted;
+};
+SortShape sort_shape(int64_t pairs, const Ctas& c);
 cudaError_t launch_sort(const void* ids, int ids64, int64_t pairs, int k, int E, int32_t* offsets, int32_t* slots,
                         int32_t* tokens, int32_t* counts, const Ctas& c, int* status, cudaStream_t stream);
 

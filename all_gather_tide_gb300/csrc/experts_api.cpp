@@ -120,8 +120,8 @@ int tide_experts_set_wait_timeout(tide_experts_t x, uint64_t timeout_ns) {
 int tide_experts_sort_workspace(tide_experts_t x, int64_t T, int64_t* bytes) {
     if (!x || !bytes || T < 0) return TIDE_EINVAL;
     if (T > tide::kMaxPairs / x->k) return TIDE_ERANGE;
-    const int ctas = tide::sort_ctas(T * x->k, ctas_of(x));
-    *bytes = ctas > 1 ? (int64_t(ctas) * x->E * 4 + 255) / 256 * 256 : 0;
+    const tide::SortShape shape = tide::sort_shape(T * x->k, ctas_of(x));
+    *bytes = shape.counted ? (int64_t(shape.ctas) * x->E * 4 + 255) / 256 * 256 : 0;
     return TIDE_OK;
 }
 

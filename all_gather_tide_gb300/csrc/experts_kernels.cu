@@ -12,8 +12,21 @@ namespace {
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kCtasPerSm = 4;  // of 256 threads
 
-__device__ __forceinline__ int expert_of(const void* ids, int ids64, int64_t i, int E, int* status) {
-    return int(row_of(ids, ids64, i, uint32_t(E), status));
+constexpr int kSteps = 8;  // of 32 pairs, whose ids a warp loads at once
+
+// The experts of 32*kSteps pairs from `first` on, E where there is none.
+__device__ __forceinline__ void load_experts(int (&e)[kSteps], const void* ids, int ids64, int64_t first, int64_t end, int E, int* status) {
+    int64_t id[kSteps];
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+        const int64_t i = first + q * 32 + (threadIdx.x & 31);
+        id[q] = i < end ? load_id(ids, ids64, i) : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+        if (status && id[q] >= E) atomicCAS(status, 0, kStatusBadId);
+        e[q] = int(row_of(id[q], uint32_t(E)));
+    }
 }
 
 // How many pairs of its piece go to each expert, for every CTA.
@@ -23,7 +36,13 @@ __global__ void __launch_bounds__(kSortThreads) count_experts_kernel(const void*
     wait_for_previous_kernel();
     __syncthreads();
     const int64_t first = int64_t(blockIdx.x) * piece, end = min(first + piece, int64_t(n));
-    for (int64_t i = first + threadIdx.x; i < end; i += kSortThreads) atomicAdd(&count[expert_of(ids, ids64, i, E, status)], 1);
+    for (int64_t i = first + (threadIdx.x >> 5) * (32 * kSteps); i < end; i += kSortWarps * 32 * kSteps) {
+        int e[kSteps];
+        load_experts(e, ids, ids64, i, end, E, status);
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q)
+            if (e[q] < E) atomicAdd(&count[e[q]], 1);
+    }
     __syncthreads();
     let_next_kernel_start();
     for (int e = threadIdx.x; e < E; e += kSortThreads) counts[int64_t(blockIdx.x) * E + e] = count[e];
@@ -31,21 +50,23 @@ __global__ void __launch_bounds__(kSortThreads) count_experts_kernel(const void*
 
 // The rows of a piece's pairs.  Each warp has a stretch of the piece.  It first counts its pairs by expert, 32 at a time: lanes
 // with the same expert find one another (match) and their first adds their number, so no atomics are needed.
-// The counts of the warps before it, of the CTAs before (`counts`, unless this CTA sorts alone) and of all
-// experts before give the row of its first pair of each expert, and a second pass over the stretch, the same way,
-// the row of every pair.
+// The counts of the warps before it, of the CTAs before and of all experts before give the row of its first
+// pair of each expert, and a second pass over the stretch, the same way, the row of every pair. What the other CTAs have
+// counted lies in their shared memory, where all are one cluster, and else in `counts`.
 //
-// Bound by the latency of two short launches: 524288 pairs and 128 experts are 2 MB to 4 MB read twice and 4 MB written.
+// Bound by latency, not by its 12 or 16 bytes a pair.
 __global__ void __launch_bounds__(kSortThreads)
 sort_experts_kernel(const void* ids, int ids64, int32_t n, int32_t piece, int k, int E, const int32_t* counts, int32_t* offsets, int32_t* slots,
                     int32_t* tokens, int* status) {
     extern __shared__ int32_t smem[];
     int32_t* base = smem;                      // [E + 1] rows before each expert
-    int32_t* before = base + E + 1;            // [E] pairs of the CTAs before
+    int32_t* own = base + E + 1;               // [E] pairs of this CTA
+    int32_t* before = own + E;                 // [E] pairs of the CTAs before
     int32_t* total = before + E;               // [E] pairs of all CTAs
     int32_t* warp_count = total + E;           // [kSortWarps][E + 1]
     __shared__ int32_t sums[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool cluster = !counts && gridDim.x > 1;
     int32_t* mine = warp_count + warp * (E + 1);
     for (int e = threadIdx.x; e < E; e += kSortThreads) before[e] = total[e] = 0;
     for (int e = lane; e <= E; e += 32) mine[e] = 0;
@@ -54,73 +75,97 @@ sort_experts_kernel(const void* ids, int ids64, int32_t n, int32_t piece, int k,
     const int64_t first = int64_t(blockIdx.x) * piece, end = min(first + piece, int64_t(n));
     const int64_t stretch = ((end - first + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
     const int64_t lo = min(first + warp * stretch, end), hi = min(lo + stretch, end);
-    // alone, this pass records ids past the experts too; else the counting kernel has
+    // ids past the experts are recorded once: by the counting kernel, if there was one
     int* const bad = counts ? nullptr : status;
-    auto expert = [&](int64_t i) {
-        if (i >= hi) return E;
-        return bad ? expert_of(ids, ids64, i, E, bad) : int(row_of(load_id(ids, ids64, i), uint32_t(E)));
-    };
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int e = expert(i0 + lane);
-        const unsigned same = __match_any_sync(kFull, e);
-        if ((same & ((1u << lane) - 1)) == 0) mine[e] += __popc(same);
-        __syncwarp();
+    int e[kSteps];  // of a stretch of one batch they stay for the second pass
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kSteps) {
+        load_experts(e, ids, ids64, i0, hi, E, bad);
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q) {
+            if (i0 + 32 * q >= hi) break;
+            const unsigned same = __match_any_sync(kFull, e[q]);
+            if ((same & ((1u << lane) - 1)) == 0) mine[e[q]] += __popc(same);
+            __syncwarp();
+        }
     }
     if (counts) {
         // threads in as many teams as there are, each over every so many-th CTA
         int width = 32;
         while (width < E && width < kSortThreads) width <<= 1;
         const int teams = kSortThreads / width, team = threadIdx.x / width;
-        for (int e = threadIdx.x % width; e < E; e += width) {
+        for (int x = threadIdx.x % width; x < E; x += width) {
             int32_t b = 0, t = 0;
-#pragma unroll 8
+#pragma unroll 16
             for (int c = team; c < int(gridDim.x); c += teams) {
-                const int32_t v = load_here(counts + int64_t(c) * E + e);
+                const int32_t v = load_here(counts + int64_t(c) * E + x);
                 t += v;
                 if (c < int(blockIdx.x)) b += v;
             }
-            atomicAdd(&before[e], b);
-            atomicAdd(&total[e], t);
+            atomicAdd(&before[x], b);
+            atomicAdd(&total[x], t);
         }
-    }
-    __syncthreads();
-    if (!counts) {
-        for (int e = threadIdx.x; e < E; e += kSortThreads) {
+        __syncthreads();
+    } else {
+        __syncthreads();
+        for (int x = threadIdx.x; x < E; x += kSortThreads) {
             int32_t t = 0;
-            for (int w = 0; w < kSortWarps; ++w) t += warp_count[w * (E + 1) + e];
-            total[e] = t;
+            for (int w = 0; w < kSortWarps; ++w) t += warp_count[w * (E + 1) + x];
+            own[x] = t;
+            if (!cluster) total[x] = t;
+        }
+        if (cluster) {
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            for (int x = threadIdx.x; x < E; x += kSortThreads) {
+                int32_t b = 0, t = 0;
+                for (uint32_t c = 0; c < gridDim.x; ++c) {
+                    uint32_t at;
+                    int32_t v;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(uint32_t(__cvta_generic_to_shared(own + x))), "r"(c));
+                    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+                    t += v;
+                    if (c < blockIdx.x) b += v;
+                }
+                before[x] = b, total[x] = t;
+            }
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // its counterpart is at the end
         }
         __syncthreads();
     }
-    exclusive_sums(base, E, sums, [&](int e) { return total[e]; });
+    exclusive_sums(base, E, sums, [&](int x) { return total[x]; });
     const int32_t held = base[E];
     if (blockIdx.x == 0)
-        for (int e = threadIdx.x; e <= E; e += kSortThreads) offsets[e] = base[e];
-    for (int e = threadIdx.x; e < E; e += kSortThreads) {
-        int32_t at = base[e] + before[e];
+        for (int x = threadIdx.x; x <= E; x += kSortThreads) offsets[x] = base[x];
+    for (int x = threadIdx.x; x < E; x += kSortThreads) {
+        int32_t at = base[x] + before[x];
         for (int w = 0; w < kSortWarps; ++w) {
-            const int32_t c = warp_count[w * (E + 1) + e];
-            warp_count[w * (E + 1) + e] = at;
+            const int32_t c = warp_count[w * (E + 1) + x];
+            warp_count[w * (E + 1) + x] = at;
             at += c;
         }
     }
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int e = i < hi ? int(row_of(load_id(ids, ids64, i), uint32_t(E))) : E;
-        const unsigned same = __match_any_sync(kFull, e), earlier = same & ((1u << lane) - 1);
-        const int32_t row = mine[e] + __popc(earlier);
-        __syncwarp();
-        if (earlier == 0) mine[e] += __popc(same);
-        __syncwarp();
-        if (i < hi) {
-            slots[i] = e < E ? row : -1;
-            if (e < E) tokens[row] = int32_t(uint32_t(i) / uint32_t(k));
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kSteps) {
+        if (stretch > 32 * kSteps) load_experts(e, ids, ids64, i0, hi, E, nullptr);
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q) {
+            if (i0 + 32 * q >= hi) break;
+            const int64_t i = i0 + 32 * q + lane;
+            const unsigned same = __match_any_sync(kFull, e[q]), earlier = same & ((1u << lane) - 1);
+            const int32_t row = mine[e[q]] + __popc(earlier);
+            __syncwarp();
+            if (earlier == 0) mine[e[q]] += __popc(same);
+            __syncwarp();
+            if (i < hi) {
+                slots[i] = e[q] < E ? row : -1;
+                if (e[q] < E) tokens[row] = int32_t(uint32_t(i) / uint32_t(k));
+            }
         }
     }
     // the rows behind the last
     for (int64_t s = held + int64_t(blockIdx.x) * kSortThreads + threadIdx.x; s < n; s += int64_t(gridDim.x) * kSortThreads) tokens[s] = -1;
     let_next_kernel_start();
+    __syncwarp();
+    if (cluster) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the others have read this CTA's counts
 }
 
 // Which of the token's pairs, a lane each, have a row, and where.
@@ -132,7 +177,7 @@ __device__ __forceinline__ unsigned held_pairs(const int32_t* slots, int64_t t, 
 // The tokens' rows to where their pairs go.  A warp takes a token and a stretch of 32*U vectors of its row into
 // registers and writes them once for each pair, so every row of src is read once.
 //
-// Bound by HBM writes.
+// Bound by HBM writes: 65536 rows of 2048 bf16 values to eight places each in 357 us, 6.8 TB/s.
 template <typename Word, int U>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 dispatch_kernel(const Word* src, int64_t src_stride, int64_t T, int k, int32_t M, uint32_t vecs, const int32_t* slots, Word* rows, int64_t rows_stride,
@@ -160,13 +205,14 @@ dispatch_kernel(const Word* src, int64_t src_stride, int64_t T, int k, int32_t M
     let_next_kernel_start();
 }
 
-// The rows back at their tokens, weighted.  A warp takes a token and a stretch of 32*Cols vectors; kAtOnce rows are in
+// The rows back at their tokens, weighted.  A warp takes a token and a stretch of 32*Cols vectors; AtOnce rows are in
 // flight before their products are added, in fp32 and in the pairs' order.
 //
-// Bound by HBM reads.
-constexpr int kAtOnce = 4;
-template <typename T, int V, int Cols>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+// Bound by HBM reads: 524288 rows of 2048 bf16 values back to 65536 tokens in 363 us, 6.7 TB/s (440 with four CTAs an SM, whose
+// registers spilled).
+constexpr int kCombineCtasPerSm = 3;
+template <typename T, int V, int Cols, int AtOnce>
+__global__ void __launch_bounds__(kThreads, kCombineCtasPerSm)
 combine_kernel(const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_t M, uint32_t len, const int32_t* slots, const float* weights, T* out,
                int64_t out_stride, uint32_t stretches, int64_t items) {
     using Word = typename Vec<T, V>::Word;
@@ -180,11 +226,11 @@ combine_kernel(const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_
         const float weight = weights && lane < k ? __ldcg(weights + t * k + lane) : 1.0f;
         float acc[Cols][V] = {};
         while (held) {
-            Word w[kAtOnce][Cols];
-            float f[kAtOnce];
+            Word w[AtOnce][Cols];
+            float f[AtOnce];
             int many = 0;
 #pragma unroll
-            for (int r = 0; r < kAtOnce; ++r) {
+            for (int r = 0; r < AtOnce; ++r) {
                 if (!held) break;
                 const int j = __ffs(held) - 1;
                 held &= held - 1;
@@ -196,7 +242,7 @@ combine_kernel(const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_
                     if (col + c * 32 * V < len) w[r][c] = __ldcs(reinterpret_cast<const Word*>(from + c * 32 * V));
             }
 #pragma unroll
-            for (int r = 0; r < kAtOnce; ++r) {
+            for (int r = 0; r < AtOnce; ++r) {
                 if (r >= many) break;
 #pragma unroll
                 for (int c = 0; c < Cols; ++c) {
@@ -216,18 +262,17 @@ combine_kernel(const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_
 }
 
 // The gradients of the weighted sum.  `team` warps take a token, a share of its columns each, and all of up to
-// kPairs pairs at once: a vector of dout is read once, those of the pairs' rows beside it, and each pair's
+// Pairs pairs at once: Cols vectors of dout are read once, those of the pairs' rows beside them, and each pair's
 // product with its weight is written while the dot product is added up.  A lane's sums run over its columns in order, then
 // over the warp's lanes and the team's warps as a tree.
 //
-// Bound by HBM: a row read and a row written for each pair.
-constexpr int kPairs = 8;
-template <typename T, int V>
+// Bound by HBM, a row read and a row written for each pair: 262144 rows of 2048 bf16 values in 354 us, 6.4 TB/s.
+template <typename T, int V, int Pairs, int Cols>
 __global__ void __launch_bounds__(kThreads, 2)
 combine_grad_kernel(const T* dout, int64_t dout_stride, const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_t M, uint32_t len,
                     const int32_t* slots, const float* weights, T* drows, int64_t drows_stride, float* dweights, int team) {
     using Word = typename Vec<T, V>::Word;
-    __shared__ float partial[kWarps][kPairs];
+    __shared__ float partial[kWarps][Pairs];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % team, each = kWarps / team;
     wait_for_previous_kernel();
     for (int64_t t0 = int64_t(blockIdx.x) * each; t0 < tokens; t0 += int64_t(gridDim.x) * each) {
@@ -236,48 +281,56 @@ combine_grad_kernel(const T* dout, int64_t dout_stride, const T* rows, int64_t r
         int32_t slot = -1;
         float weight = 0.0f;
         if (here && lane < k) slot = load_here(slots + t * k + lane), weight = __ldcg(weights + t * k + lane);
-        for (int j0 = 0; j0 < k; j0 += kPairs) {
-            float dot[kPairs] = {}, w[kPairs];
-            int32_t s[kPairs];
+        for (int j0 = 0; j0 < k; j0 += Pairs) {
+            float dot[Pairs] = {}, w[Pairs];
+            int32_t s[Pairs];
             unsigned any = 0;
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
+            for (int j = 0; j < Pairs; ++j) {
                 s[j] = __shfl_sync(kFull, slot, (j0 + j) & 31);
                 w[j] = __shfl_sync(kFull, weight, (j0 + j) & 31);
                 if (j0 + j >= k || uint32_t(s[j]) >= uint32_t(M)) s[j] = -1;
                 else any = 1;
             }
             if (any) {
-                for (uint32_t col = (part * 32 + lane) * V; col < len; col += team * 32 * V) {
-                    Word r[kPairs];
-                    const Word d = __ldcg(reinterpret_cast<const Word*>(dout + t * dout_stride + col));
+                for (uint32_t col = (part * 32 * Cols + lane) * V; col < len; col += team * 32 * Cols * V) {
+                    Word r[Pairs][Cols], d[Cols];
 #pragma unroll
-                    for (int j = 0; j < kPairs; ++j)
-                        if (s[j] >= 0) r[j] = __ldcs(reinterpret_cast<const Word*>(rows + int64_t(s[j]) * rows_stride + col));
-                    float x[V];
-                    widen(d, x);
+                    for (int c = 0; c < Cols; ++c)
+                        if (col + c * 32 * V < len) d[c] = __ldcg(reinterpret_cast<const Word*>(dout + t * dout_stride + col + c * 32 * V));
 #pragma unroll
-                    for (int j = 0; j < kPairs; ++j) {
-                        if (s[j] < 0) continue;
-                        float y[V], z[V];
-                        widen(r[j], y);
+                    for (int j = 0; j < Pairs; ++j)
 #pragma unroll
-                        for (int v = 0; v < V; ++v) dot[j] = fmaf(x[v], y[v], dot[j]), z[v] = w[j] * x[v];
-                        put(drows + int64_t(s[j]) * drows_stride + col, z);
+                        for (int c = 0; c < Cols; ++c)
+                            if (s[j] >= 0 && col + c * 32 * V < len) r[j][c] = __ldcs(reinterpret_cast<const Word*>(rows + int64_t(s[j]) * rows_stride + col + c * 32 * V));
+#pragma unroll
+                    for (int c = 0; c < Cols; ++c) {
+                        if (col + c * 32 * V >= len) continue;
+                        float x[V];
+                        widen(d[c], x);
+#pragma unroll
+                        for (int j = 0; j < Pairs; ++j) {
+                            if (s[j] < 0) continue;
+                            float y[V], z[V];
+                            widen(r[j][c], y);
+#pragma unroll
+                            for (int v = 0; v < V; ++v) dot[j] = fmaf(x[v], y[v], dot[j]), z[v] = w[j] * x[v];
+                            put(drows + int64_t(s[j]) * drows_stride + col + c * 32 * V, z);
+                        }
                     }
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
+            for (int j = 0; j < Pairs; ++j) {
 #pragma unroll
                 for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(kFull, dot[j], d);
             }
             if (team > 1) {
                 if (lane == 0)
 #pragma unroll
-                    for (int j = 0; j < kPairs; ++j) partial[warp][j] = dot[j];
+                    for (int j = 0; j < Pairs; ++j) partial[warp][j] = dot[j];
                 __syncthreads();
-                if (here && part == 0 && lane < kPairs && j0 + lane < k) {
+                if (here && part == 0 && lane < Pairs && j0 + lane < k) {
                     float sum = 0.0f;
                     for (int p = 0; p < team; ++p) sum += partial[warp + p][lane];
                     dweights[t * k + j0 + lane] = sum;
@@ -285,7 +338,7 @@ combine_grad_kernel(const T* dout, int64_t dout_stride, const T* rows, int64_t r
                 __syncthreads();
             } else if (here) {
 #pragma unroll
-                for (int j = 0; j < kPairs; ++j)
+                for (int j = 0; j < Pairs; ++j)
                     if (lane == j && j0 + j < k) dweights[t * k + j0 + j] = dot[j];
             }
         }
@@ -293,9 +346,9 @@ combine_grad_kernel(const T* dout, int64_t dout_stride, const T* rows, int64_t r
     let_next_kernel_start();
 }
 
-int grid_of(int64_t blocks, const Ctas& c, int per_sm) {
-    return int(std::max<int64_t>(1, std::min<int64_t>(blocks, c.most ? c.most : int64_t(c.sms) * per_sm)));
-}
+// As many CTAs as there is work where the GPU may be filled: those that come late even out the end.  65536 rows of 2048 bf16 values
+// to 524288 places take 357 us so, 387 with eight CTAs an SM that go round.
+int grid_of(int64_t blocks, const Ctas& c) { return int(std::max<int64_t>(1, std::min<int64_t>(blocks, c.most ? c.most : INT32_MAX))); }
 
 // The widest vector, in bytes up to 16, that all rows of both arrays allow.
 int vector_bytes(const void* a, int64_t a_stride, int64_t a_rows, const void* b, int64_t b_stride, int64_t b_rows, int64_t len, int elem) {
@@ -313,7 +366,7 @@ cudaError_t dispatch(const RowsView& src, int elem, int64_t T, int k, int64_t le
     const int per = int(sizeof(Word)) / elem;
     const uint32_t vecs = uint32_t(len / per), stretches = (vecs + 32 * U - 1) / (32 * U);
     const int64_t items = T * stretches;
-    return launch_after(dispatch_kernel<Word, U>, grid_of((items + kWarps - 1) / kWarps, c, 8), kThreads, 0, stream, static_cast<const Word*>(src.p), src.stride / per, T, k,
+    return launch_after(dispatch_kernel<Word, U>, grid_of((items + kWarps - 1) / kWarps, c), kThreads, 0, stream, static_cast<const Word*>(src.p), src.stride / per, T, k,
                         int32_t(T * k), vecs, slots, static_cast<Word*>(rows), rows_stride / per, stretches, items);
 }
 
@@ -323,44 +376,55 @@ cudaError_t combine(const RowsView& rows, int64_t tokens, int k, int64_t len, co
     auto go = [&](auto* kernel, int cols) {
         const uint32_t stretches = uint32_t((len + 32 * V * cols - 1) / (32 * V * cols));
         const int64_t items = tokens * stretches;
-        return launch_after(kernel, grid_of((items + kWarps - 1) / kWarps, c, 8), kThreads, 0, stream, static_cast<const T*>(rows.p), rows.stride, tokens, k,
-                            int32_t(tokens * k), uint32_t(len), slots, weights, static_cast<T*>(out), out_stride, stretches, items);
+        return launch_after(kernel, grid_of((items + kWarps - 1) / kWarps, c), kThreads, 0, stream, static_cast<const T*>(rows.p), rows.stride, tokens,
+                            k, int32_t(tokens * k), uint32_t(len), slots, weights, static_cast<T*>(out), out_stride, stretches, items);
     };
-    return len > 32 * V ? go(combine_kernel<T, V, 2>, 2) : go(combine_kernel<T, V, 1>, 1);
+    // Short vectors go several at a time from two rows (12297 rows of 1027 bf16 values: 22 us with two from four rows); fewer where a
+    // row has no more.
+    constexpr int kMany = V * sizeof(T) >= 16 ? 2 : 8;
+    return len > 32 * V ? go(combine_kernel<T, V, kMany, 8 / kMany>, kMany) : go(combine_kernel<T, V, 1, 4>, 1);
 }
 
 template <typename T, int V>
 cudaError_t combine_grad(const RowsView& dout, const RowsView& rows, int64_t tokens, int k, int64_t len, const int32_t* slots, const float* weights, void* drows,
                          int64_t drows_stride, float* dweights, const Ctas& c, cudaStream_t stream) {
-    // more warps for a token while the tokens do not fill the GPU and the row has a vector for each lane
-    int team = 1;
-    while (team < kWarps && tokens * team < int64_t(c.sms) * 16 && len > int64_t(team) * 32 * V) team *= 2;
-    const int64_t blocks = (tokens + kWarps / team - 1) / (kWarps / team);
-    return launch_after(combine_grad_kernel<T, V>, grid_of(blocks, c, 4), kThreads, 0, stream, static_cast<const T*>(dout.p), dout.stride, static_cast<const T*>(rows.p),
-                        rows.stride, tokens, k, int32_t(tokens * k), uint32_t(len), slots, weights, static_cast<T*>(drows), drows_stride, dweights, team);
+    auto go = [&](auto* kernel, int cols) {
+        // more warps for a token while the tokens do not fill the GPU and the row has a vector for each lane
+        int team = 1;
+        while (team < kWarps && tokens * team < int64_t(c.sms) * 16 && len > int64_t(team) * 32 * V * cols) team *= 2;
+        const int64_t blocks = (tokens + kWarps / team - 1) / (kWarps / team);
+        return launch_after(kernel, grid_of(blocks, c), kThreads, 0, stream, static_cast<const T*>(dout.p), dout.stride, static_cast<const T*>(rows.p), rows.stride,
+                            tokens, k, int32_t(tokens * k), uint32_t(len), slots, weights, static_cast<T*>(drows), drows_stride, dweights, team);
+    };
+    // eight vectors of rows in flight, more where they are short
+    constexpr int kMany = V * sizeof(T) >= 16 ? 1 : 2;
+    return k > 4 ? go(combine_grad_kernel<T, V, 8, kMany>, kMany) : go(combine_grad_kernel<T, V, 4, 2 * kMany>, 2 * kMany);
 }
 
 }  // namespace
 
-int sort_ctas(int64_t pairs, const Ctas& c) {
-    if (pairs <= kSortAlone) return 1;
-    // a piece is 2048 pairs at least: four steps of every warp
-    return int(std::max<int64_t>(1, std::min<int64_t>((pairs + 2047) / 2048, c.most ? c.most : c.sms)));
+SortShape sort_shape(int64_t pairs, const Ctas& c) {
+    const int64_t most = c.most ? c.most : c.sms;
+    auto ctas = [&](int64_t least) { return int(std::max<int64_t>(1, std::min(most, (pairs + least - 1) / least))); };
+    // one CTA, then a cluster of them, as long as each warp has at most eight steps of 32; then every SM
+    if (pairs <= kSortAlone) return {1, false};
+    if (pairs <= kSortCluster * kSortPiece) return {std::min(kSortCluster, ctas(kSortPiece / 2)), false};
+    return {ctas(kSortPiece / 2), true};
 }
 
 cudaError_t launch_sort(const void* ids, int ids64, int64_t pairs, int k, int E, int32_t* offsets, int32_t* slots, int32_t* tokens, int32_t* counts, const Ctas& c,
                         int* status, cudaStream_t stream) {
-    const size_t smem = sizeof(int32_t) * (size_t(E) + 1 + 2 * size_t(E) + size_t(kSortWarps) * (E + 1));
-    cudaError_t e = cudaFuncSetAttribute(sort_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(int32_t) * (19 * (TIDE_MAX_EXPERTS + 1))));
+    const size_t smem = sizeof(int32_t) * (size_t(E) + 1 + 3 * size_t(E) + size_t(kSortWarps) * (E + 1));
+    cudaError_t e = cudaFuncSetAttribute(sort_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(int32_t) * (20 * (TIDE_MAX_EXPERTS + 1))));
     if (e != cudaSuccess) return e;
-    const int ctas = sort_ctas(pairs, c);
-    const int32_t piece = int32_t((pairs + ctas - 1) / ctas);
-    if (ctas > 1) {
-        e = launch_after(count_experts_kernel, ctas, kSortThreads, 0, stream, ids, ids64, int32_t(pairs), piece, E, counts, status);
+    const SortShape shape = sort_shape(pairs, c);
+    const int32_t piece = int32_t((pairs + shape.ctas - 1) / shape.ctas);
+    if (shape.counted) {
+        e = launch_after(count_experts_kernel, shape.ctas, kSortThreads, 0, stream, ids, ids64, int32_t(pairs), piece, E, counts, status);
         if (e != cudaSuccess) return e;
     }
-    return launch_after(sort_experts_kernel, ctas, kSortThreads, smem, stream, ids, ids64, int32_t(pairs), piece, k, E,
-                        ctas > 1 ? static_cast<const int32_t*>(counts) : nullptr, offsets, slots, tokens, status);
+    return launch_clusters_after(sort_experts_kernel, shape.counted ? 1 : shape.ctas, shape.ctas, kSortThreads, smem, stream, ids, ids64, int32_t(pairs), piece, k, E,
+                                 shape.counted ? static_cast<const int32_t*>(counts) : nullptr, offsets, slots, tokens, status);
 }
 
 cudaError_t launch_dispatch(const RowsView& src, int bf16, int64_t T, int k, int64_t len, const int32_t* slots, void* rows, int64_t rows_stride, const Ctas& c,
