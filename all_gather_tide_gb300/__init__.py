@@ -1035,6 +1035,8 @@ class Route:
         self.tokens = torch.full((self.M,), -1, dtype=torch.int32, device="cuda")
         size = tide_experts_sort_workspace(experts.handle, T)
         self.workspace = torch.empty(size, dtype=torch.uint8, device="cuda") if size else None
+        # addresses, once: the buffers stay these
+        self._at = self.offsets.data_ptr(), self.slots.data_ptr(), self.tokens.data_ptr(), _address(self.workspace), size
 
 
 class Experts:
@@ -1043,6 +1045,7 @@ class Experts:
     def __init__(self, E: int, k: int, flags: int = 0):
         self.E, self.k = E, k
         self._table = ctypes.c_void_p * E  # the type of a pointer_table of E gradients
+        self._lib = lib()
         self.handle = None
         self.handle = tide_experts_create(E, k, flags)
 
@@ -1081,45 +1084,47 @@ class Experts:
         self._check_route(where, route)
         if not (ids.is_cuda and ids.is_contiguous() and ids.numel() == route.M) or (_gpus != 1 and _elsewhere(ids)):
             _refuse(where, f"{route.M} contiguous ids on the GPU are needed")
-        tide_experts_sort(self.handle, ids, route.T, route.offsets, route.slots, route.tokens, route.workspace, stream)
+        _check(self._lib.tide_experts_sort(self.handle, ids.data_ptr(), _dtype_code(ids), route.T, *route._at, _stream(stream)), where)
 
     def dispatch(self, x, route: Route, rows, stream=None) -> None:
         """The tokens' rows ``x`` ([T, D], bf16 or fp32) into ``rows`` ([T*k, D]) in the experts' order."""
         where = "dispatch"
         self._check_route(where, route)
-        self._check_rows(where, x, route.T, x.shape[-1])
-        self._check_rows(where, rows, route.M, x.shape[-1], x.dtype)
-        tide_experts_dispatch(self.handle, x, route.slots, rows, stream)
+        D, kind = x.shape[-1], _dtype_code(x)
+        stride, to = self._check_rows(where, x, route.T, D, kind), self._check_rows(where, rows, route.M, D, kind)
+        _check(self._lib.tide_experts_dispatch(self.handle, x.data_ptr(), kind, stride, route.T, D, route._at[1], rows.data_ptr(), to, _stream(stream)), where)
 
     def dispatch_fp8(self, x, route: Route, rows: Fp8Rows, stream=None) -> None:
         """The same into 8-bit ``rows``."""
         where = "dispatch_fp8"
         self._check_route(where, route)
-        self._check_rows(where, x, route.T, x.shape[-1])
-        self._check_fp8(where, rows, Fp8Rows, route.M, x.shape[-1])
-        tide_experts_dispatch_fp8(self.handle, x, route.slots, rows, stream)
+        D, kind = x.shape[-1], _dtype_code(x)
+        stride = self._check_rows(where, x, route.T, D, kind)
+        self._check_fp8(where, rows, Fp8Rows, route.M, D)
+        _check(self._lib.tide_experts_dispatch_fp8(self.handle, x.data_ptr(), kind, stride, route.T, D, route._at[1], rows.c, _stream(stream)), where)
 
     def combine(self, rows, route: Route, out, weights=None, stream=None) -> None:
         """The experts' ``rows`` ([T*k, D]) back at their tokens, ``out`` ([T, D]), summed with ``weights`` ([T, k] fp32; None: 1, the
         gradient of ``dispatch``)."""
         where = "combine"
         self._check_route(where, route)
-        self._check_rows(where, rows, route.M, rows.shape[-1])
-        self._check_rows(where, out, route.T, rows.shape[-1], rows.dtype)
+        D, kind = rows.shape[-1], _dtype_code(rows)
+        stride, to = self._check_rows(where, rows, route.M, D, kind), self._check_rows(where, out, route.T, D, kind)
         if weights is not None:
             self._check_weights(where, weights, route)
-        tide_experts_combine(self.handle, rows, route.slots, weights, out, stream)
+        _check(self._lib.tide_experts_combine(self.handle, rows.data_ptr(), kind, stride, route.T, D, route._at[1], _address(weights), out.data_ptr(), to,
+                                              _stream(stream)), where)
 
     def combine_grad(self, dout, rows, route: Route, weights, drows, dweights, stream=None) -> None:
         """The gradients of ``combine`` with ``weights``, into ``drows`` and ``dweights``."""
         where = "combine_grad"
         self._check_route(where, route)
-        self._check_rows(where, dout, route.T, dout.shape[-1])
-        for x in (rows, drows):
-            self._check_rows(where, x, route.M, dout.shape[-1], dout.dtype)
-        for x in (weights, dweights):
-            self._check_weights(where, x, route)
-        tide_experts_combine_grad(self.handle, dout, rows, route.slots, weights, drows, dweights, stream)
+        D, kind = dout.shape[-1], _dtype_code(dout)
+        stride, of, to = (self._check_rows(where, x, n, D, kind) for x, n in ((dout, route.T), (rows, route.M), (drows, route.M)))
+        self._check_weights(where, weights, route)
+        self._check_weights(where, dweights, route)
+        _check(self._lib.tide_experts_combine_grad(self.handle, dout.data_ptr(), kind, stride, rows.data_ptr(), of, route.T, D, route._at[1], weights.data_ptr(),
+                                                   drows.data_ptr(), to, dweights.data_ptr(), _stream(stream)), where)
 
     # ---- products in 8 bits ----
 
@@ -1128,15 +1133,18 @@ class Experts:
         """Rows in the experts' order in 8 bits: ``x`` ([T*k, D]), or with ``gather`` the tokens' rows ``x`` ([T, D]), as they are
         and/or transposed.  ``route`` may be None where one expert has all rows."""
         where = "quantize"
-        M = self._check_all_rows(where, route, x.shape[0])
+        n, D = x.shape
+        M, offsets = self._all_rows(where, route, n)
         if gather and route is None:
             _refuse(where, "gathering needs a route")
-        self._check_rows(where, x, route.T if gather else M, x.shape[-1])
+        kind = _dtype_code(x)
+        stride = self._check_rows(where, x, route.T if gather else M, D, kind)
         if rows is not None:
-            self._check_fp8(where, rows, Fp8Rows, M, x.shape[-1])
+            self._check_fp8(where, rows, Fp8Rows, M, D)
         if columns is not None:
-            self._check_fp8(where, columns, Fp8Columns, M, x.shape[-1])
-        tide_experts_quantize(self.handle, x, M, None if route is None else route.offsets, route.tokens if gather else None, rows, columns, stream)
+            self._check_fp8(where, columns, Fp8Columns, M, D)
+        _check(self._lib.tide_experts_quantize(self.handle, x.data_ptr(), kind, stride, n, M, D, offsets, route._at[2] if gather else None,
+                                               None if rows is None else rows.c, None if columns is None else columns.c, _stream(stream)), where)
 
     def matmul(self, a: Fp8Rows, w: Fp8Weights, route: Optional[Route], out, transposed: bool = False, any_scales: bool = False, stream=None) -> None:
         """Every expert's rows of ``a`` times its matrix of ``w``: ``out[s] = w[e] @ a[s]`` ([T*k, N], bf16 or fp32), or with ``transposed``
@@ -1144,37 +1152,41 @@ class Experts:
         where = "matmul"
         if not isinstance(w, Fp8Weights) or w.E != self.E or (transposed and w.c_transposed is None) or (_gpus != 1 and _elsewhere(w.codes)):
             _refuse(where, f"the Fp8Weights of {self.E} experts on this GPU are needed, with transposed codes for a transposed product")
-        N, K = (w.K, w.N) if transposed else (w.N, w.K)
-        M = self._check_all_rows(where, route, a.M)
+        N, K, codes = (w.K, w.N, w.c_transposed) if transposed else (w.N, w.K, w.c)
+        M, offsets = self._all_rows(where, route, a.M if isinstance(a, Fp8Rows) else 0)
         self._check_fp8(where, a, Fp8Rows, M, K)
-        self._check_rows(where, out, M, N)
-        tide_experts_matmul(self.handle, a, None if route is None else route.offsets, w, out, (TIDE_FP8_TRANSPOSED if transposed else 0) | (TIDE_FP8_ANY_SCALES if any_scales else 0),
-                            stream)
+        kind = _dtype_code(out)
+        to = self._check_rows(where, out, M, N, kind)
+        flags = (TIDE_FP8_TRANSPOSED if transposed else 0) | (TIDE_FP8_ANY_SCALES if any_scales else 0)
+        _check(self._lib.tide_experts_matmul(self.handle, a.c, M, offsets, codes, flags, N, K, out.data_ptr(), kind, to, _stream(stream)), where)
 
     def weight_grad(self, dy: Fp8Columns, a: Fp8Columns, route: Optional[Route], grads, grad_type: int = TIDE_BF16, any_scales: bool = False, stream=None) -> None:
         """The gradient of every expert's matrix, ``dy[e].T @ a[e]``, into ``grads``: E contiguous tensors of N*K elements, bf16 or
         fp32, one tensor [E, N, K], or the ``pointer_table`` of E tensors of ``grad_type``.  ``any_scales`` as ``matmul``'s."""
         where = "weight_grad"
-        M = self._check_all_rows(where, route, dy.M)
-        self._check_fp8(where, dy, Fp8Columns, M, dy.len)
-        self._check_fp8(where, a, Fp8Columns, M, a.len)
+        M, offsets = self._all_rows(where, route, dy.M if isinstance(dy, Fp8Columns) else 0)
+        for x in (dy, a):
+            self._check_fp8(where, x, Fp8Columns, M, x.len if isinstance(x, Fp8Columns) else 0)
+        n = dy.len * a.len
         if type(grads) is not self._table:
-            if isinstance(grads, ctypes.Array) or len(grads) != self.E:
-                _refuse(where, f"{self.E} gradients are needed")
-            grad_type = _dtype_code(grads[0])
-            if grad_type not in (TIDE_F32, TIDE_BF16):
-                _refuse(where, "gradients are bf16 or fp32")
             if isinstance(grads, (list, tuple)):
+                if len(grads) != self.E:
+                    _refuse(where, f"{self.E} gradients are needed")
+                grad_type = _dtype_code(grads[0])
                 for g in grads:
-                    if not (g.is_cuda and g.dtype is grads[0].dtype and g.is_contiguous() and g.numel() == dy.len * a.len) or (_gpus != 1 and _elsewhere(g)):
+                    if not (g.is_cuda and g.dtype is grads[0].dtype and g.is_contiguous() and g.numel() == n) or (_gpus != 1 and _elsewhere(g)):
                         _refuse(where, f"contiguous gradients of {dy.len} x {a.len} elements of one type on the GPU are needed")
                 grads = _ptr_array(grads)
             else:
-                if not (grads.is_cuda and grads.is_contiguous() and grads.numel() == self.E * dy.len * a.len) or (_gpus != 1 and _elsewhere(grads)):
+                if isinstance(grads, ctypes.Array) or not (grads.is_cuda and grads.is_contiguous() and grads.numel() == self.E * n) or (_gpus != 1 and _elsewhere(grads)):
                     _refuse(where, f"a contiguous gradient of {self.E} x {dy.len} x {a.len} elements on the GPU is needed")
-                first, each = grads.data_ptr(), dy.len * a.len * grads.element_size()
+                grad_type = _dtype_code(grads)
+                first, each = grads.data_ptr(), n * grads.element_size()
                 grads = self._table(*range(first, first + self.E * each, each))
-        tide_experts_weight_grad(self.handle, dy, a, None if route is None else route.offsets, grads, grad_type, TIDE_FP8_ANY_SCALES if any_scales else 0, stream)
+            if grad_type not in (TIDE_F32, TIDE_BF16):
+                _refuse(where, "gradients are bf16 or fp32")
+        _check(self._lib.tide_experts_weight_grad(self.handle, dy.c, a.c, M, offsets, TIDE_FP8_ANY_SCALES if any_scales else 0, dy.len, a.len, grads, grad_type,
+                                                  _stream(stream)), where)
 
     # ---- checks ----
 
@@ -1182,24 +1194,29 @@ class Experts:
         if not isinstance(route, Route) or route.E != self.E or route.k != self.k or (_gpus != 1 and _elsewhere(route.offsets)):
             _refuse(where, f"a route of {self.E} experts and {self.k} choices on this GPU is needed")
 
-    def _check_all_rows(self, where: str, route, M: int) -> int:
-        """The rows of a product: the route's, or without one all M of one expert."""
+    def _all_rows(self, where: str, route, M: int):
+        """The rows of a product, and the address of their offsets: the route's, or without one all M of one expert."""
         if route is not None:
             self._check_route(where, route)
-            return route.M
+            return route.M, route._at[0]
         if self.E != 1:
             _refuse(where, "several experts need a route")
-        return M
+        return M, None
 
     @staticmethod
-    def _check_rows(where: str, x, n: int, length: int, dtype=None) -> None:
-        """Refuses all but n rows of `length` contiguous bf16 or fp32 elements on the GPU that do not overlap."""
-        if not (x.is_cuda and x.dim() == 2 and tuple(x.shape) == (n, length) and length > 0) or (_gpus != 1 and _elsewhere(x)):
+    def _check_rows(where: str, x, n: int, length: int, kind: int) -> int:
+        """Refuses all but n rows of `length` contiguous elements on the GPU that do not overlap, of bf16 or fp32 as `kind` says; returns their
+        stride."""
+        if not (x.is_cuda and x.shape == (n, length) and length > 0) or (_gpus != 1 and _elsewhere(x)):
             _refuse(where, f"{n} rows of {length} elements on the GPU are needed")
-        if _dtype_code(x) not in (TIDE_F32, TIDE_BF16) or (dtype is not None and x.dtype is not dtype):
+        if kind > TIDE_BF16 or _dtype_code(x) != kind:
             _refuse(where, "rows are bf16 or fp32, and of one type in a call")
-        if not x.is_contiguous() and not ((length == 1 or x.stride(1) == 1) and (n <= 1 or x.stride(0) >= length)):
+        if x.is_contiguous():
+            return length
+        stride, inner = x.stride()
+        if not ((length == 1 or inner == 1) and (n <= 1 or stride >= length)):
             _refuse(where, "rows are contiguous, or a row stride apart")
+        return stride if n > 1 else length
 
     @staticmethod
     def _check_weights(where: str, x, route: Route) -> None:

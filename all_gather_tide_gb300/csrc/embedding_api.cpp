@@ -200,7 +200,7 @@ int tide_all_gather_fp8(tide_group_t g, int32_t E, const int32_t* ps, const void
         tide::ShardPtrs sp;
         int slot;
         if ((rc = shard_ptrs(g, shards, 2, st, &sp, &slot)) != TIDE_OK) return rc;
-        const cudaError_t e = tide::launch_all_gather_fp8(sp, tv, E, params, *w, wt, {g->sm_count, overlap(g) ? ctas_of(g, 1) : 0}, st);
+        const cudaError_t e = tide::launch_all_gather_fp8(sp, tv, E, params, *w, wt, {g->sm_count, overlap(g) ? ctas_of(g, 1) : 0, g->device}, st);
         return finish(g, slot, st, e == cudaSuccess ? TIDE_OK : tide::record_cuda_error(e));
     });
 }

@@ -24,10 +24,19 @@ namespace tide {
 constexpr int64_t kMaxPairs = (int64_t(1) << 31) - (int64_t(1) << 16);
 constexpr int kBlock = 128;  // values that share a scale
 
-// CTAs that a launch may have: `ctas` where it fills the GPU, `most` (0: no limit) where it may not.
+// The device, and how many CTAs a launch may have (0: as many as it likes).
 struct Ctas {
-    int sms, most;
+    int sms, most, device;
 };
+
+// Lets a kernel have so much shared memory, once on each device; `done` is the kernel's own.
+inline cudaError_t allow_smem(const void* kernel, int bytes, int device, std::atomic<uint64_t>& done) {
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // ---- order, rows there and back ----
 constexpr int kSortThreads = 512;

@@ -15,7 +15,7 @@ constexpr int64_t kMaxLen = int64_t(1) << 30;
 size_t float_size(int32_t type) { return type == TIDE_F32 ? 4 : type == TIDE_BF16 ? 2 : 0; }
 size_t id_size(int32_t type) { return type == TIDE_I32 ? 4 : type == TIDE_I64 ? 8 : 0; }
 
-tide::Ctas ctas_of(const tide_experts* x) { return {x->sm_count, x->flags & TIDE_FLAG_OVERLAP ? std::max(1, x->sm_count / 9) : 0}; }
+tide::Ctas ctas_of(const tide_experts* x) { return {x->sm_count, x->flags & TIDE_FLAG_OVERLAP ? std::max(1, x->sm_count / 9) : 0, x->device}; }
 uint64_t timeout_of(const tide_experts* x) { return x->timeout_ns.load(); }
 
 // `rows` rows of `len` elements, `stride` apart, of which an extent in bytes fits in 64 bits.

@@ -415,7 +415,8 @@ SortShape sort_shape(int64_t pairs, const Ctas& c) {
 cudaError_t launch_sort(const void* ids, int ids64, int64_t pairs, int k, int E, int32_t* offsets, int32_t* slots, int32_t* tokens, int32_t* counts, const Ctas& c,
                         int* status, cudaStream_t stream) {
     const size_t smem = sizeof(int32_t) * (size_t(E) + 1 + 3 * size_t(E) + size_t(kSortWarps) * (E + 1));
-    cudaError_t e = cudaFuncSetAttribute(sort_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(int32_t) * (20 * (TIDE_MAX_EXPERTS + 1))));
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(sort_experts_kernel), int(sizeof(int32_t) * (20 * (TIDE_MAX_EXPERTS + 1))), c.device, allowed);
     if (e != cudaSuccess) return e;
     const SortShape shape = sort_shape(pairs, c);
     const int32_t piece = int32_t((pairs + shape.ctas - 1) / shape.ctas);

@@ -42,6 +42,7 @@ struct ProductArgs {
     int transposed;
     const int32_t* offsets;
     int32_t M, E;
+    int32_t a_box;  // rows of A that a copy brings: fewer than 128 where there are no more (8 rows of 2048 by 1536 columns of 128 experts 9.6 us, 11.2)
     int32_t N, K;  // columns of the result, blocks' length in all (product only)
     int32_t rows;  // rows of the result (gradient only)
     int32_t most_blocks;  // of the transposed operands (gradient only)
@@ -50,10 +51,21 @@ struct ProductArgs {
     int scale_vectors;  // scales that lie side by side can be read four at a time
     int bulk;         // the result can be written by TMA
     int out_vectors;  // and 16 bytes of a row at a time
-    GradPtrs grads;
     int* status;
     uint64_t timeout_ns;
 };
+struct GradArgs : ProductArgs {
+    GradPtrs grads;
+};
+template <bool Grad>
+using ArgsOf = typename std::conditional<Grad, GradArgs, ProductArgs>::type;
+
+// Where the result of expert e lies.
+template <bool Grad>
+__device__ __forceinline__ void* result_of(const ArgsOf<Grad>& p, int e) {
+    if constexpr (Grad) return p.grads.p[e];
+    else return p.out;
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ uint64_t globaltimer() {
@@ -280,7 +292,7 @@ __device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles& ti
             if (!(ok = __all_sync(kFull, wait(&empty[s.at], s.phase ^ 1)))) break;
             unsigned char* a = ring + s.at * kShare;
             if (elected()) {
-                if (rank == 0) barrier_expect(&full[s.at], Pair ? 2 * kShare : kShare);
+                if (rank == 0) barrier_expect(&full[s.at], (Pair ? 2 : 1) * (kShare - (kTileM - p.a_box) * kBlock));
                 load_2d<Pair>(a, &p.a, t.k0 + b * kBlock, row, &full[s.at]);
                 if (Grad) load_2d<Pair>(a + kTileM * kBlock, &p.b, t.k0 + b * kBlock, col, &full[s.at]);
                 else load_3d<Pair>(a + kTileM * kBlock, &p.b, b * kBlock, col, t.e, &full[s.at]);
@@ -338,7 +350,7 @@ __device__ __forceinline__ void put_sums(Out* to, const uint32_t (&x)[Count], in
 // bytes each took 10 us for a tile.
 constexpr int kStagingBytes = 2048;  // a warp
 template <bool Grad, typename Out>
-__device__ __forceinline__ void put_staged(const ProductArgs& p, unsigned char* staging, const uint32_t (&w)[16], int e, int row0, int rows, int col) {
+__device__ __forceinline__ void put_staged(const ArgsOf<Grad>& p, unsigned char* staging, const uint32_t (&w)[16], int e, int row0, int rows, int col) {
     constexpr int kCols = 64 / sizeof(Out);
     const int lane = threadIdx.x & 31;
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the bytes before have been read
@@ -358,7 +370,7 @@ __device__ __forceinline__ void put_staged(const ProductArgs& p, unsigned char* 
         return;
     }
     __syncwarp();
-    Out* const to = static_cast<Out*>(Grad ? p.grads.p[e] : p.out) + row0 * p.out_stride + col;
+    Out* const to = static_cast<Out*>(result_of<Grad>(p, e)) + row0 * p.out_stride + col;
     if (p.out_vectors && col + kCols <= p.N) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -379,7 +391,7 @@ __device__ __forceinline__ void put_staged(const ProductArgs& p, unsigned char* 
 }
 // 32 sums of each row, in that way; `rows` of the warp's rows are there.
 template <bool Grad, typename Out>
-__device__ __forceinline__ void put_sums_staged(const ProductArgs& p, unsigned char* staging, const uint32_t (&x)[32], int e, int row0, int rows, int col) {
+__device__ __forceinline__ void put_sums_staged(const ArgsOf<Grad>& p, unsigned char* staging, const uint32_t (&x)[32], int e, int row0, int rows, int col) {
     constexpr int kCols = 64 / sizeof(Out);
     if (rows <= 0) return;
 #pragma unroll
@@ -534,7 +546,7 @@ __device__ __forceinline__ void both_ctas() {
 }
 
 template <int BN, bool Pair, bool Grad, typename Out>
-__global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const __grid_constant__ ProductArgs p) {
+__global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const __grid_constant__ ArgsOf<Grad> p) {
     constexpr int kChunks = BN / 32, kFirstHalf = (kChunks + 1) / 2, kStages = stages_of(BN, Pair), kShare = share_bytes(BN, Pair);
     constexpr int kCtas = Pair ? 2 : 1;
     constexpr bool kShared = second_tile(BN) < BN;
@@ -696,7 +708,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
 // them with the block's scales and add them to the tile's sums in registers, while the next block is multiplied into another
 // buffer. No sum of more than 128 products is formed before its scale is applied.
 template <int BN, bool Grad, typename Out>
-__global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid_constant__ ProductArgs p) {
+__global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid_constant__ ArgsOf<Grad> p) {
     constexpr int kBuffers = kTmemCols / BN, kHalf = BN / 2, kChunks = kHalf / 32, kStages = stages_of(BN, false), kShare = share_bytes(BN, false);
     extern __shared__ unsigned char dynamic_smem[];
     unsigned char* const ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic_smem) + 1023) & ~uintptr_t(1023));
@@ -814,7 +826,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid
                 uint32_t x[kHalf];
 #pragma unroll
                 for (int j = 0; j < kHalf / 2; ++j) x[2 * j] = uint32_t(acc[j]), x[2 * j + 1] = uint32_t(acc[j] >> 32);
-                put_sums(static_cast<Out*>(Grad ? p.grads.p[t.e] : p.out) + row * p.out_stride + col, x, p.N - col, p.out_vectors);
+                put_sums(static_cast<Out*>(result_of<Grad>(p, t.e)) + row * p.out_stride + col, x, p.N - col, p.out_vectors);
             }
         }
     }
@@ -871,12 +883,13 @@ int describe_result(ProductArgs* p, const void* at, int bf16, int64_t N, int64_t
 }
 
 template <int BN, bool Pair, bool Grad, typename Out>
-int launch(const ProductArgs& p, bool any_scales, int64_t most_tiles, const Ctas& c, cudaStream_t stream) {
-    void (*kernel)(ProductArgs) = scaled_product_kernel<BN, Pair, Grad, Out>;
+int launch(const ArgsOf<Grad>& p, bool any_scales, int64_t most_tiles, const Ctas& c, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed[2];
+    void (*kernel)(ArgsOf<Grad>) = scaled_product_kernel<BN, Pair, Grad, Out>;
     if constexpr (!Pair)
         if (any_scales) kernel = any_scales_kernel<BN, Grad, Out>;
     const int smem = stages_of(BN, Pair) * share_bytes(BN, Pair) + kSumWarps * kStagingBytes + 2 * exponent_bytes(BN) + 1024;
-    TIDE_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    TIDE_CUDA(allow_smem(reinterpret_cast<const void*>(kernel), smem, c.device, allowed[any_scales]));
     const int64_t at_once = (c.most ? c.most : c.sms) / (Pair ? 2 : 1);
     const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(most_tiles, at_once));
     TIDE_CUDA(launch_clusters_after(kernel, Pair ? 2 : 1, int(tiles * (Pair ? 2 : 1)), any_scales ? kAnyThreads : kScaledThreads, smem, stream, p));
@@ -894,7 +907,7 @@ bool pairs(int64_t rows, int64_t down, int64_t N, bool any_scales, const Ctas& c
 }
 
 template <bool Grad>
-int launch_any(const ProductArgs& p, bool pair, bool any_scales, int64_t down, int bf16, const Ctas& c, cudaStream_t stream) {
+int launch_any(const ArgsOf<Grad>& p, bool pair, bool any_scales, int64_t down, int bf16, const Ctas& c, cudaStream_t stream) {
     const int64_t tiles = down * ((p.N + (pair ? 255 : 127)) / (pair ? 256 : 128));
     if (pair) return bf16 ? launch<256, true, Grad, __nv_bfloat16>(p, false, tiles, c, stream) : launch<256, true, Grad, float>(p, false, tiles, c, stream);
     return bf16 ? launch<128, false, Grad, __nv_bfloat16>(p, any_scales, tiles, c, stream) : launch<128, false, Grad, float>(p, any_scales, tiles, c, stream);
@@ -909,7 +922,8 @@ int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets,
     const bool any = flags & TIDE_FP8_ANY_SCALES;
     const int64_t down = padded_blocks(M, E);
     const bool pair = pairs(M / E, down, N, any, c);
-    int rc = describe(&p.a, a, K, M, 0, kTileM);
+    p.a_box = int32_t(std::min<int64_t>(kTileM, (M + 7) / 8 * 8));
+    int rc = describe(&p.a, a, K, M, 0, p.a_box);
     if (rc == TIDE_OK) rc = describe(&p.b, w, K, N, E, 128);
     if (rc != TIDE_OK) return rc;
     p.a_scales = a.scales, p.a_scale_stride = a.scale_stride;
@@ -926,7 +940,7 @@ int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets,
 
 int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, uint32_t flags, int64_t N, int64_t K, const GradPtrs& grads,
                        int grad_bf16, const Ctas& c, int* status, uint64_t timeout_ns, cudaStream_t stream) {
-    ProductArgs p{};
+    GradArgs p{};
     const bool any = flags & TIDE_FP8_ANY_SCALES;
     const int64_t padded = std::max<int64_t>(1, padded_blocks(M, E)) * kBlock;
     const int64_t down = int64_t(E) * ((N + kTileM - 1) / kTileM);
@@ -937,6 +951,7 @@ int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int
         if (rc != TIDE_OK) return rc;
     }
     p.most_blocks = int32_t(padded / kBlock);
+    p.a_box = kTileM;
     p.a_scales = dy.scales, p.a_scale_stride = dy.scale_stride;
     p.b_scales = a.scales, p.b_scale_stride = a.scale_stride;
     p.scale_vectors = aligned(dy.scales, 16) && dy.scale_stride % 4 == 0 && aligned(a.scales, 16) && a.scale_stride % 4 == 0;

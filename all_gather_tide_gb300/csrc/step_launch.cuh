@@ -38,7 +38,7 @@ __device__ __forceinline__ uint4 load_here(const uint4* p) {
 
 // The same in clusters of `cluster` CTAs.
 template <typename... P, typename... A>
-cudaError_t launch_clusters_after(void (*kernel)(P...), int cluster, int grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+cudaError_t launch_clusters_after(void (*kernel)(P...), int cluster, int grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
     cudaLaunchAttribute attr[2]{};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -56,7 +56,7 @@ cudaError_t launch_clusters_after(void (*kernel)(P...), int cluster, int grid, i
 }
 
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
     return launch_clusters_after(kernel, 1, grid, threads, smem, stream, args...);
 }
 
