@@ -126,6 +126,7 @@ SIGNATURES = {
     "tide_experts_destroy": (ctypes.c_int, [_vp]),
     "tide_experts_device_status": (ctypes.c_int, [_vp, _i32p]),
     "tide_experts_set_wait_timeout": (ctypes.c_int, [_vp, ctypes.c_uint64]),
+    "tide_experts_set_debug": (ctypes.c_int, [_vp, ctypes.c_uint32]),
     "tide_experts_sort_workspace": (ctypes.c_int, [_vp, ctypes.c_int64, _i64p]),
     "tide_experts_sort": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, ctypes.c_int64, _vp, _vp, _vp, _vp, ctypes.c_int64, _vp]),
     "tide_experts_dispatch": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp, _vp,
@@ -591,6 +592,10 @@ def tide_experts_device_status(x: int) -> int:
 
 def tide_experts_set_wait_timeout(x: int, timeout_ns: int) -> None:
     _check(lib().tide_experts_set_wait_timeout(x, timeout_ns), "tide_experts_set_wait_timeout")
+
+
+def tide_experts_set_debug(x: int, flags: int) -> None:
+    _check(lib().tide_experts_set_debug(x, flags), "tide_experts_set_debug")
 
 
 def tide_experts_sort_workspace(x: int, T: int) -> int:
@@ -1071,6 +1076,9 @@ class Experts:
 
     def set_wait_timeout(self, timeout_ns: int) -> None:
         tide_experts_set_wait_timeout(self.handle, timeout_ns)
+
+    def set_debug(self, flags: int) -> None:
+        tide_experts_set_debug(self.handle, flags)
 
     def route(self, T: int) -> Route:
         """Buffers for the order of T tokens."""

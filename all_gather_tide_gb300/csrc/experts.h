@@ -16,12 +16,13 @@ struct tide_experts {
     int device = 0, sm_count = 0;
     int* d_status = nullptr;
     std::atomic<uint64_t> timeout_ns{0};
+    std::atomic<uint32_t> debug{0};
 };
 
 namespace tide {
 
-// The most pairs of a call.
-constexpr int64_t kMaxPairs = (int64_t(1) << 31) - (int64_t(1) << 16);
+// The most pairs of a call: with 127 columns for each expert behind its own, their transposed form has columns of 31 bits.
+constexpr int64_t kMaxPairs = (int64_t(1) << 31) - (int64_t(1) << 18);
 constexpr int kBlock = 128;  // values that share a scale
 
 // The device, and how many CTAs a launch may have (0: as many as it likes).
@@ -85,10 +86,16 @@ cudaError_t launch_all_gather_fp8(const ShardPtrs& shards, const TableView& tv, 
 struct GradPtrs {
     void* p[TIDE_MAX_EXPERTS];
 };
+// How long a wait lasts at most, where it tells that it did not end, and whether to let it (nothing is loaded then).
+struct WaitArgs {
+    int* status;
+    uint64_t timeout_ns;
+    bool stall;
+};
 // TIDE_OK or a negative status.
 int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, const tide_fp8_t& w, uint32_t flags, int64_t N, int64_t K,
-                  void* out, int out_bf16, int64_t out_stride, const Ctas& c, int* status, uint64_t timeout_ns, cudaStream_t stream);
+                  void* out, int out_bf16, int64_t out_stride, const Ctas& c, const WaitArgs& wait, cudaStream_t stream);
 int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, uint32_t flags, int64_t N, int64_t K,
-                       const GradPtrs& grads, int grad_bf16, const Ctas& c, int* status, uint64_t timeout_ns, cudaStream_t stream);
+                       const GradPtrs& grads, int grad_bf16, const Ctas& c, const WaitArgs& wait, cudaStream_t stream);
 
 }  // namespace tide

@@ -16,7 +16,7 @@ size_t float_size(int32_t type) { return type == TIDE_F32 ? 4 : type == TIDE_BF1
 size_t id_size(int32_t type) { return type == TIDE_I32 ? 4 : type == TIDE_I64 ? 8 : 0; }
 
 tide::Ctas ctas_of(const tide_experts* x) { return {x->sm_count, x->flags & TIDE_FLAG_OVERLAP ? std::max(1, x->sm_count / 9) : 0, x->device}; }
-uint64_t timeout_of(const tide_experts* x) { return x->timeout_ns.load(); }
+tide::WaitArgs wait_of(const tide_experts* x) { return {x->d_status, x->timeout_ns.load(), (x->debug.load() & TIDE_DEBUG_STALL_PRODUCER) != 0}; }
 
 // `rows` rows of `len` elements, `stride` apart, of which an extent in bytes fits in 64 bits.
 int check_extent(int64_t rows, int64_t stride, int64_t elem) {
@@ -114,6 +114,12 @@ int tide_experts_device_status(tide_experts_t x, int32_t* status) {
 int tide_experts_set_wait_timeout(tide_experts_t x, uint64_t timeout_ns) {
     if (!x) return TIDE_EINVAL;
     x->timeout_ns = timeout_ns == 0 ? tide::kDefaultTimeoutNs : std::max(timeout_ns, tide::kMinTimeoutNs);
+    return TIDE_OK;
+}
+
+int tide_experts_set_debug(tide_experts_t x, uint32_t flags) {
+    if (!x || (flags & ~TIDE_DEBUG_STALL_PRODUCER)) return TIDE_EINVAL;
+    x->debug = flags;
     return TIDE_OK;
 }
 
@@ -247,7 +253,7 @@ int tide_experts_matmul(tide_experts_t x, const tide_fp8_t* a, int64_t M, const 
         if (rc == TIDE_OK) rc = check_rows(out, M, out_stride, N, elem);
         if (rc == TIDE_OK) rc = tide::check_device(x->device);
         if (rc != TIDE_OK) return rc;
-        return tide::launch_matmul(*a, M, x->E, offsets, *w, flags, N, K, out, out_type == TIDE_BF16, out_stride, ctas_of(x), x->d_status, timeout_of(x),
+        return tide::launch_matmul(*a, M, x->E, offsets, *w, flags, N, K, out, out_type == TIDE_BF16, out_stride, ctas_of(x), wait_of(x),
                                    static_cast<cudaStream_t>(stream));
     });
 }
@@ -270,7 +276,7 @@ int tide_experts_weight_grad(tide_experts_t x, const tide_fp8_t* dy, const tide_
             ptrs.p[e] = grads[e];
         }
         if ((rc = tide::check_device(x->device)) != TIDE_OK) return rc;
-        return tide::launch_weight_grad(*dy, *a, M, x->E, offsets, flags, N, K, ptrs, grad_type == TIDE_BF16, ctas_of(x), x->d_status, timeout_of(x),
+        return tide::launch_weight_grad(*dy, *a, M, x->E, offsets, flags, N, K, ptrs, grad_type == TIDE_BF16, ctas_of(x), wait_of(x),
                                         static_cast<cudaStream_t>(stream));
     });
 }

@@ -51,8 +51,7 @@ struct ProductArgs {
     int scale_vectors;  // scales that lie side by side can be read four at a time
     int bulk;         // the result can be written by TMA
     int out_vectors;  // and 16 bytes of a row at a time
-    int* status;
-    uint64_t timeout_ns;
+    WaitArgs wait;
 };
 struct GradArgs : ProductArgs {
     GradPtrs grads;
@@ -285,6 +284,7 @@ __device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles& ti
     Cursor s;
     int64_t uses = 0;
     bool ok = true;
+    if (p.wait.stall) return;
     for (int64_t it = begin; ok && it < tiles.count; it += step) {
         const Tile t = tiles.at(it);
         const int row = t.row0 + rank * kTileM, col = t.col0 + rank * (BN / 2);
@@ -308,7 +308,7 @@ __device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles& ti
     for (int64_t u = max(int64_t(0), uses - kStages); u < uses; ++u) {
         const int at = int(u % kStages);
         const uint32_t parity = uint32_t(u / kStages) & 1;
-        const uint64_t end = globaltimer() + (all ? p.timeout_ns : 20000000ull);
+        const uint64_t end = globaltimer() + (all ? p.wait.timeout_ns : 20000000ull);
         while (!((all || rank == 0) && barrier_try(all ? &empty[at] : &full[at], parity)) && globaltimer() < end) {
         }
     }
@@ -534,7 +534,7 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
             }
         }
     }
-    if (bad) atomicCAS(p.status, 0, kStatusScale);
+    if (bad) atomicCAS(p.wait.status, 0, kStatusScale);
 }
 
 // All threads of the CTA, or of both of a pair.
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
     const uint32_t tmem = tmem_at;
     wait_for_previous_kernel();
     const Tiles<kCtas * kTileM, BN, Grad> tiles(p, starts, first, sums);
-    const Waits wait{&stopped, p.status, p.timeout_ns};
+    const Waits wait{&stopped, p.wait.status, p.wait.timeout_ns};
 
     if (warp == 0) {
         load_tiles<BN, Pair, Grad>(p, tiles, rank, begin, step, ring, full, empty, wait);
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid
     const uint32_t tmem = tmem_at;
     wait_for_previous_kernel();
     const Tiles<kTileM, BN, Grad> tiles(p, starts, first, sums);
-    const Waits wait{&stopped, p.status, p.timeout_ns};
+    const Waits wait{&stopped, p.wait.status, p.wait.timeout_ns};
 
     if (warp == 0) {
         load_tiles<BN, false, Grad>(p, tiles, 0, blockIdx.x, gridDim.x, ring, full, empty, wait);
@@ -916,7 +916,7 @@ int launch_any(const ArgsOf<Grad>& p, bool pair, bool any_scales, int64_t down, 
 }  // namespace
 
 int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, const tide_fp8_t& w, uint32_t flags, int64_t N, int64_t K, void* out, int out_bf16,
-                  int64_t out_stride, const Ctas& c, int* status, uint64_t timeout_ns, cudaStream_t stream) {
+                  int64_t out_stride, const Ctas& c, const WaitArgs& wait, cudaStream_t stream) {
     if (M <= 0) return TIDE_OK;
     ProductArgs p{};
     const bool any = flags & TIDE_FP8_ANY_SCALES;
@@ -932,14 +932,14 @@ int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets,
     p.scale_vectors = aligned(a.scales, 16) && a.scale_stride % 4 == 0 && aligned(w.scales, 16) && w.scale_stride % 4 == 0 && (E == 1 || w.scale_batch % 4 == 0);
     p.offsets = offsets, p.M = int32_t(M), p.E = E, p.N = int32_t(N), p.K = int32_t(K), p.rows = 0;
     p.out = out, p.out_stride = out_stride, p.out_vectors = vectors16(out, out_stride, M, out_bf16 ? 2 : 4);
-    p.status = status, p.timeout_ns = timeout_ns;
+    p.wait = wait;
     if ((rc = describe_result(&p, out, out_bf16, N, M, out_stride, 0, 0)) != TIDE_OK) return rc;
     // `down` counts tiles of 128 rows; of 256 there are fewer
     return launch_any<false>(p, pair, any, down, out_bf16, c, stream);
 }
 
 int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets, uint32_t flags, int64_t N, int64_t K, const GradPtrs& grads,
-                       int grad_bf16, const Ctas& c, int* status, uint64_t timeout_ns, cudaStream_t stream) {
+                       int grad_bf16, const Ctas& c, const WaitArgs& wait, cudaStream_t stream) {
     GradArgs p{};
     const bool any = flags & TIDE_FP8_ANY_SCALES;
     const int64_t padded = std::max<int64_t>(1, padded_blocks(M, E)) * kBlock;
@@ -959,7 +959,7 @@ int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int
     p.grads = grads, p.out_stride = K;
     p.out_vectors = 1;
     for (int e = 0; e < E; ++e) p.out_vectors &= vectors16(grads.p[e], K, N, grad_bf16 ? 2 : 4);
-    p.status = status, p.timeout_ns = timeout_ns;
+    p.wait = wait;
     // gradients at one distance from each other are one array to TMA
     const int64_t pitch = E > 1 ? static_cast<const char*>(grads.p[1]) - static_cast<const char*>(grads.p[0]) : 0;
     bool even = true;

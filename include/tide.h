@@ -561,9 +561,11 @@ int tide_experts_destroy(tide_experts_t x);
 int tide_experts_device_status(tide_experts_t x, int32_t *status);
 /* Every wait of the products' kernels gives up after `timeout_ns` (0 = the default, 2 s). */
 int tide_experts_set_wait_timeout(tide_experts_t x, uint64_t timeout_ns);
+/* Test hook: with TIDE_DEBUG_STALL_PRODUCER the products' kernels load nothing, so their waits expire. */
+int tide_experts_set_debug(tide_experts_t x, uint32_t flags);
 
 /* Bytes of device workspace (256-byte aligned) with which tide_experts_sort serves up to T tokens; 0 where
- * it needs none.  Errors: TIDE_EINVAL, TIDE_ERANGE (T*k > 2^31 - 2^16). */
+ * it needs none.  Errors: TIDE_EINVAL, TIDE_ERANGE (T*k > 2^31 - 2^18). */
 int tide_experts_sort_workspace(tide_experts_t x, int64_t T, int64_t *bytes);
 
 /*
@@ -578,7 +580,7 @@ int tide_experts_sort_workspace(tide_experts_t x, int64_t T, int64_t *bytes);
  *   T*k int32.   workspace: device, 256-byte aligned, at least tide_experts_sort_workspace's bytes for T
  *   tokens or more (may be NULL where that is 0); not shared by calls that overlap.
  * Errors: TIDE_EINVAL (null or misaligned pointers, T < 0, a type, the workspace too small, another device
- * current), TIDE_ERANGE (T*k > 2^31 - 2^16), TIDE_ECUDA.
+ * current), TIDE_ERANGE (T*k > 2^31 - 2^18), TIDE_ECUDA.
  */
 int tide_experts_sort(tide_experts_t x, const void *ids, int32_t ids_type, int64_t T, int32_t *offsets,
                       int32_t *slots, int32_t *tokens, void *workspace, int64_t workspace_bytes, void *stream);
@@ -590,7 +592,7 @@ int tide_experts_sort(tide_experts_t x, const void *ids, int32_t ids_type, int64
  * apart; T rows of src, T*k of rows.  Rows that no pair has are left as they are.  Any element alignment is
  * accepted.
  * Errors of this and the following calls: TIDE_EINVAL (null or misaligned pointers, a negative size, a type, a
- * stride too small, another device current), TIDE_ERANGE (more than 2^31 - 2^16 pairs, len > 2^30, an
+ * stride too small, another device current), TIDE_ERANGE (more than 2^31 - 2^18 pairs, len > 2^30, an
  * extent in bytes beyond int64), TIDE_ECUDA.
  */
 int tide_experts_dispatch(tide_experts_t x, const void *src, int32_t type, int64_t src_stride, int64_t T, int64_t len,

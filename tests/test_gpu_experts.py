@@ -485,3 +485,297 @@ def test_a_nan_scale_makes_its_rows_nan_alone(tide):
         want[70] = True
         want[:, 128:256] = True
         assert torch.equal(torch.isnan(out).cpu(), want) and ex.device_status() == 0
+
+
+# ---- a run of them together -------------------------------------------------------------------------
+
+
+class Layer:
+    """y = sum over choices of weights * (W_e x): every call of a training step, and its plain form in 64 bits, with the same roundings to 8
+    bits and to bf16 where rows are handed over."""
+
+    def __init__(self, tide, T, k, E, N, K, R, seed, flags=0):
+        g = gen(seed)
+        self.T, self.k, self.E, self.N, self.K = T, k, E, N, K
+        self.ids = draw_ids(g, T, k, E, 0.1)
+        self.x, self.weights, self.dout = torch.randn(T, K, generator=g).bfloat16(), torch.rand(T, k, generator=g), torch.randn(T, N, generator=g).bfloat16()
+        self.w = (torch.randn(E, N, K, generator=g) * K ** -0.5).bfloat16()
+        self.group = tide.Group(R, [(N, K)] * E, flags)
+        m = -(-N // R)
+        full = torch.zeros(E, R * m, K, dtype=torch.bfloat16)
+        full[:, :N] = self.w
+        self.shards = [full[:, d * m:(d + 1) * m].reshape(-1).cuda() for d in range(R)]
+        self.ex = tide.Experts(E, k, flags)
+        self.route = self.ex.route(T)
+        M, dev = T * k, "cuda"
+        self.dev = [x.cuda() for x in (self.ids, self.x, self.weights, self.dout)]
+        self.W = tide.Fp8Weights(E, N, K, transposed=True)
+        self.x8, self.xt8, self.dy8, self.dyt8 = tide.Fp8Rows(M, K), tide.Fp8Columns(M, K, E), tide.Fp8Rows(M, N), tide.Fp8Columns(M, N, E)
+        self.y, self.dy, self.dxr = (torch.zeros(M, n, dtype=torch.bfloat16, device=dev) for n in (N, N, K))
+        self.out, self.dx = torch.zeros(T, N, dtype=torch.bfloat16, device=dev), torch.zeros(T, K, dtype=torch.bfloat16, device=dev)
+        self.dweights = torch.zeros(T, k, device=dev)
+        self.grads = [torch.zeros(N * K, dtype=torch.bfloat16, device=dev) for _ in range(E)]
+
+    def results(self):
+        return [self.out, self.dx, self.dweights, self.y, self.dy, *self.grads]
+
+    def step(self, stream=None):
+        ex, r = self.ex, self.route
+        ids, x, weights, dout = self.dev
+        self.group.all_gather_fp8(range(self.E), self.shards, self.W, stream=stream)
+        ex.sort(ids, r, stream=stream)
+        ex.dispatch_fp8(x, r, self.x8, stream=stream)
+        ex.matmul(self.x8, self.W, r, self.y, stream=stream)
+        ex.combine(self.y, r, self.out, weights, stream=stream)
+        ex.combine_grad(dout, self.y, r, weights, self.dy, self.dweights, stream=stream)
+        ex.quantize(self.dy, r, rows=self.dy8, columns=self.dyt8, stream=stream)
+        ex.matmul(self.dy8, self.W, r, self.dxr, transposed=True, stream=stream)
+        ex.combine(self.dxr, r, self.dx, stream=stream)
+        ex.quantize(x, r, columns=self.xt8, gather=True, stream=stream)
+        ex.weight_grad(self.dyt8, self.xt8, r, self.grads, stream=stream)
+
+    def check(self):
+        """Each result against the plain form of the call that made it, from that call's own inputs."""
+        T, k, E, N, K = self.T, self.k, self.E, self.N, self.K
+        offsets, slots, tokens = order_of(self.ids, E)
+        at, s = slots >= 0, slots.clamp(min=0)
+        half = HALF["bf16"] * 1.01
+        x8, y, dy, dxr = values(*in_rows(self.x)), self.y.cpu(), self.dy.cpu(), self.dxr.cpu()
+        dy8 = values(*in_rows(dy))
+        for e, (a, b) in enumerate(zip(offsets, offsets[1:])):
+            c, sc = in_blocks(self.w[e])
+            w = c * sc.repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+            rows = x8[tokens[a:b]]
+            for got, p, q in ((y[a:b], rows, w.t()), (dxr[a:b], dy8[a:b], w),
+                              (self.grads[e].cpu().view(N, K), values(*in_rows(dy[a:b].t())) if b > a else torch.zeros(N, 0).double(),
+                               values(*in_rows(self.x[tokens[a:b]].t())).t() if b > a else torch.zeros(0, K).double())):
+                want, size = p @ q, p.abs() @ q.abs()
+                assert bool(((got.double() - want).abs() <= bound(-(-p.shape[1] // 128), size) + half * want.abs()).all())
+        parts = torch.where(at[:, :, None], y[s].double(), 0.0)
+        weighted = parts * self.weights.double()[:, :, None]
+        for got, p in ((self.out, weighted), (self.dx, torch.where(at[:, :, None], dxr[s].double(), 0.0))):
+            assert bool(((got.cpu().double() - p.sum(1)).abs() <= (k + 1) * U * p.abs().sum(1) + half * p.sum(1).abs()).all())
+        want = torch.where(at[:, :, None], self.dout[:, None].float() * self.weights[:, :, None], 0.0).bfloat16()
+        assert torch.equal(dy[slots[at]], want[at])
+        p = parts * self.dout.double()[:, None]
+        assert bool(((self.dweights.cpu().double() - p.sum(2)).abs() <= (N + 1) * U * p.abs().sum(2)).all())
+        assert self.ex.device_status() == 0
+
+
+@pytest.mark.parametrize("T, k, E, N, K, R, flags", [(1, 2, 4, 64, 96, 2, 0), (300, 3, 7, 331, 200, 3, 0), (2500, 8, 16, 640, 512, 8, 0), (700, 2, 5, 256, 384, 4, 8)])
+def test_a_layer_and_its_gradients(tide, T, k, E, N, K, R, flags):
+    layer = Layer(tide, T, k, E, N, K, R, T, flags)
+    layer.step()
+    layer.check()
+
+
+def test_a_layer_on_another_stream(tide):
+    """Work on a stream of its own, behind a long kernel there, with nothing of it on the current stream; by object and by handle."""
+    for handle in (False, True):
+        layer = Layer(tide, 300, 3, 7, 200, 264, 2, 3)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        layer.step(side.cuda_stream if handle else side)
+        side.synchronize()
+        layer.check()
+
+
+def test_two_layers_at_once(tide):
+    """One object of experts on two streams, each with its own buffers."""
+    a, b = Layer(tide, 2000, 4, 8, 384, 512, 2, 1), Layer(tide, 2000, 4, 8, 384, 512, 2, 2)
+    b.ex, b.route = a.ex, a.ex.route(2000)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        a.step(streams[0])
+        b.step(streams[1])
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+
+
+def test_a_layer_captured_and_replayed(tide):
+    """Two graphs of two layers, replayed with other tokens than they were captured with."""
+    layers = [Layer(tide, 9000, 4, 9, 200, 264, 3, 5), Layer(tide, 40, 2, 4, 136, 72, 2, 6)]
+    graphs = []
+    for layer in layers:
+        layer.step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer.step()
+        graphs.append(g)
+    for seed in (7, 8):
+        for layer in layers:
+            g = gen(seed)
+            layer.ids = draw_ids(g, layer.T, layer.k, layer.E, 0.3)
+            layer.x, layer.dout = torch.randn(layer.T, layer.K, generator=g).bfloat16(), torch.randn(layer.T, layer.N, generator=g).bfloat16()
+            for to, x in zip(layer.dev, (layer.ids, layer.x, layer.weights, layer.dout)):
+                to.copy_(x)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for layer in layers:
+            layer.check()
+
+
+def test_equal_calls_give_equal_bits(tide):
+    layer = Layer(tide, 3000, 4, 12, 520, 384, 4, 9)
+    layer.step()
+    first = [x.clone() for x in layer.results()]
+    for x in layer.results():
+        x.fill_(7)
+    held = int(layer.route.offsets[-1])
+    layer.step()
+    for x, y in zip(layer.results(), first):
+        if x is layer.y or x is layer.dy:
+            x, y = x[:held], y[:held]
+        assert torch.equal(x, y)
+
+
+# ---- far offsets, expired waits, refusals -------------------------------------------------------------
+
+
+def test_offsets_past_32_bits(tide):
+    """Rows whose bytes lie past 2^32 in every buffer: a sample of rows against the plain form."""
+    T, k, E, D, N = 300_000, 8, 4, 2048, 1040
+    M = T * k
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda")
+    x = torch.randn(T, D, generator=g, device="cuda", dtype=torch.float32).bfloat16()
+    ex = tide.Experts(E, k)
+    route = ex.route(T)
+    ex.sort(ids, route)
+    rows, q = torch.empty(M, D, dtype=torch.bfloat16, device="cuda"), tide.Fp8Rows(M, D)
+    ex.dispatch(x, route, rows)
+    ex.dispatch_fp8(x, route, q)
+    W = tide.Fp8Weights(E, N, D)
+    random_fp8(gen(1), W, False)
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    ex.matmul(q, W, route, out)
+    assert rows.numel() * 2 > 1 << 32 and q.codes.numel() > 1 << 32 and out.numel() * 2 > 1 << 32
+    some = torch.cat([torch.arange(0, 64), torch.randint(0, M, (256,), generator=gen(2)), torch.arange(M - 64, M)]).cuda()
+    tokens, offsets = route.tokens[some].long(), route.offsets.cpu()
+    assert torch.equal(rows[some], x[tokens])
+    codes, scales = in_rows(x[tokens].cpu())
+    assert same(q.codes.view(torch.uint8)[some].view(torch.float8_e4m3fn).float().cpu().double(), codes) and same(q.scales[some].cpu().double(), scales)
+    w = W.codes.cpu().float().double() * W.scales.cpu().double().repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)[:, :, :D]
+    a, e = values(codes, scales), torch.bucketize(some.cpu(), offsets[1:], right=True)
+    want, size = torch.einsum("sc,snc->sn", a, w[e]), torch.einsum("sc,snc->sn", a.abs(), w[e].abs())
+    assert bool(((out[some].cpu().double() - want).abs() <= bound(D // 128, size) + HALF["bf16"] * 1.01 * want.abs()).all())
+    # and back, out of the far rows
+    back = torch.empty(T, D, dtype=torch.bfloat16, device="cuda")
+    ex.combine(rows, route, back)
+    total = x.double() * k
+    assert bool(((back.double() - total).abs() <= (k + 1) * U * total.abs() + HALF["bf16"] * 1.01 * total.abs()).all())
+    # transposed: the last columns lie past 2^32 too
+    del rows, out, back
+    c = tide.Fp8Columns(M, D, E)
+    ex.quantize(x, route, columns=c, gather=True)
+    assert c.codes.numel() > 1 << 32
+    last = int(offsets[-2]) + (M - int(offsets[-2]) - 1) // 128 * 128  # the last block's first row
+    n, at = M - last, sum(-(-(b - a) // 128) for a, b in zip(offsets.tolist(), offsets.tolist()[1:])) - 1
+    part = torch.zeros(D, 128, dtype=torch.float64)
+    part[:, :n] = x[route.tokens[last:].long()].cpu().double().t()
+    codes, scales = in_rows(part)
+    assert same(c.codes[:, at * 128:(at + 1) * 128].float().cpu().double(), codes) and same(c.scales[at].cpu().double(), scales[:, 0])
+
+
+@pytest.mark.parametrize("T", [40, 20000])
+def test_a_wait_that_runs_out_is_told_of(tide, T):
+    """Products that load nothing: every wait gives up after a millisecond, the kernel returns, and the next call works. Both tile shapes, and
+    sums in registers."""
+    E, N, K = 4, 512, 768
+    ex = tide.Experts(E, 2)
+    route = ex.route(T)
+    ex.sort(torch.randint(0, E, (T, 2), generator=gen(0)).cuda(), route)
+    A, W, C, D = tide.Fp8Rows(2 * T, K), tide.Fp8Weights(E, N, K), tide.Fp8Columns(2 * T, K, E), tide.Fp8Columns(2 * T, N, E)
+    for i, x in enumerate((A, W, C, D)):
+        random_fp8(gen(i), x, False)
+    out, grads = torch.zeros(2 * T, N, device="cuda"), torch.zeros(E, N, K, device="cuda")
+    calls = [lambda any_scales: ex.matmul(A, W, route, out, any_scales=any_scales), lambda any_scales: ex.weight_grad(D, C, route, grads, any_scales=any_scales)]
+    for any_scales in (False, True):
+        for f in calls:
+            f(any_scales)
+            torch.cuda.synchronize()
+            first = out.clone(), grads.clone()
+            assert ex.device_status() == 0
+            ex.set_wait_timeout(1_000_000)
+            ex.set_debug(tide.TIDE_DEBUG_STALL_PRODUCER)
+            f(any_scales)
+            torch.cuda.synchronize()
+            assert ex.device_status() == 1
+            ex.set_debug(0)
+            ex.set_wait_timeout(0)
+            f(any_scales)
+            assert torch.equal(out, first[0]) and torch.equal(grads, first[1]) and ex.device_status() == 0
+
+
+def test_refusals(tide):
+    """Arguments that the C calls refuse before anything is enqueued."""
+    L, EI, ER = tide.lib(), tide.TIDE_EINVAL, tide.TIDE_ERANGE
+    ex, G = tide.Experts(5, 2), tide.Group(2, [(24, 40), (24, 40), (24, 41), (7, 1)])
+    h, B, F = ex.handle, tide.TIDE_BF16, tide.TIDE_F32
+    buf = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    p = buf.data_ptr()
+    v = ctypes.c_int64()
+    far = (1 << 31) - (1 << 18) + 2
+
+    def fp8(codes=p, stride=48, batch=24 * 48, scales=p, scale_stride=4, scale_batch=4):
+        return tide._Fp8(codes, stride, batch, scales, scale_stride, scale_batch)
+
+    assert L.tide_experts_sort_workspace(h, -1, ctypes.byref(v)) == EI and L.tide_experts_sort_workspace(h, far, ctypes.byref(v)) == ER and L.tide_experts_sort_workspace(h, 1, None) == EI
+    for status, args in ((EI, (None, tide.TIDE_I64, 3, p, p, p, None, 0)), (EI, (p, F, 3, p, p, p, None, 0)), (EI, (p + 4, tide.TIDE_I64, 3, p, p, p, None, 0)),
+                         (EI, (p, tide.TIDE_I64, -1, p, p, p, None, 0)), (EI, (p, tide.TIDE_I64, 3, None, p, p, None, 0)), (EI, (p, tide.TIDE_I64, 3, p, None, p, None, 0)),
+                         (EI, (p, tide.TIDE_I64, 3, p, p, p + 2, None, 0)), (EI, (p, tide.TIDE_I64, 3, p, p, p, p + 16, 4096)), (ER, (p, tide.TIDE_I64, far, p, p, p, None, 0)),
+                         (EI, (p, tide.TIDE_I64, 40000, p, p, p, None, 0)), (EI, (p, tide.TIDE_I64, 40000, p, p, p, p, 256))):
+        assert L.tide_experts_sort(h, *args, None) == status, args
+    for status, args in ((EI, (None, B, 8, 3, 8, p, p, 8)), (EI, (p + 1, B, 8, 3, 8, p, p, 8)), (EI, (p + 2, F, 8, 3, 8, p, p, 8)), (EI, (p, 2, 8, 3, 8, p, p, 8)),
+                         (EI, (p, B, 7, 3, 8, p, p, 8)), (EI, (p, B, 8, -1, 8, p, p, 8)), (EI, (p, B, 8, 3, 0, p, p, 8)), (EI, (p, B, 8, 3, 8, None, p, 8)),
+                         (EI, (p, B, 8, 3, 8, p, None, 8)), (EI, (p, B, 8, 3, 8, p, p, 7)), (ER, (p, B, 8, far, 8, p, p, 8)), (ER, (p, B, 1 << 31, 3, (1 << 30) + 1, p, p, 1 << 31)),
+                         (ER, (p, B, 1 << 62, 3, 8, p, p, 8))):
+        assert L.tide_experts_dispatch(h, *args, None) == status, args
+        src, kind, stride, T, n, slots, rows, rows_stride = args
+        assert L.tide_experts_combine(h, rows, kind, rows_stride, T, n, slots, None, src, stride, None) == status, args
+        assert L.tide_experts_combine_grad(h, src, kind, stride, rows, rows_stride, T, n, slots, p, p, 1 << 40, p, None) == status, args
+    assert L.tide_experts_combine(h, p, B, 8, 3, 8, p, p + 2, p, 8, None) == EI
+    assert L.tide_experts_combine_grad(h, p, B, 8, p, 8, 3, 8, p, None, p, 8, p, None) == EI and L.tide_experts_combine_grad(h, p, B, 8, p, 8, 3, 8, p, p, p, 8, None, None) == EI
+    bad = (fp8(codes=None), fp8(codes=p + 8), fp8(stride=47), fp8(stride=32), fp8(scales=None), fp8(scales=p + 2), fp8(scale_stride=0))
+    for m in bad:
+        assert L.tide_experts_dispatch_fp8(h, p, B, 40, 3, 40, p, m, None) == EI
+        assert L.tide_experts_quantize(h, p, B, 40, 6, 6, 40, p, None, m, None, None) == EI
+        assert L.tide_experts_matmul(h, m, 6, p, fp8(), 0, 24, 40, p, B, 24, None) == EI
+        assert L.tide_experts_matmul(h, fp8(), 6, p, m, 0, 24, 40, p, B, 24, None) == EI
+        assert L.tide_all_gather_fp8(G.handle, 2, (ctypes.c_int32 * 2)(0, 1), (ctypes.c_void_p * 2)(p, p), m, None, None) == EI
+    assert L.tide_experts_dispatch_fp8(h, p, B, 40, 3, 40, p, None, None) == EI
+    columns = fp8(stride=640, scale_stride=40)
+    grads = (ctypes.c_void_p * 5)(*[p] * 5)
+    for m in (fp8(stride=624, scale_stride=40), fp8(stride=640, scale_stride=39), fp8(codes=None, stride=640, scale_stride=40)):
+        assert L.tide_experts_quantize(h, p, B, 40, 6, 6, 40, p, None, None, m, None) == EI
+        assert L.tide_experts_weight_grad(h, m, columns, 6, p, 0, 40, 40, grads, B, None) == EI
+        assert L.tide_experts_weight_grad(h, columns, m, 6, p, 0, 40, 40, grads, B, None) == EI
+    for status, args in ((EI, (None, B, 40, 6, 6, 40, p, None)), (EI, (p, 3, 40, 6, 6, 40, p, None)), (EI, (p, B, 39, 6, 6, 40, p, None)), (EI, (p, B, 40, 5, 6, 40, p, None)),
+                         (EI, (p, B, 40, 6, -1, 40, p, None)), (EI, (p, B, 40, 6, 6, 0, p, None)), (EI, (p, B, 40, 6, 6, 40, None, None)), (EI, (p, B, 40, 6, 6, 40, p + 2, None)),
+                         (EI, (p, B, 40, 6, 6, 40, p, p + 1)), (ER, (p, B, 40, far, far, 40, p, None)), (ER, (p, B, 1 << 31, 6, 6, (1 << 30) + 1, p, None))):
+        assert L.tide_experts_quantize(h, *args, fp8(), None, None) == status, args
+    for status, args in ((EI, (-1, p, fp8(), 0, 24, 40, p, B, 24)), (EI, (6, None, fp8(), 0, 24, 40, p, B, 24)), (EI, (6, p, fp8(), 4, 24, 40, p, B, 24)), (EI, (6, p, fp8(), 0, 0, 40, p, B, 24)),
+                         (EI, (6, p, fp8(), 0, 24, 0, p, B, 24)), (EI, (6, p, fp8(), 0, 24, 40, None, B, 24)), (EI, (6, p, fp8(), 0, 24, 40, p + 1, B, 24)), (EI, (6, p, fp8(), 0, 24, 40, p, 2, 24)),
+                         (EI, (6, p, fp8(), 0, 24, 40, p, B, 23)), (EI, (6, p, fp8(batch=24), 0, 24, 40, p, B, 24)), (EI, (6, p, fp8(scale_batch=-1), 0, 24, 40, p, B, 24)),
+                         (ER, (far, p, fp8(), 0, 24, 40, p, B, 24)), (ER, (6, p, fp8(), 0, (1 << 30) + 1, 40, p, B, 1 << 31))):
+        assert L.tide_experts_matmul(h, fp8(), *args, None) == status, args
+    assert L.tide_experts_matmul(h, None, 6, p, fp8(), 0, 24, 40, p, B, 24, None) == EI and L.tide_experts_matmul(h, fp8(), 6, p, None, 0, 24, 40, p, B, 24, None) == EI
+    for status, args in ((EI, (-1, p, 0, 40, 40, grads, B)), (EI, (6, None, 0, 40, 40, grads, B)), (EI, (6, p, tide.TIDE_FP8_TRANSPOSED, 40, 40, grads, B)), (EI, (6, p, 0, 0, 40, grads, B)),
+                         (EI, (6, p, 0, 40, 40, None, B)), (EI, (6, p, 0, 40, 40, grads, tide.TIDE_I32)), (EI, (6, p, 0, 40, 40, (ctypes.c_void_p * 5)(p, p, p, None, p), B)),
+                         (EI, (6, p, 0, 40, 40, (ctypes.c_void_p * 5)(p, p, p, p + 2, p), F)), (ER, (far, p, 0, 40, 40, grads, B))):
+        assert L.tide_experts_weight_grad(h, columns, columns, *args, None) == status, args
+    shards = (ctypes.c_void_p * 2)(p, p)
+    for ps, sh, w, wt in (((0, 2), shards, fp8(), None), ((0, 4), shards, fp8(), None), ((-1, 0), shards, fp8(), None), ((0, 1), (ctypes.c_void_p * 2)(p, None), fp8(), None),
+                          ((0, 1), (ctypes.c_void_p * 2)(p, p + 1), fp8(), None), ((0, 1), None, fp8(), None), ((0, 1), shards, None, None), ((0, 1), shards, fp8(), fp8(stride=16)),
+                          ((0, 1), shards, fp8(), fp8(codes=None)), ((0, 1), shards, fp8(batch=8), None)):
+        assert L.tide_all_gather_fp8(G.handle, 2, (ctypes.c_int32 * 2)(*ps), sh, w, wt, None) == EI
+    assert L.tide_all_gather_fp8(G.handle, 0, (ctypes.c_int32 * 2)(0, 1), shards, fp8(), None, None) == EI
+    assert L.tide_experts_set_debug(h, 2) == EI
+    torch.cuda.synchronize()
+    assert not bool(buf.any()) and ex.device_status() == 0
