@@ -779,3 +779,54 @@ def test_refusals(tide):
     assert L.tide_experts_set_debug(h, 2) == EI
     torch.cuda.synchronize()
     assert not bool(buf.any()) and ex.device_status() == 0
+
+
+# ---- the example --------------------------------------------------------------------------------------
+
+
+def test_example_with_experts(tide):
+    """A step of the example's layer of experts runs, and its gradients are those of the plain formula, of which 8 bits hold each factor to
+    2^-4 of its value or, below a block's smallest normal number, 2^-10 of 2^-8 of the block's largest: products of two are off by (2^-4 + 2^-4 +
+    2^-8) of their magnitude, and by 2^-17 of the largest of one factor times the other's, and sums by the sum of these."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "sharded_step.py")
+    spec = importlib.util.spec_from_file_location("sharded_step", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    dim, E = 64, 5
+    model = module.ShardedModel(2, 211, dim, 96, experts=E, choices=2)
+    losses = [float(model.step(module.batches(2, 211, 96, i))) for i in range(3)]
+    assert all(x == x and 0 < x < 20 for x in losses) and model.layer.device_status() == 0
+    model.gather()
+    g = gen(4)
+    x = torch.randn(96, dim, generator=g).bfloat16().cuda().requires_grad_(True)
+    G = model.params[1].detach().requires_grad_(True)
+    h, backward = model.expert_layer(x, G)
+    dh = torch.randn(96, dim, generator=g).bfloat16().cuda()
+    x.grad = torch.zeros_like(x)
+    grads = backward(dh)
+    # the formula in 64 bits, with the layer's own choices and signs
+    offsets, tokens, slots = model.route.offsets.cpu().tolist(), model.route.tokens.cpu().long(), model.route.slots.cpu().long()
+    W = [torch.cat([model.shards[d][model.group.param_layout(2 + e)[1]:][:32 * dim].view(32, dim) for d in range(2)]).cpu().double() for e in range(E)]
+    xs, score = x.detach().cpu().double(), (x.detach().cpu().float() @ G.detach().cpu().float().t()).double()
+    eps, floor = 2.0 ** -3 + 2.0 ** -8, 2.0 ** -17
+    choice = torch.full((96, 2), -1)
+    for e in range(E):
+        for s in range(offsets[e], offsets[e + 1]):
+            choice[tokens[s]][slots[tokens[s]] == s] = e
+    p = torch.softmax(score.gather(1, choice), 1)
+    for e in range(E):
+        a, b = offsets[e], offsets[e + 1]
+        t = tokens[a:b]
+        pe = p[t][choice[t] == e]
+        y = xs[t] @ W[e].t()
+        off = eps * (xs[t].abs() @ W[e].abs().t()) + floor * dim * (xs[t].abs().amax(1, keepdim=True) * W[e].abs().max() * 2)
+        sure = y.abs() > off * 1.1  # where the sign, and so relu's gradient, is beyond doubt
+        dy = dh.cpu().double()[t] * pe[:, None] * (y > 0)
+        unsure = dh.cpu().double()[t].abs() * pe[:, None] * ~sure
+        want, size = dy.t() @ xs[t], dy.abs().t() @ xs[t].abs()
+        slack = (eps + 2.0 ** -7) * size + unsure.t() @ xs[t].abs() * (1 + eps) + floor * (b - a) * 2 * dh.abs().max().item() * xs.abs().max() + 1e-6
+        assert bool(((grads[e].cpu().double().view(dim, dim) - want).abs() <= slack).all()), e
+    assert G.grad is not None and bool(torch.isfinite(G.grad.float()).all()) and bool(torch.isfinite(x.grad.float()).all()) and bool((x.grad != 0).any())
