@@ -205,8 +205,8 @@ dispatch_kernel(const Word* src, int64_t src_stride, int64_t T, int k, int32_t M
     let_next_kernel_start();
 }
 
-// The rows back at their tokens, weighted.  A warp takes a token and a stretch of 32*Cols vectors; AtOnce rows are in
-// flight before their products are added, in fp32 and in the pairs' order.
+// The rows back at their tokens, weighted.  A warp takes a token and up to `per` stretches of 32*Cols vectors, one after the other; AtOnce
+// rows are in flight before their products are added, in fp32 and in the pairs' order.
 //
 // Bound by HBM reads: 524288 rows of 2048 bf16 values back to 65536 tokens in 363 us, 6.7 TB/s (440 with four CTAs an SM, whose
 // registers spilled).
@@ -214,49 +214,53 @@ constexpr int kCombineCtasPerSm = 3;
 template <typename T, int V, int Cols, int AtOnce>
 __global__ void __launch_bounds__(kThreads, kCombineCtasPerSm)
 combine_kernel(const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_t M, uint32_t len, const int32_t* slots, const float* weights, T* out,
-               int64_t out_stride, uint32_t stretches, int64_t items) {
+               int64_t out_stride, uint32_t stretches, uint32_t per, uint32_t shares, int64_t items) {
     using Word = typename Vec<T, V>::Word;
     const int lane = threadIdx.x & 31;
     wait_for_previous_kernel();
     for (int64_t it = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * kWarps) {
-        const int64_t t = it / stretches;
-        const uint32_t col = (uint32_t(it - t * stretches) * (32 * Cols) + lane) * V;
+        const int64_t t = it / shares;
+        const uint32_t s0 = uint32_t(it - t * shares) * per, s1 = min(s0 + per, stretches);
         int32_t slot;
-        unsigned held = held_pairs(slots, t, k, M, lane, &slot);
+        const unsigned all = held_pairs(slots, t, k, M, lane, &slot);
         const float weight = weights && lane < k ? __ldcg(weights + t * k + lane) : 1.0f;
-        float acc[Cols][V] = {};
-        while (held) {
-            Word w[AtOnce][Cols];
-            float f[AtOnce];
-            int many = 0;
+        for (uint32_t s = s0; s < s1; ++s) {
+            const uint32_t col = (s * (32 * Cols) + lane) * V;
+            float acc[Cols][V] = {};
+            unsigned held = all;
+            while (held) {
+                Word w[AtOnce][Cols];
+                float f[AtOnce];
+                int many = 0;
 #pragma unroll
-            for (int r = 0; r < AtOnce; ++r) {
-                if (!held) break;
-                const int j = __ffs(held) - 1;
-                held &= held - 1;
-                const T* from = rows + int64_t(__shfl_sync(kFull, slot, j)) * rows_stride + col;
-                f[r] = __shfl_sync(kFull, weight, j);
-                ++many;
+                for (int r = 0; r < AtOnce; ++r) {
+                    if (!held) break;
+                    const int j = __ffs(held) - 1;
+                    held &= held - 1;
+                    const T* from = rows + int64_t(__shfl_sync(kFull, slot, j)) * rows_stride + col;
+                    f[r] = __shfl_sync(kFull, weight, j);
+                    ++many;
 #pragma unroll
-                for (int c = 0; c < Cols; ++c)
-                    if (col + c * 32 * V < len) w[r][c] = __ldcs(reinterpret_cast<const Word*>(from + c * 32 * V));
-            }
+                    for (int c = 0; c < Cols; ++c)
+                        if (col + c * 32 * V < len) w[r][c] = __ldcs(reinterpret_cast<const Word*>(from + c * 32 * V));
+                }
 #pragma unroll
-            for (int r = 0; r < AtOnce; ++r) {
-                if (r >= many) break;
+                for (int r = 0; r < AtOnce; ++r) {
+                    if (r >= many) break;
 #pragma unroll
-                for (int c = 0; c < Cols; ++c) {
-                    if (col + c * 32 * V >= len) continue;
-                    float x[V];
-                    widen(w[r][c], x);
+                    for (int c = 0; c < Cols; ++c) {
+                        if (col + c * 32 * V >= len) continue;
+                        float x[V];
+                        widen(w[r][c], x);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) acc[c][v] = weights ? fmaf(f[r], x[v], acc[c][v]) : acc[c][v] + x[v];
+                        for (int v = 0; v < V; ++v) acc[c][v] = weights ? fmaf(f[r], x[v], acc[c][v]) : acc[c][v] + x[v];
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int c = 0; c < Cols; ++c)
-            if (col + c * 32 * V < len) put(out + t * out_stride + col + c * 32 * V, acc[c]);
+            for (int c = 0; c < Cols; ++c)
+                if (col + c * 32 * V < len) put(out + t * out_stride + col + c * 32 * V, acc[c]);
+        }
     }
     let_next_kernel_start();
 }
@@ -375,14 +379,18 @@ cudaError_t combine(const RowsView& rows, int64_t tokens, int k, int64_t len, co
                     const Ctas& c, cudaStream_t stream) {
     auto go = [&](auto* kernel, int cols) {
         const uint32_t stretches = uint32_t((len + 32 * V * cols - 1) / (32 * V * cols));
-        const int64_t items = tokens * stretches;
-        return launch_after(kernel, grid_of((items + kWarps - 1) / kWarps, c), kThreads, 0, stream, static_cast<const T*>(rows.p), rows.stride, tokens,
-                            k, int32_t(tokens * k), uint32_t(len), slots, weights, static_cast<T*>(out), out_stride, stretches, items);
+        // a warp takes the whole row where the tokens fill the GPU four times, so that it finds their rows once (80000 rows of 1027 bf16
+        // values 61 us, a stretch a warp 76)
+        const int64_t warps = 4 * int64_t(c.sms) * kCombineCtasPerSm * kWarps;
+        const uint32_t shares = uint32_t(std::min<int64_t>(stretches, (warps + tokens - 1) / tokens));
+        const uint32_t per = (stretches + shares - 1) / shares;
+        const int64_t items = tokens * ((stretches + per - 1) / per);
+        return launch_after(kernel, grid_of((items + kWarps - 1) / kWarps, c), kThreads, 0, stream, static_cast<const T*>(rows.p), rows.stride, tokens, k, int32_t(tokens * k),
+                            uint32_t(len), slots, weights, static_cast<T*>(out), out_stride, stretches, per, (stretches + per - 1) / per, items);
     };
-    // Short vectors go several at a time from two rows (12297 rows of 1027 bf16 values: 22 us with two from four rows); fewer where a
-    // row has no more.
-    constexpr int kMany = V * sizeof(T) >= 16 ? 2 : 8;
-    return len > 32 * V ? go(combine_kernel<T, V, kMany, 8 / kMany>, kMany) : go(combine_kernel<T, V, 1, 4>, 1);
+    // Short vectors go several at a time, fewer where a row has no more: 12297 rows of 1027 bf16 values take 22 us with two a row.
+    constexpr int kMany = V * sizeof(T) >= 16 ? 2 : V * sizeof(T) == 8 ? 4 : 8;
+    return len > 32 * V ? go(combine_kernel<T, V, kMany, 4>, kMany) : go(combine_kernel<T, V, 1, 4>, 1);
 }
 
 template <typename T, int V>

@@ -5,6 +5,7 @@
 // 1.75 * 2^8) and 2^(e - 7) else, so dividing by it is exact and codes have the one rounding of their conversion.
 #include <algorithm>
 
+#include "copy_any.cuh"
 #include "experts_device.cuh"
 
 namespace tide {
@@ -44,7 +45,7 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Eight consecutive values of a row as they lie in memory, zeros behind `left` of them; and what a power of two, or one for
+// Eight consecutive values of a row as they lie in memory, zeros behind `left` of them (load: 16-byte vectors, all or none); and what a power of two, or one for
 // each, times them looks like in that type.
 template <typename T>
 struct Eight;
@@ -53,16 +54,24 @@ struct Eight<__nv_bfloat16> {
     using Factor = uint16_t;  // a power of two, as bf16
     uint4 w;
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-    template <bool Vector>
     __device__ __forceinline__ void load(const __nv_bfloat16* p, int left) {
-        if constexpr (Vector) {
-            zero();
-            if (left > 0) w = __ldcg(reinterpret_cast<const uint4*>(p));
-        } else {
-            uint32_t h[8];
+        zero();
+        if (left > 0) w = __ldcg(reinterpret_cast<const uint4*>(p));
+    }
+    // Out of the aligned 16 bytes that hold them; what lies beside the row there is of the same allocation. (Element by element 80000
+    // rows of 1027 take 134 us in both forms, so 113.)
+    __device__ __forceinline__ void load_shifted(const __nv_bfloat16* p, int left) {
+        zero();
+        if (left <= 0) return;
+        const unsigned off = unsigned(reinterpret_cast<uintptr_t>(p)) & 15;
+        const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
+        const uint4 a = __ldcg(from), b = off + 2 * min(left, 8) > 16 ? __ldcg(from + 1) : make_uint4(0, 0, 0, 0);
+        w = off ? bytes_at(a, b, off) : a;
+        if (left < 8) {
+            uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[j] = j < left ? uint32_t(__ldcg(reinterpret_cast<const uint16_t*>(p) + j)) : 0u;
-            w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+            for (int i = 0; i < 4; ++i) v[i] = 2 * i + 1 < left ? v[i] : 2 * i < left ? v[i] & 0xffffu : 0u;
+            w = make_uint4(v[0], v[1], v[2], v[3]);
         }
     }
     // The largest magnitude, as fp32 bits.
@@ -104,18 +113,16 @@ struct Eight<float> {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = 0.0f;
     }
-    template <bool Vector>
     __device__ __forceinline__ void load(const float* p, int left) {
-        if constexpr (Vector) {
-            zero();
-            if (left > 0) {
-                const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
-                x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = j < left ? __ldcg(p + j) : 0.0f;
+        zero();
+        if (left > 0) {
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
         }
+    }
+    __device__ __forceinline__ void load_shifted(const float* p, int left) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = j < left ? __ldcg(p + j) : 0.0f;
     }
     __device__ __forceinline__ uint32_t largest() const {
         uint32_t a = 0;
@@ -154,7 +161,8 @@ __device__ __forceinline__ uint2 codes_of(const Eight<T>& x) {
 // ---- the tokens' rows to where their pairs go, in 8 bits ----------------------------------------
 //
 // A warp takes a token and 512 columns: 16 columns a lane, so that eight lanes have a block and each stores its codes as
-// one vector.  The row is read and converted once and written for each pair.
+// one vector.  The row is read and converted once and written for each pair. Rows without alignment are read as aligned words
+// (20000 rows of 1027 bf16 values to four places each 32 us, element by element 39).
 //
 // Bound by HBM writes: 65536 rows of 2048 bf16 values to eight places each in 204 us, 6.6 TB/s (242 with eight CTAs an SM that go
 // round: those that come late even out the end).
@@ -168,8 +176,10 @@ dispatch_fp8_kernel(const T* src, int64_t src_stride, int64_t tokens, int k, int
         const int64_t t = it / stretches;
         const uint32_t col = uint32_t(it - t * stretches) * 512 + lane * 16;
         Eight<T> a, b;
-        a.template load<Vector>(src + t * src_stride + col, int(len) - int(col));
-        b.template load<Vector>(src + t * src_stride + col + 8, int(len) - int(col) - 8);
+        const T* from = src + t * src_stride + col;
+        const int left = int(len) - int(col);
+        if constexpr (Vector) a.load(from, left), b.load(from + 8, left - 8);
+        else a.load_shifted(from, left), b.load_shifted(from + 8, left - 8);
         const int32_t slot = lane < k ? load_here(slots + t * k + lane) : -1;
         unsigned held = __ballot_sync(kFull, uint32_t(slot) < uint32_t(M));
         uint32_t largest = max(a.largest(), b.largest());
@@ -218,15 +228,15 @@ struct TileSmem {
     __align__(16) unsigned char turned[kBlock * kBlock];
 };
 
-template <typename T>
-__device__ __forceinline__ void load_tile(Eight<T> (&x)[8], const TileSmem<T>& sm, uint32_t col, uint32_t len, bool vector) {
+template <bool Vector, typename T>
+__device__ __forceinline__ void load_tile(Eight<T> (&x)[8], const TileSmem<T>& sm, uint32_t col, uint32_t len) {
     const int row0 = (threadIdx.x >> 4) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const T* p = reinterpret_cast<const T*>(sm.row_at[row0 + i]);
         const int left = p ? int(len) - int(col) : 0;
-        if (vector) x[i].template load<true>(p + col, left);
-        else x[i].template load<false>(p + col, left);
+        if constexpr (Vector) x[i].load(p + col, left);
+        else x[i].load_shifted(p + col, left);
     }
 }
 
@@ -284,10 +294,9 @@ struct QuantizeArgs {
     const int32_t* tokens;
     TileOut out;
     uint32_t across;  // tiles of a row of tiles
-    int vector;
 };
 
-template <typename T>
+template <typename T, bool Vector>
 __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<T>) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
     __shared__ TileSmem<T> sm;
     __shared__ int32_t starts[TIDE_MAX_EXPERTS + 1];  // row tiles before each expert
@@ -312,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<T>) quantize_kernel(c
         }
         __syncthreads();
         Eight<T> x[8];
-        load_tile(x, sm, col, a.len, a.vector);
+        load_tile<Vector>(x, sm, col, a.len);
         if (a.out.has_rows) {
             uint32_t m[8];
 #pragma unroll
@@ -365,9 +374,9 @@ struct GatherArgs {
     int has_wt;
     uint32_t across, down;  // tiles of a matrix
     int64_t tiles;
-    int vector;
 };
 
+template <bool Vector>
 __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<__nv_bfloat16>) all_gather_fp8_kernel(const __grid_constant__ GatherArgs a) {
     __shared__ TileSmem<__nv_bfloat16> sm;
     __shared__ uint32_t of_warp[kWarps];
@@ -387,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<__nv_bfloat16>) all_g
         }
         __syncthreads();
         Eight<__nv_bfloat16> x[8];
-        load_tile(x, sm, col, a.tv.len, a.vector);
+        load_tile<Vector>(x, sm, col, a.tv.len);
         uint32_t largest = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) largest = max(largest, x[i].largest());
@@ -445,9 +454,10 @@ cudaError_t launch_quantize(const RowsView& src, int bf16, int64_t src_rows, int
     if (rows) a.out.rows = *rows;
     if (columns) a.out.columns = *columns;
     a.across = uint32_t((len + kBlock - 1) / kBlock);
-    a.vector = vectors(reinterpret_cast<uintptr_t>(src.p), src.stride, src_rows, len, bf16 ? 2 : 4);
+    const bool v = vectors(reinterpret_cast<uintptr_t>(src.p), src.stride, src_rows, len, bf16 ? 2 : 4);
     const int64_t tiles = padded_blocks(M, E) * a.across;
-    return launch_after(bf16 ? quantize_kernel<__nv_bfloat16> : quantize_kernel<float>, grid_of(tiles, c, int64_t(c.sms) * (bf16 ? kTileCtasPerSm<__nv_bfloat16> : kTileCtasPerSm<float>)), kThreads, 0, stream, a);
+    auto* kernel = bf16 ? (v ? quantize_kernel<__nv_bfloat16, true> : quantize_kernel<__nv_bfloat16, false>) : (v ? quantize_kernel<float, true> : quantize_kernel<float, false>);
+    return launch_after(kernel, grid_of(tiles, c, int64_t(c.sms) * (bf16 ? kTileCtasPerSm<__nv_bfloat16> : kTileCtasPerSm<float>)), kThreads, 0, stream, a);
 }
 
 cudaError_t launch_all_gather_fp8(const ShardPtrs& shards, const TableView& tv, int E, const ExpertParams& ps, const tide_fp8_t& w, const tide_fp8_t* wt, const Ctas& c,
@@ -457,9 +467,9 @@ cudaError_t launch_all_gather_fp8(const ShardPtrs& shards, const TableView& tv, 
     if (wt) a.wt = *wt;
     a.across = (tv.len + kBlock - 1) / kBlock, a.down = (tv.rows + kBlock - 1) / kBlock;
     a.tiles = int64_t(E) * a.across * a.down;
-    a.vector = vectors(shards.bits, 0, 1, tv.len, 2);
-    for (int e = 0; e < E; ++e) a.vector &= ps.off[e] % 8 == 0;
-    return launch_after(all_gather_fp8_kernel, grid_of(a.tiles, c, INT32_MAX), kThreads, 0, stream, a);
+    bool v = vectors(shards.bits, 0, 1, tv.len, 2);
+    for (int e = 0; e < E; ++e) v &= ps.off[e] % 8 == 0;
+    return launch_after(v ? all_gather_fp8_kernel<true> : all_gather_fp8_kernel<false>, grid_of(a.tiles, c, INT32_MAX), kThreads, 0, stream, a);
 }
 
 }  // namespace tide
