@@ -29,9 +29,7 @@ constexpr int kAnyThreads = 32 * (4 + kSumWarps);
 constexpr int kTmemCols = 512;
 constexpr int kStatusWait = 1, kStatusScale = 2;
 
-// A CTA's share of a stage: 128 rows of A and its part of B's BN, half of them where two CTAs work on one tile.
-__host__ __device__ constexpr int share_bytes(int bn, bool pair) { return (kTileM + (pair ? bn / 2 : bn)) * kBlock; }
-__host__ __device__ constexpr int stages_of(int bn, bool pair) { return 196608 / share_bytes(bn, pair); }
+constexpr int kRingBytes = 196608, kMostStages = 11;
 
 struct ProductArgs {
     CUtensorMap a, b;
@@ -42,7 +40,7 @@ struct ProductArgs {
     int transposed;
     const int32_t* offsets;
     int32_t M, E;
-    int32_t a_box;  // rows of A that a copy brings: fewer than 128 where there are no more (8 rows of 2048 by 1536 columns of 128 experts 9.6 us, 11.2)
+    int32_t a_box;  // rows of A that a copy brings, a multiple of 8: fewer than 128 where there are no more
     int32_t N, K;  // columns of the result, blocks' length in all (product only)
     int32_t rows;  // rows of the result (gradient only)
     int32_t most_blocks;  // of the transposed operands (gradient only)
@@ -52,6 +50,19 @@ struct ProductArgs {
     int bulk;         // the result can be written by TMA
     int out_vectors;  // and 16 bytes of a row at a time
     WaitArgs wait;
+};
+// The ring of stages. A CTA's share of a stage is the rows of A that a copy brings and its part of B's BN, half of them where two CTAs
+// work on one tile. Where A has few rows in all, more stages fit (products read 128 rows there all the same, those behind
+// A's being B's): 8 rows of 2048 by 1536 columns of 128 experts take 9.6 us with six stages.
+template <int BN, bool Pair>
+struct Ring {
+    int share, stages;
+    __device__ __forceinline__ explicit Ring(const ProductArgs& p) {
+        share = (Pair ? kTileM + BN / 2 : p.a_box + BN) * kBlock;
+        stages = Pair ? kRingBytes / ((kTileM + BN / 2) * kBlock) : min(kMostStages, kRingBytes / share);
+    }
+    // Where B's rows begin in a stage.
+    __device__ __forceinline__ int b_at(const ProductArgs& p) const { return (Pair ? kTileM : p.a_box) * kBlock; }
 };
 struct GradArgs : ProductArgs {
     GradPtrs grads;
@@ -280,7 +291,8 @@ struct Tiles {
 template <int BN, bool Pair, bool Grad, typename Tiles>
 __device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles& tiles, int rank, int64_t begin, int64_t step, unsigned char* ring, uint64_t* full, uint64_t* empty,
                                            const Waits& wait) {
-    constexpr int kShare = share_bytes(BN, Pair), kStages = stages_of(BN, Pair);
+    const Ring<BN, Pair> r(p);
+    const int b_at = r.b_at(p);
     Cursor s;
     int64_t uses = 0;
     bool ok = true;
@@ -290,24 +302,24 @@ __device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles& ti
         const int row = t.row0 + rank * kTileM, col = t.col0 + rank * (BN / 2);
         for (int b = 0; b < t.blocks; ++b) {
             if (!(ok = __all_sync(kFull, wait(&empty[s.at], s.phase ^ 1)))) break;
-            unsigned char* a = ring + s.at * kShare;
+            unsigned char* a = ring + s.at * r.share;
             if (elected()) {
-                if (rank == 0) barrier_expect(&full[s.at], (Pair ? 2 : 1) * (kShare - (kTileM - p.a_box) * kBlock));
+                if (rank == 0) barrier_expect(&full[s.at], Pair ? 2 * (p.a_box + BN / 2) * kBlock : r.share);
                 load_2d<Pair>(a, &p.a, t.k0 + b * kBlock, row, &full[s.at]);
-                if (Grad) load_2d<Pair>(a + kTileM * kBlock, &p.b, t.k0 + b * kBlock, col, &full[s.at]);
-                else load_3d<Pair>(a + kTileM * kBlock, &p.b, b * kBlock, col, t.e, &full[s.at]);
+                if (Grad) load_2d<Pair>(a + b_at, &p.b, t.k0 + b * kBlock, col, &full[s.at]);
+                else load_3d<Pair>(a + b_at, &p.b, b * kBlock, col, t.e, &full[s.at]);
             }
             __syncwarp();
-            s.next(kStages);
+            s.next(r.stages);
             ++uses;
         }
     }
     // No copy, and no arrival of the products that read it, is left on its way to this CTA's memory. One that was
     // stopped waits for its copies alone: 20 ms, or until they are counted as landed where the barrier is its own.
     const bool all = ok && !*wait.stop;
-    for (int64_t u = max(int64_t(0), uses - kStages); u < uses; ++u) {
-        const int at = int(u % kStages);
-        const uint32_t parity = uint32_t(u / kStages) & 1;
+    for (int64_t u = max(int64_t(0), uses - r.stages); u < uses; ++u) {
+        const int at = int(u % r.stages);
+        const uint32_t parity = uint32_t(u / r.stages) & 1;
         const uint64_t end = globaltimer() + (all ? p.wait.timeout_ns : 20000000ull);
         while (!((all || rank == 0) && barrier_try(all ? &empty[at] : &full[at], parity)) && globaltimer() < end) {
         }
@@ -417,8 +429,11 @@ __device__ __forceinline__ void put_sums_staged(const ArgsOf<Grad>& p, unsigned 
 // and half of B's, the first one's MMA thread multiplies for both, and each takes out its own rows. An SM's shared memory then
 // takes in and gives out 32 KB each for 512 cycles of products, of the 128 bytes a cycle that it has for both; a tile of
 // 128 x 256 of its own needs 48 KB each, 768 cycles.
-constexpr int kExponentCols = 480;  // from here on; four blocks' take 4 + 8, two such groups' lie there
-constexpr int kAhead = 4;           // blocks in a word
+constexpr int kAhead = 4;  // blocks in a word
+// Groups of four blocks whose exponents lie there at once, and from which column on: of a wide tile 2 of 4 + 8 columns, of a narrow one,
+// whose groups are short, 8 of 4 + 4.
+__host__ __device__ constexpr int exponent_groups(int bn) { return bn == 256 ? 2 : 8; }
+__host__ __device__ constexpr int exponent_column(int bn) { return bn == 256 ? 480 : 256; }
 __host__ __device__ constexpr int exponent_words(int bn) { return (bn + 127) / 128 * 4; }  // of B for each lane
 __host__ __device__ constexpr int exponent_bytes(int bn) { return 512 + 128 * exponent_words(bn); }
 __host__ __device__ constexpr int second_tile(int bn) { return bn == 256 ? 224 : bn; }  // column of the other tile's sums
@@ -433,19 +448,21 @@ __device__ __forceinline__ bool no_power(float scale) {
     return (bits & 0x807fffffu) != 0 ? (bits & 0x7fffffffu) <= 0x7f800000u : bits == 0;
 }
 
-// The exponents of A's rows, 128 from `row0` of the tile on, or of B's BN: one warp writes every other group of four blocks, those of
-// buffer `which`. What a lane loads of a group:
+// The exponents of A's rows, 128 from `row0` of the tile on, or of B's BN: one warp writes every other group of four blocks, the even or
+// odd ones as `which` says. What a lane loads of a group, while it writes the one before:
 //   a product's A: the four blocks of rows lane, lane + 32, lane + 64 and lane + 96, v[i];
 //   a product's B: the four blocks of 32 columns, which have one scale: v[0] of lane i those of columns 32*i on;
 //   a gradient's: rows 4*lane to 4*lane + 3, and these + 128, of block q, v[q] and v[4 + q].
 // Per group it takes 4 to 8 loads and some 60 instructions: with a load for each scale, and their addresses, the writers, not the
 // products, bounded the gradient (438 us for 187).
-template <int BN, bool Grad, bool OfA, typename Tiles>
-__device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tiles& tiles, int row0, int which, int64_t begin, int64_t step, unsigned char* to, uint64_t* full,
-                                                uint64_t* empty, bool pair, const Waits& wait) {
+template <int BN, bool Pair, bool Grad, bool OfA, bool Vectors, typename Tiles>
+__device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tiles& tiles, int row0, int which, int64_t begin, int64_t step, unsigned char* exponents, uint64_t* full,
+                                                uint64_t* empty, const Waits& wait) {
     constexpr int kWords = OfA ? 4 : exponent_words(BN), kSets = kWords / 4, kLoads = Grad ? 4 * kSets : OfA ? 4 : 1;
     const int lane = threadIdx.x & 31;
-    uint32_t phase = 0, before = 0;  // groups before the tile
+    uint32_t before = 0;  // groups before the tile
+    Cursor buffer;
+    buffer.at = which;
     bool bad = false;
     for (int64_t it = begin; it < tiles.count; it += step) {
         const Tile t = tiles.at(it);
@@ -454,7 +471,6 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
         if (own >= groups) continue;
         const int from = (OfA ? t.row0 : t.col0) + row0, end = OfA ? t.rows_end : p.N;
         const int64_t stride = OfA ? p.a_scale_stride : p.b_scale_stride;
-        const bool vectors = p.scale_vectors && (Grad || OfA || !p.transposed);
         // rows past the last read the last one's, or what lies in the same 16 bytes
         const float* at[Grad ? kSets : kLoads];
 #pragma unroll
@@ -466,26 +482,25 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
                 at[i] = p.b_scales + t.e * p.b_scale_batch + (p.transposed ? n : n * stride);
             }
         }
-        float4 v[kLoads];
-        auto load = [&](int g) {
+        auto load = [&](float4 (&v)[kLoads], int g) {
+            if (g >= groups) return;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 if (Grad) {
                     const float* x = at[i / 4] + min(kAhead * g + i % 4, t.blocks - 1) * stride;
                     const int left = end - 1 - min(from + 4 * lane + 128 * (i / 4), (end - 1) & ~3);
-                    if (vectors) v[i] = *reinterpret_cast<const float4*>(x);
+                    if constexpr (Vectors) v[i] = *reinterpret_cast<const float4*>(x);
                     else v[i] = make_float4(x[0], x[min(1, left)], x[min(2, left)], x[min(3, left)]);
                 } else {
                     const int b = kAhead * g, last = t.blocks - 1;
                     const int64_t each = OfA || !p.transposed ? 1 : stride;
-                    if (vectors) v[i] = *reinterpret_cast<const float4*>(at[i] + b);
+                    if constexpr (Vectors) v[i] = *reinterpret_cast<const float4*>(at[i] + b);
                     else v[i] = make_float4(at[i][b * each], at[i][min(b + 1, last) * each], at[i][min(b + 2, last) * each], at[i][min(b + 3, last) * each]);
                 }
             }
         };
         const bool look = OfA ? t.col0 == 0 : t.row0 == (Grad ? 0 : tiles.first[t.e]);
-        load(own);
-        for (int g = own; g < groups; g += 2) {
+        auto write = [&](float4 (&v)[kLoads], int g) {
             uint32_t w[kWords];
             if (Grad) {
 #pragma unroll
@@ -513,9 +528,9 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
                         bad |= row < end && block < t.blocks && no_power(x[j]);
                     }
                 }
-            if (g + 2 < groups) load(g + 2);
-            if (!__all_sync(kFull, wait(empty, phase ^ 1))) return;
-            phase ^= 1;
+            load(v, g + 2);
+            if (!__all_sync(kFull, wait(&empty[buffer.at], buffer.phase ^ 1))) return false;
+            unsigned char* const to = exponents + buffer.at * exponent_bytes(BN);
             if (Grad) {
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) {
@@ -528,11 +543,15 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) {
-                if (pair) arrive_at_first<true>(full);
-                else arrive_at_first<false>(full);
-            }
-        }
+            if (lane == 0) arrive_at_first<Pair>(&full[buffer.at]);
+            buffer.next(exponent_groups(BN));
+            buffer.next(exponent_groups(BN));
+            return true;
+        };
+        float4 x[kLoads];
+        load(x, own);
+        for (int g = own; g < groups; g += 2)
+            if (!write(x, g)) return;
     }
     if (bad) atomicCAS(p.wait.status, 0, kStatusScale);
 }
@@ -547,14 +566,14 @@ __device__ __forceinline__ void both_ctas() {
 
 template <int BN, bool Pair, bool Grad, typename Out>
 __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const __grid_constant__ ArgsOf<Grad> p) {
-    constexpr int kChunks = BN / 32, kFirstHalf = (kChunks + 1) / 2, kStages = stages_of(BN, Pair), kShare = share_bytes(BN, Pair);
+    constexpr int kChunks = BN / 32, kFirstHalf = (kChunks + 1) / 2, kExponentGroups = exponent_groups(BN), kGroupCols = 4 + exponent_words(BN);
     constexpr int kCtas = Pair ? 2 : 1;
     constexpr bool kShared = second_tile(BN) < BN;
     extern __shared__ unsigned char dynamic_smem[];
     unsigned char* const ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic_smem) + 1023) & ~uintptr_t(1023));
-    unsigned char* const staging = ring + kStages * kShare;
+    unsigned char* const staging = ring + kRingBytes;
     unsigned char* const exponents = staging + kSumWarps * kStagingBytes;
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], scales_full[2], scales_empty[2], ready[2], drained[2], taken, ended;
+    __shared__ __align__(8) uint64_t full[kMostStages], empty[kMostStages], scales_full[kExponentGroups], scales_empty[kExponentGroups], ready[2], drained[2], taken, ended;
     __shared__ uint32_t tmem_at;
     __shared__ int stopped;
     __shared__ int32_t starts[TIDE_MAX_EXPERTS + 1], first[TIDE_MAX_EXPERTS + 1], sums[32];
@@ -563,8 +582,9 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
     const int64_t begin = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
-        for (int i = 0; i < 2; ++i) barrier_init(&scales_full[i], 2 * kCtas), barrier_init(&scales_empty[i], 1), barrier_init(&ready[i], 1);
+        for (int s = 0; s < kMostStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
+        for (int i = 0; i < kExponentGroups; ++i) barrier_init(&scales_full[i], 2 * kCtas), barrier_init(&scales_empty[i], 1);
+        for (int i = 0; i < 2; ++i) barrier_init(&ready[i], 1);
         for (int i = 0; i < 2; ++i) barrier_init(&drained[i], kSumWarps * kCtas);
         barrier_init(&taken, kSumWarps / 2 * kCtas), barrier_init(&ended, 1);
         stopped = 0;
@@ -591,6 +611,9 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
         load_tiles<BN, Pair, Grad>(p, tiles, rank, begin, step, ring, full, empty, wait);
     } else if (warp == 1) {
         if (rank == 0) {
+            const Ring<BN, Pair> r(p);
+            const int b_at = r.b_at(p);
+            const uint64_t first_a = tile_descriptor(ring);
             Cursor s, g;
             uint32_t tile = 0;
             bool ok = true;
@@ -604,49 +627,53 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
                 // the tile before the last has been taken out, and of the last the columns that it shares
                 if (!(ok = tile < 2 || __all_sync(kFull, wait(&drained[tile & 1], ((tile >> 1) - 1) & 1)))) break;
                 if (kShared && !(ok = tile == 0 || __all_sync(kFull, wait(&taken, (tile - 1) & 1)))) break;
-                uint32_t a_scales = 0, b_scales = 0;
-                for (int b = 0; b < blocks; ++b) {
-                    const uint32_t in = b % kAhead;
-                    if (in == 0) {
-                        if (!(ok = __all_sync(kFull, wait(&scales_full[g.at], g.phase)))) break;
-                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const unsigned char* x = exponents + g.at * exponent_bytes(BN);
-                        a_scales = tmem + kExponentCols + g.at * 12, b_scales = a_scales + 4;
-                        if (elected()) {
-                            copy_exponents<Pair>(a_scales, x);
-#pragma unroll
-                            for (int i = 0; i < exponent_words(BN) / 4; ++i) copy_exponents<Pair>(b_scales + 4 * i, x + 512 * (1 + i));
-                            commit<Pair>(&scales_empty[g.at]);
-                        }
-                        __syncwarp();
-                        g.next(2);
-                    }
-                    if (!(ok = __all_sync(kFull, wait(&full[s.at], s.phase)))) break;
+                for (int b0 = 0; ok && b0 < blocks; b0 += kAhead) {
+                    if (!(ok = __all_sync(kFull, wait(&scales_full[g.at], g.phase)))) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const unsigned char* a = ring + s.at * kShare;
-                    const uint64_t da = tile_descriptor(a), db = tile_descriptor(a + kTileM * kBlock);
-                    const uint32_t instruction = scaled_instruction(BN, Pair) | in << 29 | in << 4;
+                    const unsigned char* x = exponents + g.at * exponent_bytes(BN);
+                    const uint32_t a_scales = tmem + exponent_column(BN) + g.at * kGroupCols, b_scales = a_scales + 4;
                     if (elected()) {
+                        copy_exponents<Pair>(a_scales, x);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) multiply_scaled<Pair>(to, da + 2 * k, db + 2 * k, instruction, a_scales, b_scales, b > 0 || k > 0);
-                        commit<Pair>(&empty[s.at]);
-                        if (b + 1 == blocks) commit<Pair>(&ready[tile & 1]);
+                        for (int i = 0; i < exponent_words(BN) / 4; ++i) copy_exponents<Pair>(b_scales + 4 * i, x + 512 * (1 + i));
+                        commit<Pair>(&scales_empty[g.at]);
                     }
                     __syncwarp();
-                    s.next(kStages);
+                    g.next(kExponentGroups);
+#pragma unroll
+                    for (int q = 0; q < kAhead; ++q) {
+                        const int b = b0 + q;
+                        if (b >= blocks) break;
+                        if (!(ok = __all_sync(kFull, wait(&full[s.at], s.phase)))) break;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const uint64_t da = first_a + uint32_t(s.at * r.share >> 4), db = da + uint32_t(b_at >> 4);
+                        const uint32_t instruction = scaled_instruction(BN, Pair) | uint32_t(q) << 29 | uint32_t(q) << 4;
+                        if (elected()) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) multiply_scaled<Pair>(to, da + 2 * k, db + 2 * k, instruction, a_scales, b_scales, b > 0 || k > 0);
+                            commit<Pair>(&empty[s.at]);
+                            if (b + 1 == blocks) commit<Pair>(&ready[tile & 1]);
+                        }
+                        __syncwarp();
+                        s.next(r.stages);
+                    }
                     // the next tile is found while this one's products wait for their turn
-                    if (b == 0) next = it + step < tiles.count ? tiles.at(it + step).blocks : 0;
+                    if (b0 == 0) next = it + step < tiles.count ? tiles.at(it + step).blocks : 0;
                 }
                 ++tile;
             }
             if (!ok) end_products<Pair>(&ended);
         }
     } else if (warp < 4 || warp >= 4 + kSumWarps) {
-        // warps 2 and 3 write A's and B's exponents into the first buffer, the last two into the second
-        const int which = warp >= 4;
-        unsigned char* const to = exponents + which * exponent_bytes(BN);
-        if ((warp & 1) == 0) write_exponents<BN, Grad, true>(p, tiles, rank * kTileM, which, begin, step, to, &scales_full[which], &scales_empty[which], Pair, wait);
-        else write_exponents<BN, Grad, false>(p, tiles, 0, which, begin, step, to + 512, &scales_full[which], &scales_empty[which], Pair, wait);
+        // warps 2 and 3 write A's and B's exponents of every other group, the last two of the others
+        const bool vectors = p.scale_vectors && (Grad || (warp & 1) == 0 || !p.transposed);
+        if ((warp & 1) == 0) {
+            if (vectors) write_exponents<BN, Pair, Grad, true, true>(p, tiles, rank * kTileM, warp >= 4, begin, step, exponents, scales_full, scales_empty, wait);
+            else write_exponents<BN, Pair, Grad, true, false>(p, tiles, rank * kTileM, warp >= 4, begin, step, exponents, scales_full, scales_empty, wait);
+        } else {
+            if (vectors) write_exponents<BN, Pair, Grad, false, true>(p, tiles, 0, warp >= 4, begin, step, exponents + 512, scales_full, scales_empty, wait);
+            else write_exponents<BN, Pair, Grad, false, false>(p, tiles, 0, warp >= 4, begin, step, exponents + 512, scales_full, scales_empty, wait);
+        }
     } else {
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const int first_col = half * kFirstHalf * 32, chunks = half ? kChunks - kFirstHalf : kFirstHalf;
@@ -669,14 +696,12 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
             // the columns that the next tile's sums share come first: of the first buffer the last, of the second the first
             const bool backwards = kShared && !(tile & 1);
             const bool holds = kShared && half == int(backwards);
-            uint32_t x[2][32];
+            uint32_t x[32];
             auto column = [&](int c) { return (backwards ? chunks - 1 - c : c) * 32; };
-            load_sums(x[0], at + column(0));
-#pragma unroll
-            for (int c = 0; c < kFirstHalf; ++c) {
-                if (c >= chunks) break;
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                load_sums(x, at + column(c));
                 sums_loaded();
-                if (c + 1 < chunks) load_sums(x[(c + 1) & 1], at + column(c + 1));
                 if ((holds && c == 0) || c + 1 == chunks) {
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     if (lane == 0) {
@@ -684,7 +709,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
                         if (c + 1 == chunks) arrive_at_first<Pair>(&drained[tile & 1]);
                     }
                 }
-                put_sums_staged<Grad, Out>(p, mine, x[c & 1], t.e, row0, rows, col + column(c));
+                put_sums_staged<Grad, Out>(p, mine, x, t.e, row0, rows, col + column(c));
             }
             ++tile;
         }
@@ -709,10 +734,10 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
 // buffer. No sum of more than 128 products is formed before its scale is applied.
 template <int BN, bool Grad, typename Out>
 __global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid_constant__ ArgsOf<Grad> p) {
-    constexpr int kBuffers = kTmemCols / BN, kHalf = BN / 2, kChunks = kHalf / 32, kStages = stages_of(BN, false), kShare = share_bytes(BN, false);
+    constexpr int kBuffers = kTmemCols / BN, kHalf = BN / 2, kChunks = kHalf / 32;
     extern __shared__ unsigned char dynamic_smem[];
     unsigned char* const ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic_smem) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], ready[kBuffers], drained[kBuffers], ended;
+    __shared__ __align__(8) uint64_t full[kMostStages], empty[kMostStages], ready[kBuffers], drained[kBuffers], ended;
     __shared__ uint32_t tmem_at;
     __shared__ int stopped;
     __shared__ int32_t starts[TIDE_MAX_EXPERTS + 1], first[TIDE_MAX_EXPERTS + 1], sums[32];
@@ -720,7 +745,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
+        for (int s = 0; s < kMostStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
         for (int b = 0; b < kBuffers; ++b) barrier_init(&ready[b], 1), barrier_init(&drained[b], kSumWarps);
         barrier_init(&ended, 1);
         stopped = 0;
@@ -741,6 +766,8 @@ __global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid
     if (warp == 0) {
         load_tiles<BN, false, Grad>(p, tiles, 0, blockIdx.x, gridDim.x, ring, full, empty, wait);
     } else if (warp == 1) {
+        const Ring<BN, false> r(p);
+        const int b_at = r.b_at(p);
         Cursor s, d;
         bool ok = true;
         for (int64_t it = blockIdx.x; ok && it < tiles.count; it += gridDim.x) {
@@ -748,8 +775,8 @@ __global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid
             for (int b = 0; b < t.blocks; ++b) {
                 if (!(ok = __all_sync(kFull, wait(&drained[d.at], d.phase ^ 1) && wait(&full[s.at], s.phase)))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const unsigned char* a = ring + s.at * kShare;
-                const uint64_t da = tile_descriptor(a), db = tile_descriptor(a + kTileM * kBlock);
+                const unsigned char* a = ring + s.at * r.share;
+                const uint64_t da = tile_descriptor(a), db = tile_descriptor(a + b_at);
                 if (elected()) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) multiply(tmem + d.at * BN, da + 2 * k, db + 2 * k, plain_instruction(BN), k > 0);
@@ -757,7 +784,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid
                     commit<false>(&ready[d.at]);
                 }
                 __syncwarp();
-                s.next(kStages), d.next(kBuffers);
+                s.next(r.stages), d.next(kBuffers);
             }
         }
         if (!ok) end_products<false>(&ended);
@@ -888,7 +915,7 @@ int launch(const ArgsOf<Grad>& p, bool any_scales, int64_t most_tiles, const Cta
     void (*kernel)(ArgsOf<Grad>) = scaled_product_kernel<BN, Pair, Grad, Out>;
     if constexpr (!Pair)
         if (any_scales) kernel = any_scales_kernel<BN, Grad, Out>;
-    const int smem = stages_of(BN, Pair) * share_bytes(BN, Pair) + kSumWarps * kStagingBytes + 2 * exponent_bytes(BN) + 1024;
+    const int smem = kRingBytes + 1024 + (any_scales ? 0 : kSumWarps * kStagingBytes + exponent_groups(BN) * exponent_bytes(BN));
     TIDE_CUDA(allow_smem(reinterpret_cast<const void*>(kernel), smem, c.device, allowed[any_scales]));
     const int64_t at_once = (c.most ? c.most : c.sms) / (Pair ? 2 : 1);
     const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(most_tiles, at_once));
