@@ -11,6 +11,9 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// a / b where the quotient has 32 bits, as it nearly always can be had: a division of 64 bits takes some hundred instructions.
+__device__ __forceinline__ uint32_t quotient(int64_t a, uint32_t b) { return a <= int64_t(UINT32_MAX) ? uint32_t(a) / b : uint32_t(uint64_t(a) / b); }
+
 // v[0..n] = the sums of f(0..n-1) before each index, and their total at n; n <= 1024.  All of the block's
 // threads call it; `sums` is 32 words of shared memory.
 template <typename F>

@@ -185,7 +185,7 @@ dispatch_kernel(const Word* src, int64_t src_stride, int64_t T, int k, int32_t M
     const int lane = threadIdx.x & 31;
     wait_for_previous_kernel();
     for (int64_t it = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * kWarps) {
-        const int64_t t = it / stretches;
+        const int64_t t = quotient(it, stretches);
         const uint32_t col = uint32_t(it - t * stretches) * (32 * U) + lane;
         Word v[U];
 #pragma unroll
@@ -219,7 +219,7 @@ combine_kernel(const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_
     const int lane = threadIdx.x & 31;
     wait_for_previous_kernel();
     for (int64_t it = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * kWarps) {
-        const int64_t t = it / shares;
+        const int64_t t = quotient(it, shares);
         const uint32_t s0 = uint32_t(it - t * shares) * per, s1 = min(s0 + per, stretches);
         int32_t slot;
         const unsigned all = held_pairs(slots, t, k, M, lane, &slot);

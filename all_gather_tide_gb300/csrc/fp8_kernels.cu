@@ -173,7 +173,7 @@ dispatch_fp8_kernel(const T* src, int64_t src_stride, int64_t tokens, int k, int
     const int lane = threadIdx.x & 31;
     wait_for_previous_kernel();
     for (int64_t it = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * kWarps) {
-        const int64_t t = it / stretches;
+        const int64_t t = quotient(it, stretches);
         const uint32_t col = uint32_t(it - t * stretches) * 512 + lane * 16;
         Eight<T> a, b;
         const T* from = src + t * src_stride + col;
@@ -223,6 +223,7 @@ struct TileOut {
 template <typename T>
 struct TileSmem {
     uint64_t row_at[kBlock];                                     // where each row lies; 0: none
+    int32_t first, held;                                         // the tile's first row, and how many it has
     __align__(16) Eight<T> largest[kWarps][kBlock / 8];          // magnitudes of each column
     __align__(16) typename Eight<T>::Factor column[kBlock];      // what each column is multiplied by
     __align__(16) unsigned char turned[kBlock * kBlock];
@@ -306,11 +307,13 @@ __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<T>) quantize_kernel(c
     exclusive_sums(starts, a.E, sums, [&](int e) { return (span_of(a.offsets, e, a.M).count + kBlock - 1) / kBlock; });
     const int64_t tiles = int64_t(min(starts[a.E], a.most_blocks)) * a.across;
     for (int64_t it = blockIdx.x; it < tiles; it += gridDim.x) {
-        const int32_t down = int32_t(it / a.across), e = last_at_most(starts, a.E, down);
+        const int32_t down = int32_t(quotient(it, a.across));
         const uint32_t col0 = uint32_t(it - int64_t(down) * a.across) * kBlock, col = col0 + group * 8;
-        const Span span = span_of(a.offsets, e, a.M);
-        const int32_t s0 = span.first + (down - starts[e]) * kBlock, held = min(kBlock, span.first + span.count - s0);
         if (threadIdx.x < kBlock) {
+            const int e = last_at_most(starts, a.E, down);
+            const Span span = span_of(a.offsets, e, a.M);
+            const int32_t s0 = span.first + (down - starts[e]) * kBlock, held = min(kBlock, span.first + span.count - s0);
+            if (threadIdx.x == 0) sm.first = s0, sm.held = held;
             uint64_t at = 0;
             if (int(threadIdx.x) < held) {
                 int64_t row = s0 + threadIdx.x;
@@ -320,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<T>) quantize_kernel(c
             sm.row_at[threadIdx.x] = at;
         }
         __syncthreads();
+        const int32_t s0 = sm.first, held = sm.held;
         Eight<T> x[8];
         load_tile<Vector>(x, sm, col, a.len);
         if (a.out.has_rows) {
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<__nv_bfloat16>) all_g
     const int group = threadIdx.x & 15, warp = threadIdx.x >> 5;
     wait_for_previous_kernel();
     for (int64_t it = blockIdx.x; it < a.tiles; it += gridDim.x) {
-        const uint32_t each = a.across * a.down, e = uint32_t(it / each), in = uint32_t(it - int64_t(e) * each), down = in / a.across, across = in - down * a.across;
+        const uint32_t each = a.across * a.down, e = quotient(it, each), in = uint32_t(it - int64_t(e) * each), down = in / a.across, across = in - down * a.across;
         const uint32_t n0 = down * kBlock, col0 = across * kBlock, col = col0 + group * 8;
         const int held = int(min(uint32_t(kBlock), a.tv.rows - n0));
         if (threadIdx.x < kBlock) {

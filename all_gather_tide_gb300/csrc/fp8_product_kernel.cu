@@ -271,12 +271,12 @@ struct Tiles {
         Tile t;
         if (Grad) {
             const uint32_t each = across * down;
-            t.e = int(it / each);
+            t.e = int(quotient(it, each));
             const uint32_t in = uint32_t(it - int64_t(t.e) * each), d = in / across;
             t.row0 = int(d) * Rows, t.rows_end = p.rows, t.col0 = int(in - d * across) * BN;
             t.k0 = starts[t.e] * kBlock, t.blocks = starts[t.e + 1] - starts[t.e];
         } else {
-            const int32_t d = int32_t(it / across);
+            const int32_t d = int32_t(quotient(it, across));
             t.e = last_at_most(starts, p.E, d);
             t.row0 = first[t.e] + (d - starts[t.e]) * Rows;
             t.rows_end = first[t.e + 1];
