@@ -1141,6 +1141,8 @@ class Experts:
         """Rows in the experts' order in 8 bits: ``x`` ([T*k, D]), or with ``gather`` the tokens' rows ``x`` ([T, D]), as they are
         and/or transposed.  ``route`` may be None where one expert has all rows."""
         where = "quantize"
+        if x.dim() != 2:
+            _refuse(where, "rows are needed")
         n, D = x.shape
         M, offsets = self._all_rows(where, route, n)
         if gather and route is None:

@@ -113,7 +113,8 @@ int tide_experts_device_status(tide_experts_t x, int32_t* status) {
 
 int tide_experts_set_wait_timeout(tide_experts_t x, uint64_t timeout_ns) {
     if (!x) return TIDE_EINVAL;
-    x->timeout_ns = timeout_ns == 0 ? tide::kDefaultTimeoutNs : std::max(timeout_ns, tide::kMinTimeoutNs);
+    // half of what 64 bits hold at most: the kernels add it to the clock
+    x->timeout_ns = timeout_ns == 0 ? tide::kDefaultTimeoutNs : std::min(std::max(timeout_ns, tide::kMinTimeoutNs), UINT64_MAX / 2);
     return TIDE_OK;
 }
 

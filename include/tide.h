@@ -524,8 +524,8 @@ int tide_adamw(tide_tensors_t t, void *const *params, const void *const *grads, 
  * The calls that write them take for a block whose largest magnitude is a > 0 the smallest power of two
  * from 2^-126 to 2^120 with a / scale <= 448 (1 for a block of zeros), and code = x / scale rounded to
  * nearest even; a block with a NaN or an infinity gets a NaN scale.  The calls that read them take such scales,
- * which the tensor cores apply (another number counts as the power of two below it, and sets 2 in the status
- * word, if that holds 0), or with TIDE_FP8_ANY_SCALES any, at a lower rate.
+ * which the tensor cores apply (another number's magnitude counts as the power of two below it, and sets 2 in
+ * the status word, if that holds 0; an infinity counts as NaN), or with TIDE_FP8_ANY_SCALES any, at a lower rate.
  */
 #define TIDE_FP8_TRANSPOSED 0x1u
 #define TIDE_FP8_ANY_SCALES 0x2u
