@@ -357,8 +357,8 @@ __device__ __forceinline__ void put_sums(Out* to, const uint32_t (&x)[Count], in
 }
 
 // A warp's 32 rows of sums go to the result by way of 2 KB of shared memory, 64 bytes of each row at a time, in which 16-byte pieces
-// are swizzled as the tensor map says: whole boxes by TMA, others (an expert's last rows, results that TMA cannot address) row by
-// row. A lane's own stores would reach 32 lines an instruction: those of all eight warps bounded short products, and of two
+// are swizzled as the tensor map says: whole boxes by TMA, others (an expert's last rows, rows' odd ends, results that TMA cannot
+// address) row by row. A lane's own stores would reach 32 lines an instruction: those of all eight warps bounded short products, and of two
 // bytes each took 10 us for a tile.
 constexpr int kStagingBytes = 2048;  // a warp
 template <bool Grad, typename Out>
@@ -369,7 +369,8 @@ __device__ __forceinline__ void put_staged(const ArgsOf<Grad>& p, unsigned char*
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staging + lane * 64 + (i ^ (lane >> 1 & 3)) * 16) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    if (p.bulk && rows >= 32) {  // TMA writes whole boxes, so all of the rows have to be there
+    // TMA writes whole boxes, so all of the rows have to be there, and where it cuts a row's end it writes up to a multiple of 16 bytes
+    if (p.bulk && rows >= 32 && (col + kCols <= p.N || p.N % (16 / int(sizeof(Out))) == 0)) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {

@@ -435,6 +435,48 @@ def test_weight_gradients(tide, T, k, E, N, K, kind, any_scales):
     assert all(torch.equal(whole[e].cpu().flatten(), grads[e].cpu()) for e in range(E))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T, N", [(3, 1), (150, 331), (150, 515), (20000, 1003), (20000, 769)])
+def test_products_leave_what_lies_beside_their_rows(tide, T, N, kind):
+    """Results whose rows are aligned and not a multiple of 16 bytes long, in both tile shapes; an expert's last rows end inside a tile."""
+    E, k, K = 3, 2, 96
+    g = gen(N)
+    ex, route = routed(tide, E, k, draw_ids(g, T, k, E, 0.1))
+    held, offsets = int(route.offsets[-1]), route.offsets.cpu().tolist()
+    A, W = tide.Fp8Rows(T * k, K), tide.Fp8Weights(E, N, K)
+    random_fp8(g, A, False)
+    random_fp8(g, W, False)
+    out = torch.full((T * k, -(-N // 8) * 8 + 8), 55.0, device="cuda").to(TYPES[kind])
+    ex.matmul(A, W, route, out[:, :N])
+    got = out.cpu()
+    assert bool((got[held:] == 55).all()) and bool((got[:, N:] == 55).all())
+    a, w = values(A.codes.cpu().float().double(), A.scales.cpu().double()), W.codes.cpu().float().double() * W.scales.cpu().double().repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)[:, :, :K]
+    for e, (x, y) in enumerate(zip(offsets, offsets[1:])):
+        want, size = a[x:y] @ w[e].t(), a[x:y].abs() @ w[e].abs().t()
+        assert bool(((got[x:y, :N].double() - want).abs() <= bound(1, size) + HALF[kind] * want.abs() * 1.01).all()), e
+
+
+@pytest.mark.parametrize("any_scales", [False, True])
+@pytest.mark.parametrize("T", [100, 20000])
+def test_products_of_rows_with_nan_behind_their_ends(tide, T, any_scales):
+    """The bytes between a row's end and the next multiple of 16 are not a part of it."""
+    E, N, K = 2, 259, 397
+    g = gen(T)
+    ex, route = routed(tide, E, 1, draw_ids(g, T, 1, E, 0.0))
+    A, W = tide.Fp8Rows(T, K), tide.Fp8Weights(E, N, K)
+    for x in (A, W):
+        x.codes.view(torch.uint8).as_strided((x.codes[..., 0].numel(), 400), (400, 1)).fill_(0x7F)
+        random_fp8(g, x, any_scales)
+        assert bool((x.codes.view(torch.uint8).as_strided((x.codes[..., 0].numel(), 400), (400, 1))[:, K:] == 0x7F).all())
+    out = torch.empty(T, N, device="cuda")
+    ex.matmul(A, W, route, out, any_scales=any_scales)
+    offsets = route.offsets.cpu().tolist()
+    a, w = values(A.codes.cpu().float().double(), A.scales.cpu().double()), W.codes.cpu().float().double() * W.scales.cpu().double().repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)[:, :, :K]
+    for e, (x, y) in enumerate(zip(offsets, offsets[1:])):
+        want, size = a[x:y] @ w[e].t(), a[x:y].abs() @ w[e].abs().t()
+        assert bool(((out[x:y].cpu().double() - want).abs() <= bound(4, size) + HALF["f32"] * want.abs()).all()), e
+
+
 def test_a_product_of_all_rows_without_a_route(tide):
     """One expert: a plain linear layer's product and gradients."""
     g = gen(3)
@@ -566,6 +608,21 @@ class Layer:
 def test_a_layer_and_its_gradients(tide, T, k, E, N, K, R, flags):
     layer = Layer(tide, T, k, E, N, K, R, T, flags)
     layer.step()
+    layer.check()
+
+
+@pytest.mark.parametrize("T, k", [(40, 32), (9000, 2)])
+def test_a_layer_of_the_most_experts(tide, T, k):
+    layer = Layer(tide, T, k, 1024, 72, 136, 2, k)
+    layer.step()
+    layer.check()
+
+
+def test_the_longest_wait_limit(tide):
+    layer = Layer(tide, 300, 3, 7, 200, 264, 2, 11)
+    layer.ex.set_wait_timeout(2 ** 64 - 1)
+    for _ in range(20):
+        layer.step()
     layer.check()
 
 
