@@ -407,6 +407,27 @@ template <bool Grad, typename Out>
 __device__ __forceinline__ void put_sums_staged(const ArgsOf<Grad>& p, unsigned char* staging, const uint32_t (&x)[32], int e, int row0, int rows, int col) {
     constexpr int kCols = 64 / sizeof(Out);
     if (rows <= 0) return;
+    if constexpr (sizeof(Out) == 4) {
+        // 16 rows of 128 bytes at a time (64 bytes of 32 rows at a time, 120000 rows of 384 by 1203 columns take 247 us, so 170)
+        if (!p.out_vectors) {
+            const int lane = threadIdx.x & 31, here = min(rows, 32);
+            float* to = static_cast<float*>(result_of<Grad>(p, e)) + row0 * p.out_stride + col + lane;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                __syncwarp();
+                if (lane >> 4 == h)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(staging + (lane & 15) * 128 + (i ^ (lane & 7)) * 16) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                __syncwarp();
+                const unsigned char* const from = staging + (lane & 3) * 4;
+                const int left = col + lane < p.N ? here - 16 * h : 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i, to += p.out_stride)
+                    if (i < left) *to = *reinterpret_cast<const float*>(from + i * 128 + (lane >> 2 ^ (i & 7)) * 16);
+            }
+            return;
+        }
+    }
 #pragma unroll
     for (int c = 0; c < 32; c += kCols) {
         uint32_t w[16];
@@ -926,12 +947,17 @@ int launch(const ArgsOf<Grad>& p, bool any_scales, int64_t most_tiles, const Cta
 
 bool vectors16(const void* p, int64_t stride, int64_t rows, int elem) { return aligned(p, 16) && (rows <= 1 || stride * elem % 16 == 0); }
 
-// Whether `down` tiles of 128 rows by N columns go to pairs of CTAs, in tiles of 256 x 256: where these are many enough to keep all
-// SMs busy, and experts have rows enough to fill them. Else, and where sums go to registers, tiles are 128 x 128. (Pairs' tiles of
+// Whether `down` tiles of 128 rows by N columns, summed over `blocks` blocks, go to pairs of CTAs, in tiles of 256 x 256: where
+// experts have rows enough to fill them, and these are two rounds or more, or half of a round where sums are long, whose products
+// then count for more than a round that is not full (4096 rows of 2048 by 2048 columns of 4 experts 16.4 us, in tiles of 128 x 128
+// 24.5; 6000 of 512 by 1024 of 5 experts 9.8 and 9.0). Else tiles are 128 x 128: also where sums go to registers, and where taking
+// them out is what lasts, of up to four blocks in fp32 (131072 rows of 512 by 384 columns 46 us, by pairs 55), or eight in rows
+// without alignment (6000 of 1027 by 1003 columns 16 and 18). (Pairs' tiles of
 // 192 and 224 columns, whose sums share none with the next tile's, were slower at every length: 524288 rows of 2048 by 1536 columns
 // 1141 and 1122 us, with 256 1083; 131072 of 768 by 2048 195 and 296, with 256 180.)
-bool pairs(int64_t rows, int64_t down, int64_t N, bool any_scales, const Ctas& c) {
-    return !any_scales && c.most != 1 && rows >= 2 * kTileM && down * ((N + 255) / 256) >= 2 * c.sms;
+bool pairs(int64_t rows, int64_t down, int64_t N, int64_t blocks, bool bf16, bool vectors, bool any_scales, const Ctas& c) {
+    const int64_t tiles = down * ((N + 255) / 256);  // of 128 x 256
+    return !any_scales && c.most != 1 && rows >= 2 * kTileM && blocks > (bf16 ? -1 : vectors ? 4 : 8) && (tiles >= 2 * c.sms || (2 * tiles >= c.sms && blocks >= 8));
 }
 
 template <bool Grad>
@@ -949,7 +975,8 @@ int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets,
     ProductArgs p{};
     const bool any = flags & TIDE_FP8_ANY_SCALES;
     const int64_t down = padded_blocks(M, E);
-    const bool pair = pairs(M / E, down, N, any, c);
+    p.out_vectors = vectors16(out, out_stride, M, out_bf16 ? 2 : 4);
+    const bool pair = pairs(M / E, down, N, K / kBlock, out_bf16, p.out_vectors, any, c);
     p.a_box = int32_t(std::min<int64_t>(kTileM, (M + 7) / 8 * 8));
     int rc = describe(&p.a, a, K, M, 0, p.a_box);
     if (rc == TIDE_OK) rc = describe(&p.b, w, K, N, E, 128);
@@ -959,7 +986,7 @@ int launch_matmul(const tide_fp8_t& a, int64_t M, int E, const int32_t* offsets,
     // what such a vector holds behind a row's last scale is read and not used; it is of the same 16 bytes
     p.scale_vectors = aligned(a.scales, 16) && a.scale_stride % 4 == 0 && aligned(w.scales, 16) && w.scale_stride % 4 == 0 && (E == 1 || w.scale_batch % 4 == 0);
     p.offsets = offsets, p.M = int32_t(M), p.E = E, p.N = int32_t(N), p.K = int32_t(K), p.rows = 0;
-    p.out = out, p.out_stride = out_stride, p.out_vectors = vectors16(out, out_stride, M, out_bf16 ? 2 : 4);
+    p.out = out, p.out_stride = out_stride;
     p.wait = wait;
     if ((rc = describe_result(&p, out, out_bf16, N, M, out_stride, 0, 0)) != TIDE_OK) return rc;
     // `down` counts tiles of 128 rows; of 256 there are fewer
@@ -972,7 +999,9 @@ int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int
     const bool any = flags & TIDE_FP8_ANY_SCALES;
     const int64_t padded = std::max<int64_t>(1, padded_blocks(M, E)) * kBlock;
     const int64_t down = int64_t(E) * ((N + kTileM - 1) / kTileM);
-    const bool pair = pairs(N, down, K, any, c);
+    p.out_vectors = 1;
+    for (int e = 0; e < E; ++e) p.out_vectors &= vectors16(grads.p[e], K, N, grad_bf16 ? 2 : 4);
+    const bool pair = pairs(N, down, K, M / E / kBlock, grad_bf16, p.out_vectors, any, c);
     if (M > 0) {  // else there is nothing to sum
         int rc = describe(&p.a, dy, padded, N, 0, kTileM);
         if (rc == TIDE_OK) rc = describe(&p.b, a, padded, K, 0, 128);
@@ -985,8 +1014,6 @@ int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int
     p.scale_vectors = aligned(dy.scales, 16) && dy.scale_stride % 4 == 0 && aligned(a.scales, 16) && a.scale_stride % 4 == 0;
     p.offsets = offsets, p.M = int32_t(M), p.E = E, p.N = int32_t(K), p.rows = int32_t(N);
     p.grads = grads, p.out_stride = K;
-    p.out_vectors = 1;
-    for (int e = 0; e < E; ++e) p.out_vectors &= vectors16(grads.p[e], K, N, grad_bf16 ? 2 : 4);
     p.wait = wait;
     // gradients at one distance from each other are one array to TMA
     const int64_t pitch = E > 1 ? static_cast<const char*>(grads.p[1]) - static_cast<const char*>(grads.p[0]) : 0;

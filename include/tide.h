@@ -531,8 +531,9 @@ int tide_adamw(tide_tensors_t t, void *const *params, const void *const *grads, 
 #define TIDE_FP8_ANY_SCALES 0x2u
 typedef struct tide_fp8 {
     void *codes;          /* device, 16-byte aligned; the matrix's rows are `stride` bytes apart */
-    int64_t stride;       /* a multiple of 16, at least the row length; bytes behind a row's end in the last of
-                             its groups of 16 may be overwritten by calls that write rows */
+    int64_t stride;       /* a multiple of 16, at least the row length (products are fastest with multiples of
+                             128); bytes behind a row's end in the last of its groups of 16 may be overwritten
+                             by calls that write rows */
     int64_t batch;        /* bytes between the experts' matrices (weights only), a multiple of 16 */
     float *scales;        /* device; rows of ceil(row length / 128) scales `scale_stride` elements apart: one for
                              each row of the matrix, or for weights one for each 128 rows */

@@ -465,9 +465,10 @@ def test_products_of_rows_with_nan_behind_their_ends(tide, T, any_scales):
     ex, route = routed(tide, E, 1, draw_ids(g, T, 1, E, 0.0))
     A, W = tide.Fp8Rows(T, K), tide.Fp8Weights(E, N, K)
     for x in (A, W):
-        x.codes.view(torch.uint8).as_strided((x.codes[..., 0].numel(), 400), (400, 1)).fill_(0x7F)
+        whole = x.codes.view(torch.uint8).as_strided((x.codes[..., 0].numel(), x.codes.stride(-2)), (x.codes.stride(-2), 1))
+        whole.fill_(0x7F)
         random_fp8(g, x, any_scales)
-        assert bool((x.codes.view(torch.uint8).as_strided((x.codes[..., 0].numel(), 400), (400, 1))[:, K:] == 0x7F).all())
+        assert K < whole.shape[1] and bool((whole[:, K:] == 0x7F).all())
     out = torch.empty(T, N, device="cuda")
     ex.matmul(A, W, route, out, any_scales=any_scales)
     offsets = route.offsets.cpu().tolist()
