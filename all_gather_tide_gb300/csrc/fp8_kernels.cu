@@ -220,21 +220,12 @@ struct TileOut {
     int has_rows, has_columns;
 };
 
-template <typename T>
-struct TileSmem {
-    uint64_t row_at[kBlock];                                     // where each row lies; 0: none
-    int32_t first, held;                                         // the tile's first row, and how many it has
-    __align__(16) Eight<T> largest[kWarps][kBlock / 8];          // magnitudes of each column
-    __align__(16) typename Eight<T>::Factor column[kBlock];      // what each column is multiplied by
-    __align__(16) unsigned char turned[kBlock * kBlock];
-};
-
 template <bool Vector, typename T>
-__device__ __forceinline__ void load_tile(Eight<T> (&x)[8], const TileSmem<T>& sm, uint32_t col, uint32_t len) {
+__device__ __forceinline__ void load_tile(Eight<T> (&x)[8], const uint64_t* row_at, uint32_t col, uint32_t len) {
     const int row0 = (threadIdx.x >> 4) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const T* p = reinterpret_cast<const T*>(sm.row_at[row0 + i]);
+        const T* p = reinterpret_cast<const T*>(row_at[row0 + i]);
         const int left = p ? int(len) - int(col) : 0;
         if constexpr (Vector) x[i].load(p + col, left);
         else x[i].load_shifted(p + col, left);
@@ -250,19 +241,19 @@ __device__ __forceinline__ void put_row(const Eight<T>& x, int i, char* codes, i
 
 // Turns the tile, scaled already: codes of `columns` of its columns, each of `count` rows (a multiple of 16).
 template <typename T>
-__device__ __forceinline__ void put_columns(const Eight<T> (&x)[8], TileSmem<T>& sm, char* codes, int64_t stride, int columns, int count) {
+__device__ __forceinline__ void put_columns(const Eight<T> (&x)[8], unsigned char* turned, char* codes, int64_t stride, int columns, int count) {
     const int group = threadIdx.x & 15, rows8 = threadIdx.x >> 4;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint2*>(sm.turned + (group * 8 + j) * kBlock + ((rows8 ^ group) * 8)) =
+        *reinterpret_cast<uint2*>(turned + (group * 8 + j) * kBlock + ((rows8 ^ group) * 8)) =
             make_uint2(codes4(x[0].value(j), x[1].value(j), x[2].value(j), x[3].value(j)), codes4(x[4].value(j), x[5].value(j), x[6].value(j), x[7].value(j)));
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int at = q * 256 + threadIdx.x, c = at >> 3, pair = at & 7, g = c >> 3;
-        uint4 w = *reinterpret_cast<const uint4*>(sm.turned + c * kBlock + ((pair ^ (g >> 1)) * 16));
+        uint4 w = *reinterpret_cast<const uint4*>(turned + c * kBlock + ((pair ^ (g >> 1)) * 16));
         if (g & 1) w = make_uint4(w.z, w.w, w.x, w.y);
-        if (c < columns && pair * 16 < count) *reinterpret_cast<uint4*>(codes + c * stride + pair * 16) = w;
+        if (c < columns && pair * 16 < count) __stcs(reinterpret_cast<uint4*>(codes + c * stride + pair * 16), w);
     }
 }
 
@@ -297,35 +288,66 @@ struct QuantizeArgs {
     uint32_t across;  // tiles of a row of tiles
 };
 
+// A tile's first row, how many it has, its block of the transposed rows and its first column.
+struct TilePlace {
+    int32_t first, held, down;
+    uint32_t col0;
+};
+template <typename T>
+struct QuantizeSmem {
+    uint64_t row_at[2][kBlock];                              // where each row of a tile lies; 0: none
+    TilePlace place[2];
+    int32_t sums[32];
+    __align__(16) Eight<T> largest[kWarps][kBlock / 8];      // magnitudes of each column
+    __align__(16) typename Eight<T>::Factor column[kBlock];  // what each column is multiplied by
+    __align__(16) unsigned char turned[kBlock * kBlock];
+    // and the row tiles before each expert and the first row of each, E + 1 of both
+};
+template <typename T>
+int quantize_smem(int E) {
+    return int(sizeof(QuantizeSmem<T>)) + 8 * (E + 1);
+}
+
+// While a tile is worked on, the next one's place and rows are found: 131072 gathered rows of 2048 bf16 values transposed take 110 us so,
+// 125 without; 131072 of 768 in both forms 71 us, as they are 48. (To copy the next tile's values to shared memory
+// as well, asynchronously, took 145 us by 16 bytes and 147 by rows: it leaves less of the memory that loads and stores pass through.)
 template <typename T, bool Vector>
 __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<T>) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
-    __shared__ TileSmem<T> sm;
-    __shared__ int32_t starts[TIDE_MAX_EXPERTS + 1];  // row tiles before each expert
-    __shared__ int32_t sums[32];
+    extern __shared__ __align__(16) unsigned char dynamic_smem[];
+    QuantizeSmem<T>& sm = *reinterpret_cast<QuantizeSmem<T>*>(dynamic_smem);
+    int32_t* const starts = reinterpret_cast<int32_t*>(dynamic_smem + sizeof(QuantizeSmem<T>));  // [E + 1] row tiles before each expert
+    int32_t* const rows = starts + a.E + 1;                                                      // [E + 1] first row of each
     const int lane = threadIdx.x & 31, group = threadIdx.x & 15, row0 = (threadIdx.x >> 4) * 8, warp = threadIdx.x >> 5;
     wait_for_previous_kernel();
-    exclusive_sums(starts, a.E, sums, [&](int e) { return (span_of(a.offsets, e, a.M).count + kBlock - 1) / kBlock; });
-    const int64_t tiles = int64_t(min(starts[a.E], a.most_blocks)) * a.across;
-    for (int64_t it = blockIdx.x; it < tiles; it += gridDim.x) {
-        const int32_t down = int32_t(quotient(it, a.across));
-        const uint32_t col0 = uint32_t(it - int64_t(down) * a.across) * kBlock, col = col0 + group * 8;
-        if (threadIdx.x < kBlock) {
+    for (int e = threadIdx.x; e <= a.E; e += kThreads) rows[e] = !a.offsets ? (e ? a.M : 0) : min(max(load_here(a.offsets + e), 0), a.M);
+    __syncthreads();
+    exclusive_sums(starts, a.E, sm.sums, [&](int e) { return (max(rows[e + 1] - rows[e], 0) + kBlock - 1) / kBlock; });
+    const int64_t tiles = int64_t(min(starts[a.E], a.most_blocks)) * a.across, step = gridDim.x;
+
+    // The place of the CTA's n-th tile, and which row of src this thread of the first 128 looks for; -1: none.
+    auto find = [&](int64_t it, int n) {
+        int32_t row = -1;
+        if (threadIdx.x < kBlock && it < tiles) {
+            const int32_t down = int32_t(quotient(it, a.across));
             const int e = last_at_most(starts, a.E, down);
-            const Span span = span_of(a.offsets, e, a.M);
-            const int32_t s0 = span.first + (down - starts[e]) * kBlock, held = min(kBlock, span.first + span.count - s0);
-            if (threadIdx.x == 0) sm.first = s0, sm.held = held;
-            uint64_t at = 0;
-            if (int(threadIdx.x) < held) {
-                int64_t row = s0 + threadIdx.x;
-                if (a.tokens) row = load_here(a.tokens + row);
-                if (row >= 0 && row < a.src_rows) at = reinterpret_cast<uint64_t>(static_cast<const T*>(a.src) + row * a.src_stride);
-            }
-            sm.row_at[threadIdx.x] = at;
+            const int32_t s0 = rows[e] + (down - starts[e]) * kBlock, held = min(kBlock, rows[e + 1] - s0);
+            if (threadIdx.x == 0) sm.place[n & 1] = {s0, held, down, uint32_t(it - int64_t(down) * a.across) * kBlock};
+            if (int(threadIdx.x) < held) row = a.tokens ? load_here(a.tokens + s0 + threadIdx.x) : s0 + int(threadIdx.x);
         }
-        __syncthreads();
-        const int32_t s0 = sm.first, held = sm.held;
+        return row;
+    };
+    auto found = [&](int32_t row, int n) {
+        if (threadIdx.x < kBlock) sm.row_at[n & 1][threadIdx.x] = uint32_t(row) < uint32_t(a.src_rows) ? reinterpret_cast<uint64_t>(static_cast<const T*>(a.src) + row * a.src_stride) : 0;
+    };
+    int n = 0;
+    found(find(blockIdx.x, 0), 0);
+    for (int64_t it = blockIdx.x; it < tiles; it += step, ++n) {
         Eight<T> x[8];
-        load_tile<Vector>(x, sm, col, a.len);
+        __syncthreads();  // what the tile before wrote has been read, and this one's place and rows are known
+        const int32_t s0 = sm.place[n & 1].first, held = sm.place[n & 1].held, down = sm.place[n & 1].down;
+        const uint32_t col0 = sm.place[n & 1].col0, col = col0 + group * 8;
+        load_tile<Vector>(x, sm.row_at[n & 1], col, a.len);
+        const int32_t later = find(it + step, n + 1);
         if (a.out.has_rows) {
             uint32_t m[8];
 #pragma unroll
@@ -361,10 +383,10 @@ __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<T>) quantize_kernel(c
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i].scale_each(sm.column + group * 8);
-            put_columns(x, sm, static_cast<char*>(a.out.columns.codes) + int64_t(col0) * a.out.columns.stride + block * kBlock, a.out.columns.stride,
+            put_columns(x, sm.turned, static_cast<char*>(a.out.columns.codes) + int64_t(col0) * a.out.columns.stride + block * kBlock, a.out.columns.stride,
                         int(min(uint32_t(kBlock), a.len - col0)), kBlock);
         }
-        __syncthreads();  // what the next tile writes has been read
+        found(later, n + 1);
     }
     let_next_kernel_start();
 }
@@ -382,7 +404,10 @@ struct GatherArgs {
 
 template <bool Vector>
 __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<__nv_bfloat16>) all_gather_fp8_kernel(const __grid_constant__ GatherArgs a) {
-    __shared__ TileSmem<__nv_bfloat16> sm;
+    __shared__ struct {
+        uint64_t row_at[kBlock];  // where each row lies; 0: none
+        __align__(16) unsigned char turned[kBlock * kBlock];
+    } sm;
     __shared__ uint32_t of_warp[kWarps];
     const int group = threadIdx.x & 15, warp = threadIdx.x >> 5;
     wait_for_previous_kernel();
@@ -400,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<__nv_bfloat16>) all_g
         }
         __syncthreads();
         Eight<__nv_bfloat16> x[8];
-        load_tile<Vector>(x, sm, col, a.tv.len);
+        load_tile<Vector>(x, sm.row_at, col, a.tv.len);
         uint32_t largest = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) largest = max(largest, x[i].largest());
@@ -418,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<__nv_bfloat16>) all_g
             put_row(x[i], i, codes, a.w.stride, held, col, a.tv.len);
         }
         if (a.has_wt)
-            put_columns(x, sm, static_cast<char*>(a.wt.codes) + int64_t(e) * a.wt.batch + int64_t(col0) * a.wt.stride + n0, a.wt.stride, int(min(uint32_t(kBlock), a.tv.len - col0)),
+            put_columns(x, sm.turned, static_cast<char*>(a.wt.codes) + int64_t(e) * a.wt.batch + int64_t(col0) * a.wt.stride + n0, a.wt.stride, int(min(uint32_t(kBlock), a.tv.len - col0)),
                         (held + 15) / 16 * 16);
         __syncthreads();  // what the next tile writes has been read
     }
@@ -436,6 +461,18 @@ cudaError_t dispatch_fp8(const RowsView& src, int64_t tokens, int k, int64_t len
     const int64_t items = tokens * stretches;
     return launch_after(dispatch_fp8_kernel<T, Vector>, grid_of((items + kWarps - 1) / kWarps, c, INT32_MAX), kThreads, 0, stream, static_cast<const T*>(src.p), src.stride, tokens, k,
                         int32_t(tokens * k), uint32_t(len), slots, rows, stretches, items);
+}
+
+template <typename T, bool Vector>
+cudaError_t quantize(const QuantizeArgs& a, const Ctas& c, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(quantize_kernel<T, Vector>), quantize_smem<T>(TIDE_MAX_EXPERTS), c.device, allowed);
+    if (e != cudaSuccess) return e;
+    // CTAs go round with the next tile's place found beforehand; where rows are written and there are 16 tiles for each that fits, more
+    // CTAs take 8 each, so that those that come late even out the end (524288 rows of 768 bf16 values 183 us, going round 209; 131072 48
+    // going round, 53)
+    const int64_t fit = int64_t(c.sms) * kTileCtasPerSm<T>, tiles = int64_t(a.most_blocks) * a.across;
+    return launch_after(quantize_kernel<T, Vector>, grid_of(tiles, c, a.out.has_rows && tiles >= 16 * fit ? tiles / 8 : fit), kThreads, size_t(quantize_smem<T>(a.E)), stream, a);
 }
 
 }  // namespace
@@ -458,10 +495,9 @@ cudaError_t launch_quantize(const RowsView& src, int bf16, int64_t src_rows, int
     if (rows) a.out.rows = *rows;
     if (columns) a.out.columns = *columns;
     a.across = uint32_t((len + kBlock - 1) / kBlock);
-    const bool v = vectors(reinterpret_cast<uintptr_t>(src.p), src.stride, src_rows, len, bf16 ? 2 : 4);
-    const int64_t tiles = padded_blocks(M, E) * a.across;
-    auto* kernel = bf16 ? (v ? quantize_kernel<__nv_bfloat16, true> : quantize_kernel<__nv_bfloat16, false>) : (v ? quantize_kernel<float, true> : quantize_kernel<float, false>);
-    return launch_after(kernel, grid_of(tiles, c, int64_t(c.sms) * (bf16 ? kTileCtasPerSm<__nv_bfloat16> : kTileCtasPerSm<float>)), kThreads, 0, stream, a);
+    const bool v = src_rows > 0 && vectors(reinterpret_cast<uintptr_t>(src.p), src.stride, src_rows, len, bf16 ? 2 : 4);
+    if (bf16) return v ? quantize<__nv_bfloat16, true>(a, c, stream) : quantize<__nv_bfloat16, false>(a, c, stream);
+    return v ? quantize<float, true>(a, c, stream) : quantize<float, false>(a, c, stream);
 }
 
 cudaError_t launch_all_gather_fp8(const ShardPtrs& shards, const TableView& tv, int E, const ExpertParams& ps, const tide_fp8_t& w, const tide_fp8_t* wt, const Ctas& c,
