@@ -50,14 +50,19 @@ __device__ __forceinline__ void exclusive_sums(int32_t* v, int n, int32_t* sums,
     __syncthreads();
 }
 
-// Rows of expert e that are there: [first, first + count), inside [0, M) whatever the offsets hold.
-struct Span {
-    int32_t first, count;
-};
-__device__ __forceinline__ Span span_of(const int32_t* offsets, int e, int32_t M) {
-    if (!offsets) return {0, M};
-    const int32_t a = min(max(load_here(offsets + e), 0), M), b = min(max(load_here(offsets + e + 1), a), M);
-    return {a, b - a};
+// rows[0..E] = the experts' first rows, inside [0, M] and ascending whatever the offsets hold: none where these descend. Without
+// offsets one expert has all M. All of the block's threads call it.
+__device__ __forceinline__ void first_rows(int32_t* rows, const int32_t* offsets, int E, int32_t M) {
+    bool descends = false;
+    for (int e = threadIdx.x; e <= E; e += int(blockDim.x)) {
+        const int32_t at = offsets ? load_here(offsets + e) : e ? M : 0;
+        descends |= offsets && e < E && load_here(offsets + e + 1) < at;
+        rows[e] = min(max(at, 0), M);
+    }
+    if (__syncthreads_or(descends)) {
+        for (int e = threadIdx.x; e <= E; e += int(blockDim.x)) rows[e] = 0;
+        __syncthreads();
+    }
 }
 
 // The last index of starts[0..n) whose value is <= x; starts[0] = 0 <= x.  Of equal ones it is the last.

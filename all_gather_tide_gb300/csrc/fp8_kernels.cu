@@ -280,7 +280,7 @@ __device__ __forceinline__ uint32_t largest_of_rows(const uint32_t (&a)[8]) {
 struct QuantizeArgs {
     const void* src;
     int64_t src_stride;
-    int32_t src_rows, M, E, most_blocks;
+    int32_t src_rows, M, E;
     uint32_t len;
     const int32_t* offsets;
     const int32_t* tokens;
@@ -319,10 +319,9 @@ __global__ void __launch_bounds__(kThreads, kTileCtasPerSm<T>) quantize_kernel(c
     int32_t* const rows = starts + a.E + 1;                                                      // [E + 1] first row of each
     const int lane = threadIdx.x & 31, group = threadIdx.x & 15, row0 = (threadIdx.x >> 4) * 8, warp = threadIdx.x >> 5;
     wait_for_previous_kernel();
-    for (int e = threadIdx.x; e <= a.E; e += kThreads) rows[e] = !a.offsets ? (e ? a.M : 0) : min(max(load_here(a.offsets + e), 0), a.M);
-    __syncthreads();
-    exclusive_sums(starts, a.E, sm.sums, [&](int e) { return (max(rows[e + 1] - rows[e], 0) + kBlock - 1) / kBlock; });
-    const int64_t tiles = int64_t(min(starts[a.E], a.most_blocks)) * a.across, step = gridDim.x;
+    first_rows(rows, a.offsets, a.E, a.M);
+    exclusive_sums(starts, a.E, sm.sums, [&](int e) { return (rows[e + 1] - rows[e] + kBlock - 1) / kBlock; });
+    const int64_t tiles = int64_t(starts[a.E]) * a.across, step = gridDim.x;
 
     // The place of the CTA's n-th tile, and which row of src this thread of the first 128 looks for; -1: none.
     auto find = [&](int64_t it, int n) {
@@ -471,7 +470,7 @@ cudaError_t quantize(const QuantizeArgs& a, const Ctas& c, cudaStream_t stream) 
     // CTAs go round with the next tile's place found beforehand; where rows are written and there are 16 tiles for each that fits, more
     // CTAs take 8 each, so that those that come late even out the end (524288 rows of 768 bf16 values 183 us, going round 209; 131072 48
     // going round, 53)
-    const int64_t fit = int64_t(c.sms) * kTileCtasPerSm<T>, tiles = int64_t(a.most_blocks) * a.across;
+    const int64_t fit = int64_t(c.sms) * kTileCtasPerSm<T>, tiles = padded_blocks(a.M, a.E) * a.across;
     return launch_after(quantize_kernel<T, Vector>, grid_of(tiles, c, a.out.has_rows && tiles >= 16 * fit ? tiles / 8 : fit), kThreads, size_t(quantize_smem<T>(a.E)), stream, a);
 }
 
@@ -489,7 +488,7 @@ cudaError_t launch_quantize(const RowsView& src, int bf16, int64_t src_rows, int
                             const tide_fp8_t* rows, const tide_fp8_t* columns, const Ctas& c, cudaStream_t stream) {
     if (M <= 0) return cudaSuccess;
     QuantizeArgs a{};
-    a.src = src.p, a.src_stride = src.stride, a.src_rows = int32_t(src_rows), a.M = int32_t(M), a.E = E, a.most_blocks = int32_t(padded_blocks(M, E)), a.len = uint32_t(len);
+    a.src = src.p, a.src_stride = src.stride, a.src_rows = int32_t(src_rows), a.M = int32_t(M), a.E = E, a.len = uint32_t(len);
     a.offsets = offsets, a.tokens = tokens;
     a.out.has_rows = rows != nullptr, a.out.has_columns = columns != nullptr;
     if (rows) a.out.rows = *rows;

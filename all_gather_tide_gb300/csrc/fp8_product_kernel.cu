@@ -43,7 +43,6 @@ struct ProductArgs {
     int32_t a_box;  // rows of A that a copy brings, a multiple of 8: fewer than 128 where there are no more
     int32_t N, K;  // columns of the result, blocks' length in all (product only)
     int32_t rows;  // rows of the result (gradient only)
-    int32_t most_blocks;  // of the transposed operands (gradient only)
     void* out;
     int64_t out_stride;
     int scale_vectors;  // scales that lie side by side can be read four at a time
@@ -258,13 +257,8 @@ struct Tiles {
     __device__ __forceinline__ Tiles(const ProductArgs& p, int32_t* starts, int32_t* first, int32_t* sums)
         : p(p), starts(starts), first(first), across(uint32_t((p.N + BN - 1) / BN)), down(uint32_t((p.rows + Rows - 1) / Rows)) {
         constexpr int kUnit = Grad ? kBlock : Rows;
-        for (int e = threadIdx.x; e <= p.E; e += int(blockDim.x)) first[e] = !p.offsets ? (e ? p.M : 0) : min(max(load_here(p.offsets + e), 0), p.M);
-        __syncthreads();
-        exclusive_sums(starts, p.E, sums, [&](int e) { return (max(first[e + 1] - first[e], 0) + kUnit - 1) / kUnit; });
-        if (Grad) {  // whatever the offsets hold, no tile reaches past the transposed operands
-            for (int e = threadIdx.x; e <= p.E; e += int(blockDim.x)) starts[e] = min(starts[e], p.most_blocks);
-            __syncthreads();
-        }
+        first_rows(first, p.offsets, p.E, p.M);
+        exclusive_sums(starts, p.E, sums, [&](int e) { return (first[e + 1] - first[e] + kUnit - 1) / kUnit; });
         count = Grad ? int64_t(p.E) * across * down : int64_t(starts[p.E]) * across;
     }
     __device__ __forceinline__ Tile at(int64_t it) const {
@@ -1007,7 +1001,6 @@ int launch_weight_grad(const tide_fp8_t& dy, const tide_fp8_t& a, int64_t M, int
         if (rc == TIDE_OK) rc = describe(&p.b, a, padded, K, 0, 128);
         if (rc != TIDE_OK) return rc;
     }
-    p.most_blocks = int32_t(padded / kBlock);
     p.a_box = kTileM;
     p.a_scales = dy.scales, p.a_scale_stride = dy.scale_stride;
     p.b_scales = a.scales, p.b_scale_stride = a.scale_stride;

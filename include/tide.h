@@ -633,7 +633,8 @@ int tide_fp8_padded_rows(int64_t M, int32_t E, int64_t *columns);
  * sums over).
  *   src: rows of len elements of `type`, src_stride apart; row s is src[s], M of them, or with tokens (device,
  *   M int32, tide_experts_sort's) src[tokens[s]] of the src_rows rows of src.
- *   offsets: tide_experts_sort's; only rows before offsets[E] are read and written (NULL, for E = 1: all M).
+ *   offsets: tide_experts_sort's; only rows before offsets[E] are read and written (NULL, for E = 1: all M).  What
+ *   lies outside [0, M] counts as its nearest bound, and offsets that descend as no rows at all.
  *   rows: M rows of len codes, or NULL.
  *   columns: len rows of tide_fp8_padded_rows(M, E) codes, or NULL; expert e's rows are columns P_e to
  *   P_e + offsets[e+1] - offsets[e], P_e = 128 * sum over e' < e of ceil((offsets[e'+1] - offsets[e']) / 128);

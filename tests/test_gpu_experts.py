@@ -741,6 +741,40 @@ def test_offsets_past_32_bits(tide):
     assert same(c.codes[:, at * 128:(at + 1) * 128].float().cpu().double(), codes) and same(c.scales[at].cpu().double(), scales[:, 0])
 
 
+@pytest.mark.parametrize("any_scales", [False, True])
+def test_offsets_that_nobody_sorted(tide, any_scales):
+    """Descending offsets are no rows: nothing is written, and gradients are zeros. Offsets outside the rows count as their bounds."""
+    E, M, N, K = 3, 600, 384, 256
+    ex = tide.Experts(E, 1)
+    route = ex.route(M)
+    g = gen(1)
+    A, W, D, X = tide.Fp8Rows(M, K), tide.Fp8Weights(E, N, K), tide.Fp8Columns(M, N, E), tide.Fp8Columns(M, K, E)
+    for x in (A, W, D, X):
+        random_fp8(g, x, any_scales)
+    x = torch.randn(M, K, generator=g).bfloat16().cuda()
+    big = 2 ** 31 - 1
+    for offsets in ([0, 300, 200, 600], [0, big, 0, big], [5, 4, 4, 4]):
+        route.offsets.copy_(torch.tensor(offsets, dtype=torch.int32))
+        out, grads = torch.full((M, N), 55.0, device="cuda"), torch.full((E, N, K), 55.0, device="cuda")
+        q, c = tide.Fp8Rows(M, K), tide.Fp8Columns(M, K, E)
+        for b in (q.codes.view(torch.uint8), c.codes.view(torch.uint8), q.scales, c.scales):
+            b.fill_(55)
+        ex.matmul(A, W, route, out, any_scales=any_scales)
+        ex.weight_grad(D, X, route, grads, any_scales=any_scales)
+        ex.quantize(x, route, rows=q, columns=c)
+        assert bool((out == 55).all()) and not bool(grads.any())
+        assert all(bool((b == 55).all()) for b in (q.codes.view(torch.uint8), c.codes.view(torch.uint8), q.scales, c.scales))
+    results = []
+    for offsets in ([-big, 0, 200, big], [0, 0, 200, 600]):
+        route.offsets.copy_(torch.tensor(offsets, dtype=torch.int32))
+        out, grads, q = torch.full((M, N), 55.0, device="cuda"), torch.full((E, N, K), 55.0, device="cuda"), tide.Fp8Rows(M, K)
+        ex.matmul(A, W, route, out, any_scales=any_scales)
+        ex.weight_grad(D, X, route, grads, any_scales=any_scales)
+        ex.quantize(x, route, rows=q)
+        results.append((out, grads, q.codes.view(torch.uint8).clone(), q.scales.clone()))
+    assert all(torch.equal(p, q) for p, q in zip(*results)) and ex.device_status() == 0
+
+
 @pytest.mark.parametrize("T", [40, 20000])
 def test_a_wait_that_runs_out_is_told_of(tide, T):
     """Products that load nothing: every wait gives up after a millisecond, the kernel returns, and the next call works. Both tile shapes, and
