@@ -208,7 +208,7 @@ dispatch_kernel(const Word* src, int64_t src_stride, int64_t T, int k, int32_t M
 // The rows back at their tokens, weighted.  A warp takes a token and up to `per` stretches of 32*Cols vectors, one after the other; AtOnce
 // rows are in flight before their products are added, in fp32 and in the pairs' order.
 //
-// Bound by HBM reads: 524288 rows of 2048 bf16 values back to 65536 tokens in 363 us, 6.7 TB/s (440 with four CTAs an SM, whose
+// Bound by HBM reads: 524288 rows of 2048 bf16 values back to 65536 tokens in 355 us, 6.7 TB/s (440 with four CTAs an SM, whose
 // registers spilled).
 constexpr int kCombineCtasPerSm = 3;
 template <typename T, int V, int Cols, int AtOnce>
