@@ -270,7 +270,7 @@ combine_kernel(const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_
 // product with its weight is written while the dot product is added up.  A lane's sums run over its columns in order, then
 // over the warp's lanes and the team's warps as a tree.
 //
-// Bound by HBM, a row read and a row written for each pair: 262144 rows of 2048 bf16 values in 354 us, 6.4 TB/s.
+// Bound by HBM, a row read and a row written for each pair: 262144 rows of 2048 bf16 values in 341 us, 6.6 TB/s.
 template <typename T, int V, int Pairs, int Cols>
 __global__ void __launch_bounds__(kThreads, 2)
 combine_grad_kernel(const T* dout, int64_t dout_stride, const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_t M, uint32_t len,
@@ -404,9 +404,11 @@ cudaError_t combine_grad(const RowsView& dout, const RowsView& rows, int64_t tok
         return launch_after(kernel, grid_of(blocks, c), kThreads, 0, stream, static_cast<const T*>(dout.p), dout.stride, static_cast<const T*>(rows.p), rows.stride,
                             tokens, k, int32_t(tokens * k), uint32_t(len), slots, weights, static_cast<T*>(drows), drows_stride, dweights, team);
     };
-    // eight vectors of rows in flight, more where they are short
-    constexpr int kMany = V * sizeof(T) >= 16 ? 1 : 2;
-    return k > 4 ? go(combine_grad_kernel<T, V, 8, kMany>, kMany) : go(combine_grad_kernel<T, V, 4, 2 * kMany>, 2 * kMany);
+    // Vectors of each row in flight, more where they are short and where pairs are few: 262144 rows of 2048 bf16 values, eight pairs, 341
+    // us with two of 16 bytes, one 350; 12297 of 1027 fp32 values, three pairs, 17.9 with twelve, eight 18.6, four 20.7; 80000 of 1028
+    // bf16 values, four pairs, 66 with eight of 8 bytes, four 70, but 48000, eight pairs, 43 with four, two 41.
+    constexpr int kBytes = V * sizeof(T), kEight = kBytes >= 8 ? 2 : kBytes == 4 ? 6 : 4, kFour = kBytes >= 16 ? 4 : kBytes == 4 ? 12 : 8;
+    return k > 4 ? go(combine_grad_kernel<T, V, 8, kEight>, kEight) : go(combine_grad_kernel<T, V, 4, kFour>, kFour);
 }
 
 }  // namespace
