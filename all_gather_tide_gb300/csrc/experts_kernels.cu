@@ -380,7 +380,7 @@ cudaError_t combine(const RowsView& rows, int64_t tokens, int k, int64_t len, co
     auto go = [&](auto* kernel, int cols) {
         const uint32_t stretches = uint32_t((len + 32 * V * cols - 1) / (32 * V * cols));
         // a warp takes the whole row where the tokens fill the GPU four times, so that it finds their rows once (80000 rows of 1027 bf16
-        // values 61 us, a stretch a warp 76)
+        // values 53 us; with eight vectors at a time 61, and a stretch a warp 76)
         const int64_t warps = 4 * int64_t(c.sms) * kCombineCtasPerSm * kWarps;
         const uint32_t shares = uint32_t(std::min<int64_t>(stretches, (warps + tokens - 1) / tokens));
         const uint32_t per = (stretches + shares - 1) / shares;
@@ -388,8 +388,9 @@ cudaError_t combine(const RowsView& rows, int64_t tokens, int k, int64_t len, co
         return launch_after(kernel, grid_of((items + kWarps - 1) / kWarps, c), kThreads, 0, stream, static_cast<const T*>(rows.p), rows.stride, tokens, k, int32_t(tokens * k),
                             uint32_t(len), slots, weights, static_cast<T*>(out), out_stride, stretches, per, (stretches + per - 1) / per, items);
     };
-    // Short vectors go several at a time, fewer where a row has no more: 12297 rows of 1027 bf16 values take 22 us with two a row.
-    constexpr int kMany = V * sizeof(T) >= 16 ? 2 : V * sizeof(T) == 8 ? 4 : 8;
+    // Short vectors go several at a time, fewer where a row has no more: 80000 rows of 1027 bf16 values take 53 us with seven of four rows; eight,
+    // of which registers spill, 60; six 57; 12297 rows 12.9 us, with two 22.
+    constexpr int kMany = V * sizeof(T) >= 16 ? 2 : V * sizeof(T) == 8 ? 4 : 7;
     return len > 32 * V ? go(combine_kernel<T, V, kMany, 4>, kMany) : go(combine_kernel<T, V, 1, 4>, 1);
 }
 
