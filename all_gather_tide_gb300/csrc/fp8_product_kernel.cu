@@ -93,16 +93,34 @@ __device__ __forceinline__ uint32_t of_first_cta(uint64_t* bar) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
     return at;
 }
-// What is handed over this way lies in Tensor Memory, or in this CTA's shared memory behind a proxy fence, so the arrival has
-// the CTA's scope: with the cluster's it waits for all of the thread's loads and stores, 2000 cycles.
+// Arrivals at the barrier of the pair's first CTA, whose products read and write both CTAs' memory.
+//
+// Of Tensor Memory, whose accesses have ended (tcgen05.wait) and are fenced by tcgen05.fence on both sides: the arrival orders nothing
+// else, so it is relaxed. (A release of the cluster's scope waits for all of the thread's loads and stores, here those of a tile of the
+// result: 2000 cycles.)
 template <bool Pair>
-__device__ __forceinline__ void arrive_at_first(uint64_t* bar) {
-    if constexpr (Pair) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(of_first_cta(bar)) : "memory");
+__device__ __forceinline__ void arrive_after_tensor_memory(uint64_t* bar) {
+    if constexpr (Pair) asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_first_cta(bar)) : "memory");
     else barrier_arrive(bar);
+}
+// Of shared memory that this CTA has written: a release of the cluster's scope, by a thread without loads and stores of its own.
+__device__ __forceinline__ void arrive_after_shared_memory(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_first_cta(bar)) : "memory");
 }
 __device__ __forceinline__ bool barrier_try(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// The same where threads of the other CTA of a pair arrive too, or its products and copies do.
+template <bool Pair>
+__device__ __forceinline__ bool barrier_try_both(uint64_t* bar, uint32_t parity) {
+    if constexpr (!Pair) return barrier_try(bar, parity);
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
     return ok != 0;
 }
 
@@ -112,9 +130,17 @@ struct Waits {
     int* status;
     uint64_t limit;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-        if (barrier_try(bar, parity)) return true;
+        return until([&] { return barrier_try(bar, parity); });
+    }
+    template <bool Pair>
+    __device__ __forceinline__ bool both(uint64_t* bar, uint32_t parity) const {
+        return until([&] { return barrier_try_both<Pair>(bar, parity); });
+    }
+    template <typename Try>
+    __device__ __forceinline__ bool until(Try&& done) const {
+        if (done()) return true;
         const uint64_t end = globaltimer() + limit;
-        while (!barrier_try(bar, parity)) {
+        while (!done()) {
             if (*stop) return false;
             if (globaltimer() > end) {
                 atomicCAS(status, 0, kStatusWait);
@@ -295,7 +321,7 @@ __device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles& ti
         const Tile t = tiles.at(it);
         const int row = t.row0 + rank * kTileM, col = t.col0 + rank * (BN / 2);
         for (int b = 0; b < t.blocks; ++b) {
-            if (!(ok = __all_sync(kFull, wait(&empty[s.at], s.phase ^ 1)))) break;
+            if (!(ok = __all_sync(kFull, wait.both<Pair>(&empty[s.at], s.phase ^ 1)))) break;
             unsigned char* a = ring + s.at * r.share;
             if (elected()) {
                 if (rank == 0) barrier_expect(&full[s.at], Pair ? 2 * (p.a_box + BN / 2) * kBlock : r.share);
@@ -545,7 +571,7 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
                     }
                 }
             load(v, g + 2);
-            if (!__all_sync(kFull, wait(&empty[buffer.at], buffer.phase ^ 1))) return false;
+            if (!__all_sync(kFull, wait.both<Pair>(&empty[buffer.at], buffer.phase ^ 1))) return false;
             unsigned char* const to = exponents + buffer.at * exponent_bytes(BN);
             if (Grad) {
 #pragma unroll
@@ -559,7 +585,7 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) arrive_at_first<Pair>(&full[buffer.at]);
+            if (lane == 0) barrier_arrive(&full[buffer.at]);
             buffer.next(exponent_groups(BN));
             buffer.next(exponent_groups(BN));
             return true;
@@ -570,6 +596,22 @@ __device__ __forceinline__ void write_exponents(const ProductArgs& p, const Tile
             if (!write(x, g)) return;
     }
     if (bad) atomicCAS(p.wait.status, 0, kStatusScale);
+}
+
+// The second CTA of a pair: of each group of four blocks, its writers arrive at its own barrier, and the warp that waits there, which has no
+// other loads and stores, tells the first CTA.
+template <int BN, typename Tiles>
+__device__ __forceinline__ void hand_over_exponents(const Tiles& tiles, int64_t begin, int64_t step, uint64_t* full, const Waits& wait) {
+    Cursor g;
+    for (int64_t it = begin; it < tiles.count; it += step) {
+        const int blocks = tiles.at(it).blocks;
+        for (int b = 0; b < blocks; b += kAhead) {
+            if (!__all_sync(kFull, wait(&full[g.at], g.phase))) return;
+            if (elected()) arrive_after_shared_memory(&full[g.at]);
+            __syncwarp();
+            g.next(exponent_groups(BN));
+        }
+    }
 }
 
 // All threads of the CTA, or of both of a pair.
@@ -599,7 +641,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMostStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
-        for (int i = 0; i < kExponentGroups; ++i) barrier_init(&scales_full[i], 2 * kCtas), barrier_init(&scales_empty[i], 1);
+        for (int i = 0; i < kExponentGroups; ++i) barrier_init(&scales_full[i], Pair && rank == 0 ? 3 : 2), barrier_init(&scales_empty[i], 1);
         for (int i = 0; i < 2; ++i) barrier_init(&ready[i], 1);
         for (int i = 0; i < 2; ++i) barrier_init(&drained[i], kSumWarps * kCtas);
         barrier_init(&taken, kSumWarps / 2 * kCtas), barrier_init(&ended, 1);
@@ -641,10 +683,10 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
                 }
                 const uint32_t to = tmem + (tile & 1) * second_tile(BN);
                 // the tile before the last has been taken out, and of the last the columns that it shares
-                if (!(ok = tile < 2 || __all_sync(kFull, wait(&drained[tile & 1], ((tile >> 1) - 1) & 1)))) break;
-                if (kShared && !(ok = tile == 0 || __all_sync(kFull, wait(&taken, (tile - 1) & 1)))) break;
+                if (!(ok = tile < 2 || __all_sync(kFull, wait.both<Pair>(&drained[tile & 1], ((tile >> 1) - 1) & 1)))) break;
+                if (kShared && !(ok = tile == 0 || __all_sync(kFull, wait.both<Pair>(&taken, (tile - 1) & 1)))) break;
                 for (int b0 = 0; ok && b0 < blocks; b0 += kAhead) {
-                    if (!(ok = __all_sync(kFull, wait(&scales_full[g.at], g.phase)))) break;
+                    if (!(ok = __all_sync(kFull, wait.both<Pair>(&scales_full[g.at], g.phase)))) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const unsigned char* x = exponents + g.at * exponent_bytes(BN);
                     const uint32_t a_scales = tmem + exponent_column(BN) + g.at * kGroupCols, b_scales = a_scales + 4;
@@ -660,7 +702,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
                     for (int q = 0; q < kAhead; ++q) {
                         const int b = b0 + q;
                         if (b >= blocks) break;
-                        if (!(ok = __all_sync(kFull, wait(&full[s.at], s.phase)))) break;
+                        if (!(ok = __all_sync(kFull, wait.both<Pair>(&full[s.at], s.phase)))) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         const uint64_t da = first_a + uint32_t(s.at * r.share >> 4), db = da + uint32_t(b_at >> 4);
                         const uint32_t instruction = scaled_instruction(BN, Pair) | uint32_t(q) << 29 | uint32_t(q) << 4;
@@ -679,6 +721,8 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
                 ++tile;
             }
             if (!ok) end_products<Pair>(&ended);
+        } else {
+            hand_over_exponents<BN>(tiles, begin, step, scales_full, wait);
         }
     } else if (warp < 4 || warp >= 4 + kSumWarps) {
         // warps 2 and 3 write A's and B's exponents of every other group, the last two of the others
@@ -705,7 +749,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
                 for (int c = 0; c < chunks; ++c) put_sums_staged<Grad, Out>(p, mine, none, t.e, row0, rows, col + c * 32);
                 continue;
             }
-            ok = __all_sync(kFull, wait(&ready[tile & 1], (tile >> 1) & 1));
+            ok = __all_sync(kFull, wait.both<Pair>(&ready[tile & 1], (tile >> 1) & 1));
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t at = from + (tile & 1) * second_tile(BN);
@@ -720,9 +764,10 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
                 sums_loaded();
                 if ((holds && c == 0) || c + 1 == chunks) {
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
                     if (lane == 0) {
-                        if (holds && c == 0) arrive_at_first<Pair>(&taken);
-                        if (c + 1 == chunks) arrive_at_first<Pair>(&drained[tile & 1]);
+                        if (holds && c == 0) arrive_after_tensor_memory<Pair>(&taken);
+                        if (c + 1 == chunks) arrive_after_tensor_memory<Pair>(&drained[tile & 1]);
                     }
                 }
                 put_sums_staged<Grad, Out>(p, mine, x, t.e, row0, rows, col + column(c));
