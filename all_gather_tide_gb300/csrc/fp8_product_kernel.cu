@@ -796,6 +796,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1) scaled_product_kernel(const
 template <int BN, bool Grad, typename Out>
 __global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid_constant__ ArgsOf<Grad> p) {
     constexpr int kBuffers = kTmemCols / BN, kHalf = BN / 2, kChunks = kHalf / 32;
+    static_assert(kBuffers % 2 == 0, "a buffer's number tells whether a block is odd");
     extern __shared__ unsigned char dynamic_smem[];
     unsigned char* const ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic_smem) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[kMostStages], empty[kMostStages], ready[kBuffers], drained[kBuffers], ended;
@@ -861,7 +862,8 @@ __global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid
 #pragma unroll
             for (int j = 0; j < kHalf / 2; ++j) acc[j] = 0;
             // The scales of the row and of the columns' block, one block ahead.  For a gradient, whose scales lie side by side
-            // for each block, the lanes have the columns' scales between them and hand them round through shared memory.
+            // for each block, the lanes have the columns' scales between them and hand them round through shared memory: two buffers
+            // in turn, over the tiles' ends too, so that all lanes have met once between a buffer's last read and its next write.
             const int n = min(col, p.N - 1) / kBlock;
             const float* row_scales = Grad ? p.a_scales + t.k0 / kBlock * p.a_scale_stride + min(row, p.rows - 1) : p.a_scales + min(row, p.M - 1) * p.a_scale_stride;
             const float* col_scales = Grad ? p.b_scales + t.k0 / kBlock * p.b_scale_stride : p.b_scales + t.e * p.b_scale_batch + (p.transposed ? n : n * p.b_scale_stride);
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1) any_scales_kernel(const __grid
             fetch(0);
             for (int b = 0; b < t.blocks; ++b) {
                 const float f = Grad ? next_row : next_row * next_col[0];
-                float* const mine = column_scales[Grad ? warp - 4 : 0][Grad ? b & 1 : 0];
+                float* const mine = column_scales[Grad ? warp - 4 : 0][Grad ? d.at & 1 : 0];
                 if (Grad) {
 #pragma unroll
                     for (int i = 0; i < kColScales; ++i) mine[i * 32 + lane] = next_col[i];

@@ -101,3 +101,34 @@ def test_gradients_of_pairs_use_every_blocks_own_scales(tide, E, each, N, K, kin
         ex.weight_grad(dy, a, route, out)
         assert torch.equal(out, want)
     assert ex.device_status() == 0
+
+
+# ---- any scales ------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("each, N, K", [(128, 128, 384), (100, 331, 515), (300, 203, 397)])
+def test_gradients_with_any_scales_of_tiles_with_an_odd_number_of_blocks(tide, each, N, K, kind):
+    """The lanes hand their columns' scales round in two buffers; a tile that ends after one or three blocks goes over to the next with lanes unequally far, where
+    rows' ends leave by elements. Every CTA takes many such tiles."""
+    E = 200
+    g = gen(each + N)
+    ex, route = routed_evenly(tide, E, each)
+    dy, a = tide.Fp8Columns(E * each, N, E), tide.Fp8Columns(E * each, K, E)
+    small_fp8(g, dy, 4), small_fp8(g, a, 4)
+    dy.scales.mul_(3), a.scales.mul_(5)  # no powers of two, and whole numbers
+    per = -(-each // 128) * 128
+    for x in (dy, a):
+        for e in range(E):
+            x.codes.view(torch.uint8)[:, e * per + each:(e + 1) * per] = 0
+    p, q = (column_values(x)[:, :E * per].view(-1, E, per).transpose(0, 1) for x in (dy, a))
+    want = p @ q.transpose(1, 2)
+    assert float(want.abs().max()) < 1 << 24
+    want, traffic = want.to(kind), Traffic()
+    out = torch.empty_like(want)
+    for _ in range(10):
+        out.fill_(55.0)
+        traffic.more()
+        ex.weight_grad(dy, a, route, out, any_scales=True)
+        assert torch.equal(out, want)
+    assert ex.device_status() == 0
