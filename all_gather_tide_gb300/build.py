@@ -20,7 +20,7 @@ SOURCES = ["plan.cpp", "tide_api.cpp", "rs_kernel.cu", "rs_bulk_kernel.cu", "ag_
            "embedding_api.cpp", "embedding_kernel.cu", "embedding_grad_kernels.cu", "tensor_api.cpp", "tensor_kernels.cu",
            "experts_api.cpp", "experts_kernels.cu", "fp8_kernels.cu", "fp8_product_kernel.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("tide_internal.h", "table_ring.h", "group.h", "api_common.h", "step_internal.h",
-                                              "copy_any.cuh", "embedding_device.cuh", "step_launch.cuh", "experts.h", "experts_device.cuh")]
+                                              "copy_any.cuh", "embedding_device.cuh", "step_launch.cuh", "experts.h", "experts_device.cuh", "copies_end.h")]
 HEADERS.append(os.path.join(ROOT, "include", "tide.h"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

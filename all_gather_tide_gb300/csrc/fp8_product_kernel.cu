@@ -16,6 +16,7 @@
 #include <cuda.h>
 
 #include "api_common.h"
+#include "copies_end.h"
 #include "experts_device.cuh"
 
 namespace tide {
@@ -334,16 +335,18 @@ __device__ __forceinline__ void load_tiles(const ProductArgs& p, const Tiles& ti
             ++uses;
         }
     }
-    // No copy, and no arrival of the products that read it, is left on its way to this CTA's memory. One that was
-    // stopped waits for its copies alone: 20 ms, or until they are counted as landed where the barrier is its own.
-    const bool all = ok && !*wait.stop;
-    for (int64_t u = max(int64_t(0), uses - r.stages); u < uses; ++u) {
-        const int at = int(u % r.stages);
-        const uint32_t parity = uint32_t(u / r.stages) & 1;
-        const uint64_t end = globaltimer() + (all ? p.wait.timeout_ns : 20000000ull);
-        while (!((all || rank == 0) && barrier_try(all ? &empty[at] : &full[at], parity)) && globaltimer() < end) {
-        }
-    }
+    // No copy, and no arrival of the products that read it, is left on its way to this CTA's memory. Copies are counted as landed
+    // at the barriers of the first CTA alone.
+    struct {
+        uint64_t *full, *empty;
+        const volatile int* stop;
+        bool counts;
+        __device__ __forceinline__ uint64_t now() const { return globaltimer(); }
+        __device__ __forceinline__ bool stopped() const { return *stop != 0; }
+        __device__ __forceinline__ bool ended(int stage, uint32_t parity) const { return barrier_try(&empty[stage], parity); }
+        __device__ __forceinline__ bool landed(int stage, uint32_t parity) const { return counts && barrier_try(&full[stage], parity); }
+    } const at{full, empty, wait.stop, rank == 0};
+    wait_for_last_uses(uses, r.stages, !ok, p.wait.timeout_ns, at);
 }
 
 // The products on their way end before the Tensor Memory is given back.
