@@ -609,7 +609,8 @@ int tide_group_set_ag_variant(tide_group_t g, int32_t variant) {
 int tide_group_set_wait_timeout(tide_group_t g, uint64_t timeout_ns) {
     if (!g) return TIDE_EINVAL;
     std::lock_guard<std::mutex> lock(g->mu);
-    g->timeout_ns = timeout_ns ? std::max(timeout_ns, tide::kMinTimeoutNs) : tide::kDefaultTimeoutNs;
+    // half of what 64 bits hold at most: the kernels add it to the clock
+    g->timeout_ns = timeout_ns ? std::min(std::max(timeout_ns, tide::kMinTimeoutNs), UINT64_MAX / 2) : tide::kDefaultTimeoutNs;
     return TIDE_OK;
 }
 
