@@ -976,7 +976,8 @@ def _bytes_as_e4m3(*shape):
 
 class Fp8Rows:
     """M rows of ``len`` e4m3 ``codes`` and their fp32 ``scales``, one for each block of 128 columns: what
-    ``dispatch_fp8`` and ``quantize`` write and ``matmul`` reads.  The value is ``codes[s, c] * scales[s, c // 128]``."""
+    ``dispatch_fp8`` and ``quantize`` write and ``matmul`` reads.  The value is ``codes[s, c] * scales[s, c // 128]``.  The calls
+    use the memory that it was made with: other values are copied into these tensors (so of the other containers)."""""
 
     def __init__(self, M: int, len: int):
         import torch
@@ -1034,7 +1035,8 @@ class Fp8Weights:
 
 
 class Route:
-    """The order of T tokens' pairs: ``offsets`` [E + 1], ``slots`` [T, k] and ``tokens`` [T*k], int32, as ``Experts.sort`` writes them."""
+    """The order of T tokens' pairs: ``offsets`` [E + 1], ``slots`` [T, k] and ``tokens`` [T*k], int32, as ``Experts.sort`` writes them.
+    The calls use the memory that it was made with: another order is copied into these tensors."""""
 
     def __init__(self, experts: "Experts", T: int):
         import torch

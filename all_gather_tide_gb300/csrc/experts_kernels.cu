@@ -208,8 +208,8 @@ dispatch_kernel(const Word* src, int64_t src_stride, int64_t T, int k, int32_t M
 // The rows back at their tokens, weighted.  A warp takes a token and up to `per` stretches of 32*Cols vectors, one after the other; AtOnce
 // rows are in flight before their products are added, in fp32 and in the pairs' order.
 //
-// Bound by HBM reads: 524288 rows of 2048 bf16 values back to 65536 tokens in 355 us, 6.7 TB/s (440 with four CTAs an SM, whose
-// registers spilled).
+// Bound by HBM reads: 524288 rows of 2048 bf16 values back to 65536 tokens in 355 us, 6.8 TB/s (418 with four CTAs an SM, of whose
+// registers 168 bytes spill; here 20 do).  Calls in a row find a part of the rows in L2: once it has been flushed they take 2 % longer.
 constexpr int kCombineCtasPerSm = 3;
 template <typename T, int V, int Cols, int AtOnce>
 __global__ void __launch_bounds__(kThreads, kCombineCtasPerSm)
@@ -270,7 +270,7 @@ combine_kernel(const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_
 // product with its weight is written while the dot product is added up.  A lane's sums run over its columns in order, then
 // over the warp's lanes and the team's warps as a tree.
 //
-// Bound by HBM, a row read and a row written for each pair: 262144 rows of 2048 bf16 values in 341 us, 6.6 TB/s.
+// Bound by HBM, a row read and a row written for each pair: 262144 rows of 2048 bf16 values in 341 us, 6.7 TB/s.
 template <typename T, int V, int Pairs, int Cols>
 __global__ void __launch_bounds__(kThreads, 2)
 combine_grad_kernel(const T* dout, int64_t dout_stride, const T* rows, int64_t rows_stride, int64_t tokens, int k, int32_t M, uint32_t len,
@@ -380,7 +380,7 @@ cudaError_t combine(const RowsView& rows, int64_t tokens, int k, int64_t len, co
     auto go = [&](auto* kernel, int cols) {
         const uint32_t stretches = uint32_t((len + 32 * V * cols - 1) / (32 * V * cols));
         // a warp takes the whole row where the tokens fill the GPU four times, so that it finds their rows once (80000 rows of 1027 bf16
-        // values 53 us; with eight vectors at a time 61, and a stretch a warp 76)
+        // values 53 us; with eight vectors at a time 60, and a stretch a warp 76)
         const int64_t warps = 4 * int64_t(c.sms) * kCombineCtasPerSm * kWarps;
         const uint32_t shares = uint32_t(std::min<int64_t>(stretches, (warps + tokens - 1) / tokens));
         const uint32_t per = (stretches + shares - 1) / shares;
@@ -389,7 +389,7 @@ cudaError_t combine(const RowsView& rows, int64_t tokens, int k, int64_t len, co
                             uint32_t(len), slots, weights, static_cast<T*>(out), out_stride, stretches, per, (stretches + per - 1) / per, items);
     };
     // Short vectors go several at a time, fewer where a row has no more: 80000 rows of 1027 bf16 values take 53 us with seven of four rows; eight,
-    // of which registers spill, 60; six 57; 12297 rows 12.9 us, with two 22.
+    // of which registers spill, 60; six 57; 12297 rows 12.3 us, with eight 13.9.
     constexpr int kMany = V * sizeof(T) >= 16 ? 2 : V * sizeof(T) == 8 ? 4 : 7;
     return len > 32 * V ? go(combine_kernel<T, V, kMany, 4>, kMany) : go(combine_kernel<T, V, 1, 4>, 1);
 }

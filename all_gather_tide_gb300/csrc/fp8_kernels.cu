@@ -164,7 +164,7 @@ __device__ __forceinline__ uint2 codes_of(const Eight<T>& x) {
 // one vector.  The row is read and converted once and written for each pair. Rows without alignment are read as aligned words
 // (20000 rows of 1027 bf16 values to four places each 32 us, element by element 39).
 //
-// Bound by HBM writes: 65536 rows of 2048 bf16 values to eight places each in 204 us, 6.6 TB/s (242 with eight CTAs an SM that go
+// Bound by HBM writes: 65536 rows of 2048 bf16 values to eight places each in 204 us, 6.8 TB/s with their scales (242 with eight CTAs an SM that go
 // round: those that come late even out the end).
 template <typename T, bool Vector>
 __global__ void __launch_bounds__(kThreads, 4)

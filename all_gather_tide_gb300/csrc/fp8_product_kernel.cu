@@ -991,7 +991,7 @@ int launch(const ArgsOf<Grad>& p, bool any_scales, int64_t most_tiles, const Cta
 
 bool vectors16(const void* p, int64_t stride, int64_t rows, int elem) { return aligned(p, 16) && (rows <= 1 || stride * elem % 16 == 0); }
 
-// Whether `down` tiles of 128 rows by N columns, summed over `blocks` blocks, go to pairs of CTAs, in tiles of 256 x 256: where
+// Whether `down` tiles of 128 rows by N columns, summed over `blocks` whole blocks (a sum of 1027 has eight), go to pairs of CTAs, in tiles of 256 x 256: where
 // experts have rows enough to fill them, and these are two rounds or more, or half of a round where sums are long, whose products
 // then count for more than a round that is not full (4096 rows of 2048 by 2048 columns of 4 experts 16.4 us, in tiles of 128 x 128
 // 24.5; 6000 of 512 by 1024 of 5 experts 9.8 and 9.0). Else tiles are 128 x 128: also where sums go to registers, and where taking

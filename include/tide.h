@@ -524,8 +524,9 @@ int tide_adamw(tide_tensors_t t, void *const *params, const void *const *grads, 
  * The calls that write them take for a block whose largest magnitude is a > 0 the smallest power of two
  * from 2^-126 to 2^120 with a / scale <= 448 (1 for a block of zeros), and code = x / scale rounded to
  * nearest even; a block with a NaN or an infinity gets a NaN scale.  The calls that read them take such scales,
- * which the tensor cores apply (another number's magnitude counts as the power of two below it, and sets 2 in
- * the status word, if that holds 0; an infinity counts as NaN), or with TIDE_FP8_ANY_SCALES any, at a lower rate.
+ * which the tensor cores apply, or with TIDE_FP8_ANY_SCALES any, at a lower rate. Without that flag another number's
+ * magnitude counts as the power of two below it, and what is below 2^-126, 0 among it, as 2^-127; a product that meets
+ * one sets 2 in the status word, if that holds 0, and its result is not the formula's. An infinity counts as NaN.
  */
 #define TIDE_FP8_TRANSPOSED 0x1u
 #define TIDE_FP8_ANY_SCALES 0x2u
@@ -616,8 +617,8 @@ int tide_experts_combine(tide_experts_t x, const void *rows, int32_t type, int64
 /*
  * tide_experts_combine_grad — the gradients of tide_experts_combine with weights:
  *     drows[slots[i]] = weights[i] * dout[i / k]         dweights[i] = sum over columns of dout[i / k] * rows[slots[i]]
- * the products in fp32 and rounded once to `type`, the sums in fp32 in an order that depends on the sizes alone; pairs without
- * a row have dweights 0, rows without a pair are left as they are.
+ * the products in fp32 and rounded once to `type`, the sums in fp32 in an order that depends on the sizes, the rows' alignment and
+ * the GPU alone; pairs without a row have dweights 0, rows without a pair are left as they are.
  */
 int tide_experts_combine_grad(tide_experts_t x, const void *dout, int32_t type, int64_t dout_stride, const void *rows,
                               int64_t rows_stride, int64_t T, int64_t len, const int32_t *slots, const float *weights,
