@@ -211,6 +211,25 @@ def test_gradients_tell_of_every_scale_that_is_no_power_of_two(tide, each, N, K,
     assert status() == 0
 
 
+@pytest.mark.parametrize("scale, counts_as", [(1.5, 1.0), (-2.0, 2.0), (-3.9, 2.0), (0.0, 2.0 ** -127), (2.0 ** -130, 2.0 ** -127), (2.0 ** -127, 2.0 ** -127), (2.0 ** -126, 2.0 ** -126),
+                                              (2.0 ** 127, 2.0 ** 127), (float("inf"), float("nan")), (float("nan"), float("nan"))])
+@pytest.mark.parametrize("M, N", [(9, 130), (20000, 1024)])
+def test_what_a_scale_counts_as(tide, M, N, scale, counts_as):
+    """One block of codes 1 for each row: 32 of them are there, so a result is 32 times both scales. The other operand's scale keeps it in range."""
+    K, other = 32, 2.0 ** 100 if counts_as < 1 else 2.0 ** -60
+    ex, A, W = tide.Experts(1, 1), tide.Fp8Rows(M, K), tide.Fp8Weights(1, N, K)
+    out = torch.empty(M, N, device="cuda")
+    for x in (A, W):
+        x.codes.view(torch.uint8).fill_(0x38)
+    for mine, theirs in ((A, W), (W, A)):
+        mine.scales.fill_(scale), theirs.scales.fill_(other)
+        ex.matmul(A, W, None, out)
+        want = torch.full_like(out, 32.0 * counts_as * other)
+        assert torch.equal(torch.nan_to_num(out, 7.0), torch.nan_to_num(want, 7.0)) and bool((out.isnan() == want.isnan()).all())
+        told = counts_as == counts_as and (scale != counts_as or scale < 2.0 ** -126)
+        assert ex.device_status() == (2 if told else 0)
+
+
 # ---- no rows, far rows ---------------------------------------------------------------------------------
 
 
