@@ -993,7 +993,7 @@ bool vectors16(const void* p, int64_t stride, int64_t rows, int elem) { return a
 
 // Whether `down` tiles of 128 rows by N columns, summed over `blocks` whole blocks (a sum of 1027 has eight), go to pairs of CTAs, in tiles of 256 x 256: where
 // experts have rows enough to fill them, and these are two rounds or more, or half of a round where sums are long, whose products
-// then count for more than a round that is not full (4096 rows of 2048 by 2048 columns of 4 experts 16.4 us, in tiles of 128 x 128
+// then count for more than a round that is not full (4096 rows of 2048 by 2048 columns of 4 experts 17.6 us, in tiles of 128 x 128
 // 24.5; 6000 of 512 by 1024 of 5 experts 9.8 and 9.0). Else tiles are 128 x 128: also where sums go to registers, and where taking
 // them out is what lasts, of up to four blocks in fp32 (131072 rows of 512 by 384 columns 46 us, by pairs 55), or eight in rows
 // without alignment (6000 of 1027 by 1003 columns 16 and 18). (Pairs' tiles of
